@@ -438,6 +438,112 @@ moe_status fused_experts_from_host(const moe_problem* p, const void* host_x,
                                    const void* w2_scale, void* workspace,
                                    size_t workspace_bytes, void* stream);
 
+/* ---- Training an expert layer, and 4-bit operands ------------------------
+ *
+ * Element types of the entry points below. */
+typedef enum { MOE_T_BF16 = 0, MOE_T_FP16 = 1, MOE_T_FP32 = 2 } moe_dtype;
+
+/* Ragged grouped products.  Rows of x [R, K] and y [R, N] are grouped by
+ * expert without padding: rows expert_offsets[e] .. expert_offsets[e+1] - 1
+ * belong to expert e (device, E + 1 int32, non-decreasing, within [0, R]; read
+ * on the device, so a graph replay sees the offsets of the moment).  w is
+ * [E, N, K], dense.  A segment may be empty or of any length; rows before
+ * expert_offsets[0] and from expert_offsets[E] on belong to no expert: they are
+ * not read and their outputs are left as they were.  (The padded layout of
+ * moe_align_permute is such a grouping too: its expert_offsets, R = S rows,
+ * zero rows as padding.)
+ *   ragged_gemm        y[r, n]     = sum_k x[r, k] w[e, n, k] (+ bias[e, n])
+ *   ragged_gemm_dgrad  dx[r, k]    = sum_n dy[r, n] w[e, n, k]
+ *   ragged_gemm_wgrad  dw[e, n, k] = sum_{r in e} dy[r, n] x[r, k]  (+ dw)
+ * All sums in fp32, rounded once to the output's type.
+ *  - dtype: MOE_T_BF16 or MOE_T_FP16, the type of x, w, y, dy, dx and bias
+ *    ([E, N], may be NULL, added in fp32).
+ *  - N and K: multiples of 8; ldx / ldy: row strides in elements of x, dx and
+ *    of y, dy (multiples of 8, at least K / N; 0 = dense).
+ *  - dw: dtype (dw_dtype == p->dtype) or fp32 (MOE_T_FP32).  accumulate != 0
+ *    adds to dw (in fp32, rounded once); else every expert's dw is written, 0
+ *    for an expert without rows.  accumulate == 1 leaves those as they are.
+ *  - workspace: device, 128-byte aligned, moe_ragged_workspace_bytes(p) bytes;
+ *    no contents are kept from call to call.  Calls that may overlap on the
+ *    GPU take a workspace each.
+ * Offsets that decrease or leave [0, R] are reported by moe_sync_status as
+ * MOE_ERR_DEVICE_BAD_INDEX; no access leaves the tensors whatever they hold.
+ * R == 0: nothing to do (wgrad without accumulate zeroes dw).
+ * Errors: MOE_ERR_INVALID_ARG (sizes, strides, dtype, NULL or misaligned
+ * pointers), MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA. */
+typedef struct {
+  int32_t R, N, K, E;
+  int32_t dtype;         /* moe_dtype */
+  int64_t ldx, ldy;
+} moe_ragged;
+#define MOE_MAX_RAGGED_ROWS (1 << 22)
+size_t moe_ragged_workspace_bytes(const moe_ragged* p);
+moe_status ragged_gemm(const moe_ragged* p, const void* x, const void* w, const void* bias,
+                       const int32_t* expert_offsets, void* y, void* workspace,
+                       size_t workspace_bytes, void* stream);
+moe_status ragged_gemm_dgrad(const moe_ragged* p, const void* dy, const void* w,
+                             const int32_t* expert_offsets, void* dx, void* workspace,
+                             size_t workspace_bytes, void* stream);
+moe_status ragged_gemm_wgrad(const moe_ragged* p, const void* dy, const void* x,
+                             const int32_t* expert_offsets, void* dw, int dw_dtype,
+                             int accumulate, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* MXFP4 (the weight format of MOE_Q_MXFP4_W4A8): E2M1 codes [rows, K/2] (low
+ * nibble = even k) and one E8M0 scale per 32 values [rows, K/32].  K is a
+ * multiple of 32.  For each group of 32 with a = max |v|:
+ *   MOE_MXFP4_FLOOR  scale 2^(floor(log2 a) - 2): the group's largest binade
+ *                    meets E2M1's; what exceeds 6 after scaling saturates;
+ *   MOE_MXFP4_CEIL   the smallest power of two >= a / 6: nothing saturates;
+ * both at least 2^-127 (also for a == 0); codes are v / scale rounded to the
+ * nearest E2M1 value, ties to even.  A group with an infinity or NaN gets scale
+ * 255 (NaN) and codes 0.
+ *  - x: bf16, fp16 or fp32, rows ldx elements apart (a multiple of 8; 0 = K);
+ *    x, codes and out 16-byte aligned; codes and scales dense.
+ *  - moe_mxfp4_dequantize writes value * scale in out_dtype (exact in bf16 and
+ *    fp32 down to their subnormals; fp16 rounds and overflows as a cast does).
+ *  - moe_mxfp4_pack_scales rewrites weight scales [E, N, K/32] into the blocks
+ *    that moe_prepack_weights describes, for one matrix (N and K multiples of
+ *    128, else MOE_ERR_UNSUPPORTED). */
+typedef enum { MOE_MXFP4_FLOOR = 0, MOE_MXFP4_CEIL = 1 } moe_mxfp4_scale;
+moe_status moe_mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int K, int64_t ldx,
+                              int scale_mode, void* codes, void* scales, void* stream);
+moe_status moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t rows, int K,
+                                void* out, int out_dtype, int64_t ldo, void* stream);
+moe_status moe_mxfp4_pack_scales(const void* scales, int E, int N, int K, void* packed,
+                                 void* stream);
+
+/* Ragged grouped product of 4-bit operands: y[r, n] = sum_k x[r, k] w[e, n, k]
+ * with x and w in MXFP4 (x_codes [R, K/2], x_scales [R, K/32], w_codes
+ * [E, N, K/2], w_scales_packed from moe_mxfp4_pack_scales), fp32 accumulation,
+ * y [R, N] of type p->dtype with row stride ldy.  Segments, workspace and errors
+ * as for ragged_gemm; N and K multiples of 128 (else MOE_ERR_UNSUPPORTED), ldx 0
+ * or K; x_scales 4-byte aligned. */
+moe_status ragged_gemm_mxfp4(const moe_ragged* p, const void* x_codes, const void* x_scales,
+                             const void* w_codes, const void* w_scales_packed,
+                             const int32_t* expert_offsets, void* y, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Global L2 norm of n gradient tensors and clipping:
+ *   norm = sqrt(sum of all squares),  c = min(1, max_norm / (norm + 1e-6)),
+ *   outs[i] = c * grads[i].
+ *  - grads, outs, numel, dtypes: host arrays of n entries (device pointers,
+ *    element counts, moe_dtype); outs[i] == grads[i] clips in place (with c == 1
+ *    nothing is written when all are in place).  No other overlap.  Any
+ *    alignment of the element; 16-byte aligned tensors are faster.
+ *  - norm: device fp32, the norm before clipping.  Squares are summed in fp32
+ *    over at most 64 values and in fp64 beyond; a square beyond fp32's range
+ *    gives an infinite norm.  A NaN or infinite norm clips by the same formula
+ *    (c = NaN or 0).  The result does not depend on timing.
+ *  - workspace: device, 16-byte aligned, moe_clip_workspace_bytes() bytes.
+ * The arrays are read during the call only.  n == 0 gives norm 0. */
+#define MOE_MAX_CLIP_TENSORS 65536
+size_t moe_clip_workspace_bytes(void);
+moe_status moe_clip_grad_norm(int n, const void* const* grads, void* const* outs,
+                              const int64_t* numel, const int32_t* dtypes, float max_norm,
+                              float* norm, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* Synchronises `stream`, reads and clears the device error word, and returns
  * MOE_OK, MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_DEVICE_BAD_INDEX or MOE_ERR_CUDA. */
 moe_status moe_sync_status(void* stream);

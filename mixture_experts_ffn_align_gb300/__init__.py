@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from functools import cached_property
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_ffn.so")
@@ -35,7 +36,10 @@ EXPORTS = ["moe_m_sum_bound", "moe_align_workspace_bytes", "moe_align_permute_la
            "moe_batched_workspace_bytes", "fused_experts_batched", "grouped_gemm_w13_ex",
            "grouped_gemm_w2_ex", "fused_experts_ex", "moe_gemm2_splits",
            "moe_gemm2_partial_bytes", "grouped_gemm_w2_split", "unpermute_reduce_split",
-           "moe_prepacked_scale_bytes", "moe_prepack_weights"]
+           "moe_prepacked_scale_bytes", "moe_prepack_weights",
+           "moe_ragged_workspace_bytes", "ragged_gemm", "ragged_gemm_dgrad", "ragged_gemm_wgrad",
+           "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_pack_scales",
+           "ragged_gemm_mxfp4", "moe_clip_workspace_bytes", "moe_clip_grad_norm"]
 
 NOALLOC_SCRATCH_BYTES = 1 << 20   # MOE_NOALLOC_SCRATCH_BYTES in include/moe_ffn.h
 
@@ -89,6 +93,32 @@ class Problem:
         return cls(**d)
 
 
+DTYPE = {"bfloat16": 0, "float16": 1, "float32": 2}
+MXFP4_SCALE = {"floor": 0, "ceil": 1}
+
+
+class CRagged(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("R", "N", "K", "E", "dtype")] + \
+               [(n, ctypes.c_int64) for n in ("ldx", "ldy")]
+
+
+@dataclass(frozen=True)
+class Ragged:
+    """Mirror of ``moe_ragged``: R rows grouped by expert, weights [E, N, K]."""
+    R: int
+    N: int
+    K: int
+    E: int
+    dtype: str = "bfloat16"     # of x, w, y and the 16-bit gradients
+    ldx: int = 0                # row strides in elements, 0: dense
+    ldy: int = 0
+
+    @cached_property
+    def _ref(self):
+        return ctypes.byref(CRagged(self.R, self.N, self.K, self.E, DTYPE[self.dtype], self.ldx,
+                                    self.ldy))
+
+
 _lib = None
 
 
@@ -137,6 +167,21 @@ def lib() -> ctypes.CDLL:
             [ctypes.c_int64, i32], None
         L.moe_debug_set_bf16_gemm_form.argtypes, L.moe_debug_set_bf16_gemm_form.restype = \
             [i32], None
+        G, i64, f32 = ctypes.POINTER(CRagged), ctypes.c_int64, ctypes.c_float
+        L.moe_ragged_workspace_bytes.argtypes, L.moe_ragged_workspace_bytes.restype = [G], sz
+        L.ragged_gemm.argtypes = [G] + [vp] * 6 + [sz, vp]
+        L.ragged_gemm_dgrad.argtypes = [G] + [vp] * 5 + [sz, vp]
+        L.ragged_gemm_wgrad.argtypes = [G] + [vp] * 4 + [i32, i32, vp, sz, vp]
+        L.ragged_gemm_mxfp4.argtypes = [G] + [vp] * 7 + [sz, vp]
+        L.moe_mxfp4_quantize.argtypes = [vp, i32, i64, i32, i64, i32, vp, vp, vp]
+        L.moe_mxfp4_dequantize.argtypes = [vp, vp, i64, i32, vp, i32, i64, vp]
+        L.moe_mxfp4_pack_scales.argtypes = [vp, i32, i32, i32, vp, vp]
+        L.moe_clip_workspace_bytes.argtypes, L.moe_clip_workspace_bytes.restype = [], sz
+        L.moe_clip_grad_norm.argtypes = [i32] + [vp] * 4 + [f32, vp, vp, sz, vp]
+        for n in ("ragged_gemm", "ragged_gemm_dgrad", "ragged_gemm_wgrad", "ragged_gemm_mxfp4",
+                  "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_pack_scales",
+                  "moe_clip_grad_norm"):
+            getattr(L, n).restype = i32
         for n in ("moe_align_permute", "grouped_gemm_w13", "act_mul_quant", "grouped_gemm_w2",
                   "unpermute_reduce", "fused_experts", "fused_experts_from_host",
                   "moe_sync_status", "moe_topk_router", "fused_experts_batched",
@@ -328,6 +373,171 @@ def fused_experts_from_host(p: Problem, host_x, host_topk_ids, host_topk_weights
         _p(w13_scale), _p(w2), _p(w2_scale), _p(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)),
         "fused_experts_from_host")
+
+
+# --------------------------------------- ragged products, 4-bit operands, clip
+def _dtype_name(t) -> str:
+    return str(t.dtype)[6:]      # "torch.bfloat16" -> "bfloat16"
+
+
+def _arg(name: str, t, shape=None, dtype=None, strided: bool = False):
+    """Checks one tensor argument: on the GPU, of the given type and shape,
+    dense (strided: rows may lie apart)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    if dtype is not None and _dtype_name(t) != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {_dtype_name(t)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous() and not (strided and t.dim() == 2 and t.stride(1) == 1):
+        raise ValueError(f"{name} must be {'dense along its rows' if strided else 'dense'}")
+
+
+def _row_stride(name: str, t, want: int):
+    if t.shape[0] > 1 and t.stride(0) != want:
+        raise ValueError(f"{name} must have the row stride {want}, not {t.stride(0)}")
+
+
+def moe_ragged_workspace_bytes(p: Ragged) -> int:
+    return int(lib().moe_ragged_workspace_bytes(p._ref))
+
+
+def _ragged_rows(p: Ragged, name: str, t, cols: int, ld: int):
+    _arg(name, t, (p.R, cols), p.dtype, strided=True)
+    _row_stride(name, t, ld or cols)
+
+
+def _ragged_common(p: Ragged, expert_offsets, workspace):
+    _arg("expert_offsets", expert_offsets, (p.E + 1,), "int32")
+    _arg("workspace", workspace)
+    return workspace.numel() * workspace.element_size()
+
+
+def ragged_gemm(p: Ragged, x, w, expert_offsets, y, workspace, bias=None, stream=None):
+    """y[r] = W_e x[r] (+ bias_e) for the rows r of each expert e; x [R, K],
+    w [E, N, K], y [R, N], bias [E, N], expert_offsets int32 [E + 1]."""
+    _ragged_rows(p, "x", x, p.K, p.ldx)
+    _arg("w", w, (p.E, p.N, p.K), p.dtype)
+    _ragged_rows(p, "y", y, p.N, p.ldy)
+    if bias is not None:
+        _arg("bias", bias, (p.E, p.N), p.dtype)
+    n = _ragged_common(p, expert_offsets, workspace)
+    _check(lib().ragged_gemm(p._ref, _p(x), _p(w), _p(bias), _p(expert_offsets), _p(y),
+                             _p(workspace), n, _stream(stream)), "ragged_gemm")
+
+
+def ragged_gemm_dgrad(p: Ragged, dy, w, expert_offsets, dx, workspace, stream=None):
+    """dx[r] = W_e^T dy[r]: the gradient of ragged_gemm's x."""
+    _ragged_rows(p, "dy", dy, p.N, p.ldy)
+    _arg("w", w, (p.E, p.N, p.K), p.dtype)
+    _ragged_rows(p, "dx", dx, p.K, p.ldx)
+    n = _ragged_common(p, expert_offsets, workspace)
+    _check(lib().ragged_gemm_dgrad(p._ref, _p(dy), _p(w), _p(expert_offsets), _p(dx),
+                                   _p(workspace), n, _stream(stream)), "ragged_gemm_dgrad")
+
+
+def ragged_gemm_wgrad(p: Ragged, dy, x, expert_offsets, dw, workspace, accumulate=False,
+                      stream=None):
+    """dw[e] (+)= sum over e's rows of dy[r] x[r]^T: the gradient of
+    ragged_gemm's w, in the operands' type or float32 (dw's)."""
+    _ragged_rows(p, "dy", dy, p.N, p.ldy)
+    _ragged_rows(p, "x", x, p.K, p.ldx)
+    _arg("dw", dw, (p.E, p.N, p.K))
+    if _dtype_name(dw) not in (p.dtype, "float32"):
+        raise TypeError(f"dw must be {p.dtype} or float32, not {_dtype_name(dw)}")
+    n = _ragged_common(p, expert_offsets, workspace)
+    _check(lib().ragged_gemm_wgrad(p._ref, _p(dy), _p(x), _p(expert_offsets), _p(dw),
+                                   DTYPE[_dtype_name(dw)], int(bool(accumulate)), _p(workspace),
+                                   n, _stream(stream)), "ragged_gemm_wgrad")
+
+
+def moe_mxfp4_quantize(x, codes, scales, scale_mode="floor", stream=None):
+    """E2M1 codes (uint8 [rows, K/2]) and E8M0 scales (uint8 [rows, K/32]) of
+    x [rows, K] (bfloat16, float16 or float32; rows may lie apart)."""
+    if x.dim() != 2:
+        raise ValueError("x must have two dimensions")
+    rows, K = x.shape
+    _arg("x", x, strided=True)
+    if _dtype_name(x) not in DTYPE:
+        raise TypeError("x must be bfloat16, float16 or float32")
+    _arg("codes", codes, (rows, K // 2), "uint8")
+    _arg("scales", scales, (rows, K // 32), "uint8")
+    _check(lib().moe_mxfp4_quantize(_p(x), DTYPE[_dtype_name(x)], rows, K,
+                                    x.stride(0) if rows > 1 else 0, MXFP4_SCALE[scale_mode],
+                                    _p(codes), _p(scales), _stream(stream)),
+           "moe_mxfp4_quantize")
+
+
+def moe_mxfp4_dequantize(codes, scales, out, stream=None):
+    """out [rows, K] (bfloat16, float16 or float32) = value * 2^(scale - 127)."""
+    if out.dim() != 2:
+        raise ValueError("out must have two dimensions")
+    rows, K = out.shape
+    _arg("out", out, strided=True)
+    if _dtype_name(out) not in DTYPE:
+        raise TypeError("out must be bfloat16, float16 or float32")
+    _arg("codes", codes, (rows, K // 2), "uint8")
+    _arg("scales", scales, (rows, K // 32), "uint8")
+    _check(lib().moe_mxfp4_dequantize(_p(codes), _p(scales), rows, K, _p(out),
+                                      DTYPE[_dtype_name(out)], out.stride(0) if rows > 1 else 0,
+                                      _stream(stream)), "moe_mxfp4_dequantize")
+
+
+def moe_mxfp4_pack_scales(scales, packed, stream=None):
+    """Weight scales (uint8 [E, N, K/32]) in the block form that
+    ragged_gemm_mxfp4 reads; packed has as many bytes."""
+    E, N, G = scales.shape
+    _arg("scales", scales, dtype="uint8")
+    _arg("packed", packed, dtype="uint8")
+    if packed.numel() != scales.numel():
+        raise ValueError("packed must have as many bytes as scales")
+    _check(lib().moe_mxfp4_pack_scales(_p(scales), E, N, 32 * G, _p(packed), _stream(stream)),
+           "moe_mxfp4_pack_scales")
+
+
+def ragged_gemm_mxfp4(p: Ragged, x_codes, x_scales, w_codes, w_scales_packed, expert_offsets, y,
+                      workspace, stream=None):
+    """y[r] = W_e x[r] with both operands in MXFP4; p.dtype is y's."""
+    _arg("x_codes", x_codes, (p.R, p.K // 2), "uint8")
+    _arg("x_scales", x_scales, (p.R, p.K // 32), "uint8")
+    _arg("w_codes", w_codes, (p.E, p.N, p.K // 2), "uint8")
+    _arg("w_scales_packed", w_scales_packed, dtype="uint8")
+    if w_scales_packed.numel() != p.E * p.N * (p.K // 32):
+        raise ValueError("w_scales_packed must have E * N * K / 32 bytes")
+    _ragged_rows(p, "y", y, p.N, p.ldy)
+    n = _ragged_common(p, expert_offsets, workspace)
+    _check(lib().ragged_gemm_mxfp4(p._ref, _p(x_codes), _p(x_scales), _p(w_codes),
+                                   _p(w_scales_packed), _p(expert_offsets), _p(y), _p(workspace),
+                                   n, _stream(stream)), "ragged_gemm_mxfp4")
+
+
+def moe_clip_workspace_bytes() -> int:
+    return int(lib().moe_clip_workspace_bytes())
+
+
+def moe_clip_grad_norm(grads, max_norm, norm, workspace, out=None, stream=None):
+    """Global L2 norm of the gradients (into the float32 scalar tensor norm)
+    and clipping to max_norm, in place or into the tensors of ``out``."""
+    out = grads if out is None else out
+    n = len(grads)
+    if len(out) != n:
+        raise ValueError("out must have as many tensors as grads")
+    _arg("norm", norm, dtype="float32")
+    _arg("workspace", workspace)
+    src, dst = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)()
+    numel, types = (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
+    for i, (g, o) in enumerate(zip(grads, out)):
+        name = _dtype_name(g)
+        if name not in DTYPE:
+            raise TypeError("gradients must be bfloat16, float16 or float32")
+        _arg("grads", g)
+        if o is not g:
+            _arg("out", o, g.shape, name)
+        src[i], dst[i] = g.data_ptr(), o.data_ptr()
+        numel[i], types[i] = g.numel(), DTYPE[name]
+    _check(lib().moe_clip_grad_norm(n, src, dst, numel, types, float(max_norm), _p(norm),
+                                    _p(workspace), workspace.numel() * workspace.element_size(),
+                                    _stream(stream)), "moe_clip_grad_norm")
 
 
 def moe_gemm2_splits(p: Problem) -> int:

@@ -285,6 +285,14 @@ moe_status cuda_status(cudaError_t e) {
   return MOE_ERR_CUDA;
 }
 
+}  // namespace
+
+namespace moe {
+int record_cuda_status(cudaError_t e) { return cuda_status(e); }
+}  // namespace moe
+
+namespace {
+
 // The GEMMs cut each expert's segment into 128-row m-tiles whatever the block
 // size (16, 32, 64 or 128; a partial last m-tile's rows past the segment are
 // not stored), so every valid block size is served; bf16 GEMM2 tiles are 256

@@ -365,6 +365,43 @@ bool make_tmap_u8_rows(CUtensorMap* map, const void* base, uint64_t rows, uint64
   return r == CUDA_SUCCESS;
 }
 
+// Tensor map of the ragged products: a 16-bit matrix [d1, d0] (rank 2) or a
+// stack of d2 of them (rank 3), rows ld elements apart, boxes of 64 x box1
+// (x 1) values with 128-byte swizzle; what lies outside reads as zero.  Serves
+// K-major and MN-major operands alike: the MMA's descriptors tell them apart.
+bool make_tmap_rag(CUtensorMap* map, const void* base, bool half, int rank, uint64_t d0,
+                   uint64_t d1, uint64_t d2, uint64_t ld, uint32_t box1) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {ld * 2, d1 * ld * 2};
+  const cuuint32_t box[3] = {64, box1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// Tensor map of packed 4-bit values ([d1, d0 / 2] bytes, or d2 of them) for the
+// 4-bit MMA, which reads them packed: boxes of 128 bytes x box1 rows, 128-byte
+// swizzle.
+bool make_tmap_rag_fp4(CUtensorMap* map, const void* base, int rank, uint64_t d0, uint64_t d1,
+                       uint64_t d2, uint32_t box1) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {d0 / 2, d1, d2};
+  const cuuint64_t strides[2] = {d0 / 2, d1 * (d0 / 2)};
+  const cuuint32_t box[3] = {128, box1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank,
+                        const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 cudaError_t launch_ggemm_bf16(const void* A, int cap, int K, const void* B, int b_rows_total,
                               int b_rows_per_expert, int n_out, const int32_t* block_expert_ids,
                               const int32_t* num_post_padded, void* out, bool fuse_act,

@@ -197,4 +197,46 @@ cudaError_t launch_ggemm_mx_2sm(const void* A, const float* a_scale, int cap, in
 cudaError_t launch_prepack_mx_scales(const uint8_t* scale, int E, int N, int K, void* packed,
                                      cudaStream_t stream);
 
+// MOE_OK or MOE_ERR_CUDA (then remembered for moe_last_error_string).
+int record_cuda_status(cudaError_t e);
+
+// ---- ragged grouped products (ragged.cuh has the formulas)
+struct RaggedProblem {
+  bool half;              // fp16 operands, else bf16
+  int R, N, K, E;
+  long long ldx, ldy;     // row strides of x / dx and y / dy, in elements
+  const int32_t* offsets;
+};
+// op: 0 forward (rows = x, out = y), 1 dgrad (rows = dy, out = dx).  workspace
+// as moe_ragged_workspace_bytes.
+cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows, const void* w,
+                               const void* bias, void* out, cudaStream_t stream);
+// Tensor maps of dy and x cut to each expert's rows, ragged_maps_bytes(E) at
+// `workspace` (64-byte aligned), and the product that loads through them.
+size_t ragged_maps_bytes(int E);
+cudaError_t launch_ragged_maps(const RaggedProblem& p, const void* dy, const void* x,
+                               void* workspace, cudaStream_t stream);
+cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* maps, void* dw, bool out_f32,
+                                bool accumulate, cudaStream_t stream);
+// 4-bit product: x codes / scales [R, K/2] / [R, K/32], weights [E, N, K/2] with
+// packed scales; token scales are first rewritten to workspace.
+size_t ragged_mxfp4_scale_bytes(int R, int K, int E);
+cudaError_t launch_ragged_mxfp4(const RaggedProblem& p, const void* xq, const uint8_t* x_scale,
+                                const void* wq, const void* w_scale_packed, void* y,
+                                void* workspace, cudaStream_t stream);
+
+// ---- MXFP4 codec.  type: 0 bf16, 1 fp16, 2 fp32.
+cudaError_t launch_mxfp4_quantize(const void* x, int type, long long rows, int K, long long ldx,
+                                  bool ceil_scale, uint8_t* codes, uint8_t* scales,
+                                  cudaStream_t stream);
+cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, long long rows,
+                                    int K, void* out, int type, long long ldo,
+                                    cudaStream_t stream);
+
+// ---- gradient norm and clip
+size_t clip_workspace_bytes();
+cudaError_t launch_clip_grad_norm(int n, const void* const* grads, void* const* outs,
+                                  const int64_t* numel, const int32_t* types, float max_norm,
+                                  float* norm, void* workspace, cudaStream_t stream);
+
 }  // namespace moe

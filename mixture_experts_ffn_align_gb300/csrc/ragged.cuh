@@ -1,0 +1,334 @@
+// Pieces shared by the ragged grouped products (ragged_gemm.cu on one SM,
+// ragged_gemm_2sm.cu on SM pairs, ragged_mxfp4.cu): segments of rows given by
+// expert offsets on the device, their cut into tiles, operand descriptors and
+// epilogue stores.
+//
+// The products, with w [E, N, K] and the rows o[e] .. o[e+1]-1 of expert e:
+//   forward  y[r, n]     = sum_k x[r, k]  w[e, n, k]
+//   dgrad    dx[r, k]    = sum_n dy[r, n] w[e, n, k]
+//   wgrad    dw[e, n, k] = sum_r dy[r, n] x[r, k]
+//
+// Forward and dgrad put the weights in the MMA's M (128 or 256 of them) and
+// the tokens in its N: N can be any multiple of 16, so a segment's rows are
+// cut evenly into tiles of at most 256 tokens and almost no MMA work falls on
+// rows of other segments, whatever the segment's length.  With the tokens in
+// M every segment would be rounded up to 128 or 256 rows.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "moe_common.cuh"
+
+namespace moe {
+
+enum : int { RAG_FWD = 0, RAG_DGRAD = 1, RAG_WGRAD = 2 };
+
+constexpr int kRagMaxExperts = 1024;
+// Shared memory of the segment table: header, then for each segment with rows
+// the first token tile (prefix), first row, rows and expert.
+constexpr int kRagSchedBytes = 16 + 4 * (4 * (kRagMaxExperts + 1));
+
+// Everything a ragged product kernel needs beside its tensor maps.
+struct RagArgs {
+  const int32_t* offsets;   // [E + 1]
+  int R, E;
+  int W;                    // forward, dgrad: columns of the output (N or K)
+  int num_kb;               // forward, dgrad: 64-deep steps of the reduction
+  int w_tiles;              // forward, dgrad: tiles of W; wgrad: tiles of N
+  int k_tiles;              // wgrad: tiles of K
+  int N, K;                 // wgrad: the output of one expert
+  int tile_rows;            // forward, dgrad: most token rows of a tile
+  int group_max;            // token tiles (wgrad: n tiles) walked together
+  int stages;
+  void* out;
+  long long ldo;            // row stride of out (forward, dgrad)
+  const void* bias;         // forward: [E, N] in the operands' type, or null
+  int out_f32;              // wgrad: dw is fp32
+  int accumulate;           // wgrad: dw += instead of dw =
+  const CUtensorMap* maps;  // wgrad: maps of dy and x cut to each expert's rows
+  int splits;               // forward, dgrad on one SM: slices of the reduction
+  float* part;              // their fp32 sums [splits, R, W]
+  int* tile_ctr;            // SM pairs: {next tile, CTAs finished}
+  uint64_t limit_ns;
+  int never_arrive;
+  int* err;
+};
+
+struct RagSched {
+  const int* tile0;   // first token tile of each segment; tile0[nseg] = all
+  const int* row0;
+  const int* cnt;
+  const int* exp;
+  int nseg;
+};
+
+// Rows of each token tile of a segment of cnt rows: the fewest tiles of at
+// most tile_rows rows, all of the same size rounded up to G rows.
+template <int G>
+__device__ __forceinline__ int rag_rows_per_tile(int cnt, int tile_rows) {
+  const int nt = (cnt + tile_rows - 1) / tile_rows;
+  return ((cnt + nt - 1) / nt + G - 1) / G * G;
+}
+
+// Builds the segment table of this CTA from the offsets.  Every thread calls
+// it (it contains __syncthreads).  Offsets are read once, clamped into
+// [0, R] and made non-decreasing, so no table they can hold reaches outside
+// the tensors or gives a row to two experts; offsets that needed it are
+// reported in the device error word.  scratch: E + 1 ints of shared memory
+// free until this returns.
+template <int G>
+__device__ __forceinline__ RagSched rag_sched_build(const RagArgs& a, int* mem, int* scratch) {
+  int* hdr = mem;
+  int* tile0 = mem + 4;
+  int* row0 = tile0 + kRagMaxExperts + 1;
+  int* cnt = row0 + kRagMaxExperts + 1;
+  int* exp = cnt + kRagMaxExperts + 1;
+  for (int e = threadIdx.x; e <= a.E; e += blockDim.x) scratch[e] = a.offsets[e];
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int nseg = 0, tiles = 0, top = 0;   // top: largest offset so far
+    bool bad = false;
+    for (int base = 0; base < a.E; base += 32) {
+      const int e = base + lane;
+      const int b_raw = scratch[min(e, a.E)], e_raw = scratch[min(e + 1, a.E)];
+      bad |= b_raw < 0 || e_raw > a.R || e_raw < b_raw;
+      int mx = max(min(max(b_raw, 0), a.R), top);   // running maximum of the offsets
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, mx, o);
+        if (lane >= o) mx = max(mx, v);
+      }
+      const int end = max(mx, min(max(e_raw, 0), a.R));
+      const int n = e < a.E ? end - mx : 0;
+      const int per = n > 0 ? rag_rows_per_tile<G>(n, a.tile_rows) : 1;
+      const int nt = (n + per - 1) / per;
+      const unsigned has = __ballot_sync(0xffffffffu, n > 0);
+      int inc = nt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (n > 0) {
+        const int s = nseg + __popc(has & ((1u << lane) - 1u));
+        tile0[s] = tiles + inc - nt;
+        row0[s] = mx;
+        cnt[s] = n;
+        exp[s] = e;
+      }
+      nseg += __popc(has);
+      tiles += __shfl_sync(0xffffffffu, inc, 31);
+      top = __shfl_sync(0xffffffffu, end, 31);
+    }
+    if (lane == 0) {
+      tile0[nseg] = tiles;
+      hdr[0] = nseg;
+    }
+    if (bad && blockIdx.x == 0) set_dev_error(a.err, kDevErrBadIndex);
+  }
+  fence_proxy_async_smem();   // scratch lies where TMA writes next
+  __syncthreads();
+  RagSched s;
+  s.tile0 = tile0;
+  s.row0 = row0;
+  s.cnt = cnt;
+  s.exp = exp;
+  s.nseg = hdr[0];
+  return s;
+}
+
+// One tile of forward or dgrad: rows [row0, row0 + rows) of expert e, columns
+// from 128 w_tile (256 w_tile on SM pairs).
+struct RagTile {
+  int e, row0, rows, w_tile;
+  int tok;               // number of the token tile, counted over all segments
+};
+
+// Tile t: segment by segment; inside a segment groups of group_max token
+// tiles, weight tile by weight tile, the group's token tiles inner, so that
+// the CTAs running together share weight tiles and token rows in L2.
+template <int G>
+__device__ __forceinline__ RagTile rag_tile(const RagSched& s, const RagArgs& a, int t) {
+  const int q = t / a.w_tiles;
+  int lo = 0, hi = s.nseg - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.tile0[mid] <= q) lo = mid; else hi = mid - 1;
+  }
+  const int nt = s.tile0[lo + 1] - s.tile0[lo];
+  const int local = t - s.tile0[lo] * a.w_tiles;
+  const int c = local / (a.group_max * a.w_tiles);
+  const int gm = min(a.group_max, nt - c * a.group_max);
+  const int l2 = local - c * a.group_max * a.w_tiles;
+  RagTile T;
+  T.w_tile = l2 / gm;
+  const int tok = c * a.group_max + (l2 - T.w_tile * gm);
+  const int per = rag_rows_per_tile<G>(s.cnt[lo], a.tile_rows);
+  T.e = s.exp[lo];
+  T.row0 = s.row0[lo] + tok * per;
+  T.rows = min(per, s.cnt[lo] - tok * per);
+  T.tok = s.tile0[lo] + tok;
+  return T;
+}
+
+// One tile of wgrad: expert e, rows n_tile of N and columns k_tile of K, over
+// the expert's cnt rows.  Groups of group_max n tiles, k tile by k tile, the
+// group's n tiles inner.
+struct RagWTile {
+  int e, n_tile, k_tile;
+};
+__device__ __forceinline__ RagWTile rag_wtile(const RagArgs& a, int t) {
+  const int per = a.w_tiles * a.k_tiles;
+  RagWTile T;
+  T.e = t / per;
+  const int local = t - T.e * per;
+  const int c = local / (a.group_max * a.k_tiles);
+  const int gm = min(a.group_max, a.w_tiles - c * a.group_max);
+  const int l2 = local - c * a.group_max * a.k_tiles;
+  T.k_tile = l2 / gm;
+  T.n_tile = c * a.group_max + (l2 - T.k_tile * gm);
+  return T;
+}
+
+// Descriptor of an MN-major tile written by TMA with 128-byte swizzling: 64
+// values of M (or N) a row, one row for each step of the reduction, 64 rows a
+// box; 8-row atoms of 1024 bytes follow one another along the reduction
+// (stride byte offset), the box of the next 64 values of M lies 8192 bytes on
+// (leading byte offset).  Sixteen steps of the reduction are 2048 bytes.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(8192u >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;   // MN-major operands
+
+// 3-D tiled load (the weights [E, N, K]) into this CTA's shared memory.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t c0, int32_t c1, int32_t c2,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map,
+                                                 uint32_t cluster_bar, int32_t c0, int32_t c1,
+                                                 int32_t c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar),
+      "l"(policy)
+      : "memory");
+}
+// A tensor map that an earlier kernel wrote: order its use after that write.
+__device__ __forceinline__ void tensormap_acquire(const CUtensorMap* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(
+                   reinterpret_cast<uint64_t>(map))
+               : "memory");
+}
+
+// fp32 <-> the operands' 16-bit types.
+template <typename T>
+struct Half16;
+template <>
+struct Half16<__nv_bfloat16> {
+  static constexpr uint32_t kFmt = kFmtBF16;
+  static __device__ __forceinline__ uint16_t bits(float v) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  }
+  static __device__ __forceinline__ float value(uint16_t b) {
+    return __bfloat162float(__ushort_as_bfloat16(b));
+  }
+};
+template <>
+struct Half16<__half> {
+  static constexpr uint32_t kFmt = 0;   // kind::f16 operand format code for fp16
+  static __device__ __forceinline__ uint16_t bits(float v) {
+    return __half_as_ushort(__float2half_rn(v));
+  }
+  static __device__ __forceinline__ float value(uint16_t b) {
+    return __half2float(__ushort_as_half(b));
+  }
+};
+
+// Forward / dgrad epilogue of 32 tokens: r[j] is this lane's column w of token
+// row0 + j; the lanes of a warp hold 32 neighbouring columns.  Two neighbouring
+// lanes swap halves so that each holds both columns of every other token, and
+// a store instruction writes two tokens' 64 bytes (two full sectors each) in
+// 4-byte pieces.  `live` tokens are stored, columns below W (W is even: a
+// multiple of 8).
+template <typename T>
+__device__ __forceinline__ void rag_store_tokens32(const uint32_t (&r)[32], float bias,
+                                                   uint16_t* out, long long ldo, int live,
+                                                   int w, int W, int lane) {
+  const bool odd = lane & 1;
+  uint16_t* p = out + (odd ? ldo - 1 : 0);   // odd lanes: the next token, the column before
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    const uint32_t a = Half16<T>::bits(__uint_as_float(r[j]) + bias);
+    const uint32_t b = Half16<T>::bits(__uint_as_float(r[j + 1]) + bias);
+    // even lanes give away token j + 1, odd lanes token j
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+    const uint32_t v = odd ? (got | (b << 16)) : (a | (got << 16));
+    if (j + (odd ? 1 : 0) < live && w < W)
+      *reinterpret_cast<uint32_t*>(p + (long long)j * ldo) = v;
+  }
+}
+
+// wgrad epilogue of 32 columns of one row of dw: n columns are inside (a
+// multiple of 8; at least 1 column).
+template <typename T>
+__device__ __forceinline__ void rag_store_row32(const uint32_t (&r)[32], uint16_t* dst, int n,
+                                                bool accumulate) {
+  uint32_t w[16];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (8 * q < n) {
+      uint4 old = make_uint4(0, 0, 0, 0);
+      if (accumulate) old = *reinterpret_cast<const uint4*>(dst + 8 * q);
+      const uint32_t o[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v0 = __uint_as_float(r[8 * q + 2 * i]), v1 = __uint_as_float(r[8 * q + 2 * i + 1]);
+        if (accumulate) {
+          v0 += Half16<T>::value((uint16_t)(o[i] & 0xFFFFu));
+          v1 += Half16<T>::value((uint16_t)(o[i] >> 16));
+        }
+        w[4 * q + i] = (uint32_t)Half16<T>::bits(v0) | ((uint32_t)Half16<T>::bits(v1) << 16);
+      }
+    }
+  }
+  if (n >= 32) {
+    st_row64(dst, w);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (8 * q < n)
+        *reinterpret_cast<uint4*>(dst + 8 * q) =
+            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  }
+}
+__device__ __forceinline__ void rag_store_row32_f32(const uint32_t (&r)[32], float* dst, int n,
+                                                    bool accumulate) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    if (4 * q < n) {
+      float4 v = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                             __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+      float4* d = reinterpret_cast<float4*>(dst + 4 * q);
+      if (accumulate) {
+        const float4 o = *d;
+        v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+      }
+      *d = v;
+    }
+  }
+}
+
+}  // namespace moe
