@@ -46,7 +46,7 @@ RaggedProblem ragged_problem(const moe_ragged* p, const int32_t* offsets) {
 bool mxfp4_shape(const moe_ragged* p) { return p->N % 128 == 0 && p->K % 128 == 0; }
 
 size_t ragged_bytes(const moe_ragged* p) {
-  size_t b = ragged_maps_bytes(p->E);
+  size_t b = 1;
   if (mxfp4_shape(p)) b = std::max(b, ragged_mxfp4_scale_bytes(p->R, p->K, p->E));
   return pad256(b);
 }
@@ -108,11 +108,8 @@ moe_status ragged_gemm_wgrad(const moe_ragged* p, const void* dy, const void* x,
     const size_t bytes = (size_t)p->E * p->N * p->K * (dw_dtype == MOE_T_FP32 ? 4 : 2);
     return done(cudaMemsetAsync(dw, 0, bytes, st));
   }
-  const RaggedProblem q = ragged_problem(p, expert_offsets);
-  cudaError_t e = launch_ragged_maps(q, dy, x, workspace, st);
-  if (e == cudaSuccess)
-    e = launch_ragged_wgrad(q, workspace, dw, dw_dtype == MOE_T_FP32, accumulate != 0, st);
-  return done(e);
+  return done(launch_ragged_wgrad(ragged_problem(p, expert_offsets), dy, x, dw,
+                                  dw_dtype == MOE_T_FP32, accumulate != 0, st));
 }
 
 moe_status ragged_gemm_mxfp4(const moe_ragged* p, const void* x_codes, const void* x_scales,

@@ -211,13 +211,8 @@ struct RaggedProblem {
 // as moe_ragged_workspace_bytes.
 cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows, const void* w,
                                const void* bias, void* out, cudaStream_t stream);
-// Tensor maps of dy and x cut to each expert's rows, ragged_maps_bytes(E) at
-// `workspace` (64-byte aligned), and the product that loads through them.
-size_t ragged_maps_bytes(int E);
-cudaError_t launch_ragged_maps(const RaggedProblem& p, const void* dy, const void* x,
-                               void* workspace, cudaStream_t stream);
-cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* maps, void* dw, bool out_f32,
-                                bool accumulate, cudaStream_t stream);
+cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const void* x, void* dw,
+                                bool out_f32, bool accumulate, cudaStream_t stream);
 // 4-bit product: x codes / scales [R, K/2] / [R, K/32], weights [E, N, K/2] with
 // packed scales; token scales are first rewritten to workspace.
 size_t ragged_mxfp4_scale_bytes(int R, int K, int E);

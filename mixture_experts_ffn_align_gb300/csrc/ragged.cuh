@@ -45,7 +45,6 @@ struct RagArgs {
   const void* bias;         // forward: [E, N] in the operands' type, or null
   int out_f32;              // wgrad: dw is fp32
   int accumulate;           // wgrad: dw += instead of dw =
-  const CUtensorMap* maps;  // wgrad: maps of dy and x cut to each expert's rows
   int splits;               // forward, dgrad on one SM: slices of the reduction
   float* part;              // their fp32 sums [splits, R, W]
   int* tile_ctr;            // SM pairs: {next tile, CTAs finished}
@@ -191,6 +190,41 @@ __device__ __forceinline__ RagWTile rag_wtile(const RagArgs& a, int t) {
   return T;
 }
 
+// {first row, rows} of every expert, with and without rows, for wgrad, which
+// visits them all.  Takes the table's memory (the schedule's arrays are gone
+// afterwards); scratch: E int2 of shared memory free until this returns.  Every
+// thread calls it.
+__device__ __forceinline__ const int2* rag_rows_by_expert(const RagSched& s, int E, int* mem,
+                                                          int2* scratch) {
+  for (int e = threadIdx.x; e < E; e += blockDim.x) scratch[e] = make_int2(0, 0);
+  __syncthreads();
+  for (int i = threadIdx.x; i < s.nseg; i += blockDim.x)
+    scratch[s.exp[i]] = make_int2(s.row0[i], s.cnt[i]);
+  __syncthreads();
+  int2* out = reinterpret_cast<int2*>(mem + 4);
+  for (int e = threadIdx.x; e < E; e += blockDim.x) out[e] = scratch[e];
+  fence_proxy_async_smem();   // scratch lies where TMA writes next
+  __syncthreads();
+  return out;
+}
+
+// Zeros rows [from, to) of BOXES consecutive 64-row boxes (128 bytes a row;
+// swizzling permutes within a row) at shared address base, by one warp, before
+// the MMA that reads them.
+template <int BOXES>
+__device__ __forceinline__ void rag_zero_rows(uint32_t base, int from, int to, int lane) {
+  if (from >= to) return;
+  const int per = (to - from) * 8;       // 16-byte pieces of a box
+  for (int b = 0; b < BOXES; ++b)
+    for (int i = lane; i < per; i += 32)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + b * 8192 + from * 128 +
+                                                                   i * 16),
+                   "r"(0)
+                   : "memory");
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // Descriptor of an MN-major tile written by TMA with 128-byte swizzling: 64
 // values of M (or N) a row, one row for each step of the reduction, 64 rows a
 // box; 8-row atoms of 1024 bytes follow one another along the reduction
@@ -226,13 +260,6 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       "l"(policy)
       : "memory");
 }
-// A tensor map that an earlier kernel wrote: order its use after that write.
-__device__ __forceinline__ void tensormap_acquire(const CUtensorMap* map) {
-  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(
-                   reinterpret_cast<uint64_t>(map))
-               : "memory");
-}
-
 // fp32 <-> the operands' 16-bit types.
 template <typename T>
 struct Half16;

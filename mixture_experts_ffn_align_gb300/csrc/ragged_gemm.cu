@@ -13,10 +13,10 @@
 //  * dgrad reads w[e] with the reduction along its rows: the same boxes in the
 //    MMA's MN-major form, so no transposed copy of the weights exists.
 //  * wgrad reduces over an expert's rows, both operands MN-major.  Its last
-//    step ends inside the segment: the tensor maps it loads through are cut to
-//    the expert's rows (k_ragged_maps below writes them), so the rows behind
-//    come in as zeros, and an infinity or NaN of the next expert's rows
-//    cannot enter a sum as 0 x inf.
+//    step may end inside the 16 rows of an instruction: the MMA warp then
+//    writes zeros over the rows behind the segment in both operands (in one
+//    alone, an infinity or NaN of the next expert's rows would enter the sums as
+//    0 x inf).
 //  * every wait is bounded (wall clock); on a timeout the kernel records the
 //    error, drains its own copies and MMAs, frees tensor memory and returns.
 #include <algorithm>
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (OP != RAG_WGRAD && warp == 0 && lane == 0) {
+  if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
@@ -91,18 +91,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem_base = *tmem_holder;
 
   const RagSched sched = rag_sched_build<16>(args, s_sched, reinterpret_cast<int*>(smem));
-  int* s_cnt = s_sched + 4;     // wgrad: rows of each expert, over the table just built
-  if (OP == RAG_WGRAD) {
-    // the table lists experts with rows only; wgrad visits every expert
-    int* by_e = reinterpret_cast<int*>(smem);
-    for (int e = threadIdx.x; e < args.E; e += blockDim.x) by_e[e] = 0;
-    __syncthreads();
-    for (int s = threadIdx.x; s < sched.nseg; s += blockDim.x) by_e[sched.exp[s]] = sched.cnt[s];
-    __syncthreads();
-    for (int e = threadIdx.x; e < args.E; e += blockDim.x) s_cnt[e] = by_e[e];
-    fence_proxy_async_smem();   // by_e lies where TMA writes next
-    __syncthreads();
-  }
+  const int2* s_rows = OP == RAG_WGRAD
+                           ? rag_rows_by_expert(sched, args.E, s_sched, reinterpret_cast<int2*>(smem))
+                           : nullptr;
   const int total = OP == RAG_WGRAD ? args.E * args.w_tiles * args.k_tiles
                                     : sched.tile0[sched.nseg] * args.w_tiles;
   const int stages = args.stages;
@@ -115,22 +106,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int stage = 0;
     uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
     bool skip_first = args.never_arrive != 0;
-    int last_e = -1;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
       RagTile D{};
       RagWTile V{};
-      const CUtensorMap *mdy = nullptr, *mx = nullptr;
-      int kb_n = args.num_kb, boxes = 4;
+      int kb_n = args.num_kb, boxes = 4, row0 = 0;
       if (OP == RAG_WGRAD) {
         V = rag_wtile(args, t);
-        kb_n = (s_cnt[V.e] + BK - 1) / BK;
-        mdy = args.maps + 2 * V.e;
-        mx = mdy + 1;
-        if (V.e != last_e && kb_n > 0) {
-          tensormap_acquire(mdy);
-          tensormap_acquire(mx);
-          last_e = V.e;
-        }
+        kb_n = (s_rows[V.e].y + BK - 1) / BK;
+        row0 = s_rows[V.e].x;
       } else {
         D = rag_tile<16>(sched, args, t);
         boxes = (D.rows + 31) / 32;
@@ -150,10 +133,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mbar_arrive_expect_tx(bar, A_BYTES + 256 * BK * 2);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              tma_load_2d(sa + j * 8192, mdy, bar, V.n_tile * 128 + 64 * j, kb * BK, pol_t);
+              tma_load_2d(sa + j * 8192, &tmA, bar, V.n_tile * 128 + 64 * j, row0 + kb * BK, pol_t);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              tma_load_2d(sb + j * 8192, mx, bar, V.k_tile * 256 + 64 * j, kb * BK, pol_t);
+              tma_load_2d(sb + j * 8192, &tmB, bar, V.k_tile * 256 + 64 * j, row0 + kb * BK, pol_t);
           } else {
             mbar_arrive_expect_tx(bar, A_BYTES + boxes * 32 * BK * 2);
             if (OP == RAG_FWD) {
@@ -178,54 +161,67 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int s = 0; s < stages; ++s)
       if (issued_mask & (1u << s))
         mbar_wait_bounded(full_bar(s), (issued_parity >> s) & 1, nullptr, args.limit_ns, args.err);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1 && (OP == RAG_WGRAD || lane == 0)) {
     // ------------------------------------------------------------ MMA issuer
+    // wgrad: the whole warp walks along, to zero the rows behind a segment
     constexpr uint32_t major = (OP != RAG_FWD ? kIdescAMn : 0u) | (OP == RAG_WGRAD ? kIdescBMn : 0u);
     constexpr uint32_t a_step = OP != RAG_FWD ? 128 : 2, b_step = OP == RAG_WGRAD ? 128 : 2;
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+      return mbar_wait_bounded(bar, parity, abort_flag, args.limit_ns, args.err);
+    };
+    auto all = [&](bool ok) -> bool { return OP != RAG_WGRAD || __all_sync(0xffffffffu, ok) ? ok : false; };
     int stage = 0;
     uint32_t phase = 0;
     int local = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      int kb_n = args.num_kb, n = 256;
+      int kb_n = args.num_kb, n = 256, cnt = 0;
       if (OP == RAG_WGRAD) {
-        kb_n = (s_cnt[rag_wtile(args, t).e] + BK - 1) / BK;
+        cnt = s_rows[rag_wtile(args, t).e].y;
+        kb_n = (cnt + BK - 1) / BK;
         if (kb_n == 0) continue;
       } else {
         n = (rag_tile<16>(sched, args, t).rows + 15) / 16 * 16;
       }
       const uint32_t idesc = make_idesc(Half16<T>::kFmt, Half16<T>::kFmt, 128, n) | major;
       const int acc = local & 1;
-      if (!mbar_wait_bounded(tempty_bar(acc), ((local >> 1) & 1) ^ 1, abort_flag, args.limit_ns,
-                             args.err))
-        break;
+      if (!all(wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1))) break;
       tc_fence_after();
       bool ok = true;
       for (int kb = 0; kb < kb_n; ++kb) {
-        if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, args.limit_ns, args.err)) {
+        if (!all(wait(full_bar(stage), phase))) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t sa = smem_base + stage * stage_bytes;
+        int steps = BK / 16;
+        if (OP == RAG_WGRAD && kb == kb_n - 1) {
+          const int rem = cnt - kb * BK;
+          steps = (rem + 15) / 16;
+          rag_zero_rows<6>(sa, rem, 16 * steps, lane);
+        }
         const uint64_t adesc = OP != RAG_FWD ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
         const uint64_t bdesc = OP == RAG_WGRAD ? sdesc_mn_sw128(sa + A_BYTES)
                                                : sdesc_k_sw128(sa + A_BYTES);
-#pragma unroll
-        for (int k = 0; k < BK / 16; ++k)
-          umma_f16(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
-                   (kb | k) != 0);
-        tc_commit(empty_bar(stage));
+        if (lane == 0) {
+          for (int k = 0; k < steps; ++k)
+            umma_f16(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
+                     (kb | k) != 0);
+          tc_commit(empty_bar(stage));
+        }
         if (++stage == stages) {
           stage = 0;
           phase ^= 1;
         }
       }
       if (!ok) break;
-      tc_commit(tfull_bar(acc));
+      if (lane == 0) tc_commit(tfull_bar(acc));
       ++local;
     }
-    tc_commit(drain_bar);
-    mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+    if (lane == 0) {
+      tc_commit(drain_bar);
+      mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+    }
   } else if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
@@ -236,7 +232,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool empty = false;
       if (OP == RAG_WGRAD) {
         V = rag_wtile(args, t);
-        empty = s_cnt[V.e] == 0;
+        empty = s_rows[V.e].y == 0;
         if (empty && args.accumulate) continue;
       } else {
         D = rag_tile<16>(sched, args, t);
@@ -307,40 +303,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-// Tensor maps of dy and x cut to each expert's rows: the whole tensors' maps
-// with the base moved to the expert's first row and the row count replaced.
-// One warp per map; offsets clamped as in rag_sched_build.
-__global__ void k_ragged_maps(const __grid_constant__ CUtensorMap tmDy,
-                              const __grid_constant__ CUtensorMap tmX, const void* dy,
-                              const void* x, long long ld_dy_bytes, long long ld_x_bytes,
-                              const int32_t* offsets, int R, int E, CUtensorMap* maps) {
-  const int id = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int e = id >> 1;
-  if (e >= E) return;
-  // first row: the largest clamped offset up to e, as the running maximum gives it
-  int top = 0;
-  for (int i = lane; i <= e; i += 32) top = max(top, min(max(offsets[i], 0), R));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const int end = max(top, min(max(offsets[e + 1], 0), R));
-  const CUtensorMap* src = (id & 1) ? &tmX : &tmDy;
-  CUtensorMap* dst = maps + id;
-  reinterpret_cast<uint32_t*>(dst)[lane] = reinterpret_cast<const uint32_t*>(src)[lane];
-  __syncwarp();
-  if (lane == 0) {
-    const char* base = static_cast<const char*>((id & 1) ? x : dy) +
-                       (long long)top * ((id & 1) ? ld_x_bytes : ld_dy_bytes);
-    const uint64_t m = reinterpret_cast<uint64_t>(dst);
-    asm volatile("tensormap.replace.tile.global_address.global.b1024.b64 [%0], %1;" ::"l"(m),
-                 "l"(reinterpret_cast<uint64_t>(base))
-                 : "memory");
-    asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(m),
-                 "r"(max(end - top, 1))
-                 : "memory");
-    asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
-  }
-}
-
 template <int OP, typename T>
 cudaError_t launch_one(const CUtensorMap& tmA, const CUtensorMap& tmB, const RagArgs& a, int grid,
                        cudaStream_t stream) {
@@ -361,20 +323,6 @@ cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,
 }
 
 }  // namespace
-
-size_t ragged_maps_bytes(int E) { return (size_t)E * 2 * sizeof(CUtensorMap); }
-
-cudaError_t launch_ragged_maps(const RaggedProblem& p, const void* dy, const void* x,
-                               void* workspace, cudaStream_t stream) {
-  CUtensorMap tmDy, tmX;
-  if (!make_tmap_rag(&tmDy, dy, p.half, 2, p.N, p.R, 0, p.ldy, 64) ||
-      !make_tmap_rag(&tmX, x, p.half, 2, p.K, p.R, 0, p.ldx, 64))
-    return cudaErrorInvalidValue;
-  k_ragged_maps<<<(2 * p.E + 7) / 8, 256, 0, stream>>>(tmDy, tmX, dy, x, p.ldy * 2, p.ldx * 2,
-                                                       p.offsets, p.R, p.E,
-                                                       static_cast<CUtensorMap*>(workspace));
-  return cudaGetLastError();
-}
 
 cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows, const void* w,
                                const void* bias, void* out, cudaStream_t stream) {
@@ -409,8 +357,12 @@ cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows,
              : launch_op<RAG_DGRAD>(p.half, tmA, tmB, a, grid, stream);
 }
 
-cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* maps, void* dw, bool out_f32,
-                                bool accumulate, cudaStream_t stream) {
+cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const void* x, void* dw,
+                                bool out_f32, bool accumulate, cudaStream_t stream) {
+  CUtensorMap tmA, tmB;
+  if (!make_tmap_rag(&tmA, dy, p.half, 2, p.N, p.R, 0, p.ldy, 64) ||
+      !make_tmap_rag(&tmB, x, p.half, 2, p.K, p.R, 0, p.ldx, 64))
+    return cudaErrorInvalidValue;
   RagArgs a{};
   a.offsets = p.offsets;
   a.R = p.R;
@@ -425,14 +377,12 @@ cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* maps, void* 
   a.out = dw;
   a.out_f32 = out_f32;
   a.accumulate = accumulate;
-  a.maps = static_cast<const CUtensorMap*>(maps);
   watchdog_params(&a.limit_ns, &a.never_arrive);
   a.err = dev_error_word();
   if (a.err == nullptr) return cudaErrorInvalidDevice;
   const long long tiles = (long long)p.E * a.w_tiles * a.k_tiles;
   const int grid = (int)std::min<long long>(num_sms(), tiles);
-  CUtensorMap none{};
-  return launch_op<RAG_WGRAD>(p.half, none, none, a, grid, stream);
+  return launch_op<RAG_WGRAD>(p.half, tmA, tmB, a, grid, stream);
 }
 
 }  // namespace moe

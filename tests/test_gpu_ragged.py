@@ -269,6 +269,9 @@ def test_graph_replay_and_side_stream():
     assert all(bool((a == b).all()) for a, b in zip(got, (y, dx, dw)))
     X, W = f64(x), f64(w)
     check(y, ragged.forward(X, W, off), ragged.forward(abs(X), abs(W), off), k, torch.bfloat16, "y")
+    D = f64(dy)
+    check(dx, ragged.dgrad(D, W, off), ragged.dgrad(abs(D), abs(W), off), n, torch.bfloat16, "dx")
+    check(dw, ragged.wgrad(D, X, off), ragged.wgrad(abs(D), abs(X), off), 110, torch.bfloat16, "dw")
 
 
 def test_watchdog_reports_and_recovers():
