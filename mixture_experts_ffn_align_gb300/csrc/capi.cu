@@ -289,6 +289,7 @@ moe_status cuda_status(cudaError_t e) {
 
 namespace moe {
 int record_cuda_status(cudaError_t e) { return cuda_status(e); }
+int gemm_form() { return g_bf16_form; }
 }  // namespace moe
 
 namespace {

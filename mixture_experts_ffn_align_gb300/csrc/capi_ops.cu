@@ -46,9 +46,25 @@ RaggedProblem ragged_problem(const moe_ragged* p, const int32_t* offsets) {
 bool mxfp4_shape(const moe_ragged* p) { return p->N % 128 == 0 && p->K % 128 == 0; }
 
 size_t ragged_bytes(const moe_ragged* p) {
-  size_t b = 1;
+  size_t b = sizeof(int);     // the SM pairs' tile counter
   if (mxfp4_shape(p)) b = std::max(b, ragged_mxfp4_scale_bytes(p->R, p->K, p->E));
   return pad256(b);
+}
+
+// SM pairs pay from segments of about 128 rows up.
+bool use_pairs(const moe_ragged* p) {
+  const int form = gemm_form();
+  return form == 2 || (form == 0 && (int64_t)p->R >= 128ll * p->E);
+}
+
+cudaError_t ragged_rows(const moe_ragged* p, int op, const void* rows, const void* w,
+                        const void* bias, const int32_t* offsets, void* out, void* workspace,
+                        void* stream) {
+  const RaggedProblem q = ragged_problem(p, offsets);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return use_pairs(p)
+             ? launch_ragged_rows_2sm(q, op, rows, w, bias, out, static_cast<int*>(workspace), st)
+             : launch_ragged_rows(q, op, rows, w, bias, out, st);
 }
 
 // Checks shared by the products; MOE_OK to go on.
@@ -80,8 +96,7 @@ moe_status ragged_gemm(const moe_ragged* p, const void* x, const void* w, const 
   const moe_status s = ragged_args(p, x, w, expert_offsets, y, workspace, workspace_bytes);
   if (s != MOE_OK || p->R == 0) return s;
   if (misaligned(bias, 2)) return MOE_ERR_INVALID_ARG;
-  return done(launch_ragged_rows(ragged_problem(p, expert_offsets), 0, x, w, bias, y,
-                                 static_cast<cudaStream_t>(stream)));
+  return done(ragged_rows(p, 0, x, w, bias, expert_offsets, y, workspace, stream));
 }
 
 moe_status ragged_gemm_dgrad(const moe_ragged* p, const void* dy, const void* w,
@@ -89,8 +104,7 @@ moe_status ragged_gemm_dgrad(const moe_ragged* p, const void* dy, const void* w,
                              size_t workspace_bytes, void* stream) {
   const moe_status s = ragged_args(p, dy, w, expert_offsets, dx, workspace, workspace_bytes);
   if (s != MOE_OK || p->R == 0) return s;
-  return done(launch_ragged_rows(ragged_problem(p, expert_offsets), 1, dy, w, nullptr, dx,
-                                 static_cast<cudaStream_t>(stream)));
+  return done(ragged_rows(p, 1, dy, w, nullptr, expert_offsets, dx, workspace, stream));
 }
 
 moe_status ragged_gemm_wgrad(const moe_ragged* p, const void* dy, const void* x,
@@ -108,8 +122,11 @@ moe_status ragged_gemm_wgrad(const moe_ragged* p, const void* dy, const void* x,
     const size_t bytes = (size_t)p->E * p->N * p->K * (dw_dtype == MOE_T_FP32 ? 4 : 2);
     return done(cudaMemsetAsync(dw, 0, bytes, st));
   }
-  return done(launch_ragged_wgrad(ragged_problem(p, expert_offsets), dy, x, dw,
-                                  dw_dtype == MOE_T_FP32, accumulate != 0, st));
+  const RaggedProblem q = ragged_problem(p, expert_offsets);
+  const bool f32 = dw_dtype == MOE_T_FP32;
+  return done(use_pairs(p) ? launch_ragged_wgrad_2sm(q, dy, x, dw, f32, accumulate != 0,
+                                                     static_cast<int*>(workspace), st)
+                           : launch_ragged_wgrad(q, dy, x, dw, f32, accumulate != 0, st));
 }
 
 moe_status ragged_gemm_mxfp4(const moe_ragged* p, const void* x_codes, const void* x_scales,

@@ -1,0 +1,530 @@
+// Ragged grouped products on SM pairs (tcgen05 cta_group::2): forward, dgrad
+// and wgrad for segments of many rows (the formulas, the tile cut and the
+// epilogue stores are in ragged.cuh; the one-SM form is ragged_gemm.cu).
+//
+//  * a cluster of two CTAs computes 256 weights x up to 256 tokens (wgrad: 256
+//    rows x 256 columns of one expert's dw).  Each CTA stages its own 128
+//    weights and half of the tokens, 32 KB for a 64-deep step against 48 KB of
+//    the one-SM form for the same work an SM; the tensor core reads the other
+//    half of the tokens from the peer's shared memory.
+//  * six stages a CTA; both CTAs' copies complete on the leader's barrier, the
+//    leader's MMA thread issues M = 256, N = the tile's tokens rounded up to 32,
+//    K = 16 into one of two accumulators, and its commits reach both CTAs.
+//  * each CTA's warps 2-5 drain their own 128 accumulator rows.
+//  * tiles are handed out at run time by a counter in the workspace, zeroed on
+//    the stream before the launch, and passed to the other roles through a
+//    ring of four slots: with a fixed stride the pairs drift apart and weight
+//    tiles meant to be shared in L2 are read from HBM more than once.
+//  * wgrad's last step of a segment that ends inside the 16 rows of an
+//    instruction: each CTA's copies complete on a barrier of its own, its warp 1
+//    zeroes the rows behind the segment, and the peer's then signals the
+//    leader's.
+//  * every wait is bounded; the final cluster barrier is reached by both CTAs
+//    after their bounded loops.
+#include <algorithm>
+
+#include "moe_common.cuh"
+#include "moe_internal.h"
+#include "ragged.cuh"
+
+namespace moe {
+
+bool make_tmap_rag(CUtensorMap* map, const void* base, bool half, int rank, uint64_t d0,
+                   uint64_t d1, uint64_t d2, uint64_t ld, uint32_t box1);
+
+namespace {
+
+constexpr int BK = 64, STAGES = 6;
+constexpr int A_BYTES = 128 * BK * 2, B_BYTES = 128 * BK * 2;   // this CTA's halves
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int PAIR_TX = 2 * STAGE_BYTES;
+constexpr int TMEM_COLS = 512;
+constexpr int NUM_THREADS = 192;
+constexpr int RING = 4;
+constexpr int BAR_BYTES = 512;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + BAR_BYTES + kRagSchedBytes;
+static_assert(SMEM_BYTES <= 232448, "shared memory");
+
+template <int OP, typename T>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    k_ragged_2sm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const RagArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
+  // full[S], empty[S], tail[S], zeroed[S], tfull[2], tempty[2], drain, ring_full[RING],
+  // ring_empty[RING]
+  constexpr int NBARS = 4 * STAGES + 5 + 2 * RING;
+  static_assert(8 * NBARS + 8 + 4 * RING <= BAR_BYTES, "barrier area");
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* s_ring = reinterpret_cast<int*>(tmem_holder + 2);
+  int* s_sched = reinterpret_cast<int*>(smem + STAGES * STAGE_BYTES + BAR_BYTES);
+  // readers of a ring slot: the leader's MMA warp, the peer's producer, both
+  // CTAs' four epilogue warps, and in wgrad the peer's zeroing warp
+  constexpr int RING_READERS = OP == RAG_WGRAD ? 11 : 10;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const uint32_t smem_base = smem_u32(smem);
+  const uint32_t bar_base = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar_base + 8u * s; };
+  auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
+  auto tail_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + s); };
+  auto zeroed_bar = [&](int s) { return bar_base + 8u * (3 * STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (4 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar_base + 8u * (4 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar_base + 8u * (4 * STAGES + 4);
+  auto ring_full = [&](int i) { return bar_base + 8u * (4 * STAGES + 5 + i); };
+  auto ring_empty = [&](int i) { return bar_base + 8u * (4 * STAGES + 5 + RING + i); };
+  const uint32_t ring_base = smem_u32(s_ring);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 4 * STAGES; ++s) mbar_init(bar_base + 8u * s, 1);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 8);     // 4 epilogue warps in each CTA (leader's is used)
+    }
+    mbar_init(drain_bar, 1);
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(ring_full(i), 1);
+      mbar_init(ring_empty(i), RING_READERS);   // only the leader's are waited on
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc_pair(smem_u32(tmem_holder), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();        // both CTAs' barriers exist before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  const RagSched sched = rag_sched_build<32>(args, s_sched, reinterpret_cast<int*>(smem));
+  const int2* s_rows = OP == RAG_WGRAD
+                           ? rag_rows_by_expert(sched, args.E, s_sched, reinterpret_cast<int2*>(smem))
+                           : nullptr;
+  const int total = OP == RAG_WGRAD ? args.E * args.w_tiles * args.k_tiles
+                                    : sched.tile0[sched.nseg] * args.w_tiles;
+
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    return mbar_wait_bounded(bar, parity, abort_flag, args.limit_ns, args.err);
+  };
+  // Tile ring.  The leader's producer publishes tile j in slot j % RING
+  // (-1: no tiles left); every reader takes the slots in the same order.
+  auto ring_put = [&](int j, int t) -> bool {
+    const int slot = j & (RING - 1);
+    if (!mbar_wait_bounded<true>(ring_empty(slot), ((j / RING) & 1) ^ 1, abort_flag,
+                                 args.limit_ns, args.err))
+      return false;
+    s_ring[slot] = t;
+    st_shared_cluster(mapa_shared(ring_base + 4u * slot, 1), t);
+    mbar_arrive(ring_full(slot));
+    mbar_arrive_cluster(mapa_shared(ring_full(slot), 1));
+    return true;
+  };
+  auto ring_take = [&](int j) -> int {   // -2 when the wait ran out
+    const int slot = j & (RING - 1);
+    if (!mbar_wait_bounded<true>(ring_full(slot), (j / RING) & 1, abort_flag, args.limit_ns,
+                                 args.err))
+      return -2;
+    const int t = reinterpret_cast<volatile int*>(s_ring)[slot];
+    mbar_arrive_cluster(mapa_shared(ring_empty(slot), 0));
+    return t;
+  };
+  auto ring_take_warp = [&](int j) -> int {   // one read for the warp
+    int t = 0;
+    if (lane == 0) t = ring_take(j);
+    return __shfl_sync(0xffffffffu, t, 0);
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ producers
+    const uint64_t pol_w = l2_policy(0), pol_t = l2_policy(1);
+    int stage = 0;
+    uint32_t phase = 0, issued_mask = 0, issued_parity = 0, tail_mask = 0, tail_parity = 0;
+    bool skip_first = leader && args.never_arrive != 0;
+    int t_lead = -1, pending = 0;
+    bool ring_ok = true;
+    if (leader) {
+      const int f = atomicAdd(args.tile_ctr, 1);
+      t_lead = f < total ? f : -1;
+      ring_ok = ring_put(0, t_lead);
+      if (t_lead >= 0) pending = atomicAdd(args.tile_ctr, 1);
+    }
+    for (int j = 0;; ++j) {
+      int t;
+      if (leader) {
+        t = t_lead;
+        if (!ring_ok || t < 0) break;
+        t_lead = pending < total ? pending : -1;
+        ring_ok = ring_put(j + 1, t_lead);
+        if (t_lead >= 0) pending = atomicAdd(args.tile_ctr, 1);
+      } else {
+        t = ring_take(j);
+        if (t < 0) break;
+      }
+      RagTile D{};
+      RagWTile V{};
+      int kb_n = args.num_kb, row0, tail_kb = -1;
+      if (OP == RAG_WGRAD) {
+        V = rag_wtile(args, t);
+        const int2 rows = s_rows[V.e];
+        row0 = rows.x;
+        kb_n = (rows.y + BK - 1) / BK;
+        if (rows.y % 16) tail_kb = kb_n - 1;
+      } else {
+        D = rag_tile<32>(sched, args, t);
+        // this CTA's half of the token operand
+        row0 = D.row0 + (leader ? 0 : (D.rows + 31) / 32 * 16);
+      }
+      bool ok = true;
+      for (int kb = 0; kb < kb_n; ++kb) {
+        if (!wait(empty_bar(stage), phase ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (skip_first) {
+          skip_first = false;   // watchdog test: leave this stage unarmed
+        } else {
+          const uint32_t sa = smem_base + stage * STAGE_BYTES, sb = sa + A_BYTES;
+          uint32_t bar = mapa_shared(full_bar(stage), 0);
+          if (OP == RAG_WGRAD && kb == tail_kb) {
+            // copies of a step to be zeroed behind: counted on this CTA's own barrier
+            if (leader) mbar_arrive(full_bar(stage));
+            mbar_arrive_expect_tx(tail_bar(stage), STAGE_BYTES);
+            bar = mapa_shared(tail_bar(stage), rank);
+            tail_parity ^= 1u << stage;     // bit: parity of the next use's phase
+            tail_mask |= 1u << stage;
+          } else if (leader) {
+            mbar_arrive_expect_tx(full_bar(stage), PAIR_TX);
+          }
+          issued_mask |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (OP == RAG_WGRAD) {
+            const int n0 = V.n_tile * 256 + rank * 128, k0 = V.k_tile * 256 + rank * 128;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              tma_load_2d_pair(sa + i * 8192, &tmA, bar, n0 + 64 * i, row0 + kb * BK, pol_t);
+              tma_load_2d_pair(sb + i * 8192, &tmB, bar, k0 + 64 * i, row0 + kb * BK, pol_t);
+            }
+          } else {
+            const int w0 = D.w_tile * 256 + rank * 128;
+            if (OP == RAG_FWD) {
+              tma_load_3d_pair(sa, &tmA, bar, kb * BK, w0, D.e, pol_w);
+            } else {
+              tma_load_3d_pair(sa, &tmA, bar, w0, kb * BK, D.e, pol_w);
+              tma_load_3d_pair(sa + 8192, &tmA, bar, w0 + 64, kb * BK, D.e, pol_w);
+            }
+            tma_load_2d_pair(sb, &tmB, bar, kb * BK, row0, pol_t);
+          }
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+    }
+    // the leader's barrier counts both CTAs' copies: once its issued phases
+    // (and the own barrier's) complete, every copy has landed
+    for (int s = 0; s < STAGES; ++s) {
+      if (leader && (issued_mask & (1u << s)))
+        mbar_wait_bounded(full_bar(s), (issued_parity >> s) & 1, nullptr, args.limit_ns, args.err);
+      if (tail_mask & (1u << s))
+        mbar_wait_bounded(tail_bar(s), ((tail_parity >> s) & 1) ^ 1, nullptr, args.limit_ns,
+                          args.err);
+    }
+  } else if (warp == 1 && leader && (OP == RAG_WGRAD || lane == 0)) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t major = (OP != RAG_FWD ? kIdescAMn : 0u) | (OP == RAG_WGRAD ? kIdescBMn : 0u);
+    constexpr uint32_t a_step = OP != RAG_FWD ? 128 : 2, b_step = OP == RAG_WGRAD ? 128 : 2;
+    auto all = [&](bool ok) -> bool {
+      if (OP == RAG_WGRAD) return __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    int stage = 0;
+    uint32_t phase = 0, tail_parity = 0;
+    int local = 0;
+    for (int j = 0;; ++j) {
+      const int t = OP == RAG_WGRAD ? ring_take_warp(j) : ring_take(j);
+      if (t < 0) break;
+      int kb_n = args.num_kb, n = 256, cnt = 0;
+      if (OP == RAG_WGRAD) {
+        cnt = s_rows[rag_wtile(args, t).e].y;
+        kb_n = (cnt + BK - 1) / BK;
+        if (kb_n == 0) continue;
+      } else {
+        n = (rag_tile<32>(sched, args, t).rows + 31) / 32 * 32;
+      }
+      const uint32_t idesc = make_idesc(Half16<T>::kFmt, Half16<T>::kFmt, 256, n) | major;
+      const int acc = local & 1;
+      if (!all(wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1))) break;
+      tc_fence_after();
+      bool ok = true;
+      for (int kb = 0; kb < kb_n; ++kb) {
+        if (!all(wait(full_bar(stage), phase))) {
+          ok = false;
+          break;
+        }
+        const uint32_t sa = smem_base + stage * STAGE_BYTES;
+        int steps = BK / 16;
+        if (OP == RAG_WGRAD && kb == kb_n - 1) {
+          const int rem = cnt - kb * BK;
+          steps = (rem + 15) / 16;
+          if (rem % 16) {
+            const uint32_t par = (tail_parity >> stage) & 1;
+            tail_parity ^= 1u << stage;
+            if (!all(wait(tail_bar(stage), par))) {
+              ok = false;
+              break;
+            }
+            rag_zero_rows<4>(sa, rem, 16 * steps, lane);
+            // the peer has zeroed its rows
+            if (!all(mbar_wait_bounded<true>(zeroed_bar(stage), par, abort_flag, args.limit_ns,
+                                             args.err))) {
+              ok = false;
+              break;
+            }
+          }
+        }
+        tc_fence_after();
+        const uint64_t adesc = OP != RAG_FWD ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
+        const uint64_t bdesc = OP == RAG_WGRAD ? sdesc_mn_sw128(sa + A_BYTES)
+                                               : sdesc_k_sw128(sa + A_BYTES);
+        if (lane == 0) {
+          for (int k = 0; k < steps; ++k)
+            umma_f16_pair(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
+                          (kb | k) != 0);
+          tc_commit_pair(empty_bar(stage), 0x3);
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (lane == 0) tc_commit_pair(tfull_bar(acc), 0x3);
+      ++local;
+    }
+    if (lane == 0) {
+      tc_commit_pair(drain_bar, 0x1);
+      mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+    }
+  } else if (OP == RAG_WGRAD && warp == 1 && !leader) {
+    // ------------------------------------------------------------ peer's zeroing warp
+    int stage = 0;
+    uint32_t tail_parity = 0;
+    for (int j = 0;; ++j) {
+      const int t = ring_take_warp(j);
+      if (t < 0) break;
+      const int cnt = s_rows[rag_wtile(args, t).e].y;
+      const int kb_n = (cnt + BK - 1) / BK;
+      if (cnt % 16) {
+        const int s = (stage + kb_n - 1) % STAGES;      // stage of the last step
+        const uint32_t par = (tail_parity >> s) & 1;
+        tail_parity ^= 1u << s;
+        if (!__all_sync(0xffffffffu, wait(tail_bar(s), par))) break;
+        const int rem = cnt - (kb_n - 1) * BK;
+        rag_zero_rows<4>(smem_base + s * STAGE_BYTES, rem, (rem + 15) / 16 * 16, lane);
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(zeroed_bar(s), 0));
+      }
+      stage = (stage + kb_n) % STAGES;
+    }
+  } else if (warp >= 2) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;
+    int local = 0;
+    for (int j = 0;; ++j) {
+      const int t = ring_take_warp(j);
+      if (t < 0) break;
+      RagTile D{};
+      RagWTile V{};
+      bool empty = false;
+      if (OP == RAG_WGRAD) {
+        V = rag_wtile(args, t);
+        empty = s_rows[V.e].y == 0;
+        if (empty && args.accumulate) continue;
+      } else {
+        D = rag_tile<32>(sched, args, t);
+      }
+      const int acc = local & 1;
+      if (!empty) {
+        int ok = 0;
+        if (lane == 0) ok = wait(tfull_bar(acc), (local >> 1) & 1);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
+      if (OP == RAG_WGRAD) {
+        const int n = V.n_tile * 256 + rank * 128 + q * 32 + lane, k0 = V.k_tile * 256;
+        const size_t at = ((size_t)V.e * args.N + n) * args.K + k0;
+#pragma unroll 1
+        for (int c = 0; c < 256 && k0 + c < args.K; c += 32) {
+          uint32_t r[32];
+          if (empty) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0;
+          } else {
+            tmem_ld_32x32b_x32(taddr + c, r);
+            tmem_ld_wait();
+          }
+          if (n >= args.N) continue;
+          if (args.out_f32)
+            rag_store_row32_f32(r, static_cast<float*>(args.out) + at + c, args.K - k0 - c,
+                                args.accumulate);
+          else
+            rag_store_row32<T>(r, static_cast<uint16_t*>(args.out) + at + c, args.K - k0 - c,
+                               args.accumulate);
+        }
+      } else {
+        const int w = D.w_tile * 256 + rank * 128 + q * 32 + lane;
+        float bias = 0.0f;
+        if (OP == RAG_FWD && args.bias != nullptr && w < args.W)
+          bias = Half16<T>::value(
+              static_cast<const uint16_t*>(args.bias)[(size_t)D.e * args.W + w]);
+#pragma unroll 1
+        for (int c = 0; c < D.rows; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(taddr + c, r);
+          tmem_ld_wait();
+          rag_store_tokens32<T>(r, bias,
+                                static_cast<uint16_t*>(args.out) + (D.row0 + c) * args.ldo + w,
+                                args.ldo, D.rows - c, w, args.W, lane);
+        }
+      }
+      if (!empty) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+        ++local;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) {
+    // after a timeout, give copies the other CTA may still have in flight
+    // into this CTA's shared memory time to land before the pair exits
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+template <int OP, typename T>
+cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB, const RagArgs& a,
+                        long long tiles, cudaStream_t stream) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  static DeviceOnce setup;
+  static int max_pairs[kMaxDevices];
+  const int dev = device_index();
+  const cudaError_t es = setup.call([&] {
+    cudaError_t e = cudaFuncSetAttribute(k_ragged_2sm<OP, T>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(num_sms(), 1, 1);
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, k_ragged_2sm<OP, T>, &cfg);
+    if (e != cudaSuccess) return e;
+    max_pairs[dev] = n;
+    return cudaSuccess;
+  });
+  if (es != cudaSuccess) return es;
+  if (max_pairs[dev] <= 0) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(max_pairs[dev], tiles), 1, 1);
+  cfg.stream = stream;
+  const cudaError_t e = cudaMemsetAsync(a.tile_ctr, 0, sizeof(int), stream);
+  if (e != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&cfg, k_ragged_2sm<OP, T>, tmA, tmB, a);
+}
+template <int OP>
+cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB, const RagArgs& a,
+                      long long tiles, cudaStream_t stream) {
+  return half ? launch_pair<OP, __half>(tmA, tmB, a, tiles, stream)
+              : launch_pair<OP, __nv_bfloat16>(tmA, tmB, a, tiles, stream);
+}
+
+bool common(const RaggedProblem& p, RagArgs& a, int* tile_ctr) {
+  a.offsets = p.offsets;
+  a.R = p.R;
+  a.E = p.E;
+  a.tile_rows = 256;
+  a.group_max = 8;
+  a.tile_ctr = tile_ctr;
+  watchdog_params(&a.limit_ns, &a.never_arrive);
+  a.err = dev_error_word();
+  return a.err != nullptr;
+}
+
+}  // namespace
+
+cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* rows, const void* w,
+                                   const void* bias, void* out, int* tile_ctr,
+                                   cudaStream_t stream) {
+  const bool fwd = op == RAG_FWD;
+  CUtensorMap tmA, tmB;
+  const int red = fwd ? p.K : p.N;
+  if (!make_tmap_rag(&tmA, w, p.half, 3, p.K, p.N, p.E, p.K, fwd ? 128 : 64) ||
+      !make_tmap_rag(&tmB, rows, p.half, 2, red, p.R, 0, fwd ? p.ldx : p.ldy, 128))
+    return cudaErrorInvalidValue;
+  RagArgs a{};
+  if (!common(p, a, tile_ctr)) return cudaErrorInvalidDevice;
+  a.W = fwd ? p.N : p.K;
+  a.num_kb = (red + BK - 1) / BK;
+  a.w_tiles = (a.W + 255) / 256;
+  a.out = out;
+  a.ldo = fwd ? p.ldy : p.ldx;
+  a.bias = bias;
+  const long long tiles = ((long long)std::min(p.E, p.R) + p.R / 256) * a.w_tiles;   // at most
+  return fwd ? launch_op<RAG_FWD>(p.half, tmA, tmB, a, tiles, stream)
+             : launch_op<RAG_DGRAD>(p.half, tmA, tmB, a, tiles, stream);
+}
+
+cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, const void* x,
+                                    void* dw, bool out_f32, bool accumulate, int* tile_ctr,
+                                    cudaStream_t stream) {
+  CUtensorMap tmA, tmB;
+  if (!make_tmap_rag(&tmA, dy, p.half, 2, p.N, p.R, 0, p.ldy, 64) ||
+      !make_tmap_rag(&tmB, x, p.half, 2, p.K, p.R, 0, p.ldx, 64))
+    return cudaErrorInvalidValue;
+  RagArgs a{};
+  if (!common(p, a, tile_ctr)) return cudaErrorInvalidDevice;
+  a.N = p.N;
+  a.K = p.K;
+  a.w_tiles = (p.N + 255) / 256;
+  a.k_tiles = (p.K + 255) / 256;
+  a.out = dw;
+  a.out_f32 = out_f32;
+  a.accumulate = accumulate;
+  return launch_op<RAG_WGRAD>(p.half, tmA, tmB, a, (long long)p.E * a.w_tiles * a.k_tiles, stream);
+}
+
+}  // namespace moe

@@ -21,6 +21,15 @@ from oracle import ragged
 pytestmark = pytest.mark.gpu
 DT = {"bfloat16": torch.bfloat16, "float16": torch.float16}
 
+
+@pytest.fixture(autouse=True, params=["single", "pairs"])
+def form(request):
+    """Every test in both forms of the kernels."""
+    moe.moe_debug_set_bf16_gemm_form(request.param)
+    yield
+    moe.moe_debug_set_bf16_gemm_form("auto")
+
+
 # rows of each expert; offsets may leave rows in front (lead) and behind (tail)
 SEGMENTS = {
     "one_row": [1],
