@@ -46,7 +46,7 @@ RaggedProblem ragged_problem(const moe_ragged* p, const int32_t* offsets) {
 bool mxfp4_shape(const moe_ragged* p) { return p->N % 128 == 0 && p->K % 128 == 0; }
 
 size_t ragged_bytes(const moe_ragged* p) {
-  size_t b = sizeof(int);     // the SM pairs' tile counter
+  size_t b = 1;
   if (mxfp4_shape(p)) b = std::max(b, ragged_mxfp4_scale_bytes(p->R, p->K, p->E));
   return pad256(b);
 }
@@ -58,12 +58,11 @@ bool use_pairs(const moe_ragged* p) {
 }
 
 cudaError_t ragged_rows(const moe_ragged* p, int op, const void* rows, const void* w,
-                        const void* bias, const int32_t* offsets, void* out, void* workspace,
-                        void* stream) {
+                        const void* bias, const int32_t* offsets, void* out, void* stream) {
   const RaggedProblem q = ragged_problem(p, offsets);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return use_pairs(p)
-             ? launch_ragged_rows_2sm(q, op, rows, w, bias, out, static_cast<int*>(workspace), st)
+             ? launch_ragged_rows_2sm(q, op, rows, w, bias, out, st)
              : launch_ragged_rows(q, op, rows, w, bias, out, st);
 }
 
@@ -96,7 +95,7 @@ moe_status ragged_gemm(const moe_ragged* p, const void* x, const void* w, const 
   const moe_status s = ragged_args(p, x, w, expert_offsets, y, workspace, workspace_bytes);
   if (s != MOE_OK || p->R == 0) return s;
   if (misaligned(bias, 2)) return MOE_ERR_INVALID_ARG;
-  return done(ragged_rows(p, 0, x, w, bias, expert_offsets, y, workspace, stream));
+  return done(ragged_rows(p, 0, x, w, bias, expert_offsets, y, stream));
 }
 
 moe_status ragged_gemm_dgrad(const moe_ragged* p, const void* dy, const void* w,
@@ -104,7 +103,7 @@ moe_status ragged_gemm_dgrad(const moe_ragged* p, const void* dy, const void* w,
                              size_t workspace_bytes, void* stream) {
   const moe_status s = ragged_args(p, dy, w, expert_offsets, dx, workspace, workspace_bytes);
   if (s != MOE_OK || p->R == 0) return s;
-  return done(ragged_rows(p, 1, dy, w, nullptr, expert_offsets, dx, workspace, stream));
+  return done(ragged_rows(p, 1, dy, w, nullptr, expert_offsets, dx, stream));
 }
 
 moe_status ragged_gemm_wgrad(const moe_ragged* p, const void* dy, const void* x,
@@ -124,8 +123,7 @@ moe_status ragged_gemm_wgrad(const moe_ragged* p, const void* dy, const void* x,
   }
   const RaggedProblem q = ragged_problem(p, expert_offsets);
   const bool f32 = dw_dtype == MOE_T_FP32;
-  return done(use_pairs(p) ? launch_ragged_wgrad_2sm(q, dy, x, dw, f32, accumulate != 0,
-                                                     static_cast<int*>(workspace), st)
+  return done(use_pairs(p) ? launch_ragged_wgrad_2sm(q, dy, x, dw, f32, accumulate != 0, st)
                            : launch_ragged_wgrad(q, dy, x, dw, f32, accumulate != 0, st));
 }
 

@@ -137,7 +137,7 @@ __device__ __forceinline__ void chunk_scale(const Item& t, int64_t begin, int64_
         } else {
           using T = typename std::conditional<TYPE == 1, __half, __nv_bfloat16>::type;
           const float2 f = unpack<TYPE>(w[j]);
-          w[j] = (uint32_t)Half16<T>::bits(f.x * c) | ((uint32_t)Half16<T>::bits(f.y * c) << 16);
+          w[j] = Half16<T>::pack(f.x * c, f.y * c);
         }
       }
       if (at < nv) d[at] = make_uint4(w[0], w[1], w[2], w[3]);

@@ -213,13 +213,12 @@ cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows,
                                const void* bias, void* out, cudaStream_t stream);
 cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const void* x, void* dw,
                                 bool out_f32, bool accumulate, cudaStream_t stream);
-// The same on SM pairs.  tile_ctr: one int of the caller's workspace, zeroed on
-// the stream before the launch.
+// The same on SM pairs.
 cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* rows, const void* w,
-                                   const void* bias, void* out, int* tile_ctr,
+                                   const void* bias, void* out,
                                    cudaStream_t stream);
 cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, const void* x,
-                                    void* dw, bool out_f32, bool accumulate, int* tile_ctr,
+                                    void* dw, bool out_f32, bool accumulate,
                                     cudaStream_t stream);
 // 0: by size, 1: one SM, 2: SM pairs (moe_debug_set_bf16_gemm_form).
 int gemm_form();

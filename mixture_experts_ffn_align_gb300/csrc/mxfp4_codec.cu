@@ -182,8 +182,7 @@ uint32_t h[4];
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          w[j] = (uint32_t)Half16<T>::bits(v[2 * j]) |
-                 ((uint32_t)Half16<T>::bits(v[2 * j + 1]) << 16);
+          w[j] = Half16<T>::pack(v[2 * j], v[2 * j + 1]);
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
             make_uint4(w[0], w[1], w[2], w[3]);
       }

@@ -47,7 +47,6 @@ struct RagArgs {
   int accumulate;           // wgrad: dw += instead of dw =
   int splits;               // forward, dgrad on one SM: slices of the reduction
   float* part;              // their fp32 sums [splits, R, W]
-  int* tile_ctr;            // SM pairs: {next tile, CTAs finished}
   uint64_t limit_ns;
   int never_arrive;
   int* err;
@@ -269,6 +268,10 @@ struct Half16<__nv_bfloat16> {
   static __device__ __forceinline__ uint16_t bits(float v) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
   }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
   static __device__ __forceinline__ float value(uint16_t b) {
     return __bfloat162float(__ushort_as_bfloat16(b));
   }
@@ -278,6 +281,10 @@ struct Half16<__half> {
   static constexpr uint32_t kFmt = 0;   // kind::f16 operand format code for fp16
   static __device__ __forceinline__ uint16_t bits(float v) {
     return __half_as_ushort(__float2half_rn(v));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
   }
   static __device__ __forceinline__ float value(uint16_t b) {
     return __half2float(__ushort_as_half(b));
@@ -289,23 +296,36 @@ struct Half16<__half> {
 // lanes swap halves so that each holds both columns of every other token, and
 // a store instruction writes two tokens' 64 bytes (two full sectors each) in
 // 4-byte pieces.  `live` tokens are stored, columns below W (W is even: a
-// multiple of 8).
-template <typename T>
-__device__ __forceinline__ void rag_store_tokens32(const uint32_t (&r)[32], float bias,
-                                                   uint16_t* out, long long ldo, int live,
-                                                   int w, int W, int lane) {
-  const bool odd = lane & 1;
-  uint16_t* p = out + (odd ? ldo - 1 : 0);   // odd lanes: the next token, the column before
+// multiple of 8).  Packed conversion, one shuffle and one byte permute for two
+// tokens: the warps are bound by instruction issue here, not by the stores.
+template <typename T, bool ALL>
+__device__ __forceinline__ void rag_store_tokens(const uint32_t (&r)[32], uint16_t* p,
+                                                 long long ldo, int live, bool inside, int lane) {
+  const uint32_t sel = (lane & 1) ? 0x3276u : 0x5410u;
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
-    const uint32_t a = Half16<T>::bits(__uint_as_float(r[j]) + bias);
-    const uint32_t b = Half16<T>::bits(__uint_as_float(r[j + 1]) + bias);
-    // even lanes give away token j + 1, odd lanes token j
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-    const uint32_t v = odd ? (got | (b << 16)) : (a | (got << 16));
-    if (j + (odd ? 1 : 0) < live && w < W)
-      *reinterpret_cast<uint32_t*>(p + (long long)j * ldo) = v;
+    const uint32_t own = Half16<T>::pack(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+    const uint32_t v = __byte_perm(own, other, sel);
+    if (ALL || (inside && j + (lane & 1) < live)) *reinterpret_cast<uint32_t*>(p) = v;
+    p += 2 * ldo;
   }
+}
+template <typename T>
+__device__ __forceinline__ void rag_store_tokens32(uint32_t (&r)[32], bool has_bias, float bias,
+                                                   uint16_t* out, long long ldo, int live, int w,
+                                                   int W, int lane) {
+  if (has_bias) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + bias);
+  }
+  // odd lanes: the next token, from the column before
+  uint16_t* p = out + ((lane & 1) ? ldo - 1 : 0);
+  const bool inside = w < W;
+  if (live >= 32 && __all_sync(0xffffffffu, inside))
+    rag_store_tokens<T, true>(r, p, ldo, live, inside, lane);
+  else
+    rag_store_tokens<T, false>(r, p, ldo, live, inside, lane);
 }
 
 // wgrad epilogue of 32 columns of one row of dw: n columns are inside (a
@@ -327,7 +347,7 @@ __device__ __forceinline__ void rag_store_row32(const uint32_t (&r)[32], uint16_
           v0 += Half16<T>::value((uint16_t)(o[i] & 0xFFFFu));
           v1 += Half16<T>::value((uint16_t)(o[i] >> 16));
         }
-        w[4 * q + i] = (uint32_t)Half16<T>::bits(v0) | ((uint32_t)Half16<T>::bits(v1) << 16);
+        w[4 * q + i] = Half16<T>::pack(v0, v1);
       }
     }
   }

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           uint32_t r[32];
           tmem_ld_32x32b_x32(taddr + c, r);
           tmem_ld_wait();
-          rag_store_tokens32<T>(r, bias,
+          rag_store_tokens32<T>(r, OP == RAG_FWD && args.bias != nullptr, bias,
                                 static_cast<uint16_t*>(args.out) + (D.row0 + c) * args.ldo + w,
                                 args.ldo, D.rows - c, w, args.W, lane);
         }

@@ -11,10 +11,6 @@
 //    leader's MMA thread issues M = 256, N = the tile's tokens rounded up to 32,
 //    K = 16 into one of two accumulators, and its commits reach both CTAs.
 //  * each CTA's warps 2-5 drain their own 128 accumulator rows.
-//  * tiles are handed out at run time by a counter in the workspace, zeroed on
-//    the stream before the launch, and passed to the other roles through a
-//    ring of four slots: with a fixed stride the pairs drift apart and weight
-//    tiles meant to be shared in L2 are read from HBM more than once.
 //  * wgrad's last step of a segment that ends inside the 16 rows of an
 //    instruction: each CTA's copies complete on a barrier of its own, its warp 1
 //    zeroes the rows behind the segment, and the peer's then signals the
@@ -40,8 +36,7 @@ constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int PAIR_TX = 2 * STAGE_BYTES;
 constexpr int TMEM_COLS = 512;
 constexpr int NUM_THREADS = 192;
-constexpr int RING = 4;
-constexpr int BAR_BYTES = 512;
+constexpr int BAR_BYTES = 256;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + BAR_BYTES + kRagSchedBytes;
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 
@@ -53,18 +48,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
-  // full[S], empty[S], tail[S], zeroed[S], tfull[2], tempty[2], drain, ring_full[RING],
-  // ring_empty[RING]
-  constexpr int NBARS = 4 * STAGES + 5 + 2 * RING;
-  static_assert(8 * NBARS + 8 + 4 * RING <= BAR_BYTES, "barrier area");
+  // full[S], empty[S], tail[S], zeroed[S], tfull[2], tempty[2], drain
+  constexpr int NBARS = 4 * STAGES + 5;
+  static_assert(8 * NBARS + 8 <= BAR_BYTES, "barrier area");
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* s_ring = reinterpret_cast<int*>(tmem_holder + 2);
   int* s_sched = reinterpret_cast<int*>(smem + STAGES * STAGE_BYTES + BAR_BYTES);
-  // readers of a ring slot: the leader's MMA warp, the peer's producer, both
-  // CTAs' four epilogue warps, and in wgrad the peer's zeroing warp
-  constexpr int RING_READERS = OP == RAG_WGRAD ? 11 : 10;
-
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -77,9 +66,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto tfull_bar = [&](int a) { return bar_base + 8u * (4 * STAGES + a); };
   auto tempty_bar = [&](int a) { return bar_base + 8u * (4 * STAGES + 2 + a); };
   const uint32_t drain_bar = bar_base + 8u * (4 * STAGES + 4);
-  auto ring_full = [&](int i) { return bar_base + 8u * (4 * STAGES + 5 + i); };
-  auto ring_empty = [&](int i) { return bar_base + 8u * (4 * STAGES + 5 + RING + i); };
-  const uint32_t ring_base = smem_u32(s_ring);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 4 * STAGES; ++s) mbar_init(bar_base + 8u * s, 1);
@@ -88,10 +74,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(tempty_bar(a), 8);     // 4 epilogue warps in each CTA (leader's is used)
     }
     mbar_init(drain_bar, 1);
-    for (int i = 0; i < RING; ++i) {
-      mbar_init(ring_full(i), 1);
-      mbar_init(ring_empty(i), RING_READERS);   // only the leader's are waited on
-    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -120,33 +102,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
     return mbar_wait_bounded(bar, parity, abort_flag, args.limit_ns, args.err);
   };
-  // Tile ring.  The leader's producer publishes tile j in slot j % RING
-  // (-1: no tiles left); every reader takes the slots in the same order.
-  auto ring_put = [&](int j, int t) -> bool {
-    const int slot = j & (RING - 1);
-    if (!mbar_wait_bounded<true>(ring_empty(slot), ((j / RING) & 1) ^ 1, abort_flag,
-                                 args.limit_ns, args.err))
-      return false;
-    s_ring[slot] = t;
-    st_shared_cluster(mapa_shared(ring_base + 4u * slot, 1), t);
-    mbar_arrive(ring_full(slot));
-    mbar_arrive_cluster(mapa_shared(ring_full(slot), 1));
-    return true;
-  };
-  auto ring_take = [&](int j) -> int {   // -2 when the wait ran out
-    const int slot = j & (RING - 1);
-    if (!mbar_wait_bounded<true>(ring_full(slot), (j / RING) & 1, abort_flag, args.limit_ns,
-                                 args.err))
-      return -2;
-    const int t = reinterpret_cast<volatile int*>(s_ring)[slot];
-    mbar_arrive_cluster(mapa_shared(ring_empty(slot), 0));
-    return t;
-  };
-  auto ring_take_warp = [&](int j) -> int {   // one read for the warp
-    int t = 0;
-    if (lane == 0) t = ring_take(j);
-    return __shfl_sync(0xffffffffu, t, 0);
-  };
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;   // this pair's tiles
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ producers
@@ -154,26 +110,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int stage = 0;
     uint32_t phase = 0, issued_mask = 0, issued_parity = 0, tail_mask = 0, tail_parity = 0;
     bool skip_first = leader && args.never_arrive != 0;
-    int t_lead = -1, pending = 0;
-    bool ring_ok = true;
-    if (leader) {
-      const int f = atomicAdd(args.tile_ctr, 1);
-      t_lead = f < total ? f : -1;
-      ring_ok = ring_put(0, t_lead);
-      if (t_lead >= 0) pending = atomicAdd(args.tile_ctr, 1);
-    }
-    for (int j = 0;; ++j) {
-      int t;
-      if (leader) {
-        t = t_lead;
-        if (!ring_ok || t < 0) break;
-        t_lead = pending < total ? pending : -1;
-        ring_ok = ring_put(j + 1, t_lead);
-        if (t_lead >= 0) pending = atomicAdd(args.tile_ctr, 1);
-      } else {
-        t = ring_take(j);
-        if (t < 0) break;
-      }
+    for (int t = first; t < total; t += stride) {
       RagTile D{};
       RagWTile V{};
       int kb_n = args.num_kb, row0, tail_kb = -1;
@@ -256,9 +193,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int stage = 0;
     uint32_t phase = 0, tail_parity = 0;
     int local = 0;
-    for (int j = 0;; ++j) {
-      const int t = OP == RAG_WGRAD ? ring_take_warp(j) : ring_take(j);
-      if (t < 0) break;
+    for (int t = first; t < total; t += stride) {
       int kb_n = args.num_kb, n = 256, cnt = 0;
       if (OP == RAG_WGRAD) {
         cnt = s_rows[rag_wtile(args, t).e].y;
@@ -325,9 +260,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ------------------------------------------------------------ peer's zeroing warp
     int stage = 0;
     uint32_t tail_parity = 0;
-    for (int j = 0;; ++j) {
-      const int t = ring_take_warp(j);
-      if (t < 0) break;
+    for (int t = first; t < total; t += stride) {
       const int cnt = s_rows[rag_wtile(args, t).e].y;
       const int kb_n = (cnt + BK - 1) / BK;
       if (cnt % 16) {
@@ -345,9 +278,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
     int local = 0;
-    for (int j = 0;; ++j) {
-      const int t = ring_take_warp(j);
-      if (t < 0) break;
+    for (int t = first; t < total; t += stride) {
       RagTile D{};
       RagWTile V{};
       bool empty = false;
@@ -399,7 +330,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           uint32_t r[32];
           tmem_ld_32x32b_x32(taddr + c, r);
           tmem_ld_wait();
-          rag_store_tokens32<T>(r, bias,
+          rag_store_tokens32<T>(r, OP == RAG_FWD && args.bias != nullptr, bias,
                                 static_cast<uint16_t*>(args.out) + (D.row0 + c) * args.ldo + w,
                                 args.ldo, D.rows - c, w, args.W, lane);
         }
@@ -461,8 +392,6 @@ cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB, const Ra
   if (max_pairs[dev] <= 0) return cudaErrorInvalidConfiguration;
   cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(max_pairs[dev], tiles), 1, 1);
   cfg.stream = stream;
-  const cudaError_t e = cudaMemsetAsync(a.tile_ctr, 0, sizeof(int), stream);
-  if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, k_ragged_2sm<OP, T>, tmA, tmB, a);
 }
 template <int OP>
@@ -472,13 +401,12 @@ cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,
               : launch_pair<OP, __nv_bfloat16>(tmA, tmB, a, tiles, stream);
 }
 
-bool common(const RaggedProblem& p, RagArgs& a, int* tile_ctr) {
+bool common(const RaggedProblem& p, RagArgs& a) {
   a.offsets = p.offsets;
   a.R = p.R;
   a.E = p.E;
   a.tile_rows = 256;
   a.group_max = 8;
-  a.tile_ctr = tile_ctr;
   watchdog_params(&a.limit_ns, &a.never_arrive);
   a.err = dev_error_word();
   return a.err != nullptr;
@@ -487,7 +415,7 @@ bool common(const RaggedProblem& p, RagArgs& a, int* tile_ctr) {
 }  // namespace
 
 cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* rows, const void* w,
-                                   const void* bias, void* out, int* tile_ctr,
+                                   const void* bias, void* out,
                                    cudaStream_t stream) {
   const bool fwd = op == RAG_FWD;
   CUtensorMap tmA, tmB;
@@ -496,7 +424,7 @@ cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* r
       !make_tmap_rag(&tmB, rows, p.half, 2, red, p.R, 0, fwd ? p.ldx : p.ldy, 128))
     return cudaErrorInvalidValue;
   RagArgs a{};
-  if (!common(p, a, tile_ctr)) return cudaErrorInvalidDevice;
+  if (!common(p, a)) return cudaErrorInvalidDevice;
   a.W = fwd ? p.N : p.K;
   a.num_kb = (red + BK - 1) / BK;
   a.w_tiles = (a.W + 255) / 256;
@@ -509,14 +437,14 @@ cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* r
 }
 
 cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, const void* x,
-                                    void* dw, bool out_f32, bool accumulate, int* tile_ctr,
+                                    void* dw, bool out_f32, bool accumulate,
                                     cudaStream_t stream) {
   CUtensorMap tmA, tmB;
   if (!make_tmap_rag(&tmA, dy, p.half, 2, p.N, p.R, 0, p.ldy, 64) ||
       !make_tmap_rag(&tmB, x, p.half, 2, p.K, p.R, 0, p.ldx, 64))
     return cudaErrorInvalidValue;
   RagArgs a{};
-  if (!common(p, a, tile_ctr)) return cudaErrorInvalidDevice;
+  if (!common(p, a)) return cudaErrorInvalidDevice;
   a.N = p.N;
   a.K = p.K;
   a.w_tiles = (p.N + 255) / 256;

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t r[32];
         tmem_ld_32x32b_x32(taddr + c, r);
         tmem_ld_wait();
-        rag_store_tokens32<T>(r, 0.0f,
+        rag_store_tokens32<T>(r, false, 0.0f,
                               static_cast<uint16_t*>(args.out) + (V.row0 + c) * args.ldo + w,
                               args.ldo, V.rows - c, w, args.W, lane);
       }
