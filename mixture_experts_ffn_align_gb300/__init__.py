@@ -14,7 +14,8 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from functools import cached_property
+from functools import cache, cached_property
+from types import SimpleNamespace
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_ffn.so")
@@ -112,6 +113,18 @@ class Ragged:
     dtype: str = "bfloat16"     # of x, w, y and the 16-bit gradients
     ldx: int = 0                # row strides in elements, 0: dense
     ldy: int = 0
+
+    @cached_property
+    def _v(self):
+        """Shapes, strides and types that the binding checks."""
+        import torch
+        R, N, K, E = self.R, self.N, self.K, self.E
+        return SimpleNamespace(
+            x=(R, K), y=(R, N), w=(E, N, K), bias=(E, N), offsets=(E + 1,),
+            x_codes=(R, K // 2), x_scales=(R, K // 32), w_codes=(E, N, K // 2),
+            packed=E * N * (K // 32), ldx=self.ldx or K, ldy=self.ldy or N,
+            dtype=getattr(torch, self.dtype), int32=torch.int32, uint8=torch.uint8,
+            float32=torch.float32)
 
     @cached_property
     def _ref(self):
@@ -376,168 +389,198 @@ def fused_experts_from_host(p: Problem, host_x, host_topk_ids, host_topk_weights
 
 
 # --------------------------------------- ragged products, 4-bit operands, clip
-def _dtype_name(t) -> str:
-    return str(t.dtype)[6:]      # "torch.bfloat16" -> "bfloat16"
-
-
-def _arg(name: str, t, shape=None, dtype=None, strided: bool = False):
-    """Checks one tensor argument: on the GPU, of the given type and shape,
-    dense (strided: rows may lie apart)."""
+# The checks below run on every call of kernels that take a few microseconds:
+# each tests everything in one expression and looks for the reason only when
+# it fails.
+def _fail(name: str, t, shape, dtype, stride):
+    """Raises for a tensor argument that is not as the call needs it."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
-    if dtype is not None and _dtype_name(t) != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {_dtype_name(t)}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous() and not (strided and t.dim() == 2 and t.stride(1) == 1):
-        raise ValueError(f"{name} must be {'dense along its rows' if strided else 'dense'}")
+    if stride is not None:
+        raise ValueError(f"{name} must have strides ({stride}, 1), not {t.stride()}")
+    raise ValueError(f"{name} must be dense")
 
 
-def _row_stride(name: str, t, want: int):
-    if t.shape[0] > 1 and t.stride(0) != want:
-        raise ValueError(f"{name} must have the row stride {want}, not {t.stride(0)}")
+def _dense(name: str, t, shape, dtype) -> int:
+    """Data pointer of a dense GPU tensor of this shape and type."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _fail(name, t, shape, dtype, None)
+
+
+def _rows(name: str, t, shape, dtype, ld) -> int:
+    """Data pointer of a GPU matrix whose rows lie ld elements apart."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and (
+            t.stride() == (ld, 1) or shape[0] <= 1 and t.stride(1) == 1):
+        return t.data_ptr()
+    _fail(name, t, shape, dtype, ld)
+
+
+def _bytes(name: str, t):
+    """Data pointer and size of a dense GPU buffer of any type."""
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr(), t.numel() * t.element_size()
+    _fail(name, t, None, None, None)
+
+
+def _raw_stream(stream, t) -> int:
+    """The stream given, or PyTorch's current one on t's device."""
+    if stream is None:
+        return _t().raw_stream(t.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def moe_ragged_workspace_bytes(p: Ragged) -> int:
     return int(lib().moe_ragged_workspace_bytes(p._ref))
 
 
-def _ragged_rows(p: Ragged, name: str, t, cols: int, ld: int):
-    _arg(name, t, (p.R, cols), p.dtype, strided=True)
-    _row_stride(name, t, ld or cols)
-
-
-def _ragged_common(p: Ragged, expert_offsets, workspace):
-    _arg("expert_offsets", expert_offsets, (p.E + 1,), "int32")
-    _arg("workspace", workspace)
-    return workspace.numel() * workspace.element_size()
-
-
 def ragged_gemm(p: Ragged, x, w, expert_offsets, y, workspace, bias=None, stream=None):
     """y[r] = W_e x[r] (+ bias_e) for the rows r of each expert e; x [R, K],
     w [E, N, K], y [R, N], bias [E, N], expert_offsets int32 [E + 1]."""
-    _ragged_rows(p, "x", x, p.K, p.ldx)
-    _arg("w", w, (p.E, p.N, p.K), p.dtype)
-    _ragged_rows(p, "y", y, p.N, p.ldy)
-    if bias is not None:
-        _arg("bias", bias, (p.E, p.N), p.dtype)
-    n = _ragged_common(p, expert_offsets, workspace)
-    _check(lib().ragged_gemm(p._ref, _p(x), _p(w), _p(bias), _p(expert_offsets), _p(y),
-                             _p(workspace), n, _stream(stream)), "ragged_gemm")
+    v = p._v
+    ws, n = _bytes("workspace", workspace)
+    _check(lib().ragged_gemm(
+        p._ref, _rows("x", x, v.x, v.dtype, v.ldx), _dense("w", w, v.w, v.dtype),
+        None if bias is None else _dense("bias", bias, v.bias, v.dtype),
+        _dense("expert_offsets", expert_offsets, v.offsets, v.int32),
+        _rows("y", y, v.y, v.dtype, v.ldy), ws, n, _raw_stream(stream, x)), "ragged_gemm")
 
 
 def ragged_gemm_dgrad(p: Ragged, dy, w, expert_offsets, dx, workspace, stream=None):
     """dx[r] = W_e^T dy[r]: the gradient of ragged_gemm's x."""
-    _ragged_rows(p, "dy", dy, p.N, p.ldy)
-    _arg("w", w, (p.E, p.N, p.K), p.dtype)
-    _ragged_rows(p, "dx", dx, p.K, p.ldx)
-    n = _ragged_common(p, expert_offsets, workspace)
-    _check(lib().ragged_gemm_dgrad(p._ref, _p(dy), _p(w), _p(expert_offsets), _p(dx),
-                                   _p(workspace), n, _stream(stream)), "ragged_gemm_dgrad")
+    v = p._v
+    ws, n = _bytes("workspace", workspace)
+    _check(lib().ragged_gemm_dgrad(
+        p._ref, _rows("dy", dy, v.y, v.dtype, v.ldy), _dense("w", w, v.w, v.dtype),
+        _dense("expert_offsets", expert_offsets, v.offsets, v.int32),
+        _rows("dx", dx, v.x, v.dtype, v.ldx), ws, n, _raw_stream(stream, dy)),
+        "ragged_gemm_dgrad")
 
 
 def ragged_gemm_wgrad(p: Ragged, dy, x, expert_offsets, dw, workspace, accumulate=False,
                       stream=None):
     """dw[e] (+)= sum over e's rows of dy[r] x[r]^T: the gradient of
     ragged_gemm's w, in the operands' type or float32 (dw's)."""
-    _ragged_rows(p, "dy", dy, p.N, p.ldy)
-    _ragged_rows(p, "x", x, p.K, p.ldx)
-    _arg("dw", dw, (p.E, p.N, p.K))
-    if _dtype_name(dw) not in (p.dtype, "float32"):
-        raise TypeError(f"dw must be {p.dtype} or float32, not {_dtype_name(dw)}")
-    n = _ragged_common(p, expert_offsets, workspace)
-    _check(lib().ragged_gemm_wgrad(p._ref, _p(dy), _p(x), _p(expert_offsets), _p(dw),
-                                   DTYPE[_dtype_name(dw)], int(bool(accumulate)), _p(workspace),
-                                   n, _stream(stream)), "ragged_gemm_wgrad")
+    v = p._v
+    f32 = dw.dtype is v.float32
+    ws, n = _bytes("workspace", workspace)
+    _check(lib().ragged_gemm_wgrad(
+        p._ref, _rows("dy", dy, v.y, v.dtype, v.ldy), _rows("x", x, v.x, v.dtype, v.ldx),
+        _dense("expert_offsets", expert_offsets, v.offsets, v.int32),
+        _dense("dw", dw, v.w, v.float32 if f32 else v.dtype),
+        DTYPE["float32"] if f32 else DTYPE[p.dtype], 1 if accumulate else 0, ws, n,
+        _raw_stream(stream, dy)), "ragged_gemm_wgrad")
+
+
+@cache
+def _t():
+    """torch, and the library's codes of its floating types."""
+    import torch
+    return SimpleNamespace(
+        uint8=torch.uint8, float32=torch.float32, Tensor=torch.Tensor,
+        raw_stream=torch._C._cuda_getCurrentRawStream,
+        code={getattr(torch, k): v for k, v in DTYPE.items()})
+
+
+def _float_code(name: str, t) -> int:
+    """moe_dtype of a bfloat16, float16 or float32 tensor."""
+    code = _t().code.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, not {t.dtype}")
+    return code
 
 
 def moe_mxfp4_quantize(x, codes, scales, scale_mode="floor", stream=None):
     """E2M1 codes (uint8 [rows, K/2]) and E8M0 scales (uint8 [rows, K/32]) of
     x [rows, K] (bfloat16, float16 or float32; rows may lie apart)."""
-    if x.dim() != 2:
-        raise ValueError("x must have two dimensions")
     rows, K = x.shape
-    _arg("x", x, strided=True)
-    if _dtype_name(x) not in DTYPE:
-        raise TypeError("x must be bfloat16, float16 or float32")
-    _arg("codes", codes, (rows, K // 2), "uint8")
-    _arg("scales", scales, (rows, K // 32), "uint8")
-    _check(lib().moe_mxfp4_quantize(_p(x), DTYPE[_dtype_name(x)], rows, K,
-                                    x.stride(0) if rows > 1 else 0, MXFP4_SCALE[scale_mode],
-                                    _p(codes), _p(scales), _stream(stream)),
-           "moe_mxfp4_quantize")
+    ld = x.stride(0) if rows > 1 else K
+    _check(lib().moe_mxfp4_quantize(
+        _rows("x", x, (rows, K), x.dtype, ld), _float_code("x", x), rows, K, ld,
+        MXFP4_SCALE[scale_mode], _dense("codes", codes, (rows, K // 2), _t().uint8),
+        _dense("scales", scales, (rows, K // 32), _t().uint8), _raw_stream(stream, x)),
+        "moe_mxfp4_quantize")
 
 
 def moe_mxfp4_dequantize(codes, scales, out, stream=None):
     """out [rows, K] (bfloat16, float16 or float32) = value * 2^(scale - 127)."""
-    if out.dim() != 2:
-        raise ValueError("out must have two dimensions")
     rows, K = out.shape
-    _arg("out", out, strided=True)
-    if _dtype_name(out) not in DTYPE:
-        raise TypeError("out must be bfloat16, float16 or float32")
-    _arg("codes", codes, (rows, K // 2), "uint8")
-    _arg("scales", scales, (rows, K // 32), "uint8")
-    _check(lib().moe_mxfp4_dequantize(_p(codes), _p(scales), rows, K, _p(out),
-                                      DTYPE[_dtype_name(out)], out.stride(0) if rows > 1 else 0,
-                                      _stream(stream)), "moe_mxfp4_dequantize")
+    ld = out.stride(0) if rows > 1 else K
+    _check(lib().moe_mxfp4_dequantize(
+        _dense("codes", codes, (rows, K // 2), _t().uint8),
+        _dense("scales", scales, (rows, K // 32), _t().uint8), rows, K,
+        _rows("out", out, (rows, K), out.dtype, ld), _float_code("out", out), ld,
+        _raw_stream(stream, out)), "moe_mxfp4_dequantize")
 
 
 def moe_mxfp4_pack_scales(scales, packed, stream=None):
     """Weight scales (uint8 [E, N, K/32]) in the block form that
     ragged_gemm_mxfp4 reads; packed has as many bytes."""
     E, N, G = scales.shape
-    _arg("scales", scales, dtype="uint8")
-    _arg("packed", packed, dtype="uint8")
+    src = _dense("scales", scales, (E, N, G), _t().uint8)
+    dst = _dense("packed", packed, packed.shape, _t().uint8)
     if packed.numel() != scales.numel():
         raise ValueError("packed must have as many bytes as scales")
-    _check(lib().moe_mxfp4_pack_scales(_p(scales), E, N, 32 * G, _p(packed), _stream(stream)),
+    _check(lib().moe_mxfp4_pack_scales(src, E, N, 32 * G, dst, _raw_stream(stream, scales)),
            "moe_mxfp4_pack_scales")
 
 
 def ragged_gemm_mxfp4(p: Ragged, x_codes, x_scales, w_codes, w_scales_packed, expert_offsets, y,
                       workspace, stream=None):
     """y[r] = W_e x[r] with both operands in MXFP4; p.dtype is y's."""
-    _arg("x_codes", x_codes, (p.R, p.K // 2), "uint8")
-    _arg("x_scales", x_scales, (p.R, p.K // 32), "uint8")
-    _arg("w_codes", w_codes, (p.E, p.N, p.K // 2), "uint8")
-    _arg("w_scales_packed", w_scales_packed, dtype="uint8")
-    if w_scales_packed.numel() != p.E * p.N * (p.K // 32):
+    v = p._v
+    packed, have = _bytes("w_scales_packed", w_scales_packed)
+    if have != v.packed:
         raise ValueError("w_scales_packed must have E * N * K / 32 bytes")
-    _ragged_rows(p, "y", y, p.N, p.ldy)
-    n = _ragged_common(p, expert_offsets, workspace)
-    _check(lib().ragged_gemm_mxfp4(p._ref, _p(x_codes), _p(x_scales), _p(w_codes),
-                                   _p(w_scales_packed), _p(expert_offsets), _p(y), _p(workspace),
-                                   n, _stream(stream)), "ragged_gemm_mxfp4")
+    ws, n = _bytes("workspace", workspace)
+    _check(lib().ragged_gemm_mxfp4(
+        p._ref, _dense("x_codes", x_codes, v.x_codes, v.uint8),
+        _dense("x_scales", x_scales, v.x_scales, v.uint8),
+        _dense("w_codes", w_codes, v.w_codes, v.uint8), packed,
+        _dense("expert_offsets", expert_offsets, v.offsets, v.int32),
+        _rows("y", y, v.y, v.dtype, v.ldy), ws, n, _raw_stream(stream, y)), "ragged_gemm_mxfp4")
 
 
 def moe_clip_workspace_bytes() -> int:
     return int(lib().moe_clip_workspace_bytes())
 
 
+def _tensor_arrays(name: str, tensors):
+    """Pointers, lengths and types of a list of dense GPU tensors.  (map over
+    the descriptors: lists have dozens of tensors, and this is most of the
+    call's time.)"""
+    T = _t().Tensor
+    types = [*map(_t().code.get, map(T.dtype.__get__, tensors))]
+    if None in types:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32")
+    if not (all(map(T.is_cuda.__get__, tensors)) and all(map(T.is_contiguous, tensors))):
+        for t in tensors:
+            if not (t.is_cuda and t.is_contiguous()):
+                _fail(name, t, None, None, None)
+    return [*map(T.data_ptr, tensors)], [*map(T.numel, tensors)], types
+
+
 def moe_clip_grad_norm(grads, max_norm, norm, workspace, out=None, stream=None):
     """Global L2 norm of the gradients (into the float32 scalar tensor norm)
     and clipping to max_norm, in place or into the tensors of ``out``."""
-    out = grads if out is None else out
     n = len(grads)
-    if len(out) != n:
-        raise ValueError("out must have as many tensors as grads")
-    _arg("norm", norm, dtype="float32")
-    _arg("workspace", workspace)
-    src, dst = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)()
-    numel, types = (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
-    for i, (g, o) in enumerate(zip(grads, out)):
-        name = _dtype_name(g)
-        if name not in DTYPE:
-            raise TypeError("gradients must be bfloat16, float16 or float32")
-        _arg("grads", g)
-        if o is not g:
-            _arg("out", o, g.shape, name)
-        src[i], dst[i] = g.data_ptr(), o.data_ptr()
-        numel[i], types[i] = g.numel(), DTYPE[name]
-    _check(lib().moe_clip_grad_norm(n, src, dst, numel, types, float(max_norm), _p(norm),
-                                    _p(workspace), workspace.numel() * workspace.element_size(),
-                                    _stream(stream)), "moe_clip_grad_norm")
+    src, numel, types = _tensor_arrays("grads", grads)
+    src = (ctypes.c_void_p * n)(*src)
+    dst = src
+    if out is not None:
+        dst, n2, t2 = _tensor_arrays("out", out)
+        if n2 != numel or t2 != types:
+            raise ValueError("out must match grads in number, lengths and types")
+        dst = (ctypes.c_void_p * n)(*dst)
+    ws, size = _bytes("workspace", workspace)
+    _check(lib().moe_clip_grad_norm(
+        n, src, dst, (ctypes.c_int64 * n)(*numel), (ctypes.c_int32 * n)(*types), max_norm,
+        _dense("norm", norm, norm.shape, _t().float32), ws, size, _raw_stream(stream, norm)),
+        "moe_clip_grad_norm")
 
 
 def moe_gemm2_splits(p: Problem) -> int:

@@ -384,6 +384,26 @@ bool make_tmap_rag(CUtensorMap* map, const void* base, bool half, int rank, uint
   return r == CUDA_SUCCESS;
 }
 
+// Tensor map for storing dw [E, N, K] (elem 0 bf16, 1 fp16, 2 fp32; dense): boxes
+// of 128 bytes x 32 rows, 128-byte swizzle.
+bool make_tmap_rag_store(CUtensorMap* map, const void* base, int elem, uint64_t K, uint64_t N,
+                         uint64_t E) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const uint64_t size = elem == 2 ? 4 : 2;
+  const cuuint64_t dims[3] = {K, N, E};
+  const cuuint64_t strides[2] = {K * size, N * K * size};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / size), 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = elem == 2   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUresult r = fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // Tensor map of packed 4-bit values ([d1, d0 / 2] bytes, or d2 of them) for the
 // 4-bit MMA, which reads them packed: boxes of 128 bytes x box1 rows, 128-byte
 // swizzle.

@@ -27,6 +27,8 @@
 
 namespace moe {
 
+bool make_tmap_rag_store(CUtensorMap* map, const void* base, int elem, uint64_t K, uint64_t N,
+                         uint64_t E);
 bool make_tmap_rag(CUtensorMap* map, const void* base, bool half, int rank, uint64_t d0,
                    uint64_t d1, uint64_t d2, uint64_t ld, uint32_t box1);
 
@@ -35,28 +37,32 @@ namespace {
 constexpr int BK = 64, MAX_STAGES = 9;
 constexpr int A_BYTES = 128 * BK * 2;
 constexpr int RING_BYTES = 196608;
+constexpr int EPI_WARPS = 4;
+constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 512;
-constexpr int NUM_THREADS = 192;
-constexpr int SMEM_BYTES = RING_BYTES + 1024 + 256 + kRagSchedBytes;
+constexpr int BOXES = 1;                      // store boxes of each epilogue warp (wgrad)
+constexpr int BOX_BYTES = EPI_WARPS * BOXES * 4096;
+constexpr int SMEM_BYTES = RING_BYTES + BOX_BYTES + 1024 + 256 + kRagSchedBytes;
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 static_assert(8 * (2 * MAX_STAGES + 5) + 8 <= 256, "barrier area");
 
 template <int OP, typename T>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     k_ragged(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-             const RagArgs args) {
+             const __grid_constant__ CUtensorMap tmD, const RagArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING_BYTES + BOX_BYTES);
   // full[S], empty[S], tfull[2], tempty[2], drain
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * MAX_STAGES + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* s_sched = reinterpret_cast<int*>(smem + RING_BYTES + 256);
+  int* s_sched = reinterpret_cast<int*>(smem + RING_BYTES + BOX_BYTES + 256);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t smem_base = smem_u32(smem);
   const uint32_t bar_base = smem_u32(bars);
+  const uint32_t box_base = smem_base + RING_BYTES;
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
   auto empty_bar = [&](int s) { return bar_base + 8u * (MAX_STAGES + s); };
   auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * MAX_STAGES + a); };
@@ -70,7 +76,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 4);
+      mbar_init(tempty_bar(a), EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -225,7 +231,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
-    int local = 0;
+    int local = 0, turn = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
       RagTile D{};
       RagWTile V{};
@@ -248,27 +254,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after();
       }
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
+      auto release = [&] {           // the accumulator has been read
+        if (empty) return;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty_bar(acc));
+        ++local;
+      };
       if (OP == RAG_WGRAD) {
-        const int n = V.n_tile * 128 + q * 32 + lane, k0 = V.k_tile * 256;
-        const size_t at = ((size_t)V.e * args.N + n) * args.K + k0;
-#pragma unroll 1
-        for (int c = 0; c < 256 && k0 + c < args.K; c += 32) {
-          uint32_t r[32];
-          if (empty) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = 0;
-          } else {
-            tmem_ld_32x32b_x32(taddr + c, r);
-            tmem_ld_wait();
-          }
-          if (n >= args.N) continue;
-          if (args.out_f32)
-            rag_store_row32_f32(r, static_cast<float*>(args.out) + at + c, args.K - k0 - c,
-                                args.accumulate);
-          else
-            rag_store_row32<T>(r, static_cast<uint16_t*>(args.out) + at + c, args.K - k0 - c,
-                               args.accumulate);
-        }
+        rag_wgrad_epilogue<T, BOXES>(args, &tmD, box_base + (warp - 2) * BOXES * 4096, turn, taddr,
+                                     empty, V.e, V.n_tile * 128 + q * 32, V.k_tile * 256, lane, release);
       } else {
         const int w = D.w_tile * 128 + q * 32 + lane;
         float bias = 0.0f;
@@ -284,14 +279,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 static_cast<uint16_t*>(args.out) + (D.row0 + c) * args.ldo + w,
                                 args.ldo, D.rows - c, w, args.W, lane);
         }
-      }
-      if (!empty) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tempty_bar(acc));
-        ++local;
+        release();
       }
     }
+    if (OP == RAG_WGRAD && lane == 0) tma_store_wait_all();
   }
 
   tc_fence_before();
@@ -304,7 +295,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 template <int OP, typename T>
-cudaError_t launch_one(const CUtensorMap& tmA, const CUtensorMap& tmB, const RagArgs& a, int grid,
+cudaError_t launch_one(const CUtensorMap& tmA, const CUtensorMap& tmB,
+                      const CUtensorMap& tmD, const RagArgs& a, int grid,
                        cudaStream_t stream) {
   static DeviceOnce attr;
   const cudaError_t e = attr.call([] {
@@ -312,14 +304,15 @@ cudaError_t launch_one(const CUtensorMap& tmA, const CUtensorMap& tmB, const Rag
                                 SMEM_BYTES);
   });
   if (e != cudaSuccess) return e;
-  k_ragged<OP, T><<<grid, NUM_THREADS, SMEM_BYTES, stream>>>(tmA, tmB, a);
+  k_ragged<OP, T><<<grid, NUM_THREADS, SMEM_BYTES, stream>>>(tmA, tmB, tmD, a);
   return cudaGetLastError();
 }
 template <int OP>
-cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB, const RagArgs& a,
+cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,
+                      const CUtensorMap& tmD, const RagArgs& a,
                       int grid, cudaStream_t stream) {
-  return half ? launch_one<OP, __half>(tmA, tmB, a, grid, stream)
-              : launch_one<OP, __nv_bfloat16>(tmA, tmB, a, grid, stream);
+  return half ? launch_one<OP, __half>(tmA, tmB, tmD, a, grid, stream)
+              : launch_one<OP, __nv_bfloat16>(tmA, tmB, tmD, a, grid, stream);
 }
 
 }  // namespace
@@ -353,15 +346,16 @@ cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows,
   const long long most =
       ((long long)std::min(p.E, p.R) + p.R / a.tile_rows) * a.w_tiles;   // tiles at most
   const int grid = (int)std::min<long long>(num_sms(), most);
-  return fwd ? launch_op<RAG_FWD>(p.half, tmA, tmB, a, grid, stream)
-             : launch_op<RAG_DGRAD>(p.half, tmA, tmB, a, grid, stream);
+  return fwd ? launch_op<RAG_FWD>(p.half, tmA, tmB, tmB, a, grid, stream)
+             : launch_op<RAG_DGRAD>(p.half, tmA, tmB, tmB, a, grid, stream);
 }
 
 cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const void* x, void* dw,
                                 bool out_f32, bool accumulate, cudaStream_t stream) {
-  CUtensorMap tmA, tmB;
+  CUtensorMap tmA, tmB, tmD;
   if (!make_tmap_rag(&tmA, dy, p.half, 2, p.N, p.R, 0, p.ldy, 64) ||
-      !make_tmap_rag(&tmB, x, p.half, 2, p.K, p.R, 0, p.ldx, 64))
+      !make_tmap_rag(&tmB, x, p.half, 2, p.K, p.R, 0, p.ldx, 64) ||
+      !make_tmap_rag_store(&tmD, dw, out_f32 ? 2 : p.half ? 1 : 0, p.K, p.N, p.E))
     return cudaErrorInvalidValue;
   RagArgs a{};
   a.offsets = p.offsets;
@@ -382,7 +376,7 @@ cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const vo
   if (a.err == nullptr) return cudaErrorInvalidDevice;
   const long long tiles = (long long)p.E * a.w_tiles * a.k_tiles;
   const int grid = (int)std::min<long long>(num_sms(), tiles);
-  return launch_op<RAG_WGRAD>(p.half, tmA, tmB, a, grid, stream);
+  return launch_op<RAG_WGRAD>(p.half, tmA, tmB, tmD, a, grid, stream);
 }
 
 }  // namespace moe

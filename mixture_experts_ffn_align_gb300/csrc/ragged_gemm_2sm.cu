@@ -25,40 +25,48 @@
 
 namespace moe {
 
+bool make_tmap_rag_store(CUtensorMap* map, const void* base, int elem, uint64_t K, uint64_t N,
+                         uint64_t E);
 bool make_tmap_rag(CUtensorMap* map, const void* base, bool half, int rank, uint64_t d0,
                    uint64_t d1, uint64_t d2, uint64_t ld, uint32_t box1);
 
 namespace {
 
-constexpr int BK = 64, STAGES = 6;
+constexpr int BK = 64, MAX_STAGES = 6;
 constexpr int A_BYTES = 128 * BK * 2, B_BYTES = 128 * BK * 2;   // this CTA's halves
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int PAIR_TX = 2 * STAGE_BYTES;
 constexpr int TMEM_COLS = 512;
-constexpr int NUM_THREADS = 192;
+constexpr int EPI_WARPS = 4;
+constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int BAR_BYTES = 256;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + BAR_BYTES + kRagSchedBytes;
+constexpr int BOXES = 2;                      // store boxes of each epilogue warp (wgrad)
+static_assert(EPI_WARPS * BOXES * 4096 <= STAGE_BYTES, "store boxes");
+constexpr int SMEM_BYTES = MAX_STAGES * STAGE_BYTES + 1024 + BAR_BYTES + kRagSchedBytes;
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 
 template <int OP, typename T>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     k_ragged_2sm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const RagArgs args) {
+                 const __grid_constant__ CUtensorMap tmD, const RagArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + MAX_STAGES * STAGE_BYTES);
   // full[S], empty[S], tail[S], zeroed[S], tfull[2], tempty[2], drain
-  constexpr int NBARS = 4 * STAGES + 5;
+  constexpr int NBARS = 4 * MAX_STAGES + 5;
   static_assert(8 * NBARS + 8 <= BAR_BYTES, "barrier area");
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* s_sched = reinterpret_cast<int*>(smem + STAGES * STAGE_BYTES + BAR_BYTES);
+  int* s_sched = reinterpret_cast<int*>(smem + MAX_STAGES * STAGE_BYTES + BAR_BYTES);
+  // wgrad gives one stage's space to the store boxes
+  constexpr int STAGES = OP == RAG_WGRAD ? MAX_STAGES - 1 : MAX_STAGES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const uint32_t smem_base = smem_u32(smem);
   const uint32_t bar_base = smem_u32(bars);
+  const uint32_t box_base = smem_base + (MAX_STAGES - 1) * STAGE_BYTES;
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
   auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
   auto tail_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + s); };
@@ -71,7 +79,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int s = 0; s < 4 * STAGES; ++s) mbar_init(bar_base + 8u * s, 1);
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 8);     // 4 epilogue warps in each CTA (leader's is used)
+      mbar_init(tempty_bar(a), 2 * EPI_WARPS);   // both CTAs' (leader's is used)
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -277,7 +285,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
-    int local = 0;
+    int local = 0, turn = 0;
     for (int t = first; t < total; t += stride) {
       RagTile D{};
       RagWTile V{};
@@ -298,27 +306,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after();
       }
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
+      auto release = [&] {           // the accumulator has been read
+        if (empty) return;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+        ++local;
+      };
       if (OP == RAG_WGRAD) {
-        const int n = V.n_tile * 256 + rank * 128 + q * 32 + lane, k0 = V.k_tile * 256;
-        const size_t at = ((size_t)V.e * args.N + n) * args.K + k0;
-#pragma unroll 1
-        for (int c = 0; c < 256 && k0 + c < args.K; c += 32) {
-          uint32_t r[32];
-          if (empty) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = 0;
-          } else {
-            tmem_ld_32x32b_x32(taddr + c, r);
-            tmem_ld_wait();
-          }
-          if (n >= args.N) continue;
-          if (args.out_f32)
-            rag_store_row32_f32(r, static_cast<float*>(args.out) + at + c, args.K - k0 - c,
-                                args.accumulate);
-          else
-            rag_store_row32<T>(r, static_cast<uint16_t*>(args.out) + at + c, args.K - k0 - c,
-                               args.accumulate);
-        }
+        rag_wgrad_epilogue<T, BOXES>(args, &tmD, box_base + (warp - 2) * BOXES * 4096, turn, taddr,
+                                     empty, V.e, V.n_tile * 256 + rank * 128 + q * 32, V.k_tile * 256, lane, release);
       } else {
         const int w = D.w_tile * 256 + rank * 128 + q * 32 + lane;
         float bias = 0.0f;
@@ -334,14 +331,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 static_cast<uint16_t*>(args.out) + (D.row0 + c) * args.ldo + w,
                                 args.ldo, D.rows - c, w, args.W, lane);
         }
-      }
-      if (!empty) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
-        ++local;
+        release();
       }
     }
+    if (OP == RAG_WGRAD && lane == 0) tma_store_wait_all();
   }
 
   tc_fence_before();
@@ -362,7 +355,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 template <int OP, typename T>
-cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB, const RagArgs& a,
+cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB,
+                      const CUtensorMap& tmD, const RagArgs& a,
                         long long tiles, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -392,13 +386,14 @@ cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB, const Ra
   if (max_pairs[dev] <= 0) return cudaErrorInvalidConfiguration;
   cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(max_pairs[dev], tiles), 1, 1);
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, k_ragged_2sm<OP, T>, tmA, tmB, a);
+  return cudaLaunchKernelEx(&cfg, k_ragged_2sm<OP, T>, tmA, tmB, tmD, a);
 }
 template <int OP>
-cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB, const RagArgs& a,
+cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,
+                      const CUtensorMap& tmD, const RagArgs& a,
                       long long tiles, cudaStream_t stream) {
-  return half ? launch_pair<OP, __half>(tmA, tmB, a, tiles, stream)
-              : launch_pair<OP, __nv_bfloat16>(tmA, tmB, a, tiles, stream);
+  return half ? launch_pair<OP, __half>(tmA, tmB, tmD, a, tiles, stream)
+              : launch_pair<OP, __nv_bfloat16>(tmA, tmB, tmD, a, tiles, stream);
 }
 
 bool common(const RaggedProblem& p, RagArgs& a) {
@@ -432,16 +427,17 @@ cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* r
   a.ldo = fwd ? p.ldy : p.ldx;
   a.bias = bias;
   const long long tiles = ((long long)std::min(p.E, p.R) + p.R / 256) * a.w_tiles;   // at most
-  return fwd ? launch_op<RAG_FWD>(p.half, tmA, tmB, a, tiles, stream)
-             : launch_op<RAG_DGRAD>(p.half, tmA, tmB, a, tiles, stream);
+  return fwd ? launch_op<RAG_FWD>(p.half, tmA, tmB, tmB, a, tiles, stream)
+             : launch_op<RAG_DGRAD>(p.half, tmA, tmB, tmB, a, tiles, stream);
 }
 
 cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, const void* x,
                                     void* dw, bool out_f32, bool accumulate,
                                     cudaStream_t stream) {
-  CUtensorMap tmA, tmB;
+  CUtensorMap tmA, tmB, tmD;
   if (!make_tmap_rag(&tmA, dy, p.half, 2, p.N, p.R, 0, p.ldy, 64) ||
-      !make_tmap_rag(&tmB, x, p.half, 2, p.K, p.R, 0, p.ldx, 64))
+      !make_tmap_rag(&tmB, x, p.half, 2, p.K, p.R, 0, p.ldx, 64) ||
+      !make_tmap_rag_store(&tmD, dw, out_f32 ? 2 : p.half ? 1 : 0, p.K, p.N, p.E))
     return cudaErrorInvalidValue;
   RagArgs a{};
   if (!common(p, a)) return cudaErrorInvalidDevice;
@@ -452,7 +448,7 @@ cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, cons
   a.out = dw;
   a.out_f32 = out_f32;
   a.accumulate = accumulate;
-  return launch_op<RAG_WGRAD>(p.half, tmA, tmB, a, (long long)p.E * a.w_tiles * a.k_tiles, stream);
+  return launch_op<RAG_WGRAD>(p.half, tmA, tmB, tmD, a, (long long)p.E * a.w_tiles * a.k_tiles, stream);
 }
 
 }  // namespace moe

@@ -301,3 +301,23 @@ def test_watchdog_reports_and_recovers():
             moe.moe_debug_set_watchdog(0, False)
         call()
         assert moe.moe_sync_status() == 0
+
+
+def test_binding_refuses_wrong_tensors():
+    p = moe.Ragged(R=8, N=16, K=8, E=2, ldx=16)
+    x = torch.zeros(8, 16, dtype=torch.bfloat16, device="cuda")[:, :8]
+    w, y = torch.zeros(2, 16, 8, device="cuda").bfloat16(), torch.zeros(8, 16, device="cuda").bfloat16()
+    o = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
+    ws = torch.empty(moe.moe_ragged_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    moe.ragged_gemm(p, x, w, o, y, ws)
+    for kind, bad in ((TypeError, (x.half(), w, o, y)), (ValueError, (x.contiguous(), w, o, y)),
+                      (ValueError, (x, w[:1], o, y)), (TypeError, (x, w, o.long(), y)),
+                      (ValueError, (x, w, o[:2], y)), (ValueError, (x, w, o, y.T.contiguous().T)),
+                      (ValueError, (x, w, o, y.cpu())), (ValueError, (x, w.transpose(1, 2), o, y))):
+        with pytest.raises(kind):
+            moe.ragged_gemm(p, *bad, ws)
+    with pytest.raises(TypeError):
+        moe.ragged_gemm_wgrad(p, y, x, o, w.half(), ws)
+    with pytest.raises(moe.MoEError, match="WORKSPACE"):
+        moe.ragged_gemm(p, x, w, o, y, ws[:128])
+    assert moe.moe_sync_status() == 0

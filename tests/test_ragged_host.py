@@ -134,8 +134,10 @@ def test_binding_refuses_wrong_tensors():
         moe.ragged_gemm(p, x, x, x, x, x)
     with pytest.raises(ValueError, match="GPU"):
         moe.moe_mxfp4_quantize(x, x, x)
-    with pytest.raises(ValueError):
-        moe.moe_clip_grad_norm([x], 1.0, x, x, out=[])
+    with pytest.raises(ValueError, match="GPU"):
+        moe.moe_clip_grad_norm([x], 1.0, x, x)
+    with pytest.raises(TypeError):
+        moe.moe_clip_grad_norm([x.int()], 1.0, x, x)
 
 
 # ------------------------------------------------------------------- oracle
