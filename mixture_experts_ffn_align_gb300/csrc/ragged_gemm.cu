@@ -13,10 +13,10 @@
 //  * dgrad reads w[e] with the reduction along its rows: the same boxes in the
 //    MMA's MN-major form, so no transposed copy of the weights exists.
 //  * wgrad reduces over an expert's rows, both operands MN-major.  Its last
-//    step may end inside the 16 rows of an instruction: the MMA warp then
-//    writes zeros over the rows behind the segment in both operands (in one
-//    alone, an infinity or NaN of the next expert's rows would enter the sums as
-//    0 x inf).
+//    step may end inside the 16 rows of an instruction: a seventh
+//    warp then writes zeros over the rows behind the segment in both operands
+//    (in one alone, an infinity or NaN of the next expert's rows would enter the
+//    sums as 0 x inf).
 //  * every wait is bounded (wall clock); on a timeout the kernel records the
 //    error, drains its own copies and MMAs, frees tensor memory and returns.
 #include <algorithm>
@@ -36,28 +36,29 @@ namespace {
 
 constexpr int BK = 64, MAX_STAGES = 9;
 constexpr int A_BYTES = 128 * BK * 2;
-constexpr int RING_BYTES = 196608;
+constexpr int RING_BYTES = 196608, BAR_BYTES = 384;
 constexpr int EPI_WARPS = 4;
-constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
+// producer, MMA, epilogue warps; wgrad has one more, which zeroes
+constexpr int num_threads(int op) { return 64 + 32 * EPI_WARPS + (op == RAG_WGRAD ? 32 : 0); }
 constexpr int TMEM_COLS = 512;
 constexpr int BOXES = 1;                      // store boxes of each epilogue warp (wgrad)
 constexpr int BOX_BYTES = EPI_WARPS * BOXES * 4096;
-constexpr int SMEM_BYTES = RING_BYTES + BOX_BYTES + 1024 + 256 + kRagSchedBytes;
+constexpr int SMEM_BYTES = RING_BYTES + BOX_BYTES + 1024 + BAR_BYTES + kRagSchedBytes;
 static_assert(SMEM_BYTES <= 232448, "shared memory");
-static_assert(8 * (2 * MAX_STAGES + 5) + 8 <= 256, "barrier area");
+static_assert(8 * (4 * MAX_STAGES + 5) + 8 <= BAR_BYTES, "barrier area");
 
 template <int OP, typename T>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(num_threads(OP), 1)
     k_ragged(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
              const __grid_constant__ CUtensorMap tmD, const RagArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING_BYTES + BOX_BYTES);
-  // full[S], empty[S], tfull[2], tempty[2], drain
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * MAX_STAGES + 5);
+  // full[S], empty[S], tfull[2], tempty[2], drain, tail[S], zeroed[S]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 4 * MAX_STAGES + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* s_sched = reinterpret_cast<int*>(smem + RING_BYTES + BOX_BYTES + 256);
+  int* s_sched = reinterpret_cast<int*>(smem + RING_BYTES + BOX_BYTES + BAR_BYTES);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t smem_base = smem_u32(smem);
@@ -68,11 +69,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * MAX_STAGES + a); };
   auto tempty_bar = [&](int a) { return bar_base + 8u * (2 * MAX_STAGES + 2 + a); };
   const uint32_t drain_bar = bar_base + 8u * (2 * MAX_STAGES + 4);
+  auto tail_bar = [&](int s) { return bar_base + 8u * (2 * MAX_STAGES + 5 + s); };
+  auto zeroed_bar = [&](int s) { return bar_base + 8u * (3 * MAX_STAGES + 5 + s); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < MAX_STAGES; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
+      mbar_init(tail_bar(s), 1);
+      mbar_init(zeroed_bar(s), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
@@ -105,12 +110,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int stages = args.stages;
   const int stage_bytes = A_BYTES + (OP == RAG_WGRAD ? 256 : args.tile_rows) * BK * 2;
 
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    return mbar_wait_bounded(bar, parity, abort_flag, args.limit_ns, args.err);
+  };
+
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ producer
     const uint64_t pol_w = l2_policy(0);
     const uint64_t pol_t = l2_policy(1);     // tokens: re-read for every weight tile
     int stage = 0;
-    uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
+    uint32_t phase = 0, issued_mask = 0, issued_parity = 0, tail_mask = 0, tail_parity = 0;
     bool skip_first = args.never_arrive != 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
       RagTile D{};
@@ -134,8 +143,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           skip_first = false;   // watchdog test: leave this stage unarmed
         } else {
           const uint32_t sa = smem_base + stage * stage_bytes, sb = sa + A_BYTES;
-          const uint32_t bar = full_bar(stage);
+          uint32_t bar = full_bar(stage);
           if (OP == RAG_WGRAD) {
+            if (kb == kb_n - 1 && s_rows[V.e].y % 16) {
+              // copies of a step to be zeroed behind: counted on their own barrier
+              mbar_arrive(bar);
+              bar = tail_bar(stage);
+              tail_parity ^= 1u << stage;       // bit: parity of the next use's phase
+              tail_mask |= 1u << stage;
+            }
             mbar_arrive_expect_tx(bar, A_BYTES + 256 * BK * 2);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -164,20 +180,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
     }
-    for (int s = 0; s < stages; ++s)
+    for (int s = 0; s < stages; ++s) {
       if (issued_mask & (1u << s))
         mbar_wait_bounded(full_bar(s), (issued_parity >> s) & 1, nullptr, args.limit_ns, args.err);
-  } else if (warp == 1 && (OP == RAG_WGRAD || lane == 0)) {
+      if (tail_mask & (1u << s))
+        mbar_wait_bounded(tail_bar(s), ((tail_parity >> s) & 1) ^ 1, nullptr, args.limit_ns,
+                          args.err);
+    }
+  } else if (warp == 1 && lane == 0) {
     // ------------------------------------------------------------ MMA issuer
-    // wgrad: the whole warp walks along, to zero the rows behind a segment
     constexpr uint32_t major = (OP != RAG_FWD ? kIdescAMn : 0u) | (OP == RAG_WGRAD ? kIdescBMn : 0u);
     constexpr uint32_t a_step = OP != RAG_FWD ? 128 : 2, b_step = OP == RAG_WGRAD ? 128 : 2;
-    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-      return mbar_wait_bounded(bar, parity, abort_flag, args.limit_ns, args.err);
-    };
-    auto all = [&](bool ok) -> bool { return OP != RAG_WGRAD || __all_sync(0xffffffffu, ok) ? ok : false; };
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, tail_parity = 0;
     int local = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
       int kb_n = args.num_kb, n = 256, cnt = 0;
@@ -190,43 +205,64 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       const uint32_t idesc = make_idesc(Half16<T>::kFmt, Half16<T>::kFmt, 128, n) | major;
       const int acc = local & 1;
-      if (!all(wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1))) break;
+      if (!wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1)) break;
       tc_fence_after();
       bool ok = true;
       for (int kb = 0; kb < kb_n; ++kb) {
-        if (!all(wait(full_bar(stage), phase))) {
+        if (!wait(full_bar(stage), phase)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        const uint32_t sa = smem_base + stage * stage_bytes;
         int steps = BK / 16;
         if (OP == RAG_WGRAD && kb == kb_n - 1) {
           const int rem = cnt - kb * BK;
           steps = (rem + 15) / 16;
-          rag_zero_rows<6>(sa, rem, 16 * steps, lane);
+          if (rem % 16) {               // the rows behind the segment are zeros
+            const uint32_t par = (tail_parity >> stage) & 1;
+            tail_parity ^= 1u << stage;
+            if (!wait(zeroed_bar(stage), par)) {
+              ok = false;
+              break;
+            }
+          }
         }
+        tc_fence_after();
+        const uint32_t sa = smem_base + stage * stage_bytes;
         const uint64_t adesc = OP != RAG_FWD ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
         const uint64_t bdesc = OP == RAG_WGRAD ? sdesc_mn_sw128(sa + A_BYTES)
                                                : sdesc_k_sw128(sa + A_BYTES);
-        if (lane == 0) {
-          for (int k = 0; k < steps; ++k)
-            umma_f16(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
-                     (kb | k) != 0);
-          tc_commit(empty_bar(stage));
-        }
+        for (int k = 0; k < steps; ++k)
+          umma_f16(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
+                   (kb | k) != 0);
+        tc_commit(empty_bar(stage));
         if (++stage == stages) {
           stage = 0;
           phase ^= 1;
         }
       }
       if (!ok) break;
-      if (lane == 0) tc_commit(tfull_bar(acc));
+      tc_commit(tfull_bar(acc));
       ++local;
     }
-    if (lane == 0) {
-      tc_commit(drain_bar);
-      mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+    tc_commit(drain_bar);
+    mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+  } else if (OP == RAG_WGRAD && warp == 2 + EPI_WARPS) {
+    // ------------------------------------------------------------ zeroing warp
+    int stage = 0;
+    uint32_t tail_parity = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+      const int cnt = s_rows[rag_wtile(args, t).e].y;
+      const int kb_n = (cnt + BK - 1) / BK;
+      if (cnt % 16) {
+        const int s = (stage + kb_n - 1) % stages;      // stage of the last step
+        const uint32_t par = (tail_parity >> s) & 1;
+        tail_parity ^= 1u << s;
+        if (!__all_sync(0xffffffffu, wait(tail_bar(s), par))) break;
+        const int rem = cnt - (kb_n - 1) * BK;
+        rag_zero_rows<6>(smem_base + s * stage_bytes, rem, (rem + 15) / 16 * 16, lane);
+        if (lane == 0) mbar_arrive(zeroed_bar(s));
+      }
+      stage = (stage + kb_n) % stages;
     }
   } else if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
@@ -304,7 +340,7 @@ cudaError_t launch_one(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                 SMEM_BYTES);
   });
   if (e != cudaSuccess) return e;
-  k_ragged<OP, T><<<grid, NUM_THREADS, SMEM_BYTES, stream>>>(tmA, tmB, tmD, a);
+  k_ragged<OP, T><<<grid, num_threads(OP), SMEM_BYTES, stream>>>(tmA, tmB, tmD, a);
   return cudaGetLastError();
 }
 template <int OP>

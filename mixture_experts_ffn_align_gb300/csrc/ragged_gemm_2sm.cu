@@ -12,9 +12,8 @@
 //    K = 16 into one of two accumulators, and its commits reach both CTAs.
 //  * each CTA's warps 2-5 drain their own 128 accumulator rows.
 //  * wgrad's last step of a segment that ends inside the 16 rows of an
-//    instruction: each CTA's copies complete on a barrier of its own, its warp 1
-//    zeroes the rows behind the segment, and the peer's then signals the
-//    leader's.
+//    instruction: each CTA's copies complete on a barrier of its own, a seventh
+//    warp zeroes the rows behind the segment and signals the leader's issuer.
 //  * every wait is bounded; the final cluster barrier is reached by both CTAs
 //    after their bounded loops.
 #include <algorithm>
@@ -38,7 +37,8 @@ constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int PAIR_TX = 2 * STAGE_BYTES;
 constexpr int TMEM_COLS = 512;
 constexpr int EPI_WARPS = 4;
-constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
+// producer, MMA, epilogue warps; wgrad has one more, which zeroes
+constexpr int num_threads(int op) { return 64 + 32 * EPI_WARPS + (op == RAG_WGRAD ? 32 : 0); }
 constexpr int BAR_BYTES = 256;
 constexpr int BOXES = 2;                      // store boxes of each epilogue warp (wgrad)
 static_assert(EPI_WARPS * BOXES * 4096 <= STAGE_BYTES, "store boxes");
@@ -46,7 +46,7 @@ constexpr int SMEM_BYTES = MAX_STAGES * STAGE_BYTES + 1024 + BAR_BYTES + kRagSch
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 
 template <int OP, typename T>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(num_threads(OP), 1)
     k_ragged_2sm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmD, const RagArgs args) {
   extern __shared__ uint8_t smem_raw[];
@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t drain_bar = bar_base + 8u * (4 * STAGES + 4);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 4 * STAGES; ++s) mbar_init(bar_base + 8u * s, 1);
+    for (int s = 0; s < 3 * STAGES; ++s) mbar_init(bar_base + 8u * s, 1);
+    for (int s = 0; s < STAGES; ++s) mbar_init(zeroed_bar(s), 2);   // one warp of each CTA
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
       mbar_init(tempty_bar(a), 2 * EPI_WARPS);   // both CTAs' (leader's is used)
@@ -190,14 +191,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mbar_wait_bounded(tail_bar(s), ((tail_parity >> s) & 1) ^ 1, nullptr, args.limit_ns,
                           args.err);
     }
-  } else if (warp == 1 && leader && (OP == RAG_WGRAD || lane == 0)) {
+  } else if (warp == 1 && leader && lane == 0) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t major = (OP != RAG_FWD ? kIdescAMn : 0u) | (OP == RAG_WGRAD ? kIdescBMn : 0u);
     constexpr uint32_t a_step = OP != RAG_FWD ? 128 : 2, b_step = OP == RAG_WGRAD ? 128 : 2;
-    auto all = [&](bool ok) -> bool {
-      if (OP == RAG_WGRAD) return __all_sync(0xffffffffu, ok);
-      return ok;
-    };
     int stage = 0;
     uint32_t phase = 0, tail_parity = 0;
     int local = 0;
@@ -212,11 +209,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       const uint32_t idesc = make_idesc(Half16<T>::kFmt, Half16<T>::kFmt, 256, n) | major;
       const int acc = local & 1;
-      if (!all(wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1))) break;
+      if (!wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1)) break;
       tc_fence_after();
       bool ok = true;
       for (int kb = 0; kb < kb_n; ++kb) {
-        if (!all(wait(full_bar(stage), phase))) {
+        if (!wait(full_bar(stage), phase)) {
           ok = false;
           break;
         }
@@ -225,17 +222,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (OP == RAG_WGRAD && kb == kb_n - 1) {
           const int rem = cnt - kb * BK;
           steps = (rem + 15) / 16;
-          if (rem % 16) {
+          if (rem % 16) {          // the rows behind the segment are zeros in both CTAs
             const uint32_t par = (tail_parity >> stage) & 1;
             tail_parity ^= 1u << stage;
-            if (!all(wait(tail_bar(stage), par))) {
-              ok = false;
-              break;
-            }
-            rag_zero_rows<4>(sa, rem, 16 * steps, lane);
-            // the peer has zeroed its rows
-            if (!all(mbar_wait_bounded<true>(zeroed_bar(stage), par, abort_flag, args.limit_ns,
-                                             args.err))) {
+            if (!mbar_wait_bounded<true>(zeroed_bar(stage), par, abort_flag, args.limit_ns,
+                                         args.err)) {
               ok = false;
               break;
             }
@@ -245,27 +236,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint64_t adesc = OP != RAG_FWD ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
         const uint64_t bdesc = OP == RAG_WGRAD ? sdesc_mn_sw128(sa + A_BYTES)
                                                : sdesc_k_sw128(sa + A_BYTES);
-        if (lane == 0) {
-          for (int k = 0; k < steps; ++k)
-            umma_f16_pair(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
-                          (kb | k) != 0);
-          tc_commit_pair(empty_bar(stage), 0x3);
-        }
+        for (int k = 0; k < steps; ++k)
+          umma_f16_pair(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
+                        (kb | k) != 0);
+        tc_commit_pair(empty_bar(stage), 0x3);
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
         }
       }
       if (!ok) break;
-      if (lane == 0) tc_commit_pair(tfull_bar(acc), 0x3);
+      tc_commit_pair(tfull_bar(acc), 0x3);
       ++local;
     }
-    if (lane == 0) {
-      tc_commit_pair(drain_bar, 0x1);
-      mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
-    }
-  } else if (OP == RAG_WGRAD && warp == 1 && !leader) {
-    // ------------------------------------------------------------ peer's zeroing warp
+    tc_commit_pair(drain_bar, 0x1);
+    mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+  } else if (OP == RAG_WGRAD && warp == 2 + EPI_WARPS) {
+    // ------------------------------------------------------------ zeroing warp
+    // As soon as the copies of a segment's last step have landed in this CTA,
+    // well before the MMA issuer gets there (done by the issuer itself, the
+    // round trip to the peer cost 2000 cycles a tile).
     int stage = 0;
     uint32_t tail_parity = 0;
     for (int t = first; t < total; t += stride) {
@@ -310,7 +300,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (empty) return;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+        // carries no data through memory; the releasing form would wait for this
+        // warp's output stores
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(acc), 0));
         ++local;
       };
       if (OP == RAG_WGRAD) {
@@ -364,7 +356,7 @@ cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB,
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+  cfg.blockDim = dim3(num_threads(OP), 1, 1);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
