@@ -422,6 +422,23 @@ bool make_tmap_rag_fp4(CUtensorMap* map, const void* base, int rank, uint64_t d0
   return r == CUDA_SUCCESS;
 }
 
+// Tensor map of 512-byte scale blocks ([d1] or [d2, d1] of them) as rows of 128
+// words: boxes of box1 (x box2) blocks, one after the other.
+bool make_tmap_scale_blocks(CUtensorMap* map, const void* base, int rank, uint64_t d1, uint64_t d2,
+                            uint32_t box1, uint32_t box2) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {128, d1, d2};
+  const cuuint64_t strides[2] = {512, d1 * 512};
+  const cuuint32_t box[3] = {128, box1, box2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, (cuuint32_t)rank,
+                        const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 cudaError_t launch_ggemm_bf16(const void* A, int cap, int K, const void* B, int b_rows_total,
                               int b_rows_per_expert, int n_out, const int32_t* block_expert_ids,
                               const int32_t* num_post_padded, void* out, bool fuse_act,

@@ -229,6 +229,10 @@ cudaError_t launch_ragged_mxfp4(const RaggedProblem& p, const void* xq, const ui
                                 const void* wq, const void* w_scale_packed, void* y,
                                 void* workspace, cudaStream_t stream);
 
+cudaError_t launch_ragged_mxfp4_2sm(const RaggedProblem& p, const void* xq, const uint8_t* x_scale,
+                                    const void* wq, const void* w_scale_packed, void* y,
+                                    void* workspace, cudaStream_t stream);
+
 // ---- MXFP4 codec.  type: 0 bf16, 1 fp16, 2 fp32.
 cudaError_t launch_mxfp4_quantize(const void* x, int type, long long rows, int K, long long ldx,
                                   bool ceil_scale, uint8_t* codes, uint8_t* scales,

@@ -298,18 +298,30 @@ struct Half16<__half> {
 // 4-byte pieces.  `live` tokens are stored, columns below W (W is even: a
 // multiple of 8).  Packed conversion, one shuffle and one byte permute for two
 // tokens: the warps are bound by instruction issue here, not by the stores.
-template <typename T, bool ALL>
-__device__ __forceinline__ void rag_store_tokens(const uint32_t (&r)[32], uint16_t* p,
-                                                 long long ldo, int live, bool inside, int lane) {
+template <bool ALL>
+__device__ __forceinline__ void rag_store_pairs(const uint32_t* pk, uint16_t* p, long long ldo,
+                                                int live, bool inside, int lane) {
   const uint32_t sel = (lane & 1) ? 0x3276u : 0x5410u;
 #pragma unroll
-  for (int j = 0; j < 32; j += 2) {
-    const uint32_t own = Half16<T>::pack(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
-    const uint32_t v = __byte_perm(own, other, sel);
-    if (ALL || (inside && j + (lane & 1) < live)) *reinterpret_cast<uint32_t*>(p) = v;
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, pk[j], 1);
+    const uint32_t v = __byte_perm(pk[j], other, sel);
+    if (ALL || (inside && 2 * j + (lane & 1) < live)) *reinterpret_cast<uint32_t*>(p) = v;
     p += 2 * ldo;
   }
+}
+// The 32 tokens as 16 packed pairs: pk[j] holds tokens 2j and 2j + 1 of this
+// lane's column w, out points at (first token, w).
+__device__ __forceinline__ void rag_store_packed32(const uint32_t* pk, uint16_t* out,
+                                                   long long ldo, int live, int w, int W,
+                                                   int lane) {
+  // odd lanes: the next token, from the column before
+  uint16_t* p = out + ((lane & 1) ? ldo - 1 : 0);
+  const bool inside = w < W;
+  if (live >= 32 && __all_sync(0xffffffffu, inside))
+    rag_store_pairs<true>(pk, p, ldo, live, inside, lane);
+  else
+    rag_store_pairs<false>(pk, p, ldo, live, inside, lane);
 }
 template <typename T>
 __device__ __forceinline__ void rag_store_tokens32(uint32_t (&r)[32], bool has_bias, float bias,
@@ -319,13 +331,11 @@ __device__ __forceinline__ void rag_store_tokens32(uint32_t (&r)[32], bool has_b
 #pragma unroll
     for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + bias);
   }
-  // odd lanes: the next token, from the column before
-  uint16_t* p = out + ((lane & 1) ? ldo - 1 : 0);
-  const bool inside = w < W;
-  if (live >= 32 && __all_sync(0xffffffffu, inside))
-    rag_store_tokens<T, true>(r, p, ldo, live, inside, lane);
-  else
-    rag_store_tokens<T, false>(r, p, ldo, live, inside, lane);
+  uint32_t pk[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    pk[j] = Half16<T>::pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+  rag_store_packed32(pk, out, ldo, live, w, W, lane);
 }
 
 // A 128-byte wide box of shared memory (128-byte swizzled) to a 3-D tensor,

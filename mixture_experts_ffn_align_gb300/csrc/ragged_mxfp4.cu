@@ -27,7 +27,7 @@
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
-#include "ragged.cuh"
+#include "ragged_mx.cuh"
 
 namespace moe {
 
@@ -49,20 +49,6 @@ constexpr int SMEM_BYTES = STAGES * (STAGE_BYTES + SLOT_BYTES) + 1024 + 256 + kR
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 static_assert(SF_COL0 + STAGES * SF_SLOT <= TMEM_COLS, "tensor memory");
 
-// 128-row scale blocks of a token tile, and bytes of one tile's scales.
-__host__ __device__ constexpr int tile_groups(int tile_rows) { return (tile_rows + 127) / 128; }
-__host__ __device__ constexpr size_t tile_scale_bytes(int tile_rows, int K) {
-  return (size_t)(K / 128) * tile_groups(tile_rows) * 512;
-}
-
-struct Mx44Args {
-  RagArgs r;
-  const uint8_t* x_scale;    // [R, K/32]
-  const uint8_t* w_packed;   // [E][K/128][W/128][512]
-  uint8_t* x_packed;         // [token tiles][K/128][tile_groups][512]
-  int K;
-};
-
 __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                           uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                           uint32_t accumulate) {
@@ -74,21 +60,18 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-// kind::mxf4: as make_idesc_block_scaled, E2M1 operands (format code 1), scale
-// bytes sf and sf + 1 (0 or 2) of the words.
-constexpr uint32_t kFmtMxf4 = 1;
-
 // One block per token tile and trip: 16 bytes (4 rows' words) a thread.  Rows
 // past the tile get 2^0: their columns are not stored.
+template <int G>
 __global__ void __launch_bounds__(256) k_pack_token_scales(const Mx44Args args) {
   __shared__ int s_mem[kRagSchedBytes / 4];
   __shared__ int s_scratch[kRagMaxExperts + 1];
-  const RagSched sched = rag_sched_build<16>(args.r, s_mem, s_scratch);
+  const RagSched sched = rag_sched_build<G>(args.r, s_mem, s_scratch);
   const int tiles = sched.tile0[sched.nseg];
   const int groups = tile_groups(args.r.tile_rows), kb_n = args.K / 128, KQ = args.K / 32;
   const int per_tile = kb_n * groups * 32;
   for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const RagTile T = rag_tile<16>(sched, args.r, t);   // with w_tiles == 1: token tile t
+    const RagTile T = rag_tile<G>(sched, args.r, t);   // with w_tiles == 1: token tile t
     uint4* dst = reinterpret_cast<uint4*>(args.x_packed + T.tok * tile_scale_bytes(args.r.tile_rows, args.K));
     for (int i = threadIdx.x; i < per_tile; i += blockDim.x) {
       // neighbouring threads take neighbouring K words of one row
@@ -342,18 +325,22 @@ cudaError_t launch_mx(const CUtensorMap& tmA, const CUtensorMap& tmB, const Mx44
   return cudaGetLastError();
 }
 
-// Token tiles at most, whatever the segments.
-long long most_token_tiles(int R, int E, int tile_rows) {
-  return (long long)std::min(E, R) + R / tile_rows;
-}
-int mx_tile_rows(int R, int E) {
-  return R <= 128 ? 128 : 256;
-}
+int mx_tile_rows(int R) { return R <= 128 ? 128 : 256; }
 
 }  // namespace
 
+template <int G>
+cudaError_t launch_pack_token_scales(const Mx44Args& args, long long most_tiles,
+                                     cudaStream_t stream) {
+  Mx44Args a = args;
+  a.r.w_tiles = 1;          // tile numbers are token tiles
+  k_pack_token_scales<G><<<(int)std::min<long long>(most_tiles, 4 * num_sms()), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+template cudaError_t launch_pack_token_scales<32>(const Mx44Args&, long long, cudaStream_t);
+
 size_t ragged_mxfp4_scale_bytes(int R, int K, int E) {
-  const int tr = mx_tile_rows(R, E);
+  const int tr = mx_tile_rows(R);     // both forms' tiles
   return (size_t)most_token_tiles(R, E, tr) * tile_scale_bytes(tr, K);
 }
 
@@ -370,7 +357,7 @@ cudaError_t launch_ragged_mxfp4(const RaggedProblem& p, const void* xq, const ui
   a.r.E = p.E;
   a.r.W = p.N;
   a.r.num_kb = (p.K + BK - 1) / BK;
-  a.r.tile_rows = mx_tile_rows(p.R, p.E);
+  a.r.tile_rows = mx_tile_rows(p.R);
   a.r.group_max = 8;
   a.r.out = y;
   a.r.ldo = p.ldy;
@@ -382,9 +369,7 @@ cudaError_t launch_ragged_mxfp4(const RaggedProblem& p, const void* xq, const ui
   a.x_packed = static_cast<uint8_t*>(workspace);
   a.K = p.K;
   const long long tok = most_token_tiles(p.R, p.E, a.r.tile_rows);
-  a.r.w_tiles = 1;
-  k_pack_token_scales<<<(int)std::min<long long>(tok, 4 * num_sms()), 256, 0, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pack_token_scales<16>(a, tok, stream);
   if (e != cudaSuccess) return e;
   a.r.w_tiles = p.N / 128;
   const int grid = (int)std::min<long long>(num_sms(), tok * a.r.w_tiles);

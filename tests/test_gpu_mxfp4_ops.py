@@ -16,6 +16,14 @@ pytestmark = pytest.mark.gpu
 DT = {"bfloat16": torch.bfloat16, "float16": torch.float16, "float32": torch.float32}
 
 
+@pytest.fixture(params=["single", "pairs"])
+def form(request):
+    """The products in both forms of the kernel."""
+    moe.moe_debug_set_bf16_gemm_form(request.param)
+    yield
+    moe.moe_debug_set_bf16_gemm_form("auto")
+
+
 def f64(t):
     return t.double().cpu().numpy()
 
@@ -129,26 +137,26 @@ def product(counts, n, k, dtype="bfloat16", lead=0, tail=0, ldy=0, seed=0, lo=11
 
 
 @pytest.mark.parametrize("counts", [[1], [0, 3, 0, 1, 130, 0], [16, 32, 64, 127, 128, 129],
-                                    [700, 5, 256], [0, 0]])
-def test_product_segments(counts):
+                                    [700, 5, 256], [0, 0], [300] * 9])
+def test_product_segments(counts, form):
     product(counts, 256, 384)
 
 
 @pytest.mark.parametrize("n, k", [(128, 128), (128, 256), (384, 640), (256, 2048), (1152, 1152)])
-def test_product_sizes(n, k):
+def test_product_sizes(n, k, form):
     product([5, 0, 40, 260], n, k, dtype="float16", seed=n, lo=122, hi=126)
 
 
 @pytest.mark.parametrize("rows", [1, 31, 33, 127, 128, 129, 256, 257, 900])
-def test_product_one_expert(rows):
+def test_product_one_expert(rows, form):
     product([rows], 256, 512, seed=rows)
 
 
-def test_product_rows_of_no_expert_and_stride():
+def test_product_rows_of_no_expert_and_stride(form):
     product([40, 0, 90], 128, 384, lead=3, tail=9, ldy=136)
 
 
-def test_product_scales_of_their_rows_only():
+def test_product_scales_of_their_rows_only(form):
     """A NaN scale poisons its own row (token) or column (weight) only."""
     n, k = 256, 256
     off = [0, 50, 200]
@@ -171,7 +179,7 @@ def test_product_scales_of_their_rows_only():
     assert bool((y.isnan() == bad).all()) and bool((y[~bad] == 256).all())
 
 
-def test_product_each_scale_lands_on_its_group():
+def test_product_each_scale_lands_on_its_group(form):
     """One nonzero weight group at a time: y counts 32 scaled ones."""
     n, k = 128, 512
     p = moe.Ragged(R=130, N=n, K=k, E=1)
@@ -193,7 +201,7 @@ def test_product_each_scale_lands_on_its_group():
         assert bool((y.float() == want).all()), grp
 
 
-def test_product_watchdog_and_bad_offsets():
+def test_product_watchdog_and_bad_offsets(form):
     p = moe.Ragged(R=64, N=128, K=256, E=2)
     xc = torch.zeros(64, 128, dtype=torch.uint8, device="cuda")
     xs = torch.full((64, 8), 127, dtype=torch.uint8, device="cuda")
