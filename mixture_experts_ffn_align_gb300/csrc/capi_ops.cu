@@ -51,17 +51,19 @@ size_t ragged_bytes(const moe_ragged* p) {
   return pad256(b);
 }
 
-// SM pairs pay from segments of about 128 rows up.
-bool use_pairs(const moe_ragged* p) {
+// SM pairs (256-wide tiles) unless that leaves fewer tiles than two for each
+// pair: then the one-SM form's 128-wide tiles spread over twice as many CTAs.
+bool use_pairs(const moe_ragged* p, int width) {
   const int form = gemm_form();
-  return form == 2 || (form == 0 && (int64_t)p->R >= 128ll * p->E);
+  const int64_t tiles = ((int64_t)std::min(p->E, p->R) + p->R / 256) * ((width + 255) / 256);
+  return form == 2 || (form == 0 && tiles >= num_sms());
 }
 
 cudaError_t ragged_rows(const moe_ragged* p, int op, const void* rows, const void* w,
                         const void* bias, const int32_t* offsets, void* out, void* stream) {
   const RaggedProblem q = ragged_problem(p, offsets);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return use_pairs(p)
+  return use_pairs(p, op == 0 ? p->N : p->K)
              ? launch_ragged_rows_2sm(q, op, rows, w, bias, out, st)
              : launch_ragged_rows(q, op, rows, w, bias, out, st);
 }
@@ -123,7 +125,7 @@ moe_status ragged_gemm_wgrad(const moe_ragged* p, const void* dy, const void* x,
   }
   const RaggedProblem q = ragged_problem(p, expert_offsets);
   const bool f32 = dw_dtype == MOE_T_FP32;
-  return done(use_pairs(p) ? launch_ragged_wgrad_2sm(q, dy, x, dw, f32, accumulate != 0, st)
+  return done(use_pairs(p, p->N) ? launch_ragged_wgrad_2sm(q, dy, x, dw, f32, accumulate != 0, st)
                            : launch_ragged_wgrad(q, dy, x, dw, f32, accumulate != 0, st));
 }
 
@@ -138,7 +140,7 @@ moe_status ragged_gemm_mxfp4(const moe_ragged* p, const void* x_codes, const voi
   if (p->R == 0) return MOE_OK;
   if (!x_scales || !w_scales_packed || misaligned(x_scales, 4) || misaligned(w_scales_packed, 16))
     return MOE_ERR_INVALID_ARG;
-  const auto launch = use_pairs(p) && p->R > 128 ? launch_ragged_mxfp4_2sm : launch_ragged_mxfp4;
+  const auto launch = use_pairs(p, p->N) && p->R > 128 ? launch_ragged_mxfp4_2sm : launch_ragged_mxfp4;
   return done(launch(ragged_problem(p, expert_offsets), x_codes,
                      static_cast<const uint8_t*>(x_scales), w_codes, w_scales_packed, y,
                      workspace, static_cast<cudaStream_t>(stream)));

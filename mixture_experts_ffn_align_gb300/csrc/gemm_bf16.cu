@@ -384,6 +384,25 @@ bool make_tmap_rag(CUtensorMap* map, const void* base, bool half, int rank, uint
   return r == CUDA_SUCCESS;
 }
 
+// The same for an MN-major operand whose width is a multiple of 64: [batch,
+// rows, cols] seen as [batch, cols / 64, rows, 64], boxes of 64 x 64 rows x
+// `chunks` chunks, so that one copy brings chunks * 64 columns as consecutive
+// 64 x 64 boxes.
+bool make_tmap_rag_wide(CUtensorMap* map, const void* base, bool half, uint64_t rows,
+                        uint64_t cols, uint64_t batch, uint64_t ld, uint32_t chunks) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr || cols % 64 != 0) return false;
+  const cuuint64_t dims[4] = {64, rows, cols / 64, batch};
+  const cuuint64_t strides[3] = {ld * 2, 128, rows * ld * 2};
+  const cuuint32_t box[4] = {64, 64, chunks, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        4, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // Tensor map for storing dw [E, N, K] (elem 0 bf16, 1 fp16, 2 fp32; dense): boxes
 // of 128 bytes x 32 rows, 128-byte swizzle.
 bool make_tmap_rag_store(CUtensorMap* map, const void* base, int elem, uint64_t K, uint64_t N,

@@ -40,13 +40,12 @@ struct RagArgs {
   int tile_rows;            // forward, dgrad: most token rows of a tile
   int group_max;            // token tiles (wgrad: n tiles) walked together
   int stages;
+  int wide_a, wide_b;       // MN-major operand whose map has its chunks as a dimension
   void* out;
   long long ldo;            // row stride of out (forward, dgrad)
   const void* bias;         // forward: [E, N] in the operands' type, or null
   int out_f32;              // wgrad: dw is fp32
   int accumulate;           // wgrad: dw += instead of dw =
-  int splits;               // forward, dgrad on one SM: slices of the reduction
-  float* part;              // their fp32 sums [splits, R, W]
   uint64_t limit_ns;
   int never_arrive;
   int* err;
@@ -259,6 +258,30 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       "l"(policy)
       : "memory");
 }
+// 4-D tiled load: an MN-major operand with its 64-value chunks as a dimension
+// (make_tmap_rag_wide), so that one copy brings several chunks.  A copy costs
+// its issuing thread some 150 cycles, and a step has 512 cycles of MMA work.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar),
+      "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map,
+                                                 uint32_t cluster_bar, int32_t c0, int32_t c1,
+                                                 int32_t c2, int32_t c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "r"(cluster_bar), "l"(policy)
+      : "memory");
+}
+
 // fp32 <-> the operands' 16-bit types.
 template <typename T>
 struct Half16;

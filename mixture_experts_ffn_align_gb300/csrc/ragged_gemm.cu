@@ -29,6 +29,8 @@ namespace moe {
 
 bool make_tmap_rag_store(CUtensorMap* map, const void* base, int elem, uint64_t K, uint64_t N,
                          uint64_t E);
+bool make_tmap_rag_wide(CUtensorMap* map, const void* base, bool half, uint64_t rows,
+                        uint64_t cols, uint64_t batch, uint64_t ld, uint32_t chunks);
 bool make_tmap_rag(CUtensorMap* map, const void* base, bool half, int rank, uint64_t d0,
                    uint64_t d1, uint64_t d2, uint64_t ld, uint32_t box1);
 
@@ -153,16 +155,25 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
               tail_mask |= 1u << stage;
             }
             mbar_arrive_expect_tx(bar, A_BYTES + 256 * BK * 2);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              tma_load_2d(sa + j * 8192, &tmA, bar, V.n_tile * 128 + 64 * j, row0 + kb * BK, pol_t);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              tma_load_2d(sb + j * 8192, &tmB, bar, V.k_tile * 256 + 64 * j, row0 + kb * BK, pol_t);
+            const int r0 = row0 + kb * BK;
+            if (args.wide_a) {
+              tma_load_4d(sa, &tmA, bar, 0, r0, V.n_tile * 2, 0, pol_t);
+            } else {
+              for (int j = 0; j < 2; ++j)
+                tma_load_2d(sa + j * 8192, &tmA, bar, V.n_tile * 128 + 64 * j, r0, pol_t);
+            }
+            if (args.wide_b) {
+              tma_load_4d(sb, &tmB, bar, 0, r0, V.k_tile * 4, 0, pol_t);
+            } else {
+              for (int j = 0; j < 4; ++j)
+                tma_load_2d(sb + j * 8192, &tmB, bar, V.k_tile * 256 + 64 * j, r0, pol_t);
+            }
           } else {
             mbar_arrive_expect_tx(bar, A_BYTES + boxes * 32 * BK * 2);
             if (OP == RAG_FWD) {
               tma_load_3d(sa, &tmA, bar, kb * BK, D.w_tile * 128, D.e, pol_w);
+            } else if (args.wide_a) {
+              tma_load_4d(sa, &tmA, bar, 0, kb * BK, D.w_tile * 2, D.e, pol_w);
             } else {
               tma_load_3d(sa, &tmA, bar, D.w_tile * 128, kb * BK, D.e, pol_w);
               tma_load_3d(sa + 8192, &tmA, bar, D.w_tile * 128 + 64, kb * BK, D.e, pol_w);
@@ -194,14 +205,20 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     int stage = 0;
     uint32_t phase = 0, tail_parity = 0;
     int local = 0;
+    // rows of tile t (wgrad: of its expert); the next tile's are looked up while
+    // this one's MMAs run
+    auto rows_of = [&](int t) -> int {
+      if (t >= total) return 0;
+      return OP == RAG_WGRAD ? s_rows[rag_wtile(args, t).e].y : rag_tile<16>(sched, args, t).rows;
+    };
+    int rows_next = rows_of(blockIdx.x);
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      int kb_n = args.num_kb, n = 256, cnt = 0;
-      if (OP == RAG_WGRAD) {
-        cnt = s_rows[rag_wtile(args, t).e].y;
-        kb_n = (cnt + BK - 1) / BK;
-        if (kb_n == 0) continue;
-      } else {
-        n = (rag_tile<16>(sched, args, t).rows + 15) / 16 * 16;
+      const int cnt = rows_next;
+      const int kb_n = OP == RAG_WGRAD ? (cnt + BK - 1) / BK : args.num_kb;
+      const int n = OP == RAG_WGRAD ? 256 : (cnt + 15) / 16 * 16;
+      if (kb_n == 0) {
+        rows_next = rows_of(t + gridDim.x);
+        continue;
       }
       const uint32_t idesc = make_idesc(Half16<T>::kFmt, Half16<T>::kFmt, 128, n) | major;
       const int acc = local & 1;
@@ -235,6 +252,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
           umma_f16(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
                    (kb | k) != 0);
         tc_commit(empty_bar(stage));
+        if (kb == 0) rows_next = rows_of(t + gridDim.x);
         if (++stage == stages) {
           stage = 0;
           phase ^= 1;
@@ -358,7 +376,9 @@ cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows,
   const bool fwd = op == RAG_FWD;
   CUtensorMap tmA, tmB;
   const int red = fwd ? p.K : p.N;
-  if (!make_tmap_rag(&tmA, w, p.half, 3, p.K, p.N, p.E, p.K, fwd ? 128 : 64) ||
+  const bool wide = !fwd && p.K % 64 == 0;
+  if (!(wide ? make_tmap_rag_wide(&tmA, w, p.half, p.N, p.K, p.E, p.K, 2)
+             : make_tmap_rag(&tmA, w, p.half, 3, p.K, p.N, p.E, p.K, fwd ? 128 : 64)) ||
       !make_tmap_rag(&tmB, rows, p.half, 2, red, p.R, 0, fwd ? p.ldx : p.ldy, 32))
     return cudaErrorInvalidValue;
   RagArgs a{};
@@ -373,6 +393,7 @@ cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows,
   a.tile_rows = p.R <= 32 ? 32 : p.R <= 64 ? 64 : p.R <= 128 ? 128 : 256;
   a.stages = std::min(MAX_STAGES, RING_BYTES / (A_BYTES + a.tile_rows * BK * 2));
   a.group_max = 8;
+  a.wide_a = wide;
   a.out = out;
   a.ldo = fwd ? p.ldy : p.ldx;
   a.bias = bias;
@@ -389,8 +410,11 @@ cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows,
 cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const void* x, void* dw,
                                 bool out_f32, bool accumulate, cudaStream_t stream) {
   CUtensorMap tmA, tmB, tmD;
-  if (!make_tmap_rag(&tmA, dy, p.half, 2, p.N, p.R, 0, p.ldy, 64) ||
-      !make_tmap_rag(&tmB, x, p.half, 2, p.K, p.R, 0, p.ldx, 64) ||
+  const bool wide_a = p.N % 64 == 0, wide_b = p.K % 64 == 0;
+  if (!(wide_a ? make_tmap_rag_wide(&tmA, dy, p.half, p.R, p.N, 1, p.ldy, 2)
+               : make_tmap_rag(&tmA, dy, p.half, 2, p.N, p.R, 0, p.ldy, 64)) ||
+      !(wide_b ? make_tmap_rag_wide(&tmB, x, p.half, p.R, p.K, 1, p.ldx, 4)
+               : make_tmap_rag(&tmB, x, p.half, 2, p.K, p.R, 0, p.ldx, 64)) ||
       !make_tmap_rag_store(&tmD, dw, out_f32 ? 2 : p.half ? 1 : 0, p.K, p.N, p.E))
     return cudaErrorInvalidValue;
   RagArgs a{};
@@ -404,6 +428,8 @@ cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const vo
   a.tile_rows = 256;
   a.stages = RING_BYTES / (A_BYTES + 256 * BK * 2);
   a.group_max = 8;
+  a.wide_a = wide_a;
+  a.wide_b = wide_b;
   a.out = dw;
   a.out_f32 = out_f32;
   a.accumulate = accumulate;

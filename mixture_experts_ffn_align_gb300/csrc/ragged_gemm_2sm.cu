@@ -26,6 +26,8 @@ namespace moe {
 
 bool make_tmap_rag_store(CUtensorMap* map, const void* base, int elem, uint64_t K, uint64_t N,
                          uint64_t E);
+bool make_tmap_rag_wide(CUtensorMap* map, const void* base, bool half, uint64_t rows,
+                        uint64_t cols, uint64_t batch, uint64_t ld, uint32_t chunks);
 bool make_tmap_rag(CUtensorMap* map, const void* base, bool half, int rank, uint64_t d0,
                    uint64_t d1, uint64_t d2, uint64_t ld, uint32_t box1);
 
@@ -34,7 +36,7 @@ namespace {
 constexpr int BK = 64, MAX_STAGES = 6;
 constexpr int A_BYTES = 128 * BK * 2, B_BYTES = 128 * BK * 2;   // this CTA's halves
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int PAIR_TX = 2 * STAGE_BYTES;
+constexpr int SMALL_BOX = 32 * BK * 2;
 constexpr int TMEM_COLS = 512;
 constexpr int EPI_WARPS = 4;
 // producer, MMA, epilogue warps; wgrad has one more, which zeroes
@@ -45,10 +47,11 @@ static_assert(EPI_WARPS * BOXES * 4096 <= STAGE_BYTES, "store boxes");
 constexpr int SMEM_BYTES = MAX_STAGES * STAGE_BYTES + 1024 + BAR_BYTES + kRagSchedBytes;
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 
+// tmC: forward and dgrad: the tokens in boxes of 32 rows; wgrad: the output.
 template <int OP, typename T>
 __global__ void __launch_bounds__(num_threads(OP), 1)
     k_ragged_2sm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const __grid_constant__ CUtensorMap tmD, const RagArgs args) {
+                 const __grid_constant__ CUtensorMap tmC, const RagArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     for (int t = first; t < total; t += stride) {
       RagTile D{};
       RagWTile V{};
-      int kb_n = args.num_kb, row0, tail_kb = -1;
+      int kb_n = args.num_kb, row0, tail_kb = -1, b_bytes = B_BYTES;
       if (OP == RAG_WGRAD) {
         V = rag_wtile(args, t);
         const int2 rows = s_rows[V.e];
@@ -131,8 +134,12 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         if (rows.y % 16) tail_kb = kb_n - 1;
       } else {
         D = rag_tile<32>(sched, args, t);
-        // this CTA's half of the token operand
-        row0 = D.row0 + (leader ? 0 : (D.rows + 31) / 32 * 16);
+        // this CTA's half of the token operand: one box of 128 rows, or as many
+        // of 32 as it has (a decode step's few rows then move little beside the
+        // weights)
+        const int own = (D.rows + 31) / 32 * 16;
+        row0 = D.row0 + (leader ? 0 : own);
+        if (own <= 64) b_bytes = (own + 31) / 32 * SMALL_BOX;
       }
       bool ok = true;
       for (int kb = 0; kb < kb_n; ++kb) {
@@ -153,26 +160,42 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
             tail_parity ^= 1u << stage;     // bit: parity of the next use's phase
             tail_mask |= 1u << stage;
           } else if (leader) {
-            mbar_arrive_expect_tx(full_bar(stage), PAIR_TX);
+            mbar_arrive_expect_tx(full_bar(stage), 2 * (A_BYTES + b_bytes));
           }
           issued_mask |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           if (OP == RAG_WGRAD) {
             const int n0 = V.n_tile * 256 + rank * 128, k0 = V.k_tile * 256 + rank * 128;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              tma_load_2d_pair(sa + i * 8192, &tmA, bar, n0 + 64 * i, row0 + kb * BK, pol_t);
-              tma_load_2d_pair(sb + i * 8192, &tmB, bar, k0 + 64 * i, row0 + kb * BK, pol_t);
+            const int r0 = row0 + kb * BK;
+            if (args.wide_a) {
+              tma_load_4d_pair(sa, &tmA, bar, 0, r0, n0 / 64, 0, pol_t);
+            } else {
+              tma_load_2d_pair(sa, &tmA, bar, n0, r0, pol_t);
+              tma_load_2d_pair(sa + 8192, &tmA, bar, n0 + 64, r0, pol_t);
+            }
+            if (args.wide_b) {
+              tma_load_4d_pair(sb, &tmB, bar, 0, r0, k0 / 64, 0, pol_t);
+            } else {
+              tma_load_2d_pair(sb, &tmB, bar, k0, r0, pol_t);
+              tma_load_2d_pair(sb + 8192, &tmB, bar, k0 + 64, r0, pol_t);
             }
           } else {
             const int w0 = D.w_tile * 256 + rank * 128;
             if (OP == RAG_FWD) {
               tma_load_3d_pair(sa, &tmA, bar, kb * BK, w0, D.e, pol_w);
+            } else if (args.wide_a) {
+              tma_load_4d_pair(sa, &tmA, bar, 0, kb * BK, w0 / 64, D.e, pol_w);
             } else {
               tma_load_3d_pair(sa, &tmA, bar, w0, kb * BK, D.e, pol_w);
               tma_load_3d_pair(sa + 8192, &tmA, bar, w0 + 64, kb * BK, D.e, pol_w);
             }
-            tma_load_2d_pair(sb, &tmB, bar, kb * BK, row0, pol_t);
+            if (b_bytes == B_BYTES) {
+              tma_load_2d_pair(sb, &tmB, bar, kb * BK, row0, pol_t);
+            } else {
+              tma_load_2d_pair(sb, &tmC, bar, kb * BK, row0, pol_t);
+              if (b_bytes > SMALL_BOX)
+                tma_load_2d_pair(sb + SMALL_BOX, &tmC, bar, kb * BK, row0 + 32, pol_t);
+            }
           }
         }
         if (++stage == STAGES) {
@@ -198,14 +221,20 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     int stage = 0;
     uint32_t phase = 0, tail_parity = 0;
     int local = 0;
+    // rows of tile t (wgrad: of its expert); the next tile's are looked up while
+    // this one's MMAs run
+    auto rows_of = [&](int t) -> int {
+      if (t >= total) return 0;
+      return OP == RAG_WGRAD ? s_rows[rag_wtile(args, t).e].y : rag_tile<32>(sched, args, t).rows;
+    };
+    int rows_next = rows_of(first);
     for (int t = first; t < total; t += stride) {
-      int kb_n = args.num_kb, n = 256, cnt = 0;
-      if (OP == RAG_WGRAD) {
-        cnt = s_rows[rag_wtile(args, t).e].y;
-        kb_n = (cnt + BK - 1) / BK;
-        if (kb_n == 0) continue;
-      } else {
-        n = (rag_tile<32>(sched, args, t).rows + 31) / 32 * 32;
+      const int cnt = rows_next;
+      const int kb_n = OP == RAG_WGRAD ? (cnt + BK - 1) / BK : args.num_kb;
+      const int n = OP == RAG_WGRAD ? 256 : (cnt + 31) / 32 * 32;
+      if (kb_n == 0) {
+        rows_next = rows_of(t + stride);
+        continue;
       }
       const uint32_t idesc = make_idesc(Half16<T>::kFmt, Half16<T>::kFmt, 256, n) | major;
       const int acc = local & 1;
@@ -240,6 +269,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
           umma_f16_pair(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
                         (kb | k) != 0);
         tc_commit_pair(empty_bar(stage), 0x3);
+        if (kb == 0) rows_next = rows_of(t + stride);
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
@@ -306,7 +336,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         ++local;
       };
       if (OP == RAG_WGRAD) {
-        rag_wgrad_epilogue<T, BOXES>(args, &tmD, box_base + (warp - 2) * BOXES * 4096, turn, taddr,
+        rag_wgrad_epilogue<T, BOXES>(args, &tmC, box_base + (warp - 2) * BOXES * 4096, turn, taddr,
                                      empty, V.e, V.n_tile * 256 + rank * 128 + q * 32, V.k_tile * 256, lane, release);
       } else {
         const int w = D.w_tile * 256 + rank * 128 + q * 32 + lane;
@@ -348,7 +378,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
 
 template <int OP, typename T>
 cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB,
-                      const CUtensorMap& tmD, const RagArgs& a,
+                      const CUtensorMap& tmC, const RagArgs& a,
                         long long tiles, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -378,14 +408,14 @@ cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB,
   if (max_pairs[dev] <= 0) return cudaErrorInvalidConfiguration;
   cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(max_pairs[dev], tiles), 1, 1);
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, k_ragged_2sm<OP, T>, tmA, tmB, tmD, a);
+  return cudaLaunchKernelEx(&cfg, k_ragged_2sm<OP, T>, tmA, tmB, tmC, a);
 }
 template <int OP>
 cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,
-                      const CUtensorMap& tmD, const RagArgs& a,
+                      const CUtensorMap& tmC, const RagArgs& a,
                       long long tiles, cudaStream_t stream) {
-  return half ? launch_pair<OP, __half>(tmA, tmB, tmD, a, tiles, stream)
-              : launch_pair<OP, __nv_bfloat16>(tmA, tmB, tmD, a, tiles, stream);
+  return half ? launch_pair<OP, __half>(tmA, tmB, tmC, a, tiles, stream)
+              : launch_pair<OP, __nv_bfloat16>(tmA, tmB, tmC, a, tiles, stream);
 }
 
 bool common(const RaggedProblem& p, RagArgs& a) {
@@ -405,31 +435,38 @@ cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* r
                                    const void* bias, void* out,
                                    cudaStream_t stream) {
   const bool fwd = op == RAG_FWD;
-  CUtensorMap tmA, tmB;
+  CUtensorMap tmA, tmB, tmC;
   const int red = fwd ? p.K : p.N;
-  if (!make_tmap_rag(&tmA, w, p.half, 3, p.K, p.N, p.E, p.K, fwd ? 128 : 64) ||
-      !make_tmap_rag(&tmB, rows, p.half, 2, red, p.R, 0, fwd ? p.ldx : p.ldy, 128))
+  const bool wide = !fwd && p.K % 64 == 0;
+  if (!(wide ? make_tmap_rag_wide(&tmA, w, p.half, p.N, p.K, p.E, p.K, 2)
+             : make_tmap_rag(&tmA, w, p.half, 3, p.K, p.N, p.E, p.K, fwd ? 128 : 64)) ||
+      !make_tmap_rag(&tmB, rows, p.half, 2, red, p.R, 0, fwd ? p.ldx : p.ldy, 128) ||
+      !make_tmap_rag(&tmC, rows, p.half, 2, red, p.R, 0, fwd ? p.ldx : p.ldy, 32))
     return cudaErrorInvalidValue;
   RagArgs a{};
   if (!common(p, a)) return cudaErrorInvalidDevice;
   a.W = fwd ? p.N : p.K;
   a.num_kb = (red + BK - 1) / BK;
   a.w_tiles = (a.W + 255) / 256;
+  a.wide_a = wide;
   a.out = out;
   a.ldo = fwd ? p.ldy : p.ldx;
   a.bias = bias;
   const long long tiles = ((long long)std::min(p.E, p.R) + p.R / 256) * a.w_tiles;   // at most
-  return fwd ? launch_op<RAG_FWD>(p.half, tmA, tmB, tmB, a, tiles, stream)
-             : launch_op<RAG_DGRAD>(p.half, tmA, tmB, tmB, a, tiles, stream);
+  return fwd ? launch_op<RAG_FWD>(p.half, tmA, tmB, tmC, a, tiles, stream)
+             : launch_op<RAG_DGRAD>(p.half, tmA, tmB, tmC, a, tiles, stream);
 }
 
 cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, const void* x,
                                     void* dw, bool out_f32, bool accumulate,
                                     cudaStream_t stream) {
-  CUtensorMap tmA, tmB, tmD;
-  if (!make_tmap_rag(&tmA, dy, p.half, 2, p.N, p.R, 0, p.ldy, 64) ||
-      !make_tmap_rag(&tmB, x, p.half, 2, p.K, p.R, 0, p.ldx, 64) ||
-      !make_tmap_rag_store(&tmD, dw, out_f32 ? 2 : p.half ? 1 : 0, p.K, p.N, p.E))
+  CUtensorMap tmA, tmB, tmC;
+  const bool wide_a = p.N % 64 == 0, wide_b = p.K % 64 == 0;
+  if (!(wide_a ? make_tmap_rag_wide(&tmA, dy, p.half, p.R, p.N, 1, p.ldy, 2)
+               : make_tmap_rag(&tmA, dy, p.half, 2, p.N, p.R, 0, p.ldy, 64)) ||
+      !(wide_b ? make_tmap_rag_wide(&tmB, x, p.half, p.R, p.K, 1, p.ldx, 2)
+               : make_tmap_rag(&tmB, x, p.half, 2, p.K, p.R, 0, p.ldx, 64)) ||
+      !make_tmap_rag_store(&tmC, dw, out_f32 ? 2 : p.half ? 1 : 0, p.K, p.N, p.E))
     return cudaErrorInvalidValue;
   RagArgs a{};
   if (!common(p, a)) return cudaErrorInvalidDevice;
@@ -437,10 +474,12 @@ cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, cons
   a.K = p.K;
   a.w_tiles = (p.N + 255) / 256;
   a.k_tiles = (p.K + 255) / 256;
+  a.wide_a = wide_a;
+  a.wide_b = wide_b;
   a.out = dw;
   a.out_f32 = out_f32;
   a.accumulate = accumulate;
-  return launch_op<RAG_WGRAD>(p.half, tmA, tmB, tmD, a, (long long)p.E * a.w_tiles * a.k_tiles, stream);
+  return launch_op<RAG_WGRAD>(p.half, tmA, tmB, tmC, a, (long long)p.E * a.w_tiles * a.k_tiles, stream);
 }
 
 }  // namespace moe

@@ -32,6 +32,7 @@ namespace {
 constexpr int BK = 256, STAGES = 4;
 constexpr int A_BYTES = 128 * BK / 2, B_BYTES = 128 * BK / 2;   // this CTA's halves
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int SMALL_BOX = 32 * BK / 2;
 constexpr int SLOT_BYTES = 1024 + 2048;      // A: 2 words x 512; B: 2 words x 2 x 512
 constexpr int SF_COL0 = 256, SF_SLOT = 64;   // A word 0, A word 1, B word 0, B word 1: 16 each
 constexpr int TMEM_COLS = 512;
@@ -57,6 +58,7 @@ template <typename T>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     k_ragged_mxfp4_2sm(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmB32,
                        const __grid_constant__ CUtensorMap tmSA,
                        const __grid_constant__ CUtensorMap tmSB, const Mx44Args margs) {
   extern __shared__ uint8_t smem_raw[];
@@ -127,8 +129,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool skip_first = leader && args.never_arrive != 0;
     for (int t = first; t < total; t += stride) {
       const RagTile D = rag_tile<32>(sched, args, t);
-      // this CTA's half of the tokens
-      const int row0 = D.row0 + (leader ? 0 : (D.rows + 31) / 32 * 16);
+      // this CTA's half of the tokens: one box of 128 rows, or one or two of 32
+      const int own = (D.rows + 31) / 32 * 16;
+      const int row0 = D.row0 + (leader ? 0 : own);
+      const int b_bytes = own <= 64 ? (own + 31) / 32 * SMALL_BOX : B_BYTES;
       const int w0 = D.w_tile * 256 + rank * 128;
       bool ok = true;
       for (int kb = 0; kb < args.num_kb; ++kb) {
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint32_t bar = mapa_shared(full_bar(stage), 0);
           if (leader) {
             mbar_arrive_expect_tx(sfull_bar(stage), 2 * SLOT_BYTES);
-            mbar_arrive_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
+            mbar_arrive_expect_tx(full_bar(stage), 2 * (A_BYTES + b_bytes));
             issued_mask |= 1u << stage;
             issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           }
@@ -153,7 +157,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tma_load_3d_pair(slot, &tmSA, sbar, 0, w0 / 128, D.e * kb128 + 2 * kb, pol_w);
           tma_load_2d_pair(slot + 1024, &tmSB, sbar, 0, (D.tok * kb128 + 2 * kb) * 2, pol_t);
           tma_load_3d_pair(sa, &tmA, bar, kb * (BK / 2), w0, D.e, pol_w);
-          tma_load_2d_pair(sa + A_BYTES, &tmB, bar, kb * (BK / 2), row0, pol_t);
+          const uint32_t sb = sa + A_BYTES;
+          if (b_bytes == B_BYTES) {
+            tma_load_2d_pair(sb, &tmB, bar, kb * (BK / 2), row0, pol_t);
+          } else {
+            tma_load_2d_pair(sb, &tmB32, bar, kb * (BK / 2), row0, pol_t);
+            if (b_bytes > SMALL_BOX)
+              tma_load_2d_pair(sb + SMALL_BOX, &tmB32, bar, kb * (BK / 2), row0 + 32, pol_t);
+          }
         }
         if (++stage == STAGES) {
           stage = 0;
@@ -296,7 +307,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 template <typename T>
-cudaError_t launch_mx_pair(const CUtensorMap (&tm)[4], const Mx44Args& a, long long tiles,
+cudaError_t launch_mx_pair(const CUtensorMap (&tm)[5], const Mx44Args& a, long long tiles,
                            cudaStream_t stream) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -326,7 +337,7 @@ cudaError_t launch_mx_pair(const CUtensorMap (&tm)[4], const Mx44Args& a, long l
   if (max_pairs[dev] <= 0) return cudaErrorInvalidConfiguration;
   cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(max_pairs[dev], tiles), 1, 1);
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, k_ragged_mxfp4_2sm<T>, tm[0], tm[1], tm[2], tm[3], a);
+  return cudaLaunchKernelEx(&cfg, k_ragged_mxfp4_2sm<T>, tm[0], tm[1], tm[4], tm[2], tm[3], a);
 }
 
 }  // namespace
@@ -335,9 +346,10 @@ cudaError_t launch_ragged_mxfp4_2sm(const RaggedProblem& p, const void* xq, cons
                                     const void* wq, const void* w_scale_packed, void* y,
                                     void* workspace, cudaStream_t stream) {
   const long long tok = most_token_tiles(p.R, p.E, 256);
-  CUtensorMap tm[4];
+  CUtensorMap tm[5];
   if (!make_tmap_rag_fp4(&tm[0], wq, 3, p.K, p.N, p.E, 128) ||
       !make_tmap_rag_fp4(&tm[1], xq, 2, p.K, p.R, 0, 128) ||
+      !make_tmap_rag_fp4(&tm[4], xq, 2, p.K, p.R, 0, 32) ||
       !make_tmap_scale_blocks(&tm[2], w_scale_packed, 3, p.N / 128, (uint64_t)p.E * (p.K / 128), 1,
                               2) ||
       !make_tmap_scale_blocks(&tm[3], workspace, 2, (uint64_t)tok * (p.K / 128) * 2, 0, 4, 1))

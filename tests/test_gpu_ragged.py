@@ -104,7 +104,7 @@ def test_segments(name, dtype):
     run_all(SEGMENTS[name], 264, 200, dtype)
 
 
-@pytest.mark.parametrize("n, k", [(8, 8), (8, 1032), (1032, 8), (128, 64), (136, 72), (520, 264),
+@pytest.mark.parametrize("n, k", [(192, 320), (320, 192), (8, 8), (8, 1032), (1032, 8), (128, 64), (136, 72), (520, 264),
                                   (256, 4104), (2056, 128)])
 def test_odd_sizes(n, k):
     run_all([5, 0, 200, 33], n, k, "bfloat16", seed=5)
