@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from dataclasses import dataclass
 from functools import cache, cached_property
 from types import SimpleNamespace
@@ -569,16 +570,18 @@ def moe_clip_grad_norm(grads, max_norm, norm, workspace, out=None, stream=None):
     and clipping to max_norm, in place or into the tensors of ``out``."""
     n = len(grads)
     src, numel, types = _tensor_arrays("grads", grads)
-    src = (ctypes.c_void_p * n)(*src)
+    src = array("Q", src)
     dst = src
     if out is not None:
         dst, n2, t2 = _tensor_arrays("out", out)
         if n2 != numel or t2 != types:
             raise ValueError("out must match grads in number, lengths and types")
-        dst = (ctypes.c_void_p * n)(*dst)
+        dst = array("Q", dst)
+    numel, types = array("q", numel), array("i", types)
     ws, size = _bytes("workspace", workspace)
     _check(lib().moe_clip_grad_norm(
-        n, src, dst, (ctypes.c_int64 * n)(*numel), (ctypes.c_int32 * n)(*types), max_norm,
+        n, src.buffer_info()[0], dst.buffer_info()[0], numel.buffer_info()[0],
+        types.buffer_info()[0], max_norm,
         _dense("norm", norm, norm.shape, _t().float32), ws, size, _raw_stream(stream, norm)),
         "moe_clip_grad_norm")
 

@@ -19,6 +19,7 @@
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "pdl.cuh"
 #include "ragged.cuh"
 
 namespace moe {
@@ -165,6 +166,8 @@ __device__ __forceinline__ double block_sum(double v) {
 template <int CAP>
 __global__ void __launch_bounds__(kThreads)
     k_clip_norm(const __grid_constant__ List<CAP> L, double* partial) {
+  griddep_launch();
+  griddep_wait();
   double sum = 0.0;
   const int chunks = L.chunk0[L.n];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
@@ -184,6 +187,8 @@ template <int CAP>
 __global__ void __launch_bounds__(kThreads)
     k_clip_scale(const __grid_constant__ List<CAP> L, const double* partial, int partials,
                  float max_norm, float* norm_out, int in_place) {
+  griddep_launch();
+  griddep_wait();
   double sum = 0.0;
   for (int i = threadIdx.x; i < partials; i += kThreads) sum += partial[i];
   const float norm = (float)sqrt(block_sum(sum));
@@ -236,8 +241,8 @@ cudaError_t clip_lists(int n, const void* const* grads, void* const* outs, const
     const int at = l * CAP;
     const int chunks = fill(L, at, std::min(CAP, n - at), grads, outs, numel, types);
     const int grid = std::max(1, std::min(chunks, most));
-    k_clip_norm<CAP><<<grid, kThreads, 0, stream>>>(L, partial + partials);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_dependent(k_clip_norm<CAP>, grid, kThreads, 0, stream, 1, L, partial + partials);
     if (e != cudaSuccess) return e;
     partials += grid;
   }
@@ -245,9 +250,9 @@ cudaError_t clip_lists(int n, const void* const* grads, void* const* outs, const
     const int at = l * CAP;
     const int chunks = fill(L, at, std::min(CAP, n - at), grads, outs, numel, types);
     const int grid = std::max(1, std::min(chunks, most));
-    k_clip_scale<CAP><<<grid, kThreads, 0, stream>>>(L, partial, partials, max_norm,
-                                                     l == 0 ? norm : nullptr, in_place);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_dependent(k_clip_scale<CAP>, grid, kThreads, 0, stream, 1, L, partial, partials,
+                         max_norm, l == 0 ? norm : nullptr, in_place);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -21,6 +21,7 @@
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "pdl.cuh"
 #include "ragged.cuh"
 
 namespace moe {
@@ -91,9 +92,12 @@ template <int TYPE, bool DENSE>
 __global__ void __launch_bounds__(kThreads)
     k_mxfp4_quantize(const void* __restrict__ x, size_t units, int units_per_row, long long ldx,
                      int ceil_scale, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  const size_t step = (size_t)gridDim.x * kThreads;
+  griddep_launch();
+  griddep_wait();
+  constexpr int step = kThreads;      // a block's units are consecutive
   // every lane of a group of four has a unit or none has: units % 4 == 0
-  for (size_t u0 = (size_t)blockIdx.x * kThreads + threadIdx.x; u0 < units; u0 += step * kUnroll) {
+  for (size_t u0 = (size_t)blockIdx.x * kThreads * kUnroll + threadIdx.x; u0 < units;
+       u0 += (size_t)gridDim.x * kThreads * kUnroll) {
     Load8<TYPE> in[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
@@ -137,8 +141,11 @@ template <int TYPE, bool DENSE>
 __global__ void __launch_bounds__(kThreads)
     k_mxfp4_dequantize(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                        size_t units, int units_per_row, long long ldo, void* __restrict__ out) {
-  const size_t step = (size_t)gridDim.x * kThreads;
-  for (size_t u0 = (size_t)blockIdx.x * kThreads + threadIdx.x; u0 < units; u0 += step * kUnroll) {
+  griddep_launch();
+  griddep_wait();
+  constexpr int step = kThreads;
+  for (size_t u0 = (size_t)blockIdx.x * kThreads * kUnroll + threadIdx.x; u0 < units;
+       u0 += (size_t)gridDim.x * kThreads * kUnroll) {
     uint32_t c[kUnroll], s[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
@@ -190,30 +197,28 @@ uint32_t h[4];
   }
 }
 
+// A block for every kThreads * kUnroll units.  (A grid of a few blocks an SM
+// striding over the tensor ran 451 us for 229376 x 4096 bf16 against 360: its
+// loads lie 20 MB apart, and eight blocks an SM are one and a third waves.)
 int codec_grid(size_t units) {
   const size_t want = (units + kThreads * kUnroll - 1) / (kThreads * kUnroll);
-  return (int)std::min<size_t>(std::max<size_t>(want, 1), (size_t)num_sms() * 8);
+  return (int)std::min<size_t>(want, 1u << 30);
 }
 
 template <int TYPE>
-void quantize_of(const void* x, size_t units, int upr, long long ldx, int K, bool ceil_scale,
-                 uint8_t* codes, uint8_t* scales, cudaStream_t st) {
-  const int grid = codec_grid(units);
-  uint32_t* c = reinterpret_cast<uint32_t*>(codes);
-  if (ldx == K)
-    k_mxfp4_quantize<TYPE, true><<<grid, kThreads, 0, st>>>(x, units, upr, ldx, ceil_scale, c, scales);
-  else
-    k_mxfp4_quantize<TYPE, false><<<grid, kThreads, 0, st>>>(x, units, upr, ldx, ceil_scale, c, scales);
+cudaError_t quantize_of(const void* x, size_t units, int upr, long long ldx, int K,
+                        bool ceil_scale, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+  return launch_dependent(ldx == K ? k_mxfp4_quantize<TYPE, true> : k_mxfp4_quantize<TYPE, false>,
+                          codec_grid(units), kThreads, 0, st, 1, x, units, upr, ldx,
+                          ceil_scale ? 1 : 0, reinterpret_cast<uint32_t*>(codes), scales);
 }
 template <int TYPE>
-void dequantize_of(const uint8_t* codes, const uint8_t* scales, size_t units, int upr,
-                   long long ldo, int K, void* out, cudaStream_t st) {
-  const int grid = codec_grid(units);
-  const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
-  if (ldo == K)
-    k_mxfp4_dequantize<TYPE, true><<<grid, kThreads, 0, st>>>(c, scales, units, upr, ldo, out);
-  else
-    k_mxfp4_dequantize<TYPE, false><<<grid, kThreads, 0, st>>>(c, scales, units, upr, ldo, out);
+cudaError_t dequantize_of(const uint8_t* codes, const uint8_t* scales, size_t units, int upr,
+                          long long ldo, int K, void* out, cudaStream_t st) {
+  return launch_dependent(
+      ldo == K ? k_mxfp4_dequantize<TYPE, true> : k_mxfp4_dequantize<TYPE, false>,
+      codec_grid(units), kThreads, 0, st, 1, reinterpret_cast<const uint32_t*>(codes), scales,
+      units, upr, ldo, out);
 }
 
 }  // namespace
@@ -222,18 +227,16 @@ cudaError_t launch_mxfp4_quantize(const void* x, int type, long long rows, int K
                                   bool ceil_scale, uint8_t* codes, uint8_t* scales,
                                   cudaStream_t stream) {
   const size_t units = (size_t)rows * (K / 8);
-  (type == 0 ? quantize_of<0> : type == 1 ? quantize_of<1> : quantize_of<2>)(
+  return (type == 0 ? quantize_of<0> : type == 1 ? quantize_of<1> : quantize_of<2>)(
       x, units, K / 8, ldx, K, ceil_scale, codes, scales, stream);
-  return cudaGetLastError();
 }
 
 cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, long long rows,
                                     int K, void* out, int type, long long ldo,
                                     cudaStream_t stream) {
   const size_t units = (size_t)rows * (K / 8);
-  (type == 0 ? dequantize_of<0> : type == 1 ? dequantize_of<1> : dequantize_of<2>)(
+  return (type == 0 ? dequantize_of<0> : type == 1 ? dequantize_of<1> : dequantize_of<2>)(
       codes, scales, units, K / 8, ldo, K, out, stream);
-  return cudaGetLastError();
 }
 
 }  // namespace moe

@@ -23,6 +23,7 @@
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "pdl.cuh"
 #include "ragged.cuh"
 
 namespace moe {
@@ -74,6 +75,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   auto tail_bar = [&](int s) { return bar_base + 8u * (2 * MAX_STAGES + 5 + s); };
   auto zeroed_bar = [&](int s) { return bar_base + 8u * (3 * MAX_STAGES + 5 + s); };
 
+  griddep_launch();
   if (threadIdx.x == 0) {
     for (int s = 0; s < MAX_STAGES; ++s) {
       mbar_init(full_bar(s), 1);
@@ -103,6 +105,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
+  griddep_wait();
   const RagSched sched = rag_sched_build<16>(args, s_sched, reinterpret_cast<int*>(smem));
   const int2* s_rows = OP == RAG_WGRAD
                            ? rag_rows_by_expert(sched, args.E, s_sched, reinterpret_cast<int2*>(smem))
@@ -358,8 +361,8 @@ cudaError_t launch_one(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                 SMEM_BYTES);
   });
   if (e != cudaSuccess) return e;
-  k_ragged<OP, T><<<grid, num_threads(OP), SMEM_BYTES, stream>>>(tmA, tmB, tmD, a);
-  return cudaGetLastError();
+  return launch_dependent(k_ragged<OP, T>, grid, num_threads(OP), SMEM_BYTES, stream, 1, tmA, tmB,
+                          tmD, a);
 }
 template <int OP>
 cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,

@@ -20,6 +20,7 @@
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "pdl.cuh"
 #include "ragged.cuh"
 
 namespace moe {
@@ -78,6 +79,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   auto tempty_bar = [&](int a) { return bar_base + 8u * (4 * STAGES + 2 + a); };
   const uint32_t drain_bar = bar_base + 8u * (4 * STAGES + 4);
 
+  griddep_launch();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 3 * STAGES; ++s) mbar_init(bar_base + 8u * s, 1);
     for (int s = 0; s < STAGES; ++s) mbar_init(zeroed_bar(s), 2);   // one warp of each CTA
@@ -104,6 +106,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
+  griddep_wait();
   const RagSched sched = rag_sched_build<32>(args, s_sched, reinterpret_cast<int*>(smem));
   const int2* s_rows = OP == RAG_WGRAD
                            ? rag_rows_by_expert(sched, args.E, s_sched, reinterpret_cast<int2*>(smem))
@@ -406,9 +409,8 @@ cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB,
   });
   if (es != cudaSuccess) return es;
   if (max_pairs[dev] <= 0) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(max_pairs[dev], tiles), 1, 1);
-  cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, k_ragged_2sm<OP, T>, tmA, tmB, tmC, a);
+  return launch_dependent(k_ragged_2sm<OP, T>, 2 * (unsigned)std::min<long long>(max_pairs[dev], tiles),
+                          num_threads(OP), SMEM_BYTES, stream, 2, tmA, tmB, tmC, a);
 }
 template <int OP>
 cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,

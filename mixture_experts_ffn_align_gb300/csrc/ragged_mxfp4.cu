@@ -27,6 +27,7 @@
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "pdl.cuh"
 #include "ragged_mx.cuh"
 
 namespace moe {
@@ -66,6 +67,8 @@ template <int G>
 __global__ void __launch_bounds__(256) k_pack_token_scales(const Mx44Args args) {
   __shared__ int s_mem[kRagSchedBytes / 4];
   __shared__ int s_scratch[kRagMaxExperts + 1];
+  griddep_launch();
+  griddep_wait();
   const RagSched sched = rag_sched_build<G>(args.r, s_mem, s_scratch);
   const int tiles = sched.tile0[sched.nseg];
   const int groups = tile_groups(args.r.tile_rows), kb_n = args.K / 128, KQ = args.K / 32;
@@ -117,6 +120,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t drain_bar = bar_base + 8u * (4 * STAGES + 4);
   const uint32_t cdrain_bar = bar_base + 8u * (4 * STAGES + 5);
 
+  griddep_launch();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 4 * STAGES; ++s) mbar_init(bar_base + 8u * s, 1);
     for (int a = 0; a < 2; ++a) {
@@ -142,6 +146,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
+  griddep_wait();
   const RagSched sched = rag_sched_build<16>(args, s_sched, reinterpret_cast<int*>(smem));
   const int total = sched.tile0[sched.nseg] * args.w_tiles;
   const int groups = tile_groups(args.tile_rows);
@@ -321,8 +326,7 @@ cudaError_t launch_mx(const CUtensorMap& tmA, const CUtensorMap& tmB, const Mx44
                                 SMEM_BYTES);
   });
   if (e != cudaSuccess) return e;
-  k_ragged_mxfp4<T><<<grid, NUM_THREADS, SMEM_BYTES, stream>>>(tmA, tmB, a);
-  return cudaGetLastError();
+  return launch_dependent(k_ragged_mxfp4<T>, grid, NUM_THREADS, SMEM_BYTES, stream, 1, tmA, tmB, a);
 }
 
 int mx_tile_rows(int R) { return R <= 128 ? 128 : 256; }
@@ -334,8 +338,8 @@ cudaError_t launch_pack_token_scales(const Mx44Args& args, long long most_tiles,
                                      cudaStream_t stream) {
   Mx44Args a = args;
   a.r.w_tiles = 1;          // tile numbers are token tiles
-  k_pack_token_scales<G><<<(int)std::min<long long>(most_tiles, 4 * num_sms()), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(k_pack_token_scales<G>, (unsigned)std::min<long long>(most_tiles, 4 * num_sms()),
+                          256, 0, stream, 1, a);
 }
 template cudaError_t launch_pack_token_scales<32>(const Mx44Args&, long long, cudaStream_t);
 

@@ -18,6 +18,7 @@
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "pdl.cuh"
 #include "ragged_mx.cuh"
 
 namespace moe {
@@ -87,6 +88,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t drain_bar = bar_base + 8u * (4 * STAGES + 2);
   const uint32_t cdrain_bar = bar_base + 8u * (4 * STAGES + 3);
 
+  griddep_launch();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 4 * STAGES; ++s) mbar_init(bar_base + 8u * s, 1);
     mbar_init(tfull_bar, 1);
@@ -113,6 +115,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
+  griddep_wait();
   const RagSched sched = rag_sched_build<32>(args, s_sched, reinterpret_cast<int*>(smem));
   const int total = sched.tile0[sched.nseg] * args.w_tiles;
   const int kb128 = margs.K / 128;
@@ -335,9 +338,8 @@ cudaError_t launch_mx_pair(const CUtensorMap (&tm)[5], const Mx44Args& a, long l
   });
   if (es != cudaSuccess) return es;
   if (max_pairs[dev] <= 0) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(max_pairs[dev], tiles), 1, 1);
-  cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, k_ragged_mxfp4_2sm<T>, tm[0], tm[1], tm[4], tm[2], tm[3], a);
+  return launch_dependent(k_ragged_mxfp4_2sm<T>, 2 * (unsigned)std::min<long long>(max_pairs[dev], tiles),
+                          NUM_THREADS, SMEM_BYTES, stream, 2, tm[0], tm[1], tm[4], tm[2], tm[3], a);
 }
 
 }  // namespace
