@@ -46,7 +46,8 @@ RaggedProblem ragged_problem(const moe_ragged* p, const int32_t* offsets) {
 bool mxfp4_shape(const moe_ragged* p) { return p->N % 128 == 0 && p->K % 128 == 0; }
 
 size_t ragged_bytes(const moe_ragged* p) {
-  size_t b = 1;
+  size_t b = std::max<size_t>(1, std::max(ragged_split_bytes(p->R, p->E, p->N, p->K),
+                                          ragged_split_bytes(p->R, p->E, p->K, p->N)));
   if (mxfp4_shape(p)) b = std::max(b, ragged_mxfp4_scale_bytes(p->R, p->K, p->E));
   return pad256(b);
 }
@@ -60,12 +61,13 @@ bool use_pairs(const moe_ragged* p, int width) {
 }
 
 cudaError_t ragged_rows(const moe_ragged* p, int op, const void* rows, const void* w,
-                        const void* bias, const int32_t* offsets, void* out, void* stream) {
+                        const void* bias, const int32_t* offsets, void* out, void* workspace,
+                        void* stream) {
   const RaggedProblem q = ragged_problem(p, offsets);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return use_pairs(p, op == 0 ? p->N : p->K)
              ? launch_ragged_rows_2sm(q, op, rows, w, bias, out, st)
-             : launch_ragged_rows(q, op, rows, w, bias, out, st);
+             : launch_ragged_rows(q, op, rows, w, bias, out, workspace, st);
 }
 
 // Checks shared by the products; MOE_OK to go on.
@@ -97,7 +99,7 @@ moe_status ragged_gemm(const moe_ragged* p, const void* x, const void* w, const 
   const moe_status s = ragged_args(p, x, w, expert_offsets, y, workspace, workspace_bytes);
   if (s != MOE_OK || p->R == 0) return s;
   if (misaligned(bias, 2)) return MOE_ERR_INVALID_ARG;
-  return done(ragged_rows(p, 0, x, w, bias, expert_offsets, y, stream));
+  return done(ragged_rows(p, 0, x, w, bias, expert_offsets, y, workspace, stream));
 }
 
 moe_status ragged_gemm_dgrad(const moe_ragged* p, const void* dy, const void* w,
@@ -105,7 +107,7 @@ moe_status ragged_gemm_dgrad(const moe_ragged* p, const void* dy, const void* w,
                              size_t workspace_bytes, void* stream) {
   const moe_status s = ragged_args(p, dy, w, expert_offsets, dx, workspace, workspace_bytes);
   if (s != MOE_OK || p->R == 0) return s;
-  return done(ragged_rows(p, 1, dy, w, nullptr, expert_offsets, dx, stream));
+  return done(ragged_rows(p, 1, dy, w, nullptr, expert_offsets, dx, workspace, stream));
 }
 
 moe_status ragged_gemm_wgrad(const moe_ragged* p, const void* dy, const void* x,

@@ -210,7 +210,11 @@ struct RaggedProblem {
 // op: 0 forward (rows = x, out = y), 1 dgrad (rows = dy, out = dx).  workspace
 // as moe_ragged_workspace_bytes.
 cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows, const void* w,
-                               const void* bias, void* out, cudaStream_t stream);
+                               const void* bias, void* out, void* workspace,
+                               cudaStream_t stream);
+// Workspace of launch_ragged_rows for an output of `width` columns and a
+// reduction of `red`.
+size_t ragged_split_bytes(int R, int E, int width, int red);
 cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const void* x, void* dw,
                                 bool out_f32, bool accumulate, cudaStream_t stream);
 // The same on SM pairs.

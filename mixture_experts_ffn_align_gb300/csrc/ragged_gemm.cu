@@ -17,6 +17,11 @@
 //    warp then writes zeros over the rows behind the segment in both operands
 //    (in one alone, an infinity or NaN of the next expert's rows would enter the
 //    sums as 0 x inf).
+//  * forward and dgrad with fewer tiles than half the SMs (few experts, narrow
+//    outputs): a cluster of 2, 4 or 8 CTAs takes one tile, each a slice of the
+//    reduction; the fp32 sums go to the workspace (they stay in L2), and after a
+//    cluster barrier each CTA adds and rounds its share of the tile's tokens, in
+//    the order of the slices.
 //  * every wait is bounded (wall clock); on a timeout the kernel records the
 //    error, drains its own copies and MMAs, frees tensor memory and returns.
 #include <algorithm>
@@ -44,9 +49,14 @@ constexpr int EPI_WARPS = 4;
 // producer, MMA, epilogue warps; wgrad has one more, which zeroes
 constexpr int num_threads(int op) { return 64 + 32 * EPI_WARPS + (op == RAG_WGRAD ? 32 : 0); }
 constexpr int TMEM_COLS = 512;
-constexpr int BOXES = 1;                      // store boxes of each epilogue warp (wgrad)
-constexpr int BOX_BYTES = EPI_WARPS * BOXES * 4096;
-constexpr int SMEM_BYTES = RING_BYTES + BOX_BYTES + 1024 + BAR_BYTES + kRagSchedBytes;
+// wgrad: three stages and four store boxes for each epilogue warp, a tile's
+// output, in the ring's space and 16 KB more.  (Four stages and one box a warp:
+// 12.4 instead of 11.9 us for 515 rows, 16 experts, 1032 x 776.)
+constexpr int W_STAGES = 3, BOXES = 4;
+constexpr int W_STAGE_BYTES = A_BYTES + 256 * BK * 2;
+constexpr int OPERAND_BYTES = W_STAGES * W_STAGE_BYTES + EPI_WARPS * BOXES * 4096;
+static_assert(OPERAND_BYTES >= RING_BYTES, "operand space");
+constexpr int SMEM_BYTES = OPERAND_BYTES + 1024 + BAR_BYTES + kRagSchedBytes;
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 static_assert(8 * (4 * MAX_STAGES + 5) + 8 <= BAR_BYTES, "barrier area");
 
@@ -57,16 +67,16 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING_BYTES + BOX_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OPERAND_BYTES);
   // full[S], empty[S], tfull[2], tempty[2], drain, tail[S], zeroed[S]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 4 * MAX_STAGES + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* s_sched = reinterpret_cast<int*>(smem + RING_BYTES + BOX_BYTES + BAR_BYTES);
+  int* s_sched = reinterpret_cast<int*>(smem + OPERAND_BYTES + BAR_BYTES);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t smem_base = smem_u32(smem);
   const uint32_t bar_base = smem_u32(bars);
-  const uint32_t box_base = smem_base + RING_BYTES;
+  const uint32_t box_base = smem_base + W_STAGES * W_STAGE_BYTES;
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
   auto empty_bar = [&](int s) { return bar_base + 8u * (MAX_STAGES + s); };
   auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * MAX_STAGES + a); };
@@ -113,6 +123,11 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   const int total = OP == RAG_WGRAD ? args.E * args.w_tiles * args.k_tiles
                                     : sched.tile0[sched.nseg] * args.w_tiles;
   const int stages = args.stages;
+  // the CTAs of a cluster share a tile (splits > 1: one tile each cluster)
+  const int splits = OP == RAG_WGRAD ? 1 : args.splits;
+  const int rank = splits > 1 ? (int)cluster_ctarank() : 0;
+  const int first = blockIdx.x / splits, stride = gridDim.x / splits;
+  const int kb0 = args.num_kb * rank / splits, kb1 = args.num_kb * (rank + 1) / splits;
   const int stage_bytes = A_BYTES + (OP == RAG_WGRAD ? 256 : args.tile_rows) * BK * 2;
 
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -126,10 +141,10 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     int stage = 0;
     uint32_t phase = 0, issued_mask = 0, issued_parity = 0, tail_mask = 0, tail_parity = 0;
     bool skip_first = args.never_arrive != 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    for (int t = first; t < total; t += stride) {
       RagTile D{};
       RagWTile V{};
-      int kb_n = args.num_kb, boxes = 4, row0 = 0;
+      int kb_n = kb1 - kb0, boxes = 4, row0 = 0;
       if (OP == RAG_WGRAD) {
         V = rag_wtile(args, t);
         kb_n = (s_rows[V.e].y + BK - 1) / BK;
@@ -173,16 +188,17 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
             }
           } else {
             mbar_arrive_expect_tx(bar, A_BYTES + boxes * 32 * BK * 2);
+            const int k0 = (kb0 + kb) * BK;
             if (OP == RAG_FWD) {
-              tma_load_3d(sa, &tmA, bar, kb * BK, D.w_tile * 128, D.e, pol_w);
+              tma_load_3d(sa, &tmA, bar, k0, D.w_tile * 128, D.e, pol_w);
             } else if (args.wide_a) {
-              tma_load_4d(sa, &tmA, bar, 0, kb * BK, D.w_tile * 2, D.e, pol_w);
+              tma_load_4d(sa, &tmA, bar, 0, k0, D.w_tile * 2, D.e, pol_w);
             } else {
-              tma_load_3d(sa, &tmA, bar, D.w_tile * 128, kb * BK, D.e, pol_w);
-              tma_load_3d(sa + 8192, &tmA, bar, D.w_tile * 128 + 64, kb * BK, D.e, pol_w);
+              tma_load_3d(sa, &tmA, bar, D.w_tile * 128, k0, D.e, pol_w);
+              tma_load_3d(sa + 8192, &tmA, bar, D.w_tile * 128 + 64, k0, D.e, pol_w);
             }
             for (int j = 0; j < boxes; ++j)
-              tma_load_2d(sb + j * 32 * BK * 2, &tmB, bar, kb * BK, D.row0 + 32 * j, pol_t);
+              tma_load_2d(sb + j * 32 * BK * 2, &tmB, bar, k0, D.row0 + 32 * j, pol_t);
           }
           issued_mask |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -214,13 +230,13 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
       if (t >= total) return 0;
       return OP == RAG_WGRAD ? s_rows[rag_wtile(args, t).e].y : rag_tile<16>(sched, args, t).rows;
     };
-    int rows_next = rows_of(blockIdx.x);
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    int rows_next = rows_of(first);
+    for (int t = first; t < total; t += stride) {
       const int cnt = rows_next;
-      const int kb_n = OP == RAG_WGRAD ? (cnt + BK - 1) / BK : args.num_kb;
+      const int kb_n = OP == RAG_WGRAD ? (cnt + BK - 1) / BK : kb1 - kb0;
       const int n = OP == RAG_WGRAD ? 256 : (cnt + 15) / 16 * 16;
       if (kb_n == 0) {
-        rows_next = rows_of(t + gridDim.x);
+        rows_next = rows_of(t + stride);
         continue;
       }
       const uint32_t idesc = make_idesc(Half16<T>::kFmt, Half16<T>::kFmt, 128, n) | major;
@@ -255,7 +271,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
           umma_f16(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
                    (kb | k) != 0);
         tc_commit(empty_bar(stage));
-        if (kb == 0) rows_next = rows_of(t + gridDim.x);
+        if (kb == 0) rows_next = rows_of(t + stride);
         if (++stage == stages) {
           stage = 0;
           phase ^= 1;
@@ -271,7 +287,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     // ------------------------------------------------------------ zeroing warp
     int stage = 0;
     uint32_t tail_parity = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    for (int t = first; t < total; t += stride) {
       const int cnt = s_rows[rag_wtile(args, t).e].y;
       const int kb_n = (cnt + BK - 1) / BK;
       if (cnt % 16) {
@@ -289,7 +305,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
     int local = 0, turn = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    for (int t = first; t < total; t += stride) {
       RagTile D{};
       RagWTile V{};
       bool empty = false;
@@ -332,6 +348,13 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
           uint32_t r[32];
           tmem_ld_32x32b_x32(taddr + c, r);
           tmem_ld_wait();
+          if (splits > 1) {
+            float* p = args.part + (((size_t)t * splits + rank) * args.tile_rows + c) * 128 + q * 32 + lane;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < D.rows) p[128 * j] = __uint_as_float(r[j]);
+            continue;
+          }
           rag_store_tokens32<T>(r, OP == RAG_FWD && args.bias != nullptr, bias,
                                 static_cast<uint16_t*>(args.out) + (D.row0 + c) * args.ldo + w,
                                 args.ldo, D.rows - c, w, args.W, lane);
@@ -349,6 +372,42 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
+  if (OP != RAG_WGRAD && splits > 1) {
+    // join: the cluster's sums are in the workspace; a lane takes four columns
+    cluster_sync();
+    if (first < total) {
+      const RagTile D = rag_tile<16>(sched, args, first);
+      const int w = D.w_tile * 128 + 4 * lane;
+      float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (OP == RAG_FWD && args.bias != nullptr && w < args.W) {
+        const uint16_t* b = static_cast<const uint16_t*>(args.bias) + (size_t)D.e * args.W + w;
+        bias = make_float4(Half16<T>::value(b[0]), Half16<T>::value(b[1]), Half16<T>::value(b[2]),
+                           Half16<T>::value(b[3]));
+      }
+      const float* p = args.part + (size_t)first * splits * args.tile_rows * 128 + 4 * lane;
+      constexpr int WARPS = num_threads(OP) / 32;
+      for (int j = rank * WARPS + warp; j < D.rows; j += splits * WARPS) {
+        float4 v[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s < splits)
+            v[s] = *reinterpret_cast<const float4*>(p + ((size_t)s * args.tile_rows + j) * 128);
+        float4 a = v[0];
+#pragma unroll
+        for (int s = 1; s < 8; ++s)
+          if (s < splits) {
+            a.x += v[s].x;
+            a.y += v[s].y;
+            a.z += v[s].z;
+            a.w += v[s].w;
+          }
+        if (w < args.W)
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.out) + (D.row0 + j) * args.ldo + w) =
+              make_uint2(Half16<T>::pack(a.x + bias.x, a.y + bias.y),
+                         Half16<T>::pack(a.z + bias.z, a.w + bias.w));
+      }
+    }
+  }
 }
 
 template <int OP, typename T>
@@ -361,8 +420,8 @@ cudaError_t launch_one(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                 SMEM_BYTES);
   });
   if (e != cudaSuccess) return e;
-  return launch_dependent(k_ragged<OP, T>, grid, num_threads(OP), SMEM_BYTES, stream, 1, tmA, tmB,
-                          tmD, a);
+  return launch_dependent(k_ragged<OP, T>, grid, num_threads(OP), SMEM_BYTES, stream,
+                          std::max(1, a.splits), tmA, tmB, tmD, a);
 }
 template <int OP>
 cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,
@@ -374,8 +433,41 @@ cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,
 
 }  // namespace
 
+// Tiles and splits of the rows' products on one SM.
+struct RowsPlan {
+  int tile_rows, w_tiles, splits;
+  long long tiles;      // at most, whatever the segments
+};
+static RowsPlan rows_plan(int R, int E, int width, int red) {
+  RowsPlan r;
+  // Token tiles of about twice the rows an expert has on average: a narrower
+  // ring stage leaves room for more of them, and so for more weight bytes in
+  // flight (256 experts of 64 rows, 7168 x 2048: dgrad 1188 us with 128 rows,
+  // 1260 with 256); a longer segment takes more tiles.
+  const int want = std::min(R, 2 * ((R + E - 1) / E));
+  r.tile_rows = want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
+  r.w_tiles = (width + 127) / 128;
+  r.tiles = ((long long)std::min(E, R) + R / r.tile_rows) * r.w_tiles;
+  // Slices of at least eight steps, as many as the SMs of the chip hold of the
+  // tiles that even segments make (a 100 x 4096 x 4096 product of one expert:
+  // 13 us in four slices, 28 us in one).  The grid and the workspace take the
+  // tiles that any segments can make.
+  constexpr int SMS = 152;
+  const long long even =
+      (long long)std::max(std::min(E, R), (R + r.tile_rows - 1) / r.tile_rows) * r.w_tiles;
+  r.splits = 1;
+  while (r.splits < 8 && even * r.splits * 2 <= SMS && (red + BK - 1) / BK >= 16 * r.splits)
+    r.splits *= 2;
+  return r;
+}
+size_t ragged_split_bytes(int R, int E, int width, int red) {
+  const RowsPlan r = rows_plan(R, E, width, red);
+  return r.splits > 1 ? (size_t)r.tiles * r.splits * r.tile_rows * 128 * sizeof(float) : 0;
+}
+
 cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows, const void* w,
-                               const void* bias, void* out, cudaStream_t stream) {
+                               const void* bias, void* out, void* workspace,
+                               cudaStream_t stream) {
   const bool fwd = op == RAG_FWD;
   CUtensorMap tmA, tmB;
   const int red = fwd ? p.K : p.N;
@@ -390,10 +482,11 @@ cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows,
   a.E = p.E;
   a.W = fwd ? p.N : p.K;
   a.num_kb = (red + BK - 1) / BK;
-  a.w_tiles = (a.W + 127) / 128;
-  // token tiles no wider than the rows there are: a narrower ring stage leaves
-  // room for more stages, and so for more weight bytes in flight
-  a.tile_rows = p.R <= 32 ? 32 : p.R <= 64 ? 64 : p.R <= 128 ? 128 : 256;
+  const RowsPlan r = rows_plan(p.R, p.E, a.W, red);
+  a.tile_rows = r.tile_rows;
+  a.w_tiles = r.w_tiles;
+  a.splits = r.splits;
+  a.part = static_cast<float*>(workspace);
   a.stages = std::min(MAX_STAGES, RING_BYTES / (A_BYTES + a.tile_rows * BK * 2));
   a.group_max = 8;
   a.wide_a = wide;
@@ -403,9 +496,8 @@ cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows,
   watchdog_params(&a.limit_ns, &a.never_arrive);
   a.err = dev_error_word();
   if (a.err == nullptr) return cudaErrorInvalidDevice;
-  const long long most =
-      ((long long)std::min(p.E, p.R) + p.R / a.tile_rows) * a.w_tiles;   // tiles at most
-  const int grid = (int)std::min<long long>(num_sms(), most);
+  const int grid = a.splits > 1 ? (int)r.tiles * a.splits
+                                : (int)std::min<long long>(num_sms(), r.tiles);
   return fwd ? launch_op<RAG_FWD>(p.half, tmA, tmB, tmB, a, grid, stream)
              : launch_op<RAG_DGRAD>(p.half, tmA, tmB, tmB, a, grid, stream);
 }
@@ -429,7 +521,7 @@ cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const vo
   a.w_tiles = (p.N + 127) / 128;
   a.k_tiles = (p.K + 255) / 256;
   a.tile_rows = 256;
-  a.stages = RING_BYTES / (A_BYTES + 256 * BK * 2);
+  a.stages = W_STAGES;
   a.group_max = 8;
   a.wide_a = wide_a;
   a.wide_b = wide_b;

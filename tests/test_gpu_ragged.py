@@ -123,6 +123,13 @@ def test_bias():
     run_all([40, 0, 290], 264, 72, "float16", bias=True)
 
 
+@pytest.mark.parametrize("rows", [1, 31, 300])
+def test_long_reduction_of_few_tiles(rows):
+    """Few tiles, long reductions in both directions: slices that are joined."""
+    run_all([rows, 0, 7], 2056, 4104, "bfloat16", bias=True, ldx=4112, ldy=2064, lead=1, tail=2)
+    run_all([rows], 1032, 72, "float16", bias=True)
+
+
 def test_many_experts():
     rng = np.random.default_rng(3)
     run_all(list(rng.integers(0, 6, 1024)), 72, 40, "bfloat16")
