@@ -623,12 +623,12 @@ def moe_debug_set_watchdog(limit_ns: int, never_arrive: bool = False):
     lib().moe_debug_set_watchdog(int(limit_ns), int(bool(never_arrive)))
 
 
-BF16_GEMM_FORMS = {"auto": 0, "single": 1, "pairs": 2}
+BF16_GEMM_FORMS = {"auto": 0, "single": 1, "pairs": 2, "pairs_double": 3}
 
 
 def moe_debug_set_bf16_gemm_form(form: str = "auto"):
-    """Force the single-SM or the SM-pair bf16 GEMM (tests), or restore the
-    size-based choice."""
+    """Force the single-SM or the SM-pair GEMMs (tests), or restore the
+    size-based choice; "pairs_double": ragged forward and dgrad on double tiles."""
     lib().moe_debug_set_bf16_gemm_form(BF16_GEMM_FORMS[form])
 
 

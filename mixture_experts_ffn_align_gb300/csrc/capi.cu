@@ -30,6 +30,7 @@ std::mutex g_dev_mu;
 int64_t g_watchdog_ns = 0;
 int g_never_arrive = 0;
 int g_bf16_form = 0;   // 0: by size, 1: single SM, 2: SM pairs
+int g_ragged_form = 0; // the same for the ragged products, 3: SM pairs on double tiles
 
 // The current device, or -1 when it cannot be read or lies beyond the
 // per-device caches (kMaxDevices); callers then fail instead of borrowing
@@ -289,7 +290,7 @@ moe_status cuda_status(cudaError_t e) {
 
 namespace moe {
 int record_cuda_status(cudaError_t e) { return cuda_status(e); }
-int gemm_form() { return g_bf16_form; }
+int ragged_form() { return g_ragged_form; }
 }  // namespace moe
 
 namespace {
@@ -882,6 +883,9 @@ void moe_debug_set_watchdog(int64_t limit_ns, int never_arrive) {
   g_never_arrive = never_arrive != 0;
 }
 
-void moe_debug_set_bf16_gemm_form(int mode) { g_bf16_form = (mode == 1 || mode == 2) ? mode : 0; }
+void moe_debug_set_bf16_gemm_form(int mode) {
+  g_bf16_form = (mode == 1 || mode == 2) ? mode : 0;
+  g_ragged_form = mode >= 1 && mode <= 3 ? mode : 0;
+}
 
 }  // extern "C"

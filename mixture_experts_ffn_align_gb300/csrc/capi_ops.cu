@@ -55,9 +55,9 @@ size_t ragged_bytes(const moe_ragged* p) {
 // SM pairs (256-wide tiles) unless that leaves fewer tiles than two for each
 // pair: then the one-SM form's 128-wide tiles spread over twice as many CTAs.
 bool use_pairs(const moe_ragged* p, int width) {
-  const int form = gemm_form();
+  const int form = ragged_form();
   const int64_t tiles = ((int64_t)std::min(p->E, p->R) + p->R / 256) * ((width + 255) / 256);
-  return form == 2 || (form == 0 && tiles >= num_sms());
+  return form >= 2 || (form == 0 && tiles >= num_sms());
 }
 
 cudaError_t ragged_rows(const moe_ragged* p, int op, const void* rows, const void* w,

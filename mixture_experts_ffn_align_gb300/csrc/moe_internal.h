@@ -224,8 +224,9 @@ cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* r
 cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, const void* x,
                                     void* dw, bool out_f32, bool accumulate,
                                     cudaStream_t stream);
-// 0: by size, 1: one SM, 2: SM pairs (moe_debug_set_bf16_gemm_form).
-int gemm_form();
+// 0: by size, 1: one SM, 2: SM pairs, 3: SM pairs on double tiles
+// (moe_debug_set_bf16_gemm_form).
+int ragged_form();
 // 4-bit product: x codes / scales [R, K/2] / [R, K/32], weights [E, N, K/2] with
 // packed scales; token scales are first rewritten to workspace.
 size_t ragged_mxfp4_scale_bytes(int R, int K, int E);

@@ -171,6 +171,12 @@ __device__ __forceinline__ RagTile rag_tile(const RagSched& s, const RagArgs& a,
   return T;
 }
 
+// Whether a double tile of 512 weights has a second half (SM pairs).
+template <int MT>
+__device__ __forceinline__ bool rag_second_tile(const RagArgs& a, int w_tile) {
+  return MT == 2 && w_tile * 512 + 256 < a.W;
+}
+
 // One tile of wgrad: expert e, rows n_tile of N and columns k_tile of K, over
 // the expert's cnt rows.  Groups of group_max n tiles, k tile by k tile, the
 // group's n tiles inner.

@@ -11,6 +11,8 @@
 //    leader's MMA thread issues M = 256, N = the tile's tokens rounded up to 32,
 //    K = 16 into one of two accumulators, and its commits reach both CTAs.
 //  * each CTA's warps 2-5 drain their own 128 accumulator rows.
+//  * long segments: two weight tiles together against the same tokens (MT = 2,
+//    512 x up to 256), one in each accumulator.
 //  * wgrad's last step of a segment that ends inside the 16 rows of an
 //    instruction: each CTA's copies complete on a barrier of its own, a seventh
 //    warp zeroes the rows behind the segment and signals the leader's issuer.
@@ -39,18 +41,22 @@ constexpr int A_BYTES = 128 * BK * 2, B_BYTES = 128 * BK * 2;   // this CTA's ha
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int SMALL_BOX = 32 * BK * 2;
 constexpr int TMEM_COLS = 512;
-constexpr int EPI_WARPS = 4;
+// Epilogue warps: four, or four for each accumulator of a double tile.
+constexpr int epi_warps(int mt) { return 4 * mt; }
 // producer, MMA, epilogue warps; wgrad has one more, which zeroes
-constexpr int num_threads(int op) { return 64 + 32 * EPI_WARPS + (op == RAG_WGRAD ? 32 : 0); }
+constexpr int num_threads(int op, int mt) {
+  return 64 + 32 * epi_warps(mt) + (op == RAG_WGRAD ? 32 : 0);
+}
 constexpr int BAR_BYTES = 256;
 constexpr int BOXES = 2;                      // store boxes of each epilogue warp (wgrad)
-static_assert(EPI_WARPS * BOXES * 4096 <= STAGE_BYTES, "store boxes");
+static_assert(epi_warps(1) * BOXES * 4096 <= STAGE_BYTES, "store boxes");
 constexpr int SMEM_BYTES = MAX_STAGES * STAGE_BYTES + 1024 + BAR_BYTES + kRagSchedBytes;
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 
 // tmC: forward and dgrad: the tokens in boxes of 32 rows; wgrad: the output.
-template <int OP, typename T>
-__global__ void __launch_bounds__(num_threads(OP), 1)
+// MT: tiles of 256 weights that a pair computes together (forward, dgrad).
+template <int OP, typename T, int MT>
+__global__ void __launch_bounds__(num_threads(OP, MT), 1)
     k_ragged_2sm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmC, const RagArgs args) {
   extern __shared__ uint8_t smem_raw[];
@@ -63,8 +69,11 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_sched = reinterpret_cast<int*>(smem + MAX_STAGES * STAGE_BYTES + BAR_BYTES);
-  // wgrad gives one stage's space to the store boxes
-  constexpr int STAGES = OP == RAG_WGRAD ? MAX_STAGES - 1 : MAX_STAGES;
+  // a stage: MT x 16 KB of weights, 16 KB of tokens; wgrad gives one stage's
+  // space to the store boxes
+  constexpr int STEP_BYTES = MT * A_BYTES + B_BYTES;
+  constexpr int STAGES = OP == RAG_WGRAD ? MAX_STAGES - 1 : MAX_STAGES * STAGE_BYTES / STEP_BYTES;
+  constexpr int EPI_WARPS = epi_warps(MT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -85,7 +94,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     for (int s = 0; s < STAGES; ++s) mbar_init(zeroed_bar(s), 2);   // one warp of each CTA
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 2 * EPI_WARPS);   // both CTAs' (leader's is used)
+      mbar_init(tempty_bar(a), 8);   // four warps of both CTAs (leader's is used)
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -128,7 +137,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     for (int t = first; t < total; t += stride) {
       RagTile D{};
       RagWTile V{};
-      int kb_n = args.num_kb, row0, tail_kb = -1, b_bytes = B_BYTES;
+      int kb_n = args.num_kb, row0, tail_kb = -1, b_bytes = B_BYTES, a_tiles = 1;
       if (OP == RAG_WGRAD) {
         V = rag_wtile(args, t);
         const int2 rows = s_rows[V.e];
@@ -143,6 +152,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         const int own = (D.rows + 31) / 32 * 16;
         row0 = D.row0 + (leader ? 0 : own);
         if (own <= 64) b_bytes = (own + 31) / 32 * SMALL_BOX;
+        a_tiles = rag_second_tile<MT>(args, D.w_tile) ? 2 : 1;
       }
       bool ok = true;
       for (int kb = 0; kb < kb_n; ++kb) {
@@ -153,7 +163,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         if (skip_first) {
           skip_first = false;   // watchdog test: leave this stage unarmed
         } else {
-          const uint32_t sa = smem_base + stage * STAGE_BYTES, sb = sa + A_BYTES;
+          const uint32_t sa = smem_base + stage * STEP_BYTES, sb = sa + MT * A_BYTES;
           uint32_t bar = mapa_shared(full_bar(stage), 0);
           if (OP == RAG_WGRAD && kb == tail_kb) {
             // copies of a step to be zeroed behind: counted on this CTA's own barrier
@@ -163,7 +173,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
             tail_parity ^= 1u << stage;     // bit: parity of the next use's phase
             tail_mask |= 1u << stage;
           } else if (leader) {
-            mbar_arrive_expect_tx(full_bar(stage), 2 * (A_BYTES + b_bytes));
+            mbar_arrive_expect_tx(full_bar(stage), 2 * (a_tiles * A_BYTES + b_bytes));
           }
           issued_mask |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -183,14 +193,17 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
               tma_load_2d_pair(sb + 8192, &tmB, bar, k0 + 64, r0, pol_t);
             }
           } else {
-            const int w0 = D.w_tile * 256 + rank * 128;
-            if (OP == RAG_FWD) {
-              tma_load_3d_pair(sa, &tmA, bar, kb * BK, w0, D.e, pol_w);
-            } else if (args.wide_a) {
-              tma_load_4d_pair(sa, &tmA, bar, 0, kb * BK, w0 / 64, D.e, pol_w);
-            } else {
-              tma_load_3d_pair(sa, &tmA, bar, w0, kb * BK, D.e, pol_w);
-              tma_load_3d_pair(sa + 8192, &tmA, bar, w0 + 64, kb * BK, D.e, pol_w);
+            for (int i = 0; i < a_tiles; ++i) {
+              const int w0 = (D.w_tile * MT + i) * 256 + rank * 128;
+              const uint32_t s_a = sa + i * A_BYTES;
+              if (OP == RAG_FWD) {
+                tma_load_3d_pair(s_a, &tmA, bar, kb * BK, w0, D.e, pol_w);
+              } else if (args.wide_a) {
+                tma_load_4d_pair(s_a, &tmA, bar, 0, kb * BK, w0 / 64, D.e, pol_w);
+              } else {
+                tma_load_3d_pair(s_a, &tmA, bar, w0, kb * BK, D.e, pol_w);
+                tma_load_3d_pair(s_a + 8192, &tmA, bar, w0 + 64, kb * BK, D.e, pol_w);
+              }
             }
             if (b_bytes == B_BYTES) {
               tma_load_2d_pair(sb, &tmB, bar, kb * BK, row0, pol_t);
@@ -223,16 +236,21 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     constexpr uint32_t a_step = OP != RAG_FWD ? 128 : 2, b_step = OP == RAG_WGRAD ? 128 : 2;
     int stage = 0;
     uint32_t phase = 0, tail_parity = 0;
-    int local = 0;
+    int local = 0, second = 0;     // tiles so far, and those with a second half
     // rows of tile t (wgrad: of its expert); the next tile's are looked up while
     // this one's MMAs run
+    bool two_next = false;        // the next tile's second half exists (MT == 2)
     auto rows_of = [&](int t) -> int {
       if (t >= total) return 0;
-      return OP == RAG_WGRAD ? s_rows[rag_wtile(args, t).e].y : rag_tile<32>(sched, args, t).rows;
+      if (OP == RAG_WGRAD) return s_rows[rag_wtile(args, t).e].y;
+      const RagTile D = rag_tile<32>(sched, args, t);
+      two_next = rag_second_tile<MT>(args, D.w_tile);
+      return D.rows;
     };
     int rows_next = rows_of(first);
     for (int t = first; t < total; t += stride) {
       const int cnt = rows_next;
+      const bool two = two_next;
       const int kb_n = OP == RAG_WGRAD ? (cnt + BK - 1) / BK : args.num_kb;
       const int n = OP == RAG_WGRAD ? 256 : (cnt + 31) / 32 * 32;
       if (kb_n == 0) {
@@ -240,8 +258,10 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         continue;
       }
       const uint32_t idesc = make_idesc(Half16<T>::kFmt, Half16<T>::kFmt, 256, n) | major;
-      const int acc = local & 1;
-      if (!wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1)) break;
+      // one tile in turn in the two accumulators, or a double tile in both
+      const int acc = MT == 2 ? 0 : local & 1;
+      const uint32_t acc_phase = (MT == 2 ? local : local >> 1) & 1;
+      if (!wait(tempty_bar(acc), acc_phase ^ 1)) break;
       tc_fence_after();
       bool ok = true;
       for (int kb = 0; kb < kb_n; ++kb) {
@@ -249,7 +269,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
           ok = false;
           break;
         }
-        const uint32_t sa = smem_base + stage * STAGE_BYTES;
+        const uint32_t sa = smem_base + stage * STEP_BYTES;
         int steps = BK / 16;
         if (OP == RAG_WGRAD && kb == kb_n - 1) {
           const int rem = cnt - kb * BK;
@@ -267,10 +287,26 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         tc_fence_after();
         const uint64_t adesc = OP != RAG_FWD ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
         const uint64_t bdesc = OP == RAG_WGRAD ? sdesc_mn_sw128(sa + A_BYTES)
-                                               : sdesc_k_sw128(sa + A_BYTES);
+                                               : sdesc_k_sw128(sa + MT * A_BYTES);
         for (int k = 0; k < steps; ++k)
           umma_f16_pair(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
                         (kb | k) != 0);
+        if (MT == 2) {
+          // the first half is complete while the second's last MMAs still run
+          if (kb == kb_n - 1) tc_commit_pair(tfull_bar(0), 0x3);
+          if (two) {
+            if (kb == 0) {
+              if (!wait(tempty_bar(1), (second & 1) ^ 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+            for (int k = 0; k < steps; ++k)
+              umma_f16_pair(tmem_base + 256, adesc + A_BYTES / 16 + a_step * k, bdesc + b_step * k,
+                            idesc, (kb | k) != 0);
+          }
+        }
         tc_commit_pair(empty_bar(stage), 0x3);
         if (kb == 0) rows_next = rows_of(t + stride);
         if (++stage == STAGES) {
@@ -279,7 +315,11 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         }
       }
       if (!ok) break;
-      tc_commit_pair(tfull_bar(acc), 0x3);
+      if (MT == 1) tc_commit_pair(tfull_bar(acc), 0x3);
+      if (two) {
+        tc_commit_pair(tfull_bar(1), 0x3);
+        ++second;
+      }
       ++local;
     }
     tc_commit_pair(drain_bar, 0x1);
@@ -300,10 +340,54 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         tail_parity ^= 1u << s;
         if (!__all_sync(0xffffffffu, wait(tail_bar(s), par))) break;
         const int rem = cnt - (kb_n - 1) * BK;
-        rag_zero_rows<4>(smem_base + s * STAGE_BYTES, rem, (rem + 15) / 16 * 16, lane);
+        rag_zero_rows<4>(smem_base + s * STEP_BYTES, rem, (rem + 15) / 16 * 16, lane);
         if (lane == 0) mbar_arrive_cluster(mapa_shared(zeroed_bar(s), 0));
       }
       stage = (stage + kb_n) % STAGES;
+    }
+  } else if (MT == 2 && warp >= 2) {
+    // ------------------------------------------------------------ epilogue, double tile
+    // Four warps an accumulator.  Both are in use until a tile's end, so each
+    // warp first reads its 32 x 256 sums as packed pairs of tokens, hands the
+    // accumulator back, and stores while the next tile's MMAs run.
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    int local = 0;
+    for (int t = first; t < total; t += stride) {
+      const RagTile D = rag_tile<32>(sched, args, t);
+      if (half == 1 && !rag_second_tile<MT>(args, D.w_tile)) continue;
+      int ok = 0;
+      if (lane == 0) ok = wait(tfull_bar(half), local & 1);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + half * 256;
+      const int w = (D.w_tile * MT + half) * 256 + rank * 128 + q * 32 + lane;
+      float bias = 0.0f;
+      if (OP == RAG_FWD && args.bias != nullptr && w < args.W)
+        bias = Half16<T>::value(static_cast<const uint16_t*>(args.bias)[(size_t)D.e * args.W + w]);
+      uint32_t pk[128];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        if (32 * c < D.rows) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(taddr + 32 * c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            pk[16 * c + j] = Half16<T>::pack(__uint_as_float(r[2 * j]) + bias,
+                                             __uint_as_float(r[2 * j + 1]) + bias);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(half), 0));
+      ++local;
+      uint16_t* out = static_cast<uint16_t*>(args.out) + D.row0 * args.ldo + w;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (32 * c < D.rows)
+          rag_store_packed32(pk + 16 * c, out + 32 * c * args.ldo, args.ldo, D.rows - 32 * c, w,
+                             args.W, lane);
     }
   } else if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
@@ -379,7 +463,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   }
 }
 
-template <int OP, typename T>
+template <int OP, typename T, int MT>
 cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB,
                       const CUtensorMap& tmC, const RagArgs& a,
                         long long tiles, cudaStream_t stream) {
@@ -389,7 +473,7 @@ cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB,
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(num_threads(OP), 1, 1);
+  cfg.blockDim = dim3(num_threads(OP, MT), 1, 1);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -397,27 +481,46 @@ cudaError_t launch_pair(const CUtensorMap& tmA, const CUtensorMap& tmB,
   static int max_pairs[kMaxDevices];
   const int dev = device_index();
   const cudaError_t es = setup.call([&] {
-    cudaError_t e = cudaFuncSetAttribute(k_ragged_2sm<OP, T>,
+    cudaError_t e = cudaFuncSetAttribute(k_ragged_2sm<OP, T, MT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(num_sms(), 1, 1);
     int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, k_ragged_2sm<OP, T>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, k_ragged_2sm<OP, T, MT>, &cfg);
     if (e != cudaSuccess) return e;
     max_pairs[dev] = n;
     return cudaSuccess;
   });
   if (es != cudaSuccess) return es;
   if (max_pairs[dev] <= 0) return cudaErrorInvalidConfiguration;
-  return launch_dependent(k_ragged_2sm<OP, T>, 2 * (unsigned)std::min<long long>(max_pairs[dev], tiles),
-                          num_threads(OP), SMEM_BYTES, stream, 2, tmA, tmB, tmC, a);
+  return launch_dependent(k_ragged_2sm<OP, T, MT>, 2 * (unsigned)std::min<long long>(max_pairs[dev], tiles),
+                          num_threads(OP, MT), SMEM_BYTES, stream, 2, tmA, tmB, tmC, a);
 }
-template <int OP>
+template <int OP, int MT>
 cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,
                       const CUtensorMap& tmC, const RagArgs& a,
                       long long tiles, cudaStream_t stream) {
-  return half ? launch_pair<OP, __half>(tmA, tmB, tmC, a, tiles, stream)
-              : launch_pair<OP, __nv_bfloat16>(tmA, tmB, tmC, a, tiles, stream);
+  return half ? launch_pair<OP, __half, MT>(tmA, tmB, tmC, a, tiles, stream)
+              : launch_pair<OP, __nv_bfloat16, MT>(tmA, tmB, tmC, a, tiles, stream);
+}
+
+// Whether forward or dgrad of R rows, E experts and W columns takes two weight
+// tiles together: a CTA then takes in 24 KB a tile and step instead of 32, which
+// counts where the pairs run at the rate L2 feeds them (or at the power limit).
+// Both accumulators are in use until a tile ends, so it costs the time to read
+// them: about 1000 cycles against 1024 a step.  1030 rows an expert, 8 experts,
+// 4096 -> 28672: 1275 -> 1193 us (dgrad in a long run: 1372 -> 1276); below 256
+// rows the weights bound it (193 rows, 32 experts, 4096 x 4096: 195 -> 209), and
+// with 16 steps nothing is won.  Not where the wider tiles fill the last round
+// of the pairs worse than that.
+bool rows_double_tiles(int R, int E, int W, int num_kb) {
+  if (ragged_form() >= 2) return ragged_form() == 3;
+  if (R < 256ll * E || num_kb < 24) return false;
+  const long long pairs = num_sms() / 2;
+  const long long tok = (long long)E * ((R / E + 255) / 256);    // token tiles of even segments
+  const long long one = (tok * ((W + 255) / 256) + pairs - 1) / pairs;
+  const long long two = (tok * ((W + 511) / 512) + pairs - 1) / pairs;
+  return 93 * 2 * two < 100 * one;
 }
 
 bool common(const RaggedProblem& p, RagArgs& a) {
@@ -449,14 +552,16 @@ cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* r
   if (!common(p, a)) return cudaErrorInvalidDevice;
   a.W = fwd ? p.N : p.K;
   a.num_kb = (red + BK - 1) / BK;
-  a.w_tiles = (a.W + 255) / 256;
+  const int mt = rows_double_tiles(p.R, p.E, a.W, a.num_kb) ? 2 : 1;
+  a.w_tiles = (a.W + 256 * mt - 1) / (256 * mt);
   a.wide_a = wide;
   a.out = out;
   a.ldo = fwd ? p.ldy : p.ldx;
   a.bias = bias;
   const long long tiles = ((long long)std::min(p.E, p.R) + p.R / 256) * a.w_tiles;   // at most
-  return fwd ? launch_op<RAG_FWD>(p.half, tmA, tmB, tmC, a, tiles, stream)
-             : launch_op<RAG_DGRAD>(p.half, tmA, tmB, tmC, a, tiles, stream);
+  const auto launch = fwd ? (mt == 2 ? launch_op<RAG_FWD, 2> : launch_op<RAG_FWD, 1>)
+                          : (mt == 2 ? launch_op<RAG_DGRAD, 2> : launch_op<RAG_DGRAD, 1>);
+  return launch(p.half, tmA, tmB, tmC, a, tiles, stream);
 }
 
 cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, const void* x,
@@ -481,7 +586,7 @@ cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, cons
   a.out = dw;
   a.out_f32 = out_f32;
   a.accumulate = accumulate;
-  return launch_op<RAG_WGRAD>(p.half, tmA, tmB, tmC, a, (long long)p.E * a.w_tiles * a.k_tiles, stream);
+  return launch_op<RAG_WGRAD, 1>(p.half, tmA, tmB, tmC, a, (long long)p.E * a.w_tiles * a.k_tiles, stream);
 }
 
 }  // namespace moe

@@ -22,9 +22,9 @@ pytestmark = pytest.mark.gpu
 DT = {"bfloat16": torch.bfloat16, "float16": torch.float16}
 
 
-@pytest.fixture(autouse=True, params=["single", "pairs"])
+@pytest.fixture(autouse=True, params=["single", "pairs", "pairs_double"])
 def form(request):
-    """Every test in both forms of the kernels."""
+    """Every test in every form of the kernels."""
     moe.moe_debug_set_bf16_gemm_form(request.param)
     yield
     moe.moe_debug_set_bf16_gemm_form("auto")
