@@ -142,7 +142,7 @@ moe_status ragged_gemm_mxfp4(const moe_ragged* p, const void* x_codes, const voi
   if (p->R == 0) return MOE_OK;
   if (!x_scales || !w_scales_packed || misaligned(x_scales, 4) || misaligned(w_scales_packed, 16))
     return MOE_ERR_INVALID_ARG;
-  const auto launch = use_pairs(p, p->N) && p->R > 128 ? launch_ragged_mxfp4_2sm : launch_ragged_mxfp4;
+  const auto launch = use_pairs(p, p->N) ? launch_ragged_mxfp4_2sm : launch_ragged_mxfp4;
   return done(launch(ragged_problem(p, expert_offsets), x_codes,
                      static_cast<const uint8_t*>(x_scales), w_codes, w_scales_packed, y,
                      workspace, static_cast<cudaStream_t>(stream)));

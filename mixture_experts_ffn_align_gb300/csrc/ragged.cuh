@@ -28,17 +28,42 @@ constexpr int kRagMaxExperts = 1024;
 // the first token tile (prefix), first row, rows and expert.
 constexpr int kRagSchedBytes = 16 + 4 * (4 * (kRagMaxExperts + 1));
 
+// Division by a launch constant: q = (n * m) >> (31 + shift), exact for
+// 0 <= n < 2^30 (an integer division takes some 100 cycles, and a tile's lookup
+// has three on the way to its first copy).
+struct FastDiv {
+  uint32_t mul, shift;
+  int d;
+};
+inline FastDiv fast_div(int d) {
+  // With 2^s <= d < 2^(s + 1) and m = ceil(2^(31 + s) / d) <= 2^31:
+  // m d = 2^(31 + s) + r with r < d <= 2^(s + 1), so n m / 2^(31 + s) exceeds
+  // n / d by n r / (d 2^(31 + s)) < 2^30 2^(s + 1) / (d 2^(31 + s)) = 1 / d.
+  FastDiv f;
+  f.d = d;
+  uint32_t s = 0;
+  while ((2ll << s) <= d) ++s;
+  f.shift = s;
+  const uint64_t one = 1ull << (31 + s);
+  f.mul = (uint32_t)((one + d - 1) / d);
+  return f;
+}
+__device__ __forceinline__ int operator/(int n, const FastDiv& f) {
+  return (int)(((uint64_t)(uint32_t)n * f.mul) >> (31 + f.shift));
+}
+
 // Everything a ragged product kernel needs beside its tensor maps.
 struct RagArgs {
   const int32_t* offsets;   // [E + 1]
   int R, E;
   int W;                    // forward, dgrad: columns of the output (N or K)
   int num_kb;               // forward, dgrad: 64-deep steps of the reduction
-  int w_tiles;              // forward, dgrad: tiles of W; wgrad: tiles of N
-  int k_tiles;              // wgrad: tiles of K
+  FastDiv w_tiles;          // forward, dgrad: tiles of W; wgrad: tiles of N
+  FastDiv k_tiles;          // wgrad: tiles of K
+  FastDiv e_tiles;          // wgrad: tiles of an expert
   int N, K;                 // wgrad: the output of one expert
   int tile_rows;            // forward, dgrad: most token rows of a tile
-  int group_max;            // token tiles (wgrad: n tiles) walked together
+  int group_max;            // token tiles walked together (forward, dgrad)
   int stages;
   int wide_a, wide_b;       // MN-major operand whose map has its chunks as a dimension
   void* out;
@@ -65,6 +90,7 @@ struct RagSched {
 // most tile_rows rows, all of the same size rounded up to G rows.
 template <int G>
 __device__ __forceinline__ int rag_rows_per_tile(int cnt, int tile_rows) {
+  if (cnt <= tile_rows) return (cnt + G - 1) / G * G;
   const int nt = (cnt + tile_rows - 1) / tile_rows;
   return ((cnt + nt - 1) / nt + G - 1) / G * G;
 }
@@ -82,15 +108,20 @@ __device__ __forceinline__ RagSched rag_sched_build(const RagArgs& a, int* mem, 
   int* row0 = tile0 + kRagMaxExperts + 1;
   int* cnt = row0 + kRagMaxExperts + 1;
   int* exp = cnt + kRagMaxExperts + 1;
-  for (int e = threadIdx.x; e <= a.E; e += blockDim.x) scratch[e] = a.offsets[e];
-  __syncthreads();
+  // up to 32 experts: straight into the scanning warp's registers
+  const bool few = a.E <= 32;
+  if (!few) {
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) scratch[e] = a.offsets[e];
+    __syncthreads();
+  }
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int nseg = 0, tiles = 0, top = 0;   // top: largest offset so far
     bool bad = false;
     for (int base = 0; base < a.E; base += 32) {
       const int e = base + lane;
-      const int b_raw = scratch[min(e, a.E)], e_raw = scratch[min(e + 1, a.E)];
+      const int32_t* off = few ? a.offsets : scratch;
+      const int b_raw = off[min(e, a.E)], e_raw = off[min(e + 1, a.E)];
       bad |= b_raw < 0 || e_raw > a.R || e_raw < b_raw;
       int mx = max(min(max(b_raw, 0), a.R), top);   // running maximum of the offsets
 #pragma unroll
@@ -101,7 +132,7 @@ __device__ __forceinline__ RagSched rag_sched_build(const RagArgs& a, int* mem, 
       const int end = max(mx, min(max(e_raw, 0), a.R));
       const int n = e < a.E ? end - mx : 0;
       const int per = n > 0 ? rag_rows_per_tile<G>(n, a.tile_rows) : 1;
-      const int nt = (n + per - 1) / per;
+      const int nt = n <= a.tile_rows ? (n > 0 ? 1 : 0) : (n + per - 1) / per;
       const unsigned has = __ballot_sync(0xffffffffu, n > 0);
       int inc = nt;
 #pragma unroll
@@ -150,19 +181,26 @@ struct RagTile {
 template <int G>
 __device__ __forceinline__ RagTile rag_tile(const RagSched& s, const RagArgs& a, int t) {
   const int q = t / a.w_tiles;
+  const int w_tiles = a.w_tiles.d;
   int lo = 0, hi = s.nseg - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (s.tile0[mid] <= q) lo = mid; else hi = mid - 1;
   }
   const int nt = s.tile0[lo + 1] - s.tile0[lo];
-  const int local = t - s.tile0[lo] * a.w_tiles;
-  const int c = local / (a.group_max * a.w_tiles);
-  const int gm = min(a.group_max, nt - c * a.group_max);
-  const int l2 = local - c * a.group_max * a.w_tiles;
+  const int local = t - s.tile0[lo] * w_tiles;
   RagTile T;
-  T.w_tile = l2 / gm;
-  const int tok = c * a.group_max + (l2 - T.w_tile * gm);
+  int tok;
+  if (nt == 1) {               // no divisions for the short segments
+    T.w_tile = local;
+    tok = 0;
+  } else {
+    const int c = nt <= a.group_max ? 0 : local / (a.group_max * w_tiles);
+    const int gm = min(a.group_max, nt - c * a.group_max);
+    const int l2 = local - c * a.group_max * w_tiles;
+    T.w_tile = l2 / gm;
+    tok = c * a.group_max + (l2 - T.w_tile * gm);
+  }
   const int per = rag_rows_per_tile<G>(s.cnt[lo], a.tile_rows);
   T.e = s.exp[lo];
   T.row0 = s.row0[lo] + tok * per;
@@ -178,21 +216,23 @@ __device__ __forceinline__ bool rag_second_tile(const RagArgs& a, int w_tile) {
 }
 
 // One tile of wgrad: expert e, rows n_tile of N and columns k_tile of K, over
-// the expert's cnt rows.  Groups of group_max n tiles, k tile by k tile, the
+// the expert's cnt rows.  Groups of 2^kRagGroupShift n tiles, k tile by k tile, the
 // group's n tiles inner.
+constexpr int kRagGroupShift = 3;
 struct RagWTile {
   int e, n_tile, k_tile;
 };
 __device__ __forceinline__ RagWTile rag_wtile(const RagArgs& a, int t) {
-  const int per = a.w_tiles * a.k_tiles;
   RagWTile T;
-  T.e = t / per;
-  const int local = t - T.e * per;
-  const int c = local / (a.group_max * a.k_tiles);
-  const int gm = min(a.group_max, a.w_tiles - c * a.group_max);
-  const int l2 = local - c * a.group_max * a.k_tiles;
-  T.k_tile = l2 / gm;
-  T.n_tile = c * a.group_max + (l2 - T.k_tile * gm);
+  T.e = t / a.e_tiles;
+  const int local = t - T.e * a.e_tiles.d;
+  // group_max is a power of two: groups of 8 n tiles x all k tiles
+  const int g = (local >> kRagGroupShift) / a.k_tiles;
+  const int n0 = g << kRagGroupShift;
+  const int gm = min(1 << kRagGroupShift, a.w_tiles.d - n0);
+  const int l2 = local - n0 * a.k_tiles.d;
+  T.k_tile = gm == 1 << kRagGroupShift ? l2 >> kRagGroupShift : l2 / gm;
+  T.n_tile = n0 + (l2 - T.k_tile * gm);
   return T;
 }
 
@@ -397,7 +437,7 @@ __device__ __forceinline__ void tma_store_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// wgrad epilogue of one warp: its 32 accumulator rows (one a lane) x 256
+// wgrad epilogue of one warp: its 32 accumulator rows (one a lane) x SPAN
 // columns from taddr to rows n0 .. n0 + 31 and columns from k0 of dw[e].  Each
 // lane packs 128 bytes of its row (64 16-bit or 32 fp32 values) into a swizzled
 // box of shared memory, which goes out as one TMA store: whole 128-byte lines,
@@ -406,13 +446,17 @@ __device__ __forceinline__ void tma_store_wait_all() {
 // boxes of 4 KB used in turn, `turn` counting them.  fp32 sums are added to dw
 // by the store; 16-bit ones here, so that they are rounded once.
 // release() is called by the whole warp when the accumulator has been read.
-template <typename T, int BUFS, class Release>
+template <typename T, int BUFS, int SPAN, class Release>
 __device__ __forceinline__ void rag_wgrad_epilogue(const RagArgs& a, const CUtensorMap* tmD,
                                                    uint32_t buf, int& turn, uint32_t taddr,
                                                    bool empty, int e, int n0, int k0, int lane,
                                                    Release&& release) {
   const int cols = a.out_f32 ? 32 : 64;
-  const int width = min(256, a.K - k0);
+  const int width = min(SPAN, a.K - k0);
+  if (width <= 0) {
+    release();
+    return;
+  }
   const bool add16 = a.accumulate && !a.out_f32;
 #pragma unroll 1
   for (int c = 0; c < width; c += cols) {

@@ -9,11 +9,11 @@
 //    decode step (a few rows an expert) moves little beside the weights;
 //  * warp 1 lane 0: tcgen05.mma (M = 128, N = the tile's rows rounded up to 16,
 //    K = 16) into one of two 256-column accumulators;
-//  * warps 2-5: epilogue from the other accumulator.
+//  * warps 2-5 (wgrad 2-9): epilogue from the other accumulator.
 //  * dgrad reads w[e] with the reduction along its rows: the same boxes in the
 //    MMA's MN-major form, so no transposed copy of the weights exists.
 //  * wgrad reduces over an expert's rows, both operands MN-major.  Its last
-//    step may end inside the 16 rows of an instruction: a seventh
+//    step may end inside the 16 rows of an instruction: a further
 //    warp then writes zeros over the rows behind the segment in both operands
 //    (in one alone, an infinity or NaN of the next expert's rows would enter the
 //    sums as 0 x inf).
@@ -45,16 +45,17 @@ namespace {
 constexpr int BK = 64, MAX_STAGES = 9;
 constexpr int A_BYTES = 128 * BK * 2;
 constexpr int RING_BYTES = 196608, BAR_BYTES = 384;
-constexpr int EPI_WARPS = 4;
+// Epilogue warps: one for each quadrant of the accumulator's rows, wgrad two (of
+// 128 columns each).
+constexpr int epi_warps(int op) { return op == RAG_WGRAD ? 8 : 4; }
 // producer, MMA, epilogue warps; wgrad has one more, which zeroes
-constexpr int num_threads(int op) { return 64 + 32 * EPI_WARPS + (op == RAG_WGRAD ? 32 : 0); }
+constexpr int num_threads(int op) { return 64 + 32 * epi_warps(op) + (op == RAG_WGRAD ? 32 : 0); }
 constexpr int TMEM_COLS = 512;
-// wgrad: three stages and four store boxes for each epilogue warp, a tile's
-// output, in the ring's space and 16 KB more.  (Four stages and one box a warp:
-// 12.4 instead of 11.9 us for 515 rows, 16 experts, 1032 x 776.)
-constexpr int W_STAGES = 3, BOXES = 4;
+// wgrad: three stages and two store boxes for each epilogue warp, a tile's
+// output, in the ring's space and 16 KB more.
+constexpr int W_STAGES = 3, BOXES = 2;
 constexpr int W_STAGE_BYTES = A_BYTES + 256 * BK * 2;
-constexpr int OPERAND_BYTES = W_STAGES * W_STAGE_BYTES + EPI_WARPS * BOXES * 4096;
+constexpr int OPERAND_BYTES = W_STAGES * W_STAGE_BYTES + epi_warps(RAG_WGRAD) * BOXES * 4096;
 static_assert(OPERAND_BYTES >= RING_BYTES, "operand space");
 constexpr int SMEM_BYTES = OPERAND_BYTES + 1024 + BAR_BYTES + kRagSchedBytes;
 static_assert(SMEM_BYTES <= 232448, "shared memory");
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), EPI_WARPS);
+      mbar_init(tempty_bar(a), epi_warps(OP));
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -120,8 +121,8 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   const int2* s_rows = OP == RAG_WGRAD
                            ? rag_rows_by_expert(sched, args.E, s_sched, reinterpret_cast<int2*>(smem))
                            : nullptr;
-  const int total = OP == RAG_WGRAD ? args.E * args.w_tiles * args.k_tiles
-                                    : sched.tile0[sched.nseg] * args.w_tiles;
+  const int total = OP == RAG_WGRAD ? args.E * args.e_tiles.d
+                                    : sched.tile0[sched.nseg] * args.w_tiles.d;
   const int stages = args.stages;
   // the CTAs of a cluster share a tile (splits > 1: one tile each cluster)
   const int splits = OP == RAG_WGRAD ? 1 : args.splits;
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     }
     tc_commit(drain_bar);
     mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
-  } else if (OP == RAG_WGRAD && warp == 2 + EPI_WARPS) {
+  } else if (OP == RAG_WGRAD && warp == 2 + epi_warps(OP)) {
     // ------------------------------------------------------------ zeroing warp
     int stage = 0;
     uint32_t tail_parity = 0;
@@ -335,8 +336,11 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         ++local;
       };
       if (OP == RAG_WGRAD) {
-        rag_wgrad_epilogue<T, BOXES>(args, &tmD, box_base + (warp - 2) * BOXES * 4096, turn, taddr,
-                                     empty, V.e, V.n_tile * 128 + q * 32, V.k_tile * 256, lane, release);
+        const int half = (warp - 2) >> 2;
+        rag_wgrad_epilogue<T, BOXES, 128>(args, &tmD, box_base + (warp - 2) * BOXES * 4096, turn,
+                                          taddr + half * 128, empty, V.e,
+                                          V.n_tile * 128 + q * 32, V.k_tile * 256 + half * 128,
+                                          lane, release);
       } else {
         const int w = D.w_tile * 128 + q * 32 + lane;
         float bias = 0.0f;
@@ -484,7 +488,7 @@ cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows,
   a.num_kb = (red + BK - 1) / BK;
   const RowsPlan r = rows_plan(p.R, p.E, a.W, red);
   a.tile_rows = r.tile_rows;
-  a.w_tiles = r.w_tiles;
+  a.w_tiles = fast_div(r.w_tiles);
   a.splits = r.splits;
   a.part = static_cast<float*>(workspace);
   a.stages = std::min(MAX_STAGES, RING_BYTES / (A_BYTES + a.tile_rows * BK * 2));
@@ -518,11 +522,11 @@ cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const vo
   a.E = p.E;
   a.N = p.N;
   a.K = p.K;
-  a.w_tiles = (p.N + 127) / 128;
-  a.k_tiles = (p.K + 255) / 256;
+  a.w_tiles = fast_div((p.N + 127) / 128);
+  a.k_tiles = fast_div((p.K + 255) / 256);
+  a.e_tiles = fast_div(a.w_tiles.d * a.k_tiles.d);
   a.tile_rows = 256;
   a.stages = W_STAGES;
-  a.group_max = 8;
   a.wide_a = wide_a;
   a.wide_b = wide_b;
   a.out = dw;
@@ -531,7 +535,7 @@ cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const vo
   watchdog_params(&a.limit_ns, &a.never_arrive);
   a.err = dev_error_word();
   if (a.err == nullptr) return cudaErrorInvalidDevice;
-  const long long tiles = (long long)p.E * a.w_tiles * a.k_tiles;
+  const long long tiles = (long long)p.E * a.e_tiles.d;
   const int grid = (int)std::min<long long>(num_sms(), tiles);
   return launch_op<RAG_WGRAD>(p.half, tmA, tmB, tmD, a, grid, stream);
 }

@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
   const int2* s_rows = OP == RAG_WGRAD
                            ? rag_rows_by_expert(sched, args.E, s_sched, reinterpret_cast<int2*>(smem))
                            : nullptr;
-  const int total = OP == RAG_WGRAD ? args.E * args.w_tiles * args.k_tiles
-                                    : sched.tile0[sched.nseg] * args.w_tiles;
+  const int total = OP == RAG_WGRAD ? args.E * args.e_tiles.d
+                                    : sched.tile0[sched.nseg] * args.w_tiles.d;
 
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
     return mbar_wait_bounded(bar, parity, abort_flag, args.limit_ns, args.err);
@@ -423,8 +423,9 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
         ++local;
       };
       if (OP == RAG_WGRAD) {
-        rag_wgrad_epilogue<T, BOXES>(args, &tmC, box_base + (warp - 2) * BOXES * 4096, turn, taddr,
-                                     empty, V.e, V.n_tile * 256 + rank * 128 + q * 32, V.k_tile * 256, lane, release);
+        rag_wgrad_epilogue<T, BOXES, 256>(args, &tmC, box_base + (warp - 2) * BOXES * 4096, turn,
+                                          taddr, empty, V.e, V.n_tile * 256 + rank * 128 + q * 32,
+                                          V.k_tile * 256, lane, release);
       } else {
         const int w = D.w_tile * 256 + rank * 128 + q * 32 + lane;
         float bias = 0.0f;
@@ -553,12 +554,12 @@ cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* r
   a.W = fwd ? p.N : p.K;
   a.num_kb = (red + BK - 1) / BK;
   const int mt = rows_double_tiles(p.R, p.E, a.W, a.num_kb) ? 2 : 1;
-  a.w_tiles = (a.W + 256 * mt - 1) / (256 * mt);
+  a.w_tiles = fast_div((a.W + 256 * mt - 1) / (256 * mt));
   a.wide_a = wide;
   a.out = out;
   a.ldo = fwd ? p.ldy : p.ldx;
   a.bias = bias;
-  const long long tiles = ((long long)std::min(p.E, p.R) + p.R / 256) * a.w_tiles;   // at most
+  const long long tiles = ((long long)std::min(p.E, p.R) + p.R / 256) * a.w_tiles.d;   // at most
   const auto launch = fwd ? (mt == 2 ? launch_op<RAG_FWD, 2> : launch_op<RAG_FWD, 1>)
                           : (mt == 2 ? launch_op<RAG_DGRAD, 2> : launch_op<RAG_DGRAD, 1>);
   return launch(p.half, tmA, tmB, tmC, a, tiles, stream);
@@ -579,14 +580,15 @@ cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, cons
   if (!common(p, a)) return cudaErrorInvalidDevice;
   a.N = p.N;
   a.K = p.K;
-  a.w_tiles = (p.N + 255) / 256;
-  a.k_tiles = (p.K + 255) / 256;
+  a.w_tiles = fast_div((p.N + 255) / 256);
+  a.k_tiles = fast_div((p.K + 255) / 256);
+  a.e_tiles = fast_div(a.w_tiles.d * a.k_tiles.d);
   a.wide_a = wide_a;
   a.wide_b = wide_b;
   a.out = dw;
   a.out_f32 = out_f32;
   a.accumulate = accumulate;
-  return launch_op<RAG_WGRAD, 1>(p.half, tmA, tmB, tmC, a, (long long)p.E * a.w_tiles * a.k_tiles, stream);
+  return launch_op<RAG_WGRAD, 1>(p.half, tmA, tmB, tmC, a, (long long)p.E * a.e_tiles.d, stream);
 }
 
 }  // namespace moe

@@ -28,6 +28,8 @@ constexpr uint32_t kFmtMxf4 = 1;
 template <int G>
 cudaError_t launch_pack_token_scales(const Mx44Args& a, long long most_tiles, cudaStream_t stream);
 
+int ragged_mxfp4_tile_rows(int R, int E);
+
 // Token tiles at most, whatever the segments.
 inline long long most_token_tiles(int R, int E, int tile_rows) {
   return (long long)(E < R ? E : R) + R / tile_rows;

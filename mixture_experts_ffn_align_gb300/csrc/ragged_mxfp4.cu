@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   griddep_wait();
   const RagSched sched = rag_sched_build<16>(args, s_sched, reinterpret_cast<int*>(smem));
-  const int total = sched.tile0[sched.nseg] * args.w_tiles;
+  const int total = sched.tile0[sched.nseg] * args.w_tiles.d;
   const int groups = tile_groups(args.tile_rows);
   const int kb128 = margs.K / 128;
   // accumulators: two of 128 columns when tiles are no wider, else one of 256
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const RagTile T = rag_tile<16>(sched, args, t);
       const int boxes = (T.rows + 31) / 32;
       const uint8_t* wsc = margs.w_packed +
-                           ((size_t)T.e * kb128 * args.w_tiles + T.w_tile) * 512;
+                           ((size_t)T.e * kb128 * args.w_tiles.d + T.w_tile) * 512;
       const uint8_t* xsc = margs.x_packed + T.tok * tile_scale_bytes(args.tile_rows, margs.K);
       bool ok = true;
       for (int kb = 0; kb < args.num_kb; ++kb) {
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint32_t slot = slot_base + stage * SLOT_BYTES;
           mbar_arrive_expect_tx(sfull_bar(stage), words * 512 * (1 + groups));
           for (int j = 0; j < words; ++j)
-            bulk_load(slot + 512 * j, wsc + (size_t)(2 * kb + j) * args.w_tiles * 512, 512,
+            bulk_load(slot + 512 * j, wsc + (size_t)(2 * kb + j) * args.w_tiles.d * 512, 512,
                       sfull_bar(stage));
           bulk_load(slot + 1024, xsc + (size_t)(2 * kb) * groups * 512, words * groups * 512,
                     sfull_bar(stage));
@@ -329,22 +329,25 @@ cudaError_t launch_mx(const CUtensorMap& tmA, const CUtensorMap& tmB, const Mx44
   return launch_dependent(k_ragged_mxfp4<T>, grid, NUM_THREADS, SMEM_BYTES, stream, 1, tmA, tmB, a);
 }
 
-int mx_tile_rows(int R) { return R <= 128 ? 128 : 256; }
-
 }  // namespace
+
+// Rows of the token tiles: at 128 and below two accumulators fit beside the
+// scales' places, and a tile's end is hidden; long segments take wide tiles,
+// which read the weights less often.
+int ragged_mxfp4_tile_rows(int R, int E) { return R <= 64ll * E || R <= 128 ? 128 : 256; }
 
 template <int G>
 cudaError_t launch_pack_token_scales(const Mx44Args& args, long long most_tiles,
                                      cudaStream_t stream) {
   Mx44Args a = args;
-  a.r.w_tiles = 1;          // tile numbers are token tiles
+  a.r.w_tiles = fast_div(1);          // tile numbers are token tiles
   return launch_dependent(k_pack_token_scales<G>, (unsigned)std::min<long long>(most_tiles, 4 * num_sms()),
                           256, 0, stream, 1, a);
 }
 template cudaError_t launch_pack_token_scales<32>(const Mx44Args&, long long, cudaStream_t);
 
 size_t ragged_mxfp4_scale_bytes(int R, int K, int E) {
-  const int tr = mx_tile_rows(R);     // both forms' tiles
+  const int tr = ragged_mxfp4_tile_rows(R, E);
   return (size_t)most_token_tiles(R, E, tr) * tile_scale_bytes(tr, K);
 }
 
@@ -361,7 +364,7 @@ cudaError_t launch_ragged_mxfp4(const RaggedProblem& p, const void* xq, const ui
   a.r.E = p.E;
   a.r.W = p.N;
   a.r.num_kb = (p.K + BK - 1) / BK;
-  a.r.tile_rows = mx_tile_rows(p.R);
+  a.r.tile_rows = ragged_mxfp4_tile_rows(p.R, p.E);
   a.r.group_max = 8;
   a.r.out = y;
   a.r.ldo = p.ldy;
@@ -375,8 +378,8 @@ cudaError_t launch_ragged_mxfp4(const RaggedProblem& p, const void* xq, const ui
   const long long tok = most_token_tiles(p.R, p.E, a.r.tile_rows);
   const cudaError_t e = launch_pack_token_scales<16>(a, tok, stream);
   if (e != cudaSuccess) return e;
-  a.r.w_tiles = p.N / 128;
-  const int grid = (int)std::min<long long>(num_sms(), tok * a.r.w_tiles);
+  a.r.w_tiles = fast_div(p.N / 128);
+  const int grid = (int)std::min<long long>(num_sms(), tok * a.r.w_tiles.d);
   return p.half ? launch_mx<__half>(tmA, tmB, a, grid, stream)
                 : launch_mx<__nv_bfloat16>(tmA, tmB, a, grid, stream);
 }

@@ -10,7 +10,9 @@
 //    the tile's tokens; the leader's tcgen05.cp.cta_group::2 copies each CTA's
 //    slot into its own tensor memory.  The scales come by tensor copies (blocks
 //    of 128 words), whose completion may count on the leader's barrier.
-//  * one accumulator of 256 columns, beside it the four slots' places: eight
+//  * short segments (on average at most 64 rows): tiles of up to 128 tokens in
+//    two accumulators in turn.
+//  * else one accumulator of 256 columns, beside it the four slots' places: eight
 //    epilogue warps first read it whole, as packed 16-bit pairs, hand it back,
 //    and store while the next tile's MMAs run.
 //  * fixed tile order, bounded waits and teardown as in ragged_gemm_2sm.cu.
@@ -68,11 +70,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const RagArgs& args = margs.r;
   uint8_t* slots = smem + STAGES * STAGE_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(slots + STAGES * SLOT_BYTES);
-  // full[S], empty[S], sfull[S], sready[S], tfull, tempty, drain, cdrain
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 4 * STAGES + 4);
+  // full[S], empty[S], sfull[S], sready[S], tfull[2], tempty[2], drain, cdrain
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 4 * STAGES + 6);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_sched = reinterpret_cast<int*>(slots + STAGES * SLOT_BYTES + 256);
-  static_assert(8 * (4 * STAGES + 4) + 8 <= 256, "barrier area");
+  static_assert(8 * (4 * STAGES + 6) + 8 <= 256, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -83,16 +85,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
   auto sfull_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + s); };
   auto sready_bar = [&](int s) { return bar_base + 8u * (3 * STAGES + s); };
-  const uint32_t tfull_bar = bar_base + 8u * (4 * STAGES);
-  const uint32_t tempty_bar = bar_base + 8u * (4 * STAGES + 1);
-  const uint32_t drain_bar = bar_base + 8u * (4 * STAGES + 2);
-  const uint32_t cdrain_bar = bar_base + 8u * (4 * STAGES + 3);
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (4 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar_base + 8u * (4 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar_base + 8u * (4 * STAGES + 4);
+  const uint32_t cdrain_bar = bar_base + 8u * (4 * STAGES + 5);
 
   griddep_launch();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 4 * STAGES; ++s) mbar_init(bar_base + 8u * s, 1);
-    mbar_init(tfull_bar, 1);
-    mbar_init(tempty_bar, 2 * EPI_WARPS);   // both CTAs' (leader's is used)
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * EPI_WARPS);   // both CTAs' (leader's is used)
+    }
     mbar_init(drain_bar, 1);
     mbar_init(cdrain_bar, 1);
     *abort_flag = 0;
@@ -117,8 +121,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   griddep_wait();
   const RagSched sched = rag_sched_build<32>(args, s_sched, reinterpret_cast<int*>(smem));
-  const int total = sched.tile0[sched.nseg] * args.w_tiles;
+  const int total = sched.tile0[sched.nseg] * args.w_tiles.d;
   const int kb128 = margs.K / 128;
+  const int groups = tile_groups(args.tile_rows);
+  // accumulators: two of 128 columns when tiles are no wider, else one of 256
+  const bool twin = groups == 1;
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;   // this pair's tiles
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
     return mbar_wait_bounded(bar, parity, abort_flag, args.limit_ns, args.err);
@@ -151,14 +158,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint32_t sbar = mapa_shared(sfull_bar(stage), 0);
           const uint32_t bar = mapa_shared(full_bar(stage), 0);
           if (leader) {
-            mbar_arrive_expect_tx(sfull_bar(stage), 2 * SLOT_BYTES);
+            mbar_arrive_expect_tx(sfull_bar(stage), 2 * (1024 + 1024 * groups));
             mbar_arrive_expect_tx(full_bar(stage), 2 * (A_BYTES + b_bytes));
             issued_mask |= 1u << stage;
             issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           }
           // the second word of a last step of 128 is not used
           tma_load_3d_pair(slot, &tmSA, sbar, 0, w0 / 128, D.e * kb128 + 2 * kb, pol_w);
-          tma_load_2d_pair(slot + 1024, &tmSB, sbar, 0, (D.tok * kb128 + 2 * kb) * 2, pol_t);
+          tma_load_2d_pair(slot + 1024, &tmSB, sbar, 0, (D.tok * kb128 + 2 * kb) * groups, pol_t);
           tma_load_3d_pair(sa, &tmA, bar, kb * (BK / 2), w0, D.e, pol_w);
           const uint32_t sb = sa + A_BYTES;
           if (b_bytes == B_BYTES) {
@@ -201,8 +208,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           tmem_cp_pair_32x128b_x4(dst + 16 * j, sdesc_rows16(src + 512 * j));
-          tmem_cp_pair_32x128b_x4(dst + 32 + 16 * j, sdesc_rows16(src + 1024 * (1 + j)));
-          tmem_cp_pair_32x128b_x4(dst + 36 + 16 * j, sdesc_rows16(src + 1024 * (1 + j) + 512));
+          tmem_cp_pair_32x128b_x4(dst + 32 + 16 * j, sdesc_rows16(src + 1024 + 512 * groups * j));
+          if (!twin)
+            tmem_cp_pair_32x128b_x4(dst + 36 + 16 * j, sdesc_rows16(src + 1536 + 1024 * j));
         }
         tc_commit_pair(sready_bar(stage), 0x1);
         if (++stage == STAGES) {
@@ -223,7 +231,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int n = (rag_tile<32>(sched, args, t).rows + 31) / 32 * 32;
       const uint32_t id0 = make_idesc_block_scaled(kFmtMxf4, kFmtMxf4, 256, n, 0);
       const uint32_t id2 = make_idesc_block_scaled(kFmtMxf4, kFmtMxf4, 256, n, 2);
-      if (!wait(tempty_bar, (local & 1) ^ 1)) break;
+      const int acc = twin ? local & 1 : 0;
+      const uint32_t d_tmem = tmem_base + 128 * acc;
+      if (!wait(tempty_bar(acc), ((twin ? local >> 1 : local) & 1) ^ 1)) break;
       tc_fence_after();
       for (int kb = 0; kb < args.num_kb; ++kb) {
         if (!wait(full_bar(stage), phase) || !wait(sready_bar(stage), phase)) {
@@ -236,9 +246,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t sf = tmem_base + SF_COL0 + SF_SLOT * stage;
         const int words = min(2, kb128 - 2 * kb);
         for (int j = 0; j < words; ++j) {
-          umma_mxf4_pair(tmem_base, adesc + 4 * j, bdesc + 4 * j, id0, sf + 16 * j,
+          umma_mxf4_pair(d_tmem, adesc + 4 * j, bdesc + 4 * j, id0, sf + 16 * j,
                          sf + 32 + 16 * j, (kb | j) != 0);
-          umma_mxf4_pair(tmem_base, adesc + 4 * j + 2, bdesc + 4 * j + 2, id2, sf + 16 * j,
+          umma_mxf4_pair(d_tmem, adesc + 4 * j + 2, bdesc + 4 * j + 2, id2, sf + 16 * j,
                          sf + 32 + 16 * j, 1);
         }
         tc_commit_pair(empty_bar(stage), 0x3);
@@ -248,7 +258,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       if (!ok) break;
-      tc_commit_pair(tfull_bar, 0x3);
+      tc_commit_pair(tfull_bar(acc), 0x3);
       ++local;
     }
     tc_commit_pair(drain_bar, 0x1);
@@ -260,11 +270,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int t = first; t < total; t += stride) {
       const RagTile D = rag_tile<32>(sched, args, t);
       int ok = 0;
-      if (lane == 0) ok = wait(tfull_bar, local & 1);
+      const int acc = twin ? local & 1 : 0;
+      if (lane == 0) ok = wait(tfull_bar(acc), (twin ? local >> 1 : local) & 1);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + half * 128;
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (half + acc) * 128;
       const int live = D.rows - half * 128;
       uint32_t pk[64];
 #pragma unroll
@@ -280,7 +291,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar, 0));
+      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(acc), 0));
       ++local;
       const int w = D.w_tile * 256 + rank * 128 + q * 32 + lane;
       uint16_t* out = static_cast<uint16_t*>(args.out) + (D.row0 + half * 128) * args.ldo + w;
@@ -347,14 +358,17 @@ cudaError_t launch_mx_pair(const CUtensorMap (&tm)[5], const Mx44Args& a, long l
 cudaError_t launch_ragged_mxfp4_2sm(const RaggedProblem& p, const void* xq, const uint8_t* x_scale,
                                     const void* wq, const void* w_scale_packed, void* y,
                                     void* workspace, cudaStream_t stream) {
-  const long long tok = most_token_tiles(p.R, p.E, 256);
+  const int tile_rows = ragged_mxfp4_tile_rows(p.R, p.E);
+  const int groups = tile_groups(tile_rows);
+  const long long tok = most_token_tiles(p.R, p.E, tile_rows);
   CUtensorMap tm[5];
   if (!make_tmap_rag_fp4(&tm[0], wq, 3, p.K, p.N, p.E, 128) ||
       !make_tmap_rag_fp4(&tm[1], xq, 2, p.K, p.R, 0, 128) ||
       !make_tmap_rag_fp4(&tm[4], xq, 2, p.K, p.R, 0, 32) ||
       !make_tmap_scale_blocks(&tm[2], w_scale_packed, 3, p.N / 128, (uint64_t)p.E * (p.K / 128), 1,
                               2) ||
-      !make_tmap_scale_blocks(&tm[3], workspace, 2, (uint64_t)tok * (p.K / 128) * 2, 0, 4, 1))
+      !make_tmap_scale_blocks(&tm[3], workspace, 2, (uint64_t)tok * (p.K / 128) * groups, 0,
+                              2 * groups, 1))
     return cudaErrorInvalidValue;
   Mx44Args a{};
   a.r.offsets = p.offsets;
@@ -362,7 +376,7 @@ cudaError_t launch_ragged_mxfp4_2sm(const RaggedProblem& p, const void* xq, cons
   a.r.E = p.E;
   a.r.W = p.N;
   a.r.num_kb = (p.K + BK - 1) / BK;
-  a.r.tile_rows = 256;
+  a.r.tile_rows = tile_rows;
   a.r.group_max = 8;
   a.r.out = y;
   a.r.ldo = p.ldy;
@@ -374,9 +388,9 @@ cudaError_t launch_ragged_mxfp4_2sm(const RaggedProblem& p, const void* xq, cons
   a.K = p.K;
   const cudaError_t e = launch_pack_token_scales<32>(a, tok, stream);
   if (e != cudaSuccess) return e;
-  a.r.w_tiles = (p.N + 255) / 256;
-  return p.half ? launch_mx_pair<__half>(tm, a, tok * a.r.w_tiles, stream)
-                : launch_mx_pair<__nv_bfloat16>(tm, a, tok * a.r.w_tiles, stream);
+  a.r.w_tiles = fast_div((p.N + 255) / 256);
+  return p.half ? launch_mx_pair<__half>(tm, a, tok * a.r.w_tiles.d, stream)
+                : launch_mx_pair<__nv_bfloat16>(tm, a, tok * a.r.w_tiles.d, stream);
 }
 
 }  // namespace moe
