@@ -46,8 +46,9 @@ RaggedProblem ragged_problem(const moe_ragged* p, const int32_t* offsets) {
 bool mxfp4_shape(const moe_ragged* p) { return p->N % 128 == 0 && p->K % 128 == 0; }
 
 size_t ragged_bytes(const moe_ragged* p) {
-  size_t b = std::max<size_t>(1, std::max(ragged_split_bytes(p->R, p->E, p->N, p->K),
-                                          ragged_split_bytes(p->R, p->E, p->K, p->N)));
+  size_t b = std::max({(size_t)1, ragged_split_bytes(p->R, p->E, p->N, p->K),
+                       ragged_split_bytes(p->R, p->E, p->K, p->N),
+                       ragged_wgrad_bytes(p->R, p->N, p->K, p->E)});
   if (mxfp4_shape(p)) b = std::max(b, ragged_mxfp4_scale_bytes(p->R, p->K, p->E));
   return pad256(b);
 }
@@ -58,6 +59,14 @@ bool use_pairs(const moe_ragged* p, int width) {
   const int form = ragged_form();
   const int64_t tiles = ((int64_t)std::min(p->E, p->R) + p->R / 256) * ((width + 255) / 256);
   return form >= 2 || (form == 0 && tiles >= num_sms());
+}
+
+// wgrad on SM pairs from segments of about 192 rows up: 16 experts, 4096 x 4096,
+// one SM / pairs: 130 rows each 119 / 125 us, 257 rows 192 / 158 us.
+bool wgrad_pairs(const moe_ragged* p) {
+  const int form = ragged_form();
+  const int64_t tiles = (int64_t)p->E * ((p->N + 255) / 256) * ((p->K + 255) / 256);
+  return form >= 2 || (form == 0 && p->R >= 192ll * p->E && 2 * tiles >= num_sms());
 }
 
 cudaError_t ragged_rows(const moe_ragged* p, int op, const void* rows, const void* w,
@@ -127,8 +136,8 @@ moe_status ragged_gemm_wgrad(const moe_ragged* p, const void* dy, const void* x,
   }
   const RaggedProblem q = ragged_problem(p, expert_offsets);
   const bool f32 = dw_dtype == MOE_T_FP32;
-  return done(use_pairs(p, p->N) ? launch_ragged_wgrad_2sm(q, dy, x, dw, f32, accumulate != 0, st)
-                           : launch_ragged_wgrad(q, dy, x, dw, f32, accumulate != 0, st));
+  return done(wgrad_pairs(p) ? launch_ragged_wgrad_2sm(q, dy, x, dw, f32, accumulate != 0, st)
+                             : launch_ragged_wgrad(q, dy, x, dw, f32, accumulate != 0, workspace, st));
 }
 
 moe_status ragged_gemm_mxfp4(const moe_ragged* p, const void* x_codes, const void* x_scales,

@@ -215,8 +215,10 @@ cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows,
 // Workspace of launch_ragged_rows for an output of `width` columns and a
 // reduction of `red`.
 size_t ragged_split_bytes(int R, int E, int width, int red);
+size_t ragged_wgrad_bytes(int R, int N, int K, int E);
 cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const void* x, void* dw,
-                                bool out_f32, bool accumulate, cudaStream_t stream);
+                                bool out_f32, bool accumulate, void* workspace,
+                                cudaStream_t stream);
 // The same on SM pairs.
 cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* rows, const void* w,
                                    const void* bias, void* out,

@@ -71,8 +71,8 @@ struct RagArgs {
   const void* bias;         // forward: [E, N] in the operands' type, or null
   int out_f32;              // wgrad: dw is fp32
   int accumulate;           // wgrad: dw += instead of dw =
-  int splits;               // forward, dgrad on one SM: CTAs (a cluster) that share a tile's
-  float* part;              //   reduction, and their sums [tiles, splits, tile_rows, 128]
+  int splits;               // one SM: CTAs (a cluster) that share a tile's reduction, and
+  float* part;              //   their sums [tiles, splits, tile_rows, 128] (wgrad: 128, 256)
   uint64_t limit_ns;
   int never_arrive;
   int* err;

@@ -17,11 +17,11 @@
 //    warp then writes zeros over the rows behind the segment in both operands
 //    (in one alone, an infinity or NaN of the next expert's rows would enter the
 //    sums as 0 x inf).
-//  * forward and dgrad with fewer tiles than half the SMs (few experts, narrow
-//    outputs): a cluster of 2, 4 or 8 CTAs takes one tile, each a slice of the
-//    reduction; the fp32 sums go to the workspace (they stay in L2), and after a
-//    cluster barrier each CTA adds and rounds its share of the tile's tokens, in
-//    the order of the slices.
+//  * fewer tiles than half the SMs (few experts, narrow outputs): a cluster of
+//    2, 4 or 8 CTAs takes one tile, each a slice of the reduction; the fp32 sums
+//    go to the workspace (they stay in L2), and after a cluster barrier each CTA
+//    adds and rounds its share of the tile's tokens (wgrad: rows), in the order
+//    of the slices.
 //  * every wait is bounded (wall clock); on a timeout the kernel records the
 //    error, drains its own copies and MMAs, frees tensor memory and returns.
 #include <algorithm>
@@ -125,10 +125,13 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
                                     : sched.tile0[sched.nseg] * args.w_tiles.d;
   const int stages = args.stages;
   // the CTAs of a cluster share a tile (splits > 1: one tile each cluster)
-  const int splits = OP == RAG_WGRAD ? 1 : args.splits;
+  const int splits = args.splits;
   const int rank = splits > 1 ? (int)cluster_ctarank() : 0;
   const int first = blockIdx.x / splits, stride = gridDim.x / splits;
-  const int kb0 = args.num_kb * rank / splits, kb1 = args.num_kb * (rank + 1) / splits;
+  // this CTA's steps [kb0, kb1) of a reduction of n
+  auto slice0 = [&](int n) { return n * rank / splits; };
+  auto slice1 = [&](int n) { return n * (rank + 1) / splits; };
+  const int kb0 = slice0(args.num_kb), kb1 = slice1(args.num_kb);
   const int stage_bytes = A_BYTES + (OP == RAG_WGRAD ? 256 : args.tile_rows) * BK * 2;
 
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -145,11 +148,13 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     for (int t = first; t < total; t += stride) {
       RagTile D{};
       RagWTile V{};
-      int kb_n = kb1 - kb0, boxes = 4, row0 = 0;
+      int kb_n = kb1 - kb0, boxes = 4, row0 = 0, tail_kb = -1;
       if (OP == RAG_WGRAD) {
         V = rag_wtile(args, t);
-        kb_n = (s_rows[V.e].y + BK - 1) / BK;
-        row0 = s_rows[V.e].x;
+        const int cnt = s_rows[V.e].y, n = (cnt + BK - 1) / BK;
+        kb_n = slice1(n) - slice0(n);
+        row0 = s_rows[V.e].x + slice0(n) * BK;
+        if (cnt % 16 && slice1(n) == n) tail_kb = kb_n - 1;
       } else {
         D = rag_tile<16>(sched, args, t);
         boxes = (D.rows + 31) / 32;
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
           const uint32_t sa = smem_base + stage * stage_bytes, sb = sa + A_BYTES;
           uint32_t bar = full_bar(stage);
           if (OP == RAG_WGRAD) {
-            if (kb == kb_n - 1 && s_rows[V.e].y % 16) {
+            if (kb == tail_kb) {
               // copies of a step to be zeroed behind: counted on their own barrier
               mbar_arrive(bar);
               bar = tail_bar(stage);
@@ -234,7 +239,8 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     int rows_next = rows_of(first);
     for (int t = first; t < total; t += stride) {
       const int cnt = rows_next;
-      const int kb_n = OP == RAG_WGRAD ? (cnt + BK - 1) / BK : kb1 - kb0;
+      const int all = (cnt + BK - 1) / BK;      // wgrad: steps of all slices
+      const int kb_n = OP == RAG_WGRAD ? slice1(all) - slice0(all) : kb1 - kb0;
       const int n = OP == RAG_WGRAD ? 256 : (cnt + 15) / 16 * 16;
       if (kb_n == 0) {
         rows_next = rows_of(t + stride);
@@ -251,8 +257,8 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
           break;
         }
         int steps = BK / 16;
-        if (OP == RAG_WGRAD && kb == kb_n - 1) {
-          const int rem = cnt - kb * BK;
+        if (OP == RAG_WGRAD && slice0(all) + kb == all - 1) {
+          const int rem = cnt - (all - 1) * BK;
           steps = (rem + 15) / 16;
           if (rem % 16) {               // the rows behind the segment are zeros
             const uint32_t par = (tail_parity >> stage) & 1;
@@ -289,14 +295,14 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     int stage = 0;
     uint32_t tail_parity = 0;
     for (int t = first; t < total; t += stride) {
-      const int cnt = s_rows[rag_wtile(args, t).e].y;
-      const int kb_n = (cnt + BK - 1) / BK;
-      if (cnt % 16) {
+      const int cnt = s_rows[rag_wtile(args, t).e].y, n = (cnt + BK - 1) / BK;
+      const int kb_n = slice1(n) - slice0(n);
+      if (cnt % 16 && kb_n > 0 && slice1(n) == n) {
         const int s = (stage + kb_n - 1) % stages;      // stage of the last step
         const uint32_t par = (tail_parity >> s) & 1;
         tail_parity ^= 1u << s;
         if (!__all_sync(0xffffffffu, wait(tail_bar(s), par))) break;
-        const int rem = cnt - (kb_n - 1) * BK;
+        const int rem = cnt - (n - 1) * BK;
         rag_zero_rows<6>(smem_base + s * stage_bytes, rem, (rem + 15) / 16 * 16, lane);
         if (lane == 0) mbar_arrive(zeroed_bar(s));
       }
@@ -312,8 +318,9 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
       bool empty = false;
       if (OP == RAG_WGRAD) {
         V = rag_wtile(args, t);
-        empty = s_rows[V.e].y == 0;
-        if (empty && args.accumulate) continue;
+        const int n = (s_rows[V.e].y + BK - 1) / BK;
+        empty = slice1(n) == slice0(n);
+        if (empty && (args.accumulate || splits > 1)) continue;
       } else {
         D = rag_tile<16>(sched, args, t);
       }
@@ -337,6 +344,20 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
       };
       if (OP == RAG_WGRAD) {
         const int half = (warp - 2) >> 2;
+        if (splits > 1) {
+          float* p = args.part + (((size_t)t * splits + rank) * 128 + q * 32 + lane) * 256 + half * 128;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(taddr + half * 128 + c, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<uint4*>(p + c + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+          }
+          release();
+          continue;
+        }
         rag_wgrad_epilogue<T, BOXES, 128>(args, &tmD, box_base + (warp - 2) * BOXES * 4096, turn,
                                           taddr + half * 128, empty, V.e,
                                           V.n_tile * 128 + q * 32, V.k_tile * 256 + half * 128,
@@ -376,10 +397,55 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
-  if (OP != RAG_WGRAD && splits > 1) {
-    // join: the cluster's sums are in the workspace; a lane takes four columns
+  if (splits > 1) {
+    // join: the cluster's sums are in the workspace
     cluster_sync();
-    if (first < total) {
+    constexpr int WARPS = num_threads(OP) / 32;
+    if (OP == RAG_WGRAD && first < total) {
+      // a lane takes eight columns of a row
+      const RagWTile V = rag_wtile(args, first);
+      const int steps = (s_rows[V.e].y + BK - 1) / BK, k = V.k_tile * 256 + 8 * lane;
+      const float* p = args.part + (size_t)first * splits * 128 * 256 + 8 * lane;
+      for (int j = rank * WARPS + warp; j < 128; j += splits * WARPS) {
+        const int n = V.n_tile * 128 + j;
+        if (n >= args.N || k >= args.K || (steps == 0 && args.accumulate)) continue;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+        for (int s = 0; s < splits; ++s) {
+          if (steps * (s + 1) / splits == steps * s / splits) continue;   // nothing was summed
+          const float4* v = reinterpret_cast<const float4*>(p + ((size_t)s * 128 + j) * 256);
+          a = make_float4(a.x + v[0].x, a.y + v[0].y, a.z + v[0].z, a.w + v[0].w);
+          b = make_float4(b.x + v[1].x, b.y + v[1].y, b.z + v[1].z, b.w + v[1].w);
+        }
+        const size_t at = ((size_t)V.e * args.N + n) * args.K + k;
+        if (args.out_f32) {
+          float4* d = reinterpret_cast<float4*>(static_cast<float*>(args.out) + at);
+          if (args.accumulate) {
+            const float4 x = d[0], y = d[1];
+            a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+            b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
+          }
+          d[0] = a;
+          d[1] = b;
+        } else {
+          uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.out) + at);
+          if (args.accumulate) {
+            const uint4 o = *d;
+            a = make_float4(a.x + Half16<T>::value((uint16_t)(o.x & 0xFFFFu)),
+                            a.y + Half16<T>::value((uint16_t)(o.x >> 16)),
+                            a.z + Half16<T>::value((uint16_t)(o.y & 0xFFFFu)),
+                            a.w + Half16<T>::value((uint16_t)(o.y >> 16)));
+            b = make_float4(b.x + Half16<T>::value((uint16_t)(o.z & 0xFFFFu)),
+                            b.y + Half16<T>::value((uint16_t)(o.z >> 16)),
+                            b.z + Half16<T>::value((uint16_t)(o.w & 0xFFFFu)),
+                            b.w + Half16<T>::value((uint16_t)(o.w >> 16)));
+          }
+          *d = make_uint4(Half16<T>::pack(a.x, a.y), Half16<T>::pack(a.z, a.w),
+                          Half16<T>::pack(b.x, b.y), Half16<T>::pack(b.z, b.w));
+        }
+      }
+    }
+    if (OP != RAG_WGRAD && first < total) {
+      // a lane takes four columns of a token
       const RagTile D = rag_tile<16>(sched, args, first);
       const int w = D.w_tile * 128 + 4 * lane;
       float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -389,7 +455,6 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
                            Half16<T>::value(b[3]));
       }
       const float* p = args.part + (size_t)first * splits * args.tile_rows * 128 + 4 * lane;
-      constexpr int WARPS = num_threads(OP) / 32;
       for (int j = rank * WARPS + warp; j < D.rows; j += splits * WARPS) {
         float4 v[8];
 #pragma unroll
@@ -437,6 +502,16 @@ cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,
 
 }  // namespace
 
+// CTAs that share one tile's reduction of `steps` steps: as many as have at
+// least eight steps each and as clusters run at the same time (of 2 CTAs 76, of
+// 4 36, of 8 15 on a GB300's 152 SMs: a 16th tile of eight would wait).
+static int slices(long long tiles, int steps) {
+  if (tiles <= 15 && steps >= 64) return 8;
+  if (tiles <= 36 && steps >= 32) return 4;
+  if (tiles <= 76 && steps >= 16) return 2;
+  return 1;
+}
+
 // Tiles and splits of the rows' products on one SM.
 struct RowsPlan {
   int tile_rows, w_tiles, splits;
@@ -452,17 +527,21 @@ static RowsPlan rows_plan(int R, int E, int width, int red) {
   r.tile_rows = want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
   r.w_tiles = (width + 127) / 128;
   r.tiles = ((long long)std::min(E, R) + R / r.tile_rows) * r.w_tiles;
-  // Slices of at least eight steps, as many as the SMs of the chip hold of the
-  // tiles that even segments make (a 100 x 4096 x 4096 product of one expert:
-  // 13 us in four slices, 28 us in one).  The grid and the workspace take the
-  // tiles that any segments can make.
-  constexpr int SMS = 152;
+  // Slices, by the tiles that even segments make (a 100 x 4096 x 4096 product of
+  // one expert: 13 us in four slices, 28 us in one).  The grid and the workspace
+  // take the tiles that any segments can make.
   const long long even =
       (long long)std::max(std::min(E, R), (R + r.tile_rows - 1) / r.tile_rows) * r.w_tiles;
-  r.splits = 1;
-  while (r.splits < 8 && even * r.splits * 2 <= SMS && (red + BK - 1) / BK >= 16 * r.splits)
-    r.splits *= 2;
+  r.splits = slices(even, (red + BK - 1) / BK);
   return r;
+}
+static int wgrad_splits(int R, int N, int K, int E) {
+  return slices((long long)E * ((N + 127) / 128) * ((K + 255) / 256), R / E / BK);
+}
+size_t ragged_wgrad_bytes(int R, int N, int K, int E) {
+  const int s = wgrad_splits(R, N, K, E);
+  return s > 1 ? (size_t)E * ((N + 127) / 128) * ((K + 255) / 256) * s * 128 * 256 * sizeof(float)
+               : 0;
 }
 size_t ragged_split_bytes(int R, int E, int width, int red) {
   const RowsPlan r = rows_plan(R, E, width, red);
@@ -507,7 +586,8 @@ cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows,
 }
 
 cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const void* x, void* dw,
-                                bool out_f32, bool accumulate, cudaStream_t stream) {
+                                bool out_f32, bool accumulate, void* workspace,
+                                cudaStream_t stream) {
   CUtensorMap tmA, tmB, tmD;
   const bool wide_a = p.N % 64 == 0, wide_b = p.K % 64 == 0;
   if (!(wide_a ? make_tmap_rag_wide(&tmA, dy, p.half, p.R, p.N, 1, p.ldy, 2)
@@ -535,8 +615,11 @@ cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const vo
   watchdog_params(&a.limit_ns, &a.never_arrive);
   a.err = dev_error_word();
   if (a.err == nullptr) return cudaErrorInvalidDevice;
+  a.splits = wgrad_splits(p.R, p.N, p.K, p.E);
+  a.part = static_cast<float*>(workspace);
   const long long tiles = (long long)p.E * a.e_tiles.d;
-  const int grid = (int)std::min<long long>(num_sms(), tiles);
+  const int grid = a.splits > 1 ? (int)tiles * a.splits
+                                : (int)std::min<long long>(num_sms(), tiles);
   return launch_op<RAG_WGRAD>(p.half, tmA, tmB, tmD, a, grid, stream);
 }
 

@@ -41,15 +41,16 @@ constexpr int A_BYTES = 128 * BK * 2, B_BYTES = 128 * BK * 2;   // this CTA's ha
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int SMALL_BOX = 32 * BK * 2;
 constexpr int TMEM_COLS = 512;
-// Epilogue warps: four, or four for each accumulator of a double tile.
-constexpr int epi_warps(int mt) { return 4 * mt; }
+// Epilogue warps: four; wgrad two for each quadrant of the accumulator's rows, a
+// double tile four for each accumulator.
+constexpr int epi_warps(int op, int mt) { return op == RAG_WGRAD ? 8 : 4 * mt; }
 // producer, MMA, epilogue warps; wgrad has one more, which zeroes
 constexpr int num_threads(int op, int mt) {
-  return 64 + 32 * epi_warps(mt) + (op == RAG_WGRAD ? 32 : 0);
+  return 64 + 32 * epi_warps(op, mt) + (op == RAG_WGRAD ? 32 : 0);
 }
 constexpr int BAR_BYTES = 256;
-constexpr int BOXES = 2;                      // store boxes of each epilogue warp (wgrad)
-static_assert(epi_warps(1) * BOXES * 4096 <= STAGE_BYTES, "store boxes");
+constexpr int BOXES = 1;                      // store boxes of each epilogue warp (wgrad)
+static_assert(epi_warps(RAG_WGRAD, 1) * BOXES * 4096 <= STAGE_BYTES, "store boxes");
 constexpr int SMEM_BYTES = MAX_STAGES * STAGE_BYTES + 1024 + BAR_BYTES + kRagSchedBytes;
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
   // space to the store boxes
   constexpr int STEP_BYTES = MT * A_BYTES + B_BYTES;
   constexpr int STAGES = OP == RAG_WGRAD ? MAX_STAGES - 1 : MAX_STAGES * STAGE_BYTES / STEP_BYTES;
-  constexpr int EPI_WARPS = epi_warps(MT);
+  constexpr int EPI_WARPS = epi_warps(OP, MT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -94,7 +95,8 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
     for (int s = 0; s < STAGES; ++s) mbar_init(zeroed_bar(s), 2);   // one warp of each CTA
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 8);   // four warps of both CTAs (leader's is used)
+      // an accumulator's warps in both CTAs (the leader's barrier is used)
+      mbar_init(tempty_bar(a), OP == RAG_WGRAD ? 16 : 8);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -423,9 +425,11 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
         ++local;
       };
       if (OP == RAG_WGRAD) {
-        rag_wgrad_epilogue<T, BOXES, 256>(args, &tmC, box_base + (warp - 2) * BOXES * 4096, turn,
-                                          taddr, empty, V.e, V.n_tile * 256 + rank * 128 + q * 32,
-                                          V.k_tile * 256, lane, release);
+        const int half = (warp - 2) >> 2;
+        rag_wgrad_epilogue<T, BOXES, 128>(args, &tmC, box_base + (warp - 2) * BOXES * 4096, turn,
+                                          taddr + half * 128, empty, V.e,
+                                          V.n_tile * 256 + rank * 128 + q * 32,
+                                          V.k_tile * 256 + half * 128, lane, release);
       } else {
         const int w = D.w_tile * 256 + rank * 128 + q * 32 + lane;
         float bias = 0.0f;

@@ -130,6 +130,13 @@ def test_long_reduction_of_few_tiles(rows):
     run_all([rows], 1032, 72, "float16", bias=True)
 
 
+@pytest.mark.parametrize("counts", [[2100], [5, 0, 2500], [4096, 1, 64, 1500]])
+@pytest.mark.parametrize("dw_type", [None, torch.float32])
+def test_long_segments_of_few_weights(counts, dw_type):
+    """wgrad of few tiles: a long segment's rows in slices that are joined."""
+    run_all(counts, 136, 264, "bfloat16", lead=1, dw_type=dw_type)
+
+
 def test_many_experts():
     rng = np.random.default_rng(3)
     run_all(list(rng.integers(0, 6, 1024)), 72, 40, "bfloat16")
@@ -140,12 +147,13 @@ def test_wgrad_fp32_output(dtype):
     run_all([5, 0, 200, 700], 136, 264, dtype, dw_type=torch.float32)
 
 
+@pytest.mark.parametrize("counts", [[20, 0, 300], [2100, 0, 1500]])
 @pytest.mark.parametrize("dw_type", [None, torch.float32])
-def test_wgrad_accumulates(dw_type):
-    counts, n, k = [20, 0, 300], 136, 72
+def test_wgrad_accumulates(dw_type, counts):
+    n, k, rows = 136, 72, sum(counts)
     off = offsets_of(counts)
-    p = moe.Ragged(R=320, N=n, K=k, E=3)
-    x, dy = randn((320, k), "bfloat16", 1), randn((320, n), "bfloat16", 2)
+    p = moe.Ragged(R=rows, N=n, K=k, E=3)
+    x, dy = randn((rows, k), "bfloat16", 1), randn((rows, n), "bfloat16", 2)
     start = randn((3, n, k), "bfloat16", 3, 4.0).to(dw_type or torch.bfloat16)
     dw = start.clone()
     o = torch.tensor(off, dtype=torch.int32, device="cuda")
@@ -154,7 +162,7 @@ def test_wgrad_accumulates(dw_type):
     assert moe.moe_sync_status() == 0
     ref = f64(start) + ragged.wgrad(f64(dy), f64(x), off)
     mag = abs(f64(start)) + ragged.wgrad(abs(f64(dy)), abs(f64(x)), off)
-    check(dw, ref, mag, 300 + 16, dw.dtype, "dw")
+    check(dw, ref, mag, max(counts) + 16, dw.dtype, "dw")
     assert bool((dw[1] == start[1]).all())
 
 
