@@ -53,20 +53,74 @@ size_t ragged_bytes(const moe_ragged* p) {
   return pad256(b);
 }
 
-// SM pairs (256-wide tiles) unless that leaves fewer tiles than two for each
-// pair: then the one-SM form's 128-wide tiles spread over twice as many CTAs.
-bool use_pairs(const moe_ragged* p, int width) {
-  const int form = ragged_form();
-  const int64_t tiles = ((int64_t)std::min(p->E, p->R) + p->R / 256) * ((width + 255) / 256);
-  return form >= 2 || (form == 0 && tiles >= num_sms());
+// Choice of the kernels' form.  A form's time is modelled as rounds of its CTAs
+// (or pairs) times a tile's cycles, the slower of what a step's operands take at
+// the ~50 bytes a cycle that an SM gets from L2 and its MMAs, plus a tile's fixed
+// cost, on segments of the average length.  Measured beside the model, in us:
+// dgrad of 774 rows, 8 experts, 6704 -> 2968: one SM 105, pairs 84, double tiles
+// 64; forward of the same: 74, 62, 68; forward of 8240 rows, 8 experts, 4096 ->
+// 28672: pairs 1275, double tiles 1193; 100 rows, one expert, 4096 x 4096: one SM
+// in four slices 13, pairs 23; wgrad of 16 experts, 4096 x 4096: one SM / pairs
+// 119 / 125 at 130 rows each, 192 / 158 at 257.
+enum Form { ONE_SM = 1, PAIRS = 2, DOUBLE = 3 };
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+constexpr int kSms = 152, kBytesPerCycle = 50;
+
+// Cycles of `tiles` tiles of `steps` steps on `units` CTAs or pairs.
+int64_t tiles_cycles(int64_t tiles, int64_t units, int64_t steps, int64_t load_bytes,
+                     int64_t mma, int64_t fixed) {
+  return ceil_div(tiles, units) * (steps * std::max(load_bytes / kBytesPerCycle, mma) + fixed);
+}
+// Bytes as L2 serves them: rows that do not start on a 32-byte sector cost 1.4
+// times theirs (11592 against 11584 columns: 619 / 417 us).
+int64_t l2_bytes(int64_t bytes, int64_t pitch_bytes) {
+  return pitch_bytes % 32 ? bytes * 7 / 5 : bytes;
 }
 
-// wgrad on SM pairs from segments of about 192 rows up: 16 experts, 4096 x 4096,
-// one SM / pairs: 130 rows each 119 / 125 us, 257 rows 192 / 158 us.
-bool wgrad_pairs(const moe_ragged* p) {
+// Forward (w_cols: columns of the output, red: of the reduction) or dgrad.
+// step_deep: 64, or 256 4-bit values, whose 16 KB operand tiles are alike;
+// extra: bytes of scales a step.
+Form rows_form(const moe_ragged* p, int w_cols, int red, int64_t w_pitch, int64_t x_pitch,
+               int step_deep, int extra, bool may_double) {
   const int form = ragged_form();
-  const int64_t tiles = (int64_t)p->E * ((p->N + 255) / 256) * ((p->K + 255) / 256);
-  return form >= 2 || (form == 0 && p->R >= 192ll * p->E && 2 * tiles >= num_sms());
+  if (form == DOUBLE) return may_double ? DOUBLE : PAIRS;
+  if (form != 0) return static_cast<Form>(form);
+  const int64_t segs = std::min(p->E, p->R), rows = ceil_div(p->R, segs);
+  const int64_t per_seg = ceil_div(rows, 256), tok = segs * per_seg;
+  const int64_t n = ceil_div(ceil_div(rows, per_seg), 32) * 32;    // tokens of a tile
+  const int64_t steps = ceil_div(red, step_deep);
+  const int64_t a = l2_bytes(16384, w_pitch);
+  const int64_t half = n / 2 <= 64 ? ceil_div(n / 2, 32) * 4096 : 16384;
+  const int64_t b1 = l2_bytes(n / 32 * 4096, x_pitch) + extra, b2 = l2_bytes(half, x_pitch) + extra;
+  const int64_t w1 = ceil_div(w_cols, 128), w2 = ceil_div(w_cols, 256), w4 = ceil_div(w_cols, 512);
+  const int splits = step_deep == 64 ? ragged_rows_splits(p->R, p->E, w_cols, red) : 1;
+  const int64_t one = splits > 1 ? tiles_cycles(1, 1, ceil_div(steps, splits), a + b1, 2 * n, 5000)
+                                 : tiles_cycles(tok * w1, kSms, steps, a + b1, 2 * n, 1200);
+  const int64_t two = tiles_cycles(tok * w2, kSms / 2, steps, a + b2, 2 * n, 1500);
+  const int64_t dbl = tiles_cycles(tok * w4, kSms / 2, steps, 2 * a + b2, 4 * n, 2500);
+  // what no form is faster than: the weights from HBM
+  const int64_t values = segs * w_cols * red;
+  const int64_t hbm = (step_deep == 64 ? 2 * values : values / 2) / 3500;
+  const int64_t best = std::max(std::min(one, two), hbm);
+  if (may_double && std::max(dbl, hbm) < best * 97 / 100) return DOUBLE;
+  return std::max(two, hbm) <= best ? PAIRS : ONE_SM;
+}
+
+Form wgrad_form(const moe_ragged* p) {
+  const int form = ragged_form();
+  if (form != 0) return form == ONE_SM ? ONE_SM : PAIRS;
+  const int64_t segs = std::min(p->E, p->R), steps = ceil_div(ceil_div(p->R, segs), 64);
+  const int64_t k = ceil_div(p->K, 256);
+  const int splits = ragged_wgrad_splits(p->R, p->N, p->K, p->E);
+  const int64_t t1 = p->E * ceil_div(p->N, 128) * k, t2 = p->E * ceil_div(p->N, 256) * k;
+  // a tile's output: 64 KB a CTA at an SM's share of the HBM rate
+  const int64_t out = 2800;
+  const int64_t one =
+      splits > 1 ? tiles_cycles(1, 1, ceil_div(steps, splits), 49152, 512, 8000)
+                 : std::max(tiles_cycles(t1, kSms, steps, 49152, 512, 0), ceil_div(t1, kSms) * out);
+  const int64_t two =
+      std::max(tiles_cycles(t2, kSms / 2, steps, 32768, 512, 0), ceil_div(t2, kSms / 2) * out * 21 / 20);
+  return two < one ? PAIRS : ONE_SM;
 }
 
 cudaError_t ragged_rows(const moe_ragged* p, int op, const void* rows, const void* w,
@@ -74,9 +128,11 @@ cudaError_t ragged_rows(const moe_ragged* p, int op, const void* rows, const voi
                         void* stream) {
   const RaggedProblem q = ragged_problem(p, offsets);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return use_pairs(p, op == 0 ? p->N : p->K)
-             ? launch_ragged_rows_2sm(q, op, rows, w, bias, out, st)
-             : launch_ragged_rows(q, op, rows, w, bias, out, workspace, st);
+  const bool fwd = op == 0;
+  const Form f = rows_form(p, fwd ? p->N : p->K, fwd ? p->K : p->N, 2ll * p->K,
+                           2 * (fwd ? q.ldx : q.ldy), 64, 0, true);
+  return f == ONE_SM ? launch_ragged_rows(q, op, rows, w, bias, out, workspace, st)
+                     : launch_ragged_rows_2sm(q, op, f == DOUBLE, rows, w, bias, out, st);
 }
 
 // Checks shared by the products; MOE_OK to go on.
@@ -136,7 +192,7 @@ moe_status ragged_gemm_wgrad(const moe_ragged* p, const void* dy, const void* x,
   }
   const RaggedProblem q = ragged_problem(p, expert_offsets);
   const bool f32 = dw_dtype == MOE_T_FP32;
-  return done(wgrad_pairs(p) ? launch_ragged_wgrad_2sm(q, dy, x, dw, f32, accumulate != 0, st)
+  return done(wgrad_form(p) == PAIRS ? launch_ragged_wgrad_2sm(q, dy, x, dw, f32, accumulate != 0, st)
                              : launch_ragged_wgrad(q, dy, x, dw, f32, accumulate != 0, workspace, st));
 }
 
@@ -151,7 +207,8 @@ moe_status ragged_gemm_mxfp4(const moe_ragged* p, const void* x_codes, const voi
   if (p->R == 0) return MOE_OK;
   if (!x_scales || !w_scales_packed || misaligned(x_scales, 4) || misaligned(w_scales_packed, 16))
     return MOE_ERR_INVALID_ARG;
-  const auto launch = use_pairs(p, p->N) ? launch_ragged_mxfp4_2sm : launch_ragged_mxfp4;
+  const Form f = rows_form(p, p->N, p->K, p->K / 2, p->K / 2, 256, 3072, false);
+  const auto launch = f == PAIRS ? launch_ragged_mxfp4_2sm : launch_ragged_mxfp4;
   return done(launch(ragged_problem(p, expert_offsets), x_codes,
                      static_cast<const uint8_t*>(x_scales), w_codes, w_scales_packed, y,
                      workspace, static_cast<cudaStream_t>(stream)));

@@ -216,12 +216,15 @@ cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows,
 // reduction of `red`.
 size_t ragged_split_bytes(int R, int E, int width, int red);
 size_t ragged_wgrad_bytes(int R, int N, int K, int E);
+// CTAs that share a tile's reduction in these forms.
+int ragged_rows_splits(int R, int E, int width, int red);
+int ragged_wgrad_splits(int R, int N, int K, int E);
 cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const void* x, void* dw,
                                 bool out_f32, bool accumulate, void* workspace,
                                 cudaStream_t stream);
 // The same on SM pairs.
-cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* rows, const void* w,
-                                   const void* bias, void* out,
+cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, bool double_tiles,
+                                   const void* rows, const void* w, const void* bias, void* out,
                                    cudaStream_t stream);
 cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, const void* x,
                                     void* dw, bool out_f32, bool accumulate,

@@ -535,13 +535,16 @@ static RowsPlan rows_plan(int R, int E, int width, int red) {
   r.splits = slices(even, (red + BK - 1) / BK);
   return r;
 }
-static int wgrad_splits(int R, int N, int K, int E) {
+int ragged_wgrad_splits(int R, int N, int K, int E) {
   return slices((long long)E * ((N + 127) / 128) * ((K + 255) / 256), R / E / BK);
 }
 size_t ragged_wgrad_bytes(int R, int N, int K, int E) {
-  const int s = wgrad_splits(R, N, K, E);
+  const int s = ragged_wgrad_splits(R, N, K, E);
   return s > 1 ? (size_t)E * ((N + 127) / 128) * ((K + 255) / 256) * s * 128 * 256 * sizeof(float)
                : 0;
+}
+int ragged_rows_splits(int R, int E, int width, int red) {
+  return rows_plan(R, E, width, red).splits;
 }
 size_t ragged_split_bytes(int R, int E, int width, int red) {
   const RowsPlan r = rows_plan(R, E, width, red);
@@ -615,7 +618,7 @@ cudaError_t launch_ragged_wgrad(const RaggedProblem& p, const void* dy, const vo
   watchdog_params(&a.limit_ns, &a.never_arrive);
   a.err = dev_error_word();
   if (a.err == nullptr) return cudaErrorInvalidDevice;
-  a.splits = wgrad_splits(p.R, p.N, p.K, p.E);
+  a.splits = ragged_wgrad_splits(p.R, p.N, p.K, p.E);
   a.part = static_cast<float*>(workspace);
   const long long tiles = (long long)p.E * a.e_tiles.d;
   const int grid = a.splits > 1 ? (int)tiles * a.splits

@@ -509,25 +509,6 @@ cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,
               : launch_pair<OP, __nv_bfloat16, MT>(tmA, tmB, tmC, a, tiles, stream);
 }
 
-// Whether forward or dgrad of R rows, E experts and W columns takes two weight
-// tiles together: a CTA then takes in 24 KB a tile and step instead of 32, which
-// counts where the pairs run at the rate L2 feeds them (or at the power limit).
-// Both accumulators are in use until a tile ends, so it costs the time to read
-// them: about 1000 cycles against 1024 a step.  1030 rows an expert, 8 experts,
-// 4096 -> 28672: 1275 -> 1193 us (dgrad in a long run: 1372 -> 1276); below 256
-// rows the weights bound it (193 rows, 32 experts, 4096 x 4096: 195 -> 209), and
-// with 16 steps nothing is won.  Not where the wider tiles fill the last round
-// of the pairs worse than that.
-bool rows_double_tiles(int R, int E, int W, int num_kb) {
-  if (ragged_form() >= 2) return ragged_form() == 3;
-  if (R < 256ll * E || num_kb < 24) return false;
-  const long long pairs = num_sms() / 2;
-  const long long tok = (long long)E * ((R / E + 255) / 256);    // token tiles of even segments
-  const long long one = (tok * ((W + 255) / 256) + pairs - 1) / pairs;
-  const long long two = (tok * ((W + 511) / 512) + pairs - 1) / pairs;
-  return 93 * 2 * two < 100 * one;
-}
-
 bool common(const RaggedProblem& p, RagArgs& a) {
   a.offsets = p.offsets;
   a.R = p.R;
@@ -541,7 +522,13 @@ bool common(const RaggedProblem& p, RagArgs& a) {
 
 }  // namespace
 
-cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* rows, const void* w,
+// double_tiles: a CTA then takes in 24 KB a tile and step instead of 32, which
+// counts where the pairs run at the rate L2 feeds them (or at the power limit);
+// but both accumulators are in use until a tile ends, so it costs the time to
+// read them, about 1000 cycles against 1024 a step.  1030 rows an expert, 8
+// experts, 4096 -> 28672: 1275 -> 1193 us (dgrad in a long run: 1372 -> 1276).
+cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, bool double_tiles,
+                                   const void* rows, const void* w,
                                    const void* bias, void* out,
                                    cudaStream_t stream) {
   const bool fwd = op == RAG_FWD;
@@ -557,7 +544,7 @@ cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, const void* r
   if (!common(p, a)) return cudaErrorInvalidDevice;
   a.W = fwd ? p.N : p.K;
   a.num_kb = (red + BK - 1) / BK;
-  const int mt = rows_double_tiles(p.R, p.E, a.W, a.num_kb) ? 2 : 1;
+  const int mt = double_tiles ? 2 : 1;
   a.w_tiles = fast_div((a.W + 256 * mt - 1) / (256 * mt));
   a.wide_a = wide;
   a.out = out;
