@@ -324,19 +324,19 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
       } else {
         D = rag_tile<16>(sched, args, t);
       }
-      const int acc = local & 1;
-      if (!empty) {
-        int ok = 0;
-        if (lane == 0)
-          ok = mbar_wait_bounded(tfull_bar(acc), (local >> 1) & 1, abort_flag, args.limit_ns,
-                                 args.err);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        tc_fence_after();
+      if (empty) {
+        rag_zero_expert(args, V.e, t - V.e * args.e_tiles.d, args.e_tiles.d, threadIdx.x - 64,
+                        32 * epi_warps(OP));
+        continue;
       }
+      const int acc = local & 1;
+      int ok = 0;
+      if (lane == 0) ok = wait(tfull_bar(acc), (local >> 1) & 1);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
       auto release = [&] {           // the accumulator has been read
-        if (empty) return;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(tempty_bar(acc));
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
           continue;
         }
         rag_wgrad_epilogue<T, BOXES, 128>(args, &tmD, box_base + (warp - 2) * BOXES * 4096, turn,
-                                          taddr + half * 128, empty, V.e,
+                                          taddr + half * 128, V.e,
                                           V.n_tile * 128 + q * 32, V.k_tile * 256 + half * 128,
                                           lane, release);
       } else {

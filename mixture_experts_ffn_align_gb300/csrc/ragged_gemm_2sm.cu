@@ -406,17 +406,19 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
       } else {
         D = rag_tile<32>(sched, args, t);
       }
-      const int acc = local & 1;
-      if (!empty) {
-        int ok = 0;
-        if (lane == 0) ok = wait(tfull_bar(acc), (local >> 1) & 1);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        tc_fence_after();
+      if (empty) {
+        rag_zero_expert(args, V.e, 2 * (t - V.e * args.e_tiles.d) + rank, 2 * args.e_tiles.d,
+                        threadIdx.x - 64, 32 * EPI_WARPS);
+        continue;
       }
+      const int acc = local & 1;
+      int ok = 0;
+      if (lane == 0) ok = wait(tfull_bar(acc), (local >> 1) & 1);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
       auto release = [&] {           // the accumulator has been read
-        if (empty) return;
         tc_fence_before();
         __syncwarp();
         // carries no data through memory; the releasing form would wait for this
@@ -427,7 +429,7 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
       if (OP == RAG_WGRAD) {
         const int half = (warp - 2) >> 2;
         rag_wgrad_epilogue<T, BOXES, 128>(args, &tmC, box_base + (warp - 2) * BOXES * 4096, turn,
-                                          taddr + half * 128, empty, V.e,
+                                          taddr + half * 128, V.e,
                                           V.n_tile * 256 + rank * 128 + q * 32,
                                           V.k_tile * 256 + half * 128, lane, release);
       } else {
