@@ -49,7 +49,7 @@ size_t ragged_bytes(const moe_ragged* p) {
   size_t b = std::max({(size_t)1, ragged_split_bytes(p->R, p->E, p->N, p->K),
                        ragged_split_bytes(p->R, p->E, p->K, p->N),
                        ragged_wgrad_bytes(p->R, p->N, p->K, p->E)});
-  if (mxfp4_shape(p)) b = std::max(b, ragged_mxfp4_scale_bytes(p->R, p->K, p->E));
+  if (mxfp4_shape(p)) b = std::max(b, ragged_mxfp4_bytes(p->R, p->N, p->K, p->E));
   return pad256(b);
 }
 
@@ -93,7 +93,8 @@ Form rows_form(const moe_ragged* p, int w_cols, int red, int64_t w_pitch, int64_
   const int64_t half = n / 2 <= 64 ? ceil_div(n / 2, 32) * 4096 : 16384;
   const int64_t b1 = l2_bytes(n / 32 * 4096, x_pitch) + extra, b2 = l2_bytes(half, x_pitch) + extra;
   const int64_t w1 = ceil_div(w_cols, 128), w2 = ceil_div(w_cols, 256), w4 = ceil_div(w_cols, 512);
-  const int splits = step_deep == 64 ? ragged_rows_splits(p->R, p->E, w_cols, red) : 1;
+  const int splits = step_deep == 64 ? ragged_rows_splits(p->R, p->E, w_cols, red)
+                                     : ragged_mxfp4_splits(p->R, w_cols, red, p->E);
   const int64_t one = splits > 1 ? tiles_cycles(1, 1, ceil_div(steps, splits), a + b1, 2 * n, 5000)
                                  : tiles_cycles(tok * w1, kSms, steps, a + b1, 2 * n, 1200);
   const int64_t two = tiles_cycles(tok * w2, kSms / 2, steps, a + b2, 2 * n, 1500);

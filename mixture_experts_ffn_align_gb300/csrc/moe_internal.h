@@ -234,7 +234,8 @@ cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, cons
 int ragged_form();
 // 4-bit product: x codes / scales [R, K/2] / [R, K/32], weights [E, N, K/2] with
 // packed scales; token scales are first rewritten to workspace.
-size_t ragged_mxfp4_scale_bytes(int R, int K, int E);
+size_t ragged_mxfp4_bytes(int R, int N, int K, int E);
+int ragged_mxfp4_splits(int R, int N, int K, int E);
 cudaError_t launch_ragged_mxfp4(const RaggedProblem& p, const void* xq, const uint8_t* x_scale,
                                 const void* wq, const void* w_scale_packed, void* y,
                                 void* workspace, cudaStream_t stream);

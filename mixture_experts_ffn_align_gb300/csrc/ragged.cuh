@@ -409,6 +409,55 @@ __device__ __forceinline__ void rag_store_tokens32(uint32_t (&r)[32], bool has_b
   rag_store_packed32(pk, out, ldo, live, w, W, lane);
 }
 
+// A reduction that the CTAs of a cluster share (splits > 1; one tile for each
+// cluster).  32 tokens from token c of this CTA's sums of tile t: column col.
+__device__ __forceinline__ void rag_store_part(const RagArgs& a, const uint32_t (&r)[32], int t,
+                                               int rank, int c, int rows, int col) {
+  float* p = a.part + (((size_t)t * a.splits + rank) * a.tile_rows + c) * 128 + col;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (c + j < rows) p[128 * j] = __uint_as_float(r[j]);
+}
+// After the cluster barrier: this CTA's share of tile t's tokens, the slices
+// added in order; a lane takes four columns of a token.
+template <typename T, bool BIAS>
+__device__ __forceinline__ void rag_join_tokens(const RagArgs& a, const RagTile& D, int t,
+                                                int rank, int warp, int warps, int lane) {
+  const int w = D.w_tile * 128 + 4 * lane;
+  float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (BIAS && a.bias != nullptr && w < a.W) {
+    const uint16_t* b = static_cast<const uint16_t*>(a.bias) + (size_t)D.e * a.W + w;
+    bias = make_float4(Half16<T>::value(b[0]), Half16<T>::value(b[1]), Half16<T>::value(b[2]),
+                       Half16<T>::value(b[3]));
+  }
+  const float* p = a.part + (size_t)t * a.splits * a.tile_rows * 128 + 4 * lane;
+  for (int j = rank * warps + warp; j < D.rows; j += a.splits * warps) {
+    float4 v[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s < a.splits)
+        v[s] = *reinterpret_cast<const float4*>(p + ((size_t)s * a.tile_rows + j) * 128);
+    float4 x = v[0];
+#pragma unroll
+    for (int s = 1; s < 8; ++s)
+      if (s < a.splits)
+        x = make_float4(x.x + v[s].x, x.y + v[s].y, x.z + v[s].z, x.w + v[s].w);
+    if (w < a.W)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (D.row0 + j) * a.ldo + w) =
+          make_uint2(Half16<T>::pack(x.x + bias.x, x.y + bias.y),
+                     Half16<T>::pack(x.z + bias.z, x.w + bias.w));
+  }
+}
+// CTAs that share one tile's reduction of `steps` steps: as many as have at
+// least `least` steps each and as clusters run at the same time (of 2 CTAs 76,
+// of 4 36, of 8 15 on a GB300's 152 SMs: a 16th tile of eight would wait).
+inline int rag_slices(long long tiles, int steps, int least) {
+  if (tiles <= 15 && steps >= 8 * least) return 8;
+  if (tiles <= 36 && steps >= 4 * least) return 4;
+  if (tiles <= 76 && steps >= 2 * least) return 2;
+  return 1;
+}
+
 // A 128-byte wide box of shared memory (128-byte swizzled) to a 3-D tensor,
 // clipped at its ends; with `add`, added to it (fp32, one rounding).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t c0,

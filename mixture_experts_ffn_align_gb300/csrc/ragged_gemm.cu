@@ -374,10 +374,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
           tmem_ld_32x32b_x32(taddr + c, r);
           tmem_ld_wait();
           if (splits > 1) {
-            float* p = args.part + (((size_t)t * splits + rank) * args.tile_rows + c) * 128 + q * 32 + lane;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < D.rows) p[128 * j] = __uint_as_float(r[j]);
+            rag_store_part(args, r, t, rank, c, D.rows, q * 32 + lane);
             continue;
           }
           rag_store_tokens32<T>(r, OP == RAG_FWD && args.bias != nullptr, bias,
@@ -444,38 +441,9 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         }
       }
     }
-    if (OP != RAG_WGRAD && first < total) {
-      // a lane takes four columns of a token
-      const RagTile D = rag_tile<16>(sched, args, first);
-      const int w = D.w_tile * 128 + 4 * lane;
-      float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (OP == RAG_FWD && args.bias != nullptr && w < args.W) {
-        const uint16_t* b = static_cast<const uint16_t*>(args.bias) + (size_t)D.e * args.W + w;
-        bias = make_float4(Half16<T>::value(b[0]), Half16<T>::value(b[1]), Half16<T>::value(b[2]),
-                           Half16<T>::value(b[3]));
-      }
-      const float* p = args.part + (size_t)first * splits * args.tile_rows * 128 + 4 * lane;
-      for (int j = rank * WARPS + warp; j < D.rows; j += splits * WARPS) {
-        float4 v[8];
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-          if (s < splits)
-            v[s] = *reinterpret_cast<const float4*>(p + ((size_t)s * args.tile_rows + j) * 128);
-        float4 a = v[0];
-#pragma unroll
-        for (int s = 1; s < 8; ++s)
-          if (s < splits) {
-            a.x += v[s].x;
-            a.y += v[s].y;
-            a.z += v[s].z;
-            a.w += v[s].w;
-          }
-        if (w < args.W)
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.out) + (D.row0 + j) * args.ldo + w) =
-              make_uint2(Half16<T>::pack(a.x + bias.x, a.y + bias.y),
-                         Half16<T>::pack(a.z + bias.z, a.w + bias.w));
-      }
-    }
+    if (OP != RAG_WGRAD && first < total)
+      rag_join_tokens<T, OP == RAG_FWD>(args, rag_tile<16>(sched, args, first), first, rank,
+                                        warp, WARPS, lane);
   }
 }
 
@@ -502,16 +470,6 @@ cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,
 
 }  // namespace
 
-// CTAs that share one tile's reduction of `steps` steps: as many as have at
-// least eight steps each and as clusters run at the same time (of 2 CTAs 76, of
-// 4 36, of 8 15 on a GB300's 152 SMs: a 16th tile of eight would wait).
-static int slices(long long tiles, int steps) {
-  if (tiles <= 15 && steps >= 64) return 8;
-  if (tiles <= 36 && steps >= 32) return 4;
-  if (tiles <= 76 && steps >= 16) return 2;
-  return 1;
-}
-
 // Tiles and splits of the rows' products on one SM.
 struct RowsPlan {
   int tile_rows, w_tiles, splits;
@@ -532,11 +490,11 @@ static RowsPlan rows_plan(int R, int E, int width, int red) {
   // take the tiles that any segments can make.
   const long long even =
       (long long)std::max(std::min(E, R), (R + r.tile_rows - 1) / r.tile_rows) * r.w_tiles;
-  r.splits = slices(even, (red + BK - 1) / BK);
+  r.splits = rag_slices(even, (red + BK - 1) / BK, 8);
   return r;
 }
 int ragged_wgrad_splits(int R, int N, int K, int E) {
-  return slices((long long)E * ((N + 127) / 128) * ((K + 255) / 256), R / E / BK);
+  return rag_slices((long long)E * ((N + 127) / 128) * ((K + 255) / 256), R / E / BK, 8);
 }
 size_t ragged_wgrad_bytes(int R, int N, int K, int E) {
   const int s = ragged_wgrad_splits(R, N, K, E);

@@ -153,6 +153,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int kb128 = margs.K / 128;
   // accumulators: two of 128 columns when tiles are no wider, else one of 256
   const int accs = groups == 1 ? 2 : 1;
+  // the CTAs of a cluster share a tile (splits > 1: one tile each cluster)
+  const int splits = args.splits;
+  const int rank = splits > 1 ? (int)cluster_ctarank() : 0;
+  const int first = blockIdx.x / splits, stride = gridDim.x / splits;
+  const int kb0 = args.num_kb * rank / splits, kb1 = args.num_kb * (rank + 1) / splits;
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ producer
@@ -160,14 +165,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int stage = 0;
     uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
     bool skip_first = args.never_arrive != 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    for (int t = first; t < total; t += stride) {
       const RagTile T = rag_tile<16>(sched, args, t);
       const int boxes = (T.rows + 31) / 32;
       const uint8_t* wsc = margs.w_packed +
                            ((size_t)T.e * kb128 * args.w_tiles.d + T.w_tile) * 512;
       const uint8_t* xsc = margs.x_packed + T.tok * tile_scale_bytes(args.tile_rows, margs.K);
       bool ok = true;
-      for (int kb = 0; kb < args.num_kb; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1, abort_flag, args.limit_ns, args.err)) {
           ok = false;
           break;
@@ -211,8 +216,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      for (int kb = 0; kb < args.num_kb; ++kb) {
+    for (int t = first; t < total && ok; t += stride) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!mbar_wait_bounded(sfull_bar(stage), phase, abort_flag, args.limit_ns, args.err)) {
           ok = false;
           break;
@@ -242,14 +247,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t phase = 0;
     int local = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int t = first; t < total && ok; t += stride) {
       const int n = (rag_tile<16>(sched, args, t).rows + 15) / 16 * 16;
       const int acc = accs == 2 ? local & 1 : 0;
       const int use = accs == 2 ? local >> 1 : local;
       if (!mbar_wait_bounded(tempty_bar(acc), (use & 1) ^ 1, abort_flag, args.limit_ns, args.err))
         break;
       tc_fence_after();
-      for (int kb = 0; kb < args.num_kb; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, args.limit_ns, args.err) ||
             !mbar_wait_bounded(sready_bar(stage), phase, abort_flag, args.limit_ns, args.err)) {
           ok = false;
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int j = 0; j < 2 * words; ++j)
           umma_mxf4(tmem_base + acc * 128, adesc + 2 * j, bdesc + 2 * j,
                     make_idesc_block_scaled(kFmtMxf4, kFmtMxf4, 128, n, 2 * (j & 1)),
-                    sf + 16 * (j >> 1), sf + 32 + 16 * (j >> 1), (kb | j) != 0);
+                    sf + 16 * (j >> 1), sf + 32 + 16 * (j >> 1), kb != kb0 || j != 0);
         tc_commit(empty_bar(stage));
         if (++stage == STAGES) {
           stage = 0;
@@ -280,7 +285,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
     int local = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    for (int t = first; t < total; t += stride) {
       const RagTile V = rag_tile<16>(sched, args, t);
       const int acc = accs == 2 ? local & 1 : 0;
       const int use = accs == 2 ? local >> 1 : local;
@@ -297,6 +302,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t r[32];
         tmem_ld_32x32b_x32(taddr + c, r);
         tmem_ld_wait();
+        if (splits > 1) {
+          rag_store_part(args, r, t, rank, c, V.rows, q * 32 + lane);
+          continue;
+        }
         rag_store_tokens32<T>(r, false, 0.0f,
                               static_cast<uint16_t*>(args.out) + (V.row0 + c) * args.ldo + w,
                               args.ldo, V.rows - c, w, args.W, lane);
@@ -315,6 +324,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
+  if (splits > 1) {
+    cluster_sync();       // the cluster's sums are in the workspace
+    if (first < total)
+      rag_join_tokens<T, false>(args, rag_tile<16>(sched, args, first), first, rank, warp,
+                                NUM_THREADS / 32, lane);
+  }
 }
 
 template <typename T>
@@ -326,7 +341,8 @@ cudaError_t launch_mx(const CUtensorMap& tmA, const CUtensorMap& tmB, const Mx44
                                 SMEM_BYTES);
   });
   if (e != cudaSuccess) return e;
-  return launch_dependent(k_ragged_mxfp4<T>, grid, NUM_THREADS, SMEM_BYTES, stream, 1, tmA, tmB, a);
+  return launch_dependent(k_ragged_mxfp4<T>, grid, NUM_THREADS, SMEM_BYTES, stream, std::max(1, a.r.splits),
+                          tmA, tmB, a);
 }
 
 }  // namespace
@@ -346,9 +362,19 @@ cudaError_t launch_pack_token_scales(const Mx44Args& args, long long most_tiles,
 }
 template cudaError_t launch_pack_token_scales<32>(const Mx44Args&, long long, cudaStream_t);
 
-size_t ragged_mxfp4_scale_bytes(int R, int K, int E) {
+int ragged_mxfp4_splits(int R, int N, int K, int E) {
+  const int tr = ragged_mxfp4_tile_rows(R, E);
+  const long long even = (long long)std::max(std::min(E, R), (R + tr - 1) / tr) * (N / 128);
+  return rag_slices(even, (K + BK - 1) / BK, 4);
+}
+static size_t scale_bytes(int R, int K, int E) {
   const int tr = ragged_mxfp4_tile_rows(R, E);
   return (size_t)most_token_tiles(R, E, tr) * tile_scale_bytes(tr, K);
+}
+size_t ragged_mxfp4_bytes(int R, int N, int K, int E) {
+  const int tr = ragged_mxfp4_tile_rows(R, E), s = ragged_mxfp4_splits(R, N, K, E);
+  return scale_bytes(R, K, E) +
+         (s > 1 ? (size_t)most_token_tiles(R, E, tr) * (N / 128) * s * tr * 128 * sizeof(float) : 0);
 }
 
 cudaError_t launch_ragged_mxfp4(const RaggedProblem& p, const void* xq, const uint8_t* x_scale,
@@ -379,7 +405,10 @@ cudaError_t launch_ragged_mxfp4(const RaggedProblem& p, const void* xq, const ui
   const cudaError_t e = launch_pack_token_scales<16>(a, tok, stream);
   if (e != cudaSuccess) return e;
   a.r.w_tiles = fast_div(p.N / 128);
-  const int grid = (int)std::min<long long>(num_sms(), tok * a.r.w_tiles.d);
+  a.r.splits = ragged_mxfp4_splits(p.R, p.N, p.K, p.E);
+  a.r.part = reinterpret_cast<float*>(a.x_packed + scale_bytes(p.R, p.K, p.E));
+  const int grid = a.r.splits > 1 ? (int)(tok * a.r.w_tiles.d) * a.r.splits
+                                  : (int)std::min<long long>(num_sms(), tok * a.r.w_tiles.d);
   return p.half ? launch_mx<__half>(tmA, tmB, a, grid, stream)
                 : launch_mx<__nv_bfloat16>(tmA, tmB, a, grid, stream);
 }

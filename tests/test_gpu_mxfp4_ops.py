@@ -152,6 +152,12 @@ def test_product_one_expert(rows, form):
     product([rows], 256, 512, seed=rows)
 
 
+@pytest.mark.parametrize("counts", [[1], [200], [3, 0, 60]])
+def test_product_long_reduction_of_few_tiles(counts, form):
+    """Few tiles, a long reduction: slices that are joined."""
+    product(counts, 256, 8576, lo=122, hi=126)
+
+
 def test_product_rows_of_no_expert_and_stride(form):
     product([40, 0, 90], 128, 384, lead=3, tail=9, ldy=136)
 
