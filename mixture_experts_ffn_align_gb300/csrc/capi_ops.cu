@@ -95,16 +95,21 @@ Form rows_form(const moe_ragged* p, int w_cols, int red, int64_t w_pitch, int64_
   const int64_t w1 = ceil_div(w_cols, 128), w2 = ceil_div(w_cols, 256), w4 = ceil_div(w_cols, 512);
   const int splits = step_deep == 64 ? ragged_rows_splits(p->R, p->E, w_cols, red)
                                      : ragged_mxfp4_splits(p->R, w_cols, red, p->E);
+  // 4-bit tiles of more than 128 tokens leave room for one accumulator only; the
+  // pairs also read weights a little faster at the same model time
+  const bool one_acc = step_deep != 64 && p->R > 64ll * p->E && p->R > 128;
   const int64_t one = splits > 1 ? tiles_cycles(1, 1, ceil_div(steps, splits), a + b1, 2 * n, 5000)
-                                 : tiles_cycles(tok * w1, kSms, steps, a + b1, 2 * n, 1200);
-  const int64_t two = tiles_cycles(tok * w2, kSms / 2, steps, a + b2, 2 * n, 1500);
+                                 : tiles_cycles(tok * w1, kSms, steps, a + b1, 2 * n,
+                                                one_acc ? 4000 : 1200) * 21 / 20;
+  const int64_t two = tiles_cycles(tok * w2, kSms / 2, steps, a + b2, 2 * n, one_acc ? 2000 : 1500);
   const int64_t dbl = tiles_cycles(tok * w4, kSms / 2, steps, 2 * a + b2, 4 * n, 2500);
-  // what no form is faster than: the weights from HBM
+  // what no form is faster than: the weights from HBM (double tiles have to gain
+  // more than their longer end then)
   const int64_t values = segs * w_cols * red;
   const int64_t hbm = (step_deep == 64 ? 2 * values : values / 2) / 3500;
   const int64_t best = std::max(std::min(one, two), hbm);
-  if (may_double && std::max(dbl, hbm) < best * 97 / 100) return DOUBLE;
-  return std::max(two, hbm) <= best ? PAIRS : ONE_SM;
+  if (may_double && steps >= 16 && std::max(dbl, hbm) < best * 97 / 100) return DOUBLE;
+  return two <= one && w_cols > 128 ? PAIRS : ONE_SM;
 }
 
 Form wgrad_form(const moe_ragged* p) {
