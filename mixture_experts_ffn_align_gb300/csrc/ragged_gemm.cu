@@ -137,8 +137,11 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
     return mbar_wait_bounded(bar, parity, abort_flag, args.limit_ns, args.err);
   };
+  auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {   // the whole warp
+    return __all_sync(0xffffffffu, wait(bar, parity));
+  };
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ------------------------------------------------------------ producer
     const uint64_t pol_w = l2_policy(0);
     const uint64_t pol_t = l2_policy(1);     // tokens: re-read for every weight tile
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
       }
       bool ok = true;
       for (int kb = 0; kb < kb_n; ++kb) {
-        if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1, abort_flag, args.limit_ns, args.err)) {
+        if (!warp_wait(empty_bar(stage), phase ^ 1)) {
           ok = false;
           break;
         }
@@ -170,14 +173,16 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         } else {
           const uint32_t sa = smem_base + stage * stage_bytes, sb = sa + A_BYTES;
           uint32_t bar = full_bar(stage);
-          if (OP == RAG_WGRAD) {
-            if (kb == tail_kb) {
-              // copies of a step to be zeroed behind: counted on their own barrier
-              mbar_arrive(bar);
-              bar = tail_bar(stage);
-              tail_parity ^= 1u << stage;       // bit: parity of the next use's phase
-              tail_mask |= 1u << stage;
-            }
+          const bool one = elect_one();
+          if (OP == RAG_WGRAD && kb == tail_kb) {
+            // copies of a step to be zeroed behind: counted on their own barrier
+            if (one) mbar_arrive(bar);
+            bar = tail_bar(stage);
+            tail_parity ^= 1u << stage;       // bit: parity of the next use's phase
+            tail_mask |= 1u << stage;
+          }
+          if (!one) {
+          } else if (OP == RAG_WGRAD) {
             mbar_arrive_expect_tx(bar, A_BYTES + 256 * BK * 2);
             const int r0 = row0 + kb * BK;
             if (args.wide_a) {
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         mbar_wait_bounded(tail_bar(s), ((tail_parity >> s) & 1) ^ 1, nullptr, args.limit_ns,
                           args.err);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t major = (OP != RAG_FWD ? kIdescAMn : 0u) | (OP == RAG_WGRAD ? kIdescBMn : 0u);
     constexpr uint32_t a_step = OP != RAG_FWD ? 128 : 2, b_step = OP == RAG_WGRAD ? 128 : 2;
@@ -248,11 +253,11 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
       }
       const uint32_t idesc = make_idesc(Half16<T>::kFmt, Half16<T>::kFmt, 128, n) | major;
       const int acc = local & 1;
-      if (!wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1)) break;
+      if (!warp_wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1)) break;
       tc_fence_after();
       bool ok = true;
       for (int kb = 0; kb < kb_n; ++kb) {
-        if (!wait(full_bar(stage), phase)) {
+        if (!warp_wait(full_bar(stage), phase)) {
           ok = false;
           break;
         }
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
           if (rem % 16) {               // the rows behind the segment are zeros
             const uint32_t par = (tail_parity >> stage) & 1;
             tail_parity ^= 1u << stage;
-            if (!wait(zeroed_bar(stage), par)) {
+            if (!warp_wait(zeroed_bar(stage), par)) {
               ok = false;
               break;
             }
@@ -274,10 +279,12 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         const uint64_t adesc = OP != RAG_FWD ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
         const uint64_t bdesc = OP == RAG_WGRAD ? sdesc_mn_sw128(sa + A_BYTES)
                                                : sdesc_k_sw128(sa + A_BYTES);
-        for (int k = 0; k < steps; ++k)
-          umma_f16(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
-                   (kb | k) != 0);
-        tc_commit(empty_bar(stage));
+        if (elect_one()) {
+          for (int k = 0; k < steps; ++k)
+            umma_f16(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
+                     (kb | k) != 0);
+          tc_commit(empty_bar(stage));
+        }
         if (kb == 0) rows_next = rows_of(t + stride);
         if (++stage == stages) {
           stage = 0;
@@ -285,10 +292,10 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
         }
       }
       if (!ok) break;
-      tc_commit(tfull_bar(acc));
+      if (elect_one()) tc_commit(tfull_bar(acc));
       ++local;
     }
-    tc_commit(drain_bar);
+    if (elect_one()) tc_commit(drain_bar);
     mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
   } else if (OP == RAG_WGRAD && warp == 2 + epi_warps(OP)) {
     // ------------------------------------------------------------ zeroing warp

@@ -128,9 +128,12 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
     return mbar_wait_bounded(bar, parity, abort_flag, args.limit_ns, args.err);
   };
+  auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {   // the whole warp
+    return __all_sync(0xffffffffu, wait(bar, parity));
+  };
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;   // this pair's tiles
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ------------------------------------------------------------ producers
     const uint64_t pol_w = l2_policy(0), pol_t = l2_policy(1);
     int stage = 0;
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
       }
       bool ok = true;
       for (int kb = 0; kb < kb_n; ++kb) {
-        if (!wait(empty_bar(stage), phase ^ 1)) {
+        if (!warp_wait(empty_bar(stage), phase ^ 1)) {
           ok = false;
           break;
         }
@@ -167,19 +170,24 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
         } else {
           const uint32_t sa = smem_base + stage * STEP_BYTES, sb = sa + MT * A_BYTES;
           uint32_t bar = mapa_shared(full_bar(stage), 0);
-          if (OP == RAG_WGRAD && kb == tail_kb) {
+          const bool tail = OP == RAG_WGRAD && kb == tail_kb;
+          if (tail) {
             // copies of a step to be zeroed behind: counted on this CTA's own barrier
-            if (leader) mbar_arrive(full_bar(stage));
-            mbar_arrive_expect_tx(tail_bar(stage), STAGE_BYTES);
             bar = mapa_shared(tail_bar(stage), rank);
             tail_parity ^= 1u << stage;     // bit: parity of the next use's phase
             tail_mask |= 1u << stage;
-          } else if (leader) {
-            mbar_arrive_expect_tx(full_bar(stage), 2 * (a_tiles * A_BYTES + b_bytes));
           }
           issued_mask |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          if (OP == RAG_WGRAD) {
+          const bool one = elect_one();
+          if (one && tail) {
+            if (leader) mbar_arrive(full_bar(stage));
+            mbar_arrive_expect_tx(tail_bar(stage), STAGE_BYTES);
+          } else if (one && leader) {
+            mbar_arrive_expect_tx(full_bar(stage), 2 * (a_tiles * A_BYTES + b_bytes));
+          }
+          if (!one) {
+          } else if (OP == RAG_WGRAD) {
             const int n0 = V.n_tile * 256 + rank * 128, k0 = V.k_tile * 256 + rank * 128;
             const int r0 = row0 + kb * BK;
             if (args.wide_a) {
@@ -232,7 +240,7 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
         mbar_wait_bounded(tail_bar(s), ((tail_parity >> s) & 1) ^ 1, nullptr, args.limit_ns,
                           args.err);
     }
-  } else if (warp == 1 && leader && lane == 0) {
+  } else if (warp == 1 && leader) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t major = (OP != RAG_FWD ? kIdescAMn : 0u) | (OP == RAG_WGRAD ? kIdescBMn : 0u);
     constexpr uint32_t a_step = OP != RAG_FWD ? 128 : 2, b_step = OP == RAG_WGRAD ? 128 : 2;
@@ -263,11 +271,11 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
       // one tile in turn in the two accumulators, or a double tile in both
       const int acc = MT == 2 ? 0 : local & 1;
       const uint32_t acc_phase = (MT == 2 ? local : local >> 1) & 1;
-      if (!wait(tempty_bar(acc), acc_phase ^ 1)) break;
+      if (!warp_wait(tempty_bar(acc), acc_phase ^ 1)) break;
       tc_fence_after();
       bool ok = true;
       for (int kb = 0; kb < kb_n; ++kb) {
-        if (!wait(full_bar(stage), phase)) {
+        if (!warp_wait(full_bar(stage), phase)) {
           ok = false;
           break;
         }
@@ -279,8 +287,9 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
           if (rem % 16) {          // the rows behind the segment are zeros in both CTAs
             const uint32_t par = (tail_parity >> stage) & 1;
             tail_parity ^= 1u << stage;
-            if (!mbar_wait_bounded<true>(zeroed_bar(stage), par, abort_flag, args.limit_ns,
-                                         args.err)) {
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait_bounded<true>(zeroed_bar(stage), par, abort_flag,
+                                                    args.limit_ns, args.err))) {
               ok = false;
               break;
             }
@@ -290,26 +299,29 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
         const uint64_t adesc = OP != RAG_FWD ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
         const uint64_t bdesc = OP == RAG_WGRAD ? sdesc_mn_sw128(sa + A_BYTES)
                                                : sdesc_k_sw128(sa + MT * A_BYTES);
-        for (int k = 0; k < steps; ++k)
-          umma_f16_pair(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
-                        (kb | k) != 0);
+        const bool one = elect_one();
+        if (one)
+          for (int k = 0; k < steps; ++k)
+            umma_f16_pair(tmem_base + acc * 256, adesc + a_step * k, bdesc + b_step * k, idesc,
+                          (kb | k) != 0);
         if (MT == 2) {
           // the first half is complete while the second's last MMAs still run
-          if (kb == kb_n - 1) tc_commit_pair(tfull_bar(0), 0x3);
+          if (kb == kb_n - 1 && one) tc_commit_pair(tfull_bar(0), 0x3);
           if (two) {
             if (kb == 0) {
-              if (!wait(tempty_bar(1), (second & 1) ^ 1)) {
+              if (!warp_wait(tempty_bar(1), (second & 1) ^ 1)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
             }
-            for (int k = 0; k < steps; ++k)
-              umma_f16_pair(tmem_base + 256, adesc + A_BYTES / 16 + a_step * k, bdesc + b_step * k,
-                            idesc, (kb | k) != 0);
+            if (one)
+              for (int k = 0; k < steps; ++k)
+                umma_f16_pair(tmem_base + 256, adesc + A_BYTES / 16 + a_step * k,
+                              bdesc + b_step * k, idesc, (kb | k) != 0);
           }
         }
-        tc_commit_pair(empty_bar(stage), 0x3);
+        if (one) tc_commit_pair(empty_bar(stage), 0x3);
         if (kb == 0) rows_next = rows_of(t + stride);
         if (++stage == STAGES) {
           stage = 0;
@@ -317,14 +329,15 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
         }
       }
       if (!ok) break;
-      if (MT == 1) tc_commit_pair(tfull_bar(acc), 0x3);
+      const bool one = elect_one();
+      if (MT == 1 && one) tc_commit_pair(tfull_bar(acc), 0x3);
       if (two) {
-        tc_commit_pair(tfull_bar(1), 0x3);
+        if (one) tc_commit_pair(tfull_bar(1), 0x3);
         ++second;
       }
       ++local;
     }
-    tc_commit_pair(drain_bar, 0x1);
+    if (elect_one()) tc_commit_pair(drain_bar, 0x1);
     mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
   } else if (OP == RAG_WGRAD && warp == 2 + EPI_WARPS) {
     // ------------------------------------------------------------ zeroing warp

@@ -159,7 +159,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int first = blockIdx.x / splits, stride = gridDim.x / splits;
   const int kb0 = args.num_kb * rank / splits, kb1 = args.num_kb * (rank + 1) / splits;
 
-  if (warp == 0 && lane == 0) {
+  auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {   // the whole warp
+    return __all_sync(0xffffffffu,
+                      mbar_wait_bounded(bar, parity, abort_flag, args.limit_ns, args.err));
+  };
+
+  if (warp == 0) {
     // ------------------------------------------------------------ producer
     const uint64_t pol_w = l2_policy(0), pol_t = l2_policy(1);
     int stage = 0;
@@ -173,7 +178,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint8_t* xsc = margs.x_packed + T.tok * tile_scale_bytes(args.tile_rows, margs.K);
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1, abort_flag, args.limit_ns, args.err)) {
+        if (!warp_wait(empty_bar(stage), phase ^ 1)) {
           ok = false;
           break;
         }
@@ -182,18 +187,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         } else {
           const int words = min(2, kb128 - 2 * kb);
           const uint32_t slot = slot_base + stage * SLOT_BYTES;
-          mbar_arrive_expect_tx(sfull_bar(stage), words * 512 * (1 + groups));
-          for (int j = 0; j < words; ++j)
-            bulk_load(slot + 512 * j, wsc + (size_t)(2 * kb + j) * args.w_tiles.d * 512, 512,
-                      sfull_bar(stage));
-          bulk_load(slot + 1024, xsc + (size_t)(2 * kb) * groups * 512, words * groups * 512,
-                    sfull_bar(stage));
           const uint32_t sa = smem_base + stage * STAGE_BYTES;
-          mbar_arrive_expect_tx(full_bar(stage), A_BYTES + boxes * 32 * (BK / 2));
-          tma_load_3d(sa, &tmA, full_bar(stage), kb * (BK / 2), T.w_tile * 128, T.e, pol_w);
-          for (int j = 0; j < boxes; ++j)
-            tma_load_2d(sa + A_BYTES + j * 32 * (BK / 2), &tmB, full_bar(stage), kb * (BK / 2),
-                        T.row0 + 32 * j, pol_t);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(sfull_bar(stage), words * 512 * (1 + groups));
+            for (int j = 0; j < words; ++j)
+              bulk_load(slot + 512 * j, wsc + (size_t)(2 * kb + j) * args.w_tiles.d * 512, 512,
+                        sfull_bar(stage));
+            bulk_load(slot + 1024, xsc + (size_t)(2 * kb) * groups * 512, words * groups * 512,
+                      sfull_bar(stage));
+            mbar_arrive_expect_tx(full_bar(stage), A_BYTES + boxes * 32 * (BK / 2));
+            tma_load_3d(sa, &tmA, full_bar(stage), kb * (BK / 2), T.w_tile * 128, T.e, pol_w);
+            for (int j = 0; j < boxes; ++j)
+              tma_load_2d(sa + A_BYTES + j * 32 * (BK / 2), &tmB, full_bar(stage), kb * (BK / 2),
+                          T.row0 + 32 * j, pol_t);
+          }
           issued_mask |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
         }
@@ -209,7 +216,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mbar_wait_bounded(full_bar(s), (issued_parity >> s) & 1, nullptr, args.limit_ns, args.err);
         mbar_wait_bounded(sfull_bar(s), (issued_parity >> s) & 1, nullptr, args.limit_ns, args.err);
       }
-  } else if (warp == 2 && lane == 0) {
+  } else if (warp == 2) {
     // ------------------------------------------------------------ scale copier
     // The place of slot s in tensor memory is free: the slot was refilled only
     // after the MMAs of its last step completed.
@@ -218,7 +225,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     for (int t = first; t < total && ok; t += stride) {
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(sfull_bar(stage), phase, abort_flag, args.limit_ns, args.err)) {
+        if (!warp_wait(sfull_bar(stage), phase)) {
           ok = false;
           break;
         }
@@ -226,22 +233,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int words = min(2, kb128 - 2 * kb);
         const uint32_t src = slot_base + stage * SLOT_BYTES;
         const uint32_t dst = tmem_base + SF_COL0 + SF_SLOT * stage;
-        for (int j = 0; j < words; ++j) {
-          tmem_cp_32x128b_x4(dst + 16 * j, sdesc_rows16(src + 512 * j));
-          for (int g = 0; g < groups; ++g)
-            tmem_cp_32x128b_x4(dst + 32 + 16 * j + 4 * g,
-                               sdesc_rows16(src + 1024 + (j * groups + g) * 512));
+        if (elect_one()) {
+          for (int j = 0; j < words; ++j) {
+            tmem_cp_32x128b_x4(dst + 16 * j, sdesc_rows16(src + 512 * j));
+            for (int g = 0; g < groups; ++g)
+              tmem_cp_32x128b_x4(dst + 32 + 16 * j + 4 * g,
+                                 sdesc_rows16(src + 1024 + (j * groups + g) * 512));
+          }
+          tc_commit(sready_bar(stage));
         }
-        tc_commit(sready_bar(stage));
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
-    tc_commit(cdrain_bar);
+    if (elect_one()) tc_commit(cdrain_bar);
     mbar_wait_bounded(cdrain_bar, 0, nullptr, args.limit_ns, args.err);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     int stage = 0;
     uint32_t phase = 0;
@@ -249,14 +258,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     for (int t = first; t < total && ok; t += stride) {
       const int n = (rag_tile<16>(sched, args, t).rows + 15) / 16 * 16;
+      const uint32_t id0 = make_idesc_block_scaled(kFmtMxf4, kFmtMxf4, 128, n, 0);
+      const uint32_t id2 = make_idesc_block_scaled(kFmtMxf4, kFmtMxf4, 128, n, 2);
       const int acc = accs == 2 ? local & 1 : 0;
       const int use = accs == 2 ? local >> 1 : local;
-      if (!mbar_wait_bounded(tempty_bar(acc), (use & 1) ^ 1, abort_flag, args.limit_ns, args.err))
-        break;
+      if (!warp_wait(tempty_bar(acc), (use & 1) ^ 1)) break;
       tc_fence_after();
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, args.limit_ns, args.err) ||
-            !mbar_wait_bounded(sready_bar(stage), phase, abort_flag, args.limit_ns, args.err)) {
+        if (!warp_wait(full_bar(stage), phase) || !warp_wait(sready_bar(stage), phase)) {
           ok = false;
           break;
         }
@@ -265,21 +274,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint64_t adesc = sdesc_k_sw128(sa), bdesc = sdesc_k_sw128(sa + A_BYTES);
         const uint32_t sf = tmem_base + SF_COL0 + SF_SLOT * stage;
         const int words = min(2, kb128 - 2 * kb);
-        for (int j = 0; j < 2 * words; ++j)
-          umma_mxf4(tmem_base + acc * 128, adesc + 2 * j, bdesc + 2 * j,
-                    make_idesc_block_scaled(kFmtMxf4, kFmtMxf4, 128, n, 2 * (j & 1)),
-                    sf + 16 * (j >> 1), sf + 32 + 16 * (j >> 1), kb != kb0 || j != 0);
-        tc_commit(empty_bar(stage));
+        if (elect_one()) {
+          for (int j = 0; j < words; ++j) {
+            umma_mxf4(tmem_base + acc * 128, adesc + 4 * j, bdesc + 4 * j, id0, sf + 16 * j,
+                      sf + 32 + 16 * j, kb != kb0 || j != 0);
+            umma_mxf4(tmem_base + acc * 128, adesc + 4 * j + 2, bdesc + 4 * j + 2, id2,
+                      sf + 16 * j, sf + 32 + 16 * j, 1);
+          }
+          tc_commit(empty_bar(stage));
+        }
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
         }
       }
       if (!ok) break;
-      tc_commit(tfull_bar(acc));
+      if (elect_one()) tc_commit(tfull_bar(acc));
       ++local;
     }
-    tc_commit(drain_bar);
+    if (elect_one()) tc_commit(drain_bar);
     mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
   } else if (warp >= 3) {
     // ------------------------------------------------------------ epilogue

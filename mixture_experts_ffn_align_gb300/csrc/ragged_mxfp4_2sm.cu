@@ -130,8 +130,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
     return mbar_wait_bounded(bar, parity, abort_flag, args.limit_ns, args.err);
   };
+  auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {   // the whole warp
+    return __all_sync(0xffffffffu, wait(bar, parity));
+  };
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ------------------------------------------------------------ producers
     const uint64_t pol_w = l2_policy(0), pol_t = l2_policy(1);
     int stage = 0;
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int w0 = D.w_tile * 256 + rank * 128;
       bool ok = true;
       for (int kb = 0; kb < args.num_kb; ++kb) {
-        if (!wait(empty_bar(stage), phase ^ 1)) {
+        if (!warp_wait(empty_bar(stage), phase ^ 1)) {
           ok = false;
           break;
         }
@@ -157,23 +160,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint32_t sa = smem_base + stage * STAGE_BYTES;
           const uint32_t sbar = mapa_shared(sfull_bar(stage), 0);
           const uint32_t bar = mapa_shared(full_bar(stage), 0);
-          if (leader) {
-            mbar_arrive_expect_tx(sfull_bar(stage), 2 * (1024 + 1024 * groups));
-            mbar_arrive_expect_tx(full_bar(stage), 2 * (A_BYTES + b_bytes));
-            issued_mask |= 1u << stage;
-            issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          }
-          // the second word of a last step of 128 is not used
-          tma_load_3d_pair(slot, &tmSA, sbar, 0, w0 / 128, D.e * kb128 + 2 * kb, pol_w);
-          tma_load_2d_pair(slot + 1024, &tmSB, sbar, 0, (D.tok * kb128 + 2 * kb) * groups, pol_t);
-          tma_load_3d_pair(sa, &tmA, bar, kb * (BK / 2), w0, D.e, pol_w);
           const uint32_t sb = sa + A_BYTES;
-          if (b_bytes == B_BYTES) {
-            tma_load_2d_pair(sb, &tmB, bar, kb * (BK / 2), row0, pol_t);
-          } else {
-            tma_load_2d_pair(sb, &tmB32, bar, kb * (BK / 2), row0, pol_t);
-            if (b_bytes > SMALL_BOX)
-              tma_load_2d_pair(sb + SMALL_BOX, &tmB32, bar, kb * (BK / 2), row0 + 32, pol_t);
+          issued_mask |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (elect_one()) {
+            if (leader) {
+              mbar_arrive_expect_tx(sfull_bar(stage), 2 * (1024 + 1024 * groups));
+              mbar_arrive_expect_tx(full_bar(stage), 2 * (A_BYTES + b_bytes));
+            }
+            // the second word of a last step of 128 is not used
+            tma_load_3d_pair(slot, &tmSA, sbar, 0, w0 / 128, D.e * kb128 + 2 * kb, pol_w);
+            tma_load_2d_pair(slot + 1024, &tmSB, sbar, 0, (D.tok * kb128 + 2 * kb) * groups, pol_t);
+            tma_load_3d_pair(sa, &tmA, bar, kb * (BK / 2), w0, D.e, pol_w);
+            if (b_bytes == B_BYTES) {
+              tma_load_2d_pair(sb, &tmB, bar, kb * (BK / 2), row0, pol_t);
+            } else {
+              tma_load_2d_pair(sb, &tmB32, bar, kb * (BK / 2), row0, pol_t);
+              if (b_bytes > SMALL_BOX)
+                tma_load_2d_pair(sb + SMALL_BOX, &tmB32, bar, kb * (BK / 2), row0 + 32, pol_t);
+            }
           }
         }
         if (++stage == STAGES) {
@@ -191,37 +196,39 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           mbar_wait_bounded(sfull_bar(s), (issued_parity >> s) & 1, nullptr, args.limit_ns,
                             args.err);
         }
-  } else if (warp == 2 && lane == 0 && leader) {
+  } else if (warp == 2 && leader) {
     // ------------------------------------------------------------ scale copier
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += stride) {
       for (int kb = 0; kb < args.num_kb; ++kb) {
-        if (!wait(sfull_bar(stage), phase)) {
+        if (!warp_wait(sfull_bar(stage), phase)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t src = slot_base + stage * SLOT_BYTES;
         const uint32_t dst = tmem_base + SF_COL0 + SF_SLOT * stage;
+        if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          tmem_cp_pair_32x128b_x4(dst + 16 * j, sdesc_rows16(src + 512 * j));
-          tmem_cp_pair_32x128b_x4(dst + 32 + 16 * j, sdesc_rows16(src + 1024 + 512 * groups * j));
-          if (!twin)
-            tmem_cp_pair_32x128b_x4(dst + 36 + 16 * j, sdesc_rows16(src + 1536 + 1024 * j));
+          for (int j = 0; j < 2; ++j) {
+            tmem_cp_pair_32x128b_x4(dst + 16 * j, sdesc_rows16(src + 512 * j));
+            tmem_cp_pair_32x128b_x4(dst + 32 + 16 * j, sdesc_rows16(src + 1024 + 512 * groups * j));
+            if (!twin)
+              tmem_cp_pair_32x128b_x4(dst + 36 + 16 * j, sdesc_rows16(src + 1536 + 1024 * j));
+          }
+          tc_commit_pair(sready_bar(stage), 0x1);
         }
-        tc_commit_pair(sready_bar(stage), 0x1);
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
-    tc_commit_pair(cdrain_bar, 0x1);
+    if (elect_one()) tc_commit_pair(cdrain_bar, 0x1);
     mbar_wait_bounded(cdrain_bar, 0, nullptr, args.limit_ns, args.err);
-  } else if (warp == 1 && lane == 0 && leader) {
+  } else if (warp == 1 && leader) {
     // ------------------------------------------------------------ MMA issuer
     int stage = 0;
     uint32_t phase = 0;
@@ -233,10 +240,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint32_t id2 = make_idesc_block_scaled(kFmtMxf4, kFmtMxf4, 256, n, 2);
       const int acc = twin ? local & 1 : 0;
       const uint32_t d_tmem = tmem_base + 128 * acc;
-      if (!wait(tempty_bar(acc), ((twin ? local >> 1 : local) & 1) ^ 1)) break;
+      if (!warp_wait(tempty_bar(acc), ((twin ? local >> 1 : local) & 1) ^ 1)) break;
       tc_fence_after();
       for (int kb = 0; kb < args.num_kb; ++kb) {
-        if (!wait(full_bar(stage), phase) || !wait(sready_bar(stage), phase)) {
+        if (!warp_wait(full_bar(stage), phase) || !warp_wait(sready_bar(stage), phase)) {
           ok = false;
           break;
         }
@@ -245,23 +252,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint64_t adesc = sdesc_k_sw128(sa), bdesc = sdesc_k_sw128(sa + A_BYTES);
         const uint32_t sf = tmem_base + SF_COL0 + SF_SLOT * stage;
         const int words = min(2, kb128 - 2 * kb);
-        for (int j = 0; j < words; ++j) {
-          umma_mxf4_pair(d_tmem, adesc + 4 * j, bdesc + 4 * j, id0, sf + 16 * j,
-                         sf + 32 + 16 * j, (kb | j) != 0);
-          umma_mxf4_pair(d_tmem, adesc + 4 * j + 2, bdesc + 4 * j + 2, id2, sf + 16 * j,
-                         sf + 32 + 16 * j, 1);
+        if (elect_one()) {
+          for (int j = 0; j < words; ++j) {
+            umma_mxf4_pair(d_tmem, adesc + 4 * j, bdesc + 4 * j, id0, sf + 16 * j, sf + 32 + 16 * j,
+                           (kb | j) != 0);
+            umma_mxf4_pair(d_tmem, adesc + 4 * j + 2, bdesc + 4 * j + 2, id2, sf + 16 * j,
+                           sf + 32 + 16 * j, 1);
+          }
+          tc_commit_pair(empty_bar(stage), 0x3);
         }
-        tc_commit_pair(empty_bar(stage), 0x3);
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
         }
       }
       if (!ok) break;
-      tc_commit_pair(tfull_bar(acc), 0x3);
+      if (elect_one()) tc_commit_pair(tfull_bar(acc), 0x3);
       ++local;
     }
-    tc_commit_pair(drain_bar, 0x1);
+    if (elect_one()) tc_commit_pair(drain_bar, 0x1);
     mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
   } else if (warp >= EPI_WARP0) {
     // ------------------------------------------------------------ epilogue
