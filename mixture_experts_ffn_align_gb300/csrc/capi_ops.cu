@@ -55,7 +55,7 @@ size_t ragged_bytes(const moe_ragged* p) {
 
 // Choice of the kernels' form.  A form's time is modelled as rounds of its CTAs
 // (or pairs) times a tile's cycles, the slower of what a step's operands take at
-// the ~50 bytes a cycle that an SM gets from L2 and its MMAs, plus a tile's fixed
+// the ~56 bytes a cycle that an SM gets from L2 and its MMAs, plus a tile's fixed
 // cost, on segments of the average length.  Measured beside the model, in us:
 // dgrad of 774 rows, 8 experts, 6704 -> 2968: one SM 105, pairs 84, double tiles
 // 64; forward of the same: 74, 62, 68; forward of 8240 rows, 8 experts, 4096 ->
@@ -79,11 +79,15 @@ int64_t l2_bytes(int64_t bytes, int64_t pitch_bytes) {
 
 // Forward (w_cols: columns of the output, red: of the reduction) or dgrad.
 // step_deep: 64, or 256 4-bit values, whose 16 KB operand tiles are alike;
-// extra: bytes of scales a step.
+// extra: bytes of scales a step.  Double tiles are taken below double_pct percent
+// of the next best time (0: never): at the power limit dgrad gains less from
+// them than the model says (8192 rows, 8 experts, 28672 -> 4096: 1338 us against
+// 1309 in pairs where forward's are 1244 / 1276), and more where they save a
+// round.
 Form rows_form(const moe_ragged* p, int w_cols, int red, int64_t w_pitch, int64_t x_pitch,
-               int step_deep, int extra, bool may_double) {
+               int step_deep, int extra, int double_pct) {
   const int form = ragged_form();
-  if (form == DOUBLE) return may_double ? DOUBLE : PAIRS;
+  if (form == DOUBLE) return double_pct != 0 ? DOUBLE : PAIRS;
   if (form != 0) return static_cast<Form>(form);
   const int64_t segs = std::min(p->E, p->R), rows = ceil_div(p->R, segs);
   const int64_t per_seg = ceil_div(rows, 256), tok = segs * per_seg;
@@ -93,22 +97,23 @@ Form rows_form(const moe_ragged* p, int w_cols, int red, int64_t w_pitch, int64_
   const int64_t half = n / 2 <= 64 ? ceil_div(n / 2, 32) * 4096 : 16384;
   const int64_t b1 = l2_bytes(n / 32 * 4096, x_pitch) + extra, b2 = l2_bytes(half, x_pitch) + extra;
   const int64_t w1 = ceil_div(w_cols, 128), w2 = ceil_div(w_cols, 256), w4 = ceil_div(w_cols, 512);
+  const int64_t mma = 23 * n / 10;     // 2 n at the tensor cores' full rate
   const int splits = step_deep == 64 ? ragged_rows_splits(p->R, p->E, w_cols, red)
                                      : ragged_mxfp4_splits(p->R, w_cols, red, p->E);
   // 4-bit tiles of more than 128 tokens leave room for one accumulator only; the
   // pairs also read weights a little faster at the same model time
   const bool one_acc = step_deep != 64 && p->R > 64ll * p->E && p->R > 128;
-  const int64_t one = splits > 1 ? tiles_cycles(1, 1, ceil_div(steps, splits), a + b1, 2 * n, 5000)
-                                 : tiles_cycles(tok * w1, kSms, steps, a + b1, 2 * n,
+  const int64_t one = splits > 1 ? tiles_cycles(1, 1, ceil_div(steps, splits), a + b1, mma, 5000)
+                                 : tiles_cycles(tok * w1, kSms, steps, a + b1, mma,
                                                 one_acc ? 4000 : 1200) * 21 / 20;
-  const int64_t two = tiles_cycles(tok * w2, kSms / 2, steps, a + b2, 2 * n, one_acc ? 2000 : 1500);
-  const int64_t dbl = tiles_cycles(tok * w4, kSms / 2, steps, 2 * a + b2, 4 * n, 2500);
+  const int64_t two = tiles_cycles(tok * w2, kSms / 2, steps, a + b2, mma, one_acc ? 2000 : 1500);
+  const int64_t dbl = tiles_cycles(tok * w4, kSms / 2, steps, 2 * a + b2, 2 * mma, 2500);
   // what no form is faster than: the weights from HBM (double tiles have to gain
   // more than their longer end then)
   const int64_t values = segs * w_cols * red;
   const int64_t hbm = (step_deep == 64 ? 2 * values : values / 2) / 3500;
   const int64_t best = std::max(std::min(one, two), hbm);
-  if (may_double && steps >= 16 && std::max(dbl, hbm) < best * 97 / 100) return DOUBLE;
+  if (steps >= 16 && std::max(dbl, hbm) < best * double_pct / 100) return DOUBLE;
   return two <= one && w_cols > 128 ? PAIRS : ONE_SM;
 }
 
@@ -136,7 +141,7 @@ cudaError_t ragged_rows(const moe_ragged* p, int op, const void* rows, const voi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool fwd = op == 0;
   const Form f = rows_form(p, fwd ? p->N : p->K, fwd ? p->K : p->N, 2ll * p->K,
-                           2 * (fwd ? q.ldx : q.ldy), 64, 0, true);
+                           2 * (fwd ? q.ldx : q.ldy), 64, 0, fwd ? 97 : 86);
   return f == ONE_SM ? launch_ragged_rows(q, op, rows, w, bias, out, workspace, st)
                      : launch_ragged_rows_2sm(q, op, f == DOUBLE, rows, w, bias, out, st);
 }
@@ -213,7 +218,7 @@ moe_status ragged_gemm_mxfp4(const moe_ragged* p, const void* x_codes, const voi
   if (p->R == 0) return MOE_OK;
   if (!x_scales || !w_scales_packed || misaligned(x_scales, 4) || misaligned(w_scales_packed, 16))
     return MOE_ERR_INVALID_ARG;
-  const Form f = rows_form(p, p->N, p->K, p->K / 2, p->K / 2, 256, 3072, false);
+  const Form f = rows_form(p, p->N, p->K, p->K / 2, p->K / 2, 256, 3072, 0);
   const auto launch = f == PAIRS ? launch_ragged_mxfp4_2sm : launch_ragged_mxfp4;
   return done(launch(ragged_problem(p, expert_offsets), x_codes,
                      static_cast<const uint8_t*>(x_scales), w_codes, w_scales_packed, y,
