@@ -55,7 +55,7 @@ size_t ragged_bytes(const moe_ragged* p) {
 
 // Choice of the kernels' form.  A form's time is modelled as rounds of its CTAs
 // (or pairs) times a tile's cycles, the slower of what a step's operands take at
-// the ~56 bytes a cycle that an SM gets from L2 and its MMAs, plus a tile's fixed
+// the ~50 bytes a cycle that an SM gets from L2 and its MMAs, plus a tile's fixed
 // cost, on segments of the average length.  Measured beside the model, in us:
 // dgrad of 774 rows, 8 experts, 6704 -> 2968: one SM 105, pairs 84, double tiles
 // 64; forward of the same: 74, 62, 68; forward of 8240 rows, 8 experts, 4096 ->

@@ -365,99 +365,6 @@ bool make_tmap_u8_rows(CUtensorMap* map, const void* base, uint64_t rows, uint64
   return r == CUDA_SUCCESS;
 }
 
-// Tensor map of the ragged products: a 16-bit matrix [d1, d0] (rank 2) or a
-// stack of d2 of them (rank 3), rows ld elements apart, boxes of 64 x box1
-// (x 1) values with 128-byte swizzle; what lies outside reads as zero.  Serves
-// K-major and MN-major operands alike: the MMA's descriptors tell them apart.
-bool make_tmap_rag(CUtensorMap* map, const void* base, bool half, int rank, uint64_t d0,
-                   uint64_t d1, uint64_t d2, uint64_t ld, uint32_t box1) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[3] = {d0, d1, d2};
-  const cuuint64_t strides[2] = {ld * 2, d1 * ld * 2};
-  const cuuint32_t box[3] = {64, box1, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = fn(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                        (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// The same for an MN-major operand whose width is a multiple of 64: [batch,
-// rows, cols] seen as [batch, cols / 64, rows, 64], boxes of 64 x 64 rows x
-// `chunks` chunks, so that one copy brings chunks * 64 columns as consecutive
-// 64 x 64 boxes.
-bool make_tmap_rag_wide(CUtensorMap* map, const void* base, bool half, uint64_t rows,
-                        uint64_t cols, uint64_t batch, uint64_t ld, uint32_t chunks) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr || cols % 64 != 0) return false;
-  const cuuint64_t dims[4] = {64, rows, cols / 64, batch};
-  const cuuint64_t strides[3] = {ld * 2, 128, rows * ld * 2};
-  const cuuint32_t box[4] = {64, 64, chunks, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r = fn(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                        4, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// Tensor map for storing dw [E, N, K] (elem 0 bf16, 1 fp16, 2 fp32; dense): boxes
-// of 128 bytes x 32 rows, 128-byte swizzle.
-bool make_tmap_rag_store(CUtensorMap* map, const void* base, int elem, uint64_t K, uint64_t N,
-                         uint64_t E) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const uint64_t size = elem == 2 ? 4 : 2;
-  const cuuint64_t dims[3] = {K, N, E};
-  const cuuint64_t strides[2] = {K * size, N * K * size};
-  const cuuint32_t box[3] = {(cuuint32_t)(128 / size), 32, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUtensorMapDataType dt = elem == 2   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                 : elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const CUresult r = fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// Tensor map of packed 4-bit values ([d1, d0 / 2] bytes, or d2 of them) for the
-// 4-bit MMA, which reads them packed: boxes of 128 bytes x box1 rows, 128-byte
-// swizzle.
-bool make_tmap_rag_fp4(CUtensorMap* map, const void* base, int rank, uint64_t d0, uint64_t d1,
-                       uint64_t d2, uint32_t box1) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[3] = {d0 / 2, d1, d2};
-  const cuuint64_t strides[2] = {d0 / 2, d1 * (d0 / 2)};
-  const cuuint32_t box[3] = {128, box1, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank,
-                        const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// Tensor map of 512-byte scale blocks ([d1] or [d2, d1] of them) as rows of 128
-// words: boxes of box1 (x box2) blocks, one after the other.
-bool make_tmap_scale_blocks(CUtensorMap* map, const void* base, int rank, uint64_t d1, uint64_t d2,
-                            uint32_t box1, uint32_t box2) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[3] = {128, d1, d2};
-  const cuuint64_t strides[2] = {512, d1 * 512};
-  const cuuint32_t box[3] = {128, box1, box2};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, (cuuint32_t)rank,
-                        const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 cudaError_t launch_ggemm_bf16(const void* A, int cap, int K, const void* B, int b_rows_total,
                               int b_rows_per_expert, int n_out, const int32_t* block_expert_ids,
                               const int32_t* num_post_padded, void* out, bool fuse_act,

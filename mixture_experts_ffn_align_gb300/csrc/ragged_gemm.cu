@@ -4,11 +4,13 @@
 //
 //  * persistent CTAs, one per SM; tiles of 128 weights x up to 256 tokens
 //    (wgrad: 128 rows x 256 columns of one expert's dw);
-//  * warp 0 lane 0: TMA producer into a ring of 64-deep steps.  The token
+//  * warp 0: TMA producer into a ring of 64-deep steps.  The token
 //    operand comes in boxes of 32 rows, only as many as the tile has, so a
 //    decode step (a few rows an expert) moves little beside the weights;
-//  * warp 1 lane 0: tcgen05.mma (M = 128, N = the tile's rows rounded up to 16,
-//    K = 16) into one of two 256-column accumulators;
+//  * warp 1: tcgen05.mma (M = 128, N = the tile's rows rounded up to 16,
+//    K = 16) into one of two 256-column accumulators.  Both warps run their loops
+//    whole and issue from an elected lane: a loop inside a one-lane branch took
+//    some 600 cycles a step to issue four MMAs;
 //  * warps 2-5 (wgrad 2-9): epilogue from the other accumulator.
 //  * dgrad reads w[e] with the reduction along its rows: the same boxes in the
 //    MMA's MN-major form, so no transposed copy of the weights exists.
@@ -24,21 +26,22 @@
 //    of the slices.
 //  * every wait is bounded (wall clock); on a timeout the kernel records the
 //    error, drains its own copies and MMAs, frees tensor memory and returns.
+//
+// Few rows are bound by the weights' bytes: forward of 128 rows to 8 experts,
+// 7168 -> 4096 a projection of 470 MB, runs at HBM's rate (8 experts of 28672 x
+// 4096, 1.88 GB: 289 us, 6.5 TB/s); two rows of one small expert by launch and
+// latency (4.6 us in a graph, 1.5 of them an empty kernel's).  wgrad of segments
+// up to some 200 rows is bound by writing dw, 64 experts of 4096 x 4096 (2.15 GB)
+// at 4096 rows: 3.3 us for each expert's 33.5 MB.
 #include <algorithm>
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
 #include "pdl.cuh"
 #include "ragged.cuh"
+#include "ragged_maps.h"
 
 namespace moe {
-
-bool make_tmap_rag_store(CUtensorMap* map, const void* base, int elem, uint64_t K, uint64_t N,
-                         uint64_t E);
-bool make_tmap_rag_wide(CUtensorMap* map, const void* base, bool half, uint64_t rows,
-                        uint64_t cols, uint64_t batch, uint64_t ld, uint32_t chunks);
-bool make_tmap_rag(CUtensorMap* map, const void* base, bool half, int rank, uint64_t d0,
-                   uint64_t d1, uint64_t d2, uint64_t ld, uint32_t box1);
 
 namespace {
 
@@ -181,8 +184,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
             tail_parity ^= 1u << stage;       // bit: parity of the next use's phase
             tail_mask |= 1u << stage;
           }
-          if (!one) {
-          } else if (OP == RAG_WGRAD) {
+          if (one && OP == RAG_WGRAD) {
             mbar_arrive_expect_tx(bar, A_BYTES + 256 * BK * 2);
             const int r0 = row0 + kb * BK;
             if (args.wide_a) {
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
               for (int j = 0; j < 4; ++j)
                 tma_load_2d(sb + j * 8192, &tmB, bar, V.k_tile * 256 + 64 * j, r0, pol_t);
             }
-          } else {
+          } else if (one) {
             mbar_arrive_expect_tx(bar, A_BYTES + boxes * 32 * BK * 2);
             const int k0 = (kb0 + kb) * BK;
             if (OP == RAG_FWD) {

@@ -8,13 +8,17 @@
 //    the one-SM form for the same work an SM; the tensor core reads the other
 //    half of the tokens from the peer's shared memory.
 //  * six stages a CTA; both CTAs' copies complete on the leader's barrier, the
-//    leader's MMA thread issues M = 256, N = the tile's tokens rounded up to 32,
+//    leader's MMA warp issues M = 256, N = the tile's tokens rounded up to 32,
 //    K = 16 into one of two accumulators, and its commits reach both CTAs.
-//  * each CTA's warps 2-5 drain their own 128 accumulator rows.
+//  * each CTA's epilogue warps drain their own 128 accumulator rows: four, or
+//    eight where a tile has two accumulators' worth of work (double tiles) or its
+//    output goes out through boxes in shared memory (wgrad).
 //  * long segments: two weight tiles together against the same tokens (MT = 2,
-//    512 x up to 256), one in each accumulator.
+//    512 x up to 256), one in each accumulator.  A step then takes in 48 KB for
+//    1024 cycles of MMAs instead of 32 KB for 512: an SM gets some 50 to 56 bytes
+//    a cycle from L2, so single tiles wait for their operands at full clock.
 //  * wgrad's last step of a segment that ends inside the 16 rows of an
-//    instruction: each CTA's copies complete on a barrier of its own, a seventh
+//    instruction: each CTA's copies complete on a barrier of its own, a further
 //    warp zeroes the rows behind the segment and signals the leader's issuer.
 //  * every wait is bounded; the final cluster barrier is reached by both CTAs
 //    after their bounded loops.
@@ -24,15 +28,9 @@
 #include "moe_internal.h"
 #include "pdl.cuh"
 #include "ragged.cuh"
+#include "ragged_maps.h"
 
 namespace moe {
-
-bool make_tmap_rag_store(CUtensorMap* map, const void* base, int elem, uint64_t K, uint64_t N,
-                         uint64_t E);
-bool make_tmap_rag_wide(CUtensorMap* map, const void* base, bool half, uint64_t rows,
-                        uint64_t cols, uint64_t batch, uint64_t ld, uint32_t chunks);
-bool make_tmap_rag(CUtensorMap* map, const void* base, bool half, int rank, uint64_t d0,
-                   uint64_t d1, uint64_t d2, uint64_t ld, uint32_t box1);
 
 namespace {
 
@@ -190,8 +188,7 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
           } else if (one && leader) {
             mbar_arrive_expect_tx(full_bar(stage), 2 * (a_tiles * A_BYTES + b_bytes));
           }
-          if (!one) {
-          } else if (OP == RAG_WGRAD) {
+          if (one && OP == RAG_WGRAD) {
             const int n0 = V.n_tile * 256 + rank * 128, k0 = V.k_tile * 256 + rank * 128;
             const int r0 = row0 + kb * BK;
             if (args.wide_a) {
@@ -206,7 +203,7 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
               tma_load_2d_pair(sb, &tmB, bar, k0, r0, pol_t);
               tma_load_2d_pair(sb + 8192, &tmB, bar, k0 + 64, r0, pol_t);
             }
-          } else {
+          } else if (one) {
             for (int i = 0; i < a_tiles; ++i) {
               const int w0 = (D.w_tile * MT + i) * 256 + rank * 128;
               const uint32_t s_a = sa + i * A_BYTES;

@@ -7,11 +7,11 @@
 // (two values a byte, K = 64 an instruction) and applies both operands' E8M0
 // scales, so the whole reduction stays in one tensor-memory accumulator.
 //
-//  * warp 0 lane 0: TMA producer, a ring of 256-deep steps (128 bytes a row),
+//  * warp 0: TMA producer, a ring of 256-deep steps (128 bytes a row),
 //    and bulk copies of the step's scale operands into a slot of their own
 //    barrier, so the scales' way into tensor memory runs ahead of the codes;
-//  * warp 2 lane 0: copies each slot into tensor memory (tcgen05.cp);
-//  * warp 1 lane 0: MMAs, four of K = 64 a step;
+//  * warp 2: copies each slot into tensor memory (tcgen05.cp);
+//  * warp 1: MMAs, four of K = 64 a step;
 //  * warps 3-6: epilogue.
 //  * Weight scales come packed as moe_mxfp4_pack_scales writes them, 512-byte
 //    blocks of 128 rows x 128 columns in the form tcgen05.cp takes.  The
@@ -28,12 +28,10 @@
 #include "moe_common.cuh"
 #include "moe_internal.h"
 #include "pdl.cuh"
+#include "ragged_maps.h"
 #include "ragged_mx.cuh"
 
 namespace moe {
-
-bool make_tmap_rag_fp4(CUtensorMap* map, const void* base, int rank, uint64_t d0, uint64_t d1,
-                       uint64_t d2, uint32_t box1);
 
 namespace {
 

@@ -21,14 +21,10 @@
 #include "moe_common.cuh"
 #include "moe_internal.h"
 #include "pdl.cuh"
+#include "ragged_maps.h"
 #include "ragged_mx.cuh"
 
 namespace moe {
-
-bool make_tmap_rag_fp4(CUtensorMap* map, const void* base, int rank, uint64_t d0, uint64_t d1,
-                       uint64_t d2, uint32_t box1);
-bool make_tmap_scale_blocks(CUtensorMap* map, const void* base, int rank, uint64_t d1, uint64_t d2,
-                            uint32_t box1, uint32_t box2);
 
 namespace {
 
