@@ -53,23 +53,32 @@ size_t ragged_bytes(const moe_ragged* p) {
   return pad256(b);
 }
 
-// Choice of the kernels' form.  A form's time is modelled as rounds of its CTAs
-// (or pairs) times a tile's cycles, the slower of what a step's operands take at
-// the ~50 bytes a cycle that an SM gets from L2 and its MMAs, plus a tile's fixed
-// cost, on segments of the average length.  Measured beside the model, in us:
-// dgrad of 774 rows, 8 experts, 6704 -> 2968: one SM 105, pairs 84, double tiles
-// 64; forward of the same: 74, 62, 68; forward of 8240 rows, 8 experts, 4096 ->
-// 28672: pairs 1275, double tiles 1193; 100 rows, one expert, 4096 x 4096: one SM
-// in four slices 13, pairs 23; wgrad of 16 experts, 4096 x 4096: one SM / pairs
-// 119 / 125 at 130 rows each, 192 / 158 at 257.
+// Choice of the kernels' form.  A form's time is modelled in rounds of its CTAs
+// (or pairs) on segments of the average length.  A round takes a tile's cycles,
+// which are the slower of what its operands take at the ~50 bytes a cycle that an
+// SM gets from L2 and of its MMAs, and a fixed cost; or, if that is longer, what
+// HBM takes for the round's share of the bytes that are read and written once.
+// The constants are fitted to the three forms' times at 184 products each of
+// forward and dgrad (1 to 128 experts of 1 to 2048 rows): the form taken is 0.3%
+// slower than the best on average.  In us, one SM / pairs / double tiles:
+//   forward, 8 x (28672, 4096): 32 rows each 275 / 287 / 282, 256 351 / 313 / 326;
+//   forward, 8 x (6704, 2968): 128 rows each 79 / 63 / 66, 400 185 / 148 / 124;
+//   dgrad, 8 x (28672, 4096): 32 rows each 269 / 281 / 256, 400 785 / 568 / 569;
+//   dgrad, 8 x (6704, 2968): 32 rows each 66 / 70 / 57, 256 102 / 82 / 72;
+//   forward, 1 x (4096, 4096), one SM in slices: 128 rows 14 / 20 / 26, 400 24 /
+//   21 / 38.
+// wgrad of 16 experts, 4096 x 4096: one SM / pairs 140 / 145 at 130 rows each,
+// 192 / 158 at 257.
 enum Form { ONE_SM = 1, PAIRS = 2, DOUBLE = 3 };
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int kSms = 152, kBytesPerCycle = 50;
 
-// Cycles of `tiles` tiles of `steps` steps on `units` CTAs or pairs.
-int64_t tiles_cycles(int64_t tiles, int64_t units, int64_t steps, int64_t load_bytes,
-                     int64_t mma, int64_t fixed) {
-  return ceil_div(tiles, units) * (steps * std::max(load_bytes / kBytesPerCycle, mma) + fixed);
+// Cycles of `tiles` tiles on `units` CTAs or pairs: a tile's own, or those of its
+// bytes at HBM's bytes a cycle.
+int64_t tiles_cycles(int64_t tiles, int64_t units, int64_t tile, int64_t bytes, int64_t hbm) {
+  const int64_t full = tiles / units, rest = tiles % units;
+  return full * std::max(tile, bytes * units / tiles / hbm) +
+         (rest ? std::max(tile, bytes * rest / tiles / hbm) : 0);
 }
 // Bytes as L2 serves them: rows that do not start on a 32-byte sector cost 1.4
 // times theirs (11592 against 11584 columns: 619 / 417 us).
@@ -79,15 +88,13 @@ int64_t l2_bytes(int64_t bytes, int64_t pitch_bytes) {
 
 // Forward (w_cols: columns of the output, red: of the reduction) or dgrad.
 // step_deep: 64, or 256 4-bit values, whose 16 KB operand tiles are alike;
-// extra: bytes of scales a step.  Double tiles are taken below double_pct percent
-// of the next best time (0: never): at the power limit dgrad gains less from
-// them than the model says (8192 rows, 8 experts, 28672 -> 4096: 1338 us against
-// 1309 in pairs where forward's are 1244 / 1276), and more where they save a
-// round.
+// extra: bytes of scales a step.  hbm, hbm_double: bytes a cycle; dgrad's boxes of
+// the weights are 256 bytes to 1 KB wide in memory against forward's 128 bytes.
 Form rows_form(const moe_ragged* p, int w_cols, int red, int64_t w_pitch, int64_t x_pitch,
-               int step_deep, int extra, int double_pct) {
+               int step_deep, int extra, int hbm, int hbm_double) {
   const int form = ragged_form();
-  if (form == DOUBLE) return double_pct != 0 ? DOUBLE : PAIRS;
+  const bool fp4 = step_deep != 64;
+  if (form == DOUBLE) return fp4 ? PAIRS : DOUBLE;
   if (form != 0) return static_cast<Form>(form);
   const int64_t segs = std::min(p->E, p->R), rows = ceil_div(p->R, segs);
   const int64_t per_seg = ceil_div(rows, 256), tok = segs * per_seg;
@@ -97,23 +104,32 @@ Form rows_form(const moe_ragged* p, int w_cols, int red, int64_t w_pitch, int64_
   const int64_t half = n / 2 <= 64 ? ceil_div(n / 2, 32) * 4096 : 16384;
   const int64_t b1 = l2_bytes(n / 32 * 4096, x_pitch) + extra, b2 = l2_bytes(half, x_pitch) + extra;
   const int64_t w1 = ceil_div(w_cols, 128), w2 = ceil_div(w_cols, 256), w4 = ceil_div(w_cols, 512);
-  const int64_t mma = 23 * n / 10;     // 2 n at the tensor cores' full rate
-  const int splits = step_deep == 64 ? ragged_rows_splits(p->R, p->E, w_cols, red)
-                                     : ragged_mxfp4_splits(p->R, w_cols, red, p->E);
-  // 4-bit tiles of more than 128 tokens leave room for one accumulator only; the
-  // pairs also read weights a little faster at the same model time
-  const bool one_acc = step_deep != 64 && p->R > 64ll * p->E && p->R > 128;
-  const int64_t one = splits > 1 ? tiles_cycles(1, 1, ceil_div(steps, splits), a + b1, mma, 5000)
-                                 : tiles_cycles(tok * w1, kSms, steps, a + b1, mma,
-                                                one_acc ? 4000 : 1200) * 21 / 20;
-  const int64_t two = tiles_cycles(tok * w2, kSms / 2, steps, a + b2, mma, one_acc ? 2000 : 1500);
-  const int64_t dbl = tiles_cycles(tok * w4, kSms / 2, steps, 2 * a + b2, 2 * mma, 2500);
-  // what no form is faster than: the weights from HBM (double tiles have to gain
-  // more than their longer end then)
-  const int64_t values = segs * w_cols * red;
-  const int64_t hbm = (step_deep == 64 ? 2 * values : values / 2) / 3500;
-  const int64_t best = std::max(std::min(one, two), hbm);
-  if (steps >= 16 && std::max(dbl, hbm) < best * double_pct / 100) return DOUBLE;
+  // 2 n at the tensor cores' full rate, and a third more for the clock under power
+  const int64_t mma = 53 * n / 20;
+  const auto step = [&](int64_t bytes, int64_t cycles) {
+    return std::max(bytes / kBytesPerCycle, cycles);
+  };
+  const int64_t values = segs * w_cols * red, io = static_cast<int64_t>(p->R) * (w_cols + red);
+  const int64_t bytes = fp4 ? values * 17 / 32 + io / 2 : 2 * values + io;
+  // 4-bit tiles of more than 128 tokens leave room for one accumulator only
+  const bool one_acc = fp4 && p->R > 64ll * p->E && p->R > 128;
+  const int splits = fp4 ? ragged_mxfp4_splits(p->R, w_cols, red, p->E)
+                         : ragged_rows_splits(p->R, p->E, w_cols, red);
+  int64_t one;
+  if (splits > 1)
+    one = ceil_div(tok * w1 * splits, kSms) *
+          (ceil_div(steps, splits) * step(a + b1, mma) + 4000 + 50 * n);
+  else
+    one = tiles_cycles(tok * w1, kSms, steps * step(a + b1, mma) + (one_acc ? 4000 : 1200), bytes,
+                       hbm) * (fp4 ? 21 : 20) / 20;
+  const int64_t two =
+      tiles_cycles(tok * w2, kSms / 2,
+                   steps * step(a + b2, mma) + (one_acc ? 2000 : fp4 ? 1900 : 1400), bytes, hbm);
+  // both accumulators are drained before the next tile's MMAs
+  const int64_t dbl =
+      tiles_cycles(tok * w4, kSms / 2, steps * step(2 * a + b2, 2 * mma) + 2500 + 24 * n, bytes,
+                   hbm_double);
+  if (!fp4 && steps >= 16 && dbl < std::min(one, two)) return DOUBLE;
   return two <= one && w_cols > 128 ? PAIRS : ONE_SM;
 }
 
@@ -126,11 +142,10 @@ Form wgrad_form(const moe_ragged* p) {
   const int64_t t1 = p->E * ceil_div(p->N, 128) * k, t2 = p->E * ceil_div(p->N, 256) * k;
   // a tile's output: 64 KB a CTA at an SM's share of the HBM rate
   const int64_t out = 2800;
-  const int64_t one =
-      splits > 1 ? tiles_cycles(1, 1, ceil_div(steps, splits), 49152, 512, 8000)
-                 : std::max(tiles_cycles(t1, kSms, steps, 49152, 512, 0), ceil_div(t1, kSms) * out);
-  const int64_t two =
-      std::max(tiles_cycles(t2, kSms / 2, steps, 32768, 512, 0), ceil_div(t2, kSms / 2) * out * 21 / 20);
+  const int64_t load1 = 49152 / kBytesPerCycle, load2 = 32768 / kBytesPerCycle;
+  const int64_t one = splits > 1 ? ceil_div(steps, splits) * load1 + 8000
+                                 : ceil_div(t1, kSms) * std::max(steps * load1, out);
+  const int64_t two = ceil_div(t2, kSms / 2) * std::max(steps * load2, out * 21 / 20);
   return two < one ? PAIRS : ONE_SM;
 }
 
@@ -141,7 +156,7 @@ cudaError_t ragged_rows(const moe_ragged* p, int op, const void* rows, const voi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool fwd = op == 0;
   const Form f = rows_form(p, fwd ? p->N : p->K, fwd ? p->K : p->N, 2ll * p->K,
-                           2 * (fwd ? q.ldx : q.ldy), 64, 0, fwd ? 97 : 86);
+                           2 * (fwd ? q.ldx : q.ldy), 64, 0, fwd ? 3400 : 3600, fwd ? 3400 : 3650);
   return f == ONE_SM ? launch_ragged_rows(q, op, rows, w, bias, out, workspace, st)
                      : launch_ragged_rows_2sm(q, op, f == DOUBLE, rows, w, bias, out, st);
 }
@@ -218,7 +233,7 @@ moe_status ragged_gemm_mxfp4(const moe_ragged* p, const void* x_codes, const voi
   if (p->R == 0) return MOE_OK;
   if (!x_scales || !w_scales_packed || misaligned(x_scales, 4) || misaligned(w_scales_packed, 16))
     return MOE_ERR_INVALID_ARG;
-  const Form f = rows_form(p, p->N, p->K, p->K / 2, p->K / 2, 256, 3072, 0);
+  const Form f = rows_form(p, p->N, p->K, p->K / 2, p->K / 2, 256, 3072, 3400, 0);
   const auto launch = f == PAIRS ? launch_ragged_mxfp4_2sm : launch_ragged_mxfp4;
   return done(launch(ragged_problem(p, expert_offsets), x_codes,
                      static_cast<const uint8_t*>(x_scales), w_codes, w_scales_packed, y,

@@ -497,8 +497,9 @@ static RowsPlan rows_plan(int R, int E, int width, int red) {
   // Slices, by the tiles that even segments make (a 100 x 4096 x 4096 product of
   // one expert: 13 us in four slices, 28 us in one).  The grid and the workspace
   // take the tiles that any segments can make.
+  const int segs = std::max(1, std::min(E, R));
   const long long even =
-      (long long)std::max(std::min(E, R), (R + r.tile_rows - 1) / r.tile_rows) * r.w_tiles;
+      segs * (((R + segs - 1) / segs + r.tile_rows - 1ll) / r.tile_rows) * r.w_tiles;
   r.splits = rag_slices(even, (red + BK - 1) / BK, 8);
   return r;
 }

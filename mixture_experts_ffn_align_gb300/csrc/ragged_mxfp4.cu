@@ -375,7 +375,8 @@ template cudaError_t launch_pack_token_scales<32>(const Mx44Args&, long long, cu
 
 int ragged_mxfp4_splits(int R, int N, int K, int E) {
   const int tr = ragged_mxfp4_tile_rows(R, E);
-  const long long even = (long long)std::max(std::min(E, R), (R + tr - 1) / tr) * (N / 128);
+  const int segs = std::max(1, std::min(E, R));
+  const long long even = segs * (((R + segs - 1) / segs + tr - 1ll) / tr) * (N / 128);
   return rag_slices(even, (K + BK - 1) / BK, 4);
 }
 static size_t scale_bytes(int R, int K, int E) {
