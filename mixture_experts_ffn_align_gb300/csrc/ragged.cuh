@@ -530,7 +530,9 @@ __device__ __forceinline__ void rag_wgrad_epilogue(const RagArgs& a, const CUten
                                                    Release&& release) {
   const int cols = a.out_f32 ? 32 : 64;
   const int width = min(SPAN, a.K - k0);
-  if (width <= 0) {
+  // Nothing of it inside dw.  A box that is not stored must not be filled either:
+  // the wait below counts the warp's stores, one for each turn.
+  if (width <= 0 || n0 >= a.N) {
     release();
     return;
   }
@@ -585,7 +587,7 @@ __device__ __forceinline__ void rag_wgrad_epilogue(const RagArgs& a, const CUten
                    : "memory");
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0 && n0 < a.N)
+    if (lane == 0)
       tma_store_3d(tmD, box, k0 + c, n0, e, a.accumulate && a.out_f32);
   }
 }

@@ -166,6 +166,30 @@ def test_wgrad_accumulates(dw_type, counts):
     assert bool((dw[1] == start[1]).all())
 
 
+@pytest.mark.parametrize("n, k, experts", [(296, 12536, 29), (1984, 14104, 4), (1040, 5840, 60)])
+@pytest.mark.parametrize("dw_type", [None, torch.float32])
+def test_wgrad_tiles_past_the_last_row(n, k, experts, dw_type):
+    """Many short tiles a CTA in turn, some with rows past N, at HBM's pace: what
+    is not stored of one must not touch the stores of the one before that are still
+    on their way.  Small integers: every value is exact."""
+    counts = [(5 * e + 1) % 31 for e in range(experts)]
+    off = offsets_of(counts)
+    rows = int(off[-1])
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x, dy = (torch.randint(-4, 5, (rows, c), generator=g, device="cuda").bfloat16() for c in (k, n))
+    p = moe.Ragged(R=rows, N=n, K=k, E=experts)
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+    ws = torch.empty(moe.moe_ragged_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    dw = torch.empty((experts, n, k), dtype=dw_type or torch.bfloat16, device="cuda")
+    for _ in range(3):
+        dw.fill_(7.0)
+        moe.ragged_gemm_wgrad(p, dy, x, o, dw, ws)
+        assert moe.moe_sync_status() == 0
+        for e in range(experts):
+            ref = dy[off[e]:off[e + 1]].double().T @ x[off[e]:off[e + 1]].double()
+            assert bool((dw[e] == ref.to(dw.dtype)).all()), f"expert {e}"
+
+
 def test_other_rows_cannot_leak():
     """Infinities and NaN in another expert's rows, in rows of no expert and in
     the columns behind a strided row stay there."""
