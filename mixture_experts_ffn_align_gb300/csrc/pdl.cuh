@@ -6,6 +6,11 @@
 //
 // Every thread block of every such kernel executes griddep_wait, so the
 // completion of one implies that of all kernels before it.
+//
+// Kernels of clusters keep the ordinary order, before and after: on SM pairs, and
+// while their tail waits (ragged_gemm_2sm.cu) were missing too, about one in
+// 10,000 launches did not end, and no overlap is worth that.  They are the long
+// ones, which gain 2 of some hundred microseconds.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -23,25 +28,28 @@ __device__ __forceinline__ void griddep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Launches kernel<<<grid, block, smem, stream>>>(args...) with that permission;
-// cluster: CTAs of a cluster along x.
+// Launches kernel<<<grid, block, smem, stream>>>(args...) with that permission,
+// or, cluster > 1, in the ordinary order and with clusters of so many CTAs along x.
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
                              cudaStream_t stream, unsigned cluster, A&&... args) {
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[1];
+  if (cluster > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(block, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, P(std::forward<A>(args))...);
 }
 

@@ -158,6 +158,7 @@ __device__ __forceinline__ RagSched rag_sched_build(const RagArgs& a, int* mem, 
     if (bad && blockIdx.x == 0) set_dev_error(a.err, kDevErrBadIndex);
   }
   fence_proxy_async_smem();   // scratch lies where TMA writes next
+  __syncwarp();
   __syncthreads();
   RagSched s;
   s.tile0 = tile0;
@@ -344,6 +345,16 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(p));
   return p != 0;
+}
+
+// All threads of the cluster.  A role's bounded waits let the lanes of a warp go
+// on one by one, and nothing brings them together again at the end of a role, so
+// neither half may be the .aligned form, which counts a warp once for each group
+// of lanes that reaches it.
+__device__ __forceinline__ void rag_cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // fp32 <-> the operands' 16-bit types.

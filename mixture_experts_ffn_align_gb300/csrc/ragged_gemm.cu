@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   auto tail_bar = [&](int s) { return bar_base + 8u * (2 * MAX_STAGES + 5 + s); };
   auto zeroed_bar = [&](int s) { return bar_base + 8u * (3 * MAX_STAGES + 5 + s); };
 
-  griddep_launch();
+  if (args.splits == 1) griddep_launch();      // (pdl.cuh)
   if (threadIdx.x == 0) {
     for (int s = 0; s < MAX_STAGES; ++s) {
       mbar_init(full_bar(s), 1);
@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     tmem_alloc(smem_u32(tmem_holder), TMEM_COLS);
     tmem_relinquish();
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
       }
       if (!ok) break;
     }
-    for (int s = 0; s < stages; ++s) {
+    for (int s = 0; lane == 0 && s < stages; ++s) {
       if (issued_mask & (1u << s))
         mbar_wait_bounded(full_bar(s), (issued_parity >> s) & 1, nullptr, args.limit_ns, args.err);
       if (tail_mask & (1u << s))
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
       ++local;
     }
     if (elect_one()) tc_commit(drain_bar);
-    mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+    if (lane == 0) mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
   } else if (OP == RAG_WGRAD && warp == 2 + epi_warps(OP)) {
     // ------------------------------------------------------------ zeroing warp
     int stage = 0;
@@ -396,6 +397,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
     if (OP == RAG_WGRAD && lane == 0) tma_store_wait_all();
   }
 
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   }
   if (splits > 1) {
     // join: the cluster's sums are in the workspace
-    cluster_sync();
+    rag_cluster_sync();
     constexpr int WARPS = num_threads(OP) / 32;
     if (OP == RAG_WGRAD && first < total) {
       // a lane takes eight columns of a row

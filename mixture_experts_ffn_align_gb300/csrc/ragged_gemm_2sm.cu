@@ -21,7 +21,9 @@
 //    instruction: each CTA's copies complete on a barrier of its own, a further
 //    warp zeroes the rows behind the segment and signals the leader's issuer.
 //  * every wait is bounded; the final cluster barrier is reached by both CTAs
-//    after their bounded loops.
+//    after their bounded loops, and after tail waits for every signal that the
+//    peer sends to a barrier of this CTA: one that arrives at a CTA that has ended
+//    is lost, or keeps its sender from ending.
 #include <algorithm>
 
 #include "moe_common.cuh"
@@ -87,7 +89,6 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
   auto tempty_bar = [&](int a) { return bar_base + 8u * (4 * STAGES + 2 + a); };
   const uint32_t drain_bar = bar_base + 8u * (4 * STAGES + 4);
 
-  griddep_launch();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 3 * STAGES; ++s) mbar_init(bar_base + 8u * s, 1);
     for (int s = 0; s < STAGES; ++s) mbar_init(zeroed_bar(s), 2);   // one warp of each CTA
@@ -109,13 +110,13 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
     tmem_alloc_pair(smem_u32(tmem_holder), TMEM_COLS);
     tmem_relinquish_pair();
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();        // both CTAs' barriers exist before any cross-CTA signal
+  rag_cluster_sync();        // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  griddep_wait();
   const RagSched sched = rag_sched_build<32>(args, s_sched, reinterpret_cast<int*>(smem));
   const int2* s_rows = OP == RAG_WGRAD
                            ? rag_rows_by_expert(sched, args.E, s_sched, reinterpret_cast<int2*>(smem))
@@ -232,9 +233,13 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
       }
       if (!ok) break;
     }
+    // tail wait: the leader's commits signal this CTA's barriers, and nothing else
+    // waits for the last ones; they have to land before the CTA ends
+    for (int s = 0; lane == 0 && s < STAGES; ++s)
+      if ((issued_mask & (1u << s)) && !wait(empty_bar(s), (issued_parity >> s) & 1)) break;
     // the leader's barrier counts both CTAs' copies: once its issued phases
     // (and the own barrier's) complete, every copy has landed
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; lane == 0 && s < STAGES; ++s) {
       if (leader && (issued_mask & (1u << s)))
         mbar_wait_bounded(full_bar(s), (issued_parity >> s) & 1, nullptr, args.limit_ns, args.err);
       if (tail_mask & (1u << s))
@@ -339,7 +344,14 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
       ++local;
     }
     if (elect_one()) tc_commit_pair(drain_bar, 0x1);
-    mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+    if (lane == 0) {
+      mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+      // tail wait: for the last signals of both CTAs' epilogues
+      for (int a = 0; a < 2; ++a) {
+        const int uses = MT == 1 ? (local + 1 - a) >> 1 : a == 0 ? local : second;
+        if (uses > 0 && !wait(tempty_bar(a), (uses - 1) & 1)) break;
+      }
+    }
   } else if (OP == RAG_WGRAD && warp == 2 + EPI_WARPS) {
     // ------------------------------------------------------------ zeroing warp
     // As soon as the copies of a segment's last step have landed in this CTA,
@@ -467,6 +479,7 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
     if (OP == RAG_WGRAD && lane == 0) tma_store_wait_all();
   }
 
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) {
@@ -476,7 +489,7 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
     while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
   }
   __syncthreads();
-  cluster_sync();
+  rag_cluster_sync();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();

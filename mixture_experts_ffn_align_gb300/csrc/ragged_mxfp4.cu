@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t drain_bar = bar_base + 8u * (4 * STAGES + 4);
   const uint32_t cdrain_bar = bar_base + 8u * (4 * STAGES + 5);
 
-  griddep_launch();
+  if (args.splits == 1) griddep_launch();      // (pdl.cuh)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 4 * STAGES; ++s) mbar_init(bar_base + 8u * s, 1);
     for (int a = 0; a < 2; ++a) {
@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc(smem_u32(tmem_holder), TMEM_COLS);
     tmem_relinquish();
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
     }
-    for (int s = 0; s < STAGES; ++s)
+    for (int s = 0; lane == 0 && s < STAGES; ++s)
       if (issued_mask & (1u << s)) {
         mbar_wait_bounded(full_bar(s), (issued_parity >> s) & 1, nullptr, args.limit_ns, args.err);
         mbar_wait_bounded(sfull_bar(s), (issued_parity >> s) & 1, nullptr, args.limit_ns, args.err);
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
     if (elect_one()) tc_commit(cdrain_bar);
-    mbar_wait_bounded(cdrain_bar, 0, nullptr, args.limit_ns, args.err);
+    if (lane == 0) mbar_wait_bounded(cdrain_bar, 0, nullptr, args.limit_ns, args.err);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     int stage = 0;
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ++local;
     }
     if (elect_one()) tc_commit(drain_bar);
-    mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+    if (lane == 0) mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
   } else if (warp >= 3) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
@@ -328,6 +329,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   }
 
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
   if (splits > 1) {
-    cluster_sync();       // the cluster's sums are in the workspace
+    rag_cluster_sync();       // the cluster's sums are in the workspace
     if (first < total)
       rag_join_tokens<T, false>(args, rag_tile<16>(sched, args, first), first, rank, warp,
                                 NUM_THREADS / 32, lane);

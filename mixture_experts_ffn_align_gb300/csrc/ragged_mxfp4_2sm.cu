@@ -86,7 +86,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t drain_bar = bar_base + 8u * (4 * STAGES + 4);
   const uint32_t cdrain_bar = bar_base + 8u * (4 * STAGES + 5);
 
-  griddep_launch();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 4 * STAGES; ++s) mbar_init(bar_base + 8u * s, 1);
     for (int a = 0; a < 2; ++a) {
@@ -109,13 +108,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc_pair(smem_u32(tmem_holder), TMEM_COLS);
     tmem_relinquish_pair();
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();        // both CTAs' barriers exist before any cross-CTA signal
+  rag_cluster_sync();        // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  griddep_wait();
   const RagSched sched = rag_sched_build<32>(args, s_sched, reinterpret_cast<int*>(smem));
   const int total = sched.tile0[sched.nseg] * args.w_tiles.d;
   const int kb128 = margs.K / 128;
@@ -184,9 +183,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
     }
+    // tail wait, as in ragged_gemm_2sm.cu
+    for (int s = 0; lane == 0 && s < STAGES; ++s)
+      if ((issued_mask & (1u << s)) && !wait(empty_bar(s), (issued_parity >> s) & 1)) break;
     // the leader's barriers count both CTAs' copies
     if (leader)
-      for (int s = 0; s < STAGES; ++s)
+      for (int s = 0; lane == 0 && s < STAGES; ++s)
         if (issued_mask & (1u << s)) {
           mbar_wait_bounded(full_bar(s), (issued_parity >> s) & 1, nullptr, args.limit_ns, args.err);
           mbar_wait_bounded(sfull_bar(s), (issued_parity >> s) & 1, nullptr, args.limit_ns,
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
     if (elect_one()) tc_commit_pair(cdrain_bar, 0x1);
-    mbar_wait_bounded(cdrain_bar, 0, nullptr, args.limit_ns, args.err);
+    if (lane == 0) mbar_wait_bounded(cdrain_bar, 0, nullptr, args.limit_ns, args.err);
   } else if (warp == 1 && leader) {
     // ------------------------------------------------------------ MMA issuer
     int stage = 0;
@@ -267,7 +269,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ++local;
     }
     if (elect_one()) tc_commit_pair(drain_bar, 0x1);
-    mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+    if (lane == 0) {
+      mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+      for (int a = 0; a < 2; ++a) {
+        const int uses = twin ? (local + 1 - a) >> 1 : a == 0 ? local : 0;
+        if (uses > 0 && !wait(tempty_bar(a), (uses - 1) & 1)) break;
+      }
+    }
   } else if (warp >= EPI_WARP0) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - EPI_WARP0) >> 2;   // 128 of the 256 columns
@@ -308,6 +316,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   }
 
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) {
@@ -317,7 +326,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
   }
   __syncthreads();
-  cluster_sync();
+  rag_cluster_sync();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();

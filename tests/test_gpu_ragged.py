@@ -190,6 +190,27 @@ def test_wgrad_tiles_past_the_last_row(n, k, experts, dw_type):
             assert bool((dw[e] == ref.to(dw.dtype)).all()), f"expert {e}"
 
 
+def test_many_lone_calls_end():
+    """Calls that find the GPU idle, one after another: none may wait for a signal
+    that was lost at the end of the one before."""
+    p = moe.Ragged(R=24, N=1080, K=456, E=40)
+    off = [min(24, e) for e in range(41)]
+    x, dy, w = (torch.ones(s, dtype=torch.bfloat16, device="cuda")
+                for s in ((24, 456), (24, 1080), (40, 1080, 456)))
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+    ws = torch.empty(moe.moe_ragged_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    y, dx, dw = torch.empty_like(dy), torch.empty_like(x), torch.empty_like(w)
+    for _ in range(300):
+        y.fill_(0.0)
+        moe.ragged_gemm(p, x, w, o, y, ws)
+        torch.cuda.synchronize()
+        moe.ragged_gemm_dgrad(p, dy, w, o, dx, ws)
+        moe.ragged_gemm_wgrad(p, dy, x, o, dw, ws)
+        torch.cuda.synchronize()
+    assert moe.moe_sync_status() == 0
+    assert bool((y == 456).all()) and bool((dx == 1080).all()) and bool((dw[:24] == 1).all())
+
+
 def test_other_rows_cannot_leak():
     """Infinities and NaN in another expert's rows, in rows of no expert and in
     the columns behind a strided row stay there."""
