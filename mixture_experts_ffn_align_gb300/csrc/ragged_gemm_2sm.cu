@@ -554,8 +554,9 @@ bool common(const RaggedProblem& p, RagArgs& a) {
 // double_tiles: a CTA then takes in 24 KB a tile and step instead of 32, which
 // counts where the pairs run at the rate L2 feeds them (or at the power limit);
 // but both accumulators are in use until a tile ends, so it costs the time to
-// read them, about 1000 cycles against 1024 a step.  1030 rows an expert, 8
-// experts, 4096 -> 28672: 1275 -> 1193 us (dgrad in a long run: 1372 -> 1276).
+// read them, 2500 to 8000 cycles.  Pairs / double tiles, 8 experts of 1030 rows:
+// 4096 -> 28672 forward 1211 / 1185 us, of 128 rows: 6704 -> 2968 dgrad 77 / 62;
+// 8192 rows, 4096 -> 14336 forward 518 / 559.
 cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, bool double_tiles,
                                    const void* rows, const void* w,
                                    const void* bias, void* out,
