@@ -115,20 +115,27 @@ Form rows_form(const moe_ragged* p, int w_cols, int red, int64_t w_pitch, int64_
   const bool one_acc = fp4 && p->R > 64ll * p->E && p->R > 128;
   const int splits = fp4 ? ragged_mxfp4_splits(p->R, w_cols, red, p->E)
                          : ragged_rows_splits(p->R, p->E, w_cols, red);
+  // What they were fitted on started while the kernel before ended; kernels of
+  // clusters no longer do (515 rows, 16 experts, 1032 -> 776: one SM 9.6, pairs
+  // 12.4).  Few rows stream from HBM a little faster on one SM, more rows on pairs.
+  const int64_t launch = fp4 ? 0 : 3000;
+  const int64_t hbm_one = fp4 || n <= 64 ? hbm : hbm * 23 / 25;
+  const int64_t hbm_two = fp4 || n > 64 ? hbm : hbm * 97 / 100;
   int64_t one;
   if (splits > 1)
     one = ceil_div(tok * w1 * splits, kSms) *
-          (ceil_div(steps, splits) * step(a + b1, mma) + 4000 + 50 * n);
+              (ceil_div(steps, splits) * step(a + b1, mma) + 4000 + 50 * n) + launch;
   else
     one = tiles_cycles(tok * w1, kSms, steps * step(a + b1, mma) + (one_acc ? 4000 : 1200), bytes,
-                       hbm) * (fp4 ? 21 : 20) / 20;
+                       hbm_one) * (fp4 ? 21 : 20) / 20;
   const int64_t two =
       tiles_cycles(tok * w2, kSms / 2,
-                   steps * step(a + b2, mma) + (one_acc ? 2000 : fp4 ? 1900 : 1400), bytes, hbm);
+                   steps * step(a + b2, mma) + (one_acc ? 2000 : fp4 ? 1900 : 1400), bytes,
+                   hbm_two) + launch;
   // both accumulators are drained before the next tile's MMAs
   const int64_t dbl =
       tiles_cycles(tok * w4, kSms / 2, steps * step(2 * a + b2, 2 * mma) + 2500 + 24 * n, bytes,
-                   hbm_double);
+                   hbm_double) + launch;
   if (!fp4 && steps >= 16 && dbl < std::min(one, two)) return DOUBLE;
   return two <= one && w_cols > 128 ? PAIRS : ONE_SM;
 }
