@@ -88,8 +88,9 @@ int64_t l2_bytes(int64_t bytes, int64_t pitch_bytes) {
 
 // Forward (w_cols: columns of the output, red: of the reduction) or dgrad.
 // step_deep: 64, or 256 4-bit values, whose 16 KB operand tiles are alike;
-// extra: bytes of scales a step.  hbm, hbm_double: bytes a cycle; dgrad's boxes of
-// the weights are 256 bytes to 1 KB wide in memory against forward's 128 bytes.
+// extra: bytes of scales a step.  hbm, hbm_double: bytes a cycle (hbm_double unused
+// for 4-bit operands); dgrad's boxes of the weights are 256 bytes to 1 KB wide in
+// memory against forward's 128 bytes.
 Form rows_form(const moe_ragged* p, int w_cols, int red, int64_t w_pitch, int64_t x_pitch,
                int step_deep, int extra, int hbm, int hbm_double) {
   const int form = ragged_form();
@@ -132,11 +133,13 @@ Form rows_form(const moe_ragged* p, int w_cols, int red, int64_t w_pitch, int64_
       tiles_cycles(tok * w2, kSms / 2,
                    steps * step(a + b2, mma) + (one_acc ? 2000 : fp4 ? 1900 : 1400), bytes,
                    hbm_two) + launch;
-  // both accumulators are drained before the next tile's MMAs
-  const int64_t dbl =
-      tiles_cycles(tok * w4, kSms / 2, steps * step(2 * a + b2, 2 * mma) + 2500 + 24 * n, bytes,
-                   hbm_double) + launch;
-  if (!fp4 && steps >= 16 && dbl < std::min(one, two)) return DOUBLE;
+  if (!fp4 && steps >= 16) {   // no double tiles of 4-bit operands, and no rate for them
+    // both accumulators are drained before the next tile's MMAs
+    const int64_t dbl =
+        tiles_cycles(tok * w4, kSms / 2, steps * step(2 * a + b2, 2 * mma) + 2500 + 24 * n, bytes,
+                     hbm_double) + launch;
+    if (dbl < std::min(one, two)) return DOUBLE;
+  }
   return two <= one && w_cols > 128 ? PAIRS : ONE_SM;
 }
 
