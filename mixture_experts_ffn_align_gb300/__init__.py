@@ -421,6 +421,18 @@ def _rows(name: str, t, shape, dtype, ld) -> int:
     _fail(name, t, shape, dtype, ld)
 
 
+def _row_stride(name: str, t) -> int:
+    """Row stride that a matrix argument brings itself.  An expanded row's is 0,
+    which the C entry points take for "dense"."""
+    rows, cols = t.shape
+    if rows <= 1:
+        return cols
+    ld = t.stride(0)
+    if ld < cols:
+        raise ValueError(f"rows of {name} must not overlap (stride {ld} for {cols} columns)")
+    return ld
+
+
 def _bytes(name: str, t):
     """Data pointer and size of a dense GPU buffer of any type."""
     if t.is_cuda and t.is_contiguous():
@@ -499,7 +511,7 @@ def moe_mxfp4_quantize(x, codes, scales, scale_mode="floor", stream=None):
     """E2M1 codes (uint8 [rows, K/2]) and E8M0 scales (uint8 [rows, K/32]) of
     x [rows, K] (bfloat16, float16 or float32; rows may lie apart)."""
     rows, K = x.shape
-    ld = x.stride(0) if rows > 1 else K
+    ld = _row_stride("x", x)
     _check(lib().moe_mxfp4_quantize(
         _rows("x", x, (rows, K), x.dtype, ld), _float_code("x", x), rows, K, ld,
         MXFP4_SCALE[scale_mode], _dense("codes", codes, (rows, K // 2), _t().uint8),
@@ -510,7 +522,7 @@ def moe_mxfp4_quantize(x, codes, scales, scale_mode="floor", stream=None):
 def moe_mxfp4_dequantize(codes, scales, out, stream=None):
     """out [rows, K] (bfloat16, float16 or float32) = value * 2^(scale - 127)."""
     rows, K = out.shape
-    ld = out.stride(0) if rows > 1 else K
+    ld = _row_stride("out", out)
     _check(lib().moe_mxfp4_dequantize(
         _dense("codes", codes, (rows, K // 2), _t().uint8),
         _dense("scales", scales, (rows, K // 32), _t().uint8), rows, K,
