@@ -393,10 +393,12 @@ def fused_experts_from_host(p: Problem, host_x, host_topk_ids, host_topk_weights
 # The checks below run on every call of kernels that take a few microseconds:
 # each tests everything in one expression and looks for the reason only when
 # it fails.
-def _fail(name: str, t, shape, dtype, stride):
+def _fail(name: str, t, shape, dtype, stride, dev):
     """Raises for a tensor argument that is not as the call needs it."""
-    if not t.is_cuda:
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be on the GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, not cuda:{t.get_device()}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
@@ -406,19 +408,30 @@ def _fail(name: str, t, shape, dtype, stride):
     raise ValueError(f"{name} must be dense")
 
 
-def _dense(name: str, t, shape, dtype) -> int:
-    """Data pointer of a dense GPU tensor of this shape and type."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+def _device(name: str, t) -> int:
+    """GPU of a call's leading tensor, which the others have to share.  The
+    library launches on the current one."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be on the GPU")
+    if dev != _t().device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_t().device()}")
+    return dev
+
+
+def _dense(name: str, t, shape, dtype, dev) -> int:
+    """Data pointer of a dense tensor of this shape and type on GPU dev."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
-    _fail(name, t, shape, dtype, None)
+    _fail(name, t, shape, dtype, None, dev)
 
 
-def _rows(name: str, t, shape, dtype, ld) -> int:
-    """Data pointer of a GPU matrix whose rows lie ld elements apart."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and (
+def _rows(name: str, t, shape, dtype, ld, dev) -> int:
+    """Data pointer of a matrix on GPU dev whose rows lie ld elements apart."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and (
             t.stride() == (ld, 1) or shape[0] <= 1 and t.stride(1) == 1):
         return t.data_ptr()
-    _fail(name, t, shape, dtype, ld)
+    _fail(name, t, shape, dtype, ld, dev)
 
 
 def _row_stride(name: str, t) -> int:
@@ -433,17 +446,17 @@ def _row_stride(name: str, t) -> int:
     return ld
 
 
-def _bytes(name: str, t):
-    """Data pointer and size of a dense GPU buffer of any type."""
-    if t.is_cuda and t.is_contiguous():
+def _bytes(name: str, t, dev):
+    """Data pointer and size of a dense buffer of any type on GPU dev."""
+    if t.get_device() == dev and t.is_contiguous():
         return t.data_ptr(), t.numel() * t.element_size()
-    _fail(name, t, None, None, None)
+    _fail(name, t, None, None, None, dev)
 
 
-def _raw_stream(stream, t) -> int:
-    """The stream given, or PyTorch's current one on t's device."""
+def _raw_stream(stream, dev) -> int:
+    """The stream given, or PyTorch's current one on GPU dev."""
     if stream is None:
-        return _t().raw_stream(t.get_device())
+        return _t().raw_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -455,22 +468,24 @@ def ragged_gemm(p: Ragged, x, w, expert_offsets, y, workspace, bias=None, stream
     """y[r] = W_e x[r] (+ bias_e) for the rows r of each expert e; x [R, K],
     w [E, N, K], y [R, N], bias [E, N], expert_offsets int32 [E + 1]."""
     v = p._v
-    ws, n = _bytes("workspace", workspace)
+    dev = _device("x", x)
+    ws, n = _bytes("workspace", workspace, dev)
     _check(lib().ragged_gemm(
-        p._ref, _rows("x", x, v.x, v.dtype, v.ldx), _dense("w", w, v.w, v.dtype),
-        None if bias is None else _dense("bias", bias, v.bias, v.dtype),
-        _dense("expert_offsets", expert_offsets, v.offsets, v.int32),
-        _rows("y", y, v.y, v.dtype, v.ldy), ws, n, _raw_stream(stream, x)), "ragged_gemm")
+        p._ref, _rows("x", x, v.x, v.dtype, v.ldx, dev), _dense("w", w, v.w, v.dtype, dev),
+        None if bias is None else _dense("bias", bias, v.bias, v.dtype, dev),
+        _dense("expert_offsets", expert_offsets, v.offsets, v.int32, dev),
+        _rows("y", y, v.y, v.dtype, v.ldy, dev), ws, n, _raw_stream(stream, dev)), "ragged_gemm")
 
 
 def ragged_gemm_dgrad(p: Ragged, dy, w, expert_offsets, dx, workspace, stream=None):
     """dx[r] = W_e^T dy[r]: the gradient of ragged_gemm's x."""
     v = p._v
-    ws, n = _bytes("workspace", workspace)
+    dev = _device("dy", dy)
+    ws, n = _bytes("workspace", workspace, dev)
     _check(lib().ragged_gemm_dgrad(
-        p._ref, _rows("dy", dy, v.y, v.dtype, v.ldy), _dense("w", w, v.w, v.dtype),
-        _dense("expert_offsets", expert_offsets, v.offsets, v.int32),
-        _rows("dx", dx, v.x, v.dtype, v.ldx), ws, n, _raw_stream(stream, dy)),
+        p._ref, _rows("dy", dy, v.y, v.dtype, v.ldy, dev), _dense("w", w, v.w, v.dtype, dev),
+        _dense("expert_offsets", expert_offsets, v.offsets, v.int32, dev),
+        _rows("dx", dx, v.x, v.dtype, v.ldx, dev), ws, n, _raw_stream(stream, dev)),
         "ragged_gemm_dgrad")
 
 
@@ -480,13 +495,14 @@ def ragged_gemm_wgrad(p: Ragged, dy, x, expert_offsets, dw, workspace, accumulat
     ragged_gemm's w, in the operands' type or float32 (dw's)."""
     v = p._v
     f32 = dw.dtype is v.float32
-    ws, n = _bytes("workspace", workspace)
+    dev = _device("dy", dy)
+    ws, n = _bytes("workspace", workspace, dev)
     _check(lib().ragged_gemm_wgrad(
-        p._ref, _rows("dy", dy, v.y, v.dtype, v.ldy), _rows("x", x, v.x, v.dtype, v.ldx),
-        _dense("expert_offsets", expert_offsets, v.offsets, v.int32),
-        _dense("dw", dw, v.w, v.float32 if f32 else v.dtype),
+        p._ref, _rows("dy", dy, v.y, v.dtype, v.ldy, dev), _rows("x", x, v.x, v.dtype, v.ldx, dev),
+        _dense("expert_offsets", expert_offsets, v.offsets, v.int32, dev),
+        _dense("dw", dw, v.w, v.float32 if f32 else v.dtype, dev),
         DTYPE["float32"] if f32 else DTYPE[p.dtype], 1 if accumulate else 0, ws, n,
-        _raw_stream(stream, dy)), "ragged_gemm_wgrad")
+        _raw_stream(stream, dev)), "ragged_gemm_wgrad")
 
 
 @cache
@@ -495,7 +511,7 @@ def _t():
     import torch
     return SimpleNamespace(
         uint8=torch.uint8, float32=torch.float32, Tensor=torch.Tensor,
-        raw_stream=torch._C._cuda_getCurrentRawStream,
+        raw_stream=torch._C._cuda_getCurrentRawStream, device=torch._C._cuda_getDevice,
         code={getattr(torch, k): v for k, v in DTYPE.items()})
 
 
@@ -511,34 +527,35 @@ def moe_mxfp4_quantize(x, codes, scales, scale_mode="floor", stream=None):
     """E2M1 codes (uint8 [rows, K/2]) and E8M0 scales (uint8 [rows, K/32]) of
     x [rows, K] (bfloat16, float16 or float32; rows may lie apart)."""
     rows, K = x.shape
-    ld = _row_stride("x", x)
+    ld, dev = _row_stride("x", x), _device("x", x)
     _check(lib().moe_mxfp4_quantize(
-        _rows("x", x, (rows, K), x.dtype, ld), _float_code("x", x), rows, K, ld,
-        MXFP4_SCALE[scale_mode], _dense("codes", codes, (rows, K // 2), _t().uint8),
-        _dense("scales", scales, (rows, K // 32), _t().uint8), _raw_stream(stream, x)),
+        _rows("x", x, (rows, K), x.dtype, ld, dev), _float_code("x", x), rows, K, ld,
+        MXFP4_SCALE[scale_mode], _dense("codes", codes, (rows, K // 2), _t().uint8, dev),
+        _dense("scales", scales, (rows, K // 32), _t().uint8, dev), _raw_stream(stream, dev)),
         "moe_mxfp4_quantize")
 
 
 def moe_mxfp4_dequantize(codes, scales, out, stream=None):
     """out [rows, K] (bfloat16, float16 or float32) = value * 2^(scale - 127)."""
     rows, K = out.shape
-    ld = _row_stride("out", out)
+    ld, dev = _row_stride("out", out), _device("out", out)
     _check(lib().moe_mxfp4_dequantize(
-        _dense("codes", codes, (rows, K // 2), _t().uint8),
-        _dense("scales", scales, (rows, K // 32), _t().uint8), rows, K,
-        _rows("out", out, (rows, K), out.dtype, ld), _float_code("out", out), ld,
-        _raw_stream(stream, out)), "moe_mxfp4_dequantize")
+        _dense("codes", codes, (rows, K // 2), _t().uint8, dev),
+        _dense("scales", scales, (rows, K // 32), _t().uint8, dev), rows, K,
+        _rows("out", out, (rows, K), out.dtype, ld, dev), _float_code("out", out), ld,
+        _raw_stream(stream, dev)), "moe_mxfp4_dequantize")
 
 
 def moe_mxfp4_pack_scales(scales, packed, stream=None):
     """Weight scales (uint8 [E, N, K/32]) in the block form that
     ragged_gemm_mxfp4 reads; packed has as many bytes."""
     E, N, G = scales.shape
-    src = _dense("scales", scales, (E, N, G), _t().uint8)
-    dst = _dense("packed", packed, packed.shape, _t().uint8)
+    dev = _device("scales", scales)
+    src = _dense("scales", scales, (E, N, G), _t().uint8, dev)
+    dst = _dense("packed", packed, packed.shape, _t().uint8, dev)
     if packed.numel() != scales.numel():
         raise ValueError("packed must have as many bytes as scales")
-    _check(lib().moe_mxfp4_pack_scales(src, E, N, 32 * G, dst, _raw_stream(stream, scales)),
+    _check(lib().moe_mxfp4_pack_scales(src, E, N, 32 * G, dst, _raw_stream(stream, dev)),
            "moe_mxfp4_pack_scales")
 
 
@@ -546,34 +563,38 @@ def ragged_gemm_mxfp4(p: Ragged, x_codes, x_scales, w_codes, w_scales_packed, ex
                       workspace, stream=None):
     """y[r] = W_e x[r] with both operands in MXFP4; p.dtype is y's."""
     v = p._v
-    packed, have = _bytes("w_scales_packed", w_scales_packed)
+    dev = _device("x_codes", x_codes)
+    packed, have = _bytes("w_scales_packed", w_scales_packed, dev)
     if have != v.packed:
         raise ValueError("w_scales_packed must have E * N * K / 32 bytes")
-    ws, n = _bytes("workspace", workspace)
+    ws, n = _bytes("workspace", workspace, dev)
     _check(lib().ragged_gemm_mxfp4(
-        p._ref, _dense("x_codes", x_codes, v.x_codes, v.uint8),
-        _dense("x_scales", x_scales, v.x_scales, v.uint8),
-        _dense("w_codes", w_codes, v.w_codes, v.uint8), packed,
-        _dense("expert_offsets", expert_offsets, v.offsets, v.int32),
-        _rows("y", y, v.y, v.dtype, v.ldy), ws, n, _raw_stream(stream, y)), "ragged_gemm_mxfp4")
+        p._ref, _dense("x_codes", x_codes, v.x_codes, v.uint8, dev),
+        _dense("x_scales", x_scales, v.x_scales, v.uint8, dev),
+        _dense("w_codes", w_codes, v.w_codes, v.uint8, dev), packed,
+        _dense("expert_offsets", expert_offsets, v.offsets, v.int32, dev),
+        _rows("y", y, v.y, v.dtype, v.ldy, dev), ws, n, _raw_stream(stream, dev)),
+        "ragged_gemm_mxfp4")
 
 
 def moe_clip_workspace_bytes() -> int:
     return int(lib().moe_clip_workspace_bytes())
 
 
-def _tensor_arrays(name: str, tensors):
-    """Pointers, lengths and types of a list of dense GPU tensors.  (map over
+def _tensor_arrays(name: str, tensors, norm):
+    """Pointers, lengths and types of a list of dense tensors on norm's GPU.  (map over
     the descriptors: lists have dozens of tensors, and this is most of the
     call's time.)"""
     T = _t().Tensor
     types = [*map(_t().code.get, map(T.dtype.__get__, tensors))]
     if None in types:
         raise TypeError(f"{name} must be bfloat16, float16 or float32")
-    if not (all(map(T.is_cuda.__get__, tensors)) and all(map(T.is_contiguous, tensors))):
+    dev = norm.get_device()
+    if not ({*map(T.get_device, tensors)} <= {dev} and all(map(T.is_contiguous, tensors))):
+        _device("norm", norm)
         for t in tensors:
-            if not (t.is_cuda and t.is_contiguous()):
-                _fail(name, t, None, None, None)
+            if not (t.get_device() == dev and t.is_contiguous()):
+                _fail(name, t, None, None, None, dev)
     return [*map(T.data_ptr, tensors)], [*map(T.numel, tensors)], types
 
 
@@ -581,20 +602,21 @@ def moe_clip_grad_norm(grads, max_norm, norm, workspace, out=None, stream=None):
     """Global L2 norm of the gradients (into the float32 scalar tensor norm)
     and clipping to max_norm, in place or into the tensors of ``out``."""
     n = len(grads)
-    src, numel, types = _tensor_arrays("grads", grads)
+    src, numel, types = _tensor_arrays("grads", grads, norm)
     src = array("Q", src)
     dst = src
     if out is not None:
-        dst, n2, t2 = _tensor_arrays("out", out)
+        dst, n2, t2 = _tensor_arrays("out", out, norm)
         if n2 != numel or t2 != types:
             raise ValueError("out must match grads in number, lengths and types")
         dst = array("Q", dst)
     numel, types = array("q", numel), array("i", types)
-    ws, size = _bytes("workspace", workspace)
+    dev = _device("norm", norm)
+    ws, size = _bytes("workspace", workspace, dev)
     _check(lib().moe_clip_grad_norm(
         n, src.buffer_info()[0], dst.buffer_info()[0], numel.buffer_info()[0],
         types.buffer_info()[0], max_norm,
-        _dense("norm", norm, norm.shape, _t().float32), ws, size, _raw_stream(stream, norm)),
+        _dense("norm", norm, norm.shape, _t().float32, dev), ws, size, _raw_stream(stream, dev)),
         "moe_clip_grad_norm")
 
 
