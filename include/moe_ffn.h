@@ -464,7 +464,8 @@ typedef enum { MOE_T_BF16 = 0, MOE_T_FP16 = 1, MOE_T_FP32 = 2 } moe_dtype;
  *    adds to dw (in fp32, rounded once); else every expert's dw is written, 0
  *    for an expert without rows.  accumulate == 1 leaves those as they are.
  *    Into fp32 the memory adds, which may take a subnormal value for 0.
- *  - workspace: device, 128-byte aligned, moe_ragged_workspace_bytes(p) bytes;
+ *  - workspace: device, 128-byte aligned, moe_ragged_workspace_bytes(p) bytes
+ *    (which do not fall as R grows: one for the largest R serves smaller ones);
  *    no contents are kept from call to call.  Calls that may overlap on the
  *    GPU take a workspace each.
  * Offsets that decrease or leave [0, R] are reported by moe_sync_status as

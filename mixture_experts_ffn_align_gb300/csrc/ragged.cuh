@@ -478,11 +478,27 @@ __device__ __forceinline__ void rag_join_tokens(const RagArgs& a, const RagTile&
 // CTAs that share one tile's reduction of `steps` steps: as many as have at
 // least `least` steps each and as clusters run at the same time (of 2 CTAs 76,
 // of 4 36, of 8 15 on a GB300's 152 SMs: a 16th tile of eight would wait).
+constexpr int kRagClusters[3] = {15, 36, 76};     // tiles that take 8, 4, 2 CTAs each
 inline int rag_slices(long long tiles, int steps, int least) {
-  if (tiles <= 15 && steps >= 8 * least) return 8;
-  if (tiles <= 36 && steps >= 4 * least) return 4;
-  if (tiles <= 76 && steps >= 2 * least) return 2;
+  for (int i = 0; i < 3; ++i)
+    if (tiles <= kRagClusters[i] && steps >= (8 >> i) * least) return 8 >> i;
   return 1;
+}
+// Bytes for the sums of a sliced product of R rows, at least what any number of
+// rows up to R takes, so that a workspace for the largest batch serves the
+// smaller ones (fewer rows can mean more slices).  Even segments make
+// tok <= limit / w_tiles token tiles, and any segments at most min(E, R) +
+// R / tile_rows <= 2 tok; all terms grow with R, as tile_rows does.
+inline size_t rag_part_bytes(int R, int E, int w_tiles, int steps, int least, int tile_rows) {
+  size_t most = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (steps < (8 >> i) * least) continue;
+    const long long even = 2ll * (kRagClusters[i] / w_tiles) * tile_rows;
+    const long long any = (long long)(E < R ? E : R) * tile_rows + R;
+    const size_t b = (size_t)(8 >> i) * w_tiles * (size_t)(even < any ? even : any);
+    if (b > most) most = b;
+  }
+  return most * 128 * sizeof(float);
 }
 
 // A 128-byte wide box of shared memory (128-byte swizzled) to a 3-D tensor,

@@ -481,6 +481,8 @@ cudaError_t launch_op(bool half, const CUtensorMap& tmA, const CUtensorMap& tmB,
 
 }  // namespace
 
+constexpr int kLeastSteps = 8;     // of a slice of a reduction
+
 // Tiles and splits of the rows' products on one SM.
 struct RowsPlan {
   int tile_rows, w_tiles, splits;
@@ -502,11 +504,11 @@ static RowsPlan rows_plan(int R, int E, int width, int red) {
   const int segs = std::max(1, std::min(E, R));
   const long long even =
       segs * (((R + segs - 1) / segs + r.tile_rows - 1ll) / r.tile_rows) * r.w_tiles;
-  r.splits = rag_slices(even, (red + BK - 1) / BK, 8);
+  r.splits = rag_slices(even, (red + BK - 1) / BK, kLeastSteps);
   return r;
 }
 int ragged_wgrad_splits(int R, int N, int K, int E) {
-  return rag_slices((long long)E * ((N + 127) / 128) * ((K + 255) / 256), R / E / BK, 8);
+  return rag_slices((long long)E * ((N + 127) / 128) * ((K + 255) / 256), R / E / BK, kLeastSteps);
 }
 size_t ragged_wgrad_bytes(int R, int N, int K, int E) {
   const int s = ragged_wgrad_splits(R, N, K, E);
@@ -518,7 +520,7 @@ int ragged_rows_splits(int R, int E, int width, int red) {
 }
 size_t ragged_split_bytes(int R, int E, int width, int red) {
   const RowsPlan r = rows_plan(R, E, width, red);
-  return r.splits > 1 ? (size_t)r.tiles * r.splits * r.tile_rows * 128 * sizeof(float) : 0;
+  return rag_part_bytes(R, E, r.w_tiles, (red + BK - 1) / BK, kLeastSteps, r.tile_rows);
 }
 
 cudaError_t launch_ragged_rows(const RaggedProblem& p, int op, const void* rows, const void* w,

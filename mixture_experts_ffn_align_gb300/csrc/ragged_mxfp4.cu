@@ -379,20 +379,20 @@ cudaError_t launch_pack_token_scales(const Mx44Args& args, long long most_tiles,
 }
 template cudaError_t launch_pack_token_scales<32>(const Mx44Args&, long long, cudaStream_t);
 
+constexpr int kLeastSteps = 4;     // of a slice of the reduction
 int ragged_mxfp4_splits(int R, int N, int K, int E) {
   const int tr = ragged_mxfp4_tile_rows(R, E);
   const int segs = std::max(1, std::min(E, R));
   const long long even = segs * (((R + segs - 1) / segs + tr - 1ll) / tr) * (N / 128);
-  return rag_slices(even, (K + BK - 1) / BK, 4);
+  return rag_slices(even, (K + BK - 1) / BK, kLeastSteps);
 }
 static size_t scale_bytes(int R, int K, int E) {
   const int tr = ragged_mxfp4_tile_rows(R, E);
   return (size_t)most_token_tiles(R, E, tr) * tile_scale_bytes(tr, K);
 }
 size_t ragged_mxfp4_bytes(int R, int N, int K, int E) {
-  const int tr = ragged_mxfp4_tile_rows(R, E), s = ragged_mxfp4_splits(R, N, K, E);
-  return scale_bytes(R, K, E) +
-         (s > 1 ? (size_t)most_token_tiles(R, E, tr) * (N / 128) * s * tr * 128 * sizeof(float) : 0);
+  return scale_bytes(R, K, E) + rag_part_bytes(R, E, N / 128, (K + BK - 1) / BK, kLeastSteps,
+                                               ragged_mxfp4_tile_rows(R, E));
 }
 
 cudaError_t launch_ragged_mxfp4(const RaggedProblem& p, const void* xq, const uint8_t* x_scale,

@@ -41,3 +41,18 @@ def test_every_size_reaches_the_launch(form):
          + CALLS],
         cwd=ROOT, env={**os.environ, "CUDA_VISIBLE_DEVICES": ""}, capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "done", (r.returncode, r.stderr[-500:])
+
+
+def test_a_larger_batch_never_needs_less_workspace():
+    """A workspace for the largest R serves every smaller one: the bytes do not
+    fall as R grows, for bf16 and 4-bit shapes, few and many experts."""
+    rows = sorted({*range(1, 1100), *range(1100, 9000, 37), *(1 << i for i in range(23)),
+                   *((1 << i) + 1 for i in range(22))})
+    for n, k in ((4096, 4096), (8, 4104), (264, 1032), (128, 8192), (1920, 7168), (28672, 4096),
+                 (2048, 1024), (72, 72), (640, 16384), (16384, 128)):
+        for e in (1, 2, 3, 8, 15, 60, 256, 1024):
+            last = 0
+            for r in rows:
+                need = moe.moe_ragged_workspace_bytes(moe.Ragged(R=r, N=n, K=k, E=e))
+                assert need >= last, (n, k, e, r, need, last)
+                last = need
