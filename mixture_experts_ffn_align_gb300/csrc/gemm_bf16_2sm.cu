@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // peer has its next index before it reaches the tile boundary; the
     // counter read for tile j + 2 is in flight meanwhile.
     int t_lead = -1, pending = 0;
+    int last = 0;              // the last slot published
     bool ring_ok = true;
     if (leader) {
       const int f = atomicAdd(args.tile_ctr, 1);
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ring_ok || t < 0) break;
         t_lead = pending < total ? pending : -1;
         ring_ok = ring_put(j + 1, t_lead);
+        last = j + 1;
         if (t_lead >= 0) pending = atomicAdd(args.tile_ctr, 1);
       } else {
         t = ring_take(j);
@@ -221,11 +223,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         } else {
           const uint32_t sa = smem_base + stage * STAGE_BYTES;
           const uint32_t bar = mapa_shared(full_bar(stage), 0);
-          if (leader) {
-            mbar_arrive_expect_tx(full_bar(stage), PAIR_TX);
-            issued_mask |= 1u << stage;
-            issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          }
+          if (leader) mbar_arrive_expect_tx(full_bar(stage), PAIR_TX);
+          issued_mask |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           tma_load_2d_pair(sa, &tmA, bar, kb * BK, my_row, pol_a);
           tma_load_2d_pair(sa + A_BYTES, &tmB, bar, kb * BK, brow, pol_b);
         }
@@ -236,6 +236,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
     }
+    // the leader's commits arrive in both CTAs, and nothing else waits for the last
+    // ones; they, and the last releases of the ring's slots, have to land before a
+    // CTA ends
+    for (int s = 0; s < STAGES; ++s)
+      if ((issued_mask & (1u << s)) &&
+          !mbar_wait_bounded(empty_bar(s), (issued_parity >> s) & 1, abort_flag, args.limit_ns,
+                             args.err))
+        break;
+    if (leader && ring_ok)
+      for (int j = max(0, last - RING + 1); j <= last; ++j)
+        if (!mbar_wait_bounded<true>(ring_empty(j & (RING - 1)), (j / RING) & 1, abort_flag,
+                                     args.limit_ns, args.err))
+          break;
     // the leader's barrier counts both CTAs' copies: once its issued phases
     // complete, every copy of the pair has landed
     if (leader)
@@ -282,6 +295,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     tc_commit_pair(drain_bar, 0x1);
     mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+    // the peer's epilogue arrives here too: its last arrivals have to have landed
+    for (int a = 0; a < 2; ++a) {
+      const int uses = (local + 1 - a) >> 1;
+      if (uses > 0 && !mbar_wait_bounded(tempty_bar(a), (uses - 1) & 1, abort_flag, args.limit_ns,
+                                         args.err))
+        break;
+    }
   } else if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;

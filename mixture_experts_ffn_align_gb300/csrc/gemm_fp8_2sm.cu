@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // The leader publishes tile j + 1 as it starts issuing tile j, so the
     // peer has its next index before it reaches the tile boundary.
     int t_lead = -1, pending = 0;
+    int last = 0;              // the last slot published
     bool ring_ok = true;
     if (leader) {
       const int f = atomicAdd(args.tile_ctr, 1);
@@ -206,6 +207,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ring_ok || t < 0) break;
         t_lead = pending < total ? pending : -1;
         ring_ok = ring_put(j + 1, t_lead);
+        last = j + 1;
         if (t_lead >= 0) pending = atomicAdd(args.tile_ctr, 1);
       } else {
         t = ring_take(j);
@@ -227,11 +229,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         } else {
           const uint32_t sa = smem_base + stage * STAGE_BYTES;
           const uint32_t bar = mapa_shared(full_bar(stage), 0);
-          if (leader) {
-            mbar_arrive_expect_tx(full_bar(stage), PAIR_TX);
-            issued_mask |= 1u << stage;
-            issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          }
+          if (leader) mbar_arrive_expect_tx(full_bar(stage), PAIR_TX);
+          issued_mask |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           tma_load_2d_pair(sa, &tmA, bar, kb * BK, my_row, pol_a);
           tma_load_2d_pair(sa + A_BYTES, &tmB, bar, kb * BK, brow, pol_b);
         }
@@ -242,6 +242,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
     }
+    // the leader's commits arrive in both CTAs, and nothing else waits for the last
+    // ones; they, and the last releases of the ring's slots, have to land before a
+    // CTA ends
+    for (int s = 0; s < STAGES; ++s)
+      if ((issued_mask & (1u << s)) &&
+          !mbar_wait_bounded(empty_bar(s), (issued_parity >> s) & 1, abort_flag, args.limit_ns,
+                             args.err))
+        break;
+    if (leader && ring_ok)
+      for (int j = max(0, last - RING + 1); j <= last; ++j)
+        if (!mbar_wait_bounded<true>(ring_empty(j & (RING - 1)), (j / RING) & 1, abort_flag,
+                                     args.limit_ns, args.err))
+          break;
     // the leader's barrier counts both CTAs' copies: once its issued phases
     // complete, every copy of the pair has landed
     if (leader)
@@ -283,6 +296,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     tc_commit_pair(drain_bar, 0x1);
     mbar_wait_bounded(drain_bar, 0, nullptr, args.limit_ns, args.err);
+    // the peer's promotion warps arrive here too: their last arrivals have to have landed
+    for (uint32_t b = 0; b < NPART; ++b) {
+      const uint32_t uses = (pc + NPART - 1 - b) / NPART;
+      if (uses > 0 && !mbar_wait_bounded(pempty_bar(b), (uses - 1) & 1, abort_flag, args.limit_ns,
+                                         args.err))
+        break;
+    }
    }
   } else {
     setmaxnreg_inc<EPI_REGS>();      // all of warpgroups 1 and 2

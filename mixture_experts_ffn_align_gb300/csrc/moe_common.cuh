@@ -370,10 +370,19 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// All threads of both CTAs: arrive (release) and wait (acquire).
+// All threads of the cluster: arrive (release) and wait (acquire).  A role's
+// bounded waits let the lanes of a warp go on one by one, and nothing brings
+// them together again at the end of a role, so neither half may be the .aligned
+// form, which counts a warp once for each group of lanes that reaches it.
+//
+// Before the last one of a kernel each CTA waits for every signal that the other
+// sends to its barriers and that nothing else waits for: commits that arrive in
+// both CTAs, and remote arrivals.  One that lands in a CTA that has ended is
+// lost, or keeps its sender from ending.
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 // The shared::cluster address of the same shared variable in CTA `rank`.
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {

@@ -347,16 +347,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// All threads of the cluster.  A role's bounded waits let the lanes of a warp go
-// on one by one, and nothing brings them together again at the end of a role, so
-// neither half may be the .aligned form, which counts a warp once for each group
-// of lanes that reaches it.
-__device__ __forceinline__ void rag_cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-
 // fp32 <-> the operands' 16-bit types.
 template <typename T>
 struct Half16;

@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(num_threads(OP), 1)
   }
   if (splits > 1) {
     // join: the cluster's sums are in the workspace
-    rag_cluster_sync();
+    cluster_sync();
     constexpr int WARPS = num_threads(OP) / 32;
     if (OP == RAG_WGRAD && first < total) {
       // a lane takes eight columns of a row

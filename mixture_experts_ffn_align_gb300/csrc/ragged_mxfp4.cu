@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
   if (splits > 1) {
-    rag_cluster_sync();       // the cluster's sums are in the workspace
+    cluster_sync();       // the cluster's sums are in the workspace
     if (first < total)
       rag_join_tokens<T, false>(args, rag_tile<16>(sched, args, first), first, rank, warp,
                                 NUM_THREADS / 32, lane);

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  rag_cluster_sync();        // both CTAs' barriers exist before any cross-CTA signal
+  cluster_sync();        // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
   }
   __syncthreads();
-  rag_cluster_sync();
+  cluster_sync();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
