@@ -395,8 +395,8 @@ def fused_experts_from_host(p: Problem, host_x, host_topk_ids, host_topk_weights
 # it fails.
 def _fail(name: str, t, shape, dtype, stride, dev):
     """Raises for a tensor argument that is not as the call needs it."""
-    if t.get_device() < 0:
-        raise ValueError(f"{name} must be on the GPU")
+    if t.get_device() < 0 or dev < 0:
+        raise ValueError(f"{name if dev >= 0 else 'every tensor'} must be on the GPU")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}, not cuda:{t.get_device()}")
     if dtype is not None and t.dtype is not dtype:
@@ -406,17 +406,6 @@ def _fail(name: str, t, shape, dtype, stride, dev):
     if stride is not None:
         raise ValueError(f"{name} must have strides ({stride}, 1), not {t.stride()}")
     raise ValueError(f"{name} must be dense")
-
-
-def _device(name: str, t) -> int:
-    """GPU of a call's leading tensor, which the others have to share.  The
-    library launches on the current one."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be on the GPU")
-    if dev != _t().device():
-        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_t().device()}")
-    return dev
 
 
 def _dense(name: str, t, shape, dtype, dev) -> int:
@@ -434,29 +423,29 @@ def _rows(name: str, t, shape, dtype, ld, dev) -> int:
     _fail(name, t, shape, dtype, ld, dev)
 
 
-def _row_stride(name: str, t) -> int:
-    """Row stride that a matrix argument brings itself.  An expanded row's is 0,
-    which the C entry points take for "dense"."""
-    rows, cols = t.shape
-    if rows <= 1:
-        return cols
-    ld = t.stride(0)
-    if ld < cols:
-        raise ValueError(f"rows of {name} must not overlap (stride {ld} for {cols} columns)")
-    return ld
+def _overlap(name: str, ld, cols):
+    """Raises for rows that lie closer than they are long.  (An expanded row's
+    stride is 0, which the C entry points take for "dense".)"""
+    raise ValueError(f"rows of {name} must not overlap (stride {ld} for {cols} columns)")
 
 
 def _bytes(name: str, t, dev):
     """Data pointer and size of a dense buffer of any type on GPU dev."""
     if t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr(), t.numel() * t.element_size()
+        return t.data_ptr(), t.nbytes
     _fail(name, t, None, None, None, dev)
 
 
 def _raw_stream(stream, dev) -> int:
-    """The stream given, or PyTorch's current one on GPU dev."""
+    """The stream given, or PyTorch's current one on GPU dev, the call's leading
+    tensor's (-1: not on a GPU).  The library launches on the current GPU."""
+    t = _t()
+    if dev < 0:
+        raise ValueError("every tensor must be on the GPU")
+    if dev != t.device():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{t.device()}")
     if stream is None:
-        return _t().raw_stream(dev)
+        return t.raw_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -468,7 +457,7 @@ def ragged_gemm(p: Ragged, x, w, expert_offsets, y, workspace, bias=None, stream
     """y[r] = W_e x[r] (+ bias_e) for the rows r of each expert e; x [R, K],
     w [E, N, K], y [R, N], bias [E, N], expert_offsets int32 [E + 1]."""
     v = p._v
-    dev = _device("x", x)
+    dev = x.get_device()
     ws, n = _bytes("workspace", workspace, dev)
     _check(lib().ragged_gemm(
         p._ref, _rows("x", x, v.x, v.dtype, v.ldx, dev), _dense("w", w, v.w, v.dtype, dev),
@@ -480,7 +469,7 @@ def ragged_gemm(p: Ragged, x, w, expert_offsets, y, workspace, bias=None, stream
 def ragged_gemm_dgrad(p: Ragged, dy, w, expert_offsets, dx, workspace, stream=None):
     """dx[r] = W_e^T dy[r]: the gradient of ragged_gemm's x."""
     v = p._v
-    dev = _device("dy", dy)
+    dev = dy.get_device()
     ws, n = _bytes("workspace", workspace, dev)
     _check(lib().ragged_gemm_dgrad(
         p._ref, _rows("dy", dy, v.y, v.dtype, v.ldy, dev), _dense("w", w, v.w, v.dtype, dev),
@@ -495,7 +484,7 @@ def ragged_gemm_wgrad(p: Ragged, dy, x, expert_offsets, dw, workspace, accumulat
     ragged_gemm's w, in the operands' type or float32 (dw's)."""
     v = p._v
     f32 = dw.dtype is v.float32
-    dev = _device("dy", dy)
+    dev = dy.get_device()
     ws, n = _bytes("workspace", workspace, dev)
     _check(lib().ragged_gemm_wgrad(
         p._ref, _rows("dy", dy, v.y, v.dtype, v.ldy, dev), _rows("x", x, v.x, v.dtype, v.ldx, dev),
@@ -527,21 +516,27 @@ def moe_mxfp4_quantize(x, codes, scales, scale_mode="floor", stream=None):
     """E2M1 codes (uint8 [rows, K/2]) and E8M0 scales (uint8 [rows, K/32]) of
     x [rows, K] (bfloat16, float16 or float32; rows may lie apart)."""
     rows, K = x.shape
-    ld, dev = _row_stride("x", x), _device("x", x)
+    ld = x.stride(0) if rows > 1 else K
+    if ld < K:
+        _overlap("x", ld, K)
+    dev, u8 = x.get_device(), _t().uint8
     _check(lib().moe_mxfp4_quantize(
         _rows("x", x, (rows, K), x.dtype, ld, dev), _float_code("x", x), rows, K, ld,
-        MXFP4_SCALE[scale_mode], _dense("codes", codes, (rows, K // 2), _t().uint8, dev),
-        _dense("scales", scales, (rows, K // 32), _t().uint8, dev), _raw_stream(stream, dev)),
+        MXFP4_SCALE[scale_mode], _dense("codes", codes, (rows, K // 2), u8, dev),
+        _dense("scales", scales, (rows, K // 32), u8, dev), _raw_stream(stream, dev)),
         "moe_mxfp4_quantize")
 
 
 def moe_mxfp4_dequantize(codes, scales, out, stream=None):
     """out [rows, K] (bfloat16, float16 or float32) = value * 2^(scale - 127)."""
     rows, K = out.shape
-    ld, dev = _row_stride("out", out), _device("out", out)
+    ld = out.stride(0) if rows > 1 else K
+    if ld < K:
+        _overlap("out", ld, K)
+    dev, u8 = out.get_device(), _t().uint8
     _check(lib().moe_mxfp4_dequantize(
-        _dense("codes", codes, (rows, K // 2), _t().uint8, dev),
-        _dense("scales", scales, (rows, K // 32), _t().uint8, dev), rows, K,
+        _dense("codes", codes, (rows, K // 2), u8, dev),
+        _dense("scales", scales, (rows, K // 32), u8, dev), rows, K,
         _rows("out", out, (rows, K), out.dtype, ld, dev), _float_code("out", out), ld,
         _raw_stream(stream, dev)), "moe_mxfp4_dequantize")
 
@@ -550,7 +545,7 @@ def moe_mxfp4_pack_scales(scales, packed, stream=None):
     """Weight scales (uint8 [E, N, K/32]) in the block form that
     ragged_gemm_mxfp4 reads; packed has as many bytes."""
     E, N, G = scales.shape
-    dev = _device("scales", scales)
+    dev = scales.get_device()
     src = _dense("scales", scales, (E, N, G), _t().uint8, dev)
     dst = _dense("packed", packed, packed.shape, _t().uint8, dev)
     if packed.numel() != scales.numel():
@@ -563,7 +558,7 @@ def ragged_gemm_mxfp4(p: Ragged, x_codes, x_scales, w_codes, w_scales_packed, ex
                       workspace, stream=None):
     """y[r] = W_e x[r] with both operands in MXFP4; p.dtype is y's."""
     v = p._v
-    dev = _device("x_codes", x_codes)
+    dev = x_codes.get_device()
     packed, have = _bytes("w_scales_packed", w_scales_packed, dev)
     if have != v.packed:
         raise ValueError("w_scales_packed must have E * N * K / 32 bytes")
@@ -591,7 +586,6 @@ def _tensor_arrays(name: str, tensors, norm):
         raise TypeError(f"{name} must be bfloat16, float16 or float32")
     dev = norm.get_device()
     if not ({*map(T.get_device, tensors)} <= {dev} and all(map(T.is_contiguous, tensors))):
-        _device("norm", norm)
         for t in tensors:
             if not (t.get_device() == dev and t.is_contiguous()):
                 _fail(name, t, None, None, None, dev)
@@ -611,7 +605,7 @@ def moe_clip_grad_norm(grads, max_norm, norm, workspace, out=None, stream=None):
             raise ValueError("out must match grads in number, lengths and types")
         dst = array("Q", dst)
     numel, types = array("q", numel), array("i", types)
-    dev = _device("norm", norm)
+    dev = norm.get_device()
     ws, size = _bytes("workspace", workspace, dev)
     _check(lib().moe_clip_grad_norm(
         n, src.buffer_info()[0], dst.buffer_info()[0], numel.buffer_info()[0],
