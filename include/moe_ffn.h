@@ -576,9 +576,9 @@ void moe_debug_set_watchdog(int64_t limit_ns, int never_arrive);
  * scales).  The pair forms take block size 128 only.  mode 0 restores the
  * default, 1 forces the single-SM form, 2 the pair form where one exists.
  * The ragged products (ragged_gemm, its gradients, ragged_gemm_mxfp4) take the
- * same modes; by default they run on SM pairs where that leaves two tiles a
- * pair or more.  mode 3: their pair form, forward and dgrad on tiles of 512
- * weights (the other GEMMs: as mode 0).
+ * same modes; by default a model of the forms' times chooses by sizes.  mode 3:
+ * their pair form, forward and dgrad on tiles of 512 weights (the other GEMMs:
+ * as mode 0).
  * Not thread-safe; affects later launches.  No counterpart on the pages: it
  * only lets tests reach both forms at any size. */
 void moe_debug_set_bf16_gemm_form(int mode);

@@ -59,8 +59,10 @@ size_t ragged_bytes(const moe_ragged* p) {
 // SM gets from L2 and of its MMAs, and a fixed cost; or, if that is longer, what
 // HBM takes for the round's share of the bytes that are read and written once.
 // The constants are fitted to the three forms' times at 184 products each of
-// forward and dgrad (1 to 128 experts of 1 to 2048 rows): the form taken is 0.3%
-// slower than the best on average.  In us, one SM / pairs / double tiles:
+// forward and dgrad (1 to 128 experts of 1 to 2048 rows).  The form taken is slower
+// than the best by 0.8% on average for forward and wgrad (single products up to
+// 13%), 0.5% for dgrad (8%) and 0.4% for 4-bit operands (14%).  In us, one SM /
+// pairs / double tiles:
 //   forward, 8 x (28672, 4096): 32 rows each 275 / 287 / 282, 256 351 / 313 / 326;
 //   forward, 8 x (6704, 2968): 128 rows each 79 / 63 / 66, 400 185 / 148 / 124;
 //   dgrad, 8 x (28672, 4096): 32 rows each 269 / 281 / 256, 400 785 / 568 / 569;
@@ -71,6 +73,7 @@ size_t ragged_bytes(const moe_ragged* p) {
 // 192 / 158 at 257.
 enum Form { ONE_SM = 1, PAIRS = 2, DOUBLE = 3 };
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// A GB300's, which the model is fitted to (and the host may have no GPU).
 constexpr int kSms = 152, kBytesPerCycle = 50;
 
 // Cycles of `tiles` tiles on `units` CTAs or pairs: a tile's own, or those of its

@@ -33,7 +33,7 @@
 //    library-owned ring of slots, one per launch in flight; the last CTA to
 //    finish resets it.
 //  * every wait is bounded; the final cluster barrier is reached by both CTAs
-//    after their bounded loops.
+//    after their bounded loops and after waits for the other's last signals.
 #include <atomic>
 
 #include "moe_common.cuh"

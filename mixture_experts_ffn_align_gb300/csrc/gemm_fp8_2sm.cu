@@ -29,7 +29,8 @@
 //    whose peer half repeats the leader's block and is not stored;
 //  * a last column tile narrower than 256 (N % 256 == 128) computes its
 //    upper half on whatever the weight box held and never stores it;
-//  * every wait is bounded (device error word + CTA abort flag).
+//  * every wait is bounded (device error word + CTA abort flag); a CTA ends after
+//    the other's last signals.
 #include <atomic>
 
 #include "moe_common.cuh"

@@ -31,7 +31,7 @@
 //  * tiles are handed out at run time (a tile counter and a 4-slot ring, as
 //    in the other pair kernels); an expert with an odd block count ends with a
 //    pair whose peer half repeats the leader's block and is not stored;
-//  * every wait is bounded.
+//  * every wait is bounded; a CTA ends after the other's last signals.
 #include <atomic>
 #include <type_traits>
 

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads)
       const float scale =
           __uint_as_float(s[i] == 0u ? 0x400000u : s[i] == 255u ? 0x7FC00000u : s[i] << 23);
       float v[8];
-uint32_t h[4];
+      uint32_t h[4];
       asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
           "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
           "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"

@@ -227,7 +227,7 @@ __device__ __forceinline__ RagWTile rag_wtile(const RagArgs& a, int t) {
   RagWTile T;
   T.e = t / a.e_tiles;
   const int local = t - T.e * a.e_tiles.d;
-  // group_max is a power of two: groups of 8 n tiles x all k tiles
+  // groups of 8 n tiles x all k tiles
   const int g = (local >> kRagGroupShift) / a.k_tiles;
   const int n0 = g << kRagGroupShift;
   const int gm = min(1 << kRagGroupShift, a.w_tiles.d - n0);
@@ -335,8 +335,8 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap
 // MMA issuers run their loops with the whole warp and issue from this lane: with
 // the loop inside one lane's branch the compiler keeps descriptors and
 // coordinates in per-thread registers and moves them to the uniform ones that
-// the instructions take, ~600 cycles a step against 512 of MMA work (forward of
-// 8192 rows, 8 experts, 4096 -> 28672: 1068 -> 1013 us).
+// the instructions take, ~600 cycles a step against 512 of MMA work (5% of a
+// long forward).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
@@ -467,7 +467,9 @@ __device__ __forceinline__ void rag_join_tokens(const RagArgs& a, const RagTile&
 }
 // CTAs that share one tile's reduction of `steps` steps: as many as have at
 // least `least` steps each and as clusters run at the same time (of 2 CTAs 76,
-// of 4 36, of 8 15 on a GB300's 152 SMs: a 16th tile of eight would wait).
+// of 4 36, of 8 15 on a GB300's 152 SMs: a 16th tile of eight would wait).  The
+// limits are that GPU's on purpose: sizes of workspaces follow from them, which
+// are asked for without one too, and only speed would differ on another.
 constexpr int kRagClusters[3] = {15, 36, 76};     // tiles that take 8, 4, 2 CTAs each
 inline int rag_slices(long long tiles, int steps, int least) {
   for (int i = 0; i < 3; ++i)

@@ -31,8 +31,8 @@
 // 7168 -> 4096 a projection of 470 MB, runs at HBM's rate (8 experts of 28672 x
 // 4096, 1.88 GB: 279 us, 6.8 TB/s); two rows of one small expert by launch and
 // latency (4.6 us in a graph, 1.5 of them an empty kernel's).  wgrad of segments
-// up to some 200 rows is bound by writing dw, 64 experts of 4096 x 4096 (2.15 GB)
-// at 4096 rows: 3.3 us for each expert's 33.5 MB.
+// up to some 200 rows is bound by writing dw: 64 experts of 64 rows, 4096 x 4096
+// (2.15 GB), 393 us, 5.5 TB/s (a plain fill of dw: 532 us).
 #include <algorithm>
 
 #include "moe_common.cuh"

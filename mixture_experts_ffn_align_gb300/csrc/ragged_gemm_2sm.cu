@@ -25,9 +25,16 @@
 //    peer sends to a barrier of this CTA: one that arrives at a CTA that has ended
 //    is lost, or keeps its sender from ending.
 //
-// 8192 rows, 8 experts: forward 4096 -> 28672 1075 us (1790 TFLOP/s),
-// dgrad 4096 -> 14336 557 us (1727), wgrad of the same 680 us (1415, bound by what
-// the SMs take in from L2); in long runs at the power limit 1250, 640 and 710 us.
+// 8 experts of 1024 rows each, in short bursts: forward 4096 -> 28672 1050 us (1830
+// TFLOP/s), dgrad 4096 -> 14336 533 us (1807), wgrad of the same 582 us (1654); in
+// long runs at the power limit 1208, 607 and 658 us.  Forward of uneven segments
+// (900 to 1100 rows) 1140 and 1313 us: tiles round up to 32 rows, and 5.9% of the
+// MMAs' columns are no row's.
+// wgrad of segments that end inside 16 rows (1025, 1030 or 1039) takes 677 us in
+// bursts and 721 in long runs, of 1040 rows 604 and 679: the hand-off to the
+// zeroing warp at each tile's end costs some 12% there, which more rows hide.
+// wgrad without it is bound by what the SMs take in from L2: 64 bytes a cycle at
+// the tensor cores' full rate.
 #include <algorithm>
 
 #include "moe_common.cuh"
@@ -137,8 +144,8 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;   // this pair's tiles
 
   // wgrad's producer is one lane: the whole warp measured slower there (605
-  // against 574 us for 8192 rows, 8 experts, 4096 x 14336), faster in the others
-  // (68 against 81 us for 32 rows, 256 x 16384)
+  // against 574 us in turn, in bursts: 8 experts of 1024 rows, 4096 x 14336), faster
+  // in the others (68 against 81 us for 32 rows, 256 x 16384)
   constexpr bool LONE = OP == RAG_WGRAD;
   if (warp == 0 && (!LONE || lane == 0)) {
     // ------------------------------------------------------------ producers
@@ -381,7 +388,8 @@ __global__ void __launch_bounds__(num_threads(OP, MT), 1)
     // ------------------------------------------------------------ epilogue, double tile
     // Four warps an accumulator.  Both are in use until a tile's end, so each
     // warp first reads its 32 x 256 sums as packed pairs of tokens, hands the
-    // accumulator back, and stores while the next tile's MMAs run.
+    // accumulator back, and stores while the next tile's MMAs run.  (With its 128
+    // pairs a thread needs 12 words more than the 168 registers it can have.)
     const int q = warp & 3, half = (warp - 2) >> 2;
     int local = 0;
     for (int t = first; t < total; t += stride) {

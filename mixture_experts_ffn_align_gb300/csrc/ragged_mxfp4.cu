@@ -25,8 +25,8 @@
 //  * every wait is bounded, as in ragged_gemm.cu.
 //
 // Few rows are bound by the weights' 0.53 bytes a value: 512 rows, 64 experts,
-// 7168 -> 4096, 1.0 GB: 175 us here and on SM pairs.  8192 rows, 8 experts, 4096 ->
-// 28672: 508 us, bound by what an SM takes in from L2 (on pairs 377).
+// 7168 -> 4096, 1.0 GB: 180 us here and on SM pairs.  8192 rows, 8 experts, 4096 ->
+// 28672: 478 us, bound by what an SM takes in from L2 (on pairs 377).
 #include <algorithm>
 
 #include "moe_common.cuh"
