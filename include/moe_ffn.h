@@ -491,6 +491,42 @@ moe_status ragged_gemm_wgrad(const moe_ragged* p, const void* dy, const void* x,
                              int accumulate, void* workspace, size_t workspace_bytes,
                              void* stream);
 
+/* The gated block of an expert, on the same rows, segments, workspace, alignments
+ * and errors as the products above.
+ *   ragged_gated        h[r, :] = w13_e x[r] (+ bias_e), the gate's I values g then
+ *                       the up projection's I values u (N = 2 I),
+ *                       z[r, i] = g' s(alpha g') (u' + beta),
+ *                       s(v) = 1 / (1 + e^-v), g' = min(g, limit),
+ *                       u' = clamp(u, -limit, limit); limit <= 0 clamps nothing.
+ *                       alpha 1, beta 0: SiLU(g) u.  One kernel; z comes from the
+ *                       fp32 sums.
+ *   ragged_gated_dgrad  its gradient and that of the down projection y[r] = w2_e z[r]:
+ *                       with dz[r, i] = sum_n dy[r, n] w2[e, n, i], which stays in
+ *                       fp32 inside the kernel, dh[r, :] = dz times the derivatives
+ *                       of z by g (I values; 0 where g > limit) and by u (I values; 0
+ *                       where |u| > limit), and z again (for ragged_gemm_wgrad of w2),
+ *                       all from h as ragged_gated rounded it.
+ * dx and dw13 are ragged_gemm_dgrad and ragged_gemm_wgrad of dh, dw2 is
+ * ragged_gemm_wgrad of dy and z.
+ *  - ragged_gated: p is the gate/up product: N = 2 I (a multiple of 16), x [R, K],
+ *    w13 [E, 2 I, K] gate rows first, bias [E, 2 I] or NULL; z [R, I] with row
+ *    stride ldz; h [R, 2 I] with row stride p->ldy, or NULL where no gradient
+ *    follows.
+ *  - ragged_gated_dgrad: p is the down projection: K = I, dy [R, N] with row stride
+ *    p->ldy, w2 [E, N, I]; h and dh [R, 2 I] with row strides ldh and lddh; z [R, I]
+ *    with row stride p->ldx, or NULL.  dh may be h itself (with the same stride).
+ *  - row strides: multiples of 8, 0 = dense.
+ * Errors also: MOE_ERR_INVALID_ARG for an alpha or beta that is not finite, a NaN
+ * limit. */
+moe_status ragged_gated(const moe_ragged* p, const void* x, const void* w13, const void* bias,
+                        const int32_t* expert_offsets, float alpha, float beta, float limit,
+                        void* z, int64_t ldz, void* h, void* workspace, size_t workspace_bytes,
+                        void* stream);
+moe_status ragged_gated_dgrad(const moe_ragged* p, const void* dy, const void* w2, const void* h,
+                              int64_t ldh, const int32_t* expert_offsets, float alpha, float beta,
+                              float limit, void* dh, int64_t lddh, void* z, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* MXFP4 (the weight format of MOE_Q_MXFP4_W4A8): E2M1 codes [rows, K/2] (low
  * nibble = even k) and one E8M0 scale per 32 values [rows, K/32].  K is a
  * multiple of 32.  For each group of 32 with a = max |v|:
@@ -545,6 +581,34 @@ moe_status moe_clip_grad_norm(int n, const void* const* grads, void* const* outs
                               const int64_t* numel, const int32_t* dtypes, float max_norm,
                               float* norm, void* workspace, size_t workspace_bytes,
                               void* stream);
+
+/* Orthogonalised update of E matrices (an optimiser's momentum) by Newton-Schulz
+ * steps:
+ *   X = g / (|g|_F + eps);  for each step's a, b, c:
+ *     A = X X^T,  X = (a I + b A + c A^2) X;    out = scale X,
+ * which takes every singular value of g towards 1 and keeps its vectors.
+ *  - g [E, N, K] of type g_dtype (moe_dtype), dense, any N and K from 1 to 2^20 and
+ *    any alignment of the element; out [E, N, K] bf16, dense, 16-byte aligned; may
+ *    be g itself.  Each matrix by itself, whichever side is the longer.
+ *  - coefficients: host array of 3 * steps floats, read during the call; steps 1 to
+ *    MOE_MAX_ORTHOGONALIZE_STEPS.  They should keep singular values of X below 3 and
+ *    the polynomial's values within 16: elements past that are infinities.
+ *  - eps: at least 1e-12; a zero matrix gives zeros.
+ *  - Products take operands of 11 bits (22 where N or K is at most 256) and sum in
+ *    fp32; the result is within about 0.2% (rms) of the exact one, its own
+ *    rounding to bf16 among that.  A square beyond fp32's range makes the norm
+ *    infinite and the result zero; infinities and NaN give NaN in their matrix.
+ *    The result does not depend on timing.
+ *  - workspace: device, 256-byte aligned, moe_orthogonalize_workspace_bytes bytes
+ *    (0 for sizes that are refused); about four bytes an element of g and four of
+ *    every square of the shorter side.  No contents are kept from call to call; calls
+ *    that may overlap on the GPU take one each.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA. */
+#define MOE_MAX_ORTHOGONALIZE_STEPS 64
+size_t moe_orthogonalize_workspace_bytes(int E, int N, int K);
+moe_status moe_orthogonalize(int E, int N, int K, const void* g, int g_dtype, void* out, int steps,
+                             const float* coefficients, float eps, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /* Synchronises `stream`, reads and clears the device error word, and returns
  * MOE_OK, MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_DEVICE_BAD_INDEX or MOE_ERR_CUDA. */

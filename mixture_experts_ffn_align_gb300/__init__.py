@@ -41,7 +41,9 @@ EXPORTS = ["moe_m_sum_bound", "moe_align_workspace_bytes", "moe_align_permute_la
            "moe_prepacked_scale_bytes", "moe_prepack_weights",
            "moe_ragged_workspace_bytes", "ragged_gemm", "ragged_gemm_dgrad", "ragged_gemm_wgrad",
            "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_pack_scales",
-           "ragged_gemm_mxfp4", "moe_clip_workspace_bytes", "moe_clip_grad_norm"]
+           "ragged_gemm_mxfp4", "moe_clip_workspace_bytes", "moe_clip_grad_norm",
+           "ragged_gated", "ragged_gated_dgrad", "moe_orthogonalize_workspace_bytes",
+           "moe_orthogonalize"]
 
 NOALLOC_SCRATCH_BYTES = 1 << 20   # MOE_NOALLOC_SCRATCH_BYTES in include/moe_ffn.h
 
@@ -122,6 +124,7 @@ class Ragged:
         R, N, K, E = self.R, self.N, self.K, self.E
         return SimpleNamespace(
             x=(R, K), y=(R, N), w=(E, N, K), bias=(E, N), offsets=(E + 1,),
+            half_n=(R, N // 2), twice_k=(R, 2 * K),
             x_codes=(R, K // 2), x_scales=(R, K // 32), w_codes=(E, N, K // 2),
             packed=E * N * (K // 32), ldx=self.ldx or K, ldy=self.ldy or N,
             dtype=getattr(torch, self.dtype), int32=torch.int32, uint8=torch.uint8,
@@ -192,9 +195,16 @@ def lib() -> ctypes.CDLL:
         L.moe_mxfp4_pack_scales.argtypes = [vp, i32, i32, i32, vp, vp]
         L.moe_clip_workspace_bytes.argtypes, L.moe_clip_workspace_bytes.restype = [], sz
         L.moe_clip_grad_norm.argtypes = [i32] + [vp] * 4 + [f32, vp, vp, sz, vp]
+        L.ragged_gated.argtypes = [G] + [vp] * 4 + [f32] * 3 + [vp, i64, vp, vp, sz, vp]
+        L.ragged_gated_dgrad.argtypes = \
+            [G, vp, vp, vp, i64, vp] + [f32] * 3 + [vp, i64, vp, vp, sz, vp]
+        L.moe_orthogonalize_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_orthogonalize_workspace_bytes.restype = sz
+        L.moe_orthogonalize.argtypes = [i32, i32, i32, vp, i32, vp, i32, vp, f32, f32, vp, sz, vp]
         for n in ("ragged_gemm", "ragged_gemm_dgrad", "ragged_gemm_wgrad", "ragged_gemm_mxfp4",
                   "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_pack_scales",
-                  "moe_clip_grad_norm"):
+                  "moe_clip_grad_norm", "ragged_gated", "ragged_gated_dgrad",
+                  "moe_orthogonalize"):
             getattr(L, n).restype = i32
         for n in ("moe_align_permute", "grouped_gemm_w13", "act_mul_quant", "grouped_gemm_w2",
                   "unpermute_reduce", "fused_experts", "fused_experts_from_host",
@@ -494,12 +504,60 @@ def ragged_gemm_wgrad(p: Ragged, dy, x, expert_offsets, dw, workspace, accumulat
         _raw_stream(stream, dev)), "ragged_gemm_wgrad")
 
 
+def _row_stride(name: str, t, cols) -> int:
+    """Row stride of a matrix of this many columns, in elements (a single row's, which
+    PyTorch leaves open: cols)."""
+    ld = t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else cols
+    if ld < cols:
+        _overlap(name, ld, cols)
+    return ld
+
+
+def ragged_gated(p: Ragged, x, w13, expert_offsets, z, workspace, h=None, bias=None, alpha=1.0,
+                 beta=0.0, limit=0.0, stream=None):
+    """z = g' sigmoid(alpha g') (u' + beta) of h = W13_e x (+ bias_e) for the rows of
+    each expert e: g' = min(g, limit), u' = clamp(u, -limit, limit), limit <= 0: as they
+    are; the default is SiLU(g) u.  p: the gate/up product, N = 2 I; x [R, K], w13
+    [E, 2 I, K] (gate rows first), bias [E, 2 I], z [R, I]; h [R, 2 I] is written if
+    given, for ragged_gated_dgrad."""
+    v = p._v
+    dev = x.get_device()
+    ws, n = _bytes("workspace", workspace, dev)
+    ldz = _row_stride("z", z, p.N // 2)
+    _check(lib().ragged_gated(
+        p._ref, _rows("x", x, v.x, v.dtype, v.ldx, dev), _dense("w13", w13, v.w, v.dtype, dev),
+        None if bias is None else _dense("bias", bias, v.bias, v.dtype, dev),
+        _dense("expert_offsets", expert_offsets, v.offsets, v.int32, dev), alpha, beta, limit,
+        _rows("z", z, v.half_n, v.dtype, ldz, dev), ldz,
+        None if h is None else _rows("h", h, v.y, v.dtype, v.ldy, dev), ws, n,
+        _raw_stream(stream, dev)), "ragged_gated")
+
+
+def ragged_gated_dgrad(p: Ragged, dy, w2, h, expert_offsets, dh, workspace, z=None, alpha=1.0,
+                       beta=0.0, limit=0.0, stream=None):
+    """Gradient of the gated block from dy, that of its output W2_e z: dh, that of
+    ragged_gated's h, and, if given, z once more.  p: the down projection, K = I;
+    dy [R, N], w2 [E, N, I], h and dh [R, 2 I] (may be one), z [R, I]; alpha, beta and
+    limit as in ragged_gated."""
+    v = p._v
+    dev = dy.get_device()
+    ws, n = _bytes("workspace", workspace, dev)
+    ldh, lddh = _row_stride("h", h, 2 * p.K), _row_stride("dh", dh, 2 * p.K)
+    _check(lib().ragged_gated_dgrad(
+        p._ref, _rows("dy", dy, v.y, v.dtype, v.ldy, dev), _dense("w2", w2, v.w, v.dtype, dev),
+        _rows("h", h, v.twice_k, v.dtype, ldh, dev), ldh,
+        _dense("expert_offsets", expert_offsets, v.offsets, v.int32, dev), alpha, beta, limit,
+        _rows("dh", dh, v.twice_k, v.dtype, lddh, dev), lddh,
+        None if z is None else _rows("z", z, v.x, v.dtype, v.ldx, dev), ws, n,
+        _raw_stream(stream, dev)), "ragged_gated_dgrad")
+
+
 @cache
 def _t():
     """torch, and the library's codes of its floating types."""
     import torch
     return SimpleNamespace(
-        uint8=torch.uint8, float32=torch.float32, Tensor=torch.Tensor,
+        uint8=torch.uint8, float32=torch.float32, bfloat16=torch.bfloat16, Tensor=torch.Tensor,
         raw_stream=torch._C._cuda_getCurrentRawStream, device=torch._C._cuda_getDevice,
         code={getattr(torch, k): v for k, v in DTYPE.items()})
 
@@ -612,6 +670,42 @@ def moe_clip_grad_norm(grads, max_norm, norm, workspace, out=None, stream=None):
         types.buffer_info()[0], max_norm,
         _dense("norm", norm, norm.shape, _t().float32, dev), ws, size, _raw_stream(stream, dev)),
         "moe_clip_grad_norm")
+
+
+def moe_orthogonalize_workspace_bytes(E: int, N: int, K: int) -> int:
+    return int(lib().moe_orthogonalize_workspace_bytes(int(E), int(N), int(K)))
+
+
+@cache
+def _coefficients(steps, coefficients):
+    """The steps' coefficients as an array: three numbers for all, or three a step."""
+    flat = array("f")
+    for c in coefficients if isinstance(coefficients[0], tuple) else (coefficients,) * steps:
+        flat.extend(c)
+    if len(flat) != 3 * steps:
+        raise ValueError(f"coefficients must be three numbers, or three for each of {steps} steps")
+    return flat
+
+
+def moe_orthogonalize(g, out, workspace, steps=5, coefficients=(3.4445, -4.7750, 2.0315),
+                      eps=1e-7, scale=1.0, stream=None):
+    """out = scale X of every matrix of g [E, N, K] (or [N, K]; bfloat16, float16 or
+    float32): X = g / (|g|_F + eps), then in each step X = (a I + b A + c A^2) X with
+    A = X X^T.  coefficients: (a, b, c), or a sequence of such triples, one a step.  out:
+    bfloat16, of g's shape."""
+    shape = g.shape
+    if not 2 <= len(shape) <= 3:
+        raise ValueError(f"g must be [E, N, K] or [N, K], not {tuple(shape)}")
+    E, N, K = shape if len(shape) == 3 else (1, *shape)
+    dev = g.get_device()
+    ws, n = _bytes("workspace", workspace, dev)
+    if type(coefficients) is not tuple or type(coefficients[0]) is list:
+        coefficients = tuple(tuple(c) if hasattr(c, "__len__") else c for c in coefficients)
+    c = _coefficients(steps, coefficients)
+    _check(lib().moe_orthogonalize(
+        E, N, K, _dense("g", g, shape, g.dtype, dev), _float_code("g", g),
+        _dense("out", out, shape, _t().bfloat16, dev), steps, c.buffer_info()[0], eps, scale, ws,
+        n, _raw_stream(stream, dev)), "moe_orthogonalize")
 
 
 def moe_gemm2_splits(p: Problem) -> int:

@@ -1,8 +1,10 @@
 // C ABI (include/moe_ffn.h) of the training and 4-bit operators: ragged
-// grouped products, the MXFP4 codec and product, gradient norm and clip.
-// Argument validation and launch order; the kernels are in ragged_gemm.cu,
+// grouped products, the gated block and its gradient, the MXFP4 codec and product,
+// gradient norm and clip, the orthogonalised update.
+// Argument validation and launch order; the kernels are in ragged_one.cuh, ragged_pair.cuh,
 // ragged_mxfp4.cu, mxfp4_codec.cu and grad_clip.cu.
 #include <algorithm>
+#include <cmath>
 
 #include "../../include/moe_ffn.h"
 #include "moe_internal.h"
@@ -95,10 +97,10 @@ int64_t l2_bytes(int64_t bytes, int64_t pitch_bytes) {
 // for 4-bit operands); dgrad's boxes of the weights are 256 bytes to 1 KB wide in
 // memory against forward's 128 bytes.
 Form rows_form(const moe_ragged* p, int w_cols, int red, int64_t w_pitch, int64_t x_pitch,
-               int step_deep, int extra, int hbm, int hbm_double) {
+               int step_deep, int extra, int hbm, int hbm_double, bool doubles = true) {
   const int form = ragged_form();
   const bool fp4 = step_deep != 64;
-  if (form == DOUBLE) return fp4 ? PAIRS : DOUBLE;
+  if (form == DOUBLE) return doubles && !fp4 ? DOUBLE : PAIRS;
   if (form != 0) return static_cast<Form>(form);
   const int64_t segs = std::min(p->E, p->R), rows = ceil_div(p->R, segs);
   const int64_t per_seg = ceil_div(rows, 256), tok = segs * per_seg;
@@ -136,7 +138,7 @@ Form rows_form(const moe_ragged* p, int w_cols, int red, int64_t w_pitch, int64_
       tiles_cycles(tok * w2, kSms / 2,
                    steps * step(a + b2, mma) + (one_acc ? 2000 : fp4 ? 1900 : 1400), bytes,
                    hbm_two) + launch;
-  if (!fp4 && steps >= 16) {   // no double tiles of 4-bit operands, and no rate for them
+  if (doubles && !fp4 && steps >= 16) {   // no double tiles of 4-bit operands, and no rate for them
     // both accumulators are drained before the next tile's MMAs
     const int64_t dbl =
         tiles_cycles(tok * w4, kSms / 2, steps * step(2 * a + b2, 2 * mma) + 2500 + 24 * n, bytes,
@@ -174,6 +176,28 @@ cudaError_t ragged_rows(const moe_ragged* p, int op, const void* rows, const voi
                      : launch_ragged_rows_2sm(q, op, f == DOUBLE, rows, w, bias, out, st);
 }
 
+// The gated product's epilogue does not change its rounds: the plain product's model,
+// without double tiles.
+cudaError_t ragged_gated_rows(const moe_ragged* p, const GatedProblem& g, const void* rows,
+                              const void* w, const void* bias, const int32_t* offsets,
+                              void* workspace, void* stream) {
+  const RaggedProblem q = ragged_problem(p, offsets);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool fwd = !g.grad;
+  const Form f = rows_form(p, fwd ? p->N : p->K, fwd ? p->K : p->N, 2ll * p->K,
+                           2 * (fwd ? q.ldx : q.ldy), 64, 0, fwd ? 3400 : 3600, 0, false);
+  return f == ONE_SM ? launch_ragged_gated(q, g, rows, w, bias, workspace, st)
+                     : launch_ragged_gated_2sm(q, g, rows, w, bias, st);
+}
+bool valid_activation(float alpha, float beta, float limit) {
+  return std::isfinite(alpha) && std::isfinite(beta) && !std::isnan(limit);
+}
+// A row stride (0: dense) of rows of `cols` values; 0 if it is none.
+int64_t row_stride(int64_t ld, int64_t cols) {
+  if (ld == 0) return cols;
+  return ld < cols || ld % 8 || ld > (1ll << 32) ? 0 : ld;
+}
+
 // Checks shared by the products; MOE_OK to go on.
 moe_status ragged_args(const moe_ragged* p, const void* a, const void* b, const int32_t* offsets,
                        const void* out, const void* workspace, size_t workspace_bytes) {
@@ -187,6 +211,12 @@ moe_status ragged_args(const moe_ragged* p, const void* a, const void* b, const 
   return MOE_OK;
 }
 
+// Tiles within the kernels' 32-bit numbers, rows within a tensor map's.
+bool valid_orthogonalize(int E, int N, int K) {
+  if (E < 1 || E > MOE_MAX_EXPERTS || N < 1 || N > kMaxDim || K < 1 || K > kMaxDim) return false;
+  const int64_t m = std::min(N, K), t = (std::max(N, K) + 127) / 128, u = (m + 31) / 32;
+  return E * t * u < (1ll << 28) && E * m < (1ll << 30);
+}
 bool valid_dtype(int t) { return t >= MOE_T_BF16 && t <= MOE_T_FP32; }
 
 }  // namespace
@@ -233,6 +263,55 @@ moe_status ragged_gemm_wgrad(const moe_ragged* p, const void* dy, const void* x,
   const bool f32 = dw_dtype == MOE_T_FP32;
   return done(wgrad_form(p) == PAIRS ? launch_ragged_wgrad_2sm(q, dy, x, dw, f32, accumulate != 0, st)
                              : launch_ragged_wgrad(q, dy, x, dw, f32, accumulate != 0, workspace, st));
+}
+
+moe_status ragged_gated(const moe_ragged* p, const void* x, const void* w13, const void* bias,
+                        const int32_t* expert_offsets, float alpha, float beta, float limit,
+                        void* z, int64_t ldz, void* h, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  if (!valid_ragged(p) || p->N % 16 || !valid_activation(alpha, beta, limit))
+    return MOE_ERR_INVALID_ARG;
+  ldz = row_stride(ldz, p->N / 2);
+  if (ldz == 0) return MOE_ERR_INVALID_ARG;
+  const moe_status s = ragged_args(p, x, w13, expert_offsets, z, workspace, workspace_bytes);
+  if (s != MOE_OK || p->R == 0) return s;
+  if (misaligned(bias, 2) || misaligned(h, 16)) return MOE_ERR_INVALID_ARG;
+  GatedProblem g{};
+  g.inter = p->N / 2;
+  g.alpha = alpha;
+  g.beta = beta;
+  g.limit = limit;
+  g.h_out = h;
+  g.ldh_out = p->ldy != 0 ? p->ldy : p->N;
+  g.z = z;
+  g.ldz = ldz;
+  return done(ragged_gated_rows(p, g, x, w13, bias, expert_offsets, workspace, stream));
+}
+
+moe_status ragged_gated_dgrad(const moe_ragged* p, const void* dy, const void* w2, const void* h,
+                              int64_t ldh, const int32_t* expert_offsets, float alpha, float beta,
+                              float limit, void* dh, int64_t lddh, void* z, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (!valid_ragged(p) || !valid_activation(alpha, beta, limit)) return MOE_ERR_INVALID_ARG;
+  ldh = row_stride(ldh, 2ll * p->K);
+  lddh = row_stride(lddh, 2ll * p->K);
+  if (ldh == 0 || lddh == 0) return MOE_ERR_INVALID_ARG;
+  const moe_status s = ragged_args(p, dy, w2, expert_offsets, dh, workspace, workspace_bytes);
+  if (s != MOE_OK || p->R == 0) return s;
+  if (!h || misaligned(h, 16) || misaligned(z, 16)) return MOE_ERR_INVALID_ARG;
+  GatedProblem g{};
+  g.grad = true;
+  g.inter = p->K;
+  g.alpha = alpha;
+  g.beta = beta;
+  g.limit = limit;
+  g.h = h;
+  g.ldh = ldh;
+  g.h_out = dh;
+  g.ldh_out = lddh;
+  g.z = z;
+  g.ldz = p->ldx != 0 ? p->ldx : p->K;
+  return done(ragged_gated_rows(p, g, dy, w2, nullptr, expert_offsets, workspace, stream));
 }
 
 moe_status ragged_gemm_mxfp4(const moe_ragged* p, const void* x_codes, const void* x_scales,
@@ -311,6 +390,26 @@ moe_status moe_clip_grad_norm(int n, const void* const* grads, void* const* outs
   if (workspace_bytes < clip_workspace_bytes()) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return done(launch_clip_grad_norm(n, grads, outs, numel, dtypes, max_norm, norm, workspace,
                                     static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_orthogonalize_workspace_bytes(int E, int N, int K) {
+  return valid_orthogonalize(E, N, K) ? orthogonalize_bytes(E, N, K) : 0;
+}
+
+moe_status moe_orthogonalize(int E, int N, int K, const void* g, int g_dtype, void* out, int steps,
+                             const float* coefficients, float eps, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!valid_orthogonalize(E, N, K) || !valid_dtype(g_dtype)) return MOE_ERR_INVALID_ARG;
+  if (steps < 1 || steps > MOE_MAX_ORTHOGONALIZE_STEPS || !coefficients) return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < 3 * steps; ++i)
+    if (!std::isfinite(coefficients[i])) return MOE_ERR_INVALID_ARG;
+  if (!(eps >= 1e-12f) || !std::isfinite(eps) || !std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  if (!g || !out || !workspace || misaligned(g, g_dtype == MOE_T_FP32 ? 4 : 2) ||
+      misaligned(out, 16) || misaligned(workspace, 256))
+    return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < orthogonalize_bytes(E, N, K)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return done(launch_orthogonalize(E, N, K, g, g_dtype, out, steps, coefficients, eps, scale,
+                                   workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

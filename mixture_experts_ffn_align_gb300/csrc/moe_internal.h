@@ -229,6 +229,25 @@ cudaError_t launch_ragged_rows_2sm(const RaggedProblem& p, int op, bool double_t
 cudaError_t launch_ragged_wgrad_2sm(const RaggedProblem& p, const void* dy, const void* x,
                                     void* dw, bool out_f32, bool accumulate,
                                     cudaStream_t stream);
+// The gated forward product (rows = x, w = w13) and, grad, its gradient (rows = dy,
+// w = w2); formulas in ragged_epi.cuh.
+struct GatedProblem {
+  bool grad;
+  int inter;
+  float alpha, beta, limit;     // limit <= 0: none
+  const void* h;                // gradient
+  long long ldh;
+  void* h_out;                  // forward: h or null; gradient: dh
+  long long ldh_out;
+  void* z;                      // gradient: or null
+  long long ldz;
+};
+cudaError_t launch_ragged_gated(const RaggedProblem& p, const GatedProblem& g, const void* rows,
+                                const void* w, const void* bias, void* workspace,
+                                cudaStream_t stream);
+cudaError_t launch_ragged_gated_2sm(const RaggedProblem& p, const GatedProblem& g,
+                                    const void* rows, const void* w, const void* bias,
+                                    cudaStream_t stream);
 // 0: by size, 1: one SM, 2: SM pairs, 3: SM pairs on double tiles
 // (moe_debug_set_bf16_gemm_form).
 int ragged_form();
@@ -257,5 +276,12 @@ size_t clip_workspace_bytes();
 cudaError_t launch_clip_grad_norm(int n, const void* const* grads, void* const* outs,
                                   const int64_t* numel, const int32_t* types, float max_norm,
                                   float* norm, void* workspace, cudaStream_t stream);
+
+// ---- orthogonalised update (orthogonalize.cu).  type: 0 bf16, 1 fp16, 2 fp32;
+// coefficients: three a step.
+size_t orthogonalize_bytes(int E, int N, int K);
+cudaError_t launch_orthogonalize(int E, int N, int K, const void* g, int type, void* out,
+                                 int steps, const float* coefficients, float eps, float scale,
+                                 void* workspace, cudaStream_t stream);
 
 }  // namespace moe

@@ -1,0 +1,323 @@
+// Orthogonalised update of E matrices g [N, K] by Newton-Schulz steps:
+//   X = g / (|g|_F + eps),   then for each step's (a, b, c)
+//   A = X X^T,  B = a I + b A + c A^2,  X = B X,      out = scale X.
+// The steps push every singular value of X towards 1 and leave its directions, so
+// that out is near U V^T of g = U S V^T.
+//
+// X lies with its shorter side m as rows (g is transposed on the way in, and the
+// last product's stores on the way out), so A and B are m x m.  A and B are
+// symmetric and computed in tiles on and below the diagonal, each stored on both
+// sides: m^2 M + m^3 + 2 m^2 M operations a step instead of 4 m^2 M + 2 m^3 (M the
+// longer side).  B takes in a I, so that the third product needs no operand beside
+// B and X.
+//
+// Operands are fp16, whose 11 bits matter here: with bf16's 8 the result is 1% off
+// (rms), with 11 it is 0.11 to 0.13% for m of 256 to 1024 and more, less than the
+// rounding of the result to bf16 (0.17%).  X, A and B are scaled by powers of two
+// into fp16's range: |X|, |A| and |B| are at most about 1.3, 1.6 and 4 (for the usual
+// coefficients), and their typical elements are 1 / sqrt(m M) and less.  Sums over few
+// elements average less: up to m = 256, where all products are short, every
+// matrix is held as a hi and a lo part of 22 bits together, and a product is three
+// (hi hi + hi lo + lo hi) over one accumulator.
+//
+// Forming A anew in each step, rather than carrying it along as B A B, costs the m^2
+// M product but keeps small singular values: an error of A enters B X relative to
+// X, while that of a carried A grows twelvefold a step.
+#include <algorithm>
+
+#include "dense_gemm.h"
+#include "moe_common.cuh"
+#include "moe_internal.h"
+#include "pdl.cuh"
+#include "ragged.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPrecise = 256;                 // shorter sides up to here take hi and lo parts
+constexpr float kScaleX = 4096.0f, kScaleA = 1024.0f, kScaleB = 1024.0f;
+constexpr int kMaxChunks = 1024;              // partial sums of a matrix
+constexpr int kStrip = 512;                   // columns of X a block writes
+
+template <int TYPE>
+__device__ __forceinline__ float load1(const void* p, long long i) {
+  if (TYPE == 2) return static_cast<const float*>(p)[i];
+  const uint16_t b = static_cast<const uint16_t*>(p)[i];
+  return TYPE == 0 ? Half16<__nv_bfloat16>::value(b) : Half16<__half>::value(b);
+}
+
+__device__ __forceinline__ double block_sum(double v, double* smem) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) v += smem[w];
+  return v;
+}
+
+// Squares of part blockIdx.x of matrix blockIdx.y (n elements): in fp32 over 16
+// values, in fp64 beyond.
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads) k_ortho_norm(const void* g, long long n, int chunks,
+                                                         double* partial) {
+  __shared__ double smem[kThreads / 32];
+  griddep_launch();
+  griddep_wait();
+  constexpr int size = TYPE == 2 ? 4 : 2, per = 16 / size;
+  const char* base = static_cast<const char*>(g) + (long long)blockIdx.y * n * size;
+  double sum = 0.0;
+  // 16-byte pieces from the first aligned element on, the elements beside them singly
+  const long long head =
+      min((long long)((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15) / size, n);
+  const long long pieces = (n - head) / per;
+  const uint4* p = reinterpret_cast<const uint4*>(base + head * size);
+  const long long end = pieces * (blockIdx.x + 1) / chunks;
+  for (long long i = pieces * blockIdx.x / chunks + threadIdx.x; i < end; i += 4 * kThreads) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = i + k * kThreads < end ? __ldg(p + i + k * kThreads) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (TYPE == 2) {
+          const float f = __uint_as_float(w[j]);
+          s += f * f;
+        } else {
+          using T = typename std::conditional<TYPE == 1, __half, __nv_bfloat16>::type;
+          const float lo = Half16<T>::value((uint16_t)(w[j] & 0xFFFFu));
+          const float hi = Half16<T>::value((uint16_t)(w[j] >> 16));
+          s += lo * lo;
+          s += hi * hi;
+        }
+      }
+      sum += s;
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x < 32) {
+    const long long tail = head + pieces * per;
+    if (threadIdx.x < head) {
+      const float f = load1<TYPE>(base, threadIdx.x);
+      sum += (double)f * f;
+    }
+    if (threadIdx.x < n - tail) {
+      const float f = load1<TYPE>(base, tail + threadIdx.x);
+      sum += (double)f * f;
+    }
+  }
+  sum = block_sum(sum, smem);
+  if (threadIdx.x == 0) partial[(size_t)blockIdx.y * chunks + blockIdx.x] = sum;
+}
+
+// X of matrix blockIdx.z: rows from 64 blockIdx.y, columns from kStrip blockIdx.x, and
+// zeros behind its M columns.
+template <int TYPE, bool TRANSPOSED>
+__global__ void __launch_bounds__(kThreads)
+    k_ortho_scale(const void* g, int m, int M, int Mp, int ld, int lo, int chunks,
+                  const double* partial, float eps, __half* x) {
+  __shared__ double smem[kThreads / 32];
+  __shared__ float tile[TRANSPOSED ? 64 : 1][65];
+  griddep_launch();
+  griddep_wait();
+  double total = 0.0;
+  for (int i = threadIdx.x; i < chunks; i += kThreads) total += partial[(size_t)blockIdx.z * chunks + i];
+  total = block_sum(total, smem);
+  const float inv = (float)((double)kScaleX / (sqrt(total) + (double)eps));
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int r0 = 64 * blockIdx.y;
+  const long long base = (long long)blockIdx.z * m * M;
+  const int c_end = min((int)(blockIdx.x + 1) * kStrip, Mp);
+  for (int c0 = blockIdx.x * kStrip; c0 < c_end; c0 += 64) {
+    if (TRANSPOSED) {            // g is [M, m]
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = c0 + ty + 8 * i;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = r0 + tx + 32 * k;
+          tile[tx + 32 * k][ty + 8 * i] =
+              c < M && r < m ? load1<TYPE>(g, base + (long long)c * m + r) : 0.0f;
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + ty + 8 * i, c = c0 + 2 * tx;
+      if (r >= m) continue;
+      float v[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (TRANSPOSED)
+          v[k] = tile[ty + 8 * i][2 * tx + k];
+        else
+          v[k] = c + k < M ? load1<TYPE>(g, base + (long long)r * M + c + k) : 0.0f;
+        v[k] *= inv;
+      }
+      __half* out = x + ((long long)blockIdx.z * m + r) * ld + c;
+      const __half2 hi = __floats2half2_rn(v[0], v[1]);
+      *reinterpret_cast<__half2*>(out) = hi;
+      if (lo != 0)
+        *reinterpret_cast<__half2*>(out + lo) =
+            __floats2half2_rn(v[0] - __low2float(hi), v[1] - __high2float(hi));
+    }
+  }
+}
+
+struct Layout {
+  int m, M, mp, Mp, parts, chunks;
+  size_t x_bytes, a_bytes, partial, a, b, x0, x1, part, total;
+};
+size_t pad(size_t v) { return (v + 255) / 256 * 256; }
+
+DenseProduct product(const Layout& l, int E) {
+  DenseProduct d{};
+  d.E = E;
+  d.m = l.m;
+  d.segs = l.parts == 2 ? 3 : 1;
+  return d;
+}
+// A = X X^T from x, scaled
+DenseProduct gram(const Layout& l, int E, const void* x, void* a) {
+  DenseProduct d = product(l, E);
+  d.nt = d.symmetric = true;
+  d.width = l.mp;
+  d.rows = d.w = x;
+  d.rows_ld = d.w_ld = l.parts * l.Mp;
+  d.rows_lo = d.w_lo = l.Mp;
+  d.seg_kb = l.Mp / 64;
+  d.c_acc = kScaleA / (kScaleX * kScaleX);
+  d.out = a;
+  d.out_ld = l.parts * l.mp;
+  d.out_lo = l.parts == 2 ? l.mp : 0;
+  return d;
+}
+// B = a I + b A + c A^2
+DenseProduct polynomial(const Layout& l, int E, const void* a, void* b, const float* c) {
+  DenseProduct d = product(l, E);
+  d.nt = d.symmetric = true;
+  d.width = l.mp;
+  d.rows = d.w = d.mat = a;
+  d.rows_ld = d.w_ld = d.out_ld = l.parts * l.mp;
+  d.rows_lo = d.w_lo = l.mp;
+  d.out_lo = l.parts == 2 ? l.mp : 0;
+  d.seg_kb = l.mp / 64;
+  d.c_acc = c[2] * (kScaleB / (kScaleA * kScaleA));
+  d.c_mat = c[1] * (kScaleB / kScaleA);
+  d.c_diag = c[0] * kScaleB;
+  d.out = b;
+  return d;
+}
+// X = B X
+DenseProduct apply(const Layout& l, int E, const void* b, const void* x, void* out) {
+  DenseProduct d = product(l, E);
+  d.width = l.Mp;
+  d.rows = b;
+  d.rows_ld = l.parts * l.mp;
+  d.rows_lo = l.mp;
+  d.w = x;
+  d.w_ld = d.out_ld = l.parts * l.Mp;
+  d.w_lo = l.Mp;
+  d.out_lo = l.parts == 2 ? l.Mp : 0;
+  d.seg_kb = l.mp / 64;
+  d.c_acc = 1.0f / kScaleB;
+  d.out = out;
+  return d;
+}
+
+Layout layout(int E, int N, int K) {
+  Layout l;
+  l.m = std::min(N, K);
+  l.M = std::max(N, K);
+  l.mp = (l.m + 63) / 64 * 64;
+  l.Mp = (l.M + 63) / 64 * 64;
+  l.parts = l.m <= kPrecise ? 2 : 1;
+  const long long n = (long long)N * K;
+  l.chunks = (int)std::max<long long>(
+      1, std::min<long long>({(n + 8191) / 8192, kMaxChunks, std::max(1, 2432 / E)}));
+  l.x_bytes = pad((size_t)E * l.m * l.parts * l.Mp * 2);
+  l.a_bytes = pad((size_t)E * l.m * l.parts * l.mp * 2);
+  l.partial = 0;
+  l.a = pad((size_t)E * l.chunks * sizeof(double));
+  l.b = l.a + l.a_bytes;
+  l.x0 = l.b + l.a_bytes;
+  l.x1 = l.x0 + l.x_bytes;
+  l.part = l.x1 + l.x_bytes;
+  const float c[3] = {};
+  DenseProduct last = apply(l, E, nullptr, nullptr, nullptr);
+  last.width = l.M;
+  l.total = l.part + pad(std::max({dense_part_bytes(gram(l, E, nullptr, nullptr)),
+                                   dense_part_bytes(polynomial(l, E, nullptr, nullptr, c)),
+                                   dense_part_bytes(apply(l, E, nullptr, nullptr, nullptr)),
+                                   dense_part_bytes(last)}));
+  return l;
+}
+
+cudaError_t run(const DenseProduct& d, void* part, cudaStream_t stream) {
+  return dense_on_pairs(d) ? launch_dense_2sm(d, stream) : launch_dense(d, part, stream);
+}
+
+template <int TYPE>
+cudaError_t prepare(const Layout& l, int E, bool transposed, const void* g, float eps,
+                    double* partial, void* x, cudaStream_t stream) {
+  const long long n = (long long)l.m * l.M;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(l.chunks, E, 1);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k_ortho_norm<TYPE>, g, n, l.chunks, partial);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((l.Mp + kStrip - 1) / kStrip, (l.m + 63) / 64, E);
+  const int ld = l.parts * l.Mp, lo = l.parts == 2 ? l.Mp : 0;
+  const double* sums = partial;
+  return cudaLaunchKernelEx(&cfg, transposed ? k_ortho_scale<TYPE, true> : k_ortho_scale<TYPE, false>,
+                            g, l.m, l.M, l.Mp, ld, lo, l.chunks, sums, eps,
+                            static_cast<__half*>(x));
+}
+
+}  // namespace
+
+size_t orthogonalize_bytes(int E, int N, int K) { return layout(E, N, K).total; }
+
+cudaError_t launch_orthogonalize(int E, int N, int K, const void* g, int type, void* out,
+                                 int steps, const float* coefficients, float eps, float scale,
+                                 void* workspace, cudaStream_t stream) {
+  const Layout l = layout(E, N, K);
+  const bool transposed = N > K;
+  char* ws = static_cast<char*>(workspace);
+  void *a = ws + l.a, *b = ws + l.b, *x = ws + l.x0, *y = ws + l.x1, *part = ws + l.part;
+  double* partial = reinterpret_cast<double*>(ws + l.partial);
+  cudaError_t e = type == 0   ? prepare<0>(l, E, transposed, g, eps, partial, x, stream)
+                  : type == 1 ? prepare<1>(l, E, transposed, g, eps, partial, x, stream)
+                              : prepare<2>(l, E, transposed, g, eps, partial, x, stream);
+  for (int s = 0; s < steps && e == cudaSuccess; ++s) {
+    e = run(gram(l, E, x, a), part, stream);
+    if (e != cudaSuccess) return e;
+    e = run(polynomial(l, E, a, b, coefficients + 3 * s), part, stream);
+    if (e != cudaSuccess) return e;
+    DenseProduct last = apply(l, E, b, x, y);
+    if (s == steps - 1) {
+      last.width = l.M;
+      last.c_acc *= scale / kScaleX;
+      last.final_out = out;
+      last.transposed = transposed;
+    }
+    e = run(last, part, stream);
+    std::swap(x, y);
+  }
+  return e;
+}
+
+}  // namespace moe

@@ -8,7 +8,7 @@
 // completion of one implies that of all kernels before it.
 //
 // Kernels of clusters keep the ordinary order, before and after: on SM pairs, and
-// while their tail waits (ragged_gemm_2sm.cu) were missing too, about one in
+// while their tail waits (ragged_pair.cuh) were missing too, about one in
 // 10,000 launches did not end, and no overlap is worth that.  They are the long
 // ones, which gain 2 of some hundred microseconds.
 #pragma once

@@ -1,5 +1,5 @@
-// Pieces shared by the ragged grouped products (ragged_gemm.cu on one SM,
-// ragged_gemm_2sm.cu on SM pairs, ragged_mxfp4.cu): segments of rows given by
+// Pieces shared by the ragged grouped products (ragged_one.cuh on one SM,
+// ragged_pair.cuh on SM pairs, ragged_mxfp4.cu): segments of rows given by
 // expert offsets on the device, their cut into tiles, operand descriptors and
 // epilogue stores.
 //
@@ -52,6 +52,36 @@ __device__ __forceinline__ int operator/(int n, const FastDiv& f) {
   return (int)(((uint64_t)(uint32_t)n * f.mul) >> (31 + f.shift));
 }
 
+// What a product's epilogue does with the sums: rounds and stores them, or one of
+// the fused forms (ragged_epi.cuh).
+enum : int { EPI_PLAIN = 0, EPI_GATED = 1, EPI_GATED_GRAD = 2, EPI_DENSE = 3 };
+
+// Arguments of the gated forward and of its gradient.
+struct RagGated {
+  const void* h;            // gradient: the sums before the activation [R, 2 inter]
+  void* h_out;              // forward: those sums, or null; gradient: dh
+  void* z;                  // [R, inter]; gradient: or null
+  long long ldh, ldh_out, ldz;
+  int inter;
+  float alpha, beta, limit; // limit: +inf clamps nothing
+};
+// Arguments of a batch of dense products of E matrices of m rows (ragged_epi.cuh).
+struct RagDense {
+  int m;                    // rows of a matrix
+  int mp;                   // tri: columns of the output, m rounded up to 64
+  int tri;                  // symmetric output: tiles on and below the diagonal
+  int per;                  // rows of a token tile
+  int tok_tiles;
+  FastDiv e_tiles;          // tiles of a matrix
+  int seg_kb;               // steps of each of the reduction's segments (hi and lo parts)
+  int a_lo, b_lo;           // columns from the hi to the lo part of the operands
+  float c_acc, c_mat, c_diag;
+  const __half* mat;        // added, c_mat times: [E, m, ...] as the output, or null
+  int lo;                   // columns from the hi to the lo part of mat and output, or 0
+  __nv_bfloat16* final_out; // the last product: [E, m, W], or [E, W, m] with `transposed`
+  int transposed;
+};
+
 // Everything a ragged product kernel needs beside its tensor maps.
 struct RagArgs {
   const int32_t* offsets;   // [E + 1]
@@ -76,6 +106,8 @@ struct RagArgs {
   uint64_t limit_ns;
   int never_arrive;
   int* err;
+  RagGated gated;
+  RagDense dense;
 };
 
 struct RagSched {
@@ -328,6 +360,28 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap
       ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
       "r"(cluster_bar), "l"(policy)
+      : "memory");
+}
+
+// 5-D tiled load: gate and up weights interleaved (make_tmap_rag_gated).
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t c0, int32_t c3, int32_t c4,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(0), "r"(c3), "r"(c4), "r"(bar),
+      "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap* map,
+                                                 uint32_t cluster_bar, int32_t c0, int32_t c3,
+                                                 int32_t c4, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(0), "r"(c3), "r"(c4), "r"(cluster_bar),
+      "l"(policy)
       : "memory");
 }
 

@@ -1,0 +1,425 @@
+// Fused epilogues of the ragged products' kernels (ragged_one.cuh,
+// ragged_pair.cuh), and the tiles of a batch of dense products.
+//
+// EPI_GATED, on the forward product with w13 [E, 2 I, K], gate rows first:
+//   h = x W^T (+ bias),  z = g' s(alpha g') (u' + beta),   s(v) = 1 / (1 + e^-v),
+//   g' = min(g, limit), u' = clamp(u, -limit, limit), g and u the halves of h.
+// A tile's weights are gate and up rows in turn, eight of each
+// (make_tmap_rag_gated), so that g and u of a column meet in lanes l and l ^ 8 of one
+// warp and the tile, its accumulators and its slices stay those of the plain
+// product.  The two lanes swap half of their tokens, and each computes z for half.
+// (Gate and up rows in an accumulator each would need both until a tile ends.)
+// z is computed from the fp32 sums, not from h's rounded values.
+//
+// EPI_GATED_GRAD, on the gradient product dz = dy W2 with w2 [E, K, I]:
+//   dg = dz (u' + beta) s (1 + alpha g' (1 - s))  where g <= limit, else 0,
+//   du = dz g' s                                  where |u| <= limit, else 0,
+//   z as above, for the gradient of w2.
+// dz itself is never rounded or stored.  Two neighbouring lanes swap tokens first,
+// so that each reads and writes both columns of a token as 4-byte pieces, 64 bytes
+// of a row a half-warp.
+//
+// EPI_DENSE: E products of matrices of m rows, in fp16 with hi and lo parts where
+// that is asked for (dense.lo): v = c_acc sum + c_mat mat + c_diag (row == column),
+// rounded to fp16 (lo = v - hi), or the last product in bf16.
+#pragma once
+
+#include "moe_internal.h"
+#include "ragged.cuh"
+
+namespace moe {
+
+// ---------------------------------------------------------------- activation
+__device__ __forceinline__ float gated_min(float v, float limit) { return v > limit ? limit : v; }
+__device__ __forceinline__ float gated_clamp(float v, float limit) {
+  return v > limit ? limit : v < -limit ? -limit : v;      // NaN stays
+}
+__device__ __forceinline__ float gated_sigmoid(float v) {
+  return __fdividef(1.0f, 1.0f + __expf(-v));
+}
+__device__ __forceinline__ float gated_value(const RagGated& a, float g, float u) {
+  g = gated_min(g, a.limit);
+  return g * gated_sigmoid(a.alpha * g) * (gated_clamp(u, a.limit) + a.beta);
+}
+struct GatedGrad {
+  float dg, du, z;
+};
+__device__ __forceinline__ GatedGrad gated_grad(const RagGated& a, float dz, float g, float u) {
+  const float gc = gated_min(g, a.limit), uc = gated_clamp(u, a.limit) + a.beta;
+  const float s = gated_sigmoid(a.alpha * gc), act = gc * s;
+  GatedGrad r;
+  r.dg = g > a.limit ? 0.0f : dz * uc * (s + a.alpha * act * (1.0f - s));
+  r.du = fabsf(u) > a.limit ? 0.0f : dz * act;
+  r.z = act * uc;
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+  return make_float2(Half16<T>::value((uint16_t)(w & 0xFFFFu)), Half16<T>::value((uint16_t)(w >> 16)));
+}
+
+inline void gated_args(const GatedProblem& g, RagGated& a) {
+  a.h = g.h;
+  a.h_out = g.h_out;
+  a.z = g.z;
+  a.ldh = g.ldh;
+  a.ldh_out = g.ldh_out;
+  a.ldz = g.ldz;
+  a.inter = g.inter;
+  a.alpha = g.alpha;
+  a.beta = g.beta;
+  a.limit = g.limit > 0.0f ? g.limit : __builtin_huge_valf();
+}
+
+// Interleaved row w of the gate and up weights: column w of the tile is column
+// gated_col(w) of the gate (up = 0) or up half.
+__device__ __forceinline__ int gated_col(int w) { return ((w >> 4) << 3) + (w & 7); }
+
+// 32 tokens from row row0 of this lane's interleaved column w.
+template <typename T>
+__device__ __forceinline__ void rag_gated_tokens32(const RagArgs& a, uint32_t (&r)[32], float bias,
+                                                   long long row0, int live, int w, int lane) {
+  const RagGated& q = a.gated;
+  const int up = (w >> 3) & 1, col = gated_col(w);
+  const bool inside = w < a.W;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + bias);
+  if (q.h_out != nullptr) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      pk[j] = Half16<T>::pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+    rag_store_packed32(pk, static_cast<uint16_t*>(q.h_out) + row0 * q.ldh_out + up * q.inter + col,
+                       q.ldh_out, live, w, a.W, lane);
+  }
+  // the gate's lane takes the even tokens, the up half's the odd ones
+  uint32_t pk[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float z[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int j = 2 * i + k;
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, up ? r[2 * j] : r[2 * j + 1], 8);
+      z[k] = gated_value(q, __uint_as_float(up ? other : r[2 * j]),
+                         __uint_as_float(up ? r[2 * j + 1] : other));
+    }
+    pk[i] = Half16<T>::pack(z[0], z[1]);     // tokens 4 i + up and 4 i + up + 2
+  }
+  // neighbouring columns: an even lane both columns of the first token
+  const int odd = lane & 1, tok0 = up + 2 * odd;
+  uint16_t* p = static_cast<uint16_t*>(q.z) + (row0 + tok0) * q.ldz + (col - odd);
+  const uint32_t sel = odd ? 0x3276u : 0x5410u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, pk[i], 1);
+    const uint32_t v = __byte_perm(pk[i], other, sel);
+    if (inside && tok0 + 4 * i < live) *reinterpret_cast<uint32_t*>(p) = v;
+    p += 4 * q.ldz;
+  }
+}
+
+// 32 tokens from row row0 of this lane's column w of dz.
+template <typename T>
+__device__ __forceinline__ void rag_gated_grad_tokens32(const RagArgs& a, const uint32_t (&r)[32],
+                                                        long long row0, int live, int w,
+                                                        int lane) {
+  const RagGated& q = a.gated;
+  const int odd = lane & 1, c0 = w - odd;
+  const bool inside = w < a.W;
+  const uint16_t* h = static_cast<const uint16_t*>(q.h) + (row0 + odd) * q.ldh + c0;
+  uint16_t* dh = static_cast<uint16_t*>(q.h_out) + (row0 + odd) * q.ldh_out + c0;
+  uint16_t* z = q.z == nullptr ? nullptr : static_cast<uint16_t*>(q.z) + (row0 + odd) * q.ldz + c0;
+  // eight tokens at a time: their loads first
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    uint32_t hg[8], hu[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = inside && 2 * (8 * b + j) + odd < live;
+      hg[j] = in ? *reinterpret_cast<const uint32_t*>(h) : 0u;
+      hu[j] = in ? *reinterpret_cast<const uint32_t*>(h + q.inter) : 0u;
+      h += 2 * q.ldh;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int t = 8 * b + j;
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? r[2 * t] : r[2 * t + 1], 1);
+      const float dz0 = __uint_as_float(odd ? other : r[2 * t]);
+      const float dz1 = __uint_as_float(odd ? r[2 * t + 1] : other);
+      const float2 g = unpack16<T>(hg[j]), u = unpack16<T>(hu[j]);
+      const GatedGrad x = gated_grad(q, dz0, g.x, u.x), y = gated_grad(q, dz1, g.y, u.y);
+      if (inside && 2 * t + odd < live) {
+        *reinterpret_cast<uint32_t*>(dh) = Half16<T>::pack(x.dg, y.dg);
+        *reinterpret_cast<uint32_t*>(dh + q.inter) = Half16<T>::pack(x.du, y.du);
+        if (z != nullptr) *reinterpret_cast<uint32_t*>(z) = Half16<T>::pack(x.z, y.z);
+      }
+      dh += 2 * q.ldh_out;
+      if (z != nullptr) z += 2 * q.ldz;
+    }
+  }
+}
+
+// --------------------------------------------------------------- dense products
+// Tile t of the batch.  rows: of a symmetric product those of its padded output,
+// which has zeros there.  Symmetric: the tiles (w_tile, tok) with tok <= w_tile;
+// else groups of 8 token tiles, as rag_tile.
+template <int G>
+__device__ __forceinline__ RagTile rag_dense_tile(const RagArgs& a, int t) {
+  const RagDense& q = a.dense;
+  RagTile T;
+  T.e = t / q.e_tiles;
+  const int l = t - T.e * q.e_tiles.d;
+  if (q.tri) {
+    // l = i (i + 1) / 2 + tok: i from the square root, which is off by one at most
+    int i = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
+    if (i * (i + 1) / 2 > l) --i;
+    if ((i + 1) * (i + 2) / 2 <= l) ++i;
+    T.w_tile = i;
+    T.tok = l - i * (i + 1) / 2;
+    T.rows = min(q.per, q.mp - T.tok * q.per);
+  } else {
+    const int w_tiles = a.w_tiles.d;
+    const int c = q.tok_tiles <= 8 ? 0 : l / (8 * w_tiles);
+    const int gm = min(8, q.tok_tiles - 8 * c);
+    const int l2 = l - 8 * c * w_tiles;
+    T.w_tile = l2 / gm;
+    T.tok = 8 * c + (l2 - T.w_tile * gm);
+    T.rows = min(q.per, q.m - T.tok * q.per);
+  }
+  T.row0 = T.e * q.m + T.tok * q.per;
+  return T;
+}
+
+__device__ __forceinline__ float half_hi(float v, uint16_t& hi) {
+  hi = Half16<__half>::bits(v);
+  return v - Half16<__half>::value(hi);
+}
+__device__ __forceinline__ uint32_t half_hi2(float& x, float& y) {
+  const uint32_t p = Half16<__half>::pack(x, y);
+  const float2 v = unpack16<__half>(p);
+  x -= v.x;
+  y -= v.y;
+  return p;
+}
+
+// 32 tokens from row tok (of the matrix) of this lane's column w; left: the tile's.
+__device__ __forceinline__ void rag_dense_tokens32(const RagArgs& a, const RagTile& D,
+                                                   const uint32_t (&r)[32], int tok, int left,
+                                                   int w, int lane) {
+  const RagDense& q = a.dense;
+  // rows from here on in the matrix, and in the tile (the next tile's may be among 32)
+  const int live = min(q.m - tok, left);
+  const long long base = (long long)D.e * q.m;
+  float v[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = q.c_acc * __uint_as_float(r[j]);
+  if (q.final_out != nullptr) {
+    __nv_bfloat16* out = q.final_out;
+    if (q.transposed) {                       // a lane's tokens lie side by side
+      out += ((long long)D.e * a.W + w) * q.m + tok;
+      if (w >= a.W) {
+      } else if (live >= 32 && q.m % 8 == 0) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8)
+          *reinterpret_cast<uint4*>(out + j) = make_uint4(
+              Half16<__nv_bfloat16>::pack(v[j], v[j + 1]),
+              Half16<__nv_bfloat16>::pack(v[j + 2], v[j + 3]),
+              Half16<__nv_bfloat16>::pack(v[j + 4], v[j + 5]),
+              Half16<__nv_bfloat16>::pack(v[j + 6], v[j + 7]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j < live) out[j] = __float2bfloat16_rn(v[j]);
+      }
+      return;
+    }
+    out += (base + tok) * a.W + w;
+    if (a.W % 2 == 0) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) pk[j] = Half16<__nv_bfloat16>::pack(v[2 * j], v[2 * j + 1]);
+      rag_store_packed32(pk, reinterpret_cast<uint16_t*>(out), a.W, live, w, a.W, lane);
+    } else if (w < a.W) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < live) out[(long long)j * a.W] = __float2bfloat16_rn(v[j]);
+    }
+    return;
+  }
+  uint16_t* out = static_cast<uint16_t*>(a.out);
+  if (q.tri) {
+    // This lane's tokens as row w of the output: 64 bytes of it.  What lies past
+    // the matrix's columns is zero (those rows may be the next matrix's).
+    if (w < q.m) {
+      if (q.mat != nullptr) {
+        const uint4* mat =
+            reinterpret_cast<const uint4*>(q.mat + (base + w) * a.ldo + tok);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          if (part == 0 || q.lo != 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 x = mat[part * (q.lo / 8) + i];
+              const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = unpack16<__half>(xs[k]);
+                v[8 * i + 2 * k] += q.c_mat * f.x;
+                v[8 * i + 2 * k + 1] += q.c_mat * f.y;
+              }
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        if (tok + j == w) v[j] += q.c_diag;
+        if (j >= live) v[j] = 0.0f;
+      }
+    }
+    uint32_t pk[16], lo[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float x = v[2 * j], y = v[2 * j + 1];
+      pk[j] = half_hi2(x, y);
+      lo[j] = Half16<__half>::pack(x, y);
+    }
+    if (w < q.m) {
+      uint4* p = reinterpret_cast<uint4*>(out + (base + w) * a.ldo + tok);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        if (q.lo != 0)
+          p[q.lo / 8 + i] = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+      }
+    }
+    if (D.tok != D.w_tile) {                  // and as column w
+      out += (base + tok) * a.ldo + w;
+      rag_store_packed32(pk, out, a.ldo, live, w, a.W, lane);
+      if (q.lo != 0) rag_store_packed32(lo, out + q.lo, a.ldo, live, w, a.W, lane);
+    }
+    return;
+  }
+  uint32_t pk[16], lo[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float x = v[2 * j], y = v[2 * j + 1];
+    pk[j] = half_hi2(x, y);
+    lo[j] = Half16<__half>::pack(x, y);
+  }
+  out += (base + tok) * a.ldo + w;
+  rag_store_packed32(pk, out, a.ldo, live, w, a.W, lane);
+  if (q.lo != 0) rag_store_packed32(lo, out + q.lo, a.ldo, live, w, a.W, lane);
+}
+
+// ------------------------------------------------------------- joining slices
+// As rag_join_tokens, with the fused epilogues: a lane has the sums of the four
+// columns from w of row D.row0 + j.
+template <int EPI, typename T>
+__device__ __forceinline__ void rag_join_store(const RagArgs& a, const RagTile& D, int j, int w,
+                                               float4 x) {
+  const long long row = D.row0 + j;
+  if (EPI == EPI_GATED) {
+    const RagGated& q = a.gated;
+    const int up = (w >> 3) & 1, col = gated_col(w);
+    if (a.bias != nullptr && w < a.W) {
+      const uint16_t* b =
+          static_cast<const uint16_t*>(a.bias) + (long long)D.e * a.W + up * q.inter + col;
+      x = make_float4(x.x + Half16<T>::value(b[0]), x.y + Half16<T>::value(b[1]),
+                      x.z + Half16<T>::value(b[2]), x.w + Half16<T>::value(b[3]));
+    }
+    // the same columns of the other half are two lanes on
+    const float4 o = make_float4(__shfl_xor_sync(0xffffffffu, x.x, 2),
+                                 __shfl_xor_sync(0xffffffffu, x.y, 2),
+                                 __shfl_xor_sync(0xffffffffu, x.z, 2),
+                                 __shfl_xor_sync(0xffffffffu, x.w, 2));
+    if (w >= a.W) return;
+    if (q.h_out != nullptr)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(q.h_out) + row * q.ldh_out + up * q.inter +
+                                col) =
+          make_uint2(Half16<T>::pack(x.x, x.y), Half16<T>::pack(x.z, x.w));
+    if (!up)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(q.z) + row * q.ldz + col) =
+          make_uint2(Half16<T>::pack(gated_value(q, x.x, o.x), gated_value(q, x.y, o.y)),
+                     Half16<T>::pack(gated_value(q, x.z, o.z), gated_value(q, x.w, o.w)));
+  } else if (EPI == EPI_GATED_GRAD) {
+    const RagGated& q = a.gated;
+    if (w >= a.W) return;
+    const uint16_t* h = static_cast<const uint16_t*>(q.h) + row * q.ldh + w;
+    const uint2 hg = *reinterpret_cast<const uint2*>(h);
+    const uint2 hu = *reinterpret_cast<const uint2*>(h + q.inter);
+    const float2 g0 = unpack16<T>(hg.x), g1 = unpack16<T>(hg.y);
+    const float2 u0 = unpack16<T>(hu.x), u1 = unpack16<T>(hu.y);
+    const GatedGrad r0 = gated_grad(q, x.x, g0.x, u0.x), r1 = gated_grad(q, x.y, g0.y, u0.y);
+    const GatedGrad r2 = gated_grad(q, x.z, g1.x, u1.x), r3 = gated_grad(q, x.w, g1.y, u1.y);
+    uint16_t* dh = static_cast<uint16_t*>(q.h_out) + row * q.ldh_out + w;
+    *reinterpret_cast<uint2*>(dh) =
+        make_uint2(Half16<T>::pack(r0.dg, r1.dg), Half16<T>::pack(r2.dg, r3.dg));
+    *reinterpret_cast<uint2*>(dh + q.inter) =
+        make_uint2(Half16<T>::pack(r0.du, r1.du), Half16<T>::pack(r2.du, r3.du));
+    if (q.z != nullptr)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(q.z) + row * q.ldz + w) =
+          make_uint2(Half16<T>::pack(r0.z, r1.z), Half16<T>::pack(r2.z, r3.z));
+  } else {
+    const RagDense& q = a.dense;
+    if (w >= a.W) return;
+    float v[4] = {q.c_acc * x.x, q.c_acc * x.y, q.c_acc * x.z, q.c_acc * x.w};
+    const int tok = (int)(row - (long long)D.e * q.m);
+    if (q.final_out != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (w + i < a.W)
+          q.final_out[q.transposed ? ((long long)D.e * a.W + w + i) * q.m + tok
+                                   : row * a.W + w + i] = __float2bfloat16_rn(v[i]);
+      return;
+    }
+    if (q.mat != nullptr) {
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        if (part == 0 || q.lo != 0) {
+          const uint2 m = *reinterpret_cast<const uint2*>(q.mat + row * a.ldo + w + part * q.lo);
+          const float2 m0 = unpack16<__half>(m.x), m1 = unpack16<__half>(m.y);
+          v[0] += q.c_mat * m0.x;
+          v[1] += q.c_mat * m0.y;
+          v[2] += q.c_mat * m1.x;
+          v[3] += q.c_mat * m1.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (tok == w + i) v[i] += q.c_diag;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.ldo + w;
+    uint2 hi;
+    hi.x = half_hi2(v[0], v[1]);
+    hi.y = half_hi2(v[2], v[3]);
+    *reinterpret_cast<uint2*>(out) = hi;
+    if (q.lo != 0)
+      *reinterpret_cast<uint2*>(out + q.lo) =
+          make_uint2(Half16<__half>::pack(v[0], v[1]), Half16<__half>::pack(v[2], v[3]));
+  }
+}
+template <int EPI, typename T>
+__device__ __forceinline__ void rag_join_fused(const RagArgs& a, const RagTile& D, int t, int rank,
+                                               int warp, int warps, int lane) {
+  const int w = D.w_tile * 128 + 4 * lane;
+  const float* p = a.part + (size_t)t * a.splits * a.tile_rows * 128 + 4 * lane;
+  for (int j = rank * warps + warp; j < D.rows; j += a.splits * warps) {
+    float4 x = *reinterpret_cast<const float4*>(p + (size_t)j * 128);
+    for (int s = 1; s < a.splits; ++s) {
+      const float4 v = *reinterpret_cast<const float4*>(p + ((size_t)s * a.tile_rows + j) * 128);
+      x = make_float4(x.x + v.x, x.y + v.y, x.z + v.z, x.w + v.w);
+    }
+    rag_join_store<EPI, T>(a, D, j, w, x);
+  }
+}
+
+// Tile t of a product, whatever its epilogue.
+template <int EPI, int G>
+__device__ __forceinline__ RagTile rag_any_tile(const RagSched& s, const RagArgs& a, int t) {
+  if constexpr (EPI == EPI_DENSE) return rag_dense_tile<G>(a, t);
+  return rag_tile<G>(s, a, t);
+}
+
+}  // namespace moe

@@ -35,7 +35,7 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* ba
             CUtensorMapL2promotion promotion) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return fn(map, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE,
             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, promotion,
@@ -65,6 +65,18 @@ bool make_tmap_rag_wide(CUtensorMap* map, const void* base, bool half, uint64_t 
   const cuuint64_t strides[3] = {ld * 2, 128, rows * ld * 2};
   const cuuint32_t box[4] = {64, 64, chunks, 1};
   return encode(map, type16(half), 4, base, dims, strides, box, true,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// [E, 2, inter, K] seen as [E, inter / 8, 2, 8, K]: boxes of eight 8-row groups of
+// gate weights, each followed by the same rows of the up weights.
+bool make_tmap_rag_gated(CUtensorMap* map, const void* base, bool half, uint64_t K,
+                         uint64_t inter, uint64_t E) {
+  if (inter % 8 != 0) return false;
+  const cuuint64_t dims[5] = {K, 8, 2, inter / 8, E};
+  const cuuint64_t strides[4] = {K * 2, inter * K * 2, 8 * K * 2, 2 * inter * K * 2};
+  const cuuint32_t box[5] = {64, 8, 2, 8, 1};
+  return encode(map, type16(half), 5, base, dims, strides, box, true,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 

@@ -15,6 +15,10 @@ bool make_tmap_rag(CUtensorMap* map, const void* base, bool half, int rank, uint
 // brings `chunks` boxes of 64 x 64 values, side by side in the matrix.
 bool make_tmap_rag_wide(CUtensorMap* map, const void* base, bool half, uint64_t rows,
                         uint64_t cols, uint64_t batch, uint64_t ld, uint32_t chunks);
+// Gate and up weights [E, 2 inter, K] (gate rows first, inter a multiple of 8): a box
+// is 128 rows of 64 values, eight of gate and the same eight of up in turn.
+bool make_tmap_rag_gated(CUtensorMap* map, const void* base, bool half, uint64_t K,
+                         uint64_t inter, uint64_t E);
 // dw [E, N, K] for stores (elem 0 bf16, 1 fp16, 2 fp32; dense): boxes of 128
 // bytes x 32 rows.
 bool make_tmap_rag_store(CUtensorMap* map, const void* base, int elem, uint64_t K, uint64_t N,

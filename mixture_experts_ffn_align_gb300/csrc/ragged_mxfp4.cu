@@ -22,7 +22,7 @@
 //  * A slot holds a 32-bit word (four scales, 128 of K) for each row: for two
 //    such words an operand has two 16-column places in tensor memory, and MMA j
 //    of a step takes word j / 2 and its bytes 2 (j % 2) and 2 (j % 2) + 1.
-//  * every wait is bounded, as in ragged_gemm.cu.
+//  * every wait is bounded, as in ragged_one.cuh.
 //
 // Few rows are bound by the weights' 0.53 bytes a value: 512 rows, 64 experts,
 // 7168 -> 4096, 1.0 GB: 180 us here and on SM pairs.  8192 rows, 8 experts, 4096 ->

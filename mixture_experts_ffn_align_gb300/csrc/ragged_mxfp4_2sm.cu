@@ -15,7 +15,7 @@
 //  * else one accumulator of 256 columns, beside it the four slots' places: eight
 //    epilogue warps first read it whole, as packed 16-bit pairs, hand it back,
 //    and store while the next tile's MMAs run.
-//  * fixed tile order, bounded waits and teardown as in ragged_gemm_2sm.cu.
+//  * fixed tile order, bounded waits and teardown as in ragged_pair.cuh.
 //
 // 8192 rows, 8 experts, 4096 -> 28672: 363 us in bursts, 377 in long runs (5.1
 // PFLOP/s).  The tensor pipe is busy 55% of the time, for two reasons: a tile's MMAs
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
     }
-    // tail wait, as in ragged_gemm_2sm.cu
+    // tail wait, as in ragged_pair.cuh
     for (int s = 0; lane == 0 && s < STAGES; ++s)
       if ((issued_mask & (1u << s)) && !wait(empty_bar(s), (issued_parity >> s) & 1)) break;
     // the leader's barriers count both CTAs' copies

@@ -5,7 +5,9 @@ oracle (test infrastructure only), from the formulas:
   wgrad dW_e = sum_r dy[r] x[r]^T over the rows offsets[e] .. offsets[e+1]-1;
 * MXFP4: per 32 values a power-of-two scale and E2M1 codes (OCP Microscaling
   Formats specification v1.0, section 6.3, for the floor form);
-* clip: c = min(1, max_norm / (norm + 1e-6)) over all tensors' L2 norm.
+* clip: c = min(1, max_norm / (norm + 1e-6)) over all tensors' L2 norm;
+* the gated block z = g' s(alpha g') (u' + beta) and its gradient;
+* orthogonalised update: X <- (a I + b A + c A^2) X, A = X X^T.
 """
 from __future__ import annotations
 
@@ -89,3 +91,45 @@ def clip(grads, max_norm):
     norm = float(np.sqrt(sum(np.sum(np.square(g)) for g in grads)))
     c = min(1.0, max_norm / (norm + 1e-6))
     return norm, [g * c for g in grads]
+
+
+def _sigmoid(v):
+    with np.errstate(over="ignore"):
+        return 1.0 / (1.0 + np.exp(-v))
+
+
+def gated(h, alpha=1.0, beta=0.0, limit=0.0):
+    """z of the gate's and up projection's values h [R, 2 I]."""
+    g, u = np.split(h, 2, axis=1)
+    if limit > 0:
+        g, u = np.minimum(g, limit), np.clip(u, -limit, limit)
+    return g * _sigmoid(alpha * g) * (u + beta)
+
+
+def gated_grad(dz, h, alpha=1.0, beta=0.0, limit=0.0):
+    """Gradient by h of sum(dz * gated(h)): 0 for what lies outside the limit."""
+    g, u = np.split(h, 2, axis=1)
+    gc, uc = g, u
+    if limit > 0:
+        gc, uc = np.minimum(g, limit), np.clip(u, -limit, limit)
+    s = _sigmoid(alpha * gc)
+    dg = dz * (uc + beta) * s * (1 + alpha * gc * (1 - s))
+    du = dz * gc * s
+    if limit > 0:
+        dg, du = np.where(g > limit, 0.0, dg), np.where(np.abs(u) > limit, 0.0, du)
+    return np.concatenate([dg, du], 1)
+
+
+def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, rounded=None):
+    """Newton-Schulz steps on one matrix.  rounded: applied to every operand of a
+    product (X, A, B of the shorter side), to see what operands of a type cost."""
+    r = rounded or (lambda v: v)
+    x = np.asarray(g, dtype=np.float64)
+    x = x if x.shape[0] <= x.shape[1] else x.T
+    x = r(x / (np.sqrt((x * x).sum()) + eps))
+    for i in range(steps):
+        a, b, c = coefficients[i] if np.ndim(coefficients) == 2 else coefficients
+        m = r(x @ x.T)
+        x = r(a * np.eye(len(m)) + b * m + c * (m @ m)) @ x
+        x = r(x) if i + 1 < steps else x
+    return x if g.shape[0] <= g.shape[1] else x.T
