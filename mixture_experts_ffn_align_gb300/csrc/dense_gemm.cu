@@ -7,29 +7,46 @@ namespace moe {
 
 namespace {
 
-// Tiles, and CTAs that share the reduction of one.  Symmetric outputs are computed
-// in square tiles on and below the diagonal, unless there are so few tiles that the
-// reduction is sliced.
+// Tiles, and CTAs that share the reduction of one, and the cycles that takes.
 struct DensePlan {
   int tile_rows, per, tok_tiles, w_tiles, splits;
   bool tri;
-  long long e_tiles;
+  long long e_tiles, cycles;
 };
+// The plan of least modelled time.  A step takes its operands from L2 at some 55 bytes
+// a cycle, or its MMAs; a tile's epilogue runs under the next tile's steps, the last
+// one's and a kernel's start do not; a sliced reduction adds its sums' way through L2.
+// Small products want narrow token tiles (more SMs, fewer bytes a step) and slices,
+// long ones wide tiles; a symmetric output square ones on and below the diagonal.
+// (8 matrices of 256 x 512, a step of 3 products: 38 us with 256 tokens a tile.)
 DensePlan plan_of(const DenseProduct& d) {
-  DensePlan r;
-  r.tile_rows = d.m <= 32 ? 32 : d.m <= 64 ? 64 : d.m <= 128 ? 128 : 256;
-  r.w_tiles = (d.width + 127) / 128;
-  r.tok_tiles = (d.m + r.tile_rows - 1) / r.tile_rows;
-  r.per = ((d.m + r.tok_tiles - 1) / r.tok_tiles + 15) / 16 * 16;
-  r.e_tiles = (long long)r.w_tiles * r.tok_tiles;
-  r.splits = rag_slices(r.e_tiles * d.E, d.segs * d.seg_kb, kLeastSteps);
-  r.tri = d.symmetric && r.splits == 1;
-  if (r.tri) {
-    r.tile_rows = r.per = 128;
-    r.tok_tiles = r.w_tiles;
-    r.e_tiles = (long long)r.w_tiles * (r.w_tiles + 1) / 2;
+  DensePlan best{};
+  const long long kb = (long long)d.segs * d.seg_kb;
+  for (int tile = 32; tile <= 256; tile *= 2) {
+    if (tile > 32 && tile >= 2 * d.m) break;
+    for (int mode = 0; mode < 5; ++mode) {            // slices, or the triangle
+      DensePlan r;
+      r.tri = mode == 4;
+      r.splits = r.tri ? 1 : 1 << mode;
+      if (r.tri && (!d.symmetric || tile != 128)) continue;
+      r.tile_rows = tile;
+      r.w_tiles = (d.width + 127) / 128;
+      const int rows = d.symmetric ? d.width : d.m, unit = d.symmetric ? 32 : 16;
+      r.tok_tiles = (rows + tile - 1) / tile;
+      r.per = r.tri ? tile : ((rows + r.tok_tiles - 1) / r.tok_tiles + unit - 1) / unit * unit;
+      r.e_tiles = r.tri ? (long long)r.w_tiles * (r.w_tiles + 1) / 2
+                        : (long long)r.w_tiles * r.tok_tiles;
+      const long long tiles = r.e_tiles * d.E;
+      if (r.splits > 1 && (tiles > kRagClusters[3 - mode] || kb < 2 * r.splits)) continue;
+      const long long steps = (kb + r.splits - 1) / r.splits;
+      const long long step = std::max((16384 + (r.per + 31) / 32 * 4096) / 55, 53 * r.per / 20);
+      const long long epilogue = (r.tri ? 1500 : 1000) * ((r.per + 63) / 64);
+      r.cycles = 5000 + (tiles * r.splits + 151) / 152 * std::max(steps * step, epilogue) + epilogue +
+                 (r.splits > 1 ? 3500 : 0);
+      if (best.cycles == 0 || r.cycles < best.cycles) best = r;
+    }
   }
-  return r;
+  return best;
 }
 
 }  // namespace
@@ -41,21 +58,13 @@ size_t dense_part_bytes(const DenseProduct& d) {
 
 bool dense_on_pairs(const DenseProduct& d) {
   if (ragged_form() != 0) return ragged_form() != 1;
-  const DensePlan r = plan_of(d);
   const long long kb = (long long)d.segs * d.seg_kb;
-  // Cycles as the ragged products' model has them: a step's operands at 50 bytes a
-  // cycle from L2 or its MMAs, and a tile's fixed cost.
-  const auto step = [](int a, int b, int n) { return std::max((a + b) / 50, 53 * n / 20); };
-  const int n1 = r.tri ? 128 : r.per;
-  const long long tiles1 = r.e_tiles * d.E;
-  const long long one = r.splits > 1
-                            ? kb / r.splits * step(16384, n1 * 128, n1) + 4000 + 50 * n1
-                            : (tiles1 + 151) / 152 * (kb * step(16384, n1 * 128, n1) + 1200);
-  const int w2 = (d.width + 255) / 256, t2 = (d.m + 255) / 256;
-  const int n2 = d.symmetric ? 256 : ((d.m + t2 - 1) / t2 + 31) / 32 * 32;
-  const long long tiles2 = (d.symmetric ? (long long)w2 * (w2 + 1) / 2 : (long long)w2 * t2) * d.E;
-  const long long two = (tiles2 + 75) / 76 * (kb * step(16384, n2 * 64, n2) + 1400) + 3000;
-  return two < one;
+  const int w = (d.width + 255) / 256, t = (d.m + 255) / 256;
+  const int n = d.symmetric ? 256 : ((d.m + t - 1) / t + 31) / 32 * 32;
+  const long long tiles = (d.symmetric ? (long long)w * (w + 1) / 2 : (long long)w * t) * d.E;
+  const long long step = std::max((16384 + n * 64) / 55, 53 * n / 20);
+  const long long epilogue = (d.symmetric ? 1500 : 1000) * ((n + 63) / 64);
+  return 8000 + (tiles + 75) / 76 * std::max(kb * step, epilogue) + epilogue < plan_of(d).cycles;
 }
 
 cudaError_t launch_dense(const DenseProduct& d, void* workspace, cudaStream_t stream) {

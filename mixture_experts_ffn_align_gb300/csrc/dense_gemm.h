@@ -49,6 +49,7 @@ inline void dense_args(const DenseProduct& d, bool tri, int per, int tok_tiles, 
   RagDense& q = a.dense;
   q.m = d.m;
   q.mp = d.width;
+  q.sym = d.symmetric;
   q.tri = tri;
   q.per = per;
   q.tok_tiles = tok_tiles;

@@ -37,14 +37,64 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPrecise = 256;                 // shorter sides up to here take hi and lo parts
 constexpr float kScaleX = 4096.0f, kScaleA = 1024.0f, kScaleB = 1024.0f;
-constexpr int kMaxChunks = 1024;              // partial sums of a matrix
-constexpr int kStrip = 512;                   // columns of X a block writes
+constexpr int kMaxChunks = 304;               // partial sums of a matrix
+constexpr int kRowsPerThread = 4, kTiles = 2; // of k_ortho_scale, k_ortho_transpose
 
 template <int TYPE>
 __device__ __forceinline__ float load1(const void* p, long long i) {
   if (TYPE == 2) return static_cast<const float*>(p)[i];
   const uint16_t b = static_cast<const uint16_t*>(p)[i];
   return TYPE == 0 ? Half16<__nv_bfloat16>::value(b) : Half16<__half>::value(b);
+}
+// The two (16-bit) values of a word.
+template <int TYPE>
+__device__ __forceinline__ float2 word2(uint32_t w) {
+  using T = typename std::conditional<TYPE == 1, __half, __nv_bfloat16>::type;
+  return make_float2(Half16<T>::value((uint16_t)(w & 0xFFFFu)),
+                     Half16<T>::value((uint16_t)(w >> 16)));
+}
+// n (at most 8) values from element i, zeros behind them; `wide`: i and n are whole
+// 16-byte pieces.
+template <int TYPE>
+__device__ __forceinline__ void load8(const void* p, long long i, int n, bool wide, float (&v)[8]) {
+  if (wide) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) +
+                                                    i * (TYPE == 2 ? 4 : 2));
+    const uint4 a = n > 0 ? __ldg(q) : make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    if (TYPE == 2) {
+      const uint4 b = n > 4 ? __ldg(q + 1) : make_uint4(0, 0, 0, 0);
+      const uint32_t x[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = __uint_as_float(w[k]);
+        v[4 + k] = __uint_as_float(x[k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = word2<TYPE>(w[k]);
+        v[2 * k] = f.x;
+        v[2 * k + 1] = f.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k < n ? load1<TYPE>(p, i + k) : 0.0f;
+  }
+}
+// Eight values as fp16, and what that leaves of them lo columns on.
+__device__ __forceinline__ void store8(__half* out, int lo, float inv, const float (&v)[8]) {
+  uint32_t hi[4], rest[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float x = v[2 * k] * inv, y = v[2 * k + 1] * inv;
+    const __half2 h = __floats2half2_rn(x, y);
+    hi[k] = *reinterpret_cast<const uint32_t*>(&h);
+    rest[k] = Half16<__half>::pack(x - __low2float(h), y - __high2float(h));
+  }
+  *reinterpret_cast<uint4*>(out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  if (lo != 0) *reinterpret_cast<uint4*>(out + lo) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
 }
 
 __device__ __forceinline__ double block_sum(double v, double* smem) {
@@ -58,8 +108,9 @@ __device__ __forceinline__ double block_sum(double v, double* smem) {
   return v;
 }
 
-// Squares of part blockIdx.x of matrix blockIdx.y (n elements): in fp32 over 16
-// values, in fp64 beyond.
+// Squares of part blockIdx.x of matrix blockIdx.y (n elements): in fp32 over at most
+// 64 values, in fp64 beyond (fp64 additions and conversions are slow enough to
+// bound the pass if there is one for every few values).
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads) k_ortho_norm(const void* g, long long n, int chunks,
                                                          double* partial) {
@@ -75,98 +126,138 @@ __global__ void __launch_bounds__(kThreads) k_ortho_norm(const void* g, long lon
   const long long pieces = (n - head) / per;
   const uint4* p = reinterpret_cast<const uint4*>(base + head * size);
   const long long end = pieces * (blockIdx.x + 1) / chunks;
-  for (long long i = pieces * blockIdx.x / chunks + threadIdx.x; i < end; i += 4 * kThreads) {
-    uint4 v[4];
+  for (long long i = pieces * blockIdx.x / chunks + threadIdx.x; i < end; i += 8 * kThreads) {
+    uint4 v[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 8; ++k)
       v[k] = i + k * kThreads < end ? __ldg(p + i + k * kThreads) : make_uint4(0, 0, 0, 0);
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-      float s = 0.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (TYPE == 2) {
           const float f = __uint_as_float(w[j]);
-          s += f * f;
+          s[j] += f * f;
         } else {
-          using T = typename std::conditional<TYPE == 1, __half, __nv_bfloat16>::type;
-          const float lo = Half16<T>::value((uint16_t)(w[j] & 0xFFFFu));
-          const float hi = Half16<T>::value((uint16_t)(w[j] >> 16));
-          s += lo * lo;
-          s += hi * hi;
+          const float2 f = word2<TYPE>(w[j]);
+          s[j] += f.x * f.x;
+          s[j] += f.y * f.y;
         }
       }
-      sum += s;
     }
+    sum += (s[0] + s[1]) + (s[2] + s[3]);
   }
   if (blockIdx.x == 0 && threadIdx.x < 32) {
     const long long tail = head + pieces * per;
     if (threadIdx.x < head) {
       const float f = load1<TYPE>(base, threadIdx.x);
-      sum += (double)f * f;
+      sum += f * f;
     }
     if (threadIdx.x < n - tail) {
       const float f = load1<TYPE>(base, tail + threadIdx.x);
-      sum += (double)f * f;
+      sum += f * f;
     }
   }
   sum = block_sum(sum, smem);
   if (threadIdx.x == 0) partial[(size_t)blockIdx.y * chunks + blockIdx.x] = sum;
 }
 
-// X of matrix blockIdx.z: rows from 64 blockIdx.y, columns from kStrip blockIdx.x, and
-// zeros behind its M columns.
-template <int TYPE, bool TRANSPOSED>
+// Factor from matrix e's values to X's.  One warp adds, one lane divides: fp64 by
+// every thread took four times as long as the copy (466 against 70 us of the norm's
+// own pass over the same bytes).
+__device__ __forceinline__ float scale_of(const double* partial, int chunks, int e, float eps,
+                                          float* smem) {
+  if (threadIdx.x < 32) {
+    double total = 0.0;
+    for (int i = threadIdx.x; i < chunks; i += 32) total += partial[(size_t)e * chunks + i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (threadIdx.x == 0) *smem = (float)((double)kScaleX / (sqrt(total) + (double)eps));
+  }
+  __syncthreads();
+  return *smem;
+}
+
+// X of matrix blockIdx.z from g [m, M], zeros behind its M columns.  A thread takes
+// eight columns of kRowsPerThread rows, 1 << log_tx threads a row.
+template <int TYPE>
 __global__ void __launch_bounds__(kThreads)
-    k_ortho_scale(const void* g, int m, int M, int Mp, int ld, int lo, int chunks,
-                  const double* partial, float eps, __half* x) {
-  __shared__ double smem[kThreads / 32];
-  __shared__ float tile[TRANSPOSED ? 64 : 1][65];
+    k_ortho_scale(const void* g, int m, int M, int Mp, int ld, int lo, int log_tx, bool wide,
+                  int chunks, const double* partial, float eps, __half* x) {
+  __shared__ float smem;
   griddep_launch();
   griddep_wait();
-  double total = 0.0;
-  for (int i = threadIdx.x; i < chunks; i += kThreads) total += partial[(size_t)blockIdx.z * chunks + i];
-  total = block_sum(total, smem);
-  const float inv = (float)((double)kScaleX / (sqrt(total) + (double)eps));
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int rows = kThreads >> log_tx;
+  const int c = 8 * ((blockIdx.x << log_tx) + (threadIdx.x & ((1 << log_tx) - 1)));
+  const long long first = (long long)blockIdx.z * m;
+  float inv = 0.0f;
+  for (int i = blockIdx.y; i * rows * kRowsPerThread < m; i += gridDim.y) {
+    const int r0 = i * rows * kRowsPerThread + (threadIdx.x >> log_tx);
+    float v[kRowsPerThread][8];
+#pragma unroll
+    for (int u = 0; u < kRowsPerThread; ++u) {
+      const int r = r0 + u * rows;
+      load8<TYPE>(g, (first + r) * M + c, r < m ? min(M - c, 8) : 0, wide, v[u]);
+    }
+    // the sums of squares while the loads are on their way
+    if (i == blockIdx.y) inv = scale_of(partial, chunks, blockIdx.z, eps, &smem);
+#pragma unroll
+    for (int u = 0; u < kRowsPerThread; ++u) {
+      const int r = r0 + u * rows;
+      if (r < m && c < Mp) store8(x + (first + r) * ld + c, lo, inv, v[u]);
+    }
+  }
+}
+
+// The same from g [M, m]: tiles of 64 x 64 through shared memory, as fp16 pairs of
+// neighbouring columns of X.  Lanes take 4 x 8 pieces when they write the tile and 8
+// x 4 when they read it, so that with rows of 33 words no bank is hit twice.
+template <int TYPE, bool LO>
+__global__ void __launch_bounds__(kThreads)
+    k_ortho_transpose(const void* g, int m, int M, int Mp, int ld, int lo, bool wide, int chunks,
+                      const double* partial, float eps, __half* x) {
+  __shared__ float smem;
+  __shared__ uint32_t tile[LO ? 2 : 1][64][33];
+  griddep_launch();
+  griddep_wait();
+  const int ra = 8 * ((threadIdx.x & 3) + 4 * (threadIdx.x >> 7)), pair = (threadIdx.x >> 2) & 31;
+  const int cb = threadIdx.x & 7, rb = threadIdx.x >> 3;
   const int r0 = 64 * blockIdx.y;
-  const long long base = (long long)blockIdx.z * m * M;
-  const int c_end = min((int)(blockIdx.x + 1) * kStrip, Mp);
-  for (int c0 = blockIdx.x * kStrip; c0 < c_end; c0 += 64) {
-    if (TRANSPOSED) {            // g is [M, m]
-      __syncthreads();
+  const long long first = (long long)blockIdx.z * M;
+  float inv = 0.0f;
+  const int c_end = min(Mp, (int)(blockIdx.x + 1) * 64 * kTiles);
+  for (int c0 = blockIdx.x * 64 * kTiles; c0 < c_end; c0 += 64) {
+    float v[2][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = c0 + ty + 8 * i;
+    for (int u = 0; u < 2; ++u) {
+      const int c = c0 + 2 * pair + u;
+      load8<TYPE>(g, (first + c) * m + r0 + ra, c < M ? min(m - r0 - ra, 8) : 0, wide, v[u]);
+    }
+    if (c0 == blockIdx.x * 64 * kTiles) inv = scale_of(partial, chunks, blockIdx.z, eps, &smem);
+    __syncthreads();               // the tile before has been read
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r = r0 + tx + 32 * k;
-          tile[tx + 32 * k][ty + 8 * i] =
-              c < M && r < m ? load1<TYPE>(g, base + (long long)c * m + r) : 0.0f;
+    for (int k = 0; k < 8; ++k) {
+      float a = v[0][k] * inv, b = v[1][k] * inv;
+      const __half2 h = __floats2half2_rn(a, b);
+      tile[0][ra + k][pair] = *reinterpret_cast<const uint32_t*>(&h);
+      if (LO)
+        tile[LO ? 1 : 0][ra + k][pair] =
+            Half16<__half>::pack(a - __low2float(h), b - __high2float(h));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int row = rb + 32 * u;
+      if (r0 + row < m) {
+        __half* out = x + ((long long)blockIdx.z * m + r0 + row) * ld + c0 + 8 * cb;
+#pragma unroll
+        for (int p = 0; p < (LO ? 2 : 1); ++p) {
+          const uint32_t* w = &tile[p][row][4 * cb];
+          *reinterpret_cast<uint4*>(out + p * lo) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = r0 + ty + 8 * i, c = c0 + 2 * tx;
-      if (r >= m) continue;
-      float v[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (TRANSPOSED)
-          v[k] = tile[ty + 8 * i][2 * tx + k];
-        else
-          v[k] = c + k < M ? load1<TYPE>(g, base + (long long)r * M + c + k) : 0.0f;
-        v[k] *= inv;
-      }
-      __half* out = x + ((long long)blockIdx.z * m + r) * ld + c;
-      const __half2 hi = __floats2half2_rn(v[0], v[1]);
-      *reinterpret_cast<__half2*>(out) = hi;
-      if (lo != 0)
-        *reinterpret_cast<__half2*>(out + lo) =
-            __floats2half2_rn(v[0] - __low2float(hi), v[1] - __high2float(hi));
     }
   }
 }
@@ -241,7 +332,7 @@ Layout layout(int E, int N, int K) {
   l.parts = l.m <= kPrecise ? 2 : 1;
   const long long n = (long long)N * K;
   l.chunks = (int)std::max<long long>(
-      1, std::min<long long>({(n + 8191) / 8192, kMaxChunks, std::max(1, 2432 / E)}));
+      1, std::min<long long>({(n + 8191) / 8192, kMaxChunks, std::max(1, 1216 / E)}));
   l.x_bytes = pad((size_t)E * l.m * l.parts * l.Mp * 2);
   l.a_bytes = pad((size_t)E * l.m * l.parts * l.mp * 2);
   l.partial = 0;
@@ -266,7 +357,7 @@ cudaError_t run(const DenseProduct& d, void* part, cudaStream_t stream) {
 
 template <int TYPE>
 cudaError_t prepare(const Layout& l, int E, bool transposed, const void* g, float eps,
-                    double* partial, void* x, cudaStream_t stream) {
+                    double* partial, __half* x, cudaStream_t stream) {
   const long long n = (long long)l.m * l.M;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -277,14 +368,25 @@ cudaError_t prepare(const Layout& l, int E, bool transposed, const void* g, floa
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(l.chunks, E, 1);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, k_ortho_norm<TYPE>, g, n, l.chunks, partial);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_ortho_norm<TYPE>, g, n, l.chunks, partial);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((l.Mp + kStrip - 1) / kStrip, (l.m + 63) / 64, E);
   const int ld = l.parts * l.Mp, lo = l.parts == 2 ? l.Mp : 0;
   const double* sums = partial;
-  return cudaLaunchKernelEx(&cfg, transposed ? k_ortho_scale<TYPE, true> : k_ortho_scale<TYPE, false>,
-                            g, l.m, l.M, l.Mp, ld, lo, l.chunks, sums, eps,
-                            static_cast<__half*>(x));
+  // rows of g in whole 16-byte pieces
+  const bool wide = reinterpret_cast<uintptr_t>(g) % 16 == 0 &&
+                    (transposed ? l.m : l.M) % (TYPE == 2 ? 4 : 8) == 0;
+  if (transposed) {
+    cfg.gridDim = dim3((l.Mp / 64 + kTiles - 1) / kTiles, (l.m + 63) / 64, E);
+    return cudaLaunchKernelEx(&cfg, lo ? k_ortho_transpose<TYPE, true> : k_ortho_transpose<TYPE, false>, g, l.m, l.M, l.Mp, ld, lo, wide,
+                              l.chunks, sums, eps, x);
+  }
+  int log_tx = 3;
+  while (log_tx < 8 && 8 << log_tx < l.Mp) ++log_tx;
+  const int rows = (kThreads >> log_tx) * kRowsPerThread;
+  cfg.gridDim = dim3((l.Mp / 8 + (1 << log_tx) - 1) >> log_tx, std::min((l.m + rows - 1) / rows, 32768),
+                     E);
+  return cudaLaunchKernelEx(&cfg, k_ortho_scale<TYPE>, g, l.m, l.M, l.Mp, ld, lo, log_tx, wide,
+                            l.chunks, sums, eps, x);
 }
 
 }  // namespace
@@ -299,9 +401,10 @@ cudaError_t launch_orthogonalize(int E, int N, int K, const void* g, int type, v
   char* ws = static_cast<char*>(workspace);
   void *a = ws + l.a, *b = ws + l.b, *x = ws + l.x0, *y = ws + l.x1, *part = ws + l.part;
   double* partial = reinterpret_cast<double*>(ws + l.partial);
-  cudaError_t e = type == 0   ? prepare<0>(l, E, transposed, g, eps, partial, x, stream)
-                  : type == 1 ? prepare<1>(l, E, transposed, g, eps, partial, x, stream)
-                              : prepare<2>(l, E, transposed, g, eps, partial, x, stream);
+  __half* x0 = static_cast<__half*>(x);
+  cudaError_t e = type == 0   ? prepare<0>(l, E, transposed, g, eps, partial, x0, stream)
+                  : type == 1 ? prepare<1>(l, E, transposed, g, eps, partial, x0, stream)
+                              : prepare<2>(l, E, transposed, g, eps, partial, x0, stream);
   for (int s = 0; s < steps && e == cudaSuccess; ++s) {
     e = run(gram(l, E, x, a), part, stream);
     if (e != cudaSuccess) return e;

@@ -68,9 +68,10 @@ struct RagGated {
 // Arguments of a batch of dense products of E matrices of m rows (ragged_epi.cuh).
 struct RagDense {
   int m;                    // rows of a matrix
-  int mp;                   // tri: columns of the output, m rounded up to 64
-  int tri;                  // symmetric output: tiles on and below the diagonal
-  int per;                  // rows of a token tile
+  int sym;                  // symmetric output, stored as rows from its columns
+  int mp;                   // sym: columns of the output, m rounded up to 64
+  int tri;                  // sym: tiles on and below the diagonal, stored on both sides
+  int per;                  // rows of a token tile; sym: a multiple of 32
   int tok_tiles;
   FastDiv e_tiles;          // tiles of a matrix
   int seg_kb;               // steps of each of the reduction's segments (hi and lo parts)

@@ -162,8 +162,8 @@ __device__ __forceinline__ void rag_gated_grad_tokens32(const RagArgs& a, const 
 
 // --------------------------------------------------------------- dense products
 // Tile t of the batch.  rows: of a symmetric product those of its padded output,
-// which has zeros there.  Symmetric: the tiles (w_tile, tok) with tok <= w_tile;
-// else groups of 8 token tiles, as rag_tile.
+// which has zeros there.  tri: the tiles (w_tile, tok) with tok <= w_tile; else
+// groups of 8 token tiles, as rag_tile.
 template <int G>
 __device__ __forceinline__ RagTile rag_dense_tile(const RagArgs& a, int t) {
   const RagDense& q = a.dense;
@@ -185,7 +185,7 @@ __device__ __forceinline__ RagTile rag_dense_tile(const RagArgs& a, int t) {
     const int l2 = l - 8 * c * w_tiles;
     T.w_tile = l2 / gm;
     T.tok = 8 * c + (l2 - T.w_tile * gm);
-    T.rows = min(q.per, q.m - T.tok * q.per);
+    T.rows = min(q.per, (q.sym ? q.mp : q.m) - T.tok * q.per);
   }
   T.row0 = T.e * q.m + T.tok * q.per;
   return T;
@@ -218,8 +218,7 @@ __device__ __forceinline__ void rag_dense_tokens32(const RagArgs& a, const RagTi
     __nv_bfloat16* out = q.final_out;
     if (q.transposed) {                       // a lane's tokens lie side by side
       out += ((long long)D.e * a.W + w) * q.m + tok;
-      if (w >= a.W) {
-      } else if (live >= 32 && q.m % 8 == 0) {
+      if (w < a.W && live >= 32 && q.m % 8 == 0) {
 #pragma unroll
         for (int j = 0; j < 32; j += 8)
           *reinterpret_cast<uint4*>(out + j) = make_uint4(
@@ -227,10 +226,39 @@ __device__ __forceinline__ void rag_dense_tokens32(const RagArgs& a, const RagTi
               Half16<__nv_bfloat16>::pack(v[j + 2], v[j + 3]),
               Half16<__nv_bfloat16>::pack(v[j + 4], v[j + 5]),
               Half16<__nv_bfloat16>::pack(v[j + 6], v[j + 7]));
-      } else {
+      }
+      if (live < 32 || q.m % 8 != 0) {
+        // Rows that start anywhere, or end here: the warp's 32 x 32 values are turned
+        // (pairs of tokens in a register, halves swapped between lanes 16 to 1
+        // apart), so that a store writes one row's 32 tokens.  From each lane's own row
+        // they went out as 32 sectors for 64 bytes (16 matrices of 1031 x 517: 90 us).
+        uint32_t pk[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j < live) out[j] = __float2bfloat16_rn(v[j]);
+        for (int j = 0; j < 16; ++j) pk[j] = Half16<__nv_bfloat16>::pack(v[2 * j], v[2 * j + 1]);
+#pragma unroll
+        for (int o = 16; o >= 2; o >>= 1) {
+          const bool up = lane & o;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (j & (o >> 1)) continue;
+            const int k = j | (o >> 1);
+            const uint32_t x = __shfl_xor_sync(0xffffffffu, up ? pk[j] : pk[k], o);
+            if (up) pk[j] = x; else pk[k] = x;
+          }
+        }
+        // now pk[j]: tokens (lane & ~1) and the next of row 2 j + (lane & 1) of the 32
+        __nv_bfloat16* base_out =
+            q.final_out + ((long long)D.e * a.W + (w - lane)) * q.m + tok + lane;
+        const uint32_t sel = (lane & 1) ? 0x3276u : 0x5410u;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t x = __byte_perm(pk[j], __shfl_xor_sync(0xffffffffu, pk[j], 1), sel);
+          // the low half is this lane's token of row 2 j, the high half that of the next
+          const int row = w - lane + 2 * j;
+          uint16_t* p = reinterpret_cast<uint16_t*>(base_out) + (long long)2 * j * q.m;
+          if (lane < live && row < a.W) *p = (uint16_t)(x & 0xFFFFu);
+          if (lane < live && row + 1 < a.W) p[q.m] = (uint16_t)(x >> 16);
+        }
       }
       return;
     }
@@ -248,7 +276,7 @@ __device__ __forceinline__ void rag_dense_tokens32(const RagArgs& a, const RagTi
     return;
   }
   uint16_t* out = static_cast<uint16_t*>(a.out);
-  if (q.tri) {
+  if (q.sym) {
     // This lane's tokens as row w of the output: 64 bytes of it.  What lies past
     // the matrix's columns is zero (those rows may be the next matrix's).
     if (w < q.m) {
@@ -294,7 +322,7 @@ __device__ __forceinline__ void rag_dense_tokens32(const RagArgs& a, const RagTi
           p[q.lo / 8 + i] = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
       }
     }
-    if (D.tok != D.w_tile) {                  // and as column w
+    if (q.tri && D.tok != D.w_tile) {         // and as column w
       out += (base + tok) * a.ldo + w;
       rag_store_packed32(pk, out, a.ldo, live, w, a.W, lane);
       if (q.lo != 0) rag_store_packed32(lo, out + q.lo, a.ldo, live, w, a.W, lane);
@@ -366,6 +394,7 @@ __device__ __forceinline__ void rag_join_store(const RagArgs& a, const RagTile& 
     if (w >= a.W) return;
     float v[4] = {q.c_acc * x.x, q.c_acc * x.y, q.c_acc * x.z, q.c_acc * x.w};
     const int tok = (int)(row - (long long)D.e * q.m);
+    if (tok >= q.m) return;                   // sym: rows of the padded output only
     if (q.final_out != nullptr) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)

@@ -175,6 +175,9 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
         boxes = (D.rows + 31) / 32;
       }
       bool ok = true;
+      // EPI_DENSE: hi x hi, hi x lo and lo x hi parts one after the other
+      int seg = EPI == EPI_DENSE ? kb0 / args.dense.seg_kb : 0;
+      int seg_k = EPI == EPI_DENSE ? kb0 - seg * args.dense.seg_kb : 0;
       for (int kb = 0; kb < kb_n; ++kb) {
         if (!warp_wait(empty_bar(stage), phase ^ 1)) {
           ok = false;
@@ -210,9 +213,7 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
             }
           } else if (one) {
             mbar_arrive_expect_tx(bar, A_BYTES + boxes * 32 * BK * 2);
-            // hi x hi, hi x lo, lo x hi parts one after the other (EPI_DENSE)
-            const int seg = EPI == EPI_DENSE ? (kb0 + kb) / args.dense.seg_kb : 0;
-            const int k0 = (kb0 + kb - (seg ? seg * args.dense.seg_kb : 0)) * BK;
+            const int k0 = (EPI == EPI_DENSE ? seg_k : kb0 + kb) * BK;
             const int a_lo = seg == 1 ? args.dense.a_lo : 0, b_lo = seg == 2 ? args.dense.b_lo : 0;
             if (EPI == EPI_GATED) {
               tma_load_5d(sa, &tmA, bar, k0, D.w_tile * 8, D.e, pol_w);
@@ -229,6 +230,10 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
           }
           issued_mask |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+        }
+        if (EPI == EPI_DENSE && ++seg_k == args.dense.seg_kb) {
+          seg_k = 0;
+          ++seg;
         }
         if (++stage == stages) {
           stage = 0;

@@ -182,6 +182,8 @@ __global__ void __launch_bounds__(num_threads(OP, MT, EPI), 1)
         a_tiles = rag_second_tile<MT>(args, D.w_tile) ? 2 : 1;
       }
       bool ok = true;
+      // EPI_DENSE: hi x hi, hi x lo and lo x hi parts one after the other
+      int seg = 0, seg_k = 0;
       for (int kb = 0; kb < kb_n; ++kb) {
         if (!(LONE ? wait(empty_bar(stage), phase ^ 1) : warp_wait(empty_bar(stage), phase ^ 1))) {
           ok = false;
@@ -224,9 +226,7 @@ __global__ void __launch_bounds__(num_threads(OP, MT, EPI), 1)
               tma_load_2d_pair(sb + 8192, &tmB, bar, k0 + 64, r0, pol_t);
             }
           } else if (one) {
-            // hi x hi, hi x lo, lo x hi parts one after the other (EPI_DENSE)
-            const int seg = EPI == EPI_DENSE ? kb / args.dense.seg_kb : 0;
-            const int k0 = (kb - (seg ? seg * args.dense.seg_kb : 0)) * BK;
+            const int k0 = (EPI == EPI_DENSE ? seg_k : kb) * BK;
             const int a_lo = seg == 1 ? args.dense.a_lo : 0, b_lo = seg == 2 ? args.dense.b_lo : 0;
             for (int i = 0; i < a_tiles; ++i) {
               const int w0 = (D.w_tile * MT + i) * 256 + rank * 128;
@@ -250,6 +250,10 @@ __global__ void __launch_bounds__(num_threads(OP, MT, EPI), 1)
                 tma_load_2d_pair(sb + SMALL_BOX, &tmC, bar, k0 + b_lo, row0 + 32, pol_t);
             }
           }
+        }
+        if (EPI == EPI_DENSE && ++seg_k == args.dense.seg_kb) {
+          seg_k = 0;
+          ++seg;
         }
         if (++stage == STAGES) {
           stage = 0;
