@@ -38,7 +38,7 @@ constexpr int kThreads = 256;
 constexpr int kPrecise = 256;                 // shorter sides up to here take hi and lo parts
 constexpr float kScaleX = 4096.0f, kScaleA = 1024.0f, kScaleB = 1024.0f;
 constexpr int kMaxChunks = 304;               // partial sums of a matrix
-constexpr int kRowsPerThread = 4, kTiles = 2; // of k_ortho_scale, k_ortho_transpose
+constexpr int kRowsPerThread = 4, kTiles = 4; // of k_ortho_scale, k_ortho_transpose
 
 template <int TYPE>
 __device__ __forceinline__ float load1(const void* p, long long i) {
@@ -53,34 +53,52 @@ __device__ __forceinline__ float2 word2(uint32_t w) {
   return make_float2(Half16<T>::value((uint16_t)(w & 0xFFFFu)),
                      Half16<T>::value((uint16_t)(w >> 16)));
 }
-// n (at most 8) values from element i, zeros behind them; `wide`: i and n are whole
-// 16-byte pieces.
+// Eight values as they lie in memory: n (at most 8) from element i, zeros behind
+// them; `wide`: i and n are whole 16-byte pieces.
 template <int TYPE>
-__device__ __forceinline__ void load8(const void* p, long long i, int n, bool wide, float (&v)[8]) {
+struct Raw8 {
+  uint4 w[TYPE == 2 ? 2 : 1];
+};
+template <int TYPE>
+__device__ __forceinline__ Raw8<TYPE> load8(const void* p, long long i, int n, bool wide) {
+  Raw8<TYPE> r;
   if (wide) {
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) +
                                                     i * (TYPE == 2 ? 4 : 2));
-    const uint4 a = n > 0 ? __ldg(q) : make_uint4(0, 0, 0, 0);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-    if (TYPE == 2) {
-      const uint4 b = n > 4 ? __ldg(q + 1) : make_uint4(0, 0, 0, 0);
-      const uint32_t x[4] = {b.x, b.y, b.z, b.w};
+    r.w[0] = n > 0 ? __ldg(q) : make_uint4(0, 0, 0, 0);
+    if (TYPE == 2) r.w[TYPE == 2 ? 1 : 0] = n > 4 ? __ldg(q + 1) : make_uint4(0, 0, 0, 0);
+  } else if (TYPE == 2) {
+    uint32_t v[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[k] = __uint_as_float(w[k]);
-        v[4 + k] = __uint_as_float(x[k]);
-      }
-    } else {
+    for (int k = 0; k < 8; ++k) v[k] = k < n ? static_cast<const uint32_t*>(p)[i + k] : 0u;
+    r.w[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    r.w[TYPE == 2 ? 1 : 0] = make_uint4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint32_t v[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = word2<TYPE>(w[k]);
-        v[2 * k] = f.x;
-        v[2 * k + 1] = f.y;
-      }
+    for (int k = 0; k < 8; ++k) v[k] = k < n ? static_cast<const uint16_t*>(p)[i + k] : 0u;
+    r.w[0] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  }
+  return r;
+}
+template <int TYPE>
+__device__ __forceinline__ void unpack8(const Raw8<TYPE>& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+  if (TYPE == 2) {
+    const uint4& b = r.w[TYPE == 2 ? 1 : 0];
+    const uint32_t x[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = __uint_as_float(w[k]);
+      v[4 + k] = __uint_as_float(x[k]);
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k < n ? load1<TYPE>(p, i + k) : 0.0f;
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = word2<TYPE>(w[k]);
+      v[2 * k] = f.x;
+      v[2 * k + 1] = f.y;
+    }
   }
 }
 // Eight values as fp16, and what that leaves of them lo columns on.
@@ -195,18 +213,20 @@ __global__ void __launch_bounds__(kThreads)
   float inv = 0.0f;
   for (int i = blockIdx.y; i * rows * kRowsPerThread < m; i += gridDim.y) {
     const int r0 = i * rows * kRowsPerThread + (threadIdx.x >> log_tx);
-    float v[kRowsPerThread][8];
+    Raw8<TYPE> raw[kRowsPerThread];
 #pragma unroll
     for (int u = 0; u < kRowsPerThread; ++u) {
       const int r = r0 + u * rows;
-      load8<TYPE>(g, (first + r) * M + c, r < m ? min(M - c, 8) : 0, wide, v[u]);
+      raw[u] = load8<TYPE>(g, (first + r) * M + c, r < m ? min(M - c, 8) : 0, wide);
     }
     // the sums of squares while the loads are on their way
     if (i == blockIdx.y) inv = scale_of(partial, chunks, blockIdx.z, eps, &smem);
 #pragma unroll
     for (int u = 0; u < kRowsPerThread; ++u) {
       const int r = r0 + u * rows;
-      if (r < m && c < Mp) store8(x + (first + r) * ld + c, lo, inv, v[u]);
+      float v[8];
+      unpack8<TYPE>(raw[u], v);
+      if (r < m && c < Mp) store8(x + (first + r) * ld + c, lo, inv, v);
     }
   }
 }
@@ -215,7 +235,7 @@ __global__ void __launch_bounds__(kThreads)
 // neighbouring columns of X.  Lanes take 4 x 8 pieces when they write the tile and 8
 // x 4 when they read it, so that with rows of 33 words no bank is hit twice.
 template <int TYPE, bool LO>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, TYPE == 2 ? 5 : 6)
     k_ortho_transpose(const void* g, int m, int M, int Mp, int ld, int lo, bool wide, int chunks,
                       const double* partial, float eps, __half* x) {
   __shared__ float smem;
@@ -226,20 +246,27 @@ __global__ void __launch_bounds__(kThreads)
   const int cb = threadIdx.x & 7, rb = threadIdx.x >> 3;
   const int r0 = 64 * blockIdx.y;
   const long long first = (long long)blockIdx.z * M;
-  float inv = 0.0f;
   const int c_end = min(Mp, (int)(blockIdx.x + 1) * 64 * kTiles);
-  for (int c0 = blockIdx.x * 64 * kTiles; c0 < c_end; c0 += 64) {
-    float v[2][8];
+  const int begin = blockIdx.x * 64 * kTiles;
+  Raw8<TYPE> next[2];
+  auto load = [&](int c0) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int c = c0 + 2 * pair + u;
-      load8<TYPE>(g, (first + c) * m + r0 + ra, c < M ? min(m - r0 - ra, 8) : 0, wide, v[u]);
+      next[u] = load8<TYPE>(g, (first + c) * m + r0 + ra, c < M ? min(m - r0 - ra, 8) : 0, wide);
     }
-    if (c0 == blockIdx.x * 64 * kTiles) inv = scale_of(partial, chunks, blockIdx.z, eps, &smem);
-    __syncthreads();               // the tile before has been read
+  };
+  load(begin);
+  const float inv = scale_of(partial, chunks, blockIdx.z, eps, &smem);
+  for (int c0 = begin; c0 < c_end; c0 += 64) {
+    float v[2][8];
+    unpack8<TYPE>(next[0], v[0]);
+    unpack8<TYPE>(next[1], v[1]);
+    if (c0 + 64 < c_end) load(c0 + 64);      // while this tile is turned
+    __syncthreads();                         // the tile before has been read
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      float a = v[0][k] * inv, b = v[1][k] * inv;
+      const float a = v[0][k] * inv, b = v[1][k] * inv;
       const __half2 h = __floats2half2_rn(a, b);
       tile[0][ra + k][pair] = *reinterpret_cast<const uint32_t*>(&h);
       if (LO)

@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
   } else if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
+    [[maybe_unused]] const bool clamp = args.gated.limit < __int_as_float(0x7f800000);
     int local = 0, turn = 0;
     for (int t = first; t < total; t += stride) {
       RagTile D{};
@@ -358,6 +359,13 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
         continue;
       }
       const int acc = local & 1;
+      [[maybe_unused]] GatedH h_next;
+      if constexpr (EPI == EPI_GATED_GRAD) {
+        const int c = 32 * ((warp - 2) >> 2);
+        if (splits == 1 && c < D.rows)
+          rag_gated_load_h(args, h_next, D.row0 + c, D.rows - c,
+                           D.w_tile * 128 + q * 32 + lane, lane);
+      }
       int ok = 0;
       if (lane == 0) ok = wait(tfull_bar(acc), (local >> 1) & 1);
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -402,13 +410,32 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
         for (int c = 32 * ((warp - 2) >> 2); c < D.rows; c += 64) {
           uint32_t r[32];
           tmem_ld_32x32b_x32(taddr + c, r);
+          if constexpr (EPI == EPI_GATED_GRAD) {
+            const GatedH h = h_next;
+            tmem_ld_wait();
+            if (splits > 1) {
+              rag_store_part(args, r, t, rank, c, D.rows, q * 32 + lane);
+              continue;
+            }
+            if (c + 64 < D.rows)
+              rag_gated_load_h(args, h_next, D.row0 + c + 64, D.rows - c - 64, w, lane);
+            if (clamp)
+              rag_gated_grad_tokens32<T, true>(args, r, h, D.row0 + c, D.rows - c, w, lane);
+            else
+              rag_gated_grad_tokens32<T, false>(args, r, h, D.row0 + c, D.rows - c, w, lane);
+            __syncwarp();
+            continue;
+          }
           tmem_ld_wait();
           if (splits > 1)
             rag_store_part(args, r, t, rank, c, D.rows, q * 32 + lane);
           else if constexpr (EPI == EPI_GATED)
-            rag_gated_tokens32<T>(args, r, bias, D.row0 + c, D.rows - c, w, lane);
-          else if constexpr (EPI == EPI_GATED_GRAD)
-            rag_gated_grad_tokens32<T>(args, r, D.row0 + c, D.rows - c, w, lane);
+            {
+            if (clamp)
+              rag_gated_tokens32<T, true>(args, r, bias, D.row0 + c, D.rows - c, w, lane);
+            else
+              rag_gated_tokens32<T, false>(args, r, bias, D.row0 + c, D.rows - c, w, lane);
+          }
           else
             rag_dense_tokens32(args, D, r, D.tok * args.dense.per + c, D.rows - c, w, lane);
           __syncwarp();
