@@ -594,13 +594,14 @@ moe_status moe_clip_grad_norm(int n, const void* const* grads, void* const* outs
  *    MOE_MAX_ORTHOGONALIZE_STEPS.  They should keep singular values of X below 3 and
  *    the polynomial's values within 16: elements past that are infinities.
  *  - eps: at least 1e-12; a zero matrix gives zeros.
- *  - Products take operands of 11 bits (22 where N or K is at most 256) and sum in
- *    fp32; the result is within about 0.2% (rms) of the exact one, its own
- *    rounding to bf16 among that.  A square beyond fp32's range makes the norm
- *    infinite and the result zero; infinities and NaN give NaN in their matrix.
+ *  - Products take operands of 11 bits (22 where N or K is at most 128), X itself is
+ *    kept with 22 bits until the last two steps, sums are fp32: the result is within
+ *    about 0.25% (rms) of the exact one, its own rounding to bf16 (0.17%) among that.
+ *    A square beyond fp32's range makes the norm infinite and the result zero;
+ *    infinities and NaN give NaN in their matrix.
  *    The result does not depend on timing.
  *  - workspace: device, 256-byte aligned, moe_orthogonalize_workspace_bytes bytes
- *    (0 for sizes that are refused); about four bytes an element of g and four of
+ *    (0 for sizes that are refused); about six bytes an element of g and four of
  *    every square of the shorter side.  No contents are kept from call to call; calls
  *    that may overlap on the GPU take one each.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA. */
@@ -642,7 +643,8 @@ void moe_debug_set_watchdog(int64_t limit_ns, int never_arrive);
  * The ragged products (ragged_gemm, its gradients, ragged_gemm_mxfp4) take the
  * same modes; by default a model of the forms' times chooses by sizes.  mode 3:
  * their pair form, forward and dgrad on tiles of 512 weights (the other GEMMs:
- * as mode 0).
+ * as mode 0).  moe_orthogonalize: 1 and 2 its products as launches of their own on
+ * one SM or on pairs, 3 all steps in one launch of clusters.
  * Not thread-safe; affects later launches.  No counterpart on the pages: it
  * only lets tests reach both forms at any size. */
 void moe_debug_set_bf16_gemm_form(int mode);

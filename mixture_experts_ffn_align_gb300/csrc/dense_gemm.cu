@@ -41,8 +41,8 @@ DensePlan plan_of(const DenseProduct& d) {
       const long long steps = (kb + r.splits - 1) / r.splits;
       const long long step = std::max((16384 + (r.per + 31) / 32 * 4096) / 55, 53 * r.per / 20);
       const long long epilogue = (r.tri ? 1500 : 1000) * ((r.per + 63) / 64);
-      r.cycles = 5000 + (tiles * r.splits + 151) / 152 * std::max(steps * step, epilogue) + epilogue +
-                 (r.splits > 1 ? 3500 : 0);
+      r.cycles = r.splits > 1 ? 9500 + steps * step + 600 * ((r.per + 63) / 64)
+                              : 5000 + (tiles + 151) / 152 * std::max(steps * step, epilogue) + epilogue;
       if (best.cycles == 0 || r.cycles < best.cycles) best = r;
     }
   }
@@ -56,15 +56,21 @@ size_t dense_part_bytes(const DenseProduct& d) {
   return r.splits > 1 ? (size_t)r.e_tiles * d.E * r.splits * r.tile_rows * 128 * sizeof(float) : 0;
 }
 
-bool dense_on_pairs(const DenseProduct& d) {
-  if (ragged_form() != 0) return ragged_form() != 1;
+static long long pairs_cycles(const DenseProduct& d) {
   const long long kb = (long long)d.segs * d.seg_kb;
   const int w = (d.width + 255) / 256, t = (d.m + 255) / 256;
   const int n = d.symmetric ? 256 : ((d.m + t - 1) / t + 31) / 32 * 32;
   const long long tiles = (d.symmetric ? (long long)w * (w + 1) / 2 : (long long)w * t) * d.E;
   const long long step = std::max((16384 + n * 64) / 55, 53 * n / 20);
   const long long epilogue = (d.symmetric ? 1500 : 1000) * ((n + 63) / 64);
-  return 8000 + (tiles + 75) / 76 * std::max(kb * step, epilogue) + epilogue < plan_of(d).cycles;
+  return 8000 + (tiles + 75) / 76 * std::max(kb * step, epilogue) + epilogue;
+}
+long long dense_cycles(const DenseProduct& d) {
+  return std::min(plan_of(d).cycles, pairs_cycles(d));
+}
+bool dense_on_pairs(const DenseProduct& d) {
+  if (ragged_form() != 0) return ragged_form() != 1;
+  return pairs_cycles(d) < plan_of(d).cycles;
 }
 
 cudaError_t launch_dense(const DenseProduct& d, void* workspace, cudaStream_t stream) {

@@ -4,7 +4,7 @@
 //   else  out[e][r, c] = sum_k rows[e][r, k] w[e][k, c]
 // and v = c_acc out + c_mat mat + c_diag (r == c), stored in fp16 or, the last
 // product, in bf16.  Matrices have m rows; widths of rows and w are multiples of 64
-// with zeros behind the values.  segs 3: every matrix is a hi and a lo part side by
+// with zeros behind the values.  segs 1: the factors are rounded to fp16; segs 3: every matrix is a hi and a lo part side by
 // side, and hi hi + hi lo + lo hi is summed, about 22 bits of each operand.
 #pragma once
 
@@ -25,13 +25,17 @@ struct DenseProduct {
   int segs, seg_kb;          // 1 or 3; 64-deep steps of each
   float c_acc, c_mat, c_diag;
   const void* mat;           // as out, or null
+  long long mat_lo;          // elements from mat to its lo part, 0: none
   void* out;
-  int out_ld, out_lo;        // out_lo 0: no lo part
+  int out_ld;
+  long long out_lo;          // as mat_lo
   void* final_out;           // bf16 [E, m, width], transposed [E, width, m]; out unused
   bool transposed;
 };
 
 size_t dense_part_bytes(const DenseProduct& d);
+// Modelled cycles of the product on its own, and whether SM pairs take fewer.
+long long dense_cycles(const DenseProduct& d);
 bool dense_on_pairs(const DenseProduct& d);
 cudaError_t launch_dense(const DenseProduct& d, void* workspace, cudaStream_t stream);
 cudaError_t launch_dense_2sm(const DenseProduct& d, cudaStream_t stream);
@@ -61,7 +65,8 @@ inline void dense_args(const DenseProduct& d, bool tri, int per, int tok_tiles, 
   q.c_mat = d.c_mat;
   q.c_diag = d.c_diag;
   q.mat = static_cast<const __half*>(d.mat);
-  q.lo = d.out_lo;
+  q.mat_lo = d.mat_lo;
+  q.out_lo = d.out_lo;
   q.final_out = static_cast<__nv_bfloat16*>(d.final_out);
   q.transposed = d.transposed;
 }

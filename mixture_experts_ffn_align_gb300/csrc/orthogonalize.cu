@@ -8,17 +8,24 @@
 // last product's stores on the way out), so A and B are m x m.  A and B are
 // symmetric and computed in tiles on and below the diagonal, each stored on both
 // sides: m^2 M + m^3 + 2 m^2 M operations a step instead of 4 m^2 M + 2 m^3 (M the
-// longer side).  B takes in a I, so that the third product needs no operand beside
-// B and X.
+// longer side).
 //
 // Operands are fp16, whose 11 bits matter here: with bf16's 8 the result is 1% off
-// (rms), with 11 it is 0.11 to 0.13% for m of 256 to 1024 and more, less than the
-// rounding of the result to bf16 (0.17%).  X, A and B are scaled by powers of two
-// into fp16's range: |X|, |A| and |B| are at most about 1.3, 1.6 and 4 (for the usual
-// coefficients), and their typical elements are 1 / sqrt(m M) and less.  Sums over few
-// elements average less: up to m = 256, where all products are short, every
-// matrix is held as a hi and a lo part of 22 bits together, and a product is three
-// (hi hi + hi lo + lo hi) over one accumulator.
+// (rms) and more.  X, A and B are scaled by powers of two into fp16's range: |X|, |A|
+// and |B| are at most about 1.3, 1.6 and 4 (for the usual coefficients), and their
+// typical elements are 1 / sqrt(m M) and less.
+//
+// The steps raise small singular values up to 3.4-fold each while large ones stay, so
+// what a rounding of X loses beside a large singular value grows too (a gradient with
+// one direction 50 times the rest's: 1% off).  So X is kept as a hi and a lo part, 22
+// bits together, in all steps but the last two; products take the hi part, and X =
+// a X + (b A + c A^2) X adds a times both in the epilogue, where rounding the hi part
+// only costs what is multiplied by b A + c A^2.  The last two steps need that no more
+// and fold a into B: B = a I + b A + c A^2, X = B X.  The error is then 0.08 to 0.14%
+// whatever the spectrum, less than the rounding of the result to bf16 (0.17%).
+// Sums over few elements average less: up to m = 128, where all products are short,
+// operands too are the hi and the lo part, and a product is three (hi hi + hi lo + lo
+// hi) over one accumulator.
 //
 // Forming A anew in each step, rather than carrying it along as B A B, costs the m^2
 // M product but keeps small singular values: an error of A enters B X relative to
@@ -28,6 +35,7 @@
 #include "dense_gemm.h"
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "ortho_cluster.h"
 #include "pdl.cuh"
 #include "ragged.cuh"
 
@@ -35,7 +43,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPrecise = 256;                 // shorter sides up to here take hi and lo parts
+constexpr int kPrecise = 128;                 // shorter sides up to here take hi and lo parts
+constexpr int kFolded = 2;                    // last steps that fold a X into B
 constexpr float kScaleX = 4096.0f, kScaleA = 1024.0f, kScaleB = 1024.0f;
 constexpr int kMaxChunks = 304;               // partial sums of a matrix
 constexpr int kRowsPerThread = 4, kTiles = 4; // of k_ortho_scale, k_ortho_transpose
@@ -102,7 +111,7 @@ __device__ __forceinline__ void unpack8(const Raw8<TYPE>& r, float (&v)[8]) {
   }
 }
 // Eight values as fp16, and what that leaves of them lo columns on.
-__device__ __forceinline__ void store8(__half* out, int lo, float inv, const float (&v)[8]) {
+__device__ __forceinline__ void store8(__half* out, long long lo, float inv, const float (&v)[8]) {
   uint32_t hi[4], rest[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -202,7 +211,7 @@ __device__ __forceinline__ float scale_of(const double* partial, int chunks, int
 // eight columns of kRowsPerThread rows, 1 << log_tx threads a row.
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads)
-    k_ortho_scale(const void* g, int m, int M, int Mp, int ld, int lo, int log_tx, bool wide,
+    k_ortho_scale(const void* g, int m, int M, int Mp, int ld, long long lo, int log_tx, bool wide,
                   int chunks, const double* partial, float eps, __half* x) {
   __shared__ float smem;
   griddep_launch();
@@ -236,7 +245,7 @@ __global__ void __launch_bounds__(kThreads)
 // x 4 when they read it, so that with rows of 33 words no bank is hit twice.
 template <int TYPE, bool LO>
 __global__ void __launch_bounds__(kThreads, TYPE == 2 ? 5 : 6)
-    k_ortho_transpose(const void* g, int m, int M, int Mp, int ld, int lo, bool wide, int chunks,
+    k_ortho_transpose(const void* g, int m, int M, int Mp, int ld, long long lo, bool wide, int chunks,
                       const double* partial, float eps, __half* x) {
   __shared__ float smem;
   __shared__ uint32_t tile[LO ? 2 : 1][64][33];
@@ -291,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, TYPE == 2 ? 5 : 6)
 
 struct Layout {
   int m, M, mp, Mp, parts, chunks;
-  size_t x_bytes, a_bytes, partial, a, b, x0, x1, part, total;
+  size_t x_bytes, a_bytes, partial, a, b, x0, x1, lo, part, total;
 };
 size_t pad(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -325,7 +334,7 @@ DenseProduct polynomial(const Layout& l, int E, const void* a, void* b, const fl
   d.rows = d.w = d.mat = a;
   d.rows_ld = d.w_ld = d.out_ld = l.parts * l.mp;
   d.rows_lo = d.w_lo = l.mp;
-  d.out_lo = l.parts == 2 ? l.mp : 0;
+  d.mat_lo = d.out_lo = l.parts == 2 ? l.mp : 0;
   d.seg_kb = l.mp / 64;
   d.c_acc = c[2] * (kScaleB / (kScaleA * kScaleA));
   d.c_mat = c[1] * (kScaleB / kScaleA);
@@ -350,6 +359,12 @@ DenseProduct apply(const Layout& l, int E, const void* b, const void* x, void* o
   return d;
 }
 
+// Sizes of workspaces do not depend on the number of steps, so plans are made for this.
+constexpr int kModelSteps = 5;
+OrthoClusterPlan cluster_plan(const Layout& l, int E) {
+  return ortho_cluster_plan(E, l.m, l.mp, l.M, l.Mp, l.parts, kModelSteps);
+}
+
 Layout layout(int E, int N, int K) {
   Layout l;
   l.m = std::min(N, K);
@@ -367,15 +382,29 @@ Layout layout(int E, int N, int K) {
   l.b = l.a + l.a_bytes;
   l.x0 = l.b + l.a_bytes;
   l.x1 = l.x0 + l.x_bytes;
-  l.part = l.x1 + l.x_bytes;
+  l.lo = l.x1 + l.x_bytes;
+  l.part = l.lo + (l.parts == 1 ? l.x_bytes : 0);
   const float c[3] = {};
   DenseProduct last = apply(l, E, nullptr, nullptr, nullptr);
   last.width = l.M;
   l.total = l.part + pad(std::max({dense_part_bytes(gram(l, E, nullptr, nullptr)),
                                    dense_part_bytes(polynomial(l, E, nullptr, nullptr, c)),
                                    dense_part_bytes(apply(l, E, nullptr, nullptr, nullptr)),
-                                   dense_part_bytes(last)}));
+                                   dense_part_bytes(last),
+                                   ortho_cluster_part_bytes(cluster_plan(l, E), E)}));
   return l;
+}
+
+// Whether one launch for all steps (ortho_cluster.cu) is modelled to be the faster.  A
+// product of its own takes some 3500 cycles more than its model says, which does not
+// matter where products are compared among themselves.
+bool in_clusters(const Layout& l, int E) {
+  if (ragged_form() != 0) return ragged_form() == 3;
+  const float c[3] = {};
+  const long long own = dense_cycles(gram(l, E, nullptr, nullptr)) +
+                        dense_cycles(polynomial(l, E, nullptr, nullptr, c)) +
+                        dense_cycles(apply(l, E, nullptr, nullptr, nullptr)) + 3 * 3500;
+  return cluster_plan(l, E).cycles < kModelSteps * own;
 }
 
 cudaError_t run(const DenseProduct& d, void* part, cudaStream_t stream) {
@@ -384,7 +413,7 @@ cudaError_t run(const DenseProduct& d, void* part, cudaStream_t stream) {
 
 template <int TYPE>
 cudaError_t prepare(const Layout& l, int E, bool transposed, const void* g, float eps,
-                    double* partial, __half* x, cudaStream_t stream) {
+                    double* partial, __half* x, long long lo, cudaStream_t stream) {
   const long long n = (long long)l.m * l.M;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -397,14 +426,14 @@ cudaError_t prepare(const Layout& l, int E, bool transposed, const void* g, floa
   cfg.gridDim = dim3(l.chunks, E, 1);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k_ortho_norm<TYPE>, g, n, l.chunks, partial);
   if (e != cudaSuccess) return e;
-  const int ld = l.parts * l.Mp, lo = l.parts == 2 ? l.Mp : 0;
+  const int ld = l.parts * l.Mp;
   const double* sums = partial;
   // rows of g in whole 16-byte pieces
   const bool wide = reinterpret_cast<uintptr_t>(g) % 16 == 0 &&
                     (transposed ? l.m : l.M) % (TYPE == 2 ? 4 : 8) == 0;
   if (transposed) {
     cfg.gridDim = dim3((l.Mp / 64 + kTiles - 1) / kTiles, (l.m + 63) / 64, E);
-    return cudaLaunchKernelEx(&cfg, lo ? k_ortho_transpose<TYPE, true> : k_ortho_transpose<TYPE, false>, g, l.m, l.M, l.Mp, ld, lo, wide,
+    return cudaLaunchKernelEx(&cfg, lo != 0 ? k_ortho_transpose<TYPE, true> : k_ortho_transpose<TYPE, false>, g, l.m, l.M, l.Mp, ld, lo, wide,
                               l.chunks, sums, eps, x);
   }
   int log_tx = 3;
@@ -428,16 +457,44 @@ cudaError_t launch_orthogonalize(int E, int N, int K, const void* g, int type, v
   char* ws = static_cast<char*>(workspace);
   void *a = ws + l.a, *b = ws + l.b, *x = ws + l.x0, *y = ws + l.x1, *part = ws + l.part;
   double* partial = reinterpret_cast<double*>(ws + l.partial);
+  // steps that add a X in the epilogue, from X's hi and lo parts
+  const int kept = l.parts == 1 ? std::max(0, steps - kFolded) : 0;
+  __half* lo = reinterpret_cast<__half*>(ws + l.lo);
   __half* x0 = static_cast<__half*>(x);
-  cudaError_t e = type == 0   ? prepare<0>(l, E, transposed, g, eps, partial, x0, stream)
-                  : type == 1 ? prepare<1>(l, E, transposed, g, eps, partial, x0, stream)
-                              : prepare<2>(l, E, transposed, g, eps, partial, x0, stream);
+  const long long x_lo = l.parts == 2 ? l.Mp : kept > 0 ? lo - x0 : 0;
+  cudaError_t e = type == 0   ? prepare<0>(l, E, transposed, g, eps, partial, x0, x_lo, stream)
+                  : type == 1 ? prepare<1>(l, E, transposed, g, eps, partial, x0, x_lo, stream)
+                              : prepare<2>(l, E, transposed, g, eps, partial, x0, x_lo, stream);
+  if (e == cudaSuccess && in_clusters(l, E)) {
+    OrthoClusterProblem d{cluster_plan(l, E), E, l.m, l.M, l.mp, l.Mp, l.parts, steps, transposed,
+                          {x, y}, l.parts == 1 ? lo : nullptr, a, b, out, part, kept};
+    d.c_gram = gram(l, E, x, a).c_acc;
+    d.c_apply = apply(l, E, b, x, y).c_acc;
+    d.c_last = d.c_apply * (scale / kScaleX);
+    float coef[3 * MOE_MAX_ORTHOGONALIZE_STEPS];
+    for (int s = 0; s < steps; ++s) {
+      const DenseProduct p = polynomial(l, E, a, b, coefficients + 3 * s);
+      coef[3 * s] = s < kept ? coefficients[3 * s] : p.c_diag;
+      coef[3 * s + 1] = p.c_mat;
+      coef[3 * s + 2] = p.c_acc;
+    }
+    d.coef = coef;
+    return launch_ortho_cluster(d, stream);
+  }
   for (int s = 0; s < steps && e == cudaSuccess; ++s) {
     e = run(gram(l, E, x, a), part, stream);
     if (e != cudaSuccess) return e;
-    e = run(polynomial(l, E, a, b, coefficients + 3 * s), part, stream);
-    if (e != cudaSuccess) return e;
+    DenseProduct poly = polynomial(l, E, a, b, coefficients + 3 * s);
     DenseProduct last = apply(l, E, b, x, y);
+    if (s < kept) {
+      poly.c_diag = 0.0f;
+      last.mat = x;
+      last.c_mat = coefficients[3 * s];
+      last.mat_lo = lo - static_cast<__half*>(x);
+      if (s + 1 < kept) last.out_lo = lo - static_cast<__half*>(y);
+    }
+    e = run(poly, part, stream);
+    if (e != cudaSuccess) return e;
     if (s == steps - 1) {
       last.width = l.M;
       last.c_acc *= scale / kScaleX;

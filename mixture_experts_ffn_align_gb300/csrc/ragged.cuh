@@ -78,7 +78,7 @@ struct RagDense {
   int a_lo, b_lo;           // columns from the hi to the lo part of the operands
   float c_acc, c_mat, c_diag;
   const __half* mat;        // added, c_mat times: [E, m, ...] as the output, or null
-  int lo;                   // columns from the hi to the lo part of mat and output, or 0
+  long long mat_lo, out_lo; // from mat and the output to their lo parts, or 0
   __nv_bfloat16* final_out; // the last product: [E, m, W], or [E, W, m] with `transposed`
   int transposed;
 };

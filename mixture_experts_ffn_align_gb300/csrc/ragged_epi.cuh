@@ -20,8 +20,8 @@
 // of a row a half-warp.
 //
 // EPI_DENSE: E products of matrices of m rows, in fp16 with hi and lo parts where
-// that is asked for (dense.lo): v = c_acc sum + c_mat mat + c_diag (row == column),
-// rounded to fp16 (lo = v - hi), or the last product in bf16.
+// that is asked for (mat_lo, out_lo): v = c_acc sum + c_mat mat + c_diag (row ==
+// column), rounded to fp16 (lo = v - hi), or the last product in bf16.
 #pragma once
 
 #include "moe_internal.h"
@@ -126,32 +126,52 @@ __device__ __forceinline__ void rag_gated_tokens32(const RagArgs& a, uint32_t (&
   }
 }
 
-// h at 32 tokens of two columns: what one lane needs for rag_gated_grad_tokens32.
-// Read a chunk ahead (the first before the sums are complete): read where they are
-// used, they kept the gradient of 8 x (2048, 1024), 256 rows each, at 26 us instead of
-// the plain product's 12.
-struct GatedH {
-  uint32_t g[16], u[16];
+// What a lane's two columns of 32 tokens need from memory beside the sums: the words
+// of every other token from two places.  Read a chunk ahead (the first before the sums
+// are complete): read where they are used, they kept the gradient of 8 x (2048,
+// 1024), 256 rows each, at 28 us instead of 20.
+struct Words32 {
+  uint32_t a[16], b[16];
 };
-__device__ __forceinline__ void rag_gated_load_h(const RagArgs& a, GatedH& x, long long row0,
-                                                 int live, int w, int lane) {
-  const RagGated& q = a.gated;
-  const int odd = lane & 1;
-  const bool inside = w < a.W;
-  const uint16_t* h = static_cast<const uint16_t*>(q.h) + (row0 + odd) * q.ldh + (w - odd);
+__device__ __forceinline__ void rag_load_words(Words32& x, const uint16_t* p, const uint16_t* p2,
+                                               long long ld, int live, bool inside, int odd) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     const bool in = inside && 2 * j + odd < live;
-    x.g[j] = in ? *reinterpret_cast<const uint32_t*>(h) : 0u;
-    x.u[j] = in ? *reinterpret_cast<const uint32_t*>(h + q.inter) : 0u;
-    h += 2 * q.ldh;
+    x.a[j] = in ? __ldcg(reinterpret_cast<const uint32_t*>(p)) : 0u;
+    x.b[j] = in && p2 != nullptr ? __ldcg(reinterpret_cast<const uint32_t*>(p2)) : 0u;
+    p += 2 * ld;
+    p2 = p2 != nullptr ? p2 + 2 * ld : nullptr;
   }
+}
+// c: tokens of the tile before the 32.
+template <int EPI>
+__device__ __forceinline__ void rag_epi_load(const RagArgs& a, const RagTile& D, Words32& x, int c,
+                                             int w, int lane) {
+  const int odd = lane & 1;
+  if (EPI == EPI_GATED_GRAD) {
+    const RagGated& q = a.gated;
+    const uint16_t* h = static_cast<const uint16_t*>(q.h) + (long long)(D.row0 + c + odd) * q.ldh +
+                        (w - odd);
+    rag_load_words(x, h, h + q.inter, q.ldh, D.rows - c, w < a.W, odd);
+  } else {
+    const RagDense& q = a.dense;
+    const uint16_t* mat = reinterpret_cast<const uint16_t*>(q.mat) +
+                          (long long)(D.row0 + c + odd) * a.ldo + (w - odd);
+    rag_load_words(x, mat, q.mat_lo != 0 ? mat + q.mat_lo : nullptr, a.ldo, D.rows - c, w < a.W,
+                   odd);
+  }
+}
+// Whether there is something to read.
+template <int EPI>
+__device__ __forceinline__ bool rag_epi_loads(const RagArgs& a) {
+  return EPI == EPI_GATED_GRAD || (EPI == EPI_DENSE && a.dense.mat != nullptr && !a.dense.sym);
 }
 
 // 32 tokens from row row0 of this lane's column w of dz.
 template <typename T, bool CLAMP>
 __device__ __forceinline__ void rag_gated_grad_tokens32(const RagArgs& a, const uint32_t (&r)[32],
-                                                        const GatedH& h, long long row0, int live,
+                                                        const Words32& h, long long row0, int live,
                                                         int w, int lane) {
   const RagGated& q = a.gated;
   const int odd = lane & 1, c0 = w - odd;
@@ -163,7 +183,7 @@ __device__ __forceinline__ void rag_gated_grad_tokens32(const RagArgs& a, const 
     const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? r[2 * t] : r[2 * t + 1], 1);
     const float dz0 = __uint_as_float(odd ? other : r[2 * t]);
     const float dz1 = __uint_as_float(odd ? r[2 * t + 1] : other);
-    const float2 g = unpack16<T>(h.g[t]), u = unpack16<T>(h.u[t]);
+    const float2 g = unpack16<T>(h.a[t]), u = unpack16<T>(h.b[t]);
     const GatedGrad x = gated_grad<CLAMP>(q, dz0, g.x, u.x), y = gated_grad<CLAMP>(q, dz1, g.y, u.y);
     if (inside && 2 * t + odd < live) {
       *reinterpret_cast<uint32_t*>(dh) = Half16<T>::pack(x.dg, y.dg);
@@ -300,10 +320,10 @@ __device__ __forceinline__ void rag_dense_tokens32(const RagArgs& a, const RagTi
             reinterpret_cast<const uint4*>(q.mat + (base + w) * a.ldo + tok);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
-          if (part == 0 || q.lo != 0) {
+          if (part == 0 || q.mat_lo != 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint4 x = mat[part * (q.lo / 8) + i];
+              const uint4 x = __ldcg(mat + part * (q.mat_lo / 8) + i);
               const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -333,14 +353,14 @@ __device__ __forceinline__ void rag_dense_tokens32(const RagArgs& a, const RagTi
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         p[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-        if (q.lo != 0)
-          p[q.lo / 8 + i] = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+        if (q.out_lo != 0)
+          p[q.out_lo / 8 + i] = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
       }
     }
     if (q.tri && D.tok != D.w_tile) {         // and as column w
       out += (base + tok) * a.ldo + w;
       rag_store_packed32(pk, out, a.ldo, live, w, a.W, lane);
-      if (q.lo != 0) rag_store_packed32(lo, out + q.lo, a.ldo, live, w, a.W, lane);
+      if (q.out_lo != 0) rag_store_packed32(lo, out + q.out_lo, a.ldo, live, w, a.W, lane);
     }
     return;
   }
@@ -353,12 +373,37 @@ __device__ __forceinline__ void rag_dense_tokens32(const RagArgs& a, const RagTi
   }
   out += (base + tok) * a.ldo + w;
   rag_store_packed32(pk, out, a.ldo, live, w, a.W, lane);
-  if (q.lo != 0) rag_store_packed32(lo, out + q.lo, a.ldo, live, w, a.W, lane);
+  if (q.out_lo != 0) rag_store_packed32(lo, out + q.out_lo, a.ldo, live, w, a.W, lane);
+}
+
+// The same of a product that is not symmetric, with mat (as h, read by
+// rag_dense_load): two neighbouring lanes swap tokens first.  A lo part of mat may
+// be the output's own: each word is read and written by one lane.
+__device__ __forceinline__ void rag_dense_add_tokens32(const RagArgs& a, const RagTile& D,
+                                                       const uint32_t (&r)[32], const Words32& h,
+                                                       int tok, int left, int w, int lane) {
+  const RagDense& q = a.dense;
+  const int live = min(q.m - tok, left), odd = lane & 1;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + ((long long)D.e * q.m + tok + odd) * a.ldo + w - odd;
+#pragma unroll
+  for (int t = 0; t < 16; ++t) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? r[2 * t] : r[2 * t + 1], 1);
+    const float2 hi = unpack16<__half>(h.a[t]), lo = unpack16<__half>(h.b[t]);
+    float x = q.c_acc * __uint_as_float(odd ? other : r[2 * t]) + q.c_mat * (hi.x + lo.x);
+    float y = q.c_acc * __uint_as_float(odd ? r[2 * t + 1] : other) + q.c_mat * (hi.y + lo.y);
+    const uint32_t p = half_hi2(x, y);
+    if (w < a.W && 2 * t + odd < live) {
+      *reinterpret_cast<uint32_t*>(out) = p;
+      if (q.out_lo != 0) *reinterpret_cast<uint32_t*>(out + q.out_lo) = Half16<__half>::pack(x, y);
+    }
+    out += 2 * a.ldo;
+  }
 }
 
 // ------------------------------------------------------------- joining slices
 // As rag_join_tokens, with the fused epilogues: a lane has the sums of the four
-// columns from w of row D.row0 + j.
+// columns from w of row D.row0 + j.  Loads of what other CTAs of the cluster wrote
+// in this launch bypass L1 (__ldcg).
 template <int EPI, typename T>
 __device__ __forceinline__ void rag_join_store(const RagArgs& a, const RagTile& D, int j, int w,
                                                float4 x) {
@@ -421,8 +466,9 @@ __device__ __forceinline__ void rag_join_store(const RagArgs& a, const RagTile& 
     if (q.mat != nullptr) {
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
-        if (part == 0 || q.lo != 0) {
-          const uint2 m = *reinterpret_cast<const uint2*>(q.mat + row * a.ldo + w + part * q.lo);
+        if (part == 0 || q.mat_lo != 0) {
+          const uint2 m =
+              __ldcg(reinterpret_cast<const uint2*>(q.mat + row * a.ldo + w + part * q.mat_lo));
           const float2 m0 = unpack16<__half>(m.x), m1 = unpack16<__half>(m.y);
           v[0] += q.c_mat * m0.x;
           v[1] += q.c_mat * m0.y;
@@ -439,20 +485,21 @@ __device__ __forceinline__ void rag_join_store(const RagArgs& a, const RagTile& 
     hi.x = half_hi2(v[0], v[1]);
     hi.y = half_hi2(v[2], v[3]);
     *reinterpret_cast<uint2*>(out) = hi;
-    if (q.lo != 0)
-      *reinterpret_cast<uint2*>(out + q.lo) =
+    if (q.out_lo != 0)
+      *reinterpret_cast<uint2*>(out + q.out_lo) =
           make_uint2(Half16<__half>::pack(v[0], v[1]), Half16<__half>::pack(v[2], v[3]));
   }
 }
 template <int EPI, typename T>
 __device__ __forceinline__ void rag_join_fused(const RagArgs& a, const RagTile& D, int t, int rank,
-                                               int warp, int warps, int lane) {
+                                               int ctas, int warp, int warps, int lane) {
   const int w = D.w_tile * 128 + 4 * lane;
   const float* p = a.part + (size_t)t * a.splits * a.tile_rows * 128 + 4 * lane;
-  for (int j = rank * warps + warp; j < D.rows; j += a.splits * warps) {
-    float4 x = *reinterpret_cast<const float4*>(p + (size_t)j * 128);
+  for (int j = rank * warps + warp; j < D.rows; j += ctas * warps) {
+    float4 x = __ldcg(reinterpret_cast<const float4*>(p + (size_t)j * 128));
     for (int s = 1; s < a.splits; ++s) {
-      const float4 v = *reinterpret_cast<const float4*>(p + ((size_t)s * a.tile_rows + j) * 128);
+      const float4 v =
+          __ldcg(reinterpret_cast<const float4*>(p + ((size_t)s * a.tile_rows + j) * 128));
       x = make_float4(x.x + v.x, x.y + v.y, x.z + v.z, x.w + v.w);
     }
     rag_join_store<EPI, T>(a, D, j, w, x);

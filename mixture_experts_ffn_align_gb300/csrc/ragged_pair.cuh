@@ -469,12 +469,12 @@ __global__ void __launch_bounds__(num_threads(OP, MT, EPI), 1)
         continue;
       }
       const int acc = local & 1;
-      [[maybe_unused]] GatedH h_next;
-      if constexpr (EPI == EPI_GATED_GRAD) {
+      [[maybe_unused]] Words32 h_next;
+      [[maybe_unused]] const bool loads = rag_epi_loads<EPI>(args);
+      if constexpr (EPI == EPI_GATED_GRAD || EPI == EPI_DENSE) {
         const int c = 32 * ((warp - 2) >> 2);
-        if (c < D.rows)
-          rag_gated_load_h(args, h_next, D.row0 + c, D.rows - c,
-                           D.w_tile * 256 + rank * 128 + q * 32 + lane, lane);
+        if (loads && c < D.rows)
+          rag_epi_load<EPI>(args, D, h_next, c, D.w_tile * 256 + rank * 128 + q * 32 + lane, lane);
       }
       int ok = 0;
       if (lane == 0) ok = wait(tfull_bar(acc), (local >> 1) & 1);
@@ -508,17 +508,12 @@ __global__ void __launch_bounds__(num_threads(OP, MT, EPI), 1)
         for (int c = 32 * ((warp - 2) >> 2); c < D.rows; c += 64) {
           uint32_t r[32];
           tmem_ld_32x32b_x32(taddr + c, r);
-          if constexpr (EPI == EPI_GATED_GRAD) {
-            const GatedH h = h_next;
-            tmem_ld_wait();
-            if (c + 64 < D.rows)
-              rag_gated_load_h(args, h_next, D.row0 + c + 64, D.rows - c - 64, w, lane);
-            if (clamp)
-              rag_gated_grad_tokens32<T, true>(args, r, h, D.row0 + c, D.rows - c, w, lane);
-            else
-              rag_gated_grad_tokens32<T, false>(args, r, h, D.row0 + c, D.rows - c, w, lane);
-            __syncwarp();
-            continue;
+          [[maybe_unused]] Words32 h;
+          if constexpr (EPI == EPI_GATED_GRAD || EPI == EPI_DENSE) {
+            if (loads) {
+              h = h_next;
+              if (c + 64 < D.rows) rag_epi_load<EPI>(args, D, h_next, c + 64, w, lane);
+            }
           }
           tmem_ld_wait();
           if constexpr (EPI == EPI_GATED)
@@ -528,8 +523,18 @@ __global__ void __launch_bounds__(num_threads(OP, MT, EPI), 1)
             else
               rag_gated_tokens32<T, false>(args, r, bias, D.row0 + c, D.rows - c, w, lane);
           }
-          else
-            rag_dense_tokens32(args, D, r, D.tok * args.dense.per + c, D.rows - c, w, lane);
+          else if constexpr (EPI == EPI_GATED_GRAD) {
+            if (clamp)
+              rag_gated_grad_tokens32<T, true>(args, r, h, D.row0 + c, D.rows - c, w, lane);
+            else
+              rag_gated_grad_tokens32<T, false>(args, r, h, D.row0 + c, D.rows - c, w, lane);
+          } else {
+            const int tok = D.tok * args.dense.per + c;
+            if (loads)
+              rag_dense_add_tokens32(args, D, r, h, tok, D.rows - c, w, lane);
+            else
+              rag_dense_tokens32(args, D, r, tok, D.rows - c, w, lane);
+          }
           __syncwarp();
         }
         release();

@@ -120,16 +120,21 @@ def gated_grad(dz, h, alpha=1.0, beta=0.0, limit=0.0):
     return np.concatenate([dg, du], 1)
 
 
-def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, rounded=None):
+def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, rounded=None,
+                  kept=0):
     """Newton-Schulz steps on one matrix.  rounded: applied to every operand of a
-    product (X, A, B of the shorter side), to see what operands of a type cost."""
+    product (X, A, B of the shorter side), to see what operands of a type cost; the
+    first `kept` steps add a X as it is, the others round it with B."""
     r = rounded or (lambda v: v)
     x = np.asarray(g, dtype=np.float64)
     x = x if x.shape[0] <= x.shape[1] else x.T
-    x = r(x / (np.sqrt((x * x).sum()) + eps))
+    x = x / (np.sqrt((x * x).sum()) + eps)
     for i in range(steps):
         a, b, c = coefficients[i] if np.ndim(coefficients) == 2 else coefficients
-        m = r(x @ x.T)
-        x = r(a * np.eye(len(m)) + b * m + c * (m @ m)) @ x
-        x = r(x) if i + 1 < steps else x
+        m = r(r(x) @ r(x).T)
+        p = b * m + c * (m @ m)
+        if i < kept:
+            x = a * x + r(p) @ r(x)
+        else:
+            x = r(a * np.eye(len(m)) + p) @ r(x)
     return x if g.shape[0] <= g.shape[1] else x.T
