@@ -28,10 +28,10 @@ DensePlan plan_of(const DenseProduct& d) {
       DensePlan r;
       r.tri = mode == 4;
       r.splits = r.tri ? 1 : 1 << mode;
-      if (r.tri && (!d.symmetric || tile != 128)) continue;
+      if (r.tri && (!d.nt || tile != 128)) continue;
       r.tile_rows = tile;
       r.w_tiles = (d.width + 127) / 128;
-      const int rows = d.symmetric ? d.width : d.m, unit = d.symmetric ? 32 : 16;
+      const int rows = d.nt ? d.width : d.m, unit = d.nt ? 32 : 16;
       r.tok_tiles = (rows + tile - 1) / tile;
       r.per = r.tri ? tile : ((rows + r.tok_tiles - 1) / r.tok_tiles + unit - 1) / unit * unit;
       r.e_tiles = r.tri ? (long long)r.w_tiles * (r.w_tiles + 1) / 2
@@ -59,10 +59,10 @@ size_t dense_part_bytes(const DenseProduct& d) {
 static long long pairs_cycles(const DenseProduct& d) {
   const long long kb = (long long)d.segs * d.seg_kb;
   const int w = (d.width + 255) / 256, t = (d.m + 255) / 256;
-  const int n = d.symmetric ? 256 : ((d.m + t - 1) / t + 31) / 32 * 32;
-  const long long tiles = (d.symmetric ? (long long)w * (w + 1) / 2 : (long long)w * t) * d.E;
+  const int n = d.nt ? 256 : ((d.m + t - 1) / t + 31) / 32 * 32;
+  const long long tiles = (d.nt ? (long long)w * (w + 1) / 2 : (long long)w * t) * d.E;
   const long long step = std::max((16384 + n * 64) / 55, 53 * n / 20);
-  const long long epilogue = (d.symmetric ? 1500 : 1000) * ((n + 63) / 64);
+  const long long epilogue = (d.nt ? 1500 : 1000) * ((n + 63) / 64);
   return 8000 + (tiles + 75) / 76 * std::max(kb * step, epilogue) + epilogue;
 }
 long long dense_cycles(const DenseProduct& d) {

@@ -4,8 +4,9 @@
 //   else  out[e][r, c] = sum_k rows[e][r, k] w[e][k, c]
 // and v = c_acc out + c_mat mat + c_diag (r == c), stored in fp16 or, the last
 // product, in bf16.  Matrices have m rows; widths of rows and w are multiples of 64
-// with zeros behind the values.  segs 1: the factors are rounded to fp16; segs 3: every matrix is a hi and a lo part side by
-// side, and hi hi + hi lo + lo hi is summed, about 22 bits of each operand.
+// with zeros behind the values.  segs 1: the operands have fp16's 11 bits; segs 3:
+// every matrix is a hi and a lo part side by side, and hi hi + hi lo + lo hi is
+// summed, about 22 bits of each operand.
 #pragma once
 
 #include "moe_internal.h"
@@ -14,8 +15,7 @@
 namespace moe {
 
 struct DenseProduct {
-  bool nt;
-  bool symmetric;            // nt with rows == w, or commuting factors: out is symmetric
+  bool nt;                   // rows == w: the output is symmetric
   int E, m;
   int width;                 // columns of the output
   const void* rows;
@@ -53,7 +53,7 @@ inline void dense_args(const DenseProduct& d, bool tri, int per, int tok_tiles, 
   RagDense& q = a.dense;
   q.m = d.m;
   q.mp = d.width;
-  q.sym = d.symmetric;
+  q.sym = d.nt;
   q.tri = tri;
   q.per = per;
   q.tok_tiles = tok_tiles;

@@ -17,12 +17,12 @@ cudaError_t launch_dense_2sm(const DenseProduct& d, cudaStream_t stream) {
   const int w_tiles = (d.width + 255) / 256;
   int tok_tiles = (d.m + 255) / 256, per = ((d.m + tok_tiles - 1) / tok_tiles + 31) / 32 * 32;
   long long e_tiles = (long long)w_tiles * tok_tiles;
-  if (d.symmetric) {
+  if (d.nt) {
     per = 256;
     tok_tiles = w_tiles;
     e_tiles = (long long)w_tiles * (w_tiles + 1) / 2;
   }
-  dense_args(d, d.symmetric, per, tok_tiles, e_tiles, a);
+  dense_args(d, d.nt, per, tok_tiles, e_tiles, a);
   a.tile_rows = 256;
   a.w_tiles = fast_div(w_tiles);
   watchdog_params(&a.limit_ns, &a.never_arrive);

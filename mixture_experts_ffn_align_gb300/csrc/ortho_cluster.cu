@@ -261,28 +261,31 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool loads = f.splits == 1 && rag_epi_loads<EPI_DENSE>(a);
       for (int i = rank; ok && i < items; i += ctas) {
         const Item it = item_of(f, args, e, i);
-        const int acc = local & 1;
+        const int acc = local & 1, w = it.tile.w_tile * 128 + q * 32 + lane;
+        Words32 h_next;
+        if (loads && 32 * ((warp - 2) >> 2) < it.tile.rows)
+          rag_epi_load<EPI_DENSE>(a, it.tile, h_next, 32 * ((warp - 2) >> 2), w, lane);
         int got = 0;
         if (lane == 0) got = wait(tfull_bar(acc), (local >> 1) & 1);
         ok = __shfl_sync(0xffffffffu, got, 0);
         if (!ok) break;
         tc_fence_after();
         const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
-        const int w = it.tile.w_tile * 128 + q * 32 + lane;
 #pragma unroll 1
         for (int c = 32 * ((warp - 2) >> 2); c < it.tile.rows; c += 64) {
           uint32_t r[32];
-          Words32 h;
+          const Words32 h = h_next;
           tmem_ld_32x32b_x32(taddr + c, r);
-          if (loads) rag_epi_load<EPI_DENSE>(a, it.tile, h, c, w, lane);
+          if (loads && c + 64 < it.tile.rows) rag_epi_load<EPI_DENSE>(a, it.tile, h_next, c + 64, w, lane);
           tmem_ld_wait();
           if (f.splits > 1)
             rag_store_part(a, r, e * f.tiles + it.t, it.slice, c, it.tile.rows, q * 32 + lane);
-          else if (loads)
-            rag_dense_add_tokens32(a, it.tile, r, h, it.tile.tok * f.per + c, it.tile.rows - c, w,
-                                   lane);
+          else if (f.nt)
+            rag_dense_store32<true>(a, it.tile, r, h, loads, it.tile.tok * f.per + c,
+                                    it.tile.rows - c, w, lane);
           else
-            rag_dense_tokens32(a, it.tile, r, it.tile.tok * f.per + c, it.tile.rows - c, w, lane);
+            rag_dense_store32<false>(a, it.tile, r, h, loads, it.tile.tok * f.per + c,
+                                     it.tile.rows - c, w, lane);
           __syncwarp();
         }
         tc_fence_before();

@@ -314,7 +314,7 @@ DenseProduct product(const Layout& l, int E) {
 // A = X X^T from x, scaled
 DenseProduct gram(const Layout& l, int E, const void* x, void* a) {
   DenseProduct d = product(l, E);
-  d.nt = d.symmetric = true;
+  d.nt = true;
   d.width = l.mp;
   d.rows = d.w = x;
   d.rows_ld = d.w_ld = l.parts * l.Mp;
@@ -329,7 +329,7 @@ DenseProduct gram(const Layout& l, int E, const void* x, void* a) {
 // B = a I + b A + c A^2
 DenseProduct polynomial(const Layout& l, int E, const void* a, void* b, const float* c) {
   DenseProduct d = product(l, E);
-  d.nt = d.symmetric = true;
+  d.nt = true;
   d.width = l.mp;
   d.rows = d.w = d.mat = a;
   d.rows_ld = d.w_ld = d.out_ld = l.parts * l.mp;
@@ -395,16 +395,19 @@ Layout layout(int E, int N, int K) {
   return l;
 }
 
-// Whether one launch for all steps (ortho_cluster.cu) is modelled to be the faster.  A
-// product of its own takes some 3500 cycles more than its model says, which does not
-// matter where products are compared among themselves.
+// Whether one launch for all steps (ortho_cluster.cu) is modelled to be the faster.  The
+// models leave out what both take alike; against each other, a product of its own takes
+// some 3500 cycles more (its launch), and the clusters' cycles count 5/4: they read and
+// add a X where it is used, and a matrix has eight SMs at most.  Measured in clusters /
+// as products, us a step: 8 x 64 x 64 12.3 / 15.4, 8 x 256 x 512 17.4 / 19.9, 64 x 128
+// x 1024 34.5 / 40.2; 8 x 257 x 512 24.7 / 21.9, 8 x 256 x 2048 37.3 / 29.9.
 bool in_clusters(const Layout& l, int E) {
   if (ragged_form() != 0) return ragged_form() == 3;
   const float c[3] = {};
   const long long own = dense_cycles(gram(l, E, nullptr, nullptr)) +
                         dense_cycles(polynomial(l, E, nullptr, nullptr, c)) +
                         dense_cycles(apply(l, E, nullptr, nullptr, nullptr)) + 3 * 3500;
-  return cluster_plan(l, E).cycles < kModelSteps * own;
+  return cluster_plan(l, E).cycles * 5 / 4 < kModelSteps * own;
 }
 
 cudaError_t run(const DenseProduct& d, void* part, cudaStream_t stream) {

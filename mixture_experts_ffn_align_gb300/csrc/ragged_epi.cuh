@@ -158,14 +158,14 @@ __device__ __forceinline__ void rag_epi_load(const RagArgs& a, const RagTile& D,
     const RagDense& q = a.dense;
     const uint16_t* mat = reinterpret_cast<const uint16_t*>(q.mat) +
                           (long long)(D.row0 + c + odd) * a.ldo + (w - odd);
-    rag_load_words(x, mat, q.mat_lo != 0 ? mat + q.mat_lo : nullptr, a.ldo, D.rows - c, w < a.W,
-                   odd);
+    rag_load_words(x, mat, q.mat_lo != 0 ? mat + q.mat_lo : nullptr, a.ldo,
+                   min(D.rows - c, q.m - (D.row0 - D.e * q.m) - c), w < a.W, odd);
   }
 }
 // Whether there is something to read.
 template <int EPI>
 __device__ __forceinline__ bool rag_epi_loads(const RagArgs& a) {
-  return EPI == EPI_GATED_GRAD || (EPI == EPI_DENSE && a.dense.mat != nullptr && !a.dense.sym);
+  return EPI == EPI_GATED_GRAD || (EPI == EPI_DENSE && a.dense.mat != nullptr);
 }
 
 // 32 tokens from row row0 of this lane's column w of dz.
@@ -239,6 +239,7 @@ __device__ __forceinline__ uint32_t half_hi2(float& x, float& y) {
 }
 
 // 32 tokens from row tok (of the matrix) of this lane's column w; left: the tile's.
+// For products that are not symmetric and have no mat.
 __device__ __forceinline__ void rag_dense_tokens32(const RagArgs& a, const RagTile& D,
                                                    const uint32_t (&r)[32], int tok, int left,
                                                    int w, int lane) {
@@ -311,59 +312,6 @@ __device__ __forceinline__ void rag_dense_tokens32(const RagArgs& a, const RagTi
     return;
   }
   uint16_t* out = static_cast<uint16_t*>(a.out);
-  if (q.sym) {
-    // This lane's tokens as row w of the output: 64 bytes of it.  What lies past
-    // the matrix's columns is zero (those rows may be the next matrix's).
-    if (w < q.m) {
-      if (q.mat != nullptr) {
-        const uint4* mat =
-            reinterpret_cast<const uint4*>(q.mat + (base + w) * a.ldo + tok);
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          if (part == 0 || q.mat_lo != 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 x = __ldcg(mat + part * (q.mat_lo / 8) + i);
-              const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 f = unpack16<__half>(xs[k]);
-                v[8 * i + 2 * k] += q.c_mat * f.x;
-                v[8 * i + 2 * k + 1] += q.c_mat * f.y;
-              }
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if (tok + j == w) v[j] += q.c_diag;
-        if (j >= live) v[j] = 0.0f;
-      }
-    }
-    uint32_t pk[16], lo[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      float x = v[2 * j], y = v[2 * j + 1];
-      pk[j] = half_hi2(x, y);
-      lo[j] = Half16<__half>::pack(x, y);
-    }
-    if (w < q.m) {
-      uint4* p = reinterpret_cast<uint4*>(out + (base + w) * a.ldo + tok);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-        if (q.out_lo != 0)
-          p[q.out_lo / 8 + i] = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-      }
-    }
-    if (q.tri && D.tok != D.w_tile) {         // and as column w
-      out += (base + tok) * a.ldo + w;
-      rag_store_packed32(pk, out, a.ldo, live, w, a.W, lane);
-      if (q.out_lo != 0) rag_store_packed32(lo, out + q.out_lo, a.ldo, live, w, a.W, lane);
-    }
-    return;
-  }
   uint32_t pk[16], lo[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -376,28 +324,95 @@ __device__ __forceinline__ void rag_dense_tokens32(const RagArgs& a, const RagTi
   if (q.out_lo != 0) rag_store_packed32(lo, out + q.out_lo, a.ldo, live, w, a.W, lane);
 }
 
-// The same of a product that is not symmetric, with mat (as h, read by
-// rag_dense_load): two neighbouring lanes swap tokens first.  A lo part of mat may
-// be the output's own: each word is read and written by one lane.
-__device__ __forceinline__ void rag_dense_add_tokens32(const RagArgs& a, const RagTile& D,
-                                                       const uint32_t (&r)[32], const Words32& h,
-                                                       int tok, int left, int w, int lane) {
+// The same with mat (as h, read by rag_epi_load) where `loads`: two neighbouring lanes
+// swap tokens first.  A lo part of mat may be the output's own: each word is read and
+// written by one lane.  Of a symmetric product's tiles beside the diagonal (tri) the
+// values are stored once more as rows from the columns: lanes swap back, and four of
+// them put 64 bytes of a row together.
+template <bool SYM>
+__device__ __forceinline__ void rag_dense_pairs32(const RagArgs& a, const RagTile& D,
+                                                  const uint32_t (&r)[32], const Words32& h,
+                                                  bool loads, int tok, int left, int w, int lane) {
   const RagDense& q = a.dense;
-  const int live = min(q.m - tok, left), odd = lane & 1;
-  uint16_t* out = static_cast<uint16_t*>(a.out) + ((long long)D.e * q.m + tok + odd) * a.ldo + w - odd;
+  const int live = min(q.m - tok, left), odd = lane & 1, c0 = w - odd;
+  const long long base = (long long)D.e * q.m;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + (base + tok + odd) * a.ldo + c0;
+  uint32_t pk[16], lo[16];
 #pragma unroll
   for (int t = 0; t < 16; ++t) {
     const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? r[2 * t] : r[2 * t + 1], 1);
-    const float2 hi = unpack16<__half>(h.a[t]), lo = unpack16<__half>(h.b[t]);
-    float x = q.c_acc * __uint_as_float(odd ? other : r[2 * t]) + q.c_mat * (hi.x + lo.x);
-    float y = q.c_acc * __uint_as_float(odd ? r[2 * t + 1] : other) + q.c_mat * (hi.y + lo.y);
-    const uint32_t p = half_hi2(x, y);
-    if (w < a.W && 2 * t + odd < live) {
-      *reinterpret_cast<uint32_t*>(out) = p;
-      if (q.out_lo != 0) *reinterpret_cast<uint32_t*>(out + q.out_lo) = Half16<__half>::pack(x, y);
+    float x = q.c_acc * __uint_as_float(odd ? other : r[2 * t]);
+    float y = q.c_acc * __uint_as_float(odd ? r[2 * t + 1] : other);
+    if (loads) {
+      const float2 mh = unpack16<__half>(h.a[t]), ml = unpack16<__half>(h.b[t]);
+      x += q.c_mat * (mh.x + ml.x);
+      y += q.c_mat * (mh.y + ml.y);
+    }
+    const bool in = 2 * t + odd < live;
+    if (SYM) {
+      // rows behind the matrix (the next one's) are zero columns of the output
+      if (tok + 2 * t + odd == c0) x += q.c_diag;
+      if (tok + 2 * t + odd == c0 + 1) y += q.c_diag;
+      x = in ? x : 0.0f;
+      y = in ? y : 0.0f;
+    }
+    pk[t] = half_hi2(x, y);
+    lo[t] = Half16<__half>::pack(x, y);
+    if (in && w < a.W) {
+      *reinterpret_cast<uint32_t*>(out) = pk[t];
+      if (q.out_lo != 0) *reinterpret_cast<uint32_t*>(out + q.out_lo) = lo[t];
     }
     out += 2 * a.ldo;
   }
+  if (!SYM || !q.tri || D.tok == D.w_tile) return;
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    if (part == 1 && q.out_lo == 0) break;
+    // tokens 2 t and 2 t + 1 of this lane's column w
+    uint32_t p[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      const uint32_t v = part == 0 ? pk[t] : lo[t];
+      p[t] = __byte_perm(v, __shfl_xor_sync(0xffffffffu, v, 1), odd ? 0x3276u : 0x5410u);
+    }
+    // the four 16-byte pieces of four lanes' rows, transposed among the lanes
+    uint32_t x[8], y[8];
+    const bool b1 = lane & 2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t v = __shfl_xor_sync(0xffffffffu, b1 ? p[i] : p[8 + i], 2);
+      x[i] = b1 ? v : p[i];
+      y[i] = b1 ? p[8 + i] : v;
+    }
+    uint4 row[4];
+    uint32_t* rw = reinterpret_cast<uint32_t*>(row);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = __shfl_xor_sync(0xffffffffu, odd ? x[i] : x[4 + i], 1);
+      const uint32_t v = __shfl_xor_sync(0xffffffffu, odd ? y[i] : y[4 + i], 1);
+      rw[i] = odd ? u : x[i];
+      rw[4 + i] = odd ? x[4 + i] : u;
+      rw[8 + i] = odd ? v : y[i];
+      rw[12 + i] = odd ? y[4 + i] : v;
+    }
+    const int w0 = w & ~3;
+    uint16_t* to = static_cast<uint16_t*>(a.out) + (base + w0) * a.ldo + tok + 8 * (lane & 3) +
+                   (part == 0 ? 0 : q.out_lo);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (w0 + i < q.m) *reinterpret_cast<uint4*>(to + i * a.ldo) = row[i];
+  }
+}
+template <bool SYM>
+__device__ __forceinline__ void rag_dense_store32(const RagArgs& a, const RagTile& D,
+                                                  const uint32_t (&r)[32], const Words32& h,
+                                                  bool loads, int tok, int left, int w, int lane) {
+  if (SYM)
+    rag_dense_pairs32<true>(a, D, r, h, loads, tok, left, w, lane);
+  else if (loads)
+    rag_dense_pairs32<false>(a, D, r, h, true, tok, left, w, lane);
+  else
+    rag_dense_tokens32(a, D, r, tok, left, w, lane);
 }
 
 // ------------------------------------------------------------- joining slices

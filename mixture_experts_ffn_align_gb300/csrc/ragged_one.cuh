@@ -433,11 +433,9 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
             else
               rag_gated_grad_tokens32<T, false>(args, r, h, D.row0 + c, D.rows - c, w, lane);
           } else {
-            const int tok = D.tok * args.dense.per + c;
-            if (loads)
-              rag_dense_add_tokens32(args, D, r, h, tok, D.rows - c, w, lane);
-            else
-              rag_dense_tokens32(args, D, r, tok, D.rows - c, w, lane);
+            // the symmetric products are the forward ones
+            rag_dense_store32<OP == RAG_FWD>(args, D, r, h, loads, D.tok * args.dense.per + c,
+                                             D.rows - c, w, lane);
           }
           __syncwarp();
         }
