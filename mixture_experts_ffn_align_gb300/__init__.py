@@ -504,13 +504,19 @@ def ragged_gemm_wgrad(p: Ragged, dy, x, expert_offsets, dw, workspace, accumulat
         _raw_stream(stream, dev)), "ragged_gemm_wgrad")
 
 
-def _row_stride(name: str, t, cols) -> int:
-    """Row stride of a matrix of this many columns, in elements (a single row's, which
-    PyTorch leaves open: cols)."""
-    ld = t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else cols
-    if ld < cols:
-        _overlap(name, ld, cols)
-    return ld
+def _matrix(name: str, t, shape, dtype, dev):
+    """Data pointer and row stride (in elements, any that holds a row) of a matrix on GPU
+    dev."""
+    rows, cols = shape
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        ld, one = t.stride()
+        if one == 1 and ld >= cols:
+            return t.data_ptr(), ld
+        if rows <= 1 and (one == 1 or cols == 1):      # PyTorch leaves it open
+            return t.data_ptr(), cols
+        if one == 1:
+            _overlap(name, ld, cols)
+    _fail(name, t, shape, dtype, "any", dev)
 
 
 def ragged_gated(p: Ragged, x, w13, expert_offsets, z, workspace, h=None, bias=None, alpha=1.0,
@@ -523,12 +529,12 @@ def ragged_gated(p: Ragged, x, w13, expert_offsets, z, workspace, h=None, bias=N
     v = p._v
     dev = x.get_device()
     ws, n = _bytes("workspace", workspace, dev)
-    ldz = _row_stride("z", z, p.N // 2)
+    zp, ldz = _matrix("z", z, v.half_n, v.dtype, dev)
     _check(lib().ragged_gated(
         p._ref, _rows("x", x, v.x, v.dtype, v.ldx, dev), _dense("w13", w13, v.w, v.dtype, dev),
         None if bias is None else _dense("bias", bias, v.bias, v.dtype, dev),
         _dense("expert_offsets", expert_offsets, v.offsets, v.int32, dev), alpha, beta, limit,
-        _rows("z", z, v.half_n, v.dtype, ldz, dev), ldz,
+        zp, ldz,
         None if h is None else _rows("h", h, v.y, v.dtype, v.ldy, dev), ws, n,
         _raw_stream(stream, dev)), "ragged_gated")
 
@@ -542,12 +548,12 @@ def ragged_gated_dgrad(p: Ragged, dy, w2, h, expert_offsets, dh, workspace, z=No
     v = p._v
     dev = dy.get_device()
     ws, n = _bytes("workspace", workspace, dev)
-    ldh, lddh = _row_stride("h", h, 2 * p.K), _row_stride("dh", dh, 2 * p.K)
+    hp, ldh = _matrix("h", h, v.twice_k, v.dtype, dev)
+    dhp, lddh = _matrix("dh", dh, v.twice_k, v.dtype, dev)
     _check(lib().ragged_gated_dgrad(
         p._ref, _rows("dy", dy, v.y, v.dtype, v.ldy, dev), _dense("w2", w2, v.w, v.dtype, dev),
-        _rows("h", h, v.twice_k, v.dtype, ldh, dev), ldh,
-        _dense("expert_offsets", expert_offsets, v.offsets, v.int32, dev), alpha, beta, limit,
-        _rows("dh", dh, v.twice_k, v.dtype, lddh, dev), lddh,
+        hp, ldh, _dense("expert_offsets", expert_offsets, v.offsets, v.int32, dev), alpha, beta, limit,
+        dhp, lddh,
         None if z is None else _rows("z", z, v.x, v.dtype, v.ldx, dev), ws, n,
         _raw_stream(stream, dev)), "ragged_gated_dgrad")
 

@@ -397,7 +397,7 @@ Layout layout(int E, int N, int K) {
 
 // Whether one launch for all steps (ortho_cluster.cu) is modelled to be the faster.  The
 // models leave out what both take alike; against each other, a product of its own takes
-// some 3500 cycles more (its launch), and the clusters' cycles count 5/4: they read and
+// some 3500 cycles more (its launch), and the clusters' cycles count 6/5: they read and
 // add a X where it is used, and a matrix has eight SMs at most.  Measured in clusters /
 // as products, us a step: 8 x 64 x 64 12.3 / 15.4, 8 x 256 x 512 17.4 / 19.9, 64 x 128
 // x 1024 34.5 / 40.2; 8 x 257 x 512 24.7 / 21.9, 8 x 256 x 2048 37.3 / 29.9.
@@ -407,7 +407,7 @@ bool in_clusters(const Layout& l, int E) {
   const long long own = dense_cycles(gram(l, E, nullptr, nullptr)) +
                         dense_cycles(polynomial(l, E, nullptr, nullptr, c)) +
                         dense_cycles(apply(l, E, nullptr, nullptr, nullptr)) + 3 * 3500;
-  return cluster_plan(l, E).cycles * 5 / 4 < kModelSteps * own;
+  return cluster_plan(l, E).cycles * 6 / 5 < kModelSteps * own;
 }
 
 cudaError_t run(const DenseProduct& d, void* part, cudaStream_t stream) {

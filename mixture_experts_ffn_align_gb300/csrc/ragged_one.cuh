@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
       }
       const int acc = local & 1;
       [[maybe_unused]] Words32 h_next;
-      [[maybe_unused]] const bool loads = splits == 1 && rag_epi_loads<EPI>(args);
+      [[maybe_unused]] const bool loads =
+          splits == 1 && rag_epi_loads<EPI>(args);
       if constexpr (EPI == EPI_GATED_GRAD || EPI == EPI_DENSE) {
         const int c = 32 * ((warp - 2) >> 2);
         if (loads && c < D.rows)
@@ -410,32 +411,30 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
         for (int c = 32 * ((warp - 2) >> 2); c < D.rows; c += 64) {
           uint32_t r[32];
           tmem_ld_32x32b_x32(taddr + c, r);
-          [[maybe_unused]] Words32 h;
-          if constexpr (EPI == EPI_GATED_GRAD || EPI == EPI_DENSE) {
-            if (loads) {
-              h = h_next;
-              if (c + 64 < D.rows) rag_epi_load<EPI>(args, D, h_next, c + 64, w, lane);
-            }
-          }
-          tmem_ld_wait();
-          if (splits > 1)
-            rag_store_part(args, r, t, rank, c, D.rows, q * 32 + lane);
-          else if constexpr (EPI == EPI_GATED)
-            {
-            if (clamp)
+          if constexpr (EPI == EPI_GATED) {
+            tmem_ld_wait();
+            if (splits > 1)
+              rag_store_part(args, r, t, rank, c, D.rows, q * 32 + lane);
+            else if (clamp)
               rag_gated_tokens32<T, true>(args, r, bias, D.row0 + c, D.rows - c, w, lane);
             else
               rag_gated_tokens32<T, false>(args, r, bias, D.row0 + c, D.rows - c, w, lane);
-          }
-          else if constexpr (EPI == EPI_GATED_GRAD) {
-            if (clamp)
+          } else {
+            const Words32 h = h_next;
+            tmem_ld_wait();
+            if (splits > 1) {
+              rag_store_part(args, r, t, rank, c, D.rows, q * 32 + lane);
+              continue;
+            }
+            if (loads && c + 64 < D.rows) rag_epi_load<EPI>(args, D, h_next, c + 64, w, lane);
+            if constexpr (EPI == EPI_DENSE)
+              // the symmetric products are the forward ones
+              rag_dense_store32<OP == RAG_FWD>(args, D, r, h, loads, D.tok * args.dense.per + c,
+                                               D.rows - c, w, lane);
+            else if (clamp)
               rag_gated_grad_tokens32<T, true>(args, r, h, D.row0 + c, D.rows - c, w, lane);
             else
               rag_gated_grad_tokens32<T, false>(args, r, h, D.row0 + c, D.rows - c, w, lane);
-          } else {
-            // the symmetric products are the forward ones
-            rag_dense_store32<OP == RAG_FWD>(args, D, r, h, loads, D.tok * args.dense.per + c,
-                                             D.rows - c, w, lane);
           }
           __syncwarp();
         }
