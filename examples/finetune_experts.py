@@ -1,13 +1,14 @@
 """Fine-tunes a routed expert layer, then serves it in four bits.
 
-A student layer learns a random teacher's outputs: router, padded layout,
-expert products, their gradients, clipping by the global norm and a plain
-gradient step, all on the library's kernels (the activation between the two
-products and the parameter update are elementary torch).  Then the learned
-weights are quantised to MXFP4 and run in the two forms the library has for
-them: 4-bit activations (ragged_gemm_mxfp4) and 8-bit ones (fused_experts).
+A student layer learns a random teacher's outputs: router, padded layout, the gated
+block with its gradient, the down projection and the weights' gradients, clipping by
+the global norm and an update, all on the library's kernels.  The update is a plain
+gradient step or, with "orthogonal", momentum whose matrices are orthogonalised
+(moe_orthogonalize) before they are subtracted.  Then the learned weights are
+quantised to MXFP4 and run in the two forms the library has for them: 4-bit
+activations (ragged_gemm_mxfp4) and 8-bit ones (fused_experts).
 
-    python examples/finetune_experts.py [steps]
+    python examples/finetune_experts.py [steps] [plain|orthogonal]
 """
 from __future__ import annotations
 
@@ -45,7 +46,7 @@ class ExpertLayer:
                            for _ in range(2))
         self.y2, self.dy2 = (torch.zeros(rows, H, dtype=torch.bfloat16, device="cuda")
                              for _ in range(2))
-        self.dz = torch.zeros(rows, I, dtype=torch.bfloat16, device="cuda")
+        self.z = torch.zeros(rows, I, dtype=torch.bfloat16, device="cuda")
         self.y = torch.empty(M, H, dtype=torch.bfloat16, device="cuda")
 
     def route(self, x, logits):
@@ -62,9 +63,7 @@ class ExpertLayer:
 
     def forward(self, w13, w2):
         b, off = self.b, self.b["expert_offsets"]
-        moe.ragged_gemm(self.up, b["x_perm"], w13, off, self.h, self.ws)
-        g, u = self.h.float().split(I, 1)
-        self.z = (torch.nn.functional.silu(g) * u).bfloat16()
+        moe.ragged_gated(self.up, b["x_perm"], w13, off, self.z, self.ws, h=self.h)
         moe.ragged_gemm(self.down, self.z, w2, off, self.y2, self.ws)
         moe.unpermute_reduce(self.p, self.y2, b["inv_perm"], self.weights, self.y)
         return self.y
@@ -74,12 +73,25 @@ class ExpertLayer:
         off = self.b["expert_offsets"]
         self.dy2.copy_(dy.float()[self.token] * self.row_weight[:, None])
         moe.ragged_gemm_wgrad(self.down, self.dy2, self.z, off, dw2, self.ws)
-        moe.ragged_gemm_dgrad(self.down, self.dy2, w2, off, self.dz, self.ws)
-        g, u = self.h.float().split(I, 1)
-        s, dz = torch.sigmoid(g), self.dz.float()
-        self.dh[:, :I] = dz * u * s * (1 + g * (1 - s))
-        self.dh[:, I:] = dz * g * s
+        moe.ragged_gated_dgrad(self.down, self.dy2, w2, self.h, off, self.dh, self.ws)
         moe.ragged_gemm_wgrad(self.up, self.dh, self.b["x_perm"], off, dw13, self.ws)
+
+
+class Orthogonal:
+    """Momentum of float32 weights [E, N, K]; each matrix of the update is orthogonalised,
+    with singular values near sqrt(max(1, N / K))."""
+
+    def __init__(self, w, momentum=0.9):
+        self.m, self.momentum = torch.zeros_like(w), momentum
+        self.out = torch.empty(w.shape, dtype=torch.bfloat16, device="cuda")
+        self.scale = max(1.0, w.shape[1] / w.shape[2]) ** 0.5
+        self.ws = torch.empty(moe.moe_orthogonalize_workspace_bytes(*w.shape), dtype=torch.uint8,
+                              device="cuda")
+
+    def step(self, w, grad, lr):
+        self.m.mul_(self.momentum).add_(grad)
+        moe.moe_orthogonalize(self.m, self.out, self.ws, scale=self.scale)
+        w.sub_(self.out, alpha=lr)
 
 
 def mxfp4(w):
@@ -121,7 +133,8 @@ def serve_w4a8(layer, x, q13, q2):
     return y
 
 
-def main(steps: int = 60, lr: float = 2.0, max_norm: float = 1.0, verbose: bool = True):
+def main(steps: int = 60, update: str = "plain", lr: float | None = None, max_norm: float = 1.0,
+         verbose: bool = True):
     g = torch.Generator(device="cuda").manual_seed(0)
 
     def randn(*shape, scale=1.0):
@@ -135,6 +148,8 @@ def main(steps: int = 60, lr: float = 2.0, max_norm: float = 1.0, verbose: bool 
     masters = [randn(E, 2 * I, H, scale=0.06), randn(E, H, I, scale=0.06)]
     w13, w2 = (w.bfloat16() for w in masters)
     grads = [torch.empty(w.shape, device="cuda") for w in masters]      # float32
+    orthogonal = [Orthogonal(m) for m in masters] if update == "orthogonal" else None
+    lr = lr if lr is not None else 0.02 if orthogonal else 2.0
     norm = torch.empty((), device="cuda")
     ws = torch.empty(moe.moe_clip_workspace_bytes(), dtype=torch.uint8, device="cuda")
     losses, norms = [], []
@@ -144,8 +159,11 @@ def main(steps: int = 60, lr: float = 2.0, max_norm: float = 1.0, verbose: bool 
         layer.backward(err * (2 / M), w13, w2, *grads)
         moe.moe_clip_grad_norm(grads, max_norm, norm, ws)
         norms.append(norm.clone())
-        for w, m, d in zip((w13, w2), masters, grads):
-            m.sub_(d, alpha=lr)
+        for i, (w, m, d) in enumerate(zip((w13, w2), masters, grads)):
+            if orthogonal:
+                orthogonal[i].step(m, d, lr)
+            else:
+                m.sub_(d, alpha=lr)
             w.copy_(m)
         if verbose and step % 10 == 0:
             print(f"step {step:3d}  loss {float(losses[-1]):.4f}  gradient norm {float(norm):.3f}")
@@ -168,4 +186,4 @@ def main(steps: int = 60, lr: float = 2.0, max_norm: float = 1.0, verbose: bool 
 
 
 if __name__ == "__main__":
-    main(*(int(a) for a in sys.argv[1:2]))
+    main(*(int(a) for a in sys.argv[1:2]), *sys.argv[2:3])

@@ -595,7 +595,7 @@ moe_status moe_clip_grad_norm(int n, const void* const* grads, void* const* outs
  *    the polynomial's values within 16: elements past that are infinities.
  *  - eps: at least 1e-12; a zero matrix gives zeros.
  *  - Products take operands of 11 bits (22 where N or K is at most 128), X itself is
- *    kept with 22 bits until the last two steps, sums are fp32: the result is within
+ *    kept with 22 bits until the last step, sums are fp32: the result is within
  *    about 0.25% (rms) of the exact one, its own rounding to bf16 (0.17%) among that.
  *    A square beyond fp32's range makes the norm infinite and the result zero;
  *    infinities and NaN give NaN in their matrix.

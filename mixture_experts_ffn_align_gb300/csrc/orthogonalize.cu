@@ -16,13 +16,15 @@
 // typical elements are 1 / sqrt(m M) and less.
 //
 // The steps raise small singular values up to 3.4-fold each while large ones stay, so
-// what a rounding of X loses beside a large singular value grows too (a gradient with
-// one direction 50 times the rest's: 1% off).  So X is kept as a hi and a lo part, 22
-// bits together, in all steps but the last two; products take the hi part, and X =
-// a X + (b A + c A^2) X adds a times both in the epilogue, where rounding the hi part
-// only costs what is multiplied by b A + c A^2.  The last two steps need that no more
-// and fold a into B: B = a I + b A + c A^2, X = B X.  The error is then 0.08 to 0.14%
-// whatever the spectrum, less than the rounding of the result to bf16 (0.17%).
+// what a rounding of X loses beside a large singular value grows too (one direction
+// 50 times the rest's: 1% off; and what is noise in the null space of a gradient of
+// few rows grows likewise).  So X is kept as a hi and a lo part, 22 bits together, in
+// all steps but the last; products take the hi part, and X = a X + (b A + c A^2) X
+// adds a times both in the epilogue, where rounding the hi part only costs what is
+// multiplied by b A + c A^2.  The last step folds a into B: B = a I + b A + c A^2, X =
+// B X, whose smaller elements round better.  The error is then 0.02 to 0.16% whatever
+// the spectrum and rank, less than the rounding of the result to bf16 (0.17%); with the
+// last two steps folded it was up to 0.29% where the rank is low.
 // Sums over few elements average less: up to m = 128, where all products are short,
 // operands too are the hi and the lo part, and a product is three (hi hi + hi lo + lo
 // hi) over one accumulator.
@@ -44,7 +46,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPrecise = 128;                 // shorter sides up to here take hi and lo parts
-constexpr int kFolded = 2;                    // last steps that fold a X into B
+constexpr int kFolded = 1;                    // last steps that fold a X into B
 constexpr float kScaleX = 4096.0f, kScaleA = 1024.0f, kScaleB = 1024.0f;
 constexpr int kMaxChunks = 304;               // partial sums of a matrix
 constexpr int kRowsPerThread = 4, kTiles = 4; // of k_ortho_scale, k_ortho_transpose
