@@ -258,13 +258,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
       // ---------------------------------------------------------- epilogue
       const int q = warp & 3;
-      const bool loads = f.splits == 1 && rag_epi_loads<EPI_DENSE>(a);
+      const bool loads = f.splits == 1 && a.dense.mat != nullptr;
+      const int part = (warp - 2) >> 2;
+      constexpr int STEP = 4 * EPI_WARPS;
       for (int i = rank; ok && i < items; i += ctas) {
         const Item it = item_of(f, args, e, i);
         const int acc = local & 1, w = it.tile.w_tile * 128 + q * 32 + lane;
-        Words32 h_next;
-        if (loads && 32 * ((warp - 2) >> 2) < it.tile.rows)
-          rag_epi_load<EPI_DENSE>(a, it.tile, h_next, 32 * ((warp - 2) >> 2), w, lane);
+        Words16 mat_next;
+        if (loads && 16 * part < it.tile.rows)
+          rag_dense_load(a, it.tile, mat_next, 16 * part, w, lane);
         int got = 0;
         if (lane == 0) got = wait(tfull_bar(acc), (local >> 1) & 1);
         ok = __shfl_sync(0xffffffffu, got, 0);
@@ -272,20 +274,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
 #pragma unroll 1
-        for (int c = 32 * ((warp - 2) >> 2); c < it.tile.rows; c += 64) {
-          uint32_t r[32];
-          const Words32 h = h_next;
-          tmem_ld_32x32b_x32(taddr + c, r);
-          if (loads && c + 64 < it.tile.rows) rag_epi_load<EPI_DENSE>(a, it.tile, h_next, c + 64, w, lane);
+        for (int c = 16 * part; c < it.tile.rows; c += STEP) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(taddr + c, r);
+          const Words16 h = mat_next;
           tmem_ld_wait();
+          const int tok = it.tile.tok * f.per + c, left = it.tile.rows - c;
+          if (loads && c + STEP < it.tile.rows) rag_dense_load(a, it.tile, mat_next, c + STEP, w, lane);
           if (f.splits > 1)
             rag_store_part(a, r, e * f.tiles + it.t, it.slice, c, it.tile.rows, q * 32 + lane);
           else if (f.nt)
-            rag_dense_store32<true>(a, it.tile, r, h, loads, it.tile.tok * f.per + c,
-                                    it.tile.rows - c, w, lane);
+            rag_dense_store16<true>(a, it.tile, r, h, loads, tok, left, w, lane);
           else
-            rag_dense_store32<false>(a, it.tile, r, h, loads, it.tile.tok * f.per + c,
-                                     it.tile.rows - c, w, lane);
+            rag_dense_store16<false>(a, it.tile, r, h, loads, tok, left, w, lane);
           __syncwarp();
         }
         tc_fence_before();

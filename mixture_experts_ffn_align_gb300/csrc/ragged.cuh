@@ -482,12 +482,13 @@ __device__ __forceinline__ void rag_store_tokens32(uint32_t (&r)[32], bool has_b
 }
 
 // A reduction that the CTAs of a cluster share (splits > 1; one tile for each
-// cluster).  32 tokens from token c of this CTA's sums of tile t: column col.
-__device__ __forceinline__ void rag_store_part(const RagArgs& a, const uint32_t (&r)[32], int t,
+// cluster).  N tokens from token c of this CTA's sums of tile t: column col.
+template <int N>
+__device__ __forceinline__ void rag_store_part(const RagArgs& a, const uint32_t (&r)[N], int t,
                                                int rank, int c, int rows, int col) {
   float* p = a.part + (((size_t)t * a.splits + rank) * a.tile_rows + c) * 128 + col;
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
+  for (int j = 0; j < N; ++j)
     if (c + j < rows) p[128 * j] = __uint_as_float(r[j]);
 }
 // After the cluster barrier: this CTA's share of tile t's tokens, the slices

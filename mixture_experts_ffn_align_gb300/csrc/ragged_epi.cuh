@@ -133,44 +133,21 @@ __device__ __forceinline__ void rag_gated_tokens32(const RagArgs& a, uint32_t (&
 struct Words32 {
   uint32_t a[16], b[16];
 };
-// c: tokens of the tile before the 32.  (One loop for both, with two pointers, spilled
-// registers in the gradient's kernel: 256 experts, 7168 -> 2048, 1168 us instead of
-// 1113.)
-template <int EPI>
-__device__ __forceinline__ void rag_epi_load(const RagArgs& a, const RagTile& D, Words32& x, int c,
-                                             int w, int lane) {
-  const int odd = lane & 1;
+// c: tokens of the tile before the 32.
+__device__ __forceinline__ void rag_gated_load(const RagArgs& a, const RagTile& D, Words32& x, int c,
+                                               int w, int lane) {
+  const RagGated& q = a.gated;
+  const int odd = lane & 1, live = D.rows - c;
   const bool inside = w < a.W;
-  if (EPI == EPI_GATED_GRAD) {
-    const RagGated& q = a.gated;
-    const int live = D.rows - c;
-    const uint16_t* h = static_cast<const uint16_t*>(q.h) + (long long)(D.row0 + c + odd) * q.ldh +
-                        (w - odd);
+  const uint16_t* h = static_cast<const uint16_t*>(q.h) + (long long)(D.row0 + c + odd) * q.ldh +
+                      (w - odd);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const bool in = inside && 2 * j + odd < live;
-      x.a[j] = in ? *reinterpret_cast<const uint32_t*>(h) : 0u;
-      x.b[j] = in ? *reinterpret_cast<const uint32_t*>(h + q.inter) : 0u;
-      h += 2 * q.ldh;
-    }
-  } else {
-    const RagDense& q = a.dense;
-    const int live = min(D.rows - c, q.m - (D.row0 - D.e * q.m) - c);
-    const uint16_t* mat = reinterpret_cast<const uint16_t*>(q.mat) +
-                          (long long)(D.row0 + c + odd) * a.ldo + (w - odd);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const bool in = inside && 2 * j + odd < live;
-      x.a[j] = in ? __ldcg(reinterpret_cast<const uint32_t*>(mat)) : 0u;
-      x.b[j] = in && q.mat_lo != 0 ? __ldcg(reinterpret_cast<const uint32_t*>(mat + q.mat_lo)) : 0u;
-      mat += 2 * a.ldo;
-    }
+  for (int j = 0; j < 16; ++j) {
+    const bool in = inside && 2 * j + odd < live;
+    x.a[j] = in ? *reinterpret_cast<const uint32_t*>(h) : 0u;
+    x.b[j] = in ? *reinterpret_cast<const uint32_t*>(h + q.inter) : 0u;
+    h += 2 * q.ldh;
   }
-}
-// Whether there is something to read.
-template <int EPI>
-__device__ __forceinline__ bool rag_epi_loads(const RagArgs& a) {
-  return EPI == EPI_GATED_GRAD || (EPI == EPI_DENSE && a.dense.mat != nullptr);
 }
 
 // 32 tokens from row row0 of this lane's column w of dz.
@@ -231,10 +208,6 @@ __device__ __forceinline__ RagTile rag_dense_tile(const RagArgs& a, int t) {
   return T;
 }
 
-__device__ __forceinline__ float half_hi(float v, uint16_t& hi) {
-  hi = Half16<__half>::bits(v);
-  return v - Half16<__half>::value(hi);
-}
 __device__ __forceinline__ uint32_t half_hi2(float& x, float& y) {
   const uint32_t p = Half16<__half>::pack(x, y);
   const float2 v = unpack16<__half>(p);
@@ -243,181 +216,195 @@ __device__ __forceinline__ uint32_t half_hi2(float& x, float& y) {
   return p;
 }
 
-// 32 tokens from row tok (of the matrix) of this lane's column w; left: the tile's.
-// For products that are not symmetric and have no mat.
-__device__ __forceinline__ void rag_dense_tokens32(const RagArgs& a, const RagTile& D,
-                                                   const uint32_t (&r)[32], int tok, int left,
-                                                   int w, int lane) {
+// Sixteen tokens at a time: with 32, twice the unrolled code and registers, the steps of
+// short products took a sixth longer (16 x 517 x 1031: 58 us).
+//
+// mat and its lo part at two columns of 16 tokens, read a chunk ahead.
+struct Words16 {
+  uint32_t a[8], b[8];
+};
+template <bool FULL, bool LO>
+__device__ __forceinline__ void rag_load_mat(Words16& x, const uint16_t* mat, long long lo,
+                                             long long ld, int live, int odd) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const bool in = FULL || 2 * j + odd < live;
+    x.a[j] = in ? __ldcg(reinterpret_cast<const uint32_t*>(mat)) : 0u;
+    x.b[j] = LO && in ? __ldcg(reinterpret_cast<const uint32_t*>(mat + lo)) : 0u;
+    mat += 2 * ld;
+  }
+}
+__device__ __forceinline__ void rag_dense_load(const RagArgs& a, const RagTile& D, Words16& x, int c,
+                                               int w, int lane) {
   const RagDense& q = a.dense;
-  // rows from here on in the matrix, and in the tile (the next tile's may be among 32)
-  const int live = min(q.m - tok, left);
-  const long long base = (long long)D.e * q.m;
-  float v[32];
+  const int odd = lane & 1, live = min(D.rows - c, q.m - (D.row0 - D.e * q.m) - c);
+  const bool inside = w < a.W, full = w - lane + 32 <= a.W && live >= 16;
+  const uint16_t* mat = reinterpret_cast<const uint16_t*>(q.mat) +
+                        (long long)(D.row0 + c + odd) * a.ldo + (w - odd);
+  if (q.mat_lo == 0) {
+    if (full)
+      rag_load_mat<true, false>(x, mat, 0, a.ldo, 16, odd);
+    else
+      rag_load_mat<false, false>(x, mat, 0, a.ldo, inside ? live : 0, odd);
+  } else {
+    if (full)
+      rag_load_mat<true, true>(x, mat, q.mat_lo, a.ldo, 16, odd);
+    else
+      rag_load_mat<false, true>(x, mat, q.mat_lo, a.ldo, inside ? live : 0, odd);
+  }
+}
+
+// The last product: 16 tokens from row tok (of the matrix) of this lane's column w,
+// `live` of them to be stored.
+__device__ __forceinline__ void rag_dense_final16(const RagArgs& a, const RagTile& D,
+                                                  const uint32_t (&r)[16], int tok, int live, int w,
+                                                  int lane) {
+  const RagDense& q = a.dense;
+  uint32_t pk[8];              // tokens 2 j and 2 j + 1
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = q.c_acc * __uint_as_float(r[j]);
-  if (q.final_out != nullptr) {
-    __nv_bfloat16* out = q.final_out;
-    if (q.transposed) {                       // a lane's tokens lie side by side
-      out += ((long long)D.e * a.W + w) * q.m + tok;
-      if (w < a.W && live >= 32 && q.m % 8 == 0) {
+  for (int j = 0; j < 8; ++j)
+    pk[j] = Half16<__nv_bfloat16>::pack(q.c_acc * __uint_as_float(r[2 * j]),
+                                        q.c_acc * __uint_as_float(r[2 * j + 1]));
+  uint16_t* out = reinterpret_cast<uint16_t*>(q.final_out);
+  if (!q.transposed) {
+    out += ((long long)D.e * q.m + tok) * a.W + w;
+    if (a.W % 2 == 0) {        // neighbouring columns swap: 4-byte pieces of two tokens
+      const int odd = lane & 1;
+      out += odd ? a.W - 1 : 0;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8)
-          *reinterpret_cast<uint4*>(out + j) = make_uint4(
-              Half16<__nv_bfloat16>::pack(v[j], v[j + 1]),
-              Half16<__nv_bfloat16>::pack(v[j + 2], v[j + 3]),
-              Half16<__nv_bfloat16>::pack(v[j + 4], v[j + 5]),
-              Half16<__nv_bfloat16>::pack(v[j + 6], v[j + 7]));
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t v = __byte_perm(pk[j], __shfl_xor_sync(0xffffffffu, pk[j], 1),
+                                       odd ? 0x3276u : 0x5410u);
+        if (w < a.W && 2 * j + odd < live) *reinterpret_cast<uint32_t*>(out) = v;
+        out += 2 * a.W;
       }
-      if (live < 32 || q.m % 8 != 0) {
-        // Rows that start anywhere, or end here: the warp's 32 x 32 values are turned
-        // (pairs of tokens in a register, halves swapped between lanes 16 to 1
-        // apart), so that a store writes one row's 32 tokens.  From each lane's own row
-        // they went out as 32 sectors for 64 bytes (16 matrices of 1031 x 517: 90 us).
-        uint32_t pk[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) pk[j] = Half16<__nv_bfloat16>::pack(v[2 * j], v[2 * j + 1]);
-#pragma unroll
-        for (int o = 16; o >= 2; o >>= 1) {
-          const bool up = lane & o;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (j & (o >> 1)) continue;
-            const int k = j | (o >> 1);
-            const uint32_t x = __shfl_xor_sync(0xffffffffu, up ? pk[j] : pk[k], o);
-            if (up) pk[j] = x; else pk[k] = x;
-          }
-        }
-        // now pk[j]: tokens (lane & ~1) and the next of row 2 j + (lane & 1) of the 32
-        __nv_bfloat16* base_out =
-            q.final_out + ((long long)D.e * a.W + (w - lane)) * q.m + tok + lane;
-        const uint32_t sel = (lane & 1) ? 0x3276u : 0x5410u;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint32_t x = __byte_perm(pk[j], __shfl_xor_sync(0xffffffffu, pk[j], 1), sel);
-          // the low half is this lane's token of row 2 j, the high half that of the next
-          const int row = w - lane + 2 * j;
-          uint16_t* p = reinterpret_cast<uint16_t*>(base_out) + (long long)2 * j * q.m;
-          if (lane < live && row < a.W) *p = (uint16_t)(x & 0xFFFFu);
-          if (lane < live && row + 1 < a.W) p[q.m] = (uint16_t)(x >> 16);
-        }
-      }
-      return;
-    }
-    out += (base + tok) * a.W + w;
-    if (a.W % 2 == 0) {
-      uint32_t pk[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) pk[j] = Half16<__nv_bfloat16>::pack(v[2 * j], v[2 * j + 1]);
-      rag_store_packed32(pk, reinterpret_cast<uint16_t*>(out), a.W, live, w, a.W, lane);
     } else if (w < a.W) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < live) out[(long long)j * a.W] = __float2bfloat16_rn(v[j]);
+      for (int j = 0; j < 16; ++j)
+        if (j < live) out[(long long)j * a.W] = (uint16_t)(pk[j >> 1] >> (16 * (j & 1)));
     }
     return;
   }
-  uint16_t* out = static_cast<uint16_t*>(a.out);
-  uint32_t pk[16], lo[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    float x = v[2 * j], y = v[2 * j + 1];
-    pk[j] = half_hi2(x, y);
-    lo[j] = Half16<__half>::pack(x, y);
+  // a lane's tokens lie side by side
+  if (q.m % 8 == 0 && live >= 16) {
+    uint4* to = reinterpret_cast<uint4*>(out + ((long long)D.e * a.W + w) * q.m + tok);
+    if (w < a.W) {
+      to[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+      to[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+    }
+    return;
   }
-  out += (base + tok) * a.ldo + w;
-  rag_store_packed32(pk, out, a.ldo, live, w, a.W, lane);
-  if (q.out_lo != 0) rag_store_packed32(lo, out + q.out_lo, a.ldo, live, w, a.W, lane);
+  // Rows that start anywhere, or end here: the warp's 32 x 16 values are turned, so that a
+  // store writes two rows' 16 tokens.  (From each lane's own row they went out as 32
+  // sectors for 64 bytes: 16 matrices of 1031 x 517 took 90 us here instead of 22.)
+#pragma unroll
+  for (int o = 8; o >= 2; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j & (o >> 1)) continue;
+      const int k = j | (o >> 1);
+      const uint32_t x = __shfl_xor_sync(0xffffffffu, up ? pk[j] : pk[k], o);
+      if (up) pk[j] = x; else pk[k] = x;
+    }
+  }
+  // now pk[j]: a pair of tokens of row 2 j + (lane & 17); the low half after the swap
+  // this lane's token of row 2 j + (lane & 16), the high half that of the next row
+  const int row0 = w - lane + (lane & 16), t = lane & 15;
+  uint16_t* to = out + ((long long)D.e * a.W + row0) * q.m + tok + t;
+  const uint32_t sel = (lane & 1) ? 0x3276u : 0x5410u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t x = __byte_perm(pk[j], __shfl_xor_sync(0xffffffffu, pk[j], 1), sel);
+    if (t < live && row0 + 2 * j < a.W) to[(long long)2 * j * q.m] = (uint16_t)(x & 0xFFFFu);
+    if (t < live && row0 + 2 * j + 1 < a.W) to[(long long)(2 * j + 1) * q.m] = (uint16_t)(x >> 16);
+  }
 }
 
-// The same with mat (as h, read by rag_epi_load) where `loads`: two neighbouring lanes
-// swap tokens first.  A lo part of mat may be the output's own: each word is read and
-// written by one lane.  Of a symmetric product's tiles beside the diagonal (tri) the
-// values are stored once more as rows from the columns: lanes swap back, and four of
-// them put 64 bytes of a row together.
-template <bool SYM>
-__device__ __forceinline__ void rag_dense_pairs32(const RagArgs& a, const RagTile& D,
-                                                  const uint32_t (&r)[32], const Words32& h,
-                                                  bool loads, int tok, int left, int w, int lane) {
+// The others: two neighbouring lanes swap tokens first.  A lo part of mat may be the
+// output's own: each word is read and written by one lane.  Of a symmetric product's
+// tiles beside the diagonal (tri) the values are stored once more as rows from the
+// columns: lanes swap back, and two of them put 32 bytes of a row together.
+template <bool SYM, bool LO, bool FULL>
+__device__ __forceinline__ void rag_dense_pairs16(const RagArgs& a, const RagTile& D,
+                                                  const uint32_t (&r)[16], const Words16& h,
+                                                  bool loads, int tok, int live, int w, int lane) {
   const RagDense& q = a.dense;
-  const int live = min(q.m - tok, left), odd = lane & 1, c0 = w - odd;
+  const int odd = lane & 1;
   const long long base = (long long)D.e * q.m;
-  uint16_t* out = static_cast<uint16_t*>(a.out) + (base + tok + odd) * a.ldo + c0;
-  uint32_t pk[16], lo[16];
+  uint16_t* out = static_cast<uint16_t*>(a.out) + (base + tok + odd) * a.ldo + w - odd;
+  uint32_t pk[8], lo[8];
+  const int diagonal = SYM ? w - tok : -1;       // this lane's token in its column
 #pragma unroll
-  for (int t = 0; t < 16; ++t) {
+  for (int t = 0; t < 8; ++t) {
     const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? r[2 * t] : r[2 * t + 1], 1);
     float x = q.c_acc * __uint_as_float(odd ? other : r[2 * t]);
     float y = q.c_acc * __uint_as_float(odd ? r[2 * t + 1] : other);
     if (loads) {
       const float2 mh = unpack16<__half>(h.a[t]), ml = unpack16<__half>(h.b[t]);
-      x += q.c_mat * (mh.x + ml.x);
-      y += q.c_mat * (mh.y + ml.y);
+      x += q.c_mat * (LO || !SYM ? mh.x + ml.x : mh.x);
+      y += q.c_mat * (LO || !SYM ? mh.y + ml.y : mh.y);
     }
-    const bool in = 2 * t + odd < live;
-    if (SYM) {
-      // rows behind the matrix (the next one's) are zero columns of the output
-      if (tok + 2 * t + odd == c0) x += q.c_diag;
-      if (tok + 2 * t + odd == c0 + 1) y += q.c_diag;
+    if (SYM && diagonal == 2 * t + odd) {
+      if (odd) y += q.c_diag; else x += q.c_diag;
+    }
+    const bool in = FULL || 2 * t + odd < live;
+    if (SYM && !FULL) {       // rows behind the matrix (the next one's) are zero columns
       x = in ? x : 0.0f;
       y = in ? y : 0.0f;
     }
     pk[t] = half_hi2(x, y);
-    lo[t] = Half16<__half>::pack(x, y);
-    if (in && w < a.W) {
-      *reinterpret_cast<uint32_t*>(out) = pk[t];
-      if (q.out_lo != 0) *reinterpret_cast<uint32_t*>(out + q.out_lo) = lo[t];
+    if (in && (FULL || w < a.W)) *reinterpret_cast<uint32_t*>(out) = pk[t];
+    if (LO) {
+      lo[t] = Half16<__half>::pack(x, y);
+      if (in && (FULL || w < a.W)) *reinterpret_cast<uint32_t*>(out + q.out_lo) = lo[t];
     }
     out += 2 * a.ldo;
   }
   if (!SYM || !q.tri || D.tok == D.w_tile) return;
 #pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    if (part == 1 && q.out_lo == 0) break;
+  for (int part = 0; part < (LO ? 2 : 1); ++part) {
     // tokens 2 t and 2 t + 1 of this lane's column w
-    uint32_t p[16];
+    uint32_t p[8];
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
+    for (int t = 0; t < 8; ++t) {
       const uint32_t v = part == 0 ? pk[t] : lo[t];
       p[t] = __byte_perm(v, __shfl_xor_sync(0xffffffffu, v, 1), odd ? 0x3276u : 0x5410u);
     }
-    // the four 16-byte pieces of four lanes' rows, transposed among the lanes
-    uint32_t x[8], y[8];
-    const bool b1 = lane & 2;
+    // the two 16-byte pieces of two lanes' rows: one piece of both rows each
+    uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t v = __shfl_xor_sync(0xffffffffu, b1 ? p[i] : p[8 + i], 2);
-      x[i] = b1 ? v : p[i];
-      y[i] = b1 ? p[8 + i] : v;
-    }
-    uint4 row[4];
-    uint32_t* rw = reinterpret_cast<uint32_t*>(row);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t u = __shfl_xor_sync(0xffffffffu, odd ? x[i] : x[4 + i], 1);
-      const uint32_t v = __shfl_xor_sync(0xffffffffu, odd ? y[i] : y[4 + i], 1);
-      rw[i] = odd ? u : x[i];
-      rw[4 + i] = odd ? x[4 + i] : u;
-      rw[8 + i] = odd ? v : y[i];
-      rw[12 + i] = odd ? y[4 + i] : v;
-    }
-    const int w0 = w & ~3;
-    uint16_t* to = static_cast<uint16_t*>(a.out) + (base + w0) * a.ldo + tok + 8 * (lane & 3) +
+    for (int i = 0; i < 4; ++i) u[i] = __shfl_xor_sync(0xffffffffu, odd ? p[i] : p[4 + i], 1);
+    const int w0 = w - odd;
+    uint16_t* to = static_cast<uint16_t*>(a.out) + (base + w0) * a.ldo + tok + 8 * odd +
                    (part == 0 ? 0 : q.out_lo);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (w0 + i < q.m) *reinterpret_cast<uint4*>(to + i * a.ldo) = row[i];
+    if (w0 < q.m)
+      *reinterpret_cast<uint4*>(to) = odd ? make_uint4(u[0], u[1], u[2], u[3])
+                                          : make_uint4(p[0], p[1], p[2], p[3]);
+    if (w0 + 1 < q.m)
+      *reinterpret_cast<uint4*>(to + a.ldo) = odd ? make_uint4(p[4], p[5], p[6], p[7])
+                                                  : make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
+
+// 16 tokens from row tok (of the matrix) of this lane's column w; left: the tile's
+// (the next tile's may be among the 16).
 template <bool SYM>
-__device__ __forceinline__ void rag_dense_store32(const RagArgs& a, const RagTile& D,
-                                                  const uint32_t (&r)[32], const Words32& h,
+__device__ __forceinline__ void rag_dense_store16(const RagArgs& a, const RagTile& D,
+                                                  const uint32_t (&r)[16], const Words16& h,
                                                   bool loads, int tok, int left, int w, int lane) {
-  if (SYM)
-    rag_dense_pairs32<true>(a, D, r, h, loads, tok, left, w, lane);
-  else if (loads)
-    rag_dense_pairs32<false>(a, D, r, h, true, tok, left, w, lane);
+  const int live = min(a.dense.m - tok, left);
+  const bool full = live >= 16 && w - lane + 32 <= a.W;
+  if (!SYM && a.dense.final_out != nullptr)
+    rag_dense_final16(a, D, r, tok, live, w, lane);
+  else if (full && a.dense.out_lo == 0)
+    rag_dense_pairs16<SYM, false, true>(a, D, r, h, loads, tok, 16, w, lane);
+  else if (full)
+    rag_dense_pairs16<SYM, true, true>(a, D, r, h, loads, tok, 16, w, lane);
+  else if (a.dense.out_lo == 0)
+    rag_dense_pairs16<SYM, false, false>(a, D, r, h, loads, tok, live, w, lane);
   else
-    rag_dense_tokens32(a, D, r, tok, left, w, lane);
+    rag_dense_pairs16<SYM, true, false>(a, D, r, h, loads, tok, live, w, lane);
 }
 
 // ------------------------------------------------------------- joining slices
