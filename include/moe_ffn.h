@@ -587,7 +587,7 @@ moe_status moe_clip_grad_norm(int n, const void* const* grads, void* const* outs
  *   X = g / (|g|_F + eps);  for each step's a, b, c:
  *     A = X X^T,  X = (a I + b A + c A^2) X;    out = scale X,
  * which takes every singular value of g towards 1 and keeps its vectors.
- *  - g [E, N, K] of type g_dtype (moe_dtype), dense, any N and K from 1 to 2^20 and
+ *  - g [E, N, K] of type g_dtype (moe_dtype), dense, any N and K from 1 to 2^18 and
  *    any alignment of the element; out [E, N, K] bf16, dense, 16-byte aligned; may
  *    be g itself.  Each matrix by itself, whichever side is the longer.
  *  - coefficients: host array of 3 * steps floats, read during the call; steps 1 to

@@ -211,9 +211,13 @@ moe_status ragged_args(const moe_ragged* p, const void* a, const void* b, const 
   return MOE_OK;
 }
 
-// Tiles within the kernels' 32-bit numbers, rows within a tensor map's.
+// Tiles within the kernels' 32-bit numbers, rows within a tensor map's.  Sides: the
+// tensor core truncates as it adds, half a step of 2^-24 of a sum of squares every 16
+// values on average; 2^18 values lose 0.05%, 2^20 took a row's result 0.27% off.
+constexpr int kMaxOrthogonalizeSide = 1 << 18;
 bool valid_orthogonalize(int E, int N, int K) {
-  if (E < 1 || E > MOE_MAX_EXPERTS || N < 1 || N > kMaxDim || K < 1 || K > kMaxDim) return false;
+  if (E < 1 || E > MOE_MAX_EXPERTS || N < 1 || K < 1 || std::max(N, K) > kMaxOrthogonalizeSide)
+    return false;
   const int64_t m = std::min(N, K), t = (std::max(N, K) + 127) / 128, u = (m + 31) / 32;
   return E * t * u < (1ll << 28) && E * m < (1ll << 30);
 }

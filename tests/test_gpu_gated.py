@@ -221,6 +221,14 @@ def test_many_experts():
     run_grad(counts, 40, 72, "bfloat16")
 
 
+@pytest.mark.parametrize("counts, inter, hidden", [
+    ([0] * 1000 + [1] + [0] * 23, 8, 8), ([1] * 1024, 16, 24), ([3000, 0, 2000], 8, 24),
+    ([5], 2056, 8), ([2], 8, 8200)])
+def test_extreme_shapes(counts, inter, hidden, form):
+    run_forward(counts, inter, hidden, "bfloat16", "clamped", bias=True)
+    run_grad(counts, inter, hidden, "bfloat16", "clamped")
+
+
 def test_the_limit_itself_passes_gradients(form):
     """h of exactly the limit, just beyond it, and of large values of both signs."""
     v = torch.tensor([2.0, -2.0, 2.015625, -2.015625, 0.0, 100.0, -100.0, 1.0], device="cuda")

@@ -148,20 +148,47 @@ def test_many_matrices(shape, form):
     check(call(g), g)
 
 
-def test_each_matrix_by_itself(form):
+@pytest.mark.parametrize("size", [(270, 300), (20, 90), (90, 20), (3, 7), (1, 5)])
+def test_each_matrix_by_itself(size, form):
     """A matrix of another scale, a zero one and one of NaN beside the others."""
-    g = gradient((5, 270, 300), "float32", 8)
+    g = gradient((5, *size), "float32", 8)
     alone = [call(g[i:i + 1].contiguous())[0] for i in range(5)]
     g2 = g.clone()
     g2[1] *= 1e6
     g2[2] = 0
-    g2[3, 7, 9] = float("nan")
+    g2[3, size[0] // 2, size[1] // 2] = float("nan")
     out = call(g2)
     assert torch.equal(out[0], call(g)[0]) and torch.equal(out[4], call(g)[4])
     check(out[:2], g2[:2])
     assert bool((out[2] == 0).all()) and bool(out[3].isnan().all())
     for i in (0, 4):
         check(alone[i][None], g[i:i + 1])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("size", [(300, 140), (12, 40)])
+def test_infinities_stay_in_their_matrix(size, bad):
+    g = gradient((3, *size), "bfloat16", 5)
+    want = call(g)
+    g[1, -1, 0] = bad
+    out = call(g)
+    assert torch.equal(out[0], want[0]) and torch.equal(out[2], want[2])
+    assert bool(out[1].isnan().all())
+
+
+@pytest.mark.parametrize("shape", [(1024, 1, 1), (1024, 9, 5), (300, 40, 24), (1, 1, 1 << 18),
+                                   (1, 1 << 18, 1), (2, 3, 100003), (1, 60001, 70), (1, 130, 30011)],
+                         ids=str)
+def test_extreme_shapes(shape):
+    g = gradient(shape, "bfloat16", 13)
+    out = call(g)
+    some = sorted({0, shape[0] // 2, shape[0] - 1})
+    for e in some:
+        G, y = f64(g[e]), f64(out[e])
+        ref = ragged.orthogonalize(G)
+        err = np.sqrt(np.mean((y - ref) ** 2) / np.mean(ref ** 2))
+        assert err <= 0.0025, (e, err)             # what the library states
+    assert bool(out.isfinite().all())
 
 
 def test_options():

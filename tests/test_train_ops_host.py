@@ -72,8 +72,8 @@ def test_workspaces_and_empty_problems():
     assert grad(dy=None, w=None, h=None, dh=None, z=None, **none) == OK
 
 
-@pytest.mark.parametrize("bad", [dict(E=0), dict(E=1025), dict(N=0), dict(K=0), dict(K=(1 << 20) + 1),
-                                 dict(N=1 << 20, K=1 << 20), dict(dtype=3), dict(dtype=-1),
+@pytest.mark.parametrize("bad", [dict(E=0), dict(E=1025), dict(N=0), dict(K=0), dict(K=(1 << 18) + 1), dict(N=(1 << 18) + 1),
+                                 dict(E=1024, N=1 << 18, K=1 << 18), dict(dtype=3), dict(dtype=-1),
                                  dict(steps=0), dict(steps=65), dict(c=None), dict(c=(1.0, NAN, 0.0)),
                                  dict(c=(INF, 0.0, 0.0)), dict(eps=0.0), dict(eps=-1.0),
                                  dict(eps=NAN), dict(eps=INF), dict(scale=NAN), dict(scale=INF),
