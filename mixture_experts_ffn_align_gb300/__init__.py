@@ -756,7 +756,8 @@ BF16_GEMM_FORMS = {"auto": 0, "single": 1, "pairs": 2, "pairs_double": 3}
 
 def moe_debug_set_bf16_gemm_form(form: str = "auto"):
     """Force the single-SM or the SM-pair GEMMs (tests), or restore the
-    size-based choice; "pairs_double": ragged forward and dgrad on double tiles."""
+    size-based choice; "pairs_double": ragged forward and dgrad on double tiles, the
+    orthogonalised update in one launch of clusters."""
     lib().moe_debug_set_bf16_gemm_form(BF16_GEMM_FORMS[form])
 
 

@@ -109,7 +109,7 @@ __device__ __forceinline__ void rag_gated_tokens32(const RagArgs& a, uint32_t (&
       const int j = 2 * i + k;
       const uint32_t other = __shfl_xor_sync(0xffffffffu, up ? r[2 * j] : r[2 * j + 1], 8);
       z[k] = gated_value<CLAMP>(q, __uint_as_float(up ? other : r[2 * j]),
-                         __uint_as_float(up ? r[2 * j + 1] : other));
+                                __uint_as_float(up ? r[2 * j + 1] : other));
     }
     pk[i] = Half16<T>::pack(z[0], z[1]);     // tokens 4 i + up and 4 i + up + 2
   }

@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
       // what the epilogue reads beside the sums, while they are computed
       [[maybe_unused]] Words32 h_next;
       [[maybe_unused]] Words16 mat_next;
-      [[maybe_unused]] const bool loads = splits == 1 && (EPI == EPI_GATED_GRAD || args.dense.mat != nullptr);
+      [[maybe_unused]] const bool loads =
+          splits == 1 && (EPI == EPI_GATED_GRAD || args.dense.mat != nullptr);
       [[maybe_unused]] const int part = (warp - 2) >> 2;
       if constexpr (EPI == EPI_GATED_GRAD) {
         if (loads && 32 * part < D.rows)
