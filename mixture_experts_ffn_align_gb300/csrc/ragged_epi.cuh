@@ -82,27 +82,37 @@ inline void gated_args(const GatedProblem& g, RagGated& a) {
 // gated_col(w) of the gate (up = 0) or up half.
 __device__ __forceinline__ int gated_col(int w) { return ((w >> 4) << 3) + (w & 7); }
 
-// 32 tokens from row row0 of this lane's interleaved column w.
+// All fused epilogues take sixteen tokens at a time: with 32, twice the unrolled code and
+// registers, the gated product and its gradient took 1 to 8% longer (512 rows, 16
+// experts, 776 -> 520: 9.5 us instead of 8.7), the steps of the update's short products a
+// sixth (16 x 517 x 1031: 58 us instead of 50).
+//
+// 16 tokens from row row0 of this lane's interleaved column w.
 template <typename T, bool CLAMP>
-__device__ __forceinline__ void rag_gated_tokens32(const RagArgs& a, uint32_t (&r)[32], float bias,
+__device__ __forceinline__ void rag_gated_tokens16(const RagArgs& a, uint32_t (&r)[16], float bias,
                                                    long long row0, int live, int w, int lane) {
   const RagGated& q = a.gated;
-  const int up = (w >> 3) & 1, col = gated_col(w);
+  const int up = (w >> 3) & 1, col = gated_col(w), odd = lane & 1;
   const bool inside = w < a.W;
+  const uint32_t sel = odd ? 0x3276u : 0x5410u;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + bias);
-  if (q.h_out != nullptr) {
-    uint32_t pk[16];
+  for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + bias);
+  if (q.h_out != nullptr) {      // neighbouring columns swap: 4-byte pieces of two tokens
+    uint16_t* p = static_cast<uint16_t*>(q.h_out) + (row0 + odd) * q.ldh_out + up * q.inter + col - odd;
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      pk[j] = Half16<T>::pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-    rag_store_packed32(pk, static_cast<uint16_t*>(q.h_out) + row0 * q.ldh_out + up * q.inter + col,
-                       q.ldh_out, live, w, a.W, lane);
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t pk = Half16<T>::pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+      const uint32_t v = __byte_perm(pk, __shfl_xor_sync(0xffffffffu, pk, 1), sel);
+      if (inside && 2 * j + odd < live) *reinterpret_cast<uint32_t*>(p) = v;
+      p += 2 * q.ldh_out;
+    }
   }
-  // the gate's lane takes the even tokens, the up half's the odd ones
-  uint32_t pk[8];
+  // the gate's lane takes the even tokens, the up half's the odd ones; then of
+  // neighbouring columns an even lane both columns of the first token
+  const int tok0 = up + 2 * odd;
+  uint16_t* p = static_cast<uint16_t*>(q.z) + (row0 + tok0) * q.ldz + (col - odd);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     float z[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -111,30 +121,21 @@ __device__ __forceinline__ void rag_gated_tokens32(const RagArgs& a, uint32_t (&
       z[k] = gated_value<CLAMP>(q, __uint_as_float(up ? other : r[2 * j]),
                                 __uint_as_float(up ? r[2 * j + 1] : other));
     }
-    pk[i] = Half16<T>::pack(z[0], z[1]);     // tokens 4 i + up and 4 i + up + 2
-  }
-  // neighbouring columns: an even lane both columns of the first token
-  const int odd = lane & 1, tok0 = up + 2 * odd;
-  uint16_t* p = static_cast<uint16_t*>(q.z) + (row0 + tok0) * q.ldz + (col - odd);
-  const uint32_t sel = odd ? 0x3276u : 0x5410u;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, pk[i], 1);
-    const uint32_t v = __byte_perm(pk[i], other, sel);
+    const uint32_t pk = Half16<T>::pack(z[0], z[1]);     // tokens 4 i + up and 4 i + up + 2
+    const uint32_t v = __byte_perm(pk, __shfl_xor_sync(0xffffffffu, pk, 1), sel);
     if (inside && tok0 + 4 * i < live) *reinterpret_cast<uint32_t*>(p) = v;
     p += 4 * q.ldz;
   }
 }
 
-// What a lane's two columns of 32 tokens need from memory beside the sums: the words
-// of every other token from two places.  Read a chunk ahead (the first before the sums
-// are complete): read where they are used, they kept the gradient of 8 x (2048,
-// 1024), 256 rows each, at 28 us instead of 20.
-struct Words32 {
-  uint32_t a[16], b[16];
+// Two words at a lane's two columns of every other of 16 tokens, read a chunk ahead (the
+// first before the sums are complete): read where they are used, they kept the gradient
+// of 8 x (2048, 1024), 256 rows each, at 28 us instead of 20.
+struct Words16 {
+  uint32_t a[8], b[8];
 };
-// c: tokens of the tile before the 32.
-__device__ __forceinline__ void rag_gated_load(const RagArgs& a, const RagTile& D, Words32& x, int c,
+// h for the gradient.  c: tokens of the tile before the 16.
+__device__ __forceinline__ void rag_gated_load(const RagArgs& a, const RagTile& D, Words16& x, int c,
                                                int w, int lane) {
   const RagGated& q = a.gated;
   const int odd = lane & 1, live = D.rows - c;
@@ -142,7 +143,7 @@ __device__ __forceinline__ void rag_gated_load(const RagArgs& a, const RagTile& 
   const uint16_t* h = static_cast<const uint16_t*>(q.h) + (long long)(D.row0 + c + odd) * q.ldh +
                       (w - odd);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < 8; ++j) {
     const bool in = inside && 2 * j + odd < live;
     x.a[j] = in ? *reinterpret_cast<const uint32_t*>(h) : 0u;
     x.b[j] = in ? *reinterpret_cast<const uint32_t*>(h + q.inter) : 0u;
@@ -150,10 +151,10 @@ __device__ __forceinline__ void rag_gated_load(const RagArgs& a, const RagTile& 
   }
 }
 
-// 32 tokens from row row0 of this lane's column w of dz.
+// 16 tokens from row row0 of this lane's column w of dz.
 template <typename T, bool CLAMP>
-__device__ __forceinline__ void rag_gated_grad_tokens32(const RagArgs& a, const uint32_t (&r)[32],
-                                                        const Words32& h, long long row0, int live,
+__device__ __forceinline__ void rag_gated_grad_tokens16(const RagArgs& a, const uint32_t (&r)[16],
+                                                        const Words16& h, long long row0, int live,
                                                         int w, int lane) {
   const RagGated& q = a.gated;
   const int odd = lane & 1, c0 = w - odd;
@@ -161,7 +162,7 @@ __device__ __forceinline__ void rag_gated_grad_tokens32(const RagArgs& a, const 
   uint16_t* dh = static_cast<uint16_t*>(q.h_out) + (row0 + odd) * q.ldh_out + c0;
   uint16_t* z = static_cast<uint16_t*>(q.z) + (row0 + odd) * q.ldz + c0;
 #pragma unroll
-  for (int t = 0; t < 16; ++t) {
+  for (int t = 0; t < 8; ++t) {
     const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? r[2 * t] : r[2 * t + 1], 1);
     const float dz0 = __uint_as_float(odd ? other : r[2 * t]);
     const float dz1 = __uint_as_float(odd ? r[2 * t + 1] : other);
@@ -216,13 +217,7 @@ __device__ __forceinline__ uint32_t half_hi2(float& x, float& y) {
   return p;
 }
 
-// Sixteen tokens at a time: with 32, twice the unrolled code and registers, the steps of
-// short products took a sixth longer (16 x 517 x 1031: 58 us).
-//
-// mat and its lo part at two columns of 16 tokens, read a chunk ahead.
-struct Words16 {
-  uint32_t a[8], b[8];
-};
+// mat and its lo part at two columns of 16 tokens.
 template <bool FULL, bool LO>
 __device__ __forceinline__ void rag_load_mat(Words16& x, const uint16_t* mat, long long lo,
                                              long long ld, int live, int odd) {

@@ -52,7 +52,7 @@ constexpr int BK = 64, MAX_STAGES = 9;
 constexpr int A_BYTES = 128 * BK * 2;
 constexpr int RING_BYTES = 196608, BAR_BYTES = 384;
 // Epilogue warps: one for each quadrant of the accumulator's rows, wgrad two (of
-// 128 columns each), the gated ones two (of every other 32 tokens), the dense four: a
+// 128 columns each), the gated ones two (of every other 16 tokens), the dense four: a
 // short product's epilogue is as long as its reduction (16 x 517 x 1031, a step of three
 // products 53.7 us with two, 49.8 with four; on pairs, where products are long, two
 // are better, 5.07 against 5.24 ms for 2 x 4096 x 14336).
@@ -365,17 +365,18 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
       }
       const int acc = local & 1;
       // what the epilogue reads beside the sums, while they are computed
-      [[maybe_unused]] Words32 h_next;
-      [[maybe_unused]] Words16 mat_next;
+      [[maybe_unused]] Words16 next;
       [[maybe_unused]] const bool loads =
-          splits == 1 && (EPI == EPI_GATED_GRAD || args.dense.mat != nullptr);
+          splits == 1 && (EPI == EPI_GATED_GRAD || (EPI == EPI_DENSE && args.dense.mat != nullptr));
       [[maybe_unused]] const int part = (warp - 2) >> 2;
-      if constexpr (EPI == EPI_GATED_GRAD) {
-        if (loads && 32 * part < D.rows)
-          rag_gated_load(args, D, h_next, 32 * part, D.w_tile * 128 + q * 32 + lane, lane);
-      } else if constexpr (EPI == EPI_DENSE) {
-        if (loads && 16 * part < D.rows)
-          rag_dense_load(args, D, mat_next, 16 * part, D.w_tile * 128 + q * 32 + lane, lane);
+      if constexpr (EPI == EPI_GATED_GRAD || EPI == EPI_DENSE) {
+        const int w = D.w_tile * 128 + q * 32 + lane;
+        if (loads && 16 * part < D.rows) {
+          if constexpr (EPI == EPI_DENSE)
+            rag_dense_load(args, D, next, 16 * part, w, lane);
+          else
+            rag_gated_load(args, D, next, 16 * part, w, lane);
+        }
       }
       int ok = 0;
       if (lane == 0) ok = wait(tfull_bar(acc), (local >> 1) & 1);
@@ -409,26 +410,6 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
                                           taddr + half * 128, V.e,
                                           V.n_tile * 128 + q * 32, V.k_tile * 256 + half * 128,
                                           lane, release);
-      } else if constexpr (EPI == EPI_DENSE) {
-        const int w = D.w_tile * 128 + q * 32 + lane;
-        constexpr int STEP = 4 * epi_warps(OP, EPI);
-#pragma unroll 1
-        for (int c = 16 * part; c < D.rows; c += STEP) {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(taddr + c, r);
-          const Words16 h = mat_next;
-          tmem_ld_wait();
-          if (splits > 1) {
-            rag_store_part(args, r, t, rank, c, D.rows, q * 32 + lane);
-            continue;
-          }
-          if (loads && c + STEP < D.rows) rag_dense_load(args, D, mat_next, c + STEP, w, lane);
-          // the symmetric products are the forward ones
-          rag_dense_store16<OP == RAG_FWD>(args, D, r, h, loads, D.tok * args.dense.per + c,
-                                           D.rows - c, w, lane);
-          __syncwarp();
-        }
-        release();
       } else if constexpr (EPI != EPI_PLAIN) {
         const int w = D.w_tile * 128 + q * 32 + lane;
         float bias = 0.0f;
@@ -437,30 +418,34 @@ __global__ void __launch_bounds__(num_threads(OP, EPI), 1)
               static_cast<const uint16_t*>(args.bias)[(size_t)D.e * args.W +
                                                       ((w >> 3) & 1) * args.gated.inter +
                                                       gated_col(w)]);
+        constexpr int STEP = 4 * epi_warps(OP, EPI);
 #pragma unroll 1
-        for (int c = 32 * part; c < D.rows; c += 64) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(taddr + c, r);
+        for (int c = 16 * part; c < D.rows; c += STEP) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(taddr + c, r);
+          [[maybe_unused]] Words16 h;
+          if constexpr (EPI != EPI_GATED) h = next;
+          tmem_ld_wait();
+          if (splits > 1) {
+            rag_store_part(args, r, t, rank, c, D.rows, q * 32 + lane);
+            continue;
+          }
           if constexpr (EPI == EPI_GATED) {
-            tmem_ld_wait();
-            if (splits > 1)
-              rag_store_part(args, r, t, rank, c, D.rows, q * 32 + lane);
-            else if (clamp)
-              rag_gated_tokens32<T, true>(args, r, bias, D.row0 + c, D.rows - c, w, lane);
-            else
-              rag_gated_tokens32<T, false>(args, r, bias, D.row0 + c, D.rows - c, w, lane);
-          } else {
-            const Words32 h = h_next;
-            tmem_ld_wait();
-            if (splits > 1) {
-              rag_store_part(args, r, t, rank, c, D.rows, q * 32 + lane);
-              continue;
-            }
-            if (c + 64 < D.rows) rag_gated_load(args, D, h_next, c + 64, w, lane);
             if (clamp)
-              rag_gated_grad_tokens32<T, true>(args, r, h, D.row0 + c, D.rows - c, w, lane);
+              rag_gated_tokens16<T, true>(args, r, bias, D.row0 + c, D.rows - c, w, lane);
             else
-              rag_gated_grad_tokens32<T, false>(args, r, h, D.row0 + c, D.rows - c, w, lane);
+              rag_gated_tokens16<T, false>(args, r, bias, D.row0 + c, D.rows - c, w, lane);
+          } else if constexpr (EPI == EPI_GATED_GRAD) {
+            if (c + STEP < D.rows) rag_gated_load(args, D, next, c + STEP, w, lane);
+            if (clamp)
+              rag_gated_grad_tokens16<T, true>(args, r, h, D.row0 + c, D.rows - c, w, lane);
+            else
+              rag_gated_grad_tokens16<T, false>(args, r, h, D.row0 + c, D.rows - c, w, lane);
+          } else {
+            if (loads && c + STEP < D.rows) rag_dense_load(args, D, next, c + STEP, w, lane);
+            // the symmetric products are the forward ones
+            rag_dense_store16<OP == RAG_FWD>(args, D, r, h, loads, D.tok * args.dense.per + c,
+                                             D.rows - c, w, lane);
           }
           __syncwarp();
         }
