@@ -3,11 +3,12 @@
 // products A = X X^T, B = a I + b A + c A^2, X = B X of every step, with a cluster
 // barrier between them.
 //
-// Small products are bound by latency: as launches of their own they take 4.5 us
+// Small products are bound by latency: as launches of their own they take 4.7 us
 // each (a launch's end and start, cold instructions, the first copies), 15 of them
-// for five steps.  Here the barrier, the first copies and the last tile's epilogue
-// remain.  Matrices and sums stay in L2.  Products of many tiles are better off with
-// all SMs: ortho_cluster_plan compares both by modelled cycles.
+// for five steps; here 3.1 us, for the barrier, the first copies and the last tile's
+// epilogue (8 x 64 x 64 in five steps: 76 and 54 us).  Matrices and sums stay in L2.
+// Products of many tiles are better off with all SMs: orthogonalize.cu compares both by
+// modelled cycles.
 //
 // Roles, tiles, epilogue and slices of a reduction are those of ragged_one.cuh's
 // EPI_DENSE (128 columns x up to 256 rows, fp32 sums in tensor memory, slices joined
@@ -32,6 +33,11 @@ constexpr int A_BYTES = 128 * BK * 2, RING_BYTES = 196608, BAR_BYTES = 256;
 constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 512;
 constexpr int SMEM_BYTES = RING_BYTES + 1024 + BAR_BYTES;
+
+// Orders this thread's generic accesses to global memory with the asynchronous ones.
+__device__ __forceinline__ void fence_proxy_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
 
 struct Maps {
   CUtensorMap x_nt[2], x_mn[2], x_rows[2], a_nt, a_rows, b_rows;
@@ -172,14 +178,21 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
   bool ok = true, skip_first = args.never_arrive != 0;
 
+  RagArgs a;
+  Phase f = phase_of(maps, args, 0, a);
+  Item first = item_of(f, args, e, rank);
   for (int p = 0; p < 3 * args.steps; ++p) {
-    RagArgs a;
-    const Phase f = phase_of(maps, args, p, a);
+    // Arguments and the first item: the producer and the MMA issuer have them before
+    // the barrier opens, the epilogue's warps find them while the sums are computed.
+    if (warp >= 2 && p > 0) {
+      f = phase_of(maps, args, p, a);
+      first = item_of(f, args, e, rank);
+    }
     const int items = f.tiles * f.splits;
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       for (int i = rank; ok && i < items; i += ctas) {
-        const Item it = item_of(f, args, e, i);
+        const Item it = i == rank ? first : item_of(f, args, e, i);
         const int boxes = (it.tile.rows + 31) / 32;
         int seg = it.kb0 >= 2 * f.seg_kb ? 2 : it.kb0 >= f.seg_kb ? 1 : 0;
         int seg_k = it.kb0 - seg * f.seg_kb;
@@ -222,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // ---------------------------------------------------------- MMA issuer
       const uint32_t major = f.nt ? 0u : kIdescAMn, a_step = f.nt ? 2 : 128;
       for (int i = rank; ok && i < items; i += ctas) {
-        const Item it = item_of(f, args, e, i);
+        const Item it = i == rank ? first : item_of(f, args, e, i);
         const int n = (it.tile.rows + 15) / 16 * 16;
         const uint32_t idesc = make_idesc(Half16<__half>::kFmt, Half16<__half>::kFmt, 128, n) | major;
         const int acc = local & 1;
@@ -262,7 +275,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int part = (warp - 2) >> 2;
       constexpr int STEP = 4 * EPI_WARPS;
       for (int i = rank; ok && i < items; i += ctas) {
-        const Item it = item_of(f, args, e, i);
+        const Item it = i == rank ? first : item_of(f, args, e, i);
         const int acc = local & 1, w = it.tile.w_tile * 128 + q * 32 + lane;
         Words16 mat_next;
         if (loads && 16 * part < it.tile.rows)
@@ -295,9 +308,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         ++local;
       }
     }
-    fence_proxy_async_all();
-    cluster_sync();
     if (f.splits > 1) {
+      cluster_sync();
       if (*abort_flag == 0) {
         for (int t = 0; t < f.tiles; ++t) {
           const RagTile D = item_of(f, args, e, t * f.splits).tile;
@@ -305,10 +317,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                                             lane);
         }
       }
-      fence_proxy_async_all();
-      cluster_sync();
     }
-    fence_proxy_async_all();
+    if (f.splits > 1 || warp >= 2) fence_proxy_async_global();
+    if (warp < 2 && p + 1 < 3 * args.steps) {
+      f = phase_of(maps, args, p + 1, a);
+      first = item_of(f, args, e, rank);
+    }
+    cluster_sync();
+    if (warp == 0) fence_proxy_async_global();
   }
 
   // copies and MMAs still in flight after a wait that ran out

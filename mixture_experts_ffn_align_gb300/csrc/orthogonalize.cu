@@ -401,8 +401,8 @@ Layout layout(int E, int N, int K) {
 // models leave out what both take alike; against each other, a product of its own takes
 // some 3500 cycles more (its launch), and the clusters' cycles count 6/5: they read and
 // add a X where it is used, and a matrix has eight SMs at most.  Measured in clusters /
-// as products, us a step: 8 x 64 x 64 12.3 / 15.4, 8 x 256 x 512 17.4 / 19.9, 64 x 128
-// x 1024 34.5 / 40.2; 8 x 257 x 512 24.7 / 21.9, 8 x 256 x 2048 37.3 / 29.9.
+// as products, us a step: 8 x 64 x 64 9.3 / 14.3, 8 x 256 x 512 14.4 / 16.9, 64 x 128 x
+// 1024 33.9 / 38.6; 8 x 257 x 512 20.0 / 18.7, 8 x 256 x 2048 32.7 / 25.5.
 bool in_clusters(const Layout& l, int E) {
   if (ragged_form() != 0) return ragged_form() == 3;
   const float c[3] = {};
