@@ -15,7 +15,7 @@ import ctypes
 import os
 from array import array
 from dataclasses import dataclass
-from functools import cache, cached_property
+from functools import cache, cached_property, lru_cache
 from types import SimpleNamespace
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -682,10 +682,12 @@ def moe_orthogonalize_workspace_bytes(E: int, N: int, K: int) -> int:
     return int(lib().moe_orthogonalize_workspace_bytes(int(E), int(N), int(K)))
 
 
-@cache
+@lru_cache(64)
 def _coefficients(steps, coefficients):
     """The steps' coefficients as an array: three numbers for all, or three a step."""
     flat = array("f")
+    if not coefficients:
+        raise ValueError("coefficients must not be empty")
     for c in coefficients if isinstance(coefficients[0], tuple) else (coefficients,) * steps:
         flat.extend(c)
     if len(flat) != 3 * steps:
@@ -705,7 +707,7 @@ def moe_orthogonalize(g, out, workspace, steps=5, coefficients=(3.4445, -4.7750,
     E, N, K = shape if len(shape) == 3 else (1, *shape)
     dev = g.get_device()
     ws, n = _bytes("workspace", workspace, dev)
-    if type(coefficients) is not tuple or type(coefficients[0]) is list:
+    if type(coefficients) is not tuple or list in map(type, coefficients):
         coefficients = tuple(tuple(c) if hasattr(c, "__len__") else c for c in coefficients)
     c = _coefficients(steps, coefficients)
     _check(lib().moe_orthogonalize(

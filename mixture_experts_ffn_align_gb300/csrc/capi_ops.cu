@@ -302,7 +302,8 @@ moe_status ragged_gated_dgrad(const moe_ragged* p, const void* dy, const void* w
   if (ldh == 0 || lddh == 0) return MOE_ERR_INVALID_ARG;
   const moe_status s = ragged_args(p, dy, w2, expert_offsets, dh, workspace, workspace_bytes);
   if (s != MOE_OK || p->R == 0) return s;
-  if (!h || misaligned(h, 16) || misaligned(z, 16)) return MOE_ERR_INVALID_ARG;
+  if (!h || misaligned(h, 16) || misaligned(z, 16) || (h == dh && ldh != lddh))
+    return MOE_ERR_INVALID_ARG;
   GatedProblem g{};
   g.grad = true;
   g.inter = p->K;

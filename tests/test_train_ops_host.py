@@ -30,7 +30,8 @@ def gated(x=PTR, w=PTR, bias=None, offsets=PTR, alpha=1.0, beta=0.0, limit=0.0, 
                                   size, None)
 
 
-def grad(dy=PTR, w=PTR, h=PTR, ldh=0, offsets=PTR, alpha=1.0, beta=0.0, limit=0.0, dh=PTR, lddh=0,
+def grad(dy=PTR, w=PTR, h=PTR, ldh=0, offsets=PTR, alpha=1.0, beta=0.0, limit=0.0,
+         dh=ctypes.c_void_p(8192), lddh=0,
          z=PTR, ws=PTR, size=BIG, **kw):
     p = moe.Ragged(**{**dict(R=16, N=128, K=128, E=4), **kw})
     return moe.lib().ragged_gated_dgrad(p._ref, dy, w, h, ldh, offsets, alpha, beta, limit, dh, lddh,
@@ -59,7 +60,8 @@ def test_gated_refusals(bad):
                                  dict(beta=INF), dict(limit=NAN), dict(ldh=248), dict(ldh=260),
                                  dict(lddh=128), dict(lddh=-256), dict(dy=None), dict(w=None),
                                  dict(h=None), dict(dh=None), dict(ws=None), dict(offsets=None),
-                                 dict(dy=ODD), dict(h=ODD), dict(dh=ODD), dict(z=ODD)], ids=str)
+                                 dict(dy=ODD), dict(h=ODD), dict(dh=ODD), dict(z=ODD),
+                                 dict(dh=PTR, lddh=264)], ids=str)
 def test_gated_grad_refusals(bad):
     assert grad(**bad) == INVALID
 
@@ -100,7 +102,7 @@ def test_coefficient_forms():
     one = moe._coefficients(2, (1.0, 2.0, 3.0))
     assert list(one) == [1.0, 2.0, 3.0] * 2
     assert list(moe._coefficients(2, ((1.0, 2.0, 3.0), (4.0, 5.0, 6.0)))) == [1, 2, 3, 4, 5, 6]
-    for bad in (((1.0, 2.0, 3.0),) * 3, (1.0, 2.0), ((1.0, 2.0),) * 2):
+    for bad in (((1.0, 2.0, 3.0),) * 3, (1.0, 2.0), ((1.0, 2.0),) * 2, ()):
         with pytest.raises(ValueError):
             moe._coefficients(2, bad)
 
