@@ -438,8 +438,9 @@ cudaError_t prepare(const Layout& l, int E, bool transposed, const void* g, floa
                     (transposed ? l.m : l.M) % (TYPE == 2 ? 4 : 8) == 0;
   if (transposed) {
     cfg.gridDim = dim3((l.Mp / 64 + kTiles - 1) / kTiles, (l.m + 63) / 64, E);
-    return cudaLaunchKernelEx(&cfg, lo != 0 ? k_ortho_transpose<TYPE, true> : k_ortho_transpose<TYPE, false>, g, l.m, l.M, l.Mp, ld, lo, wide,
-                              l.chunks, sums, eps, x);
+    return cudaLaunchKernelEx(
+        &cfg, lo != 0 ? k_ortho_transpose<TYPE, true> : k_ortho_transpose<TYPE, false>, g, l.m, l.M,
+        l.Mp, ld, lo, wide, l.chunks, sums, eps, x);
   }
   int log_tx = 3;
   while (log_tx < 8 && 8 << log_tx < l.Mp) ++log_tx;
