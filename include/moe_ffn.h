@@ -644,7 +644,8 @@ void moe_debug_set_watchdog(int64_t limit_ns, int never_arrive);
  * same modes; by default a model of the forms' times chooses by sizes.  mode 3:
  * their pair form, forward and dgrad on tiles of 512 weights (the other GEMMs:
  * as mode 0).  moe_orthogonalize: 1 and 2 its products as launches of their own on
- * one SM or on pairs, 3 all steps in one launch of clusters.
+ * one SM or on pairs, 3 all steps in one launch of clusters, 4 in one launch over
+ * the whole grid (all others: as mode 0).
  * Not thread-safe; affects later launches.  No counterpart on the pages: it
  * only lets tests reach both forms at any size. */
 void moe_debug_set_bf16_gemm_form(int mode);

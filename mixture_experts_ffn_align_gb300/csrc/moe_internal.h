@@ -251,6 +251,8 @@ cudaError_t launch_ragged_gated_2sm(const RaggedProblem& p, const GatedProblem& 
 // 0: by size, 1: one SM, 2: SM pairs, 3: SM pairs on double tiles
 // (moe_debug_set_bf16_gemm_form).
 int ragged_form();
+// The same for the orthogonalised update; 4: one launch over the whole grid.
+int ortho_form();
 // 4-bit product: x codes / scales [R, K/2] / [R, K/32], weights [E, N, K/2] with
 // packed scales; token scales are first rewritten to workspace.
 size_t ragged_mxfp4_bytes(int R, int N, int K, int E);

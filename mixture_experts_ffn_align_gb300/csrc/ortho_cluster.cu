@@ -1,20 +1,31 @@
-// All steps of the orthogonalised update of small matrices (orthogonalize.cu has the
-// formulas) in one launch: a cluster of 1 to 8 CTAs takes a matrix and goes through the
-// products A = X X^T, B = a I + b A + c A^2, X = B X of every step, with a cluster
-// barrier between them.
+// All steps of the orthogonalised update (orthogonalize.cu has the formulas) in one
+// launch.  Two forms of one kernel:
 //
-// Small products are bound by latency: as launches of their own they take 4.7 us
+// Clusters, for small matrices: a cluster of 1 to 8 CTAs takes a matrix and goes through
+// the products A = X X^T, B = a I + b A + c A^2, X = B X of every step, with a cluster
+// barrier between them.  Small products are bound by latency: as launches of their own they take 4.7 us
 // each (a launch's end and start, cold instructions, the first copies), 15 of them
 // for five steps; here 3.1 us, for the barrier, the first copies and the last tile's
 // epilogue (8 x 64 x 64 in five steps: 76 and 54 us).  Matrices and sums stay in L2.
-// Products of many tiles are better off with all SMs: orthogonalize.cu compares both by
-// modelled cycles.
+//
+// The whole grid, for matrices of some tiles (GRID): the tiles of all products of all
+// matrices stand in one order, step by step, product by product, matrix by matrix, and
+// CTA i of n takes the tiles i, i + n, ...  A tile waits until its matrix's products
+// before are finished, which it counts in the workspace; other matrices' tiles fill the
+// time.  A tile waits for earlier ones only, every CTA goes through its own in order and
+// all run at once (a cooperative launch), so the earliest unfinished tile can always go
+// on.  Against launches of their own no launch's end is waited for and no partly filled
+// round is left between products, only after the last: 8 x 1024 x 1024 307 and 236 us,
+// 16 x 517 x 1031 267 and 210, 64 x 512 x 1024 673 and 554.  Long sums in few tiles (no
+// slices here) and tiles of 256 x 256 on SM pairs stay ahead as launches of their own.
+//
+// orthogonalize.cu compares the forms by modelled cycles.
 //
 // Roles, tiles, epilogue and slices of a reduction are those of ragged_one.cuh's
 // EPI_DENSE (128 columns x up to 256 rows, fp32 sums in tensor memory, slices joined
 // through the workspace in their order).  What a product's epilogue writes, the next
 // product's copies read through the asynchronous proxy: a proxy fence stands on both
-// sides of the barrier.  Every wait is bounded; a CTA whose wait ran out skips the
+// sides of the barrier or flag.  Every wait is bounded; a CTA whose wait ran out skips the
 // rest of its work but keeps to the cluster's barriers.
 #include <algorithm>
 
@@ -30,7 +41,9 @@ namespace {
 
 constexpr int BK = 64, MAX_STAGES = 9;
 constexpr int A_BYTES = 128 * BK * 2, RING_BYTES = 196608, BAR_BYTES = 256;
-constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
+constexpr int EPI_WARPS = 8;
+// producer, MMA, epilogue warps; whole grid: one that tells it of finished tiles
+constexpr int threads(bool grid) { return 64 + 32 * EPI_WARPS + (grid ? 32 : 0); }
 constexpr int TMEM_COLS = 512;
 constexpr int SMEM_BYTES = RING_BYTES + 1024 + BAR_BYTES;
 
@@ -48,6 +61,7 @@ struct Args {
   __half *x[2], *lo, *a, *b;
   __nv_bfloat16* out;
   float* part;
+  uint32_t* done;
   float c_gram, c_apply, c_last;                 // c_acc of the products
   float coef[3 * MOE_MAX_ORTHOGONALIZE_STEPS];   // a or c_diag, c_mat and c_acc of B
   uint64_t limit_ns;
@@ -58,7 +72,7 @@ struct Args {
 // One product: its tiles and slices, operands, and the epilogue's arguments.
 struct Phase {
   int per, tok_tiles, tiles, splits, log_splits, seg_kb, segs, rows_end;
-  bool nt;
+  bool nt, tri;
   const CUtensorMap *w, *rows;
 };
 __device__ __forceinline__ Phase phase_of(const Maps& maps, const Args& q, int p, RagArgs& a) {
@@ -68,7 +82,8 @@ __device__ __forceinline__ Phase phase_of(const Maps& maps, const Args& q, int p
   Phase f;
   f.per = t.per;
   f.tok_tiles = t.tok_tiles;
-  f.tiles = t.w_tiles * t.tok_tiles;
+  f.tiles = t.tiles;
+  f.tri = t.tri;
   f.splits = t.splits;
   f.log_splits = t.splits == 1 ? 0 : t.splits == 2 ? 1 : t.splits == 4 ? 2 : 3;
   f.segs = q.parts == 2 ? 3 : 1;
@@ -87,7 +102,7 @@ __device__ __forceinline__ Phase phase_of(const Maps& maps, const Args& q, int p
   d.m = q.m;
   d.sym = type != 2;
   d.mp = q.mp;
-  d.tri = 0;
+  d.tri = t.tri;
   d.per = t.per;
   d.c_acc = type == 0 ? q.c_gram : type == 1 ? q.coef[3 * step + 2] : last ? q.c_last : q.c_apply;
   const bool kept = step < q.kept;
@@ -111,8 +126,12 @@ __device__ __forceinline__ Item item_of(const Phase& f, const Args& q, int e, in
   r.t = i >> f.log_splits;
   r.slice = i - (r.t << f.log_splits);
   r.tile.e = e;
-  r.tile.w_tile = f.tok_tiles == 1 ? r.t : r.t / f.tok_tiles;
-  r.tile.tok = r.t - r.tile.w_tile * f.tok_tiles;
+  if (f.tri) {
+    rag_triangle(r.t, r.tile);
+  } else {
+    r.tile.w_tile = f.tok_tiles == 1 ? r.t : r.t / f.tok_tiles;
+    r.tile.tok = r.t - r.tile.w_tile * f.tok_tiles;
+  }
   r.tile.row0 = e * q.m + r.tile.tok * f.per;
   r.tile.rows = min(f.per, f.rows_end - r.tile.tok * f.per);
   const int n = f.segs * f.seg_kb;
@@ -121,14 +140,25 @@ __device__ __forceinline__ Item item_of(const Phase& f, const Args& q, int e, in
   return r;
 }
 
-__global__ void __launch_bounds__(THREADS, 1)
+// Tiles of matrix e that are finished, with all that their CTAs wrote before.
+__device__ __forceinline__ uint32_t done_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void done_release(uint32_t* p) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
+}
+
+template <bool GRID>
+__global__ void __launch_bounds__(threads(GRID), 1)
     k_ortho_cluster(const __grid_constant__ Maps maps, const __grid_constant__ Args args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
-  // full[S], empty[S], tfull[2], tempty[2], drain
-  constexpr int NBARS = 2 * MAX_STAGES + 5;
+  // full[S], empty[S], tfull[2], tempty[2], drain, stored[2], told[2]
+  constexpr int NBARS = 2 * MAX_STAGES + 9;
   static_assert(8 * NBARS + 8 <= BAR_BYTES, "barrier area");
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
@@ -139,6 +169,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * MAX_STAGES + a); };
   auto tempty_bar = [&](int a) { return bar_base + 8u * (2 * MAX_STAGES + 2 + a); };
   const uint32_t drain_bar = bar_base + 8u * (2 * MAX_STAGES + 4);
+  auto stored_bar = [&](int b) { return bar_base + 8u * (2 * MAX_STAGES + 5 + b); };
+  auto told_bar = [&](int b) { return bar_base + 8u * (2 * MAX_STAGES + 7 + b); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < MAX_STAGES; ++s) {
@@ -148,6 +180,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
       mbar_init(tempty_bar(a), EPI_WARPS);
+      mbar_init(stored_bar(a), EPI_WARPS);
+      mbar_init(told_bar(a), 1);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -165,8 +199,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem_base = *tmem_holder;
   griddep_wait();
 
-  const int ctas = args.plan.ctas, stages = args.plan.stages, stage_bytes = args.plan.stage_bytes;
-  const int rank = blockIdx.x % ctas, e = blockIdx.x / ctas;
+  const int ctas = GRID ? (int)gridDim.x : args.plan.ctas;
+  const int stages = args.plan.stages, stage_bytes = args.plan.stage_bytes;
+  const int rank = GRID ? (int)blockIdx.x : blockIdx.x % ctas, e = GRID ? 0 : blockIdx.x / ctas;
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
     return mbar_wait_bounded(bar, parity, abort_flag, args.limit_ns, args.err);
   };
@@ -178,22 +213,58 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
   bool ok = true, skip_first = args.never_arrive != 0;
 
+  // GRID: until `need` tiles of matrix m are finished, by the whole warp
+  auto wait_done = [&](int m, uint32_t need) -> bool {
+    int got = 1;
+    if (lane == 0 && need != 0) {
+      const uint64_t t0 = globaltimer_ns();
+      for (uint32_t it = 1; done_acquire(args.done + m) < need; ++it) {
+        if ((it & 15) != 0) continue;
+        if (*abort_flag || globaltimer_ns() - t0 > args.limit_ns) {
+          if (!*abort_flag) set_dev_error(args.err, kDevErrTimeout);
+          *abort_flag = 1;
+          got = 0;
+          break;
+        }
+      }
+    }
+    got = __shfl_sync(0xffffffffu, got, 0);
+    __syncwarp();
+    return got != 0;
+  };
+  // item i of a product
+  auto at = [&](const Phase& f, int i) -> Item {
+    if (!GRID) return item_of(f, args, e, i);
+    const int m = i / f.tiles;
+    return item_of(f, args, m, i - m * f.tiles);
+  };
+
   RagArgs a;
   Phase f = phase_of(maps, args, 0, a);
-  Item first = item_of(f, args, e, rank);
+  Item first{};
+  if (!GRID) first = item_of(f, args, e, rank);
+  int begin = rank;               // GRID: this CTA's next item, counted from the product's first
+  uint32_t before = 0;            // GRID: tiles of a matrix in the products before
   for (int p = 0; p < 3 * args.steps; ++p) {
     // Arguments and the first item: the producer and the MMA issuer have them before
     // the barrier opens, the epilogue's warps find them while the sums are computed.
-    if (warp >= 2 && p > 0) {
+    if ((GRID || warp >= 2) && p > 0) {
       f = phase_of(maps, args, p, a);
-      first = item_of(f, args, e, rank);
+      if (!GRID) first = item_of(f, args, e, rank);
     }
-    const int items = f.tiles * f.splits;
+    const int items = GRID ? args.E * f.tiles : f.tiles * f.splits;
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      for (int i = rank; ok && i < items; i += ctas) {
-        const Item it = i == rank ? first : item_of(f, args, e, i);
+      for (int i = begin; ok && i < items; i += ctas) {
+        const Item it = !GRID && i == rank ? first : at(f, i);
         const int boxes = (it.tile.rows + 31) / 32;
+        if (GRID) {
+          if (!wait_done(it.tile.e, before)) {
+            ok = false;
+            break;
+          }
+          fence_proxy_async_global();
+        }
         int seg = it.kb0 >= 2 * f.seg_kb ? 2 : it.kb0 >= f.seg_kb ? 1 : 0;
         int seg_k = it.kb0 - seg * f.seg_kb;
         const int w_lo = f.nt ? (f.seg_kb * BK) : args.Mp, rows_lo = f.seg_kb * BK;
@@ -211,9 +282,10 @@ __global__ void __launch_bounds__(THREADS, 1)
               mbar_arrive_expect_tx(bar, A_BYTES + boxes * 32 * BK * 2);
               const int k0 = seg_k * BK, a_lo = seg == 1 ? w_lo : 0, b_lo = seg == 2 ? rows_lo : 0;
               if (f.nt)
-                tma_load_3d(sa, f.w, bar, k0 + a_lo, it.tile.w_tile * 128, e, pol);
+                tma_load_3d(sa, f.w, bar, k0 + a_lo, it.tile.w_tile * 128, it.tile.e, pol);
               else
-                tma_load_4d(sa, f.w, bar, 0, k0, it.tile.w_tile * 2 + a_lo / 64, e, pol);
+                tma_load_4d(sa, f.w, bar, 0, k0, it.tile.w_tile * 2 + a_lo / 64, it.tile.e,
+                            pol);
               for (int j = 0; j < boxes; ++j)
                 tma_load_2d(sb + j * 32 * BK * 2, f.rows, bar, k0 + b_lo, it.tile.row0 + 32 * j,
                             pol);
@@ -234,8 +306,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
       const uint32_t major = f.nt ? 0u : kIdescAMn, a_step = f.nt ? 2 : 128;
-      for (int i = rank; ok && i < items; i += ctas) {
-        const Item it = i == rank ? first : item_of(f, args, e, i);
+      for (int i = begin; ok && i < items; i += ctas) {
+        const Item it = !GRID && i == rank ? first : at(f, i);
         const int n = (it.tile.rows + 15) / 16 * 16;
         const uint32_t idesc = make_idesc(Half16<__half>::kFmt, Half16<__half>::kFmt, 128, n) | major;
         const int acc = local & 1;
@@ -268,16 +340,38 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (elect_one()) tc_commit(tfull_bar(acc));
         ++local;
       }
+    } else if (GRID && warp == 2 + EPI_WARPS) {
+      // ---------------------------------------------------------- flags
+      // Tells the grid of a tile when its stores are done: the fences wait for all of
+      // them (some 2000 cycles), the epilogue's warps go on with the next tile.
+      for (int i = begin; ok && i < items; i += ctas) {
+        if (!warp_wait(stored_bar(local & 1), (local >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        fence_proxy_async_global();
+        __threadfence();
+        if (lane == 0) {
+          done_release(args.done + i / f.tiles);
+          mbar_arrive(told_bar(local & 1));
+        }
+        __syncwarp();
+        ++local;
+      }
     } else {
       // ---------------------------------------------------------- epilogue
       const int q = warp & 3;
       const bool loads = f.splits == 1 && a.dense.mat != nullptr;
       const int part = (warp - 2) >> 2;
       constexpr int STEP = 4 * EPI_WARPS;
-      for (int i = rank; ok && i < items; i += ctas) {
-        const Item it = i == rank ? first : item_of(f, args, e, i);
+      for (int i = begin; ok && i < items; i += ctas) {
+        const Item it = !GRID && i == rank ? first : at(f, i);
         const int acc = local & 1, w = it.tile.w_tile * 128 + q * 32 + lane;
         Words16 mat_next;
+        if (GRID && loads && !wait_done(it.tile.e, before)) {
+          ok = false;
+          break;
+        }
         if (loads && 16 * part < it.tile.rows)
           rag_dense_load(a, it.tile, mat_next, 16 * part, w, lane);
         int got = 0;
@@ -294,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_ld_wait();
           const int tok = it.tile.tok * f.per + c, left = it.tile.rows - c;
           if (loads && c + STEP < it.tile.rows) rag_dense_load(a, it.tile, mat_next, c + STEP, w, lane);
-          if (f.splits > 1)
+          if (!GRID && f.splits > 1)
             rag_store_part(a, r, e * f.tiles + it.t, it.slice, c, it.tile.rows, q * 32 + lane);
           else if (f.nt)
             rag_dense_store16<true>(a, it.tile, r, h, loads, tok, left, w, lane);
@@ -306,15 +400,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(tempty_bar(acc));
         ++local;
+        if (GRID) {                 // (the tile two before has been told)
+          const int n = local - 1;
+          if (!warp_wait(told_bar(n & 1), ((n >> 1) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive(stored_bar(n & 1));
+        }
       }
+    }
+    if (GRID) {
+      const int mine = begin < items ? (items - begin + ctas - 1) / ctas : 0;
+      begin += mine * ctas - items;
+      before += f.tiles;
+      continue;
     }
     if (f.splits > 1) {
       cluster_sync();
       if (*abort_flag == 0) {
         for (int t = 0; t < f.tiles; ++t) {
           const RagTile D = item_of(f, args, e, t * f.splits).tile;
-          rag_join_fused<EPI_DENSE, __half>(a, D, e * f.tiles + t, rank, ctas, warp, THREADS / 32,
-                                            lane);
+          rag_join_fused<EPI_DENSE, __half>(a, D, e * f.tiles + t, rank, ctas, warp,
+                                            threads(false) / 32, lane);
         }
       }
     }
@@ -366,12 +474,13 @@ OrthoClusterPlan ortho_cluster_plan(int E, int m, int mp, int M, int Mp, int par
       for (int tile = 32; tile <= 256; tile *= 2) {
         if (tile > 32 && tile >= 2 * rows) break;
         for (int splits = 1; splits <= ctas; splits *= 2) {
-          OrthoTiles t;
+          OrthoTiles t{};
           t.splits = splits;
           t.w_tiles = (width + 127) / 128;
           t.tok_tiles = (rows + tile - 1) / tile;
           t.per = ((rows + t.tok_tiles - 1) / t.tok_tiles + unit - 1) / unit * unit;
-          const long long items = (long long)t.w_tiles * t.tok_tiles * splits;
+          t.tiles = t.w_tiles * t.tok_tiles;
+          const long long items = (long long)t.tiles * splits;
           if (splits > 1 && (items > ctas || kb < 2 * splits)) continue;
           const long long k = (kb + splits - 1) / splits;
           const long long step = std::max((16384 + (t.per + 31) / 32 * 4096) / 55, 53 * t.per / 20);
@@ -395,6 +504,51 @@ OrthoClusterPlan ortho_cluster_plan(int E, int m, int mp, int M, int Mp, int par
     if (best.cycles == 0 || r.cycles < best.cycles) best = r;
   }
   return best;
+}
+
+// For the whole grid: tiles of least time.  A product takes its tiles' share of the
+// SMs, or what stands between one matrix's products: the flag and its fences, the first
+// copies, a tile.  Between unlike forms (`cycles`) the latter counts more than between
+// tiles, as measured: its operands were just written by other SMs.  The last product
+// takes what its epilogue moves of X's two parts.
+OrthoClusterPlan ortho_grid_plan(int E, int m, int mp, int M, int Mp, int parts, int steps) {
+  OrthoClusterPlan r{};
+  const int segs = parts == 2 ? 3 : 1;
+  int widest = 32;
+  for (int type = 0; type < 3; ++type) {
+    const int width = type == 2 ? Mp : mp, rows = type == 2 ? m : mp;
+    const int kb = segs * (type == 0 ? Mp : mp) / BK, unit = type == 2 ? 16 : 32;
+    long long least = 0, cycles = 0;
+    for (int tile = 32; tile <= 256; tile *= 2) {
+      if (tile > 32 && tile >= 2 * rows) break;
+      for (int tri = 0; tri < 2; ++tri) {
+        if (tri && (type == 2 || tile != 128)) continue;
+        OrthoTiles t{};
+        t.splits = 1;
+        t.tri = tri;
+        t.w_tiles = (width + 127) / 128;
+        t.tok_tiles = (rows + tile - 1) / tile;
+        t.per = tri ? tile : ((rows + t.tok_tiles - 1) / t.tok_tiles + unit - 1) / unit * unit;
+        t.tiles = tri ? t.w_tiles * (t.w_tiles + 1) / 2 : t.w_tiles * t.tok_tiles;
+        const long long step = std::max((16384 + (t.per + 31) / 32 * 4096) / 55, 53 * t.per / 20);
+        const long long epilogue = (tri ? 1700 : 1400) * ((t.per + 31) / 32);
+        const long long each = std::max(kb * step, epilogue);
+        const long long share = ((long long)E * t.tiles + 151) / 152 * (each + 1200);
+        const long long c = std::max(share, 6000 + kb * step + epilogue);
+        if (least == 0 || c < least) {
+          least = c;
+          cycles = std::max(share, 8000 + 6 * kb * step / 5 + epilogue);
+          r.t[type] = t;
+        }
+      }
+    }
+    if (type == 2 && parts == 1) cycles = std::max(cycles, 8ll * E * m * Mp / 2100);
+    r.cycles += steps * cycles;
+    widest = std::max(widest, (r.t[type].per + 31) / 32 * 32);
+  }
+  r.stage_bytes = A_BYTES + widest * BK * 2;
+  r.stages = std::min(MAX_STAGES, RING_BYTES / r.stage_bytes);
+  return r;
 }
 
 size_t ortho_cluster_part_bytes(const OrthoClusterPlan& p, int E) {
@@ -445,12 +599,31 @@ cudaError_t launch_ortho_cluster(const OrthoClusterProblem& d, cudaStream_t stre
   if (q.err == nullptr) return cudaErrorInvalidDevice;
   static DeviceOnce attr;
   const cudaError_t e = attr.call([] {
-    return cudaFuncSetAttribute(k_ortho_cluster, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t r = cudaFuncSetAttribute(
+        k_ortho_cluster<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (r != cudaSuccess) return r;
+    return cudaFuncSetAttribute(k_ortho_cluster<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 SMEM_BYTES);
   });
   if (e != cudaSuccess) return e;
-  return launch_dependent(k_ortho_cluster, (unsigned)(d.E * d.plan.ctas), THREADS, SMEM_BYTES, stream,
-                          d.plan.ctas, maps, q);
+  if (d.plan.ctas == 0) {          // all CTAs at the same time: one an SM
+    q.done = d.done;
+    int most = 0;
+    for (const OrthoTiles& t : d.plan.t) most = std::max(most, t.tiles);
+    cudaLaunchAttribute coop;
+    coop.id = cudaLaunchAttributeCooperative;
+    coop.val.cooperative = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<long long>(num_sms(), (long long)d.E * most), 1, 1);
+    cfg.blockDim = dim3(threads(true), 1, 1);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = &coop;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_ortho_cluster<true>, maps, q);
+  }
+  return launch_dependent(k_ortho_cluster<false>, (unsigned)(d.E * d.plan.ctas), threads(false),
+                          SMEM_BYTES, stream, d.plan.ctas, maps, q);
 }
 
 }  // namespace moe

@@ -142,7 +142,7 @@ __device__ __forceinline__ double block_sum(double v, double* smem) {
 // bound the pass if there is one for every few values).
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads) k_ortho_norm(const void* g, long long n, int chunks,
-                                                         double* partial) {
+                                                         double* partial, uint32_t* done) {
   __shared__ double smem[kThreads / 32];
   griddep_launch();
   griddep_wait();
@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kThreads) k_ortho_norm(const void* g, long lon
       sum += f * f;
     }
   }
+  if (blockIdx.x == 0 && threadIdx.x == 0) done[blockIdx.y] = 0;     // for ortho_cluster.cu
   sum = block_sum(sum, smem);
   if (threadIdx.x == 0) partial[(size_t)blockIdx.y * chunks + blockIdx.x] = sum;
 }
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, TYPE == 2 ? 5 : 6)
 
 struct Layout {
   int m, M, mp, Mp, parts, chunks;
-  size_t x_bytes, a_bytes, partial, a, b, x0, x1, lo, part, total;
+  size_t x_bytes, a_bytes, partial, done, a, b, x0, x1, lo, part, total;
 };
 size_t pad(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -366,6 +367,9 @@ constexpr int kModelSteps = 5;
 OrthoClusterPlan cluster_plan(const Layout& l, int E) {
   return ortho_cluster_plan(E, l.m, l.mp, l.M, l.Mp, l.parts, kModelSteps);
 }
+OrthoClusterPlan grid_plan(const Layout& l, int E) {
+  return ortho_grid_plan(E, l.m, l.mp, l.M, l.Mp, l.parts, kModelSteps);
+}
 
 Layout layout(int E, int N, int K) {
   Layout l;
@@ -380,7 +384,8 @@ Layout layout(int E, int N, int K) {
   l.x_bytes = pad((size_t)E * l.m * l.parts * l.Mp * 2);
   l.a_bytes = pad((size_t)E * l.m * l.parts * l.mp * 2);
   l.partial = 0;
-  l.a = pad((size_t)E * l.chunks * sizeof(double));
+  l.done = pad((size_t)E * l.chunks * sizeof(double));
+  l.a = l.done + pad(E * sizeof(uint32_t));
   l.b = l.a + l.a_bytes;
   l.x0 = l.b + l.a_bytes;
   l.x1 = l.x0 + l.x_bytes;
@@ -397,19 +402,35 @@ Layout layout(int E, int N, int K) {
   return l;
 }
 
-// Whether one launch for all steps (ortho_cluster.cu) is modelled to be the faster.  The
-// models leave out what both take alike; against each other, a product of its own takes
-// some 3500 cycles more (its launch), and the clusters' cycles count 6/5: they read and
-// add a X where it is used, and a matrix has eight SMs at most.  Measured in clusters /
-// as products, us a step: 8 x 64 x 64 9.3 / 14.3, 8 x 256 x 512 14.4 / 16.9, 64 x 128 x
-// 1024 33.9 / 38.6; 8 x 257 x 512 20.0 / 18.7, 8 x 256 x 2048 32.7 / 25.5.
-bool in_clusters(const Layout& l, int E) {
-  if (ragged_form() != 0) return ragged_form() == 3;
+// Products as launches of their own, or one launch for all steps (ortho_cluster.cu): in
+// clusters or over the whole grid.  By modelled cycles, each with the factor that its
+// model was measured to be off by; X is kept in two parts beyond kPrecise, and what the
+// last product of a step moves for it (hi and lo, read and written) is counted at the
+// rates that the forms' epilogues reach.  A product of its own takes some 3500 cycles
+// more (its launch).  Up to kPrecise the whole grid never was the fastest.  us for five
+// steps as products / in clusters / over the grid:
+//   8 x 64 x 64     78 /  55 /  70      8 x 1024 x 1024   307 /  513 /  236
+//   8 x 256 x 512   84 /  78 /  89      16 x 768 x 2048   583 /  998 /  458
+//   8 x 512 x 512  125 / 149 / 117      64 x 512 x 1024   673 /  707 /  554
+//   2 x 200 x 2000 103 / 157 / 118      1 x 1024 x 2048   174 /  758 /  220
+//                                       16 x 2048 x 7168 6145 / 19047 / 7596
+enum class Form { PRODUCTS, CLUSTERS, GRID };
+Form form_of(const Layout& l, int E) {
+  if (ortho_form() != 0)
+    return ortho_form() == 4 ? Form::GRID : ortho_form() == 3 ? Form::CLUSTERS : Form::PRODUCTS;
   const float c[3] = {};
-  const long long own = dense_cycles(gram(l, E, nullptr, nullptr)) +
-                        dense_cycles(polynomial(l, E, nullptr, nullptr, c)) +
-                        dense_cycles(apply(l, E, nullptr, nullptr, nullptr)) + 3 * 3500;
-  return cluster_plan(l, E).cycles * 6 / 5 < kModelSteps * own;
+  const long long x_bytes = l.parts == 1 ? 8ll * E * l.m * l.Mp : 0;
+  const long long products =
+      kModelSteps * (dense_cycles(gram(l, E, nullptr, nullptr)) +
+                     dense_cycles(polynomial(l, E, nullptr, nullptr, c)) +
+                     std::max(dense_cycles(apply(l, E, nullptr, nullptr, nullptr)), x_bytes / 1450) +
+                     3 * 3500);
+  const long long clusters = cluster_plan(l, E).cycles * 6 / 5 + kModelSteps * x_bytes / 3300;
+  if (l.parts == 1) {
+    const long long grid = grid_plan(l, E).cycles;
+    if (grid * 19 / 20 < products && grid < clusters) return Form::GRID;
+  }
+  return clusters < products ? Form::CLUSTERS : Form::PRODUCTS;
 }
 
 cudaError_t run(const DenseProduct& d, void* part, cudaStream_t stream) {
@@ -418,7 +439,8 @@ cudaError_t run(const DenseProduct& d, void* part, cudaStream_t stream) {
 
 template <int TYPE>
 cudaError_t prepare(const Layout& l, int E, bool transposed, const void* g, float eps,
-                    double* partial, __half* x, long long lo, cudaStream_t stream) {
+                    double* partial, uint32_t* done, __half* x, long long lo,
+                    cudaStream_t stream) {
   const long long n = (long long)l.m * l.M;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -429,7 +451,7 @@ cudaError_t prepare(const Layout& l, int E, bool transposed, const void* g, floa
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(l.chunks, E, 1);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_ortho_norm<TYPE>, g, n, l.chunks, partial);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_ortho_norm<TYPE>, g, n, l.chunks, partial, done);
   if (e != cudaSuccess) return e;
   const int ld = l.parts * l.Mp;
   const double* sums = partial;
@@ -463,16 +485,20 @@ cudaError_t launch_orthogonalize(int E, int N, int K, const void* g, int type, v
   char* ws = static_cast<char*>(workspace);
   void *a = ws + l.a, *b = ws + l.b, *x = ws + l.x0, *y = ws + l.x1, *part = ws + l.part;
   double* partial = reinterpret_cast<double*>(ws + l.partial);
+  uint32_t* done = reinterpret_cast<uint32_t*>(ws + l.done);
   // steps that add a X in the epilogue, from X's hi and lo parts
   const int kept = l.parts == 1 ? std::max(0, steps - kFolded) : 0;
   __half* lo = reinterpret_cast<__half*>(ws + l.lo);
   __half* x0 = static_cast<__half*>(x);
   const long long x_lo = l.parts == 2 ? l.Mp : kept > 0 ? lo - x0 : 0;
-  cudaError_t e = type == 0   ? prepare<0>(l, E, transposed, g, eps, partial, x0, x_lo, stream)
-                  : type == 1 ? prepare<1>(l, E, transposed, g, eps, partial, x0, x_lo, stream)
-                              : prepare<2>(l, E, transposed, g, eps, partial, x0, x_lo, stream);
-  if (e == cudaSuccess && in_clusters(l, E)) {
-    OrthoClusterProblem d{cluster_plan(l, E), E, l.m, l.M, l.mp, l.Mp, l.parts, steps, transposed,
+  cudaError_t e = type == 0   ? prepare<0>(l, E, transposed, g, eps, partial, done, x0, x_lo, stream)
+                  : type == 1 ? prepare<1>(l, E, transposed, g, eps, partial, done, x0, x_lo, stream)
+                              : prepare<2>(l, E, transposed, g, eps, partial, done, x0, x_lo, stream);
+  if (e != cudaSuccess) return e;
+  const Form form = form_of(l, E);
+  if (form != Form::PRODUCTS) {
+    OrthoClusterProblem d{form == Form::GRID ? grid_plan(l, E) : cluster_plan(l, E),
+                          E, l.m, l.M, l.mp, l.Mp, l.parts, steps, transposed,
                           {x, y}, l.parts == 1 ? lo : nullptr, a, b, out, part, kept};
     d.c_gram = gram(l, E, x, a).c_acc;
     d.c_apply = apply(l, E, b, x, y).c_acc;
@@ -485,6 +511,7 @@ cudaError_t launch_orthogonalize(int E, int N, int K, const void* g, int type, v
       coef[3 * s + 2] = p.c_acc;
     }
     d.coef = coef;
+    d.done = done;
     return launch_ortho_cluster(d, stream);
   }
   for (int s = 0; s < steps && e == cudaSuccess; ++s) {

@@ -182,6 +182,14 @@ __device__ __forceinline__ void rag_gated_grad_tokens16(const RagArgs& a, const 
 // Tile t of the batch.  rows: of a symmetric product those of its padded output,
 // which has zeros there.  tri: the tiles (w_tile, tok) with tok <= w_tile; else
 // groups of 8 token tiles, as rag_tile.
+__device__ __forceinline__ void rag_triangle(int l, RagTile& T) {
+  // l = i (i + 1) / 2 + tok: i from the square root, which is off by one at most
+  int i = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
+  if (i * (i + 1) / 2 > l) --i;
+  if ((i + 1) * (i + 2) / 2 <= l) ++i;
+  T.w_tile = i;
+  T.tok = l - i * (i + 1) / 2;
+}
 template <int G>
 __device__ __forceinline__ RagTile rag_dense_tile(const RagArgs& a, int t) {
   const RagDense& q = a.dense;
@@ -189,12 +197,7 @@ __device__ __forceinline__ RagTile rag_dense_tile(const RagArgs& a, int t) {
   T.e = t / q.e_tiles;
   const int l = t - T.e * q.e_tiles.d;
   if (q.tri) {
-    // l = i (i + 1) / 2 + tok: i from the square root, which is off by one at most
-    int i = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
-    if (i * (i + 1) / 2 > l) --i;
-    if ((i + 1) * (i + 2) / 2 <= l) ++i;
-    T.w_tile = i;
-    T.tok = l - i * (i + 1) / 2;
+    rag_triangle(l, T);
     T.rows = min(q.per, q.mp - T.tok * q.per);
   } else {
     const int w_tiles = a.w_tiles.d;

@@ -27,9 +27,10 @@ pytestmark = pytest.mark.gpu
 DT = {"bfloat16": torch.bfloat16, "float16": torch.float16, "float32": torch.float32}
 
 
-@pytest.fixture(params=["auto", "single", "pairs", "pairs_double"])
+@pytest.fixture(params=["auto", "single", "pairs", "pairs_double", "whole_grid"])
 def form(request):
-    """By size; products one launch each, on one SM or SM pairs; all steps in one launch."""
+    """By size; products one launch each, on one SM or SM pairs; all steps in one launch,
+    in clusters or over the whole grid."""
     moe.moe_debug_set_bf16_gemm_form(request.param)
     yield request.param
     moe.moe_debug_set_bf16_gemm_form("auto")

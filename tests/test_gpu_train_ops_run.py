@@ -141,7 +141,7 @@ def test_gradients_against_differences():
             assert abs((g * d).sum() - want) <= 4 * 3 * 2.0 ** -9 * np.sqrt((g ** 2).sum())
 
 
-@pytest.mark.parametrize("form", ["auto", "single", "pairs", "pairs_double"])
+@pytest.mark.parametrize("form", ["auto", "single", "pairs", "pairs_double", "whole_grid"])
 def test_streams_and_graphs_give_the_same_bits(form):
     """Two layers on two streams at once, eager and captured into one graph together,
     against each by itself."""
@@ -211,7 +211,7 @@ def test_two_graphs_share_a_workspace_in_turn():
             assert all(torch.equal(t, v) for t, v in zip(block.outputs(), w))
 
 
-@pytest.mark.parametrize("form", ["single", "pairs", "pairs_double"])
+@pytest.mark.parametrize("form", ["single", "pairs", "pairs_double", "whole_grid"])
 def test_wait_that_runs_out_is_reported(form):
     """The producer leaves its first copy out, the waits run out and are reported, and the
     next calls give the same bits as before."""
@@ -351,7 +351,7 @@ print("done")
 """
 
 
-@pytest.mark.parametrize("form", ["auto", "single", "pairs", "pairs_double"])
+@pytest.mark.parametrize("form", ["auto", "single", "pairs", "pairs_double", "whole_grid"])
 def test_first_call_of_a_process_in_a_capture(form):
     r = subprocess.run([sys.executable, "-c", FIRST.replace("{form!r}", repr(form))], cwd=ROOT,
                        capture_output=True, text=True, timeout=300)
