@@ -41,6 +41,8 @@ namespace {
 
 constexpr int BK = 64, MAX_STAGES = 9;
 constexpr int A_BYTES = 128 * BK * 2, RING_BYTES = 196608, BAR_BYTES = 256;
+// 12 over the whole grid measured 5% slower where sums are long (8 x 1536 x 1536: 639 and
+// 607 us) and 6% faster where they are short (64 x 256 x 2048: 423 and 449); 16 spill.
 constexpr int EPI_WARPS = 8;
 // producer, MMA, epilogue warps; whole grid: one that tells it of finished tiles
 constexpr int threads(bool grid) { return 64 + 32 * EPI_WARPS + (grid ? 32 : 0); }
@@ -149,6 +151,17 @@ __device__ __forceinline__ uint32_t done_acquire(const uint32_t* p) {
 __device__ __forceinline__ void done_release(uint32_t* p) {
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
 }
+// Tiles of this CTA whose matrix's products before are finished: its producer's count
+// for the epilogue's warps, which load A or X before the sums are complete (eight warps more that read
+// the grid's counter in L2 cost 1 to 4%).
+__device__ __forceinline__ uint32_t ready_acquire(uint32_t p) {
+  uint32_t v;
+  asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void ready_release(uint32_t p, uint32_t v) {
+  asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(p), "r"(v) : "memory");
+}
 
 template <bool GRID>
 __global__ void __launch_bounds__(threads(GRID), 1)
@@ -159,9 +172,10 @@ __global__ void __launch_bounds__(threads(GRID), 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
   // full[S], empty[S], tfull[2], tempty[2], drain, stored[2], told[2]
   constexpr int NBARS = 2 * MAX_STAGES + 9;
-  static_assert(8 * NBARS + 8 <= BAR_BYTES, "barrier area");
+  static_assert(8 * NBARS + 12 <= BAR_BYTES, "barrier area");
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  const uint32_t ready = smem_u32(tmem_holder + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t smem_base = smem_u32(smem), bar_base = smem_u32(bars);
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
@@ -185,6 +199,7 @@ __global__ void __launch_bounds__(threads(GRID), 1)
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
+    tmem_holder[2] = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -213,12 +228,12 @@ __global__ void __launch_bounds__(threads(GRID), 1)
   uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
   bool ok = true, skip_first = args.never_arrive != 0;
 
-  // GRID: until `need` tiles of matrix m are finished, by the whole warp
-  auto wait_done = [&](int m, uint32_t need) -> bool {
+  // GRID: until get() is at least `need`, by the whole warp
+  auto wait_count = [&](auto get, uint32_t need) -> bool {
     int got = 1;
     if (lane == 0 && need != 0) {
       const uint64_t t0 = globaltimer_ns();
-      for (uint32_t it = 1; done_acquire(args.done + m) < need; ++it) {
+      for (uint32_t it = 1; get() < need; ++it) {
         if ((it & 15) != 0) continue;
         if (*abort_flag || globaltimer_ns() - t0 > args.limit_ns) {
           if (!*abort_flag) set_dev_error(args.err, kDevErrTimeout);
@@ -259,10 +274,12 @@ __global__ void __launch_bounds__(threads(GRID), 1)
         const Item it = !GRID && i == rank ? first : at(f, i);
         const int boxes = (it.tile.rows + 31) / 32;
         if (GRID) {
-          if (!wait_done(it.tile.e, before)) {
+          const uint32_t* done = args.done + it.tile.e;
+          if (!wait_count([&] { return done_acquire(done); }, before)) {
             ok = false;
             break;
           }
+          if (lane == 0) ready_release(ready, ++local);
           fence_proxy_async_global();
         }
         int seg = it.kb0 >= 2 * f.seg_kb ? 2 : it.kb0 >= f.seg_kb ? 1 : 0;
@@ -368,7 +385,7 @@ __global__ void __launch_bounds__(threads(GRID), 1)
         const Item it = !GRID && i == rank ? first : at(f, i);
         const int acc = local & 1, w = it.tile.w_tile * 128 + q * 32 + lane;
         Words16 mat_next;
-        if (GRID && loads && !wait_done(it.tile.e, before)) {
+        if (GRID && loads && !wait_count([&] { return ready_acquire(ready); }, local + 1)) {
           ok = false;
           break;
         }
