@@ -152,8 +152,8 @@ __device__ __forceinline__ void done_release(uint32_t* p) {
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
 }
 // Tiles of this CTA whose matrix's products before are finished: its producer's count
-// for the epilogue's warps, which load A or X before the sums are complete (eight warps more that read
-// the grid's counter in L2 cost 1 to 4%).
+// for the epilogue's warps, which load A or X before the sums are complete (eight warps
+// more that read the grid's counter in L2 cost 1 to 4%).
 __device__ __forceinline__ uint32_t ready_acquire(uint32_t p) {
   uint32_t v;
   asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
