@@ -695,6 +695,15 @@ def _coefficients(steps, coefficients):
     return flat
 
 
+def _numbers(c):
+    """The sequence c, or a sequence of such, with floats in place of what it holds:
+    tensors and arrays of one number hash by identity, and may change between calls."""
+    try:
+        return tuple(map(float, c))
+    except (TypeError, ValueError, RuntimeError):       # not numbers: a triple a step
+        return tuple(tuple(map(float, row)) for row in c)
+
+
 def moe_orthogonalize(g, out, workspace, steps=5, coefficients=(3.4445, -4.7750, 2.0315),
                       eps=1e-7, scale=1.0, stream=None):
     """out = scale X of every matrix of g [E, N, K] (or [N, K]; bfloat16, float16 or
@@ -707,8 +716,8 @@ def moe_orthogonalize(g, out, workspace, steps=5, coefficients=(3.4445, -4.7750,
     E, N, K = shape if len(shape) == 3 else (1, *shape)
     dev = g.get_device()
     ws, n = _bytes("workspace", workspace, dev)
-    if type(coefficients) is not tuple or list in map(type, coefficients):
-        coefficients = tuple(tuple(c) if hasattr(c, "__len__") else c for c in coefficients)
+    if type(coefficients) is not tuple or set(map(type, coefficients)) != {float}:
+        coefficients = _numbers(coefficients)
     c = _coefficients(steps, coefficients)
     _check(lib().moe_orthogonalize(
         E, N, K, _dense("g", g, shape, g.dtype, dev), _float_code("g", g),
