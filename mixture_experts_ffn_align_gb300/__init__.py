@@ -682,6 +682,9 @@ def moe_orthogonalize_workspace_bytes(E: int, N: int, K: int) -> int:
     return int(lib().moe_orthogonalize_workspace_bytes(int(E), int(N), int(K)))
 
 
+MAX_ORTHOGONALIZE_STEPS = 64      # MOE_MAX_ORTHOGONALIZE_STEPS in include/moe_ffn.h
+
+
 @lru_cache(64)
 def _coefficients(steps, coefficients):
     """The steps' coefficients as an array: three numbers for all, or three a step."""
@@ -716,6 +719,8 @@ def moe_orthogonalize(g, out, workspace, steps=5, coefficients=(3.4445, -4.7750,
     E, N, K = shape if len(shape) == 3 else (1, *shape)
     dev = g.get_device()
     ws, n = _bytes("workspace", workspace, dev)
+    if not 1 <= steps <= MAX_ORTHOGONALIZE_STEPS:
+        raise ValueError(f"steps must be 1 to {MAX_ORTHOGONALIZE_STEPS}, not {steps}")
     if type(coefficients) is not tuple or set(map(type, coefficients)) != {float}:
         coefficients = _numbers(coefficients)
     c = _coefficients(steps, coefficients)

@@ -66,6 +66,13 @@ def test_default_and_longest(passed):
     assert passed(steps=64) == f * 64
 
 
+@pytest.mark.parametrize("steps", [-1, 0, 65, 1 << 32, (1 << 32) + 5, 1 << 60])
+def test_step_counts_are_refused_before_anything_is_laid_out(passed, steps):
+    """A count past 32 bits would wrap to another one, a huge one fill the memory."""
+    with pytest.raises(ValueError, match="steps"):
+        passed(steps=steps)
+
+
 @pytest.mark.parametrize("bad", [(1.0, 2.0), (), ((1.0, 2.0),) * 5, ((1.0, 2.0, 3.0),) * 4])
 def test_wrong_numbers_of_coefficients(passed, bad):
     with pytest.raises(ValueError, match="coefficients"):
