@@ -139,7 +139,7 @@ __device__ __forceinline__ double block_sum(double v, double* smem) {
 
 // Squares of part blockIdx.x of matrix blockIdx.y (n elements): in fp32 over at most
 // 64 values, in fp64 beyond (fp64 additions and conversions are slow enough to
-// bound the pass if there is one for every few values).
+// bound the pass if there is one for every few values) or where that sum overflows.
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads) k_ortho_norm(const void* g, long long n, int chunks,
                                                          double* partial, uint32_t* done) {
@@ -176,7 +176,18 @@ __global__ void __launch_bounds__(kThreads) k_ortho_norm(const void* g, long lon
         }
       }
     }
-    sum += (s[0] + s[1]) + (s[2] + s[3]);
+    const float all = (s[0] + s[1]) + (s[2] + s[3]);
+    if (all <= 3.402823466e38f) {
+      sum += all;
+    } else {       // squares within fp32's range whose sum is not: once more, one by one
+      const long long first = head + i * per;
+#pragma unroll 1
+      for (int k = 0; k < 8 * per; ++k) {
+        const long long at = first + (long long)(k / per) * kThreads * per + k % per;
+        const float f = at < head + end * per ? load1<TYPE>(base, at) : 0.0f;
+        sum += f * f;
+      }
+    }
   }
   if (blockIdx.x == 0 && threadIdx.x < 32) {
     const long long tail = head + pieces * per;
