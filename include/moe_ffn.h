@@ -594,16 +594,30 @@ moe_status moe_clip_grad_norm(int n, const void* const* grads, void* const* outs
  *    MOE_MAX_ORTHOGONALIZE_STEPS.  They should keep singular values of X below 3 and
  *    the polynomial's values within 16: elements past that are infinities.
  *  - eps: at least 1e-12; a zero matrix gives zeros.
- *  - Products take operands of 11 bits (22 where N or K is at most 128), X itself is
- *    kept with 22 bits until the last step, sums are fp32: the result is within
- *    about 0.25% (rms) of the exact one, its own rounding to bf16 (0.17%) among that.
+ *  - Sums are fp32, X is kept with 22 bits until the last step.  Errors, as rms of the
+ *    result's, its own rounding to bf16 among them (0.17%; up to 0.39% where its values
+ *    are equal):
+ *    Where N or K is at most 128, and where the steps enlarge roundings more than five of
+ *    (3.4445, -4.7750, 2.0315) do (six of them; steeper triples; a product of the later
+ *    a's above 160), products take operands of 22 bits: within 0.25% for up to eight
+ *    steps and sides up to 2^14.  Beyond, steps enlarge what the sums lose by truncation
+ *    (2^-28 of their length): 20 steps of that triple end within 0.3% at 2048 x 7168, and
+ *    within 2% at 200 x 2^18, five steep ones there within 0.5% (low rank: 1.3%).
+ *    Directions that g does not have (its rank is low) come out as up to 2^-20 of the
+ *    product of the a's, which eight steps of that triple make 1% and twelve all of it.
+ *    Elsewhere operands have 11 bits, which is 1.6 to three times as fast: below 0.2% for
+ *    settled triples as (1.5, -0.5, 0), 0.19 to 0.26% for five of the triple above;
+ *    up to 0.5%, a single singular value 1.2%, where many of g's singular values are
+ *    equal or few of its rows are not zero, so that roundings do not average.
+ *    Norms far below eps: X's values have steps of 2^-36.
  *    A square beyond fp32's range makes the norm infinite and the result zero;
  *    infinities and NaN give NaN in their matrix.
  *    The result does not depend on timing.
  *  - workspace: device, 256-byte aligned, moe_orthogonalize_workspace_bytes bytes
  *    (0 for sizes that are refused); about six bytes an element of g and four of
- *    every square of the shorter side.  No contents are kept from call to call; calls
- *    that may overlap on the GPU take one each.
+ *    every square of the shorter side (one matrix: eight and eight), and up to 32 MB
+ *    where that keeps operands of 22 bits together.  No contents are kept from call to
+ *    call; calls that may overlap on the GPU take one each.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA. */
 #define MOE_MAX_ORTHOGONALIZE_STEPS 64
 size_t moe_orthogonalize_workspace_bytes(int E, int N, int K);

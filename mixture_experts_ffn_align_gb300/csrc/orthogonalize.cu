@@ -22,17 +22,28 @@
 // all steps but the last; products take the hi part, and X = a X + (b A + c A^2) X
 // adds a times both in the epilogue, where rounding the hi part only costs what is
 // multiplied by b A + c A^2.  The last step folds a into B: B = a I + b A + c A^2, X =
-// B X, whose smaller elements round better.  The error is then 0.02 to 0.16% whatever
-// the spectrum and rank, less than the rounding of the result to bf16 (0.17%); with the
-// last two steps folded it was up to 0.29% where the rank is low.
-// Sums over few elements average less: up to m = 128, where all products are short,
-// operands too are the hi and the lo part, and a product is three (hi hi + hi lo + lo
-// hi) over one accumulator.
+// B X, whose smaller elements round better; with the last two steps folded the error was
+// up to 0.29% where the rank is low.
+//
+// What remains are the roundings of A and B themselves.  They count against |b| |A| + |c|
+// |A|^2, which may be ten times what a + b A + c A^2 leaves, and later steps enlarge them
+// again: by the polynomial's slope where a singular value is large, a-fold where it is
+// small.  Five steps of (3.4445, -4.7750, 2.0315) end at 0.19 to 0.25% (rms, with the
+// rounding of the result to bf16, 0.17%), where many singular values are equal at 0.4%
+// (roundings of equal numbers add up instead of averaging; at most 1.2% of a singular
+// value), eight such steps at 0.35%, twenty at 0.6%, steeper schedules at 0.5 to 2.5%.
+// So in two cases the operands too are the hi and the lo part, and a product is three (hi
+// hi + hi lo + lo hi) over one accumulator: where the steps enlarge roundings more than
+// those five do (`steep`), and, since sums over few elements average less, up to m = 128,
+// where all products are short.  That leaves 0.17% for sides up to 2^14, and costs (five
+// steps) 139 us instead of 86 for 8 x 512 x 256, 690 instead of 220 for 16 x 1031 x 517,
+// 16.1 ms instead of 5.8 for 16 x 7168 x 2048.
 //
 // Forming A anew in each step, rather than carrying it along as B A B, costs the m^2
 // M product but keeps small singular values: an error of A enters B X relative to
 // X, while that of a carried A grows twelvefold a step.
 #include <algorithm>
+#include <cmath>
 
 #include "dense_gemm.h"
 #include "moe_common.cuh"
@@ -47,6 +58,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPrecise = 128;                 // shorter sides up to here take hi and lo parts
 constexpr int kFolded = 1;                    // last steps that fold a X into B
+constexpr float kGain = 400.0f, kGrowth = 160.0f;   // of schedules for 11 bits
 constexpr float kScaleX = 4096.0f, kScaleA = 1024.0f, kScaleB = 1024.0f;
 constexpr int kMaxChunks = 304;               // partial sums of a matrix
 constexpr int kRowsPerThread = 4, kTiles = 4; // of k_ortho_scale, k_ortho_transpose
@@ -382,13 +394,14 @@ OrthoClusterPlan grid_plan(const Layout& l, int E) {
   return ortho_grid_plan(E, l.m, l.mp, l.M, l.Mp, l.parts, kModelSteps);
 }
 
-Layout layout(int E, int N, int K) {
+// Where everything lies, up to the slices' sums.
+Layout places(int E, int N, int K, int parts) {
   Layout l;
   l.m = std::min(N, K);
   l.M = std::max(N, K);
   l.mp = (l.m + 63) / 64 * 64;
   l.Mp = (l.M + 63) / 64 * 64;
-  l.parts = l.m <= kPrecise ? 2 : 1;
+  l.parts = parts;
   const long long n = (long long)N * K;
   l.chunks = (int)std::max<long long>(
       1, std::min<long long>({(n + 8191) / 8192, kMaxChunks, std::max(1, 1216 / E)}));
@@ -402,6 +415,11 @@ Layout layout(int E, int N, int K) {
   l.x1 = l.x0 + l.x_bytes;
   l.lo = l.x1 + l.x_bytes;
   l.part = l.lo + (l.parts == 1 ? l.x_bytes : 0);
+  l.total = l.part;
+  return l;
+}
+Layout layout(int E, int N, int K, int parts) {
+  Layout l = places(E, N, K, parts);
   const float c[3] = {};
   DenseProduct last = apply(l, E, nullptr, nullptr, nullptr);
   last.width = l.M;
@@ -418,8 +436,8 @@ Layout layout(int E, int N, int K) {
 // model was measured to be off by; X is kept in two parts beyond kPrecise, and what the
 // last product of a step moves for it (hi and lo, read and written) is counted at the
 // rates that the forms' epilogues reach.  A product of its own takes some 3500 cycles
-// more (its launch).  Up to kPrecise the whole grid never was the fastest.  us for five
-// steps as products / in clusters / over the grid:
+// more (its launch).  Up to kPrecise the whole grid never was the fastest, and with 22 bits
+// beyond it is not considered.  us for five steps as products / in clusters / over the grid:
 //   8 x 64 x 64     78 /  55 /  70      8 x 1024 x 1024   307 /  513 /  236
 //   8 x 256 x 512   84 /  78 /  89      16 x 768 x 2048   583 /  998 /  458
 //   8 x 512 x 512  125 / 149 / 117      64 x 512 x 1024   673 /  707 /  554
@@ -484,14 +502,64 @@ cudaError_t prepare(const Layout& l, int E, bool transposed, const void* g, floa
                             l.chunks, sums, eps, x);
 }
 
-}  // namespace
+// Whether the steps enlarge roundings of their operands more than five steps of the usual
+// triple do, which are 310 and 141 by these two figures; six are 476 and 485.
+// gain: relative roundings of 1 of A, B and X in a step move a singular value s by
+//   s (2 |b| s^2 + 5 |c| s^4 + |p - a| + |p|),  p = a + b s^2 + c s^4,
+// (A enters b A and twice A^2, whose sum counts once; B, its product with X) and each later
+// step enlarges that by its slope a + 3 b s^2 + 5 c s^4.  The largest over s from 2^-14 to
+// 1 and over the steps.
+// growth: of what is left in directions of (nearly) no singular value.
+// Steps that raise neither, as (1.5, -0.5, 0) or (2, -1.5, 0.5), stay with 11 bits and end
+// below 0.2%.
+bool steep(int steps, const float* c) {
+  constexpr int kValues = 64;
+  const float ratio = exp2f(-14.0f / (kValues - 1));
+  float s[kValues], d[kValues], growth = 1.0f;
+  for (int i = 0; i < kValues; ++i) {
+    s[i] = i == 0 ? 1.0f : s[i - 1] * ratio;
+    d[i] = 0.0f;
+  }
+  for (int k = 0; k < steps; ++k, c += 3) {
+    if (k > 0) growth *= fabsf(c[0]);
+    bool below = growth <= kGrowth;
+    for (int i = 0; i < kValues; ++i) {
+      const float s2 = s[i] * s[i], b = c[1] * s2, q = c[2] * s2 * s2, p = c[0] + b + q;
+      d[i] = fabsf(c[0] + 3.0f * b + 5.0f * q) * d[i] +
+             s[i] * (2.0f * fabsf(b) + 5.0f * fabsf(q) + fabsf(b + q) + fabsf(p));
+      s[i] = fabsf(s[i] * p);
+      below &= d[i] <= kGain;
+    }
+    if (!below) return true;
+  }
+  return false;
+}
 
-size_t orthogonalize_bytes(int E, int N, int K) { return layout(E, N, K).total; }
+// The workspace takes E matrices of 11 bits (6 bytes an element and 4 of a square).  Those
+// of 22 bits (8 and 8) go through the steps in groups that fit there, or in kSlack bytes
+// more: a launch of few small matrices takes as long as one of many (8 x 512 x 256, one by
+// one: 482 us).
+constexpr size_t kSlack = 32 << 20;
+struct Groups {
+  int n, last;          // matrices of each, and of the last one
+  Layout l, l_last;
+  size_t bytes() const { return std::max(l.total, l_last.total); }
+};
+Groups groups_of(int E, int N, int K, size_t bytes) {
+  Groups r;
+  for (int groups = 1;; ++groups) {
+    r.n = (E + groups - 1) / groups;
+    if (r.n > 1 && places(r.n, N, K, 2).total > bytes + kSlack) continue;
+    r.last = (E - 1) % r.n + 1;
+    r.l = layout(r.n, N, K, 2);
+    r.l_last = r.last == r.n ? r.l : layout(r.last, N, K, 2);   // (fewer may be sliced more)
+    if (r.n == 1 || r.bytes() <= bytes + kSlack) return r;
+  }
+}
 
-cudaError_t launch_orthogonalize(int E, int N, int K, const void* g, int type, void* out,
-                                 int steps, const float* coefficients, float eps, float scale,
-                                 void* workspace, cudaStream_t stream) {
-  const Layout l = layout(E, N, K);
+cudaError_t launch(const Layout& l, int E, int N, int K, const void* g, int type, void* out,
+                   int steps, const float* coefficients, float eps, float scale, void* workspace,
+                   cudaStream_t stream) {
   const bool transposed = N > K;
   char* ws = static_cast<char*>(workspace);
   void *a = ws + l.a, *b = ws + l.b, *x = ws + l.x0, *y = ws + l.x1, *part = ws + l.part;
@@ -549,6 +617,33 @@ cudaError_t launch_orthogonalize(int E, int N, int K, const void* g, int type, v
     std::swap(x, y);
   }
   return e;
+}
+
+}  // namespace
+
+size_t orthogonalize_bytes(int E, int N, int K) {
+  if (std::min(N, K) <= kPrecise) return layout(E, N, K, 2).total;
+  const size_t all = layout(E, N, K, 1).total;
+  return std::max(all, groups_of(E, N, K, all).bytes());
+}
+
+cudaError_t launch_orthogonalize(int E, int N, int K, const void* g, int type, void* out,
+                                 int steps, const float* coefficients, float eps, float scale,
+                                 void* workspace, cudaStream_t stream) {
+  if (std::min(N, K) <= kPrecise || !steep(steps, coefficients))
+    return launch(layout(E, N, K, std::min(N, K) <= kPrecise ? 2 : 1), E, N, K, g, type, out, steps,
+                  coefficients, eps, scale, workspace, stream);
+  const Groups r = groups_of(E, N, K, layout(E, N, K, 1).total);
+  const size_t each = (size_t)N * K;
+  for (int at = 0; at < E; at += r.n) {
+    const bool last = E - at <= r.n;
+    const cudaError_t e = launch(last ? r.l_last : r.l, last ? r.last : r.n, N, K,
+                                 static_cast<const char*>(g) + at * each * (type == 2 ? 4 : 2), type,
+                                 static_cast<char*>(out) + at * each * 2, steps, coefficients, eps,
+                                 scale, workspace, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace moe
