@@ -613,6 +613,11 @@ moe_status moe_clip_grad_norm(int n, const void* const* grads, void* const* outs
  *    A square beyond fp32's range makes the norm infinite and the result zero;
  *    infinities and NaN give NaN in their matrix.
  *    The result does not depend on timing.
+ *  - Middle sizes (several matrices of sides from some 130 to 1500) take one cooperative
+ *    launch: it starts when every SM has room for it, so it waits for a long kernel of
+ *    another stream to end, where other sizes share the GPU with it.  In a context of
+ *    fewer SMs than the device's these sizes run as the others do (but a capture there
+ *    ends with MOE_ERR_CUDA).
  *  - workspace: device, 256-byte aligned, moe_orthogonalize_workspace_bytes bytes
  *    (0 for sizes that are refused); about six bytes an element of g and four of
  *    every square of the shorter side (one matrix: eight and eight), and up to 32 MB
@@ -663,6 +668,12 @@ void moe_debug_set_watchdog(int64_t limit_ns, int never_arrive);
  * Not thread-safe; affects later launches.  No counterpart on the pages: it
  * only lets tests reach both forms at any size. */
 void moe_debug_set_bf16_gemm_form(int mode);
+
+/* Test hook: CTAs that moe_orthogonalize's launch over the whole grid takes at most
+ * (0: one for every SM).  More than the GPU can run at once are refused by the driver,
+ * as where a context has fewer SMs than the device; the products then run as launches
+ * of their own.  Not thread-safe; affects later launches. */
+void moe_debug_set_grid_ctas(int ctas);
 
 #ifdef __cplusplus
 }

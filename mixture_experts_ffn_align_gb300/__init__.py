@@ -33,7 +33,7 @@ EXPORTS = ["moe_m_sum_bound", "moe_align_workspace_bytes", "moe_align_permute_la
            "moe_host_workspace_bytes", "moe_align_permute", "grouped_gemm_w13", "act_mul_quant",
            "grouped_gemm_w2", "unpermute_reduce", "fused_experts", "fused_experts_from_host",
            "moe_sync_status", "moe_status_string", "moe_debug_set_watchdog",
-           "moe_debug_set_bf16_gemm_form",
+           "moe_debug_set_bf16_gemm_form", "moe_debug_set_grid_ctas",
            "moe_align_permute_noalloc", "moe_last_error_string", "moe_topk_router",
            "moe_batched_workspace_bytes", "fused_experts_batched", "grouped_gemm_w13_ex",
            "grouped_gemm_w2_ex", "fused_experts_ex", "moe_gemm2_splits",
@@ -184,6 +184,7 @@ def lib() -> ctypes.CDLL:
             [ctypes.c_int64, i32], None
         L.moe_debug_set_bf16_gemm_form.argtypes, L.moe_debug_set_bf16_gemm_form.restype = \
             [i32], None
+        L.moe_debug_set_grid_ctas.argtypes, L.moe_debug_set_grid_ctas.restype = [i32], None
         G, i64, f32 = ctypes.POINTER(CRagged), ctypes.c_int64, ctypes.c_float
         L.moe_ragged_workspace_bytes.argtypes, L.moe_ragged_workspace_bytes.restype = [G], sz
         L.ragged_gemm.argtypes = [G] + [vp] * 6 + [sz, vp]
@@ -777,6 +778,12 @@ def moe_debug_set_bf16_gemm_form(form: str = "auto"):
     orthogonalised update in one launch of clusters; "whole_grid": that update in one
     launch over the whole grid, all else by size."""
     lib().moe_debug_set_bf16_gemm_form(BF16_GEMM_FORMS[form])
+
+
+def moe_debug_set_grid_ctas(ctas: int = 0):
+    """CTAs of the orthogonalised update's launch over the whole grid (tests; 0: one an
+    SM).  More than the GPU runs at once are refused as where a context has few SMs."""
+    lib().moe_debug_set_grid_ctas(int(ctas))
 
 
 # ------------------------------------------------- buffer allocation helper

@@ -32,6 +32,7 @@ int g_never_arrive = 0;
 int g_bf16_form = 0;   // 0: by size, 1: single SM, 2: SM pairs
 int g_ragged_form = 0; // the same for the ragged products, 3: SM pairs on double tiles
 int g_ortho_form = 0;
+int g_ortho_grid_ctas = 0;
 
 // The current device, or -1 when it cannot be read or lies beyond the
 // per-device caches (kMaxDevices); callers then fail instead of borrowing
@@ -293,6 +294,7 @@ namespace moe {
 int record_cuda_status(cudaError_t e) { return cuda_status(e); }
 int ragged_form() { return g_ragged_form; }
 int ortho_form() { return g_ortho_form; }
+int ortho_grid_ctas() { return g_ortho_grid_ctas; }
 }  // namespace moe
 
 namespace {
@@ -890,5 +892,7 @@ void moe_debug_set_bf16_gemm_form(int mode) {
   g_ragged_form = mode >= 1 && mode <= 3 ? mode : 0;
   g_ortho_form = mode >= 1 && mode <= 4 ? mode : 0;
 }
+
+void moe_debug_set_grid_ctas(int ctas) { g_ortho_grid_ctas = ctas > 0 ? ctas : 0; }
 
 }  // extern "C"

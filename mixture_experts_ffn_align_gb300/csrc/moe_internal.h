@@ -253,6 +253,8 @@ cudaError_t launch_ragged_gated_2sm(const RaggedProblem& p, const GatedProblem& 
 int ragged_form();
 // The same for the orthogonalised update; 4: one launch over the whole grid.
 int ortho_form();
+// CTAs of that launch at most, 0: one an SM (moe_debug_set_grid_ctas).
+int ortho_grid_ctas();
 // 4-bit product: x codes / scales [R, K/2] / [R, K/32], weights [E, N, K/2] with
 // packed scales; token scales are first rewritten to workspace.
 size_t ragged_mxfp4_bytes(int R, int N, int K, int E);

@@ -631,7 +631,14 @@ cudaError_t launch_ortho_cluster(const OrthoClusterProblem& d, cudaStream_t stre
     coop.id = cudaLaunchAttributeCooperative;
     coop.val.cooperative = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<long long>(num_sms(), (long long)d.E * most), 1, 1);
+    const int ctas = ortho_grid_ctas() > 0 ? ortho_grid_ctas() : num_sms();
+    cfg.gridDim = dim3((unsigned)std::min<long long>(ctas, (long long)d.E * most), 1, 1);
+    if ((int)cfg.gridDim.x > num_sms()) {      // a refusal inside a capture would end it
+      cudaStreamCaptureStatus status;
+      const cudaError_t c = cudaStreamIsCapturing(stream, &status);
+      if (c != cudaSuccess) return c;
+      if (status != cudaStreamCaptureStatusNone) return cudaErrorCooperativeLaunchTooLarge;
+    }
     cfg.blockDim = dim3(threads(true), 1, 1);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = stream;

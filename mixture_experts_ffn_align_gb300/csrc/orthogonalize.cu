@@ -591,7 +591,12 @@ cudaError_t launch(const Layout& l, int E, int N, int K, const void* g, int type
     }
     d.coef = coef;
     d.done = done;
-    return launch_ortho_cluster(d, stream);
+    e = launch_ortho_cluster(d, stream);
+    // The whole grid has to be on the GPU at once.  Where the context has fewer SMs than the
+    // device (a partition), that is refused, and the products need no such thing.
+    if (form != Form::GRID || e != cudaErrorCooperativeLaunchTooLarge) return e;
+    (void)cudaGetLastError();       // seen
+    e = cudaSuccess;
   }
   for (int s = 0; s < steps && e == cudaSuccess; ++s) {
     e = run(gram(l, E, x, a), part, stream);
