@@ -621,7 +621,7 @@ moe_status moe_clip_grad_norm(int n, const void* const* grads, void* const* outs
  *  - workspace: device, 256-byte aligned, moe_orthogonalize_workspace_bytes bytes
  *    (0 for sizes that are refused).  With rows rounded up to 64 elements: six bytes an
  *    element of g and four of every square of the shorter side, for one matrix and where
- *    N or K is at most 128 eight and eight; besides sums of slices, up to 20 MB or 256 KB
+ *    N or K is at most 128 eight and eight; besides sums of slices, up to 20 MB or 512 KB
  *    a matrix, and up to 32 MB where that keeps operands of 22 bits together.  No contents
  *    are kept from call to call; calls that may overlap on the GPU take one each.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA. */

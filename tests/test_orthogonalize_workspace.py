@@ -28,7 +28,7 @@ def test_bytes_are_those_stated(shape):
     need = moe.moe_orthogonalize_workspace_bytes(E, N, K)
     assert need == moe.moe_orthogonalize_workspace_bytes(E, K, N)
     x, a = E * m * up(M), E * m * up(m)
-    more = max(20 << 20, E << 18) + (1 << 20)   # sums of slices; of squares, counters, alignment
+    more = max(20 << 20, E << 19) + (1 << 20)   # sums of slices; of squares, counters, alignment
     if m <= 128 or E == 1:
         assert 8 * (x + a) <= need <= 8 * (x + a) + more
     else:
