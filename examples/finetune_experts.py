@@ -135,6 +135,8 @@ def serve_w4a8(layer, x, q13, q2):
 
 def main(steps: int = 60, update: str = "plain", lr: float | None = None, max_norm: float = 1.0,
          verbose: bool = True):
+    if update not in ("plain", "orthogonal"):
+        raise ValueError(f'update must be "plain" or "orthogonal", not {update!r}')
     g = torch.Generator(device="cuda").manual_seed(0)
 
     def randn(*shape, scale=1.0):
