@@ -768,15 +768,16 @@ def moe_debug_set_watchdog(limit_ns: int, never_arrive: bool = False):
     lib().moe_debug_set_watchdog(int(limit_ns), int(bool(never_arrive)))
 
 
-BF16_GEMM_FORMS = {"auto": 0, "single": 1, "pairs": 2, "pairs_double": 3,
+# "clusters" is "pairs_double", under what it is for the orthogonalised update
+BF16_GEMM_FORMS = {"auto": 0, "single": 1, "pairs": 2, "pairs_double": 3, "clusters": 3,
                    "whole_grid": 4}
 
 
 def moe_debug_set_bf16_gemm_form(form: str = "auto"):
     """Force the single-SM or the SM-pair GEMMs (tests), or restore the
-    size-based choice; "pairs_double": ragged forward and dgrad on double tiles, the
-    orthogonalised update in one launch of clusters; "whole_grid": that update in one
-    launch over the whole grid, all else by size."""
+    size-based choice; "pairs_double" or "clusters": ragged forward and dgrad on double
+    tiles, the orthogonalised update in one launch of clusters; "whole_grid": that update
+    in one launch over the whole grid, all else by size."""
     lib().moe_debug_set_bf16_gemm_form(BF16_GEMM_FORMS[form])
 
 
