@@ -3,10 +3,11 @@
 //
 // Clusters, for small matrices: a cluster of 1 to 8 CTAs takes a matrix and goes through
 // the products A = X X^T, B = a I + b A + c A^2, X = B X of every step, with a cluster
-// barrier between them.  Small products are bound by latency: as launches of their own they take 4.7 us
-// each (a launch's end and start, cold instructions, the first copies), 15 of them
-// for five steps; here 3.1 us, for the barrier, the first copies and the last tile's
-// epilogue (8 x 64 x 64 in five steps: 76 and 54 us).  Matrices and sums stay in L2.
+// barrier between them.  Small products are bound by latency: as launches of their own
+// they take 4.7 us each (a launch's end and start, cold instructions, the first copies),
+// 15 of them for five steps; here 3.1 us, for the barrier, the first copies and the last
+// tile's epilogue (8 x 64 x 64 in five steps: 78 and 57 us with the norm and the scaling).
+// Matrices and sums stay in L2.
 //
 // The whole grid, for matrices of some tiles (GRID): the tiles of all products of all
 // matrices stand in one order, step by step, product by product, matrix by matrix, and
@@ -15,8 +16,8 @@
 // time.  A tile waits for earlier ones only, every CTA goes through its own in order and
 // all run at once (a cooperative launch), so the earliest unfinished tile can always go
 // on.  Against launches of their own no launch's end is waited for and no partly filled
-// round is left between products, only after the last: 8 x 1024 x 1024 307 and 236 us,
-// 16 x 517 x 1031 267 and 210, 64 x 512 x 1024 673 and 554.  Long sums in few tiles (no
+// round is left between products, only after the last: 8 x 1024 x 1024 313 and 238 us,
+// 16 x 517 x 1031 270 and 213, 64 x 512 x 1024 677 and 548.  Long sums in few tiles (no
 // slices here) and tiles of 256 x 256 on SM pairs stay ahead as launches of their own.
 //
 // orthogonalize.cu compares the forms by modelled cycles.
@@ -43,6 +44,7 @@ constexpr int BK = 64, MAX_STAGES = 9;
 constexpr int A_BYTES = 128 * BK * 2, RING_BYTES = 196608, BAR_BYTES = 256;
 // 12 over the whole grid measured 5% slower where sums are long (8 x 1536 x 1536: 639 and
 // 607 us) and 6% faster where they are short (64 x 256 x 2048: 423 and 449); 16 spill.
+// (8 take 168 registers, with 16 bytes spilled in clusters, 4 over the grid.)
 constexpr int EPI_WARPS = 8;
 // producer, MMA, epilogue warps; whole grid: one that tells it of finished tiles
 constexpr int threads(bool grid) { return 64 + 32 * EPI_WARPS + (grid ? 32 : 0); }

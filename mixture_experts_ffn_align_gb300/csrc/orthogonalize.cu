@@ -6,9 +6,10 @@
 //
 // X lies with its shorter side m as rows (g is transposed on the way in, and the
 // last product's stores on the way out), so A and B are m x m.  A and B are
-// symmetric and computed in tiles on and below the diagonal, each stored on both
-// sides: m^2 M + m^3 + 2 m^2 M operations a step instead of 4 m^2 M + 2 m^3 (M the
-// longer side).
+// symmetric: in square tiles (128 on one SM, 256 on a pair) only those on and below the
+// diagonal are computed, each stored on both sides, m^2 M + m^3 + 2 m^2 M operations a
+// step instead of 4 m^2 M + 2 m^3 (M the longer side) but for the tiles' upper halves.
+// Tiles of other shapes, and those of clusters, compute all of A and B.
 //
 // Operands are fp16, whose 11 bits matter here: with bf16's 8 the result is 1% off
 // (rms) and more.  X, A and B are scaled by powers of two into fp16's range: |X|, |A|
@@ -432,17 +433,21 @@ Layout layout(int E, int N, int K, int parts) {
 }
 
 // Products as launches of their own, or one launch for all steps (ortho_cluster.cu): in
-// clusters or over the whole grid.  By modelled cycles, each with the factor that its
-// model was measured to be off by; X is kept in two parts beyond kPrecise, and what the
+// clusters or over the whole grid.  By modelled cycles; against the products, clusters and
+// the grid count with the factors that their models were measured to be off by (the grid
+// against clusters without).  X is kept in two parts beyond kPrecise, and what the
 // last product of a step moves for it (hi and lo, read and written) is counted at the
 // rates that the forms' epilogues reach.  A product of its own takes some 3500 cycles
 // more (its launch).  Up to kPrecise the whole grid never was the fastest, and with 22 bits
-// beyond it is not considered.  us for five steps as products / in clusters / over the grid:
-//   8 x 64 x 64     78 /  55 /  70      8 x 1024 x 1024   307 /  513 /  236
-//   8 x 256 x 512   84 /  78 /  89      16 x 768 x 2048   583 /  998 /  458
-//   8 x 512 x 512  125 / 149 / 117      64 x 512 x 1024   673 /  707 /  554
-//   2 x 200 x 2000 103 / 157 / 118      1 x 1024 x 2048   174 /  758 /  220
-//                                       16 x 2048 x 7168 6145 / 19047 / 7596
+// beyond it is not considered.  us for five steps in a graph (bf16), as products / in
+// clusters / over the grid:
+//   8 x 64 x 64     78 /  57 /  76      8 x 1024 x 1024   313 /  519 /  238
+//   8 x 256 x 512   92 /  82 /  90      16 x 768 x 2048   592 / 1003 /  475
+//   8 x 512 x 512  124 / 153 / 121      64 x 512 x 1024   677 /  712 /  548
+//   2 x 200 x 2000 103 / 162 / 119      1 x 1024 x 2048   174 /  766 /  215
+//                                       16 x 2048 x 7168 6300 / 19084 / 7690
+// It is not always right: 200 x 160 x 160 takes the products (256, the grid 203), 2 x 1024
+// x 1024 the grid (174, the products 162), 8 x 256 x 2048 too (141, 137).
 enum class Form { PRODUCTS, CLUSTERS, GRID };
 Form form_of(const Layout& l, int E) {
   if (ortho_form() != 0)

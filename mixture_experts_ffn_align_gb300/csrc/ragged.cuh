@@ -68,7 +68,7 @@ struct RagGated {
 // Arguments of a batch of dense products of E matrices of m rows (ragged_epi.cuh).
 struct RagDense {
   int m;                    // rows of a matrix
-  int sym;                  // symmetric output, stored as rows from its columns
+  int sym;                  // symmetric output of mp rows and columns, zeros from m on
   int mp;                   // sym: columns of the output, m rounded up to 64
   int tri;                  // sym: tiles on and below the diagonal, stored on both sides
   int per;                  // rows of a token tile; sym: a multiple of 32

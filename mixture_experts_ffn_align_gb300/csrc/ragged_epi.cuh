@@ -190,7 +190,6 @@ __device__ __forceinline__ void rag_triangle(int l, RagTile& T) {
   T.w_tile = i;
   T.tok = l - i * (i + 1) / 2;
 }
-template <int G>
 __device__ __forceinline__ RagTile rag_dense_tile(const RagArgs& a, int t) {
   const RagDense& q = a.dense;
   RagTile T;
@@ -514,7 +513,7 @@ __device__ __forceinline__ void rag_join_fused(const RagArgs& a, const RagTile& 
 // Tile t of a product, whatever its epilogue.
 template <int EPI, int G>
 __device__ __forceinline__ RagTile rag_any_tile(const RagSched& s, const RagArgs& a, int t) {
-  if constexpr (EPI == EPI_DENSE) return rag_dense_tile<G>(a, t);
+  if constexpr (EPI == EPI_DENSE) return rag_dense_tile(a, t);
   return rag_tile<G>(s, a, t);
 }
 

@@ -55,7 +55,8 @@ constexpr int RING_BYTES = 196608, BAR_BYTES = 384;
 // 128 columns each), the gated ones two (of every other 16 tokens), the dense four: a
 // short product's epilogue is as long as its reduction (16 x 517 x 1031, a step of three
 // products 53.7 us with two, 49.8 with four; on pairs, where products are long, two
-// are better, 5.07 against 5.24 ms for 2 x 4096 x 14336).
+// are better, 5.07 against 5.24 ms for 2 x 4096 x 14336; four leave 96 registers, and
+// the form with MN-major weights spills 8 bytes).
 constexpr int epi_warps(int op, int epi) {
   return epi == EPI_DENSE ? 16 : op == RAG_WGRAD || epi != EPI_PLAIN ? 8 : 4;
 }
