@@ -712,8 +712,9 @@ def moe_orthogonalize(g, out, workspace, steps=5, coefficients=(3.4445, -4.7750,
                       eps=1e-7, scale=1.0, stream=None):
     """out = scale X of every matrix of g [E, N, K] (or [N, K]; bfloat16, float16 or
     float32): X = g / (|g|_F + eps), then in each step X = (a I + b A + c A^2) X with
-    A = X X^T.  coefficients: (a, b, c), or a sequence of such triples, one a step.  out:
-    bfloat16, of g's shape."""
+    A = X X^T.  coefficients: (a, b, c), or a sequence of such triples, one a step; steps:
+    1 to 64.  out: bfloat16, of g's shape.  Products take operands of 22 bits where the
+    steps or short sides need them, else of 11 (include/moe_ffn.h has the errors)."""
     shape = g.shape
     if not 2 <= len(shape) <= 3:
         raise ValueError(f"g must be [E, N, K] or [N, K], not {tuple(shape)}")

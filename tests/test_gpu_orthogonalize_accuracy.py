@@ -6,8 +6,8 @@ that enlarge roundings more than five of the default triple do): 0.25% of the re
 of which its rounding to bf16 is 2^-8 / sqrt(12) .. 2^-8 / sqrt(3) of a value, 0.17% on
 average.  The rest is sqrt(0.25^2 - 0.17^2) = 0.18%; sums of L products are truncated by
 (L / 16 + 17) 2^-24, 4e-6 for 3 x 300, which the schedules below enlarge up to 100-fold
-where all singular values are equal (measured in fp64 with the rounding points alone, 2.5%
-of 2^-12).  Single values: half a step of bf16 and five deviations of the rest, 1% of the
+where all singular values are equal (2.5% from the roundings of 11-bit operands alone,
+2^-12 each, restated in fp64).  Single values: half a step of bf16 and five deviations of the rest, 1% of the
 rms.
 11-bit operands: 1.3 times the error of the oracle with the same rounding points, as in
 test_gpu_orthogonalize.py, and 0.35%, between what the library states for broad spectra and
