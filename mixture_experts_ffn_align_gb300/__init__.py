@@ -702,6 +702,7 @@ def _coefficients(steps, coefficients):
 def _numbers(c):
     """The sequence c, or a sequence of such, with floats in place of what it holds:
     tensors and arrays of one number hash by identity, and may change between calls."""
+    c = tuple(c)
     try:
         return tuple(map(float, c))
     except (TypeError, ValueError, RuntimeError):       # not numbers: a triple a step

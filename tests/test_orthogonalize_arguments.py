@@ -60,6 +60,15 @@ def test_sequences_of_any_kind(passed, sequence):
     assert passed(steps=2, coefficients=tuple(sequence(s) for s in steps)) == [1, 2, 3, 4, 5, 6]
 
 
+def test_sequences_that_are_read_once(passed):
+    steps = ((1.0, 2.0, 3.0), (4.0, 5.0, 6.0))
+    assert passed(steps=2, coefficients=iter(steps)) == [1, 2, 3, 4, 5, 6]
+    assert passed(steps=2, coefficients=(iter(s) for s in steps)) == [1, 2, 3, 4, 5, 6]
+    assert passed(steps=2, coefficients=iter(steps[0])) == [1, 2, 3] * 2
+    with pytest.raises(ValueError, match="coefficients"):
+        passed(steps=1, coefficients=iter(steps))
+
+
 def test_default_and_longest(passed):
     f = np.float32([3.4445, -4.7750, 2.0315]).tolist()
     assert passed() == f * 5
