@@ -55,7 +55,8 @@ __device__ __forceinline__ GatedGrad gated_grad(const RagGated& a, float dz, flo
   const float gc = gated_min<CLAMP>(g, a.limit), uc = gated_clamp<CLAMP>(u, a.limit) + a.beta;
   const float s = gated_sigmoid(a.alpha * gc), act = gc * s;
   GatedGrad r;
-  r.dg = CLAMP && g > a.limit ? 0.0f : dz * uc * (s + a.alpha * act * (1.0f - s));
+  // (act (1 - s) first: alpha act may be past fp32's range where 1 - s is 0)
+  r.dg = CLAMP && g > a.limit ? 0.0f : dz * uc * (s + a.alpha * (act * (1.0f - s)));
   r.du = CLAMP && fabsf(u) > a.limit ? 0.0f : dz * act;
   r.z = act * uc;
   return r;
