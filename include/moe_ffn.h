@@ -592,7 +592,7 @@ moe_status moe_clip_grad_norm(int n, const void* const* grads, void* const* outs
  *    be g itself.  Each matrix by itself, whichever side is the longer.
  *  - coefficients: host array of 3 * steps floats, read during the call; steps 1 to
  *    MOE_MAX_ORTHOGONALIZE_STEPS.  They should keep singular values of X below 3 and
- *    the polynomial's values within 16: elements past that are infinities.
+ *    the polynomial's values within 16: elements past that are infinities or NaN.
  *  - eps: at least 1e-12; a zero matrix gives zeros.
  *  - Sums are fp32, X is kept with 22 bits until the last step.  Errors, as rms of the
  *    result's, its own rounding to bf16 among them (0.17%; up to 0.39% where its values
@@ -671,7 +671,7 @@ void moe_debug_set_watchdog(int64_t limit_ns, int never_arrive);
 void moe_debug_set_bf16_gemm_form(int mode);
 
 /* Test hook: CTAs that moe_orthogonalize's launch over the whole grid takes at most
- * (0: one for every SM).  More than the GPU can run at once are refused by the driver,
+ * (0: one for every SM).  More than the GPU can run at once are refused by CUDA,
  * as where a context has fewer SMs than the device; the products then run as launches
  * of their own.  Not thread-safe; affects later launches. */
 void moe_debug_set_grid_ctas(int ctas);

@@ -1,5 +1,5 @@
 """The orthogonalised update's launch over the whole grid where the GPU has fewer SMs for it
-than the device: smaller grids, and one that the driver refuses."""
+than the device: smaller grids, and one that CUDA refuses."""
 import pytest
 
 torch = pytest.importorskip("torch")
